@@ -140,6 +140,7 @@ def lib():
     L.mlp_trace_read.restype = ctypes.c_int
     L.mlp_kernel_name.argtypes = [ctypes.c_int]
     L.mlp_kernel_name.restype = ctypes.c_char_p
+    experts.declare(L)
     _LIB = L
     return L
 
@@ -435,3 +436,11 @@ def mlp_debug_set_flags(flags: int) -> None:
 from .autograd import mlp_block_func, mlp_func  # noqa: E402  (differentiable forms)
 
 __all__ += ["mlp_func", "mlp_block_func"]
+
+from . import experts  # noqa: E402  (mixture of experts)
+from .experts import (Moe, alloc_moe_plan, mlp_moe_combine, mlp_moe_combine_bwd,  # noqa: E402
+                  mlp_moe_dispatch, mlp_moe_dispatch_bwd, mlp_moe_rows, mlp_moe_sort, moe,
+                  moe_plan_views)
+
+__all__ += ["Moe", "moe", "alloc_moe_plan", "moe_plan_views", "mlp_moe_rows", "mlp_moe_sort",
+            "mlp_moe_dispatch", "mlp_moe_dispatch_bwd", "mlp_moe_combine", "mlp_moe_combine_bwd"]

@@ -952,6 +952,10 @@ const char* mlp_kernel_name(int tag) {
     case MLP_KERNEL_QUANT: return "quant_f8";
     case MLP_KERNEL_FWD_FUSED: return "fwd_fused";
     case MLP_KERNEL_REFRESH: return "refresh_scales";
+    case MLP_KERNEL_MOE_SORT: return "moe_sort";
+    case MLP_KERNEL_MOE_DISPATCH: return "moe_dispatch";
+    case MLP_KERNEL_MOE_COMBINE: return "moe_combine";
+    case MLP_KERNEL_MOE_COMBINE_BWD: return "moe_combine_bwd";
     default: return "unknown";
   }
 }

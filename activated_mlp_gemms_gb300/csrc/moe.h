@@ -1,0 +1,64 @@
+// moe.h -- the sorted layout of the mixture-of-experts calls, and the
+// launchers of its kernels.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mlpk {
+
+constexpr int MOE_ALIGN = 16;          // MLP_MOE_ROW_ALIGN
+constexpr int MOE_MAX_EXPERTS = 1024;  // MLP_MOE_MAX_EXPERTS
+
+// One 128- or 256-row output tile of the experts' GEMMs: rows [row, end) of
+// `expert` (at most the tile's height of them).
+struct MoeTile {
+  int expert, row, end, pad;
+};
+
+// Where the parts of the plan are, in int32 values.
+struct MoePlan {
+  long long n, rows;                  // slots, rows of the sorted layout
+  long long offsets, counts, ntiles;  // [E + 1], [E], [2] (128- and 256-row tiles)
+  long long tiles[2];                 // MoeTile lists: 128 rows, 256 rows
+  long long tile_cap[2];
+  long long pos, src, ints;
+};
+
+inline MoePlan moe_plan(int T, int E, int top_k) {
+  MoePlan L;
+  L.n = static_cast<long long>(T) * top_k;
+  const long long used = L.n < E ? L.n : E;
+  L.rows = (L.n + used * (MOE_ALIGN - 1)) / MOE_ALIGN * MOE_ALIGN;
+  auto r4 = [](long long v) { return (v + 3) / 4 * 4; };  // 16-byte parts
+  L.offsets = 0;
+  L.counts = r4(E + 1);
+  L.ntiles = L.counts + r4(E);
+  long long at = L.ntiles + 4;
+  for (int h = 0; h < 2; ++h) {
+    // an expert's last tile may be partial: at most one a non-empty expert
+    L.tiles[h] = at;
+    L.tile_cap[h] = L.rows / (h == 0 ? 128 : 256) + used;
+    at += 4 * L.tile_cap[h];
+  }
+  L.pos = at;
+  L.src = L.pos + r4(L.n);
+  L.ints = L.src + r4(L.rows);
+  return L;
+}
+
+// The routing weights' type: fp32 or bf16.
+cudaError_t launch_moe_sort(const int* ids, int* plan, const MoePlan& L, int E, cudaStream_t stream,
+                            bool pdl);
+cudaError_t launch_moe_dispatch(const void* x, const int* plan, const MoePlan& L, int T, int top_k,
+                                int H, void* xs, cudaStream_t stream, bool pdl);
+// weights == nullptr: ones (the gradient of the dispatch)
+cudaError_t launch_moe_combine(const void* y, const int* plan, const MoePlan& L, int T, int top_k,
+                               int H, const void* weights, bool w_bf16, const void* residual,
+                               void* out, cudaStream_t stream, bool pdl);
+cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* plan,
+                                   const MoePlan& L, int T, int top_k, int H, const void* weights,
+                                   bool w_bf16, void* dy, void* dweights, cudaStream_t stream,
+                                   bool pdl);
+
+}  // namespace mlpk

@@ -1,0 +1,156 @@
+"""The mixture-of-experts MLP (include/mlp_moe.h): tokens sorted by expert and
+back with their routing weights, and the gradients.
+
+Argument marshalling only, as in the package's other calls: outputs are
+tensors that the caller passes.  Every shape is checked, because the kernels
+take their row numbers from the plan.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import ACTS, MlpError, _check, _ptr, _stream, lib
+
+ROW_ALIGN = 16  # MLP_MOE_ROW_ALIGN
+MAX_EXPERTS = 1024  # MLP_MOE_MAX_EXPERTS
+MAX_TOP_K = 64  # MLP_MOE_MAX_TOP_K
+_W_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class Moe(ctypes.Structure):
+    """mlp_moe_t"""
+    _fields_ = [("T", ctypes.c_int), ("E", ctypes.c_int), ("top_k", ctypes.c_int),
+                ("H", ctypes.c_int), ("I", ctypes.c_int), ("act", ctypes.c_int),
+                ("gate_mult", ctypes.c_float), ("down_mult", ctypes.c_float),
+                ("weights_type", ctypes.c_int)]
+
+
+class _Layout(ctypes.Structure):
+    """mlp_moe_plan_t"""
+    _fields_ = [(n, ctypes.c_longlong) for n in ("ints", "offsets", "counts", "pos", "src")]
+
+
+def declare(L):
+    """Argument types of mlp_moe.h's functions (called when the library is loaded)."""
+    P, VP = ctypes.POINTER(Moe), ctypes.c_void_p
+    L.mlp_moe_rows.argtypes = [P]
+    L.mlp_moe_rows.restype = ctypes.c_longlong
+    L.mlp_moe_plan_layout.argtypes = [P, ctypes.POINTER(_Layout)]
+    L.mlp_moe_sort.argtypes = [P] + [VP] * 3
+    L.mlp_moe_dispatch.argtypes = [P] + [VP] * 4
+    L.mlp_moe_dispatch_bwd.argtypes = [P] + [VP] * 4
+    L.mlp_moe_combine.argtypes = [P] + [VP] * 6
+    L.mlp_moe_combine_bwd.argtypes = [P] + [VP] * 7
+    for n in ("plan_layout", "sort", "dispatch", "dispatch_bwd", "combine", "combine_bwd"):
+        getattr(L, "mlp_moe_" + n).restype = ctypes.c_int
+
+
+def moe(T, E, top_k, H, I=0, act="swiglu", gate_mult=1.0, down_mult=1.0,
+        weights_dtype=torch.float32) -> Moe:
+    """The problem: T tokens of H values, E experts, top_k slots a token; the experts'
+    intermediate size I, activation and multipliers; the routing weights' type."""
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}; one of {list(ACTS)}")
+    if weights_dtype not in _W_TYPES:
+        raise ValueError("weights_dtype must be torch.float32 or torch.bfloat16")
+    return Moe(int(T), int(E), int(top_k), int(H), int(I), ACTS[act], float(gate_mult),
+               float(down_mult), _W_TYPES[weights_dtype])
+
+
+def _shaped(t, shape, name, dtype=torch.bfloat16):
+    """The tensor's address (None stays None) once its type, device and shape are right."""
+    if t is None:
+        return None
+    p = _ptr(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return p
+
+
+def _w_dtype(p: Moe):
+    return torch.bfloat16 if p.weights_type else torch.float32
+
+
+def _layout(p: Moe) -> _Layout:
+    out = _Layout()
+    _check(lib().mlp_moe_plan_layout(ctypes.byref(p), ctypes.byref(out)), "mlp_moe_plan_layout")
+    return out
+
+
+def mlp_moe_rows(p: Moe) -> int:
+    """Rows of the sorted layout's buffers (xs, y, dxs, dy, G, U)."""
+    rows = int(lib().mlp_moe_rows(ctypes.byref(p)))
+    if rows == 0:
+        raise MlpError(lib().mlp_moe_plan_layout(ctypes.byref(p), ctypes.byref(_Layout())),
+                       "mlp_moe_rows")
+    return rows
+
+
+def alloc_moe_plan(p: Moe, device=None) -> torch.Tensor:
+    return torch.empty(_layout(p).ints, dtype=torch.int32, device=device or "cuda")
+
+
+def _plan(p: Moe, plan):
+    return _shaped(plan, (_layout(p).ints,), "plan", torch.int32)
+
+
+def moe_plan_views(p: Moe, plan) -> dict:
+    """The plan's public parts as views: offsets [E + 1] (first row of each expert),
+    counts [E], pos [T, top_k] (row of each slot, -1 when dropped), src [rows] (slot of
+    each row, -1 for padding)."""
+    _plan(p, plan)
+    L = _layout(p)
+    n, rows = p.T * p.top_k, mlp_moe_rows(p)
+    return {"offsets": plan[L.offsets:L.offsets + p.E + 1],
+            "counts": plan[L.counts:L.counts + p.E],
+            "pos": plan[L.pos:L.pos + n].view(p.T, p.top_k), "src": plan[L.src:L.src + rows]}
+
+
+def mlp_moe_sort(p: Moe, ids, plan, stream=None) -> None:
+    """Fills the plan from ids (int32 [T, top_k]; an id outside [0, E) drops the slot)."""
+    rc = lib().mlp_moe_sort(ctypes.byref(p),
+                            _shaped(ids, (p.T, p.top_k), "ids", torch.int32), _plan(p, plan),
+                            _stream(stream))
+    _check(rc, "mlp_moe_sort")
+
+
+def mlp_moe_dispatch(p: Moe, plan, x, xs, stream=None) -> None:
+    """xs[pos[t, j]] = x[t]; the other rows of xs become zero."""
+    rc = lib().mlp_moe_dispatch(ctypes.byref(p), _plan(p, plan), _shaped(x, (p.T, p.H), "x"),
+                                _shaped(xs, (mlp_moe_rows(p), p.H), "xs"), _stream(stream))
+    _check(rc, "mlp_moe_dispatch")
+
+
+def mlp_moe_dispatch_bwd(p: Moe, plan, dxs, dx, stream=None) -> None:
+    """dx[t] = sum_j dxs[pos[t, j]]."""
+    rc = lib().mlp_moe_dispatch_bwd(ctypes.byref(p), _plan(p, plan),
+                                    _shaped(dxs, (mlp_moe_rows(p), p.H), "dxs"),
+                                    _shaped(dx, (p.T, p.H), "dx"), _stream(stream))
+    _check(rc, "mlp_moe_dispatch_bwd")
+
+
+def mlp_moe_combine(p: Moe, plan, y, weights, residual, out, stream=None) -> None:
+    """out[t] = residual[t] + sum_j weights[t, j] y[pos[t, j]] (residual may be None)."""
+    rc = lib().mlp_moe_combine(ctypes.byref(p), _plan(p, plan),
+                               _shaped(y, (mlp_moe_rows(p), p.H), "y"),
+                               _shaped(weights, (p.T, p.top_k), "weights", _w_dtype(p)),
+                               _shaped(residual, (p.T, p.H), "residual"),
+                               _shaped(out, (p.T, p.H), "out"), _stream(stream))
+    _check(rc, "mlp_moe_combine")
+
+
+def mlp_moe_combine_bwd(p: Moe, plan, dout, y, weights, dy=None, dweights=None,
+                        stream=None) -> None:
+    """dy[pos[t, j]] = weights[t, j] dout[t] (the other rows zero) and
+    dweights[t, j] = <dout[t], y[pos[t, j]]>; either may be None."""
+    rows = mlp_moe_rows(p)
+    rc = lib().mlp_moe_combine_bwd(ctypes.byref(p), _plan(p, plan),
+                                   _shaped(dout, (p.T, p.H), "dout"),
+                                   _shaped(y, (rows, p.H), "y"),
+                                   _shaped(weights, (p.T, p.top_k), "weights", _w_dtype(p)),
+                                   _shaped(dy, (rows, p.H), "dy"),
+                                   _shaped(dweights, (p.T, p.top_k), "dweights", _w_dtype(p)),
+                                   _stream(stream))
+    _check(rc, "mlp_moe_combine_bwd")

@@ -464,7 +464,12 @@ typedef enum {
   MLP_KERNEL_FWD_FUSED = 11,    /* the gated forward's gate/up and down GEMMs in one launch
                                    (CTA-pair tiles, M <= 32768): a down tile starts once the
                                    postact of its 256 rows is stored */
-  MLP_KERNEL_REFRESH = 12       /* the FP8 delayed-scale refresh */
+  MLP_KERNEL_REFRESH = 12,      /* the FP8 delayed-scale refresh */
+  /* mlp_moe.h */
+  MLP_KERNEL_MOE_SORT = 13,        /* the slots' counting sort by expert */
+  MLP_KERNEL_MOE_DISPATCH = 14,    /* token rows to the sorted layout */
+  MLP_KERNEL_MOE_COMBINE = 15,     /* (weighted) sum of a token's rows of the sorted layout */
+  MLP_KERNEL_MOE_COMBINE_BWD = 16  /* its gradients */
 } mlp_kernel_t;
 
 /* on != 0 starts recording, 0 stops (records already taken are kept). */

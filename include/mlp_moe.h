@@ -1,0 +1,92 @@
+/*
+ * mlp_moe.h -- C ABI of the mixture-of-experts MLP of libmlp.so: tokens
+ * sorted by expert and back with their routing weights, each expert's MLP
+ * over its own rows, and the gradients.  An addition of this library; the
+ * conventions of mlp.h (ownership, streams, alignment, return values,
+ * workspace, device-side errors) hold for every call here.
+ *
+ * A token t has top_k slots; slot (t, j) names an expert ids[t, j] and
+ * carries a weight w[t, j].  A slot whose id is not in [0, E) is dropped: it
+ * takes no row, and contributes nothing.  With MLP_e the expert's MLP of
+ * mlp.h (bias-free, gated or not):
+ *
+ *   out[t] = residual[t] + sum_j w[t, j] * MLP_{ids[t, j]}(x[t])
+ *
+ * The sorted layout.  Every expert owns a contiguous block of rows that
+ * begins at a multiple of MLP_MOE_ROW_ALIGN (16, the K step of a bf16
+ * tensor-core instruction: a weight gradient sums over an expert's rows, so
+ * whole steps belong to one expert).  Inside the block the slots come in
+ * the order of t, then j; the rows that fill up the block's last 16 are
+ * padding.  mlp_moe_rows gives the most rows any assignment can need, and
+ * the row buffers have that many.
+ */
+#ifndef MLP_GB300_MOE_H
+#define MLP_GB300_MOE_H
+
+#include "mlp.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MLP_MOE_ROW_ALIGN 16
+#define MLP_MOE_MAX_EXPERTS 1024
+#define MLP_MOE_MAX_TOP_K 64
+
+typedef enum { MLP_MOE_W_F32 = 0, MLP_MOE_W_BF16 = 1 } mlp_moe_weight_t;
+
+/* T tokens of H values, E experts, top_k slots a token; the experts' MLPs:
+ * intermediate size I, activation and multipliers as mlp_problem_t's (I and
+ * act are read by the calls that run the experts only).  weights_type: the
+ * type of the routing weights and of their gradient. */
+typedef struct {
+  int T, E, top_k, H, I;
+  int act;           /* mlp_act_t */
+  float gate_mult, down_mult;
+  int weights_type;  /* mlp_moe_weight_t */
+} mlp_moe_t;
+
+/* Rows of the sorted layout's buffers: n + 15 min(E, n), rounded down to a
+ * multiple of 16, with n = T top_k.  0 on invalid arguments. */
+long long mlp_moe_rows(const mlp_moe_t* p);
+
+/* The plan: one caller-owned int32 device buffer (16-byte aligned) that
+ * mlp_moe_sort fills and every other call reads. */
+typedef struct {
+  long long ints;     /* size of the plan, in int32 values */
+  long long offsets;  /* [E + 1]: first row of each expert; [E] = rows in use */
+  long long counts;   /* [E]: slots of each expert */
+  long long pos;      /* [T, top_k]: row of each slot, -1 when dropped */
+  long long src;      /* [rows]: slot t * top_k + j of each row, -1 for padding and past the end */
+} mlp_moe_plan_t;     /* the last four: where in the plan, in int32 values */
+int mlp_moe_plan_layout(const mlp_moe_t* p, mlp_moe_plan_t* layout);
+
+/* Fills the plan from ids (int32 [T, top_k], 4-byte aligned).  Stable and
+ * deterministic. */
+int mlp_moe_sort(const mlp_moe_t* p, const int* ids, void* plan, void* stream);
+
+/* xs[pos[t, j]] = x[t]; every other row of xs is zero.
+ *   x bf16 [T,H] in, xs bf16 [rows,H] out */
+int mlp_moe_dispatch(const mlp_moe_t* p, const void* plan, const void* x, void* xs, void* stream);
+
+/* Its gradient: dx[t] = sum_j dxs[pos[t, j]] (fp32 sum, rounded once).
+ *   dxs bf16 [rows,H] in, dx bf16 [T,H] out */
+int mlp_moe_dispatch_bwd(const mlp_moe_t* p, const void* plan, const void* dxs, void* dx,
+                         void* stream);
+
+/* out[t] = residual[t] + sum_j weights[t, j] y[pos[t, j]] (fp32, rounded once).
+ *   y bf16 [rows,H], weights [T,top_k] (weights_type, 4-byte aligned),
+ *   residual bf16 [T,H] or NULL, out bf16 [T,H] (may be residual itself) */
+int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const void* weights,
+                    const void* residual, void* out, void* stream);
+
+/* Its gradients: dy[pos[t, j]] = weights[t, j] dout[t], every other row of dy
+ * zero; dweights[t, j] = sum_h dout[t,h] y[pos[t, j],h] (fp32 sum; 0 for a
+ * dropped slot).  dy or dweights may be NULL (then y, or weights, too). */
+int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, const void* y,
+                        const void* weights, void* dy, void* dweights, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MLP_GB300_MOE_H */
