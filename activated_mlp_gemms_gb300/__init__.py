@@ -141,6 +141,7 @@ def lib():
     L.mlp_kernel_name.argtypes = [ctypes.c_int]
     L.mlp_kernel_name.restype = ctypes.c_char_p
     experts.declare(L)
+    linear_op.declare(L)
     _LIB = L
     return L
 
@@ -437,10 +438,16 @@ from .autograd import mlp_block_func, mlp_func  # noqa: E402  (differentiable fo
 
 __all__ += ["mlp_func", "mlp_block_func"]
 
-from . import experts  # noqa: E402  (mixture of experts)
+from . import experts, linear_op  # noqa: E402  (mixture of experts; linear layer)
 from .experts import (Moe, alloc_moe_plan, mlp_moe_combine, mlp_moe_combine_bwd,  # noqa: E402
                   mlp_moe_dispatch, mlp_moe_dispatch_bwd, mlp_moe_rows, mlp_moe_sort, moe,
                   moe_plan_views)
 
 __all__ += ["Moe", "moe", "alloc_moe_plan", "moe_plan_views", "mlp_moe_rows", "mlp_moe_sort",
             "mlp_moe_dispatch", "mlp_moe_dispatch_bwd", "mlp_moe_combine", "mlp_moe_combine_bwd"]
+
+from .linear_op import (LINEAR_ACTS, Linear, alloc_linear_workspace, linear,  # noqa: E402
+                        mlp_linear_bwd, mlp_linear_fwd, mlp_linear_workspace_size)
+
+__all__ += ["LINEAR_ACTS", "Linear", "linear", "alloc_linear_workspace", "mlp_linear_fwd",
+            "mlp_linear_bwd", "mlp_linear_workspace_size"]

@@ -30,7 +30,9 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
-  if constexpr (ACT == ACT_SILU) {
+  if constexpr (ACT == ACT_NONE) {
+    return z;
+  } else if constexpr (ACT == ACT_SILU) {
     return z * sigmoid_f(z);
   } else if constexpr (ACT == ACT_RELU_SQ) {
     float r = fmaxf(z, 0.0f);
@@ -49,7 +51,10 @@ __device__ __forceinline__ float act_f(float z) {
 // act(z) and act'(z) together.
 template <int ACT>
 __device__ __forceinline__ void act_and_grad(float z, float& a, float& da) {
-  if constexpr (ACT == ACT_SILU) {
+  if constexpr (ACT == ACT_NONE) {
+    a = z;
+    da = 1.0f;
+  } else if constexpr (ACT == ACT_SILU) {
     float s = sigmoid_f(z);
     a = z * s;
     da = s * fmaf(z, 1.0f - s, 1.0f);

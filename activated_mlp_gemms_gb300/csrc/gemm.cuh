@@ -89,7 +89,8 @@ struct EpiTraits {
   // dU, a; dact: dP, a; plain: D) and bytes of one staged 32 x 32 box
   static constexpr int NOUT = (EPI == EPI_GATED_FWD || EPI == EPI_DGATED || EPI == EPI_FWD_FUSED) ? 3
                               : (EPI == EPI_ACT_FWD || EPI == EPI_DACT ||
-                                 EPI == EPI_DACT_RECOMP || EPI == EPI_ACT_FWD_F8) ? 2
+                                 EPI == EPI_DACT_RECOMP || EPI == EPI_ACT_FWD_F8 ||
+                                 EPI == EPI_LINEAR) ? 2
                                                                                   : 1;
   // bytes of a staged 32 x 32 output box: fp32 4096, bf16 2048 (the 8-bit
   // epilogues stage their own boxes, below)
@@ -885,6 +886,65 @@ __device__ __forceinline__ void epi_recomp_f8_dh(const EpiUnit& P, const EpiWarp
   }
 }
 
+// The linear layer: z = acc + bias, D = act(z) + alpha * residual.  A chunk's
+// 32 biases are the same for every lane (broadcast loads that stay in L1).
+// The residual is read row-coalesced, a chunk ahead of the stores (the first
+// chunk before the accumulator is waited for), and moved to one row per lane
+// through the first staging box, as the saved preacts of epi_dact are; every
+// element is read before its chunk's store, so D may be the residual itself.
+template <int ACT>
+__device__ __forceinline__ void epi_linear(const Params& p, const EpiUnit& P, const EpiWarp& e,
+                                           uint32_t tb, int col0, int cb, int ce, uint4 (&pg)[4]) {
+  const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(P.in1);
+  uint4 unused[4];
+#pragma unroll 1
+  for (int c = cb; c < ce; c += 32) {
+    const int col = col0 + c;
+    if (col >= P.N) break;  // warp-uniform
+    uint4 ng[4];
+    const bool more = P.in0 != nullptr && c + 32 < ce;
+    if (more) dact_load_rows<false>(P, e.row0, e.lane, col + 32, ng, unused);
+    uint32_t d[32];
+    __syncwarp();
+    tmem_ld32(tb + c, d);
+    uint4 bv[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      bv[v] = (bias != nullptr && col + 8 * v < P.N) ? ld_global_v4(bias + col + 8 * v)
+                                                     : make_uint4(0, 0, 0, 0);
+    tmem_wait_ld();
+    staging_acquire(e);
+    if (P.in0 != nullptr) dact_rows_to_lanes<false>(e, pg, unused);
+    uint32_t po[16], pz[16];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const uint32_t bw[4] = {bv[v].x, bv[v].y, bv[v].z, bv[v].w};
+      const uint32_t rw[4] = {pg[v].x, pg[v].y, pg[v].z, pg[v].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 b = unpack_bf16x2(bw[j]);
+        const float z0 = __uint_as_float(d[8 * v + 2 * j]) + b.x;
+        const float z1 = __uint_as_float(d[8 * v + 2 * j + 1]) + b.y;
+        float o0 = act_f<ACT>(z0), o1 = act_f<ACT>(z1);
+        if (P.in0 != nullptr) {
+          const float2 r = unpack_bf16x2(rw[j]);
+          o0 = fmaf(P.alpha, r.x, o0);
+          o1 = fmaf(P.alpha, r.y, o1);
+        }
+        po[4 * v + j] = pack_bf16x2(o0, o1);
+        pz[4 * v + j] = pack_bf16x2(z0, z1);
+      }
+    }
+    stage_bf16(e.stg, e.lane, po);
+    if (P.out[1]) stage_bf16(e.stg + 2048, e.lane, pz);
+    flush_chunk<2, 2048, false>(p, P, e, col);
+    if (more) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) pg[v] = ng[v];
+    }
+  }
+}
+
 template <int EPI>
 __device__ __forceinline__ void epi_plain(const Params& p, const EpiUnit& P, const EpiWarp& e,
                                           uint32_t tb, int col0, int cb, int ce) {
@@ -1528,6 +1588,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           dact_load_rows<EPI == EPI_DGATED>(P, e.row0, lane, col0 + cb, pg, pu);
         }
       }
+      if constexpr (EPI == EPI_LINEAR) {
+        if (e.rows_ok && P.in0 != nullptr)
+          dact_load_rows<false>(P, e.row0, lane, col0 + cb, pg, pu);
+      }
       if (!mbar_wait<PAIR>(bar_s(TFULL + acc), aphase, lim, abort_flag)) {
         record_timeout(p, abort_flag);
         if constexpr (EPI == EPI_DGRAD_F8) dgrad_f8_drain(e);
@@ -1543,6 +1607,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           else epi_plain<EPI_STORE_BF16>(p, P, e, tb, col0, cb, ce);
         } else if constexpr (EPI == EPI_ACT_FWD) {
           epi_act_fwd<ACT>(p, P, e, tb, col0, cb, ce);
+        } else if constexpr (EPI == EPI_LINEAR) {
+          epi_linear<ACT>(p, P, e, tb, col0, cb, ce, pg);
         } else if constexpr (EPI == EPI_DGATED) {
           epi_dact<ACT, true>(p, P, e, tb, col0, cb, ce, pg, pu);
         } else if constexpr (EPI == EPI_DACT) {

@@ -58,7 +58,11 @@ enum Epi : int {
   // e5m2(dpre / *sq) (map 0), amax|dpre| -> *amax.  dd is the value the
   // saved-preact path forms from the preact it stores in bf16, so both give
   // the same codes.
-  EPI_DGRAD_F8_RECOMP = 11
+  EPI_DGRAD_F8_RECOMP = 11,
+  // The linear layer: z = acc + bias (in1, bf16 [N]; may be null), D = act(z) +
+  // alpha * residual (in0, bf16, row pitch ld; may be null) -> map 0, and
+  // bf16(z) -> map 1 if requested
+  EPI_LINEAR = 12
 };
 
 __host__ __device__ constexpr bool is_f8(int epi) {
@@ -74,7 +78,15 @@ __host__ __device__ constexpr bool is_recomp(int epi) {
 constexpr int F8_E4M3 = 0, F8_E5M2 = 1;
 
 // The function applied to the gate (gated MLPs) or to the preact (non-gated).
-enum Act : int { ACT_SILU = 0, ACT_RELU_SQ = 1, ACT_GELU_TANH = 2, ACT_RELU = 3, ACT_SIGMOID = 4 };
+// (ACT_NONE: the linear layer without one.)
+enum Act : int {
+  ACT_SILU = 0,
+  ACT_RELU_SQ = 1,
+  ACT_GELU_TANH = 2,
+  ACT_RELU = 3,
+  ACT_SIGMOID = 4,
+  ACT_NONE = 5
+};
 
 // One GEMM D[M,N] = sum_k A[m,k] B[n,k] of a (possibly grouped) launch.
 struct Prob {

@@ -169,36 +169,38 @@ struct Gemm {
   int nmaps = 0;
   int cg = 1;
   bool ok = true;
-  Gemm(const mlp_problem_t& pr, int* counter, int* status, int cg_) : cg(cg_) {
+  Gemm(const mlp_problem_t& pr, int* counter, int* status, int cg_)
+      : Gemm(device_act(pr.act), pr.gate_mult * pr.down_mult, counter, status, cg_) {}
+  Gemm(int act, float scale, int* counter, int* status, int cg_) : cg(cg_) {
     std::memset(&p, 0, sizeof(p));
     p.a_tx_bytes = BM * BK * 2;
-    p.act = device_act(pr.act);
-    p.scale = pr.gate_mult * pr.down_mult;
+    p.act = act;
+    p.scale = scale;
     p.group_m = 16;
     p.counter = counter;
     p.status = status;
     p.timeout_ns = wait_limit_ns();
     p.debug_flags = g_debug_flags.load();
   }
-  // K-major operand: array [rows, K] (row pitch K), box {64, box_rows}
-  int kmajor(const void* ptr, int rows, int K, int box_rows) {
+  // K-major operand: array [rows, K] (row pitch K unless given), box {64, box_rows}
+  int kmajor(const void* ptr, int rows, int K, int box_rows, int pitch = 0) {
     if (nmaps >= MAX_MAPS) { ok = false; return 0; }
-    if (!make_map(&p.maps[nmaps], ptr, K, rows, K, BK, box_rows)) ok = false;
+    if (!make_map(&p.maps[nmaps], ptr, K, rows, pitch ? pitch : K, BK, box_rows)) ok = false;
     return nmaps++;
   }
   // K-major A operand [rows, K]: an output with fewer than 128 rows loads
   // boxes of its rows only (rounded up to 16); the MMA's rows beyond them
   // read stale shared memory and only produce accumulator rows past the
   // output, which the epilogue never stores.
-  int kmajor_a(const void* ptr, int rows, int K) {
+  int kmajor_a(const void* ptr, int rows, int K, int pitch = 0) {
     const int box = rows < BM ? ((rows + 15) / 16) * 16 : BM;
     p.a_tx_bytes = box * BK * 2;
-    return kmajor(ptr, rows, K, box);
+    return kmajor(ptr, rows, K, box, pitch);
   }
-  // MN-major operand: array [K, MN] (row pitch MN), box {64, 64}
-  int mnmajor(const void* ptr, int K, int MN) {
+  // MN-major operand: array [K, MN] (row pitch MN unless given), box {64, 64}
+  int mnmajor(const void* ptr, int K, int MN, int pitch = 0) {
     if (nmaps >= MAX_MAPS) { ok = false; return 0; }
-    if (!make_map(&p.maps[nmaps], ptr, MN, K, MN, 64, BK)) ok = false;
+    if (!make_map(&p.maps[nmaps], ptr, MN, K, pitch ? pitch : MN, 64, BK)) ok = false;
     return nmaps++;
   }
   // e4m3 operands [rows, K] (K bytes per row), boxes {128 k, box_rows}; the
@@ -239,12 +241,12 @@ struct Gemm {
       ok = false;
     return nmaps++;
   }
-  // Epilogue output [rows, cols] (row pitch cols), stored in 32 x 32 boxes;
-  // -1 when the output is not requested.
-  int output(void* ptr, int rows, int cols, bool f32 = false) {
+  // Epilogue output [rows, cols] (row pitch cols unless given), stored in 32 x 32
+  // boxes; -1 when the output is not requested.
+  int output(void* ptr, int rows, int cols, bool f32 = false, int pitch = 0) {
     if (!ptr) return -1;
     if (nmaps >= MAX_MAPS) { ok = false; return -1; }
-    if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, 32, 32, f32,
+    if (!make_map(&p.maps[nmaps], ptr, cols, rows, pitch ? pitch : cols, 32, 32, f32,
                   f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       ok = false;
     return nmaps++;
@@ -438,6 +440,48 @@ inline int opt(const void* ptr) { return (!ptr || aligned16(ptr)) ? MLP_OK : MLP
     int _rc = (__VA_ARGS__);         \
     if (_rc != MLP_OK) return _rc;   \
   } while (0)
+
+// Split-K factor of a bf16-output GEMM [rows, cols] x K whose output tiles
+// cannot fill the GPU: the splits' fp32 partial sums meet in a zeroed region
+// of the workspace (TMA reduce-add) and one elementwise pass converts it to
+// bf16.  It depends on the shape only (a nominal 152 SMs), so the workspace
+// size does too.
+//  - Decode-sized token counts (at most 32 tiles of 128 x 256): about 128
+//    work units with at least 8 k-blocks each.
+//  - `fill` (the forward's down projection): when its 256 x 256 tiles (CTA
+//    pairs) would occupy at most half of the 76 pairs, the smallest split
+//    whose units fill at least 80 % of their last wave, again with at least
+//    8 k-blocks a unit.  (A 512-token Llama-3-8B down projection is 32 such
+//    tiles.)  Measured against the unsplit forward (the gated forward then
+//    runs as one launch): 9-13 % faster at 384 and 512 tokens of the
+//    4096-wide shapes, 3-10 % at 640-1024 tokens of a 2048-wide one; with
+//    more tiles, splitting until the units filled their waves lost to the
+//    one-launch forward.  The backward's dx is left whole: its last wave
+//    shares the GPU with the weight gradients on the second stream.
+constexpr int SPLIT_NOMINAL_SMS = 152;
+inline int bf16_split(int rows, int cols, int K, bool fill) {
+  const long long tiles =
+      (long long)((rows + BM - 1) / BM) * (long long)((cols + MMA_N - 1) / MMA_N);
+  const int kb = (K + BK - 1) / BK;
+  if (kb < 16) return 1;
+  if (tiles <= 32) {
+    int split = static_cast<int>(128 / tiles);
+    if (split > kb / 8) split = kb / 8;
+    return split < 2 ? 1 : split;
+  }
+  if (!fill) return 1;
+  // 256 x 256 tiles on CTA pairs (rows > 128 take pairs)
+  const int pairs = SPLIT_NOMINAL_SMS / 2;
+  const long long ptiles =
+      (long long)((rows + 2 * BM - 1) / (2 * BM)) * (long long)((cols + MMA_N - 1) / MMA_N);
+  if (2 * ptiles > pairs) return 1;
+  for (int s = 2; s <= 8 && kb / s >= 8; ++s) {
+    const long long units = ptiles * s;
+    const long long waves = (units + pairs - 1) / pairs;
+    if (units * 5 >= waves * pairs * 4) return s;
+  }
+  return 1;
+}
 
 // Output tiles (256 columns, 128 x cg rows) of a GEMM output [rows, cols].
 inline long long out_tiles(int rows, int cols, int cg) {

@@ -1,0 +1,31 @@
+// linear.h -- launchers of the linear layer's own kernels (the GEMM instances
+// with its epilogue are launch_gemm<EPI_LINEAR, ...>).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+namespace mlpk {
+
+// out = act(x W^T + bias) + rs * resid for 1 <= M <= LINEAR_STREAM_MAX_M rows
+// (`act` a device activation; bias, resid, pre may be null).  Clears *status.
+constexpr int LINEAR_STREAM_MAX_M = 8;
+cudaError_t launch_linear_stream(const void* x, int ldx, const void* W, const void* bias,
+                                 const void* resid, int ldr, float rs, void* out, int ldo,
+                                 void* pre, int M, int N, int K, int act, cudaStream_t stream,
+                                 bool pdl, int* status);
+
+// The same epilogue on split-K sums acc fp32 [M, N].
+cudaError_t launch_linear_finish(const float* acc, const void* bias, const void* resid, int ldr,
+                                 float rs, void* out, int ldo, void* pre, int M, int N, int act,
+                                 cudaStream_t stream, bool pdl);
+
+// dz = dout * act'(pre) into dz (bf16 [M, N] dense; null: not written) and the
+// column sums of dz over each chunk of rows into part fp32 [chunks, N] (null:
+// not formed); then db[n] = sum over chunks (bf16), or db[n] += (fp32).
+int linear_db_chunks(int M, int N);
+cudaError_t launch_linear_dact(const void* dout, int ldd, const void* pre, void* dz, float* part,
+                               int M, int N, int act, cudaStream_t stream, bool pdl);
+cudaError_t launch_linear_db(const float* part, int chunks, void* db, int N, bool accum,
+                             cudaStream_t stream, bool pdl);
+
+}  // namespace mlpk

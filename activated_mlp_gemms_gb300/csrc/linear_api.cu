@@ -1,0 +1,252 @@
+// linear_api.cu -- the C entry points of mlp_linear.h: argument validation,
+// workspace layout and launch sequences.
+//   mlp_linear_fwd   one GEMM with the bias / activation / residual epilogue
+//                    (split K: fp32 sums, then the epilogue as its own pass;
+//                    up to eight rows: the weight stream)
+//   mlp_linear_bwd   dz = dout act'(z) and the bias gradient's partial sums in
+//                    one pass (no activation: only those sums, dz is dout),
+//                    dx = dz W, and dW = dz^T x on the second stream beside it
+#include "mlp_linear.h"
+
+#include "host.h"
+#include "linear.h"
+
+using namespace mlpk;
+
+namespace {
+
+int check_linear(const mlp_linear_t* p) {
+  if (!p) return MLP_ERR_INVALID_ARG;
+  if (p->M <= 0 || p->N <= 0 || p->K <= 0) return MLP_ERR_INVALID_ARG;
+  if (p->act < MLP_LINEAR_NONE || p->act > MLP_LINEAR_SIGMOID) return MLP_ERR_INVALID_ARG;
+  if (!std::isfinite(p->resid_scale)) return MLP_ERR_INVALID_ARG;
+  auto pitch = [](int ld, int row) { return ld == 0 || ld >= row; };
+  if (!pitch(p->ldx, p->K) || !pitch(p->ldr, p->N) || !pitch(p->ldo, p->N))
+    return MLP_ERR_INVALID_ARG;
+  if (p->N % 8 || p->K % 8 || p->ldx % 8 || p->ldr % 8 || p->ldo % 8) return MLP_ERR_ALIGNMENT;
+  if ((long long)p->M * p->N >= (1LL << 40) || (long long)p->M * p->K >= (1LL << 40))
+    return MLP_ERR_UNSUPPORTED;
+  return MLP_OK;
+}
+
+int linear_act(int act) {
+  switch (act) {
+    case MLP_LINEAR_RELU: return ACT_RELU;
+    case MLP_LINEAR_RELU_SQ: return ACT_RELU_SQ;
+    case MLP_LINEAR_GELU_TANH: return ACT_GELU_TANH;
+    case MLP_LINEAR_SILU: return ACT_SILU;
+    case MLP_LINEAR_SIGMOID: return ACT_SIGMOID;
+    default: return ACT_NONE;
+  }
+}
+
+// The workspace after the control block.
+struct Layout {
+  int split;                      // split-K factor of the forward's GEMM, or of dx
+  size_t part, dz, db, total;     // split-K sums, dz, the bias gradient's partial sums
+};
+Layout layout(const mlp_linear_t* p, bool backward) {
+  Layout L = {};
+  const size_t mn = (size_t)p->M * p->N, mk = (size_t)p->M * p->K;
+  size_t at = CTRL_BYTES;
+  // (dx is left whole from 33 tiles on: its last wave runs beside dW)
+  L.split = backward ? bf16_split(p->M, p->K, p->N, false) : bf16_split(p->M, p->N, p->K, true);
+  L.part = at;
+  if (L.split > 1) at += round256((backward ? mk : mn) * 4);
+  L.dz = at;
+  if (backward && p->act != MLP_LINEAR_NONE) at += round256(mn * 2);
+  L.db = at;
+  if (backward) at += round256((size_t)linear_db_chunks(p->M, p->N) * p->N * 4);
+  L.total = at;
+  return L;
+}
+
+int check_ws(const Layout& L, const void* ws, size_t ws_bytes) {
+  if (!ws) return MLP_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return MLP_ERR_ALIGNMENT;
+  return ws_bytes < L.total ? MLP_ERR_WORKSPACE_TOO_SMALL : MLP_OK;
+}
+
+template <int ACT>
+int run_linear(Gemm& g, Call& c) {
+  return run_act<EPI_LINEAR, false, false, ACT>(g, c, MLP_KERNEL_LINEAR);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mlp_linear_workspace_size(const mlp_linear_t* p, int backward) {
+  if (check_linear(p) != MLP_OK || (backward != 0 && backward != 1)) return 0;
+  return layout(p, backward == 1).total;
+}
+
+int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const void* bias,
+                   const void* residual, void* out, void* pre_save, void* ws, size_t ws_bytes,
+                   void* stream) {
+  MLP_TRY(check_linear(p));
+  MLP_TRY(need(x));
+  MLP_TRY(need(W));
+  MLP_TRY(opt(bias));
+  MLP_TRY(opt(residual));
+  MLP_TRY(need(out));
+  MLP_TRY(opt(pre_save));
+  const Layout L = layout(p, false);
+  MLP_TRY(check_ws(L, ws, ws_bytes));
+  const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
+  const int ldx = p->ldx ? p->ldx : K, ldr = p->ldr ? p->ldr : N, ldo = p->ldo ? p->ldo : N;
+  const bool streamed = M <= LINEAR_STREAM_MAX_M;
+  Call c;
+  MLP_TRY(begin_call(c, ws, stream, !streamed));
+  if (streamed) {
+    const bool pdl = c.pdl();
+    return traced(MLP_KERNEL_LINEAR, c.stream, [&] {
+      return launch_linear_stream(x, ldx, W, bias, residual, ldr, p->resid_scale, out, ldo,
+                                  pre_save, M, N, K, act, c.stream, pdl, c.status);
+    });
+  }
+  Gemm g(act, 1.f, c.counter(), c.status, pick_cg(M));
+  const int mA = g.kmajor_a(x, M, K, ldx);
+  const int mB = g.kmajor(W, N, K, g.b_rows());
+  if (L.split > 1) {
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part);
+    MLP_TRY(cuda_err(cudaMemsetAsync(part, 0, (size_t)M * N * 4, c.stream)));
+    const int oP = g.output(part, M, N, true);
+    Prob& P = g.add(M, N, K, 0, MMA_N, L.split);
+    P.l2a = L2_EVICT_LAST;   // x: re-read by every tile column
+    P.l2b = L2_EVICT_FIRST;  // the weights
+    P.mapA0 = mA;
+    P.mapB0 = mB;
+    P.mapO[0] = oP;
+    MLP_TRY((run<EPI_ACCUM_F32, false, false>(g, c, MLP_KERNEL_LINEAR)));
+    const bool pdl = c.pdl();
+    return traced(MLP_KERNEL_LINEAR_FINISH, c.stream, [&] {
+      return launch_linear_finish(part, bias, residual, ldr, p->resid_scale, out, ldo, pre_save, M,
+                                  N, act, c.stream, pdl);
+    });
+  }
+  const int oO = g.output(out, M, N, false, ldo);
+  const int oZ = g.output(pre_save, M, N);
+  Prob& P = g.add(M, N, K, 0, MMA_N);
+  P.l2a = L2_EVICT_LAST;
+  P.l2b = L2_EVICT_FIRST;
+  P.mapA0 = mA;
+  P.mapB0 = mB;
+  P.mapO[0] = oO;
+  P.mapO[1] = oZ;
+  P.in0 = residual;
+  P.in1 = bias;
+  P.ld = ldr;
+  P.alpha = p->resid_scale;
+  switch (act) {
+    case ACT_RELU: return run_linear<ACT_RELU>(g, c);
+    case ACT_RELU_SQ: return run_linear<ACT_RELU_SQ>(g, c);
+    case ACT_GELU_TANH: return run_linear<ACT_GELU_TANH>(g, c);
+    case ACT_SILU: return run_linear<ACT_SILU>(g, c);
+    case ACT_SIGMOID: return run_linear<ACT_SIGMOID>(g, c);
+    default: return run_linear<ACT_NONE>(g, c);
+  }
+}
+
+int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const void* W,
+                   const void* pre, void* dx, void* dW, void* db, int fuse_grad_accum, void* ws,
+                   size_t ws_bytes, void* stream) {
+  MLP_TRY(check_linear(p));
+  if (fuse_grad_accum != 0 && fuse_grad_accum != 1) return MLP_ERR_INVALID_ARG;
+  const int fuse = fuse_grad_accum;
+  MLP_TRY(need(dout));
+  MLP_TRY(dW ? need(x) : opt(x));
+  MLP_TRY(dx ? need(W) : opt(W));
+  const bool has_act = p->act != MLP_LINEAR_NONE;
+  MLP_TRY(has_act ? need(pre) : opt(pre));
+  MLP_TRY(opt(dx));
+  MLP_TRY(opt(dW));
+  MLP_TRY(opt(db));
+  const Layout L = layout(p, true);
+  MLP_TRY(check_ws(L, ws, ws_bytes));
+  if (!dx && !dW && !db) return MLP_OK;
+  const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
+  const int ldx = p->ldx ? p->ldx : K, ldd = p->ldo ? p->ldo : N;
+  char* base = static_cast<char*>(ws);
+  Call c;
+  MLP_TRY(begin_call(c, ws, stream));
+  const bool split = dx && L.split > 1;
+  float* part = reinterpret_cast<float*>(base + L.part);
+  if (split) MLP_TRY(cuda_err(cudaMemsetAsync(part, 0, (size_t)M * K * 4, c.stream)));
+
+  const void* dz = dout;
+  int ldz = ldd;
+  float* sums = reinterpret_cast<float*>(base + L.db);
+  void* dz_out = has_act && (dx || dW) ? base + L.dz : nullptr;
+  if (dz_out || db) {
+    const bool pdl = c.pdl();
+    MLP_TRY(traced(MLP_KERNEL_LINEAR_DACT, c.stream, [&] {
+      return launch_linear_dact(dout, ldd, pre, dz_out, db ? sums : nullptr, M, N, act, c.stream,
+                                pdl);
+    }));
+  }
+  if (dz_out) {
+    dz = dz_out;
+    ldz = N;
+  }
+
+  // dW and db go to the second stream when dx runs too (mlp_bwd's reasons)
+  Side* side = dx && (dW || db) && !g_trace_flag.load() ? side_stream(c.stream) : nullptr;
+  std::unique_lock<std::mutex> side_lk;
+  if (side) {
+    side_lk = std::unique_lock<std::mutex>(side->mu);
+    MLP_TRY(cuda_err(cudaEventRecord(side->fork, c.stream)));
+  }
+  if (dx) {
+    Gemm g(act, 1.f, c.counter(), c.status, pick_cg(M));
+    const int mA = g.kmajor_a(dz, M, N, ldz);
+    const int mB = g.mnmajor(W, N, K);  // W [N,K]: B(n=k, k=n) is contiguous along K
+    const int oX = split ? g.output(part, M, K, true) : g.output(dx, M, K);
+    Prob& P = g.add(M, K, N, 0, MMA_N, split ? L.split : 1);
+    P.l2a = L2_EVICT_LAST;   // dz: re-read by every tile column
+    P.l2b = L2_EVICT_FIRST;  // W
+    P.mapA0 = mA;
+    P.mapB0 = mB;
+    P.mapO[0] = oX;
+    if (split) {
+      MLP_TRY((run<EPI_ACCUM_F32, false, true>(g, c, MLP_KERNEL_DX)));
+      MLP_TRY(convert_out(c, part, dx, (long long)M * K));
+    } else {
+      MLP_TRY((run<EPI_STORE_BF16, false, true>(g, c, MLP_KERNEL_DX)));
+    }
+  }
+  if (dW || db) {
+    Call cw = c;
+    if (side) {
+      cw.stream = side->stream;
+      cw.launches = 0;  // its first kernel follows an event wait, not a kernel
+      MLP_TRY(cuda_err(cudaStreamWaitEvent(side->stream, side->fork, 0)));
+    }
+    if (db) {
+      const bool pdl = cw.pdl();
+      MLP_TRY(traced(MLP_KERNEL_LINEAR_DB, cw.stream, [&] {
+        return launch_linear_db(sums, linear_db_chunks(M, N), db, N, fuse != 0, cw.stream, pdl);
+      }));
+    }
+    if (dW) {
+      Gemm g(act, 1.f, cw.counter(), cw.status, pick_cg(N < K ? N : K));
+      const int mA = g.mnmajor(dz, M, N, ldz);
+      const int mB = g.mnmajor(x, M, K, ldx);
+      const int oW = g.output(dW, N, K, fuse != 0);
+      Prob& P = g.add(N, K, M, 0, MMA_N, wgrad_split(M, out_tiles(N, K, g.cg), g.cg, fuse));
+      P.l2b = L2_EVICT_LAST;  // x: shared by the tile rows
+      P.mapA0 = mA;
+      P.mapB0 = mB;
+      P.mapO[0] = oW;
+      if (fuse) MLP_TRY((run<EPI_ACCUM_F32, true, true>(g, cw, MLP_KERNEL_WGRAD)));
+      else MLP_TRY((run<EPI_STORE_BF16, true, true>(g, cw, MLP_KERNEL_WGRAD)));
+    }
+    if (side) {
+      MLP_TRY(cuda_err(cudaEventRecord(side->join, side->stream)));
+      MLP_TRY(cuda_err(cudaStreamWaitEvent(c.stream, side->join, 0)));
+    }
+  }
+  return MLP_OK;
+}
+
+}  // extern "C"

@@ -62,48 +62,6 @@ bool gated(const mlp_problem_t* p) {
 
 size_t inter_bytes(const mlp_problem_t* p) { return round256((size_t)p->M * p->I * 2); }
 
-// Split-K factor of a bf16-output GEMM [rows, cols] x K whose output tiles
-// cannot fill the GPU: the splits' fp32 partial sums meet in a zeroed region
-// of the workspace (TMA reduce-add) and one elementwise pass converts it to
-// bf16.  It depends on the shape only (a nominal 152 SMs), so the workspace
-// size does too.
-//  - Decode-sized token counts (at most 32 tiles of 128 x 256): about 128
-//    work units with at least 8 k-blocks each.
-//  - `fill` (the forward's down projection): when its 256 x 256 tiles (CTA
-//    pairs) would occupy at most half of the 76 pairs, the smallest split
-//    whose units fill at least 80 % of their last wave, again with at least
-//    8 k-blocks a unit.  (A 512-token Llama-3-8B down projection is 32 such
-//    tiles.)  Measured against the unsplit forward (the gated forward then
-//    runs as one launch): 9-13 % faster at 384 and 512 tokens of the
-//    4096-wide shapes, 3-10 % at 640-1024 tokens of a 2048-wide one; with
-//    more tiles, splitting until the units filled their waves lost to the
-//    one-launch forward.  The backward's dx is left whole: its last wave
-//    shares the GPU with the weight gradients on the second stream.
-constexpr int SPLIT_NOMINAL_SMS = 152;
-int bf16_split(int rows, int cols, int K, bool fill) {
-  const long long tiles =
-      (long long)((rows + BM - 1) / BM) * (long long)((cols + MMA_N - 1) / MMA_N);
-  const int kb = (K + BK - 1) / BK;
-  if (kb < 16) return 1;
-  if (tiles <= 32) {
-    int split = static_cast<int>(128 / tiles);
-    if (split > kb / 8) split = kb / 8;
-    return split < 2 ? 1 : split;
-  }
-  if (!fill) return 1;
-  // 256 x 256 tiles on CTA pairs (rows > 128 take pairs)
-  const int pairs = SPLIT_NOMINAL_SMS / 2;
-  const long long ptiles =
-      (long long)((rows + 2 * BM - 1) / (2 * BM)) * (long long)((cols + MMA_N - 1) / MMA_N);
-  if (2 * ptiles > pairs) return 1;
-  for (int s = 2; s <= 8 && kb / s >= 8; ++s) {
-    const long long units = ptiles * s;
-    const long long waves = (units + pairs - 1) / pairs;
-    if (units * 5 >= waves * pairs * 4) return s;
-  }
-  return 1;
-}
-
 // K of the bf16-output GEMM of a mode: the down projection (forward) or dx.
 int split_k_of(const mlp_problem_t* p, int mode) {
   if (mode == MLP_MODE_FWD || mode == MLP_MODE_INFER) return p->I;
@@ -956,6 +914,10 @@ const char* mlp_kernel_name(int tag) {
     case MLP_KERNEL_MOE_DISPATCH: return "moe_dispatch";
     case MLP_KERNEL_MOE_COMBINE: return "moe_combine";
     case MLP_KERNEL_MOE_COMBINE_BWD: return "moe_combine_bwd";
+    case MLP_KERNEL_LINEAR: return "linear";
+    case MLP_KERNEL_LINEAR_FINISH: return "linear_finish";
+    case MLP_KERNEL_LINEAR_DACT: return "linear_dact";
+    case MLP_KERNEL_LINEAR_DB: return "linear_db";
     default: return "unknown";
   }
 }
