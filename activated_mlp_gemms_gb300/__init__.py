@@ -439,12 +439,15 @@ from .autograd import mlp_block_func, mlp_func  # noqa: E402  (differentiable fo
 __all__ += ["mlp_func", "mlp_block_func"]
 
 from . import experts, linear_op  # noqa: E402  (mixture of experts; linear layer)
-from .experts import (Moe, alloc_moe_plan, mlp_moe_combine, mlp_moe_combine_bwd,  # noqa: E402
-                  mlp_moe_dispatch, mlp_moe_dispatch_bwd, mlp_moe_rows, mlp_moe_sort, moe,
-                  moe_plan_views)
+from .experts import (Moe, alloc_moe_plan, alloc_moe_workspace, mlp_moe_combine,  # noqa: E402
+                      mlp_moe_combine_bwd, mlp_moe_dispatch, mlp_moe_dispatch_bwd,
+                      mlp_moe_experts_bwd, mlp_moe_experts_fwd, mlp_moe_fwd_infer, mlp_moe_rows,
+                      mlp_moe_sort, mlp_moe_workspace_size, moe, moe_plan_views)
 
 __all__ += ["Moe", "moe", "alloc_moe_plan", "moe_plan_views", "mlp_moe_rows", "mlp_moe_sort",
-            "mlp_moe_dispatch", "mlp_moe_dispatch_bwd", "mlp_moe_combine", "mlp_moe_combine_bwd"]
+            "mlp_moe_dispatch", "mlp_moe_dispatch_bwd", "mlp_moe_combine", "mlp_moe_combine_bwd",
+            "mlp_moe_experts_fwd", "mlp_moe_experts_bwd", "mlp_moe_fwd_infer",
+            "mlp_moe_workspace_size", "alloc_moe_workspace"]
 
 from .linear_op import (LINEAR_ACTS, Linear, alloc_linear_workspace, linear,  # noqa: E402
                         mlp_linear_bwd, mlp_linear_fwd, mlp_linear_workspace_size)

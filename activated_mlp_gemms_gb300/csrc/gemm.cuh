@@ -48,6 +48,9 @@ constexpr int MLP_ERR_TIMEOUT_CODE = -6;
 
 struct Work {
   int prob, tm, tn, kb_begin, kb_end;
+  // GRP: the expert, and the rows [row0, row_end) of the sorted layout: the
+  // output tile's (A K-major), or those the gradient sums over (A MN-major)
+  int expert, row0, row_end;
 };
 
 __device__ __forceinline__ Work decode_unit(const Params& p, int unit) {
@@ -72,7 +75,68 @@ __device__ __forceinline__ Work decode_unit(const Params& p, int unit) {
   int kb_total = P.kb0 + P.kb1;
   w.kb_begin = ks * P.kper;
   w.kb_end = min(kb_total, w.kb_begin + P.kper);
+  w.expert = w.row0 = w.row_end = 0;
   return w;
+}
+
+// GRP, A K-major: unit -> (row tile of the plan, tile column), the row tiles
+// in groups of group_m as above.
+__device__ __forceinline__ Work decode_row_unit(const Params& p, int unit, int ntiles) {
+  const Prob& P = p.prob[0];
+  const int per_group = p.group_m * P.tiles_n;
+  const int g = unit / per_group;
+  const int first_m = g * p.group_m;
+  const int gsz = min(ntiles - first_m, p.group_m);
+  const int r = unit - g * per_group;
+  Work w;
+  w.prob = 0;
+  w.tm = first_m + r % gsz;
+  w.tn = r / gsz;
+  w.kb_begin = 0;
+  w.kb_end = P.kb0 + P.kb1;
+  const int4 t = __ldg(reinterpret_cast<const int4*>(p.tiles + w.tm));
+  w.expert = t.x;
+  w.row0 = t.y;
+  w.row_end = t.z;
+  return w;
+}
+
+// GRP, A MN-major: unit -> (problem, expert, output tile); K runs over the
+// expert's rows.  An expert without rows sums one k-block past the end of the
+// buffers, which TMA fills with zeros.
+__device__ __forceinline__ Work decode_expert_unit(const Params& p, int unit) {
+  int pi = 0;
+  while (pi + 1 < p.nprob && unit >= p.prob[pi + 1].unit_begin) ++pi;
+  const Prob& P = p.prob[pi];
+  const int u = unit - P.unit_begin;
+  const int tiles = P.tiles_m * P.tiles_n;
+  Work w;
+  w.prob = pi;
+  w.expert = u / tiles;
+  const int t = u - w.expert * tiles;
+  const int per_group = p.group_m * P.tiles_n;
+  const int g = t / per_group;
+  const int first_m = g * p.group_m;
+  const int gsz = min(P.tiles_m - first_m, p.group_m);
+  const int r = t - g * per_group;
+  w.tm = first_m + r % gsz;
+  w.tn = r / gsz;
+  w.row0 = __ldg(p.offsets + w.expert);
+  w.row_end = __ldg(p.offsets + w.expert + 1);
+  if (w.row_end <= w.row0) {
+    w.row0 = p.rows;
+    w.row_end = p.rows + MOE_ALIGN;
+  }
+  w.kb_begin = 0;
+  w.kb_end = (w.row_end - w.row0 + BK - 1) / BK;
+  return w;
+}
+
+template <bool GRP, bool A_MN>
+__device__ __forceinline__ Work decode(const Params& p, int unit, int ntiles) {
+  if constexpr (!GRP) return decode_unit(p, unit);
+  else if constexpr (A_MN) return decode_expert_unit(p, unit);
+  else return decode_row_unit(p, unit, ntiles);
 }
 
 // The units of a problem that run the gated forward epilogue.
@@ -135,6 +199,7 @@ struct EpiWarp {
   bool rows_ok;  // any of the 32 rows inside the output
   uint32_t box;  // EPI_DACT_RECOMP: which of the two boxes the next chunk fills
   float rs;      // this lane's row scale (the block's RMS norm; 1 without it)
+  int expert;    // GRP weight gradients: which matrix of the output stack
   // EPI_DGRAD_F8 with TMA-loaded preact boxes: the two halves of the staging
   // box each have a barrier (ebar, ebar + 8); ephase holds their parities,
   // epend the halves with a load in flight (bit per half)
@@ -216,8 +281,9 @@ __device__ __forceinline__ void staging_acquire(const EpiWarp& e) {
   __syncwarp();
 }
 
-// Store the staged boxes of outputs whose map exists at (col, row0).
-template <int NOUT, int OUT_BYTES, bool REDUCE>
+// Store the staged boxes of outputs whose map exists at (col, row0) (STACK: of
+// the expert's matrix of a 3-D output).
+template <int NOUT, int OUT_BYTES, bool REDUCE, bool STACK = false>
 __device__ __forceinline__ void flush_chunk(const Params& p, const EpiUnit& P, const EpiWarp& e,
                                             int col) {
   fence_proxy_async_smem();
@@ -227,7 +293,10 @@ __device__ __forceinline__ void flush_chunk(const Params& p, const EpiUnit& P, c
     for (int o = 0; o < NOUT; ++o) {
       if (P.out[o]) {
         const CUtensorMap* m = P.out[o];
-        if constexpr (REDUCE) tma_reduce_add_2d(m, e.stg + o * OUT_BYTES, col, e.row0);
+        if constexpr (STACK && REDUCE)
+          tma_reduce_add_3d(m, e.stg + o * OUT_BYTES, col, e.row0, e.expert);
+        else if constexpr (STACK) tma_store_3d(m, e.stg + o * OUT_BYTES, col, e.row0, e.expert);
+        else if constexpr (REDUCE) tma_reduce_add_2d(m, e.stg + o * OUT_BYTES, col, e.row0);
         else tma_store_2d(m, e.stg + o * OUT_BYTES, col, e.row0);
       }
     }
@@ -945,7 +1014,7 @@ __device__ __forceinline__ void epi_linear(const Params& p, const EpiUnit& P, co
   }
 }
 
-template <int EPI>
+template <int EPI, bool STACK = false>
 __device__ __forceinline__ void epi_plain(const Params& p, const EpiUnit& P, const EpiWarp& e,
                                           uint32_t tb, int col0, int cb, int ce) {
 #pragma unroll 1
@@ -990,10 +1059,10 @@ __device__ __forceinline__ void epi_plain(const Params& p, const EpiUnit& P, con
           q[j] = pack_bf16x2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
       }
       stage_bf16(e.stg, e.lane, q);
-      flush_chunk<1, 2048, false>(p, P, e, col);
+      flush_chunk<1, 2048, false, STACK>(p, P, e, col);
     } else {
       stage_f32(e.stg, e.lane, d);
-      flush_chunk<1, 4096, true>(p, P, e, col);
+      flush_chunk<1, 4096, true, STACK>(p, P, e, col);
     }
   }
 }
@@ -1068,16 +1137,20 @@ struct UnitLoads {
   const CUtensorMap* i1;
   int icol;               // the tile's first column
   int l2a, l2b;           // the operands' L2 policies (Prob::l2a, l2b)
+  int expert;             // GRP: the weights' matrix of the stack (A K-major)
+  int krow0;              // GRP: first K row (A MN-major)
 };
 
-template <int EPI, int CG>
+template <int EPI, int CG, bool GRP = false, bool A_MN = false>
 __device__ __forceinline__ UnitLoads unit_loads(const Params& p, const Prob& P, const Work& w,
                                                 uint32_t rank) {
   UnitLoads L;
   L.a0 = &p.maps[P.mapA0];
   L.a1 = &p.maps[P.mapA1];
-  L.m0 = w.tm * (BM * CG) + static_cast<int>(rank) * BM;
-  L.kb0 = P.kb0;
+  L.m0 = (GRP && !A_MN ? w.row0 : w.tm * (BM * CG)) + static_cast<int>(rank) * BM;
+  L.expert = w.expert;
+  L.krow0 = w.row0;
+  L.kb0 = GRP && A_MN ? w.kb_end : P.kb0;  // (an expert's rows are one segment)
   L.l2a = P.l2a;
   L.l2b = P.l2b;
   if (gated_unit<EPI>(w.prob)) {
@@ -1112,7 +1185,9 @@ __device__ __forceinline__ UnitLoads unit_loads(const Params& p, const Prob& P, 
 //   {128 m, 128 k}; B MN-major 2 / CG boxes {128 n, 128 k}.
 //   EPI_DACT_RECOMP, EPI_DGRAD_F8_RECOMP: segment 0 B K-major (W1), segment 1
 //   B MN-major (Wd, W2_8).
-template <int EPI, bool A_MN, bool B_MN, int CG>
+//   GRP: the weights (B, when A is K-major) are a stack, loaded at L.expert;
+//   the weight gradients' operands start at K row L.krow0.
+template <int EPI, bool A_MN, bool B_MN, int CG, bool GRP = false>
 __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, uint32_t sA,
                                            uint32_t sB, uint32_t full, uint64_t polA,
                                            uint64_t polB) {
@@ -1121,6 +1196,12 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
     if constexpr (CG == 2) tma_load_2d_pair(dst, m, c0, c1, full, pol);
     else tma_load_2d(dst, m, c0, c1, full, pol);
   };
+  auto ldw = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {  // weights
+    if constexpr (!GRP || A_MN) ld(dst, m, c0, c1);
+    else if constexpr (CG == 2) tma_load_3d_pair(dst, m, c0, c1, L.expert, full, pol);
+    else tma_load_3d(dst, m, c0, c1, L.expert, full, pol);
+  };
+  if constexpr (GRP && A_MN) kc += L.krow0;
   const CUtensorMap* mA = seg == 0 ? L.a0 : L.a1;
   if constexpr (!A_MN) {
     ld(sA, mA, kc, L.m0);
@@ -1132,31 +1213,35 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
   }
   pol = polB;
   if constexpr (EPI == EPI_GATED_FWD) {
-    ld(sB, L.b0, kc, L.n0);
-    if constexpr (CG == 1) ld(sB + 16384, L.b1, kc, L.n0);
+    ldw(sB, L.b0, kc, L.n0);
+    if constexpr (CG == 1) ldw(sB + 16384, L.b1, kc, L.n0);
   } else {
     const CUtensorMap* mB = seg == 0 ? L.b0 : L.b1;
     // the fused recomputes read W1 (K-major) in segment 0, Wd (MN-major) in 1
     const bool b_mn = is_recomp(EPI) ? seg == 1 : B_MN;
     if (!b_mn) {
-      ld(sB, mB, kc, L.n0);
+      ldw(sB, mB, kc, L.n0);
     } else if constexpr (is_f8(EPI)) {
 #pragma unroll
       for (int j = 0; j < 2 / CG; ++j) ld(sB + j * 16384, mB, L.n0 + j * 128, kc);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4 / CG; ++j) ld(sB + j * 8192, mB, L.n0 + j * 64, kc);
+      for (int j = 0; j < 4 / CG; ++j) ldw(sB + j * 8192, mB, L.n0 + j * 64, kc);
     }
   }
 }
 
 // ACT: the activation of the activation epilogues (Act; 0 for the others).
-template <int EPI, bool A_MN, bool B_MN, int CG, int ACT>
+template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP>
 __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   using C = Cfg<EPI, CG>;
   constexpr bool PAIR = CG == 2;
   static_assert(EPI != EPI_FWD_FUSED || CG == 2, "the fused forward runs on CTA pairs");
+  static_assert(!GRP || (!is_f8(EPI) && !is_recomp(EPI) && EPI != EPI_FWD_FUSED),
+                "no grouped form of this epilogue");
+  constexpr bool GRP_ROWS = GRP && !A_MN;  // output tiles are the plan's row tiles
+  constexpr bool GRP_SUM = GRP && A_MN;    // every expert's own sum over its rows
   // 8-bit operands: a 128-byte k-block row holds 128 elements (bf16: 64)
   constexpr bool F8 = is_f8(EPI);
   constexpr int KE = F8 ? 2 * BK : BK;
@@ -1242,6 +1327,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
 
   const uint64_t lim = p.timeout_ns;
   const int ncl = gridDim.x / CG;          // clusters (CTA groups) in the grid
+  // GRP over rows: how many tiles there are is in the plan
+  const int ntiles = GRP_ROWS ? __ldg(p.ntiles) : 0;
+  const int total_units = GRP_ROWS ? ntiles * p.prob[0].tiles_n : p.total_units;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -1283,13 +1371,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           constexpr bool EARLY_PUB = !A_MN;
           if (!EARLY_PUB || first_pub) {
             first_pub = false;
-            if (!publish(unit < p.total_units ? unit : -1)) {
+            if (!publish(unit < total_units ? unit : -1)) {
               ok = false;
               break;
             }
           }
-          if (unit >= p.total_units) break;
-          const Work w = decode_unit(p, unit);
+          if (unit >= total_units) break;
+          const Work w = decode<GRP, A_MN>(p, unit, ntiles);
           // The next unit, fetched now and needed when it is published.  A
           // down unit of the fused forward (K = I, several times a gate/up
           // unit's length) fetches it only when it publishes it, half-way
@@ -1302,7 +1390,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             if (late_claim) next = atomicAdd(p.counter, 1);
           };
           bool published = !EARLY_PUB;
-          const UnitLoads L = unit_loads<EPI, CG>(p, p.prob[w.prob], w, rank);
+          const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
           if constexpr (EpiTraits<EPI>::DACT) {
             // the epilogue reads this tile's saved inputs a tile or two later
             if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
@@ -1327,13 +1415,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             const int seg = kb < L.kb0 ? 0 : 1;
             const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
             const uint32_t sA = base_s + stage * C::STAGE;
-            load_stage<EPI, A_MN, B_MN, CG>(L, seg, kc, sA, sA + C::A_BYTES, full,
+            load_stage<EPI, A_MN, B_MN, CG, GRP>(L, seg, kc, sA, sA + C::A_BYTES, full,
                                             pol_of(L.l2a), pol_of(L.l2b));
             ++issued;
             if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
             if (!published && kb == w.kb_begin + (w.kb_end - w.kb_begin) / 2) {
               claim();
-              if (!publish(next < p.total_units ? next : -1)) {
+              if (!publish(next < total_units ? next : -1)) {
                 ok = false;
                 break;
               }
@@ -1342,7 +1430,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           }
           if (ok && !published) {
             claim();
-            if (!publish(next < p.total_units ? next : -1)) ok = false;
+            if (!publish(next < total_units ? next : -1)) ok = false;
           }
           unit = next;
         } else {
@@ -1355,8 +1443,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           if (v < 0) break;
-          const Work w = decode_unit(p, v);
-          const UnitLoads L = unit_loads<EPI, CG>(p, p.prob[w.prob], w, rank);
+          const Work w = decode<GRP, A_MN>(p, v, ntiles);
+          const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
           if constexpr (EpiTraits<EPI>::DACT) {
             if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
             if (L.i1) tma_prefetch_l2_2d(L.i1, L.icol, L.m0);
@@ -1376,7 +1464,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             const int seg = kb < L.kb0 ? 0 : 1;
             const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
             const uint32_t sA = base_s + stage * C::STAGE;
-            load_stage<EPI, A_MN, B_MN, CG>(L, seg, kc, sA, sA + C::A_BYTES,
+            load_stage<EPI, A_MN, B_MN, CG, GRP>(L, seg, kc, sA, sA + C::A_BYTES,
                                             full_lead + 8u * stage, pol_of(L.l2a),
                                             pol_of(L.l2b));
             ++issued;
@@ -1426,7 +1514,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         mbar_arrive(bar_s(SEMPTY + slot));
         if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
         if (unit < 0) break;
-        const Work w = decode_unit(p, unit);
+        const Work w = decode<GRP, A_MN>(p, unit, ntiles);
         // the fused recompute's second K segment goes to the other accumulator
         const int kswitch = is_recomp(EPI) ? p.prob[w.prob].kb0 : -1;
         if (!mbar_wait<PAIR>(bar_s(TEMPTY + acc), aphase ^ 1u, lim, abort_flag)) { ok = false; break; }
@@ -1454,8 +1542,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           const uint32_t sA = base_s + stage * C::STAGE;
           const uint32_t sB = sA + C::A_BYTES;
           const bool b_mn = B_MN || seg1;
+          // GRP_SUM: the last k-block's steps past the expert's rows hold the
+          // next expert's (an expert's rows are whole steps)
+          const int k_rows = GRP_SUM ? w.row_end - w.row0 - kb * BK : BK;
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k) {
+            if (GRP_SUM && 16 * k >= k_rows) break;
             // MN-major: bf16 K=16 steps of 16 rows, 8-bit K=32 steps of 32 rows
             constexpr uint32_t MN_STEP = F8 ? 4096 : 2048, MN_LBO = F8 ? 16384 : 8192;
             const uint64_t ad = A_MN ? sdesc_sw128(sA + k * MN_STEP, MN_LBO, 1024)
@@ -1539,13 +1631,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
       }
       if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
       if (unit < 0) break;
-      const Work w = decode_unit(p, unit);
+      const Work w = decode<GRP, A_MN>(p, unit, ntiles);
       const int pi = w.prob;
-      const EpiUnit P = epi_unit<EPI>(p, p.prob[pi],
+      EpiUnit P = epi_unit<EPI>(p, p.prob[pi],
                                       pi == 0 ? f8_deq[0] : pi == 1 ? f8_deq[1] : f8_deq[2],
                                       pi == 0 ? f8_inv[0] : pi == 1 ? f8_inv[1] : f8_inv[2],
                                       f8_deq0);
-      e.row0 = w.tm * C::TILE_M + static_cast<int>(rank) * BM + q * 32;
+      e.row0 = (GRP_ROWS ? w.row0 : w.tm * C::TILE_M) + static_cast<int>(rank) * BM + q * 32;
+      if constexpr (GRP_ROWS) {
+        // rows end with the expert's, at a multiple of 16: a warp with 16
+        // rows left stores boxes of 16
+        P.M = w.row_end;
+        if (w.row_end - e.row0 < 32) {
+#pragma unroll
+          for (int o = 0; o < 3; ++o)
+            if (P.out[o]) P.out[o] = &p.maps[p.prob[pi].mapO16[o]];
+        }
+      }
+      e.expert = w.expert;
       e.rows_ok = e.row0 < P.M;
       e.rs = (P.rstd && e.row0 + lane < P.M) ? P.rstd[e.row0 + lane] : 1.f;
       const int tile_n = tile_n_of<EPI>(pi);
@@ -1627,7 +1730,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         } else if constexpr (EPI == EPI_DGRAD_F8_RECOMP) {
           epi_recomp_f8_dh(P, e, tb, col0, cb, dd);
         } else {
-          epi_plain<EPI>(p, P, e, tb, col0, cb, ce);
+          epi_plain<EPI, GRP_SUM>(p, P, e, tb, col0, cb, ce);
         }
       }
       tc_fence_before();
@@ -1657,9 +1760,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
   }
 }
 
-template <int EPI, bool A_MN, bool B_MN, int CG, int ACT>
+template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP>
 cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl) {
-  auto kern = k_mlp_gemm<EPI, A_MN, B_MN, CG, ACT>;
+  auto kern = k_mlp_gemm<EPI, A_MN, B_MN, CG, ACT, GRP>;
   static std::atomic<unsigned> configured_dev_mask{0};  // devices that got the smem attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1698,9 +1801,9 @@ cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl
 }
 
 // Largest number of CTA pairs that can be co-resident (0 on error).
-template <int EPI, bool A_MN, bool B_MN, int CG, int ACT>
+template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP>
 int max_groups() {
-  auto kern = k_mlp_gemm<EPI, A_MN, B_MN, CG, ACT>;
+  auto kern = k_mlp_gemm<EPI, A_MN, B_MN, CG, ACT, GRP>;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "moe.h"
+
 namespace mlpk {
 
 // Tile: (128 x CTA-group size) x (MMA N = 256) x BK, bf16 operands, fp32
@@ -104,6 +106,8 @@ struct Prob {
   int mapE;               // EPI_DGRAD_F8: map of in0 with the epilogue warps' 32 x 32 bf16
                           // boxes (64-byte swizzle), loaded by TMA (-1: plain loads)
   int mapO[3];            // tensor maps of the epilogue's outputs (-1: output not written)
+  int mapO16[3];          // GRP over token rows: the same outputs with boxes of 16 rows, for the
+                          // last rows of an expert
   void* out0;
   void* out1;
   void* out2;
@@ -145,15 +149,25 @@ struct Params {  // 64-byte aligned through CUtensorMap
   int* dep;               // EPI_FWD_FUSED: per 256-row block, the gate/up epilogue warps whose
                           // stores have completed (one count per warp and tile; zero at launch)
   unsigned long long timeout_ns;
+  // GRP (the experts' GEMMs): the row tiles of the sorted layout and their
+  // number, and the experts' first rows [E + 1] (device, from the plan)
+  const MoeTile* tiles;
+  const int* ntiles;
+  const int* offsets;
+  int rows;               // rows of the sorted layout's buffers
 };
 
 // Host-side launcher and co-residency query, explicitly instantiated in the
 // kernel translation units.  CG = CTA-group size (1: single CTA, 2: CTA
 // pair with tcgen05 cta_group::2); `grid` is in CTAs (a multiple of CG).
 // ACT is the activation of the activation epilogues (0 for the others).
-template <int EPI, bool A_MN, bool B_MN, int CG, int ACT>
+// GRP: the rows are the sorted layout of a mixture of experts, the weights a
+// stack [E, ., .] (3-D maps).  With A K-major the output tiles are the plan's
+// row tiles, each against its expert's weights; with A MN-major (the weight
+// gradients) every expert has its own output [E, M, N], summed over its rows.
+template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP = false>
 cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl);
-template <int EPI, bool A_MN, bool B_MN, int CG, int ACT>
+template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP = false>
 int max_groups();
 
 // Elementwise postact a = s*act(G)*U (U == nullptr: non-gated), n elements;

@@ -51,9 +51,11 @@ struct MapKey {
   uint64_t inner, outer, stride;
   uint32_t box0, box1;
   int dtype, swizzle;
+  uint64_t depth, stride2;
   bool operator==(const MapKey& o) const {
     return ptr == o.ptr && inner == o.inner && outer == o.outer && stride == o.stride &&
-           box0 == o.box0 && box1 == o.box1 && dtype == o.dtype && swizzle == o.swizzle;
+           box0 == o.box0 && box1 == o.box1 && dtype == o.dtype && swizzle == o.swizzle &&
+           depth == o.depth && stride2 == o.stride2;
   }
 };
 struct MapKeyHash {
@@ -64,6 +66,8 @@ struct MapKeyHash {
     h = h * 1000003u ^ k.stride;
     h = h * 1000003u ^ (static_cast<size_t>(k.box0) << 16 | k.box1);
     h = h * 1000003u ^ (static_cast<size_t>(k.dtype) << 8 | static_cast<size_t>(k.swizzle));
+    h = h * 1000003u ^ k.depth;
+    h = h * 1000003u ^ k.stride2;
     return h;
   }
 };
@@ -75,11 +79,14 @@ inline std::unordered_map<MapKey, CUtensorMap, MapKeyHash> g_map_cache;
 // zero and are not written.  bf16 operands use the 128-byte swizzle; the
 // epilogue's 32 x 32 output boxes use the 64-byte (bf16) or 128-byte (fp32)
 // swizzle of the staging buffers.
-// dtype: 0 bf16, 1 fp32, 2 e4m3 bytes (uint8).
+// dtype: 0 bf16, 1 fp32, 2 e4m3 bytes (uint8).  depth > 0: a stack of `depth`
+// such arrays, pitch2 elements apart, as a 3-D map with boxes one array deep.
 inline bool make_map(CUtensorMap* out, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
               uint32_t box0, uint32_t box1, int dtype = 0,
-              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-  MapKey key{ptr, inner, outer, pitch, box0, box1, dtype, static_cast<int>(swz)};
+              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B,
+                     uint64_t depth = 0, uint64_t pitch2 = 0) {
+  MapKey key{ptr, inner, outer, pitch, box0, box1, dtype, static_cast<int>(swz),
+             depth, pitch2};
   {
     std::lock_guard<std::mutex> lk(g_map_mu);
     auto it = g_map_cache.find(key);
@@ -93,12 +100,12 @@ inline bool make_map(CUtensorMap* out, const void* ptr, uint64_t inner, uint64_t
   const CUtensorMapDataType dt = dtype == 1   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                  : dtype == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {pitch * esize};
-  cuuint32_t box[2] = {box0, box1};
-  cuuint32_t estr[2] = {1, 1};
+  cuuint64_t dims[3] = {inner, outer, depth};
+  cuuint64_t strides[2] = {pitch * esize, pitch2 * esize};
+  cuuint32_t box[3] = {box0, box1, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
   CUtensorMap m;
-  CUresult r = g_encode(&m, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  CUresult r = g_encode(&m, dt, depth ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
@@ -251,6 +258,42 @@ struct Gemm {
       ok = false;
     return nmaps++;
   }
+  // Stacks [depth, rows, cols] (dense): a K-major weight operand, an MN-major
+  // one ([K, MN] each), and a stack of outputs
+  int kmajor_stack(const void* ptr, int depth, int rows, int K, int box_rows) {
+    if (nmaps >= MAX_MAPS) { ok = false; return 0; }
+    if (!make_map(&p.maps[nmaps], ptr, K, rows, K, BK, box_rows, 0, CU_TENSOR_MAP_SWIZZLE_128B,
+                  depth, (uint64_t)rows * K))
+      ok = false;
+    return nmaps++;
+  }
+  int mnmajor_stack(const void* ptr, int depth, int K, int MN) {
+    if (nmaps >= MAX_MAPS) { ok = false; return 0; }
+    if (!make_map(&p.maps[nmaps], ptr, MN, K, MN, 64, BK, 0, CU_TENSOR_MAP_SWIZZLE_128B, depth,
+                  (uint64_t)K * MN))
+      ok = false;
+    return nmaps++;
+  }
+  int output_stack(void* ptr, int depth, int rows, int cols, bool f32) {
+    if (!ptr) return -1;
+    if (nmaps >= MAX_MAPS) { ok = false; return -1; }
+    if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, 32, 32, f32,
+                  f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, depth,
+                  (uint64_t)rows * cols))
+      ok = false;
+    return nmaps++;
+  }
+  // bf16 output of P over the sorted rows: boxes of 32 rows, and of 16 for the
+  // last rows of an expert
+  void output_rows(Prob& P, int i, void* ptr, int rows, int cols) {
+    P.mapO[i] = output(ptr, rows, cols);
+    P.mapO16[i] = -1;
+    if (!ptr) return;
+    if (nmaps >= MAX_MAPS) { ok = false; return; }
+    if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, 32, 16, 0, CU_TENSOR_MAP_SWIZZLE_64B))
+      ok = false;
+    P.mapO16[i] = nmaps++;
+  }
   // ke: K elements per k-block (bf16 64, e4m3 128: a 128-byte row either way)
   Prob& add(int M, int N, int K0, int K1, int tile_n, int ksplit = 1, int ke = BK) {
     Prob& P = p.prob[p.nprob++];
@@ -365,7 +408,7 @@ int traced(int tag, cudaStream_t s, F&& launch) {
 }
 
 // Co-resident CTA groups of a kernel instance on the current device (cached).
-template <int EPI, bool A_MN, bool B_MN, int CG, int ACT>
+template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP = false>
 int groups_cached() {
   static std::atomic<int> cache[64];
   int dev = 0;
@@ -374,23 +417,23 @@ int groups_cached() {
     int v = cache[dev].load();
     if (v > 0) return v;
   }
-  int v = max_groups<EPI, A_MN, B_MN, CG, ACT>();
+  int v = max_groups<EPI, A_MN, B_MN, CG, ACT, GRP>();
   if (v > 0 && dev >= 0 && dev < 64) cache[dev].store(v);
   return v;
 }
 
-template <int EPI, bool A_MN, bool B_MN, int ACT>
+template <int EPI, bool A_MN, bool B_MN, int ACT, bool GRP = false>
 int run_act(Gemm& g, Call& c, int tag) {
   if (!g.ok) return MLP_ERR_CUDA;
   if (g.p.total_units == 0) return MLP_OK;
   g.p.nmaps = g.nmaps;
   const bool pdl = c.pdl();
   if (g.cg == 2) {
-    const int groups = groups_cached<EPI, A_MN, B_MN, 2, ACT>();
+    const int groups = groups_cached<EPI, A_MN, B_MN, 2, ACT, GRP>();
     if (groups <= 0) return MLP_ERR_CUDA;
     const int n = g.p.total_units < groups ? g.p.total_units : groups;
     return traced(tag, c.stream,
-                  [&] { return launch_gemm<EPI, A_MN, B_MN, 2, ACT>(g.p, 2 * n, c.stream, pdl); });
+                  [&] { return launch_gemm<EPI, A_MN, B_MN, 2, ACT, GRP>(g.p, 2 * n, c.stream, pdl); });
   }
   if constexpr (EPI == EPI_FWD_FUSED) {
     return MLP_ERR_UNSUPPORTED;  // CTA pairs only
@@ -398,33 +441,33 @@ int run_act(Gemm& g, Call& c, int tag) {
     const int sms = num_sms();
     const int n = g.p.total_units < sms ? g.p.total_units : sms;
     return traced(tag, c.stream, [&] {
-      return launch_gemm<EPI, A_MN, B_MN, 1, ACT>(g.p, n < 1 ? 1 : n, c.stream, pdl);
+      return launch_gemm<EPI, A_MN, B_MN, 1, ACT, GRP>(g.p, n < 1 ? 1 : n, c.stream, pdl);
     });
   }
 }
 
 // Kernels without an activation epilogue.
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool GRP = false>
 int run(Gemm& g, Call& c, int tag) {
-  return run_act<EPI, A_MN, B_MN, 0>(g, c, tag);
+  return run_act<EPI, A_MN, B_MN, 0, GRP>(g, c, tag);
 }
 
 // Activation epilogues: one kernel instance per activation.
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool GRP = false>
 int run_gated(Gemm& g, Call& c, int tag) {
   switch (g.p.act) {
-    case ACT_RELU: return run_act<EPI, A_MN, B_MN, ACT_RELU>(g, c, tag);
-    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, ACT_GELU_TANH>(g, c, tag);
-    case ACT_SIGMOID: return run_act<EPI, A_MN, B_MN, ACT_SIGMOID>(g, c, tag);
-    default: return run_act<EPI, A_MN, B_MN, ACT_SILU>(g, c, tag);
+    case ACT_RELU: return run_act<EPI, A_MN, B_MN, ACT_RELU, GRP>(g, c, tag);
+    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, ACT_GELU_TANH, GRP>(g, c, tag);
+    case ACT_SIGMOID: return run_act<EPI, A_MN, B_MN, ACT_SIGMOID, GRP>(g, c, tag);
+    default: return run_act<EPI, A_MN, B_MN, ACT_SILU, GRP>(g, c, tag);
   }
 }
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool GRP = false>
 int run_nongated(Gemm& g, Call& c, int tag) {
   switch (g.p.act) {
-    case ACT_RELU: return run_act<EPI, A_MN, B_MN, ACT_RELU>(g, c, tag);
-    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, ACT_GELU_TANH>(g, c, tag);
-    default: return run_act<EPI, A_MN, B_MN, ACT_RELU_SQ>(g, c, tag);
+    case ACT_RELU: return run_act<EPI, A_MN, B_MN, ACT_RELU, GRP>(g, c, tag);
+    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, ACT_GELU_TANH, GRP>(g, c, tag);
+    default: return run_act<EPI, A_MN, B_MN, ACT_RELU_SQ, GRP>(g, c, tag);
   }
 }
 

@@ -32,6 +32,132 @@ int need4(const void* ptr) {
 
 bool w_bf16(const mlp_moe_t* p) { return p->weights_type == MLP_MOE_W_BF16; }
 
+bool gated(const mlp_moe_t* p) {
+  return p->act == MLP_ACT_SWIGLU || p->act == MLP_ACT_REGLU || p->act == MLP_ACT_GEGLU ||
+         p->act == MLP_ACT_GLU;
+}
+
+// The calls that run the experts.
+int check_experts(const mlp_moe_t* p) {
+  MLP_TRY(check_moe(p));
+  if (p->I <= 0 || p->act < MLP_ACT_SWIGLU || p->act > MLP_ACT_GLU) return MLP_ERR_INVALID_ARG;
+  if (!std::isfinite(p->gate_mult) || !std::isfinite(p->down_mult)) return MLP_ERR_INVALID_ARG;
+  if (p->I % 8) return MLP_ERR_ALIGNMENT;
+  const MoePlan L = plan_of(p);
+  // 32-bit work units (three weight gradients of 128 x 256 tiles at most)
+  const long long tiles = out_tiles(p->I, p->H, 1) + out_tiles(p->H, p->I, 1);
+  if (L.rows * p->I >= (1LL << 40) || tiles * 2 * p->E >= (1LL << 31) ||
+      (L.tile_cap[0]) * ((p->H > p->I ? p->H : p->I) / 128 + 1) >= (1LL << 31))
+    return MLP_ERR_UNSUPPORTED;
+  return MLP_OK;
+}
+
+int check_weights(const mlp_moe_t* p, const void* Wg, const void* Wu, const void* Wd) {
+  MLP_TRY(need(Wg));
+  MLP_TRY(need(Wd));
+  return gated(p) ? need(Wu) : (Wu ? MLP_ERR_INVALID_ARG : MLP_OK);
+}
+
+// The workspace after the control block.
+struct Layout {
+  size_t inter;              // the postact [rows, I]
+  size_t plan, xs, y, total; // MLP_MODE_INFER: the plan and the sorted rows
+};
+Layout layout(const mlp_moe_t* p, int mode) {
+  const MoePlan L = plan_of(p);
+  Layout w = {};
+  size_t at = CTRL_BYTES;
+  w.inter = at;
+  at += round256((size_t)L.rows * p->I * 2);
+  if (mode == MLP_MODE_INFER) {
+    w.plan = at;
+    at += round256((size_t)L.ints * 4);
+    w.xs = at;
+    at += round256((size_t)L.rows * p->H * 2);
+    w.y = at;
+    at += round256((size_t)L.rows * p->H * 2);
+  }
+  w.total = at;
+  return w;
+}
+
+int check_ws(const mlp_moe_t* p, int mode, const void* ws, size_t ws_bytes) {
+  if (!ws) return MLP_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return MLP_ERR_ALIGNMENT;
+  return ws_bytes < layout(p, mode).total ? MLP_ERR_WORKSPACE_TOO_SMALL : MLP_OK;
+}
+
+// CTA pairs (256-row tiles) from an average of more than 128 rows an expert.
+int moe_cg(const mlp_moe_t* p) {
+  const int pol = g_tile_policy.load();
+  if (pol == 1 || pol == 2) return pol;
+  return (long long)p->T * p->top_k > 128LL * p->E ? 2 : 1;
+}
+
+// A GEMM over the sorted rows: its output tiles are the plan's.
+struct RowGemm : Gemm {
+  RowGemm(const mlp_moe_t* p, Call& c, const int* plan)
+      : Gemm(device_act(p->act), p->gate_mult * p->down_mult, c.counter(), c.status, moe_cg(p)),
+        L(plan_of(p)) {
+    this->p.tiles = reinterpret_cast<const MoeTile*>(plan + L.tiles[cg - 1]);
+    this->p.ntiles = plan + L.ntiles + cg - 1;
+    this->p.offsets = plan + L.offsets;
+    this->p.rows = static_cast<int>(L.rows);
+  }
+  Prob& add_rows(int N, int K0, int K1, int tile_n) {
+    Prob& P = add(static_cast<int>(L.rows), N, K0, K1, tile_n);
+    P.units = static_cast<int>(L.tile_cap[cg - 1] * P.tiles_n);  // at most; the plan has the number
+    p.total_units = P.units;
+    return P;
+  }
+  int rows_a(const void* ptr, int K) { return kmajor(ptr, static_cast<int>(L.rows), K, BM); }
+  MoePlan L;
+};
+
+int launch_experts_act(const mlp_moe_t* p, Call& c, const int* plan, const void* xs, const void* Wg,
+                       const void* Wu, void* a, void* G, void* U) {
+  RowGemm g(p, c, plan);
+  const int rows = static_cast<int>(g.L.rows);
+  const int mA = g.rows_a(xs, p->H);
+  if (gated(p)) {
+    const int mG = g.kmajor_stack(Wg, p->E, p->I, p->H, 128);
+    const int mU = g.kmajor_stack(Wu, p->E, p->I, p->H, 128);
+    Prob& P = g.add_rows(p->I, p->H, 0, 128);
+    P.l2a = L2_EVICT_LAST;   // the rows: every tile column re-reads them
+    P.l2b = L2_EVICT_FIRST;  // the weights: a panel's reuse is by consecutive row tiles
+    P.mapA0 = mA;
+    P.mapB0 = mG;
+    P.mapB1 = mU;
+    g.output_rows(P, 0, a, rows, p->I);
+    g.output_rows(P, 1, G, rows, p->I);
+    g.output_rows(P, 2, U, rows, p->I);
+    return run_gated<EPI_GATED_FWD, false, false, true>(g, c, MLP_KERNEL_GATE_UP);
+  }
+  const int mW = g.kmajor_stack(Wg, p->E, p->I, p->H, g.b_rows());
+  Prob& P = g.add_rows(p->I, p->H, 0, MMA_N);
+  P.l2a = L2_EVICT_LAST;
+  P.l2b = L2_EVICT_FIRST;
+  P.mapA0 = mA;
+  P.mapB0 = mW;
+  g.output_rows(P, 0, a, rows, p->I);
+  g.output_rows(P, 1, G, rows, p->I);
+  return run_nongated<EPI_ACT_FWD, false, false, true>(g, c, MLP_KERNEL_GATE_UP);
+}
+
+int launch_experts_down(const mlp_moe_t* p, Call& c, const int* plan, const void* a, const void* Wd,
+                        void* y) {
+  RowGemm g(p, c, plan);
+  const int mA = g.rows_a(a, p->I);
+  const int mB = g.kmajor_stack(Wd, p->E, p->H, p->I, g.b_rows());
+  Prob& P = g.add_rows(p->H, p->I, 0, MMA_N);
+  P.l2a = L2_EVICT_LAST;
+  P.l2b = L2_EVICT_FIRST;
+  P.mapA0 = mA;
+  P.mapB0 = mB;
+  g.output_rows(P, 0, y, static_cast<int>(g.L.rows), p->H);
+  return run<EPI_STORE_BF16, false, false, true>(g, c, MLP_KERNEL_DOWN);
+}
+
 }  // namespace
 
 extern "C" {
@@ -120,6 +246,190 @@ int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, 
   return traced(MLP_KERNEL_MOE_COMBINE_BWD, s, [&] {
     return launch_moe_combine_bwd(dout, y, static_cast<const int*>(plan), plan_of(p), p->T,
                                   p->top_k, p->H, weights, w_bf16(p), dy, dweights, s, false);
+  });
+}
+
+size_t mlp_moe_workspace_size(const mlp_moe_t* p, int mode) {
+  if (check_experts(p) != MLP_OK) return 0;
+  if (mode != MLP_MODE_FWD && mode != MLP_MODE_BWD && mode != MLP_MODE_INFER) return 0;
+  return layout(p, mode).total;
+}
+
+int mlp_moe_experts_fwd(const mlp_moe_t* p, const void* plan, const void* xs, const void* Wg,
+                        const void* Wu, const void* Wd, void* y, void* G_save, void* U_save,
+                        void* ws, size_t ws_bytes, void* stream) {
+  MLP_TRY(check_experts(p));
+  MLP_TRY(need(plan));
+  MLP_TRY(need(xs));
+  MLP_TRY(check_weights(p, Wg, Wu, Wd));
+  MLP_TRY(need(y));
+  MLP_TRY(opt(G_save));
+  MLP_TRY(opt(U_save));
+  if (!gated(p) && U_save) return MLP_ERR_INVALID_ARG;
+  MLP_TRY(check_ws(p, MLP_MODE_FWD, ws, ws_bytes));
+  Call c;
+  MLP_TRY(begin_call(c, ws, stream));
+  void* a = static_cast<char*>(ws) + layout(p, MLP_MODE_FWD).inter;
+  const int* pl = static_cast<const int*>(plan);
+  MLP_TRY(launch_experts_act(p, c, pl, xs, Wg, Wu, a, G_save, U_save));
+  return launch_experts_down(p, c, pl, a, Wd, y);
+}
+
+int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, const void* xs,
+                        const void* Wg, const void* Wu, const void* Wd, void* G, void* U,
+                        void* dxs, void* dWg, void* dWu, void* dWd, int fuse_grad_accum, void* ws,
+                        size_t ws_bytes, void* stream) {
+  MLP_TRY(check_experts(p));
+  if (fuse_grad_accum != 0 && fuse_grad_accum != 1) return MLP_ERR_INVALID_ARG;
+  MLP_TRY(need(plan));
+  MLP_TRY(need(dy));
+  MLP_TRY(need(xs));
+  MLP_TRY(check_weights(p, Wg, Wu, Wd));
+  MLP_TRY(need(G));
+  const bool gt = gated(p);
+  if (gt) {
+    MLP_TRY(need(U));
+  } else if (U || dWu) {
+    return MLP_ERR_INVALID_ARG;
+  }
+  MLP_TRY(opt(dxs));
+  MLP_TRY(opt(dWg));
+  MLP_TRY(opt(dWu));
+  MLP_TRY(opt(dWd));
+  MLP_TRY(check_ws(p, MLP_MODE_BWD, ws, ws_bytes));
+  const bool need_dact = dxs || dWg || dWu;
+  if (!need_dact && !dWd) return MLP_OK;
+  Call c;
+  MLP_TRY(begin_call(c, ws, stream));
+  void* a = static_cast<char*>(ws) + layout(p, MLP_MODE_BWD).inter;
+  const int* pl = static_cast<const int*>(plan);
+  const int rows = static_cast<int>(plan_of(p).rows);
+
+  if (need_dact) {
+    // dh = dy Wd; dG, dU over G, U, and the postact for dWd
+    RowGemm g(p, c, pl);
+    const int mA = g.rows_a(dy, p->H);
+    const int mB = g.mnmajor_stack(Wd, p->E, p->H, p->I);
+    Prob& P = g.add_rows(p->I, p->H, 0, MMA_N);
+    P.l2a = L2_EVICT_LAST;
+    P.mapA0 = mA;
+    P.mapB0 = mB;
+    P.in0 = G;
+    P.in1 = U;
+    g.output_rows(P, 0, G, rows, p->I);
+    if (gt) {
+      g.output_rows(P, 1, U, rows, p->I);
+      g.output_rows(P, 2, dWd ? a : nullptr, rows, p->I);
+      MLP_TRY((run_gated<EPI_DGATED, false, true, true>(g, c, MLP_KERNEL_DGATED)));
+    } else {
+      g.output_rows(P, 1, dWd ? a : nullptr, rows, p->I);
+      MLP_TRY((run_nongated<EPI_DACT, false, true, true>(g, c, MLP_KERNEL_DGATED)));
+    }
+  } else {
+    const bool pdl = c.pdl();
+    MLP_TRY(traced(MLP_KERNEL_POSTACT, c.stream, [&] {
+      return launch_postact(G, U, a, (long long)rows * p->I, device_act(p->act),
+                            p->gate_mult * p->down_mult, c.stream, pdl);
+    }));
+  }
+
+  // the input gradient, and the weight gradients beside it (mlp_bwd's reasons)
+  const bool want_w = dWg || dWu || dWd;
+  Side* side = (dxs && want_w && !g_trace_flag.load()) ? side_stream(c.stream) : nullptr;
+  std::unique_lock<std::mutex> side_lk;
+  if (side) {
+    side_lk = std::unique_lock<std::mutex>(side->mu);
+    MLP_TRY(cuda_err(cudaEventRecord(side->fork, c.stream)));
+  }
+  if (dxs) {
+    RowGemm g(p, c, pl);
+    const int mA0 = g.rows_a(G, p->I);
+    const int mB0 = g.mnmajor_stack(Wg, p->E, p->I, p->H);
+    int mA1 = 0, mB1 = 0;
+    if (gt) {
+      mA1 = g.rows_a(U, p->I);
+      mB1 = g.mnmajor_stack(Wu, p->E, p->I, p->H);
+    }
+    Prob& P = g.add_rows(p->H, p->I, gt ? p->I : 0, MMA_N);
+    P.l2a = L2_EVICT_LAST;
+    P.l2b = L2_EVICT_FIRST;
+    P.mapA0 = mA0;
+    P.mapB0 = mB0;
+    P.mapA1 = mA1;
+    P.mapB1 = mB1;
+    g.output_rows(P, 0, dxs, rows, p->H);
+    MLP_TRY((run<EPI_STORE_BF16, false, true, true>(g, c, MLP_KERNEL_DX)));
+  }
+  if (want_w) {
+    Call cw = c;
+    if (side) {
+      cw.stream = side->stream;
+      cw.launches = 0;  // its first kernel follows an event wait, not a kernel
+      MLP_TRY(cuda_err(cudaStreamWaitEvent(side->stream, side->fork, 0)));
+    }
+    const int fuse = fuse_grad_accum;
+    Gemm g(device_act(p->act), 1.f, cw.counter(), cw.status, pick_cg(p->H < p->I ? p->H : p->I));
+    g.p.offsets = pl + plan_of(p).offsets;
+    g.p.rows = rows;
+    struct W { const void* A; int m; const void* B; int n; void* out; };
+    W list[3];
+    int n = 0;
+    if (dWg) list[n++] = {G, p->I, xs, p->H, dWg};
+    if (dWu) list[n++] = {U, p->I, xs, p->H, dWu};
+    if (dWd) list[n++] = {dy, p->H, a, p->I, dWd};
+    for (int i = 0; i < n; ++i) {
+      const int mA = g.mnmajor(list[i].A, rows, list[i].m);
+      const int mB = g.mnmajor(list[i].B, rows, list[i].n);
+      const int oW = g.output_stack(list[i].out, p->E, list[i].m, list[i].n, fuse != 0);
+      Prob& P = g.add(list[i].m, list[i].n, BK, 0, MMA_N);  // K: each expert's rows
+      g.p.total_units += P.units * (p->E - 1);
+      P.units *= p->E;
+      P.l2b = L2_EVICT_LAST;
+      P.mapA0 = mA;
+      P.mapB0 = mB;
+      P.mapO[0] = oW;
+    }
+    if (fuse) MLP_TRY((run<EPI_ACCUM_F32, true, true, true>(g, cw, MLP_KERNEL_WGRAD)));
+    else MLP_TRY((run<EPI_STORE_BF16, true, true, true>(g, cw, MLP_KERNEL_WGRAD)));
+    if (side) {
+      MLP_TRY(cuda_err(cudaEventRecord(side->join, side->stream)));
+      MLP_TRY(cuda_err(cudaStreamWaitEvent(c.stream, side->join, 0)));
+    }
+  }
+  return MLP_OK;
+}
+
+int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const void* weights,
+                      const void* Wg, const void* Wu, const void* Wd, const void* residual,
+                      void* out, void* ws, size_t ws_bytes, void* stream) {
+  MLP_TRY(check_experts(p));
+  MLP_TRY(need(x));
+  MLP_TRY(need4(ids));
+  MLP_TRY(need4(weights));
+  MLP_TRY(check_weights(p, Wg, Wu, Wd));
+  MLP_TRY(opt(residual));
+  MLP_TRY(need(out));
+  MLP_TRY(check_ws(p, MLP_MODE_INFER, ws, ws_bytes));
+  const Layout w = layout(p, MLP_MODE_INFER);
+  const MoePlan L = plan_of(p);
+  char* base = static_cast<char*>(ws);
+  int* plan = reinterpret_cast<int*>(base + w.plan);
+  void *a = base + w.inter, *xs = base + w.xs, *y = base + w.y;
+  Call c;
+  MLP_TRY(begin_call(c, ws, stream));
+  bool pdl = c.pdl();
+  MLP_TRY(traced(MLP_KERNEL_MOE_SORT, c.stream,
+                 [&] { return launch_moe_sort(ids, plan, L, p->E, c.stream, pdl); }));
+  pdl = c.pdl();
+  MLP_TRY(traced(MLP_KERNEL_MOE_DISPATCH, c.stream, [&] {
+    return launch_moe_dispatch(x, plan, L, p->T, p->top_k, p->H, xs, c.stream, pdl);
+  }));
+  MLP_TRY(launch_experts_act(p, c, plan, xs, Wg, Wu, a, nullptr, nullptr));
+  MLP_TRY(launch_experts_down(p, c, plan, a, Wd, y));
+  pdl = c.pdl();
+  return traced(MLP_KERNEL_MOE_COMBINE, c.stream, [&] {
+    return launch_moe_combine(y, plan, L, p->T, p->top_k, p->H, weights, w_bf16(p), residual, out,
+                              c.stream, pdl);
   });
 }
 

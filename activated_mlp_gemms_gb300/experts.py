@@ -11,7 +11,8 @@ import ctypes
 
 import torch
 
-from . import ACTS, MlpError, _check, _ptr, _stream, lib
+from . import (ACTS, MODE_BWD, MODE_FWD, MODE_INFER, MlpError, _check, _ptr, _stream,
+               _wdt, lib)
 
 ROW_ALIGN = 16  # MLP_MOE_ROW_ALIGN
 MAX_EXPERTS = 1024  # MLP_MOE_MAX_EXPERTS
@@ -43,6 +44,13 @@ def declare(L):
     L.mlp_moe_dispatch_bwd.argtypes = [P] + [VP] * 4
     L.mlp_moe_combine.argtypes = [P] + [VP] * 6
     L.mlp_moe_combine_bwd.argtypes = [P] + [VP] * 7
+    L.mlp_moe_workspace_size.argtypes = [P, ctypes.c_int]
+    L.mlp_moe_workspace_size.restype = ctypes.c_size_t
+    L.mlp_moe_experts_fwd.argtypes = [P] + [VP] * 9 + [ctypes.c_size_t, VP]
+    L.mlp_moe_experts_bwd.argtypes = [P] + [VP] * 12 + [ctypes.c_int, VP, ctypes.c_size_t, VP]
+    L.mlp_moe_fwd_infer.argtypes = [P] + [VP] * 9 + [ctypes.c_size_t, VP]
+    for n in ("experts_fwd", "experts_bwd", "fwd_infer"):
+        getattr(L, "mlp_moe_" + n).restype = ctypes.c_int
     for n in ("plan_layout", "sort", "dispatch", "dispatch_bwd", "combine", "combine_bwd"):
         getattr(L, "mlp_moe_" + n).restype = ctypes.c_int
 
@@ -154,3 +162,79 @@ def mlp_moe_combine_bwd(p: Moe, plan, dout, y, weights, dy=None, dweights=None,
                                    _shaped(dweights, (p.T, p.top_k), "dweights", _w_dtype(p)),
                                    _stream(stream))
     _check(rc, "mlp_moe_combine_bwd")
+
+
+def mlp_moe_workspace_size(p: Moe, mode: int) -> int:
+    return int(lib().mlp_moe_workspace_size(ctypes.byref(p), int(mode)))
+
+
+def alloc_moe_workspace(p: Moe, mode: int, device=None) -> torch.Tensor:
+    n = mlp_moe_workspace_size(p, mode)
+    if n == 0:
+        raise MlpError(-1, "mlp_moe_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _ws(ws, p, mode, device):
+    if ws is None:
+        return alloc_moe_workspace(p, mode, device)
+    if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
+    return ws
+
+
+def _weights(p: Moe, Wg, Wu, Wd, dtype=torch.bfloat16, names=("Wg", "Wu", "Wd")):
+    up, down = (p.E, p.I, p.H), (p.E, p.H, p.I)
+    return (_shaped(Wg, up, names[0], dtype), _shaped(Wu, up, names[1], dtype),
+            _shaped(Wd, down, names[2], dtype))
+
+
+def mlp_moe_experts_fwd(p: Moe, plan, xs, Wg, Wu, Wd, y, G_save=None, U_save=None, ws=None,
+                        stream=None):
+    """Each expert's MLP over its rows of xs: y[r] = MLP_e(xs[r]); optionally stores the
+    preacts (bf16 [rows, I]) for the backward.  Wg, Wu [E, I, H] (Wu None when non-gated),
+    Wd [E, H, I].  Rows of y past the plan's offsets[E] are not written.  Returns the
+    workspace used."""
+    rows = mlp_moe_rows(p)
+    ws = _ws(ws, p, MODE_FWD, y.device)
+    rc = lib().mlp_moe_experts_fwd(ctypes.byref(p), _plan(p, plan), _shaped(xs, (rows, p.H), "xs"),
+                                   *_weights(p, Wg, Wu, Wd), _shaped(y, (rows, p.H), "y"),
+                                   _shaped(G_save, (rows, p.I), "G_save"),
+                                   _shaped(U_save, (rows, p.I), "U_save"), ws.data_ptr(),
+                                   ws.numel(), _stream(stream))
+    _check(rc, "mlp_moe_experts_fwd")
+    return ws
+
+
+def mlp_moe_experts_bwd(p: Moe, plan, dy, xs, Wg, Wu, Wd, G, U, dxs=None, dWg=None, dWu=None,
+                        dWd=None, fuse_grad_accum=False, ws=None, stream=None):
+    """Gradients of mlp_moe_experts_fwd from its saved G, U (overwritten with dG, dU).
+    Outputs that are None are skipped; weight gradients are bf16 (overwritten) or fp32
+    (+= in place) when fuse_grad_accum.  The padding rows of dy and xs are zero."""
+    rows = mlp_moe_rows(p)
+    ws = _ws(ws, p, MODE_BWD, dy.device)
+    rc = lib().mlp_moe_experts_bwd(ctypes.byref(p), _plan(p, plan), _shaped(dy, (rows, p.H), "dy"),
+                                   _shaped(xs, (rows, p.H), "xs"), *_weights(p, Wg, Wu, Wd),
+                                   _shaped(G, (rows, p.I), "G"), _shaped(U, (rows, p.I), "U"),
+                                   _shaped(dxs, (rows, p.H), "dxs"),
+                                   *_weights(p, dWg, dWu, dWd, _wdt(fuse_grad_accum),
+                                             ("dWg", "dWu", "dWd")),
+                                   int(bool(fuse_grad_accum)), ws.data_ptr(), ws.numel(),
+                                   _stream(stream))
+    _check(rc, "mlp_moe_experts_bwd")
+    return ws
+
+
+def mlp_moe_fwd_infer(p: Moe, x, ids, weights, Wg, Wu, Wd, residual, out, ws=None, stream=None):
+    """The whole layer without gradients: out[t] = residual[t] + sum_j weights[t, j]
+    MLP_{ids[t, j]}(x[t]) (residual may be None).  Returns the workspace used."""
+    ws = _ws(ws, p, MODE_INFER, out.device)
+    th, tk = (p.T, p.H), (p.T, p.top_k)
+    rc = lib().mlp_moe_fwd_infer(ctypes.byref(p), _shaped(x, th, "x"),
+                                 _shaped(ids, tk, "ids", torch.int32),
+                                 _shaped(weights, tk, "weights", _w_dtype(p)),
+                                 *_weights(p, Wg, Wu, Wd), _shaped(residual, th, "residual"),
+                                 _shaped(out, th, "out"), ws.data_ptr(), ws.numel(),
+                                 _stream(stream))
+    _check(rc, "mlp_moe_fwd_infer")
+    return ws

@@ -86,6 +86,41 @@ int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const v
 int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, const void* y,
                         const void* weights, void* dy, void* dweights, void* stream);
 
+/* Bytes of workspace of a call (0 on invalid arguments): MLP_MODE_FWD for
+ * mlp_moe_experts_fwd, MLP_MODE_BWD for mlp_moe_experts_bwd, MLP_MODE_INFER
+ * for mlp_moe_fwd_infer. */
+size_t mlp_moe_workspace_size(const mlp_moe_t* p, int mode);
+
+/* The experts' MLPs over the sorted rows, y[r] = MLP_e(xs[r]) for the rows r of
+ * expert e (padding rows as any other).
+ *   xs  bf16 [rows,H];  Wg, Wu bf16 [E,I,H] (Wu NULL when non-gated);
+ *   Wd  bf16 [E,H,I];   y bf16 [rows,H] out
+ *   G_save, U_save  bf16 [rows,I] out, optional: the preacts, for the backward
+ * Rows from offsets[E] on are not written. */
+int mlp_moe_experts_fwd(const mlp_moe_t* p, const void* plan, const void* xs, const void* Wg,
+                        const void* Wu, const void* Wd, void* y, void* G_save, void* U_save,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients, from the saved preacts (which become dG, dU, as in mlp_bwd):
+ *   dy   bf16 [rows,H] in, with zero padding rows (mlp_moe_combine_bwd's)
+ *   dxs  bf16 [rows,H] out; dWg, dWu [E,I,H], dWd [E,H,I]: bf16, or with
+ *        fuse_grad_accum = 1 fp32 that the gradients are added to; each NULL
+ *        to skip.  An expert without rows gets a zero gradient.
+ * xs has zero padding rows (mlp_moe_dispatch's).  dxs is not written from
+ * offsets[E] on. */
+int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, const void* xs,
+                        const void* Wg, const void* Wu, const void* Wd, void* G, void* U,
+                        void* dxs, void* dWg, void* dWu, void* dWd, int fuse_grad_accum, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* The whole layer without gradients: sort, dispatch, experts, combine, with
+ * everything between in the workspace.
+ *   x bf16 [T,H], ids int32 [T,top_k], weights [T,top_k] (weights_type),
+ *   residual bf16 [T,H] or NULL, out bf16 [T,H] (may be residual itself) */
+int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const void* weights,
+                      const void* Wg, const void* Wu, const void* Wd, const void* residual,
+                      void* out, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

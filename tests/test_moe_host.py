@@ -95,3 +95,56 @@ def test_python_refusals(L):
     with pytest.raises(ValueError):  # not on the GPU
         m.mlp_moe_sort(p, torch.zeros(4, 1, dtype=torch.int32),
                        torch.zeros(10, dtype=torch.int32))
+
+
+def _experts(L, p, plan=FAKE, xs=FAKE, Wg=FAKE, Wu=FAKE, Wd=FAKE, y=FAKE, G=FAKE, U=FAKE, ws=FAKE,
+             n=1 << 40):
+    return L.mlp_moe_experts_fwd(ctypes.byref(p), plan, xs, Wg, Wu, Wd, y, G, U, ws, n, None)
+
+
+def _experts_bwd(L, p, plan=FAKE, dy=FAKE, xs=FAKE, Wg=FAKE, Wu=FAKE, Wd=FAKE, G=FAKE, U=FAKE,
+                 dxs=FAKE, dWg=FAKE, dWu=FAKE, dWd=FAKE, fuse=0, ws=FAKE, n=1 << 40):
+    return L.mlp_moe_experts_bwd(ctypes.byref(p), plan, dy, xs, Wg, Wu, Wd, G, U, dxs, dWg, dWu,
+                                 dWd, fuse, ws, n, None)
+
+
+def _layer(L, p, x=FAKE, ids=FAKE, w=FAKE, Wg=FAKE, Wu=FAKE, Wd=FAKE, r=None, out=FAKE, ws=FAKE,
+           n=1 << 40):
+    return L.mlp_moe_fwd_infer(ctypes.byref(p), x, ids, w, Wg, Wu, Wd, r, out, ws, n, None)
+
+
+def test_experts_refusals(L):
+    ok = lambda **kw: m.moe(16, 8, 2, 64, 128, **kw)  # noqa: E731
+    calls = (_experts, _experts_bwd, _layer)
+    for change, code in ((dict(I=0), -1), (dict(act=7), -1), (dict(I=100), -2), (dict(H=20), -2),
+                         (dict(gate_mult=float("nan")), -1), (dict(T=0), -1), (dict(E=2000), -3)):
+        p = ok()
+        for k, v in change.items():
+            setattr(p, k, v)
+        for call in calls:
+            assert call(L, p) == code, (change, call)
+        assert m.mlp_moe_workspace_size(p, m.MODE_FWD) == 0
+    p, q = ok(), ok(act="relu_sq")
+    for call in calls:
+        assert call(L, q) == -1  # a non-gated MLP takes no Wu
+        assert call(L, p, Wu=None) == -1
+        assert call(L, p, Wg=FAKE + 8) == -2
+        assert call(L, p, ws=None) == -1
+        assert call(L, p, ws=FAKE + 16) == -2
+        assert call(L, p, n=2048) == -4
+    for name in ("plan", "xs", "Wg", "Wd", "y"):
+        assert _experts(L, p, **{name: None}) == -1
+    assert _experts(L, q, Wu=None, G=FAKE, U=FAKE) == -1  # no up preact without an up weight
+    assert _experts(L, p, G=FAKE + 4) == -2
+    for name in ("plan", "dy", "xs", "Wg", "Wd", "G", "U"):
+        assert _experts_bwd(L, p, **{name: None}) == -1
+    assert _experts_bwd(L, p, fuse=2) == -1
+    assert _experts_bwd(L, p, dWd=FAKE + 4) == -2
+    assert _experts_bwd(L, q, Wu=None, U=None, dWu=FAKE) == -1
+    assert _experts_bwd(L, p, dxs=None, dWg=None, dWu=None, dWd=None) == 0  # nothing asked for
+    for name in ("x", "ids", "w", "out"):
+        assert _layer(L, p, **{name: None}) == -1
+    assert _layer(L, p, r=FAKE + 8) == -2
+    assert m.mlp_moe_workspace_size(p, m.MODE_BWD_RECOMPUTE) == 0
+    rows = m.mlp_moe_rows(p)
+    assert m.mlp_moe_workspace_size(p, m.MODE_FWD) == 1024 + rows * 128 * 2
