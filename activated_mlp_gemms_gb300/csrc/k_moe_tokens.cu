@@ -25,31 +25,33 @@ __device__ __forceinline__ float ld_weight(const void* w, size_t i) {
 }
 
 // Rows of the sorted layout that hold no slot (padding, and past the end)
-// become zero: a warp looks at 32 rows and writes those that src marks.
+// become zero: warp `group` looks at `per` rows and writes those that src
+// marks.  (They come in runs, the rows past the end in one: with few rows a
+// warp there are enough warps to write a run at HBM's rate.)
 __device__ __forceinline__ void zero_empty_rows(const int* src, long long rows, long long group,
-                                                __nv_bfloat16* out, int H) {
+                                                int per, __nv_bfloat16* out, int H) {
   const int lane = threadIdx.x & 31;
-  const long long r = group * 32 + lane;
-  unsigned empty = __ballot_sync(0xffffffffu, r < rows && src[r < rows ? r : 0] < 0);
+  const long long r0 = group * per, r = r0 + lane;
+  unsigned empty = __ballot_sync(0xffffffffu, lane < per && r < rows && src[r < rows ? r : 0] < 0);
   while (empty) {
     const int i = __ffs(empty) - 1;
     empty &= empty - 1;
-    __nv_bfloat16* o = out + static_cast<size_t>(group * 32 + i) * H;
+    __nv_bfloat16* o = out + static_cast<size_t>(r0 + i) * H;
     for (int c = 8 * lane; c < H; c += 256) st_global_v4(o + c, make_uint4(0, 0, 0, 0));
   }
 }
 
 // Blocks [0, T segs): one column segment of one token each; the blocks after
-// them clear the empty rows (TOK_THREADS / 32 groups of 32 rows a block).
+// them clear the empty rows (TOK_THREADS / 32 groups of `per` rows a block).
 __global__ void __launch_bounds__(TOK_THREADS)
     k_moe_dispatch(const __nv_bfloat16* __restrict__ x, const int* __restrict__ pos,
                    const int* __restrict__ src, __nv_bfloat16* __restrict__ xs, long long rows,
-                   int top_k, int H, int segs, long long token_blocks) {
+                   int top_k, int H, int segs, long long token_blocks, int per) {
   pdl_wait();
   pdl_launch_dependents();
   if (blockIdx.x >= token_blocks) {
     const long long group = (blockIdx.x - token_blocks) * (TOK_THREADS / 32) + (threadIdx.x >> 5);
-    zero_empty_rows(src, rows, group, xs, H);
+    zero_empty_rows(src, rows, group, per, xs, H);
     return;
   }
   const int t = blockIdx.x / segs, c = (blockIdx.x % segs) * TOK_COLS + 8 * threadIdx.x;
@@ -116,13 +118,14 @@ __global__ void __launch_bounds__(TOK_THREADS)
     k_moe_combine_bwd(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ y,
                       const int* __restrict__ pos, const int* __restrict__ src,
                       const void* __restrict__ weights, __nv_bfloat16* __restrict__ dy,
-                      void* __restrict__ dweights, long long rows, int T, int top_k, int H) {
+                      void* __restrict__ dweights, long long rows, int T, int top_k, int H,
+                      int per) {
   __shared__ float part[TOK_THREADS / 32][BWD_SLOTS];
   pdl_wait();
   pdl_launch_dependents();
   if (blockIdx.x >= T) {
     const long long group = (blockIdx.x - T) * (TOK_THREADS / 32) + (threadIdx.x >> 5);
-    zero_empty_rows(src, rows, group, dy, H);
+    zero_empty_rows(src, rows, group, per, dy, H);
     return;
   }
   const size_t t = blockIdx.x;
@@ -211,9 +214,11 @@ cudaError_t launch_tok(void (*kern)(Args...), long long blocks, cudaStream_t str
 
 using bf = __nv_bfloat16;
 
-// Blocks that look for empty rows.
+// Rows a warp looks at for empty ones: one while that leaves few warps (up to
+// about 64 an SM), at most four.
+int zero_rows(const MoePlan& L) { return L.rows <= 10240 ? 1 : L.rows <= 20480 ? 2 : 4; }
 long long zero_blocks(const MoePlan& L) {
-  const long long groups = (L.rows + 31) / 32;
+  const long long groups = (L.rows + zero_rows(L) - 1) / zero_rows(L);
   return (groups + TOK_THREADS / 32 - 1) / (TOK_THREADS / 32);
 }
 
@@ -225,7 +230,7 @@ cudaError_t launch_moe_dispatch(const void* x, const int* plan, const MoePlan& L
   const long long tokens = static_cast<long long>(T) * segs;
   return launch_tok(k_moe_dispatch, tokens + zero_blocks(L), stream, pdl,
                     static_cast<const bf*>(x), plan + L.pos, plan + L.src, static_cast<bf*>(xs),
-                    L.rows, top_k, H, segs, tokens);
+                    L.rows, top_k, H, segs, tokens, zero_rows(L));
 }
 
 cudaError_t launch_moe_combine(const void* y, const int* plan, const MoePlan& L, int T, int top_k,
@@ -247,7 +252,8 @@ cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* p
   auto kern = w_bf16 ? k_moe_combine_bwd<true> : k_moe_combine_bwd<false>;
   return launch_tok(kern, T + (dy ? zero_blocks(L) : 0), stream, pdl, static_cast<const bf*>(dout),
                     static_cast<const bf*>(y), plan + L.pos, plan + L.src, weights,
-                    static_cast<bf*>(dy), dweights, L.rows, T, top_k, H);
+                    static_cast<bf*>(dy), dweights, L.rows, T, top_k, H,
+                    zero_rows(L));
 }
 
 }  // namespace mlpk

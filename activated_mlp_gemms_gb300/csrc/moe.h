@@ -61,4 +61,18 @@ cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* p
                                    bool w_bf16, void* dy, void* dweights, cudaStream_t stream,
                                    bool pdl);
 
+// Up to eight tokens (and 128 slots): the touched experts' weights streamed,
+// straight from the tokens and ids: h[slot] bf16 [n, I] (the slots that use an
+// expert first for their token), then out[t] = residual[t] + sum of weighted
+// down projections.  Clears *status.
+constexpr int MOE_DECODE_MAX_T = 8;
+constexpr int MOE_DECODE_MAX_SLOTS = 128;
+cudaError_t launch_moe_decode_act(const void* x, const int* ids, const void* Wg, const void* Wu,
+                                  const void* Wd, void* h, int T, int top_k, int E, int H, int I,
+                                  int act, bool gated, float s, cudaStream_t stream, bool pdl,
+                                  int* status);
+cudaError_t launch_moe_decode_down(const void* h, const int* ids, const void* weights, bool w_bf16,
+                                   const void* Wd, const void* residual, void* out, int T,
+                                   int top_k, int E, int H, int I, cudaStream_t stream, bool pdl);
+
 }  // namespace mlpk

@@ -87,11 +87,21 @@ int check_ws(const mlp_moe_t* p, int mode, const void* ws, size_t ws_bytes) {
   return ws_bytes < layout(p, mode).total ? MLP_ERR_WORKSPACE_TOO_SMALL : MLP_OK;
 }
 
-// CTA pairs (256-row tiles) from an average of more than 128 rows an expert.
+// CTA pairs (256-row tiles) from an average of more than 512 rows an expert:
+// an expert's last tile is half empty on average, 128 rows of a pair's tile or
+// 64 of a single CTA's, while a pair's tile is the faster one per row.
 int moe_cg(const mlp_moe_t* p) {
   const int pol = g_tile_policy.load();
   if (pol == 1 || pol == 2) return pol;
-  return (long long)p->T * p->top_k > 128LL * p->E ? 2 : 1;
+  return (long long)p->T * p->top_k > 512LL * p->E ? 2 : 1;
+}
+
+// Whether the inference layer streams the touched experts' weights: few tokens,
+// unless a tile policy asks for the tiles.
+bool decode_moe(const mlp_moe_t* p) {
+  const int pol = g_tile_policy.load();
+  return (pol == 0 || pol == 3) && p->T <= MOE_DECODE_MAX_T &&
+         p->T * p->top_k <= MOE_DECODE_MAX_SLOTS;
 }
 
 // A GEMM over the sorted rows: its output tiles are the plan's.
@@ -158,6 +168,10 @@ int launch_experts_down(const mlp_moe_t* p, Call& c, const int* plan, const void
   return run<EPI_STORE_BF16, false, false, true>(g, c, MLP_KERNEL_DOWN);
 }
 
+// The sort and the token kernels start while the kernel before them on the
+// stream, whatever it is, still runs (programmatic launch): each waits for its
+// end before it touches memory, and what is saved is the launch itself.
+
 }  // namespace
 
 extern "C" {
@@ -184,7 +198,7 @@ int mlp_moe_sort(const mlp_moe_t* p, const int* ids, void* plan, void* stream) {
   MLP_TRY(need(plan));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_SORT, s, [&] {
-    return launch_moe_sort(ids, static_cast<int*>(plan), plan_of(p), p->E, s, false);
+    return launch_moe_sort(ids, static_cast<int*>(plan), plan_of(p), p->E, s, true);
   });
 }
 
@@ -196,7 +210,7 @@ int mlp_moe_dispatch(const mlp_moe_t* p, const void* plan, const void* x, void* 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_DISPATCH, s, [&] {
     return launch_moe_dispatch(x, static_cast<const int*>(plan), plan_of(p), p->T, p->top_k, p->H,
-                               xs, s, false);
+                               xs, s, true);
   });
 }
 
@@ -209,7 +223,7 @@ int mlp_moe_dispatch_bwd(const mlp_moe_t* p, const void* plan, const void* dxs, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_COMBINE, s, [&] {
     return launch_moe_combine(dxs, static_cast<const int*>(plan), plan_of(p), p->T, p->top_k, p->H,
-                              nullptr, false, nullptr, dx, s, false);
+                              nullptr, false, nullptr, dx, s, true);
   });
 }
 
@@ -224,7 +238,7 @@ int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_COMBINE, s, [&] {
     return launch_moe_combine(y, static_cast<const int*>(plan), plan_of(p), p->T, p->top_k, p->H,
-                              weights, w_bf16(p), residual, out, s, false);
+                              weights, w_bf16(p), residual, out, s, true);
   });
 }
 
@@ -245,7 +259,7 @@ int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_COMBINE_BWD, s, [&] {
     return launch_moe_combine_bwd(dout, y, static_cast<const int*>(plan), plan_of(p), p->T,
-                                  p->top_k, p->H, weights, w_bf16(p), dy, dweights, s, false);
+                                  p->top_k, p->H, weights, w_bf16(p), dy, dweights, s, true);
   });
 }
 
@@ -368,7 +382,8 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
       MLP_TRY(cuda_err(cudaStreamWaitEvent(side->stream, side->fork, 0)));
     }
     const int fuse = fuse_grad_accum;
-    Gemm g(device_act(p->act), 1.f, cw.counter(), cw.status, pick_cg(p->H < p->I ? p->H : p->I));
+    Gemm g(device_act(p->act), 1.f, cw.counter(), cw.status,
+           p->H > BM && p->I > BM ? moe_cg(p) : pick_cg(p->H < p->I ? p->H : p->I));
     g.p.offsets = pl + plan_of(p).offsets;
     g.p.rows = rows;
     struct W { const void* A; int m; const void* B; int n; void* out; };
@@ -415,9 +430,22 @@ int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const v
   char* base = static_cast<char*>(ws);
   int* plan = reinterpret_cast<int*>(base + w.plan);
   void *a = base + w.inter, *xs = base + w.xs, *y = base + w.y;
+  const bool stream_weights = decode_moe(p);
   Call c;
-  MLP_TRY(begin_call(c, ws, stream));
+  MLP_TRY(begin_call(c, ws, stream, !stream_weights));
   bool pdl = c.pdl();
+  if (stream_weights) {
+    MLP_TRY(traced(MLP_KERNEL_GATE_UP, c.stream, [&] {
+      return launch_moe_decode_act(x, ids, Wg, Wu, Wd, a, p->T, p->top_k, p->E, p->H, p->I,
+                                   device_act(p->act), gated(p), p->gate_mult * p->down_mult,
+                                   c.stream, pdl, c.status);
+    }));
+    pdl = c.pdl();
+    return traced(MLP_KERNEL_DOWN, c.stream, [&] {
+      return launch_moe_decode_down(a, ids, weights, w_bf16(p), Wd, residual, out, p->T, p->top_k,
+                                    p->E, p->H, p->I, c.stream, pdl);
+    });
+  }
   MLP_TRY(traced(MLP_KERNEL_MOE_SORT, c.stream,
                  [&] { return launch_moe_sort(ids, plan, L, p->E, c.stream, pdl); }));
   pdl = c.pdl();

@@ -8,6 +8,7 @@ take their row numbers from the plan.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -72,7 +73,7 @@ def _shaped(t, shape, name, dtype=torch.bfloat16):
     if t is None:
         return None
     p = _ptr(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return p
 
@@ -81,19 +82,21 @@ def _w_dtype(p: Moe):
     return torch.bfloat16 if p.weights_type else torch.float32
 
 
-def _layout(p: Moe) -> _Layout:
-    out = _Layout()
+@functools.lru_cache(maxsize=1024)
+def _sizes(T, E, top_k, H, weights_type):
+    """(plan layout, rows): a function of the sizes alone."""
+    p, out = Moe(T, E, top_k, H, weights_type=weights_type), _Layout()
     _check(lib().mlp_moe_plan_layout(ctypes.byref(p), ctypes.byref(out)), "mlp_moe_plan_layout")
-    return out
+    return out, int(lib().mlp_moe_rows(ctypes.byref(p)))
+
+
+def _layout(p: Moe) -> _Layout:
+    return _sizes(p.T, p.E, p.top_k, p.H, p.weights_type)[0]
 
 
 def mlp_moe_rows(p: Moe) -> int:
     """Rows of the sorted layout's buffers (xs, y, dxs, dy, G, U)."""
-    rows = int(lib().mlp_moe_rows(ctypes.byref(p)))
-    if rows == 0:
-        raise MlpError(lib().mlp_moe_plan_layout(ctypes.byref(p), ctypes.byref(_Layout())),
-                       "mlp_moe_rows")
-    return rows
+    return _sizes(p.T, p.E, p.top_k, p.H, p.weights_type)[1]
 
 
 def alloc_moe_plan(p: Moe, device=None) -> torch.Tensor:
@@ -110,10 +113,11 @@ def moe_plan_views(p: Moe, plan) -> dict:
     each row, -1 for padding)."""
     _plan(p, plan)
     L = _layout(p)
-    n, rows = p.T * p.top_k, mlp_moe_rows(p)
-    return {"offsets": plan[L.offsets:L.offsets + p.E + 1],
-            "counts": plan[L.counts:L.counts + p.E],
-            "pos": plan[L.pos:L.pos + n].view(p.T, p.top_k), "src": plan[L.src:L.src + rows]}
+    at = plan.storage_offset()
+    return {"offsets": plan.as_strided((p.E + 1,), (1,), at + L.offsets),
+            "counts": plan.as_strided((p.E,), (1,), at + L.counts),
+            "pos": plan.as_strided((p.T, p.top_k), (p.top_k, 1), at + L.pos),
+            "src": plan.as_strided((mlp_moe_rows(p),), (1,), at + L.src)}
 
 
 def mlp_moe_sort(p: Moe, ids, plan, stream=None) -> None:

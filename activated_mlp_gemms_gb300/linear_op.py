@@ -48,7 +48,7 @@ def _dense(t, shape, name, dtype=torch.bfloat16):
     if t is None:
         return None
     p = _ptr(t, dtype, name)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return p
 
