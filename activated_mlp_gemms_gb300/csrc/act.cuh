@@ -41,6 +41,10 @@ __device__ __forceinline__ float act_f(float z) {
     return fmaxf(z, 0.0f);
   } else if constexpr (ACT == ACT_SIGMOID) {
     return sigmoid_f(z);
+  } else if constexpr (ACT == ACT_GELU_HW) {
+    const float c = 0.7978845608028654f;  // sqrt(2/pi)
+    const float h = 0.5f * z;
+    return fmaf(h, tanh_hw(c * fmaf(0.044715f * z, z * z, z)), h);
   } else {
     const float c = 0.7978845608028654f;  // sqrt(2/pi)
     float t = tanhf(c * fmaf(0.044715f * z, z * z, z));
@@ -69,6 +73,13 @@ __device__ __forceinline__ void act_and_grad(float z, float& a, float& da) {
     const float s = sigmoid_f(z);
     a = s;
     da = s * (1.0f - s);
+  } else if constexpr (ACT == ACT_GELU_HW) {
+    const float c = 0.7978845608028654f;
+    const float k = 0.044715f;
+    const float z2 = z * z, h = 0.5f * z;
+    const float t = tanh_hw(c * fmaf(k * z, z2, z));
+    a = fmaf(h, t, h);
+    da = fmaf(0.5f, t, 0.5f) + h * fmaf(-t, t, 1.0f) * fmaf(3.0f * k * c, z2, c);
   } else {
     const float c = 0.7978845608028654f;
     const float k = 0.044715f;

@@ -1067,6 +1067,42 @@ __device__ __forceinline__ void epi_plain(const Params& p, const EpiUnit& P, con
   }
 }
 
+// The experts' plain bf16 store.  A tile of few k-blocks (an expert's rows, in
+// a weight gradient) is bound by its epilogue: chunk c + 1 leaves the
+// accumulator while chunk c is packed, and the two boxes alternate, so a box
+// is refilled while the other's store still reads.
+template <bool STACK>
+__device__ __forceinline__ void epi_store_grp(const EpiUnit& P, EpiWarp& e, uint32_t tb, int col0,
+                                              int cb, int ce) {
+  if (col0 + cb >= P.N) return;
+  uint32_t d[2][32];
+  __syncwarp();
+  tmem_ld32(tb + cb, d[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = cb + 32 * i, col = col0 + c;
+    if (col >= P.N) break;  // warp-uniform
+    tmem_wait_ld();
+    if (i < 3 && col + 32 < P.N) tmem_ld32(tb + c + 32, d[(i + 1) & 1]);
+    uint32_t q[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      q[j] = pack_bf16x2(__uint_as_float(d[i & 1][2 * j]), __uint_as_float(d[i & 1][2 * j + 1]));
+    const uint32_t buf = e.stg + e.box * 2048u;
+    e.box ^= 1u;
+    staging_wait_read_but_one(e);
+    stage_bf16(buf, e.lane, q);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (e.lane == 0) {
+      if constexpr (STACK) tma_store_3d(P.out[0], buf, col, e.row0, e.expert);
+      else tma_store_2d(P.out[0], buf, col, e.row0);
+      bulk_commit();
+    }
+  }
+  tmem_wait_ld();
+}
+
 // EPI_FWD_FUSED: the producer thread of a down unit waits (bounded) until
 // every gate/up tile of its 256-row block is stored, then orders its TMA
 // loads of the postact after that.  False on expiry or abort.
@@ -1104,13 +1140,15 @@ __device__ __forceinline__ void signal_block_part(const Params& p, int tm, int l
 // of the 256 B rows, so a stage is 32 KB and six fit in shared memory.
 // After the stage ring come the epilogue warps' staging buffers; the ring
 // takes as many stages as fit beside them in the 227 KB of shared memory.
-template <int EPI, int CG>
+template <int EPI, int CG, bool GRP = false>
 struct Cfg {
   static constexpr int B_ROWS = CG == 2 ? 128 : 256;
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STG = NUM_EPI_WARPS * EpiTraits<EPI>::STG_WARP;
+  // (the experts' plain store alternates two boxes per warp)
+  static constexpr int STG_WARP = GRP && EPI == EPI_STORE_BF16 ? 4096 : EpiTraits<EPI>::STG_WARP;
+  static constexpr int STG = NUM_EPI_WARPS * STG_WARP;
   static constexpr int MAX_SMEM = 232448;  // per-block opt-in limit
   static constexpr int FIT = (MAX_SMEM - 2048 - STG) / STAGE;
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
@@ -1235,7 +1273,7 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
 template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP>
 __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
-  using C = Cfg<EPI, CG>;
+  using C = Cfg<EPI, CG, GRP>;
   constexpr bool PAIR = CG == 2;
   static_assert(EPI != EPI_FWD_FUSED || CG == 2, "the fused forward runs on CTA pairs");
   static_assert(!GRP || (!is_f8(EPI) && !is_recomp(EPI) && EPI != EPI_FWD_FUSED),
@@ -1591,7 +1629,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
     const int q = warp & 3;            // TMEM lane quadrant this warp may access
     const int half = (warp - 2) >> 2;  // which half of the tile's columns
     EpiWarp e;
-    e.stg = stg_s + static_cast<uint32_t>(warp - 2) * EpiTraits<EPI>::STG_WARP;
+    e.stg = stg_s + static_cast<uint32_t>(warp - 2) * C::STG_WARP;
     e.lane = lane;
     e.box = 0;
     e.ebar = bar_s(EBAR + 2 * (warp - 2));
@@ -1730,7 +1768,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         } else if constexpr (EPI == EPI_DGRAD_F8_RECOMP) {
           epi_recomp_f8_dh(P, e, tb, col0, cb, dd);
         } else {
-          epi_plain<EPI, GRP_SUM>(p, P, e, tb, col0, cb, ce);
+          if constexpr (GRP && EPI == EPI_STORE_BF16) {
+            static_assert(MMA_N == 256, "four chunks of 32 columns a warp");
+            epi_store_grp<GRP_SUM>(P, e, tb, col0, cb, ce);
+          } else {
+            epi_plain<EPI, GRP_SUM>(p, P, e, tb, col0, cb, ce);
+          }
         }
       }
       tc_fence_before();
@@ -1768,7 +1811,7 @@ cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 31 || !(configured_dev_mask.load() & (1u << dev))) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<EPI, CG>::SMEM);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<EPI, CG, GRP>::SMEM);
     if (e != cudaSuccess) return e;
     if (CG == 2) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
@@ -1779,7 +1822,7 @@ cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<EPI, CG>::SMEM;
+  cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   int na = 0;
@@ -1808,13 +1851,13 @@ int max_groups() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   if (CG == 1) return sms;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<EPI, CG>::SMEM) !=
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<EPI, CG, GRP>::SMEM) !=
       cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<EPI, CG>::SMEM;
+  cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;

@@ -41,7 +41,7 @@ cudaError_t with_act(int act, F&& f) {
   switch (act) {
     case ACT_SILU: return f(std::integral_constant<int, ACT_SILU>{});
     case ACT_RELU_SQ: return f(std::integral_constant<int, ACT_RELU_SQ>{});
-    case ACT_GELU_TANH: return f(std::integral_constant<int, ACT_GELU_TANH>{});
+    case ACT_GELU_HW: return f(std::integral_constant<int, ACT_GELU_HW>{});
     case ACT_RELU: return f(std::integral_constant<int, ACT_RELU>{});
     case ACT_SIGMOID: return f(std::integral_constant<int, ACT_SIGMOID>{});
     default: return f(std::integral_constant<int, ACT_NONE>{});

@@ -27,6 +27,7 @@ constexpr int SORT_THREADS = 32 * SORT_WARPS;
 // groups of 32 per pass, less than a cluster barrier costs.
 constexpr int SORT_ONE_CTA = 2 * SORT_THREADS;
 constexpr int SORT_CLUSTER = 8;
+constexpr int SORT_AHEAD = 8;  // groups of 32 ids in flight per warp
 
 __device__ __forceinline__ int ld_cluster_int(uint32_t addr) {
   int v;
@@ -122,13 +123,22 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
   const int lo = static_cast<int>(begin < n ? begin : n);
   const int hi = static_cast<int>(begin + per_warp < n ? begin + per_warp : n);
   int* mine = wcnt + warp * E;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const int id = i < hi ? ids[i] : -1;
-    const int e = (id >= 0 && id < E) ? id : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  // eight groups of 32 ids are loaded at a time
+  for (int i0 = lo; i0 < hi; i0 += 32 * SORT_AHEAD) {
+    int id[SORT_AHEAD];
+#pragma unroll
+    for (int j = 0; j < SORT_AHEAD; ++j) {
+      const int i = i0 + 32 * j + lane;
+      id[j] = i < hi ? ids[i] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < SORT_AHEAD; ++j) {
+      if (i0 + 32 * j >= hi) break;
+      const int e = (id[j] >= 0 && id[j] < E) ? id[j] : -1;
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   for (int e = tid; e < E; e += SORT_THREADS) {
@@ -168,22 +178,31 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
 
   int* pos = plan + L.pos;
   int* src = plan + L.src;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const int id = i < hi ? ids[i] : -1;
-    const int e = (id >= 0 && id < E) ? id : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const int at = e >= 0 ? mine[e] : 0;
-    __syncwarp();
-    if (e >= 0) {
-      const int row = base[e] + at + __popc(same & ((1u << lane) - 1u));
-      pos[i] = row;
-      src[row] = i;
-      if (lane == __ffs(same) - 1) mine[e] = at + __popc(same);
-    } else if (i < hi) {
-      pos[i] = -1;
+  for (int i0 = lo; i0 < hi; i0 += 32 * SORT_AHEAD) {
+    int id[SORT_AHEAD];
+#pragma unroll
+    for (int j = 0; j < SORT_AHEAD; ++j) {
+      const int i = i0 + 32 * j + lane;
+      id[j] = i < hi ? ids[i] : -1;
     }
-    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < SORT_AHEAD; ++j) {
+      if (i0 + 32 * j >= hi) break;
+      const int i = i0 + 32 * j + lane;
+      const int e = (id[j] >= 0 && id[j] < E) ? id[j] : -1;
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int at = e >= 0 ? mine[e] : 0;
+      __syncwarp();
+      if (e >= 0) {
+        const int row = base[e] + at + __popc(same & ((1u << lane) - 1u));
+        pos[i] = row;
+        src[row] = i;
+        if (lane == __ffs(same) - 1) mine[e] = at + __popc(same);
+      } else if (i < hi) {
+        pos[i] = -1;
+      }
+      __syncwarp();
+    }
   }
   // the padding rows, the tables and the rows past the end
   if (cta == 0 && tid < E) {

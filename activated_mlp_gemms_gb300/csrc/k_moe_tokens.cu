@@ -8,6 +8,8 @@
 // goes by token, not by sorted row, so that a token's row (or its gradient)
 // is read once for all its slots and the sum over its slots needs no atomic
 // (the same bits on every run).  Sums are fp32 and rounded once.
+#include <type_traits>
+
 #include "moe.h"
 #include "ptx.cuh"
 
@@ -41,8 +43,11 @@ __device__ __forceinline__ void zero_empty_rows(const int* src, long long rows, 
   }
 }
 
-// Blocks [0, T segs): one column segment of one token each; the blocks after
-// them clear the empty rows (TOK_THREADS / 32 groups of `per` rows a block).
+// Blocks [0, T segs): one segment of CH x TOK_COLS columns of one token each
+// (CH pieces of 16 bytes a thread, all loaded before any is stored); the blocks
+// after them clear the empty rows (TOK_THREADS / 32 groups of `per` rows a
+// block).
+template <int CH>
 __global__ void __launch_bounds__(TOK_THREADS)
     k_moe_dispatch(const __nv_bfloat16* __restrict__ x, const int* __restrict__ pos,
                    const int* __restrict__ src, __nv_bfloat16* __restrict__ xs, long long rows,
@@ -54,13 +59,19 @@ __global__ void __launch_bounds__(TOK_THREADS)
     zero_empty_rows(src, rows, group, per, xs, H);
     return;
   }
-  const int t = blockIdx.x / segs, c = (blockIdx.x % segs) * TOK_COLS + 8 * threadIdx.x;
-  if (c >= H) return;
-  const uint4 v = ld_global_v4(x + static_cast<size_t>(t) * H + c);
+  const int t = blockIdx.x / segs, c0 = (blockIdx.x % segs) * (CH * TOK_COLS) + 8 * threadIdx.x;
+  uint4 v[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    if (c0 + i * TOK_COLS < H) v[i] = ld_global_v4(x + static_cast<size_t>(t) * H + c0 + i * TOK_COLS);
   const int* p = pos + static_cast<size_t>(t) * top_k;
   for (int j = 0; j < top_k; ++j) {
     const int r = p[j];
-    if (r >= 0) st_global_v4(xs + static_cast<size_t>(r) * H + c, v);
+    if (r < 0) continue;
+    __nv_bfloat16* o = xs + static_cast<size_t>(r) * H + c0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (c0 + i * TOK_COLS < H) st_global_v4(o + i * TOK_COLS, v[i]);
   }
 }
 
@@ -74,42 +85,58 @@ __device__ __forceinline__ void fma8(float (&a)[8], float w, const uint4& v) {
   }
 }
 
-template <bool HAS_W, bool W_BF16>
+template <bool HAS_W, bool W_BF16, int CH>
 __global__ void __launch_bounds__(TOK_THREADS)
     k_moe_combine(const __nv_bfloat16* __restrict__ y, const int* __restrict__ pos,
                   const void* __restrict__ weights, const __nv_bfloat16* residual,
                   __nv_bfloat16* out, int top_k, int H, int segs) {
   pdl_wait();
   pdl_launch_dependents();
-  const int t = blockIdx.x / segs, c = (blockIdx.x % segs) * TOK_COLS + 8 * threadIdx.x;
-  if (c >= H) return;
-  const size_t s0 = static_cast<size_t>(t) * top_k, o = static_cast<size_t>(t) * H + c;
-  float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (residual) fma8(a, 1.f, ld_global_v4(residual + o));
-  // four slots' rows in flight at a time
-  for (int j0 = 0; j0 < top_k; j0 += 4) {
-    uint4 v[4];
-    float w[4];
-    int r[4];
+  const int t = blockIdx.x / segs, c0 = (blockIdx.x % segs) * (CH * TOK_COLS) + 8 * threadIdx.x;
+  const size_t s0 = static_cast<size_t>(t) * top_k, o = static_cast<size_t>(t) * H + c0;
+  float a[CH][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = j0 + j < top_k ? pos[s0 + j0 + j] : -1;
+  for (int i = 0; i < CH; ++i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int e = 0; e < 8; ++e) a[i][e] = 0.f;
+    if (residual && c0 + i * TOK_COLS < H) fma8(a[i], 1.f, ld_global_v4(residual + o + i * TOK_COLS));
+  }
+  // SL slots' rows in flight at a time
+  constexpr int SL = CH == 1 ? 4 : 2;
+  for (int j0 = 0; j0 < top_k; j0 += SL) {
+    uint4 v[SL][CH];
+    float w[SL];
+    int r[SL];
+#pragma unroll
+    for (int j = 0; j < SL; ++j) r[j] = j0 + j < top_k ? pos[s0 + j0 + j] : -1;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
       w[j] = 1.f;
-      if (r[j] >= 0) {
-        v[j] = ld_global_v4(y + static_cast<size_t>(r[j]) * H + c);
-        if constexpr (HAS_W) w[j] = ld_weight<W_BF16>(weights, s0 + j0 + j);
-      }
+      if (r[j] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (c0 + i * TOK_COLS < H)
+          v[j][i] = ld_global_v4(y + static_cast<size_t>(r[j]) * H + c0 + i * TOK_COLS);
+      if constexpr (HAS_W) w[j] = ld_weight<W_BF16>(weights, s0 + j0 + j);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (r[j] >= 0) fma8(a, w[j], v[j]);
+    for (int j = 0; j < SL; ++j) {
+      if (r[j] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (c0 + i * TOK_COLS < H) fma8(a[i], w[j], v[j][i]);
+    }
   }
-  st_global_v4(out + o, make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
-                                   pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7])));
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    if (c0 + i * TOK_COLS < H)
+      st_global_v4(out + o + i * TOK_COLS,
+                   make_uint4(pack_bf16x2(a[i][0], a[i][1]), pack_bf16x2(a[i][2], a[i][3]),
+                              pack_bf16x2(a[i][4], a[i][5]), pack_bf16x2(a[i][6], a[i][7])));
 }
 
-constexpr int BWD_SLOTS = 4;  // slots of a token in one walk over its columns
+constexpr int BWD_SLOTS = 4;   // slots of a token in one walk over its columns
+constexpr int BWD_PIECES = 2;  // 16-byte pieces of each row a thread has in flight
 
 // One block per token (and the blocks that clear dy's empty rows): the
 // token's gradient row against the rows of up to BWD_SLOTS slots at a time.
@@ -141,40 +168,50 @@ __global__ void __launch_bounds__(TOK_THREADS)
       w[j] = dy != nullptr && r[j] >= 0 ? ld_weight<W_BF16>(weights, s) : 0.f;
       acc[j] = 0.f;
     }
-    for (int c = 8 * threadIdx.x; c < H; c += TOK_COLS) {
-      const uint4 dv = ld_global_v4(d + c);
-      const uint32_t dq[4] = {dv.x, dv.y, dv.z, dv.w};
-      float f[8];
+    for (int c0 = 8 * threadIdx.x; c0 < H; c0 += BWD_PIECES * TOK_COLS) {
+      uint4 dv[BWD_PIECES], v[BWD_PIECES][BWD_SLOTS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = unpack_bf16x2(dq[i]);
-        f[2 * i] = u.x;
-        f[2 * i + 1] = u.y;
-      }
-      uint4 v[BWD_SLOTS];
-      if (dweights) {
-#pragma unroll
-        for (int j = 0; j < BWD_SLOTS; ++j)
-          if (r[j] >= 0) v[j] = ld_global_v4(y + static_cast<size_t>(r[j]) * H + c);
-      }
-#pragma unroll
-      for (int j = 0; j < BWD_SLOTS; ++j) {
-        if (r[j] < 0) continue;
+      for (int i = 0; i < BWD_PIECES; ++i) {
+        const int c = c0 + i * TOK_COLS;
+        if (c >= H) continue;
+        dv[i] = ld_global_v4(d + c);
         if (dweights) {
-          const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 u = unpack_bf16x2(q[i]);
-            acc[j] = fmaf(f[2 * i], u.x, acc[j]);
-            acc[j] = fmaf(f[2 * i + 1], u.y, acc[j]);
-          }
+          for (int j = 0; j < BWD_SLOTS; ++j)
+            if (r[j] >= 0) v[i][j] = ld_global_v4(y + static_cast<size_t>(r[j]) * H + c);
         }
-        if (dy)
-          st_global_v4(dy + static_cast<size_t>(r[j]) * H + c,
-                       make_uint4(pack_bf16x2(w[j] * f[0], w[j] * f[1]),
-                                  pack_bf16x2(w[j] * f[2], w[j] * f[3]),
-                                  pack_bf16x2(w[j] * f[4], w[j] * f[5]),
-                                  pack_bf16x2(w[j] * f[6], w[j] * f[7])));
+      }
+#pragma unroll
+      for (int i = 0; i < BWD_PIECES; ++i) {
+        const int c = c0 + i * TOK_COLS;
+        if (c >= H) continue;
+        const uint32_t dq[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 u = unpack_bf16x2(dq[k]);
+          f[2 * k] = u.x;
+          f[2 * k + 1] = u.y;
+        }
+#pragma unroll
+        for (int j = 0; j < BWD_SLOTS; ++j) {
+          if (r[j] < 0) continue;
+          if (dweights) {
+            const uint32_t q[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 u = unpack_bf16x2(q[k]);
+              acc[j] = fmaf(f[2 * k], u.x, acc[j]);
+              acc[j] = fmaf(f[2 * k + 1], u.y, acc[j]);
+            }
+          }
+          if (dy)
+            st_global_v4(dy + static_cast<size_t>(r[j]) * H + c,
+                         make_uint4(pack_bf16x2(w[j] * f[0], w[j] * f[1]),
+                                    pack_bf16x2(w[j] * f[2], w[j] * f[3]),
+                                    pack_bf16x2(w[j] * f[4], w[j] * f[5]),
+                                    pack_bf16x2(w[j] * f[6], w[j] * f[7])));
+        }
       }
     }
     if (!dweights) continue;
@@ -214,6 +251,15 @@ cudaError_t launch_tok(void (*kern)(Args...), long long blocks, cudaStream_t str
 
 using bf = __nv_bfloat16;
 
+// 16-byte pieces of a row that a thread holds: with many slots a token their
+// rows are in flight together; with few, more pieces of each row are, once
+// there are enough blocks for all SMs without.
+int pieces(int T, int top_k, int H) {
+  const long long blocks = static_cast<long long>(T) * ((H + TOK_COLS - 1) / TOK_COLS);
+  if (blocks < 16 * 152 || H <= TOK_COLS) return 1;
+  return top_k >= 4 || H <= 2 * TOK_COLS ? 2 : 4;
+}
+
 // Rows a warp looks at for empty ones: one while that leaves few warps (up to
 // about 64 an SM), at most four.
 int zero_rows(const MoePlan& L) { return L.rows <= 10240 ? 1 : L.rows <= 20480 ? 2 : 4; }
@@ -226,9 +272,10 @@ long long zero_blocks(const MoePlan& L) {
 
 cudaError_t launch_moe_dispatch(const void* x, const int* plan, const MoePlan& L, int T, int top_k,
                                 int H, void* xs, cudaStream_t stream, bool pdl) {
-  const int segs = (H + TOK_COLS - 1) / TOK_COLS;
+  const int ch = pieces(T, top_k, H), segs = (H + ch * TOK_COLS - 1) / (ch * TOK_COLS);
   const long long tokens = static_cast<long long>(T) * segs;
-  return launch_tok(k_moe_dispatch, tokens + zero_blocks(L), stream, pdl,
+  return launch_tok(ch == 1 ? k_moe_dispatch<1> : ch == 2 ? k_moe_dispatch<2> : k_moe_dispatch<4>,
+                    tokens + zero_blocks(L), stream, pdl,
                     static_cast<const bf*>(x), plan + L.pos, plan + L.src, static_cast<bf*>(xs),
                     L.rows, top_k, H, segs, tokens, zero_rows(L));
 }
@@ -236,10 +283,16 @@ cudaError_t launch_moe_dispatch(const void* x, const int* plan, const MoePlan& L
 cudaError_t launch_moe_combine(const void* y, const int* plan, const MoePlan& L, int T, int top_k,
                                int H, const void* weights, bool w_bf16, const void* residual,
                                void* out, cudaStream_t stream, bool pdl) {
-  const int segs = (H + TOK_COLS - 1) / TOK_COLS;
-  auto kern = weights == nullptr ? k_moe_combine<false, false>
-              : w_bf16           ? k_moe_combine<true, true>
-                                 : k_moe_combine<true, false>;
+  const int ch = pieces(T, top_k, H), segs = (H + ch * TOK_COLS - 1) / (ch * TOK_COLS);
+  auto pick = [&](auto c) {
+    constexpr int CH = decltype(c)::value;
+    return weights == nullptr ? k_moe_combine<false, false, CH>
+           : w_bf16           ? k_moe_combine<true, true, CH>
+                              : k_moe_combine<true, false, CH>;
+  };
+  auto kern = ch == 1   ? pick(std::integral_constant<int, 1>{})
+              : ch == 2 ? pick(std::integral_constant<int, 2>{})
+                        : pick(std::integral_constant<int, 4>{});
   return launch_tok(kern, static_cast<long long>(T) * segs, stream, pdl, static_cast<const bf*>(y),
                     plan + L.pos, weights, static_cast<const bf*>(residual), static_cast<bf*>(out),
                     top_k, H, segs);

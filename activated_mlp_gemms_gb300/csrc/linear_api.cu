@@ -33,7 +33,7 @@ int linear_act(int act) {
   switch (act) {
     case MLP_LINEAR_RELU: return ACT_RELU;
     case MLP_LINEAR_RELU_SQ: return ACT_RELU_SQ;
-    case MLP_LINEAR_GELU_TANH: return ACT_GELU_TANH;
+    case MLP_LINEAR_GELU_TANH: return ACT_GELU_HW;
     case MLP_LINEAR_SILU: return ACT_SILU;
     case MLP_LINEAR_SIGMOID: return ACT_SIGMOID;
     default: return ACT_NONE;
@@ -141,7 +141,7 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   switch (act) {
     case ACT_RELU: return run_linear<ACT_RELU>(g, c);
     case ACT_RELU_SQ: return run_linear<ACT_RELU_SQ>(g, c);
-    case ACT_GELU_TANH: return run_linear<ACT_GELU_TANH>(g, c);
+    case ACT_GELU_HW: return run_linear<ACT_GELU_HW>(g, c);
     case ACT_SILU: return run_linear<ACT_SILU>(g, c);
     case ACT_SIGMOID: return run_linear<ACT_SIGMOID>(g, c);
     default: return run_linear<ACT_NONE>(g, c);

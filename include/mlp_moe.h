@@ -114,8 +114,9 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
                         size_t ws_bytes, void* stream);
 
 /* The whole layer without gradients: sort, dispatch, experts, combine, with
- * everything between in the workspace.  Up to eight tokens (and 128 slots)
- * stream the weights of the experts they use instead, in two kernels.
+ * everything between in the workspace.  Up to eight tokens (with at
+ * most 128 slots and 1 GB of the experts' weights between them) stream the
+ * weights of the experts they use instead, in two kernels.
  *   x bf16 [T,H], ids int32 [T,top_k], weights [T,top_k] (weights_type),
  *   residual bf16 [T,H] or NULL, out bf16 [T,H] (may be residual itself) */
 int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const void* weights,
