@@ -79,25 +79,29 @@ __device__ __forceinline__ Work decode_unit(const Params& p, int unit) {
   return w;
 }
 
-// GRP, A K-major: unit -> (row tile of the plan, tile column), the row tiles
-// in groups of group_m as above.
-__device__ __forceinline__ Work decode_row_unit(const Params& p, int unit, int ntiles) {
+// GRP, A K-major: unit -> (expert, row tile, tile column).  Experts one after
+// the other, so that the pairs at work share one expert's weights (with row
+// tiles of several experts in a raster group, each weight panel was read for
+// fewer of them); within an expert the raster above.
+template <int TILE_M>
+__device__ __forceinline__ Work decode_row_unit(const Params& p, int unit) {
   const Prob& P = p.prob[0];
+  const int4 t = __ldg(reinterpret_cast<const int4*>(p.tiles + unit / P.tiles_n));
+  const int u = unit - t.w * P.tiles_n, tiles = (t.z - t.y + TILE_M - 1) / TILE_M;
   const int per_group = p.group_m * P.tiles_n;
-  const int g = unit / per_group;
+  const int g = u / per_group;
   const int first_m = g * p.group_m;
-  const int gsz = min(ntiles - first_m, p.group_m);
-  const int r = unit - g * per_group;
+  const int gsz = min(tiles - first_m, p.group_m);
+  const int r = u - g * per_group;
   Work w;
   w.prob = 0;
   w.tm = first_m + r % gsz;
   w.tn = r / gsz;
   w.kb_begin = 0;
   w.kb_end = P.kb0 + P.kb1;
-  const int4 t = __ldg(reinterpret_cast<const int4*>(p.tiles + w.tm));
   w.expert = t.x;
-  w.row0 = t.y;
-  w.row_end = t.z;
+  w.row0 = t.y + w.tm * TILE_M;
+  w.row_end = min(t.z, w.row0 + TILE_M);
   return w;
 }
 
@@ -132,11 +136,11 @@ __device__ __forceinline__ Work decode_expert_unit(const Params& p, int unit) {
   return w;
 }
 
-template <bool GRP, bool A_MN>
-__device__ __forceinline__ Work decode(const Params& p, int unit, int ntiles) {
+template <bool GRP, bool A_MN, int TILE_M>
+__device__ __forceinline__ Work decode(const Params& p, int unit) {
   if constexpr (!GRP) return decode_unit(p, unit);
   else if constexpr (A_MN) return decode_expert_unit(p, unit);
-  else return decode_row_unit(p, unit, ntiles);
+  else return decode_row_unit<TILE_M>(p, unit);
 }
 
 // The units of a problem that run the gated forward epilogue.
@@ -1068,39 +1072,42 @@ __device__ __forceinline__ void epi_plain(const Params& p, const EpiUnit& P, con
 }
 
 // The experts' plain bf16 store.  A tile of few k-blocks (an expert's rows, in
-// a weight gradient) is bound by its epilogue: chunk c + 1 leaves the
-// accumulator while chunk c is packed, and the two boxes alternate, so a box
-// is refilled while the other's store still reads.
+// a weight gradient) is bound by its stores, so they go out in boxes of 32 rows
+// x 64 columns: 128-byte rows, half as many of them for the TMA unit as the
+// 32 x 32 boxes make.  (Box of 4 KB, 128-byte swizzle: 16-byte unit u of row r
+// at unit u ^ (r % 8).)
 template <bool STACK>
-__device__ __forceinline__ void epi_store_grp(const EpiUnit& P, EpiWarp& e, uint32_t tb, int col0,
-                                              int cb, int ce) {
-  if (col0 + cb >= P.N) return;
-  uint32_t d[2][32];
-  __syncwarp();
-  tmem_ld32(tb + cb, d[0]);
+__device__ __forceinline__ void epi_store_grp(const EpiUnit& P, const EpiWarp& e, uint32_t tb,
+                                              int col0, int cb, int ce) {
+  const uint32_t rb = e.stg + static_cast<uint32_t>(e.lane) * 128u;
+  const uint32_t x = static_cast<uint32_t>(e.lane) & 7u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = cb + 32 * i, col = col0 + c;
+  for (int c = cb; c < ce; c += 64) {
+    const int col = col0 + c;
     if (col >= P.N) break;  // warp-uniform
+    uint32_t d[2][32];
+    __syncwarp();
+    tmem_ld32(tb + c, d[0]);
+    tmem_ld32(tb + c + 32, d[1]);
     tmem_wait_ld();
-    if (i < 3 && col + 32 < P.N) tmem_ld32(tb + c + 32, d[(i + 1) & 1]);
-    uint32_t q[16];
+    staging_acquire(e);
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      q[j] = pack_bf16x2(__uint_as_float(d[i & 1][2 * j]), __uint_as_float(d[i & 1][2 * j + 1]));
-    const uint32_t buf = e.stg + e.box * 2048u;
-    e.box ^= 1u;
-    staging_wait_read_but_one(e);
-    stage_bf16(buf, e.lane, q);
+    for (uint32_t u = 0; u < 8; ++u) {
+      const uint32_t(&v)[32] = d[u >> 2];
+      const uint32_t k = 8 * (u & 3);
+      auto pk = [&](uint32_t i) {
+        return pack_bf16x2(__uint_as_float(v[k + i]), __uint_as_float(v[k + i + 1]));
+      };
+      st_shared_v4(rb + ((u ^ x) << 4), pk(0), pk(2), pk(4), pk(6));
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (e.lane == 0) {
-      if constexpr (STACK) tma_store_3d(P.out[0], buf, col, e.row0, e.expert);
-      else tma_store_2d(P.out[0], buf, col, e.row0);
+      if constexpr (STACK) tma_store_3d(P.out[0], e.stg, col, e.row0, e.expert);
+      else tma_store_2d(P.out[0], e.stg, col, e.row0);
       bulk_commit();
     }
   }
-  tmem_wait_ld();
 }
 
 // EPI_FWD_FUSED: the producer thread of a down unit waits (bounded) until
@@ -1146,7 +1153,7 @@ struct Cfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  // (the experts' plain store alternates two boxes per warp)
+  // (the experts' plain store: one box of 32 x 64)
   static constexpr int STG_WARP = GRP && EPI == EPI_STORE_BF16 ? 4096 : EpiTraits<EPI>::STG_WARP;
   static constexpr int STG = NUM_EPI_WARPS * STG_WARP;
   static constexpr int MAX_SMEM = 232448;  // per-block opt-in limit
@@ -1366,8 +1373,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
   const uint64_t lim = p.timeout_ns;
   const int ncl = gridDim.x / CG;          // clusters (CTA groups) in the grid
   // GRP over rows: how many tiles there are is in the plan
-  const int ntiles = GRP_ROWS ? __ldg(p.ntiles) : 0;
-  const int total_units = GRP_ROWS ? ntiles * p.prob[0].tiles_n : p.total_units;
+  const int total_units = GRP_ROWS ? __ldg(p.ntiles) * p.prob[0].tiles_n : p.total_units;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -1415,7 +1421,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             }
           }
           if (unit >= total_units) break;
-          const Work w = decode<GRP, A_MN>(p, unit, ntiles);
+          const Work w = decode<GRP, A_MN, C::TILE_M>(p, unit);
           // The next unit, fetched now and needed when it is published.  A
           // down unit of the fused forward (K = I, several times a gate/up
           // unit's length) fetches it only when it publishes it, half-way
@@ -1481,7 +1487,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           if (v < 0) break;
-          const Work w = decode<GRP, A_MN>(p, v, ntiles);
+          const Work w = decode<GRP, A_MN, C::TILE_M>(p, v);
           const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
           if constexpr (EpiTraits<EPI>::DACT) {
             if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
@@ -1552,7 +1558,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         mbar_arrive(bar_s(SEMPTY + slot));
         if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
         if (unit < 0) break;
-        const Work w = decode<GRP, A_MN>(p, unit, ntiles);
+        const Work w = decode<GRP, A_MN, C::TILE_M>(p, unit);
         // the fused recompute's second K segment goes to the other accumulator
         const int kswitch = is_recomp(EPI) ? p.prob[w.prob].kb0 : -1;
         if (!mbar_wait<PAIR>(bar_s(TEMPTY + acc), aphase ^ 1u, lim, abort_flag)) { ok = false; break; }
@@ -1669,7 +1675,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
       }
       if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
       if (unit < 0) break;
-      const Work w = decode<GRP, A_MN>(p, unit, ntiles);
+      const Work w = decode<GRP, A_MN, C::TILE_M>(p, unit);
       const int pi = w.prob;
       EpiUnit P = epi_unit<EPI>(p, p.prob[pi],
                                       pi == 0 ? f8_deq[0] : pi == 1 ? f8_deq[1] : f8_deq[2],
@@ -1769,7 +1775,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           epi_recomp_f8_dh(P, e, tb, col0, cb, dd);
         } else {
           if constexpr (GRP && EPI == EPI_STORE_BF16) {
-            static_assert(MMA_N == 256, "four chunks of 32 columns a warp");
             epi_store_grp<GRP_SUM>(P, e, tb, col0, cb, ce);
           } else {
             epi_plain<EPI, GRP_SUM>(p, P, e, tb, col0, cb, ce);

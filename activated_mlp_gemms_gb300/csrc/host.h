@@ -277,22 +277,24 @@ struct Gemm {
   int output_stack(void* ptr, int depth, int rows, int cols, bool f32) {
     if (!ptr) return -1;
     if (nmaps >= MAX_MAPS) { ok = false; return -1; }
-    if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, 32, 32, f32,
-                  f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, depth,
-                  (uint64_t)rows * cols))
+    // fp32 boxes 32 x 32, bf16 boxes 64 x 32: 128-byte rows
+    if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, f32 ? 32 : 64, 32, f32,
+                  CU_TENSOR_MAP_SWIZZLE_128B, depth, (uint64_t)rows * cols))
       ok = false;
     return nmaps++;
   }
   // bf16 output of P over the sorted rows: boxes of 32 rows, and of 16 for the
-  // last rows of an expert
-  void output_rows(Prob& P, int i, void* ptr, int rows, int cols) {
-    P.mapO[i] = output(ptr, rows, cols);
-    P.mapO16[i] = -1;
+  // last rows of an expert; 32 columns (64-byte swizzle), or 64 (wide, the
+  // plain store's; 128-byte swizzle)
+  void output_rows(Prob& P, int i, void* ptr, int rows, int cols, bool wide = false) {
+    P.mapO[i] = P.mapO16[i] = -1;
     if (!ptr) return;
-    if (nmaps >= MAX_MAPS) { ok = false; return; }
-    if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, 32, 16, 0, CU_TENSOR_MAP_SWIZZLE_64B))
-      ok = false;
-    P.mapO16[i] = nmaps++;
+    const CUtensorMapSwizzle swz = wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    for (int box : {32, 16}) {
+      if (nmaps >= MAX_MAPS) { ok = false; return; }
+      if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, wide ? 64 : 32, box, 0, swz)) ok = false;
+      (box == 32 ? P.mapO : P.mapO16)[i] = nmaps++;
+    }
   }
   // ke: K elements per k-block (bf16 64, e4m3 128: a 128-byte row either way)
   Prob& add(int M, int N, int K0, int K1, int tile_n, int ksplit = 1, int ke = BK) {

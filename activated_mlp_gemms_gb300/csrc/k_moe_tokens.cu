@@ -138,25 +138,29 @@ __global__ void __launch_bounds__(TOK_THREADS)
 constexpr int BWD_SLOTS = 4;   // slots of a token in one walk over its columns
 constexpr int BWD_PIECES = 2;  // 16-byte pieces of each row a thread has in flight
 
-// One block per token (and the blocks that clear dy's empty rows): the
-// token's gradient row against the rows of up to BWD_SLOTS slots at a time.
-template <bool W_BF16>
+// TPT threads per token (and the blocks that clear dy's empty rows): the token's
+// gradient row against the rows of up to BWD_SLOTS slots at a time.  A warp per
+// token needs no block-wide sum; a block per token serves few tokens.
+template <bool W_BF16, int TPT>
 __global__ void __launch_bounds__(TOK_THREADS)
     k_moe_combine_bwd(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ y,
                       const int* __restrict__ pos, const int* __restrict__ src,
                       const void* __restrict__ weights, __nv_bfloat16* __restrict__ dy,
                       void* __restrict__ dweights, long long rows, int T, int top_k, int H,
-                      int per) {
+                      int per, int token_blocks) {
   __shared__ float part[TOK_THREADS / 32][BWD_SLOTS];
   pdl_wait();
   pdl_launch_dependents();
-  if (blockIdx.x >= T) {
-    const long long group = (blockIdx.x - T) * (TOK_THREADS / 32) + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x >= token_blocks) {
+    const long long group = (blockIdx.x - token_blocks) * (TOK_THREADS / 32) + warp;
     zero_empty_rows(src, rows, group, per, dy, H);
     return;
   }
-  const size_t t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int STEP = 8 * TPT;  // columns of one piece of all the token's threads
+  const int tid = threadIdx.x % TPT;
+  const size_t t = static_cast<size_t>(blockIdx.x) * (TOK_THREADS / TPT) + threadIdx.x / TPT;
+  if (t >= T) return;  // warp-uniform (TPT = 32) or never
   const __nv_bfloat16* d = dout + t * H;
   for (int j0 = 0; j0 < top_k; j0 += BWD_SLOTS) {
     int r[BWD_SLOTS];
@@ -168,11 +172,11 @@ __global__ void __launch_bounds__(TOK_THREADS)
       w[j] = dy != nullptr && r[j] >= 0 ? ld_weight<W_BF16>(weights, s) : 0.f;
       acc[j] = 0.f;
     }
-    for (int c0 = 8 * threadIdx.x; c0 < H; c0 += BWD_PIECES * TOK_COLS) {
+    for (int c0 = 8 * tid; c0 < H; c0 += BWD_PIECES * STEP) {
       uint4 dv[BWD_PIECES], v[BWD_PIECES][BWD_SLOTS];
 #pragma unroll
       for (int i = 0; i < BWD_PIECES; ++i) {
-        const int c = c0 + i * TOK_COLS;
+        const int c = c0 + i * STEP;
         if (c >= H) continue;
         dv[i] = ld_global_v4(d + c);
         if (dweights) {
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(TOK_THREADS)
       }
 #pragma unroll
       for (int i = 0; i < BWD_PIECES; ++i) {
-        const int c = c0 + i * TOK_COLS;
+        const int c = c0 + i * STEP;
         if (c >= H) continue;
         const uint32_t dq[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
         float f[8];
@@ -219,18 +223,24 @@ __global__ void __launch_bounds__(TOK_THREADS)
     for (int j = 0; j < BWD_SLOTS; ++j) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-      if (lane == 0) part[warp][j] = acc[j];
+      if (TPT > 32 && lane == 0) part[warp][j] = acc[j];
     }
-    __syncthreads();
-    if (threadIdx.x < BWD_SLOTS && j0 + threadIdx.x < top_k) {
+    if (TPT > 32) __syncthreads();
+    if (tid < BWD_SLOTS && j0 + tid < top_k) {
       float sum = 0.f;
+      if constexpr (TPT > 32) {
 #pragma unroll
-      for (int k = 0; k < TOK_THREADS / 32; ++k) sum += part[k][threadIdx.x];
-      const size_t s = t * top_k + j0 + threadIdx.x;
+        for (int k = 0; k < TOK_THREADS / 32; ++k) sum += part[k][tid];
+      } else {
+#pragma unroll
+        for (int j = 0; j < BWD_SLOTS; ++j)
+          if (tid == j) sum = acc[j];
+      }
+      const size_t s = t * top_k + j0 + tid;
       if constexpr (W_BF16) static_cast<__nv_bfloat16*>(dweights)[s] = __float2bfloat16_rn(sum);
       else static_cast<float*>(dweights)[s] = sum;
     }
-    __syncthreads();
+    if (TPT > 32) __syncthreads();
   }
 }
 
@@ -302,11 +312,15 @@ cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* p
                                    const MoePlan& L, int T, int top_k, int H, const void* weights,
                                    bool w_bf16, void* dy, void* dweights, cudaStream_t stream,
                                    bool pdl) {
-  auto kern = w_bf16 ? k_moe_combine_bwd<true> : k_moe_combine_bwd<false>;
-  return launch_tok(kern, T + (dy ? zero_blocks(L) : 0), stream, pdl, static_cast<const bf*>(dout),
-                    static_cast<const bf*>(y), plan + L.pos, plan + L.src, weights,
-                    static_cast<bf*>(dy), dweights, L.rows, T, top_k, H,
-                    zero_rows(L));
+  // a warp per token once that gives every SM eight of them
+  const bool warps = T >= 8 * 152;
+  auto kern = w_bf16 ? (warps ? k_moe_combine_bwd<true, 32> : k_moe_combine_bwd<true, TOK_THREADS>)
+                     : (warps ? k_moe_combine_bwd<false, 32> : k_moe_combine_bwd<false, TOK_THREADS>);
+  const int tokens = warps ? (T + TOK_THREADS / 32 - 1) / (TOK_THREADS / 32) : T;
+  return launch_tok(kern, tokens + (dy ? zero_blocks(L) : 0), stream, pdl,
+                    static_cast<const bf*>(dout), static_cast<const bf*>(y), plan + L.pos,
+                    plan + L.src, weights, static_cast<bf*>(dy), dweights, L.rows, T, top_k, H,
+                    zero_rows(L), tokens);
 }
 
 }  // namespace mlpk

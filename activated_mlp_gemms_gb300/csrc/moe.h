@@ -10,10 +10,10 @@ namespace mlpk {
 constexpr int MOE_ALIGN = 16;          // MLP_MOE_ROW_ALIGN
 constexpr int MOE_MAX_EXPERTS = 1024;  // MLP_MOE_MAX_EXPERTS
 
-// One 128- or 256-row output tile of the experts' GEMMs: rows [row, end) of
-// `expert` (at most the tile's height of them).
+// What a row tile of the experts' GEMMs (128 or 256 rows) belongs to: its
+// expert's rows [row, end), whose tiles begin at tile `first`.
 struct MoeTile {
-  int expert, row, end, pad;
+  int expert, row, end, first;
 };
 
 // Where the parts of the plan are, in int32 values.

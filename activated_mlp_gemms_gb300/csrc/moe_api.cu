@@ -170,7 +170,7 @@ int launch_experts_down(const mlp_moe_t* p, Call& c, const int* plan, const void
   P.l2b = L2_EVICT_FIRST;
   P.mapA0 = mA;
   P.mapB0 = mB;
-  g.output_rows(P, 0, y, static_cast<int>(g.L.rows), p->H);
+  g.output_rows(P, 0, y, static_cast<int>(g.L.rows), p->H, true);
   return run<EPI_STORE_BF16, false, false, true>(g, c, MLP_KERNEL_DOWN);
 }
 
@@ -377,7 +377,7 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
     P.mapB0 = mB0;
     P.mapA1 = mA1;
     P.mapB1 = mB1;
-    g.output_rows(P, 0, dxs, rows, p->H);
+    g.output_rows(P, 0, dxs, rows, p->H, true);
     MLP_TRY((run<EPI_STORE_BF16, false, true, true>(g, c, MLP_KERNEL_DX)));
   }
   if (want_w) {

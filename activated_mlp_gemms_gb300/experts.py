@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from collections.abc import Mapping
 
 import torch
 
@@ -107,17 +108,35 @@ def _plan(p: Moe, plan):
     return _shaped(plan, (_layout(p).ints,), "plan", torch.int32)
 
 
-def moe_plan_views(p: Moe, plan) -> dict:
+class _PlanViews(Mapping):
+    """The plan's public parts, each made a view when it is asked for."""
+
+    def __init__(self, p, plan):
+        self._p, self._plan = p, plan
+
+    def __getitem__(self, name):
+        p, L = self._p, _layout(self._p)
+        if name == "pos":
+            size, stride = (p.T, p.top_k), (p.top_k, 1)
+        else:
+            size, stride = {"offsets": (p.E + 1,), "counts": (p.E,),
+                            "src": (mlp_moe_rows(p),)}[name], (1,)
+        return self._plan.as_strided(size, stride,
+                                     self._plan.storage_offset() + getattr(L, name))
+
+    def __iter__(self):
+        return iter(("offsets", "counts", "pos", "src"))
+
+    def __len__(self):
+        return 4
+
+
+def moe_plan_views(p: Moe, plan) -> Mapping:
     """The plan's public parts as views: offsets [E + 1] (first row of each expert),
     counts [E], pos [T, top_k] (row of each slot, -1 when dropped), src [rows] (slot of
     each row, -1 for padding)."""
     _plan(p, plan)
-    L = _layout(p)
-    at = plan.storage_offset()
-    return {"offsets": plan.as_strided((p.E + 1,), (1,), at + L.offsets),
-            "counts": plan.as_strided((p.E,), (1,), at + L.counts),
-            "pos": plan.as_strided((p.T, p.top_k), (p.top_k, 1), at + L.pos),
-            "src": plan.as_strided((mlp_moe_rows(p),), (1,), at + L.src)}
+    return _PlanViews(p, plan)
 
 
 def mlp_moe_sort(p: Moe, ids, plan, stream=None) -> None:
@@ -172,6 +191,12 @@ def mlp_moe_workspace_size(p: Moe, mode: int) -> int:
     return int(lib().mlp_moe_workspace_size(ctypes.byref(p), int(mode)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _ws_size(T, E, top_k, H, I, act, mode):
+    """The workspace size: a function of the sizes alone."""
+    return mlp_moe_workspace_size(Moe(T, E, top_k, H, I, act, 1.0, 1.0, 0), mode)
+
+
 def alloc_moe_workspace(p: Moe, mode: int, device=None) -> torch.Tensor:
     n = mlp_moe_workspace_size(p, mode)
     if n == 0:
@@ -181,7 +206,10 @@ def alloc_moe_workspace(p: Moe, mode: int, device=None) -> torch.Tensor:
 
 def _ws(ws, p, mode, device):
     if ws is None:
-        return alloc_moe_workspace(p, mode, device)
+        n = _ws_size(p.T, p.E, p.top_k, p.H, p.I, p.act, mode)
+        if n == 0:  # (the call itself says why)
+            n = 256
+        return torch.empty(n, dtype=torch.uint8, device=device)
     if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return ws

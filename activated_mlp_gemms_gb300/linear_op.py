@@ -10,6 +10,7 @@ of 8); the other tensors are contiguous.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -45,6 +46,7 @@ def linear(M, N, K, act="none", resid_scale=1.0) -> Linear:
 
 
 def _dense(t, shape, name, dtype=torch.bfloat16):
+    """The tensor's address (None stays None) once its type, device and shape are right."""
     if t is None:
         return None
     p = _ptr(t, dtype, name)
@@ -57,13 +59,13 @@ def _pitched(t, shape, name):
     """(address, row pitch or 0 when dense) of a bf16 matrix with unit column stride."""
     if t is None:
         return None, 0
-    if isinstance(t, torch.Tensor) and t.is_contiguous():
-        return _dense(t, shape, name), 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.is_contiguous():
+        return _dense(t, shape, name), 0
     if not t.is_cuda or t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.stride(1) != 1 or t.stride(0) < shape[1]:
         raise ValueError(f"{name} must have unit stride along its last dimension and rows "
@@ -82,6 +84,12 @@ def mlp_linear_workspace_size(p: Linear, backward=False) -> int:
     return int(lib().mlp_linear_workspace_size(ctypes.byref(p), int(bool(backward))))
 
 
+@functools.lru_cache(maxsize=1024)
+def _ws_size(M, N, K, act, backward):
+    """The workspace size: a function of the sizes alone."""
+    return mlp_linear_workspace_size(Linear(M, N, K, act), backward)
+
+
 def alloc_linear_workspace(p: Linear, backward=False, device=None) -> torch.Tensor:
     n = mlp_linear_workspace_size(p, backward)
     if n == 0:
@@ -91,7 +99,10 @@ def alloc_linear_workspace(p: Linear, backward=False, device=None) -> torch.Tens
 
 def _ws(ws, p, backward, device):
     if ws is None:
-        return alloc_linear_workspace(p, backward, device)
+        n = _ws_size(p.M, p.N, p.K, p.act, backward)
+        if n == 0:  # (the call itself says why)
+            n = 256
+        return torch.empty(n, dtype=torch.uint8, device=device)
     if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return ws
