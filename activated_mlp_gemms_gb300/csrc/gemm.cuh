@@ -79,68 +79,96 @@ __device__ __forceinline__ Work decode_unit(const Params& p, int unit) {
   return w;
 }
 
-// GRP, A K-major: unit -> (expert, row tile, tile column).  Experts one after
-// the other, so that the pairs at work share one expert's weights (with row
-// tiles of several experts in a raster group, each weight panel was read for
-// fewer of them); within an expert the raster above.
-template <int TILE_M>
-__device__ __forceinline__ Work decode_row_unit(const Params& p, int unit) {
-  const Prob& P = p.prob[0];
-  const int4 t = __ldg(reinterpret_cast<const int4*>(p.tiles + unit / P.tiles_n));
-  const int u = unit - t.w * P.tiles_n, tiles = (t.z - t.y + TILE_M - 1) / TILE_M;
+// GRP: a unit is decoded in two steps, so that the loads of the first (the
+// plan's tables) are in flight while the producer issues its copies.
+struct UnitKey {
+  int prob, u;   // the problem, and the unit within it
+  int4 t;        // A K-major: the expert's entry of the plan's tile list;
+                 // A MN-major: {expert, its first row, the next expert's, -}
+};
+template <bool A_MN>
+__device__ __forceinline__ UnitKey unit_key(const Params& p, int unit) {
+  UnitKey k;
+  k.prob = 0;
+  if constexpr (!A_MN) {
+    k.u = unit;
+    k.t = __ldg(reinterpret_cast<const int4*>(p.tiles + unit / p.prob[0].tiles_n));
+  } else {
+    while (k.prob + 1 < p.nprob && unit >= p.prob[k.prob + 1].unit_begin) ++k.prob;
+    const Prob& P = p.prob[k.prob];
+    const int u = unit - P.unit_begin, tiles = P.tiles_m * P.tiles_n;
+    k.t.x = u / tiles;
+    k.u = u - k.t.x * tiles;
+    k.t.y = __ldg(p.offsets + k.t.x);
+    k.t.z = __ldg(p.offsets + k.t.x + 1);
+    k.t.w = 0;
+  }
+  return k;
+}
+// A K-major: (expert, row tile, tile column), the experts one after the other,
+// so that the pairs at work share one expert's weights (with row tiles of
+// several experts in a raster group, each weight panel was read for fewer of
+// them); within an expert the raster above.
+// A MN-major: (problem, expert, output tile); K runs over the expert's rows.  An
+// expert without rows sums one k-block past the end of the buffers, which TMA
+// fills with zeros.
+template <bool A_MN, int TILE_M>
+__device__ __forceinline__ Work unit_work(const Params& p, const UnitKey& k) {
+  const Prob& P = p.prob[k.prob];
+  const int u = A_MN ? k.u : k.u - k.t.w * P.tiles_n;
+  const int tiles_m = A_MN ? P.tiles_m : (k.t.z - k.t.y + TILE_M - 1) / TILE_M;
   const int per_group = p.group_m * P.tiles_n;
   const int g = u / per_group;
   const int first_m = g * p.group_m;
-  const int gsz = min(tiles - first_m, p.group_m);
+  const int gsz = min(tiles_m - first_m, p.group_m);
   const int r = u - g * per_group;
   Work w;
-  w.prob = 0;
-  w.tm = first_m + r % gsz;
+  w.prob = k.prob;
   w.tn = r / gsz;
+  w.tm = first_m + r - w.tn * gsz;
+  w.expert = k.t.x;
   w.kb_begin = 0;
-  w.kb_end = P.kb0 + P.kb1;
-  w.expert = t.x;
-  w.row0 = t.y + w.tm * TILE_M;
-  w.row_end = min(t.z, w.row0 + TILE_M);
-  return w;
-}
-
-// GRP, A MN-major: unit -> (problem, expert, output tile); K runs over the
-// expert's rows.  An expert without rows sums one k-block past the end of the
-// buffers, which TMA fills with zeros.
-__device__ __forceinline__ Work decode_expert_unit(const Params& p, int unit) {
-  int pi = 0;
-  while (pi + 1 < p.nprob && unit >= p.prob[pi + 1].unit_begin) ++pi;
-  const Prob& P = p.prob[pi];
-  const int u = unit - P.unit_begin;
-  const int tiles = P.tiles_m * P.tiles_n;
-  Work w;
-  w.prob = pi;
-  w.expert = u / tiles;
-  const int t = u - w.expert * tiles;
-  const int per_group = p.group_m * P.tiles_n;
-  const int g = t / per_group;
-  const int first_m = g * p.group_m;
-  const int gsz = min(P.tiles_m - first_m, p.group_m);
-  const int r = t - g * per_group;
-  w.tm = first_m + r % gsz;
-  w.tn = r / gsz;
-  w.row0 = __ldg(p.offsets + w.expert);
-  w.row_end = __ldg(p.offsets + w.expert + 1);
-  if (w.row_end <= w.row0) {
-    w.row0 = p.rows;
-    w.row_end = p.rows + MOE_ALIGN;
+  if constexpr (A_MN) {
+    const bool none = k.t.z <= k.t.y;
+    w.row0 = none ? p.rows : k.t.y;
+    w.row_end = none ? p.rows + MOE_ALIGN : k.t.z;
+    w.kb_end = (w.row_end - w.row0 + BK - 1) / BK;
+  } else {
+    w.row0 = k.t.y + w.tm * TILE_M;
+    w.row_end = min(k.t.z, w.row0 + TILE_M);
+    w.kb_end = P.kb0 + P.kb1;
   }
-  w.kb_begin = 0;
-  w.kb_end = (w.row_end - w.row0 + BK - 1) / BK;
   return w;
 }
 
-template <bool GRP, bool A_MN, int TILE_M>
+// Decodes a unit number: the kernels whose ring carries those.
+template <bool GRP_SUM, int TILE_M>
 __device__ __forceinline__ Work decode(const Params& p, int unit) {
-  if constexpr (!GRP) return decode_unit(p, unit);
-  else if constexpr (A_MN) return decode_expert_unit(p, unit);
-  else return decode_row_unit<TILE_M>(p, unit);
+  if constexpr (GRP_SUM) return unit_work<true, TILE_M>(p, unit_key<true>(p, unit));
+  else return decode_unit(p, unit);
+}
+
+// GRP over rows: the ring carries decoded units, so that only the leader's
+// producer decodes, ahead of time (before, its peer and the MMA issuer did too,
+// between one unit's last k-block and the next one's first: 2-4 % of the down
+// projection and dx).  The weight gradients lost 3-4 % this way, at every
+// length of their sums, and keep a ring of unit numbers.
+struct alignas(16) RingUnit {
+  int prob, tm, tn, kb_end;  // prob < 0: no more work
+  int expert, row0, row_end, pad;
+};
+__device__ __forceinline__ Work ring_get(uint32_t slot) {
+  const uint4 a = ld_shared_v4(slot), b = ld_shared_v4(slot + 16);
+  Work w;
+  w.prob = static_cast<int>(a.x);
+  w.tm = static_cast<int>(a.y);
+  w.tn = static_cast<int>(a.z);
+  w.kb_begin = 0;
+  w.kb_end = static_cast<int>(a.w);
+  w.expert = static_cast<int>(b.x);
+  w.row0 = static_cast<int>(b.y);
+  w.row_end = static_cast<int>(b.z);
+  return w;
 }
 
 // The units of a problem that run the gated forward epilogue.
@@ -1307,8 +1335,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
   // EPI_DGRAD_F8: two barriers per epilogue warp for its TMA-loaded preact boxes
   constexpr int EBAR = DRAIN + 1;
   constexpr int NBAR = EBAR + 2 * NUM_EPI_WARPS;
-  int* sched = reinterpret_cast<int*>(ctrl + 8 * NBAR);
-  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(sched + SCHED_SLOTS);
+  // the unit ring: unit numbers, or decoded units
+  constexpr bool RING = GRP_ROWS;
+  constexpr int RING_AT = RING ? (8 * NBAR + 15) / 16 * 16 : 8 * NBAR;
+  constexpr int RING_BYTES = SCHED_SLOTS * static_cast<int>(RING ? sizeof(RingUnit) : sizeof(int));
+  static_assert(RING_AT + RING_BYTES + 8 <= 1024, "control area");
+  int* sched = reinterpret_cast<int*>(ctrl + RING_AT);
+  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(ctrl + RING_AT + RING_BYTES);
+  auto ring_s = [&](int slot) { return smem_u32(ctrl + RING_AT) + 32u * static_cast<uint32_t>(slot); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_s + 1);
   auto bar_s = [&](int i) { return smem_u32(bar + i); };
 
@@ -1392,7 +1426,92 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
       // testing hook: publish no work, so the consumers' bounded waits expire
       const bool publish_nothing = leader && (p.debug_flags & 1);
       bool first_pub = true;
-      while (ok && !publish_nothing) {
+      if constexpr (RING) {
+        // The leader decodes the next unit in two steps in the middle of the
+        // current one's k-blocks and publishes it decoded there.
+        auto publish = [&](const Work& w, bool valid) -> bool {
+          if (!mbar_wait<PAIR>(bar_s(SEMPTY + slot), sphase ^ 1u, lim, abort_flag)) return false;
+          const uint32_t a = ring_s(slot);
+          const uint32_t prob = static_cast<uint32_t>(valid ? w.prob : -1);
+          auto put = [&](uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t v) {
+            st_shared_v4(at, x, y, z, v);
+            if constexpr (PAIR) st_shared_cluster_v4(peer(at), x, y, z, v);
+          };
+          put(a, prob, w.tm, w.tn, w.kb_end);
+          put(a + 16, w.expert, w.row0, w.row_end, 0);
+          if constexpr (PAIR) mbar_arrive_cluster(peer(bar_s(SFULL + slot)));
+          mbar_arrive(bar_s(SFULL + slot));
+          if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
+          return true;
+        };
+        const uint32_t full_lead = leader ? 0u : lead(bar_s(FULL));
+        Work w{};
+        bool valid = unit < total_units;
+        if (leader && !publish_nothing) {
+          if (valid) w = unit_work<false, C::TILE_M>(p, unit_key<false>(p, unit));
+          ok = publish(w, valid);
+        }
+        while (ok && !publish_nothing) {
+          if (!leader) {
+            if (!mbar_wait<PAIR>(bar_s(SFULL + slot), sphase, lim, abort_flag)) {
+              ok = false;
+              break;
+            }
+            w = ring_get(ring_s(slot));
+            valid = w.prob >= 0;
+            mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
+            if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
+          }
+          if (!valid) break;
+          const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
+          if constexpr (EpiTraits<EPI>::DACT) {
+            if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
+            if (L.i1) tma_prefetch_l2_2d(L.i1, L.icol, L.m0);
+          }
+          const int next = leader ? ncl + atomicAdd(p.counter, 1) : 0;
+          const bool next_valid = next < total_units;
+          UnitKey key{};
+          Work nw{};
+          int step = 0;  // of the next unit: 1 its key is being loaded, 2 published
+          auto advance = [&]() -> bool {
+            if (++step == 1) {
+              if (next_valid) key = unit_key<false>(p, next);
+              return true;
+            }
+            if (next_valid) nw = unit_work<false, C::TILE_M>(p, key);
+            return publish(nw, next_valid);
+          };
+          const int mid = w.kb_end / 2;
+          for (int kb = 0; kb < w.kb_end; ++kb) {
+            if (!mbar_wait<PAIR>(bar_s(EMPTY + stage), phase ^ 1u, lim, abort_flag)) {
+              ok = false;
+              break;
+            }
+            uint32_t full = full_lead + 8u * stage;
+            if (leader) {
+              full = bar_s(FULL + stage);
+              mbar_expect_tx(full, tx_bytes);
+            }
+            const int seg = kb < L.kb0 ? 0 : 1;
+            const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
+            const uint32_t sA = base_s + stage * C::STAGE;
+            load_stage<EPI, A_MN, B_MN, CG, GRP>(L, seg, kc, sA, sA + C::A_BYTES, full,
+                                                 pol_of(L.l2a), pol_of(L.l2b));
+            ++issued;
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+            if (leader && (kb == mid || kb == mid + 1) && !advance()) {
+              ok = false;
+              break;
+            }
+          }
+          while (ok && leader && step < 2) ok = advance();
+          if (leader) {
+            w = nw;
+            valid = next_valid;
+          }
+        }
+      }
+      while (!RING && ok && !publish_nothing) {
         if (leader) {
           // Publishes unit v (-1: no more work) to the pair's rings.  A unit
           // is published while the previous one is still being loaded (at
@@ -1421,7 +1540,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             }
           }
           if (unit >= total_units) break;
-          const Work w = decode<GRP, A_MN, C::TILE_M>(p, unit);
+          const Work w = decode<GRP_SUM, C::TILE_M>(p, unit);
           // The next unit, fetched now and needed when it is published.  A
           // down unit of the fused forward (K = I, several times a gate/up
           // unit's length) fetches it only when it publishes it, half-way
@@ -1487,7 +1606,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           if (v < 0) break;
-          const Work w = decode<GRP, A_MN, C::TILE_M>(p, v);
+          const Work w = decode<GRP_SUM, C::TILE_M>(p, v);
           const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
           if constexpr (EpiTraits<EPI>::DACT) {
             if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
@@ -1554,11 +1673,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
       bool any = false;
       while (ok) {
         if (!mbar_wait<PAIR>(bar_s(SFULL + slot), sphase, lim, abort_flag)) { ok = false; break; }
-        const int unit = sched[slot];
+        Work w;
+        int unit;
+        if constexpr (RING) {
+          w = ring_get(ring_s(slot));
+          unit = w.prob;
+        } else {
+          unit = sched[slot];
+        }
         mbar_arrive(bar_s(SEMPTY + slot));
         if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
         if (unit < 0) break;
-        const Work w = decode<GRP, A_MN, C::TILE_M>(p, unit);
+        if constexpr (!RING) w = decode<GRP_SUM, C::TILE_M>(p, unit);
         // the fused recompute's second K segment goes to the other accumulator
         const int kswitch = is_recomp(EPI) ? p.prob[w.prob].kb0 : -1;
         if (!mbar_wait<PAIR>(bar_s(TEMPTY + acc), aphase ^ 1u, lim, abort_flag)) { ok = false; break; }
@@ -1667,7 +1793,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         record_timeout(p, abort_flag);
         break;
       }
-      const int unit = sched[slot];
+      Work w;
+      int unit;
+      if constexpr (RING) {
+        w = ring_get(ring_s(slot));
+        unit = w.prob;
+      } else {
+        unit = sched[slot];
+      }
       __syncwarp();
       if (lane == 0) {
         if (leader) mbar_arrive(bar_s(SEMPTY + slot));
@@ -1675,7 +1808,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
       }
       if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
       if (unit < 0) break;
-      const Work w = decode<GRP, A_MN, C::TILE_M>(p, unit);
+      if constexpr (!RING) w = decode<GRP_SUM, C::TILE_M>(p, unit);
       const int pi = w.prob;
       EpiUnit P = epi_unit<EPI>(p, p.prob[pi],
                                       pi == 0 ? f8_deq[0] : pi == 1 ? f8_deq[1] : f8_deq[2],
