@@ -435,9 +435,6 @@ def mlp_debug_set_flags(flags: int) -> None:
     _check(lib().mlp_debug_set_flags(int(flags)), "mlp_debug_set_flags")
 
 
-from .autograd import mlp_block_func, mlp_func  # noqa: E402  (differentiable forms)
-
-__all__ += ["mlp_func", "mlp_block_func"]
 
 from . import experts, linear_op  # noqa: E402  (mixture of experts; linear layer)
 from .experts import (Moe, alloc_moe_plan, alloc_moe_workspace, mlp_moe_combine,  # noqa: E402
@@ -455,3 +452,7 @@ from .linear_op import (LINEAR_ACTS, Linear, alloc_linear_workspace, linear,  # 
 
 __all__ += ["LINEAR_ACTS", "Linear", "linear", "alloc_linear_workspace", "mlp_linear_fwd",
             "mlp_linear_bwd", "mlp_linear_workspace_size"]
+
+from .autograd import linear_func, mlp_block_func, mlp_func, moe_func  # noqa: E402  (differentiable)
+
+__all__ += ["mlp_func", "mlp_block_func", "linear_func", "moe_func"]

@@ -22,6 +22,9 @@ differentiated once; recompute=True keeps only x and may be run again.
 mlp_block_func is modded-nanogpt gpt.py's "process mlp" step, y =
 resid_lambda x + post_lambda MLP(norm(x)), as one mlp_block_fwd and one
 mlp_block_bwd call (saved preacts and the per-token 1/rms).
+
+linear_func is the linear layer with bias, activation and residual, and
+moe_func the mixture-of-experts MLP (at the end of this file).
 """
 from __future__ import annotations
 
@@ -29,6 +32,10 @@ import torch
 
 from . import (GATED_ACTS, block, mlp_block_bwd, mlp_block_fwd, mlp_bwd, mlp_bwd_recompute,
                mlp_fwd, problem)
+from .experts import (alloc_moe_plan, mlp_moe_combine, mlp_moe_combine_bwd, mlp_moe_dispatch,
+                      mlp_moe_dispatch_bwd, mlp_moe_experts_bwd, mlp_moe_experts_fwd,
+                      mlp_moe_fwd_infer, mlp_moe_rows, mlp_moe_sort, moe)
+from .linear_op import linear, mlp_linear_bwd, mlp_linear_fwd
 
 
 def _check_operand(t, name):
@@ -199,3 +206,155 @@ def mlp_block_func(x, Wg, Wu, Wd, activation="swiglu", gate_mult=1.0, down_mult=
     return _MlpBlockFunction.apply(x, Wg, Wu, Wd, activation, gate_mult, down_mult,
                                    float(resid_lambda), float(post_lambda), float(eps),
                                    bool(fuse_grad_accum))
+
+
+def _grad_like(t, fuse, name):
+    """Where a weight's gradient goes: a fresh bf16 tensor, or its fp32 main_grad."""
+    if not fuse:
+        return torch.empty_like(t)
+    g = getattr(t, "main_grad", None)
+    if (g is None or g.dtype != torch.float32 or g.shape != t.shape or not g.is_contiguous()
+            or g.device != t.device):
+        raise ValueError(f"fuse_grad_accum: {name} needs a contiguous fp32 `main_grad` of its "
+                         "own shape")
+    return g
+
+
+class _LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, bias, residual, act, resid_scale, fuse_grad_accum):
+        for t, name in ((x, "x"), (W, "W")) + (((bias, "bias"),) if bias is not None else ()) + (
+                ((residual, "residual"),) if residual is not None else ()):
+            _check_operand(t, name)
+        N, K = W.shape
+        shape = x.shape
+        x2 = x.reshape(-1, K).contiguous()
+        M = x2.shape[0]
+        ctx.x_shape, ctx.fuse, ctx.scale = shape, fuse_grad_accum, resid_scale
+        ctx.has_residual = residual is not None
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        ctx.prob = linear(M, N, K, act, resid_scale)
+        pre = None
+        if M:
+            r2 = residual.reshape(M, N).contiguous() if residual is not None else None
+            if act != "none" and any(ctx.needs_input_grad[:3]):
+                pre = torch.empty_like(out)
+            mlp_linear_fwd(ctx.prob, x2, W, bias, r2, out, pre)
+        ctx.save_for_backward(x2, W, bias, pre)
+        return out.view(*shape[:-1], N)
+
+    @staticmethod
+    def backward(ctx, dout):
+        x2, W, bias, pre = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        M, N = x2.shape[0], W.shape[0]
+        d2 = dout.reshape(M, N)
+        if d2.dtype != torch.bfloat16:
+            d2 = d2.to(torch.bfloat16)
+        d2 = d2.contiguous()
+        dx = torch.empty_like(x2) if need[0] else None
+        dW = _grad_like(W, ctx.fuse, "W") if need[1] else None
+        db = _grad_like(bias, ctx.fuse, "bias") if bias is not None and need[2] else None
+        if M == 0:
+            if not ctx.fuse:
+                for g in (dW, db):
+                    if g is not None:
+                        g.zero_()
+        elif dx is not None or dW is not None or db is not None:
+            mlp_linear_bwd(ctx.prob, d2, x2, W, pre, dx, dW, db, fuse_grad_accum=ctx.fuse)
+        dr = None
+        if ctx.has_residual and need[3]:
+            dr = dout if ctx.scale == 1.0 else dout * ctx.scale
+        return (dx.view(ctx.x_shape) if dx is not None else None, None if ctx.fuse else dW,
+                None if ctx.fuse else db, dr, None, None, None)
+
+
+def linear_func(x, W, bias=None, residual=None, activation="none", resid_scale=1.0,
+                fuse_grad_accum=False):
+    """out = act(x W^T + bias) + resid_scale * residual over the last dimension of x,
+    differentiable with respect to x, W, bias and residual (one mlp_linear_fwd and one
+    mlp_linear_bwd call)."""
+    return _LinearFunction.apply(x, W, bias, residual, activation, float(resid_scale),
+                                 bool(fuse_grad_accum))
+
+
+class _MoeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weights, Wg, Wu, Wd, residual, ids, prob, fuse_grad_accum):
+        T, H = x.shape
+        new = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=x.device)  # noqa: E731
+        rows = mlp_moe_rows(prob)
+        plan = alloc_moe_plan(prob, x.device)
+        xs, y, G = new(rows, H), new(rows, H), new(rows, prob.I)
+        U = new(rows, prob.I) if Wu is not None else None
+        out = new(T, H)
+        mlp_moe_sort(prob, ids, plan)
+        mlp_moe_dispatch(prob, plan, x, xs)
+        mlp_moe_experts_fwd(prob, plan, xs, Wg, Wu, Wd, y, G, U)
+        mlp_moe_combine(prob, plan, y, weights, residual, out)
+        ctx.prob, ctx.fuse, ctx.spent = prob, fuse_grad_accum, False
+        keep_y = y if ctx.needs_input_grad[1] else None  # only the weights' gradient reads it
+        ctx.save_for_backward(plan, xs, weights, Wg, Wu, Wd, G, U, keep_y)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        plan, xs, weights, Wg, Wu, Wd, G, U, y = ctx.saved_tensors
+        need, p = ctx.needs_input_grad, ctx.prob
+        experts = need[0] or any(need[2:5])
+        if ctx.spent and experts:
+            raise RuntimeError("moe_func: the saved preacts were overwritten by the first backward")
+        d = dout if dout.dtype == torch.bfloat16 else dout.to(torch.bfloat16)
+        d = d.contiguous()
+        dy = torch.empty_like(xs) if experts else None
+        dw = torch.empty_like(weights) if need[1] else None
+        mlp_moe_combine_bwd(p, plan, d, y, weights, dy, dw)
+        dx = dxs = None
+        dW = [None, None, None]
+        if experts:
+            ctx.spent = True
+            for i, (w, name) in enumerate(((Wg, "Wg"), (Wu, "Wu"), (Wd, "Wd"))):
+                if w is not None and need[2 + i]:
+                    dW[i] = _grad_like(w, ctx.fuse, name)
+            if need[0]:
+                dxs = torch.empty_like(xs)
+            mlp_moe_experts_bwd(p, plan, dy, xs, Wg, Wu, Wd, G, U, dxs, *dW,
+                                fuse_grad_accum=ctx.fuse)
+            if need[0]:
+                dx = torch.empty((p.T, p.H), dtype=torch.bfloat16, device=xs.device)
+                mlp_moe_dispatch_bwd(p, plan, dxs, dx)
+        dW = [None if ctx.fuse else g for g in dW]
+        return (dx, dw, *dW, dout if need[5] else None, None, None, None)
+
+
+def moe_func(x, ids, weights, Wg, Wu, Wd, activation="swiglu", residual=None, gate_mult=1.0,
+             down_mult=1.0, fuse_grad_accum=False):
+    """The mixture-of-experts MLP, out[t] = residual[t] + sum_j weights[t, j]
+    MLP_{ids[t, j]}(x[t]), over the last dimension of x: ids int32 and weights (fp32 or
+    bf16) [..., top_k], Wg and Wu [E, I, H] (Wu None when non-gated), Wd [E, H, I].  A slot
+    whose id is outside [0, E) is dropped.  Differentiable with respect to x, weights, the
+    experts' weights and residual; without gradients to take it is one mlp_moe_fwd_infer
+    call.  The graph can be differentiated once (the saved preacts become their
+    gradients)."""
+    gated = _check_weights(activation, Wg, Wu, Wd)
+    _check_operand(x, "x")
+    E, inner, H = Wg.shape
+    shape, k = x.shape, ids.shape[-1]
+    x2 = x.reshape(-1, H).contiguous()
+    T = x2.shape[0]
+    r2 = None
+    if residual is not None:
+        _check_operand(residual, "residual")
+        r2 = residual.reshape(T, H).contiguous()
+    if T == 0:
+        parts = [t for t in (x2, weights, Wg, Wu if gated else None, Wd, r2) if t is not None]
+        return x2.new_zeros((0, H)).view(shape) + 0 * sum(t.sum() for t in parts)
+    i2, w2 = ids.reshape(T, k).contiguous(), weights.reshape(T, k).contiguous()
+    prob = moe(T, E, k, H, inner, activation, gate_mult, down_mult, weights_dtype=w2.dtype)
+    args = [t for t in (x2, w2, Wg, Wu, Wd, r2) if t is not None]
+    if torch.is_grad_enabled() and any(t.requires_grad for t in args):
+        out = _MoeFunction.apply(x2, w2, Wg, Wu, Wd, r2, i2, prob, bool(fuse_grad_accum))
+    else:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        mlp_moe_fwd_infer(prob, x2, i2, w2, Wg, Wu, Wd, r2, out)
+    return out.view(shape)
