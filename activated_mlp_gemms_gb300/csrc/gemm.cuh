@@ -190,7 +190,7 @@ struct EpiTraits {
                                                                                   : 1;
   // bytes of a staged 32 x 32 output box: fp32 4096, bf16 2048 (the 8-bit
   // epilogues stage their own boxes, below)
-  static constexpr int OUT_BYTES = (EPI == EPI_ACCUM_F32) ? 4096 : 2048;
+  static constexpr int OUT_BYTES = (EPI == EPI_ACCUM_F32 || EPI == EPI_STORE_F32) ? 4096 : 2048;
   // the epilogue reads saved preacts (in0 / in1), fetched ahead of the accumulator
   static constexpr bool DACT = (EPI == EPI_DGATED || EPI == EPI_DACT || EPI == EPI_DGRAD_F8);
   // staged boxes per warp: at most two (a third output reuses the first box
@@ -1094,7 +1094,7 @@ __device__ __forceinline__ void epi_plain(const Params& p, const EpiUnit& P, con
       flush_chunk<1, 2048, false, STACK>(p, P, e, col);
     } else {
       stage_f32(e.stg, e.lane, d);
-      flush_chunk<1, 4096, true, STACK>(p, P, e, col);
+      flush_chunk<1, 4096, EPI == EPI_ACCUM_F32, STACK>(p, P, e, col);
     }
   }
 }

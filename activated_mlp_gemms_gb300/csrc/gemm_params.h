@@ -64,7 +64,8 @@ enum Epi : int {
   // The linear layer: z = acc + bias (in1, bf16 [N]; may be null), D = act(z) +
   // alpha * residual (in0, bf16, row pitch ld; may be null) -> map 0, and
   // bf16(z) -> map 1 if requested
-  EPI_LINEAR = 12
+  EPI_LINEAR = 12,
+  EPI_STORE_F32 = 13  // D = acc (fp32; the experts' down projection of the inference layer)
 };
 
 __host__ __device__ constexpr bool is_f8(int epi) {

@@ -283,16 +283,19 @@ struct Gemm {
       ok = false;
     return nmaps++;
   }
-  // bf16 output of P over the sorted rows: boxes of 32 rows, and of 16 for the
-  // last rows of an expert; 32 columns (64-byte swizzle), or 64 (wide, the
-  // plain store's; 128-byte swizzle)
-  void output_rows(Prob& P, int i, void* ptr, int rows, int cols, bool wide = false) {
+  // Output of P over the sorted rows: boxes of 32 rows, and of 16 for the last
+  // rows of an expert.  bf16 boxes have 32 columns (64-byte swizzle), or 64
+  // (ROWS_WIDE, the plain store's; 128-byte swizzle), fp32 boxes 32.
+  enum RowsKind { ROWS_BF16, ROWS_WIDE, ROWS_F32 };
+  void output_rows(Prob& P, int i, void* ptr, int rows, int cols, RowsKind kind = ROWS_BF16) {
     P.mapO[i] = P.mapO16[i] = -1;
     if (!ptr) return;
-    const CUtensorMapSwizzle swz = wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     for (int box : {32, 16}) {
       if (nmaps >= MAX_MAPS) { ok = false; return; }
-      if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, wide ? 64 : 32, box, 0, swz)) ok = false;
+      if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, kind == ROWS_WIDE ? 64 : 32, box,
+                    kind == ROWS_F32,
+                    kind == ROWS_BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+        ok = false;
       (box == 32 ? P.mapO : P.mapO16)[i] = nmaps++;
     }
   }

@@ -10,7 +10,8 @@
 //   2. the counts become exclusive prefixes over the CTA's warps; the CTAs
 //      read each other's totals through distributed shared memory,
 //   3. every CTA scans the padded totals over the experts,
-//   4. the warps walk their slots again and write pos and src.
+//   4. the warps walk their slots again and write pos and src (a slot's rank
+//      within its warp, known from 1, waits in pos).
 // Bound by the latency of its phases (a few cluster barriers and two passes
 // over ids), not by its bytes: 12 bytes a slot.
 #include "gemm_params.h"
@@ -136,7 +137,10 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
   const int lo = static_cast<int>(begin < n ? begin : n);
   const int hi = static_cast<int>(begin + per_warp < n ? begin + per_warp : n);
   int* mine = wcnt + warp * E;
-  // eight groups of 32 ids are loaded at a time
+  int* pos = plan + L.pos;
+  int* src = plan + L.src;
+  // SORT_AHEAD groups of 32 ids are loaded at a time; pos holds each slot's
+  // rank within the warp's sub-chunk until the prefixes are known
   for (int i0 = lo; i0 < hi; i0 += 32 * SORT_AHEAD) {
     int id[SORT_AHEAD];
 #pragma unroll
@@ -147,9 +151,13 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
 #pragma unroll
     for (int j = 0; j < SORT_AHEAD; ++j) {
       if (i0 + 32 * j >= hi) break;
+      const int i = i0 + 32 * j + lane;
       const int e = (id[j] >= 0 && id[j] < E) ? id[j] : -1;
       const unsigned same = same_key(e < 0 ? E : e, bits);
-      if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+      const int at = e >= 0 ? mine[e] : 0;
+      __syncwarp();
+      if (e >= 0 && lane == __ffs(same) - 1) mine[e] = at + __popc(same);
+      if (i < hi) pos[i] = at + __popc(same & ((1u << lane) - 1u));
       __syncwarp();
     }
   }
@@ -170,10 +178,13 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
   if (tid < E) {
     if (ncta > 1) {
       const uint32_t a = smem_u32(ctot + tid);
-      for (int c = 0; c < ncta; ++c) {
-        const int v = ld_cluster_int(mapa_shared(a, c));
-        if (c < cta) before += v;
-        total += v;
+      int v[SORT_CLUSTER];
+#pragma unroll
+      for (int c = 0; c < SORT_CLUSTER; ++c) v[c] = ld_cluster_int(mapa_shared(a, c));
+#pragma unroll
+      for (int c = 0; c < SORT_CLUSTER; ++c) {
+        if (c < cta) before += v[c];
+        total += v[c];
       }
     } else {
       total = ctot[tid];
@@ -189,32 +200,22 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
   if (tid == 0) off[E] = used;
   __syncthreads();
 
-  int* pos = plan + L.pos;
-  int* src = plan + L.src;
   for (int i0 = lo; i0 < hi; i0 += 32 * SORT_AHEAD) {
-    int id[SORT_AHEAD];
+    int id[SORT_AHEAD], rank[SORT_AHEAD];
 #pragma unroll
     for (int j = 0; j < SORT_AHEAD; ++j) {
       const int i = i0 + 32 * j + lane;
       id[j] = i < hi ? ids[i] : -1;
+      rank[j] = i < hi ? pos[i] : 0;
     }
 #pragma unroll
     for (int j = 0; j < SORT_AHEAD; ++j) {
-      if (i0 + 32 * j >= hi) break;
       const int i = i0 + 32 * j + lane;
-      const int e = (id[j] >= 0 && id[j] < E) ? id[j] : -1;
-      const unsigned same = same_key(e < 0 ? E : e, bits);
-      const int at = e >= 0 ? mine[e] : 0;
-      __syncwarp();
-      if (e >= 0) {
-        const int row = base[e] + at + __popc(same & ((1u << lane) - 1u));
-        pos[i] = row;
-        src[row] = i;
-        if (lane == __ffs(same) - 1) mine[e] = at + __popc(same);
-      } else if (i < hi) {
-        pos[i] = -1;
-      }
-      __syncwarp();
+      if (i >= hi) continue;
+      const bool used = id[j] >= 0 && id[j] < E;
+      const int row = used ? base[id[j]] + mine[id[j]] + rank[j] : -1;
+      pos[i] = row;
+      if (used) src[row] = i;
     }
   }
   // the padding rows, the tables and the rows past the end
@@ -227,12 +228,11 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
   for (long long r = used + static_cast<long long>(cta) * SORT_THREADS + tid; r < L.rows;
        r += static_cast<long long>(ncta) * SORT_THREADS)
     src[r] = -1;
-  if (cta == ncta - 1) {
-    write_tiles(off, E, 128, first, tmp, plan + L.ntiles,
-                reinterpret_cast<MoeTile*>(plan + L.tiles[0]));
-    write_tiles(off, E, 256, first, tmp, plan + L.ntiles + 1,
-                reinterpret_cast<MoeTile*>(plan + L.tiles[1]));
-  }
+  // the two tile lists, by a CTA each where there are several
+  for (int h = 0; h < 2; ++h)
+    if (cta == (ncta > 1 ? ncta - 1 - h : 0))
+      write_tiles(off, E, h == 0 ? 128 : 256, first, tmp, plan + L.ntiles + h,
+                  reinterpret_cast<MoeTile*>(plan + L.tiles[h]));
   if (ncta > 1) cluster_sync();  // no CTA leaves while another reads its totals
 }
 

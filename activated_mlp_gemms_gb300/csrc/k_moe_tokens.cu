@@ -85,9 +85,33 @@ __device__ __forceinline__ void fma8(float (&a)[8], float w, const uint4& v) {
   }
 }
 
-template <bool HAS_W, bool W_BF16, int CH>
+// Eight values of a row of y, bf16 or fp32.
+template <bool Y32>
+struct Piece {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* y, size_t at) {
+    v = ld_global_v4(static_cast<const __nv_bfloat16*>(y) + at);
+  }
+  __device__ __forceinline__ void add(float (&a)[8], float w) const { fma8(a, w, v); }
+};
+template <>
+struct Piece<true> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const void* y, size_t at) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(y) + at);
+    v[0] = p[0];
+    v[1] = p[1];
+  }
+  __device__ __forceinline__ void add(float (&a)[8], float w) const {
+    const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmaf(w, f[i], a[i]);
+  }
+};
+
+template <bool HAS_W, bool W_BF16, int CH, bool Y32>
 __global__ void __launch_bounds__(TOK_THREADS)
-    k_moe_combine(const __nv_bfloat16* __restrict__ y, const int* __restrict__ pos,
+    k_moe_combine(const void* __restrict__ y, const int* __restrict__ pos,
                   const void* __restrict__ weights, const __nv_bfloat16* residual,
                   __nv_bfloat16* out, int top_k, int H, int segs) {
   pdl_wait();
@@ -104,7 +128,7 @@ __global__ void __launch_bounds__(TOK_THREADS)
   // SL slots' rows in flight at a time
   constexpr int SL = CH == 1 ? 4 : 2;
   for (int j0 = 0; j0 < top_k; j0 += SL) {
-    uint4 v[SL][CH];
+    Piece<Y32> v[SL][CH];
     float w[SL];
     int r[SL];
 #pragma unroll
@@ -116,7 +140,7 @@ __global__ void __launch_bounds__(TOK_THREADS)
 #pragma unroll
       for (int i = 0; i < CH; ++i)
         if (c0 + i * TOK_COLS < H)
-          v[j][i] = ld_global_v4(y + static_cast<size_t>(r[j]) * H + c0 + i * TOK_COLS);
+          v[j][i].load(y, static_cast<size_t>(r[j]) * H + c0 + i * TOK_COLS);
       if constexpr (HAS_W) w[j] = ld_weight<W_BF16>(weights, s0 + j0 + j);
     }
 #pragma unroll
@@ -124,7 +148,7 @@ __global__ void __launch_bounds__(TOK_THREADS)
       if (r[j] < 0) continue;
 #pragma unroll
       for (int i = 0; i < CH; ++i)
-        if (c0 + i * TOK_COLS < H) fma8(a[i], w[j], v[j][i]);
+        if (c0 + i * TOK_COLS < H) v[j][i].add(a[i], w[j]);
     }
   }
 #pragma unroll
@@ -290,21 +314,22 @@ cudaError_t launch_moe_dispatch(const void* x, const int* plan, const MoePlan& L
                     L.rows, top_k, H, segs, tokens, zero_rows(L));
 }
 
-cudaError_t launch_moe_combine(const void* y, const int* plan, const MoePlan& L, int T, int top_k,
+cudaError_t launch_moe_combine(const void* y, bool y32, const int* plan, const MoePlan& L, int T, int top_k,
                                int H, const void* weights, bool w_bf16, const void* residual,
                                void* out, cudaStream_t stream, bool pdl) {
   const int ch = pieces(T, top_k, H), segs = (H + ch * TOK_COLS - 1) / (ch * TOK_COLS);
   auto pick = [&](auto c) {
     constexpr int CH = decltype(c)::value;
-    return weights == nullptr ? k_moe_combine<false, false, CH>
-           : w_bf16           ? k_moe_combine<true, true, CH>
-                              : k_moe_combine<true, false, CH>;
+    if (y32) return w_bf16 ? k_moe_combine<true, true, CH, true> : k_moe_combine<true, false, CH, true>;
+    return weights == nullptr ? k_moe_combine<false, false, CH, false>
+           : w_bf16           ? k_moe_combine<true, true, CH, false>
+                              : k_moe_combine<true, false, CH, false>;
   };
   auto kern = ch == 1   ? pick(std::integral_constant<int, 1>{})
               : ch == 2 ? pick(std::integral_constant<int, 2>{})
                         : pick(std::integral_constant<int, 4>{});
-  return launch_tok(kern, static_cast<long long>(T) * segs, stream, pdl, static_cast<const bf*>(y),
-                    plan + L.pos, weights, static_cast<const bf*>(residual), static_cast<bf*>(out),
+  if (y32 && weights == nullptr) return cudaErrorInvalidValue;
+  return launch_tok(kern, static_cast<long long>(T) * segs, stream, pdl, y, plan + L.pos, weights, static_cast<const bf*>(residual), static_cast<bf*>(out),
                     top_k, H, segs);
 }
 

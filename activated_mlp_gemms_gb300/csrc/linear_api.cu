@@ -50,7 +50,9 @@ Layout layout(const mlp_linear_t* p, bool backward) {
   const size_t mn = (size_t)p->M * p->N, mk = (size_t)p->M * p->K;
   size_t at = CTRL_BYTES;
   // (dx is left whole from 33 tiles on: its last wave runs beside dW)
-  L.split = backward ? bf16_split(p->M, p->K, p->N, false) : bf16_split(p->M, p->N, p->K, true);
+  L.split = backward                        ? bf16_split(p->M, p->K, p->N, false)
+            : p->M <= LINEAR_STREAM_MAX_M ? 1
+                                          : bf16_split(p->M, p->N, p->K, true);
   L.part = at;
   if (L.split > 1) at += round256((backward ? mk : mn) * 4);
   L.dz = at;

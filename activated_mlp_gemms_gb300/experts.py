@@ -73,7 +73,10 @@ def _shaped(t, shape, name, dtype=torch.bfloat16):
     """The tensor's address (None stays None) once its type, device and shape are right."""
     if t is None:
         return None
-    p = _ptr(t, dtype, name)
+    if (t.__class__ is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
+    p = _ptr(t, dtype, name)  # says what is wrong (or passes a subclass)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return p

@@ -49,7 +49,10 @@ def _dense(t, shape, name, dtype=torch.bfloat16):
     """The tensor's address (None stays None) once its type, device and shape are right."""
     if t is None:
         return None
-    p = _ptr(t, dtype, name)
+    if (t.__class__ is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
+    p = _ptr(t, dtype, name)  # says what is wrong (or passes a subclass)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return p
@@ -59,9 +62,7 @@ def _pitched(t, shape, name):
     """(address, row pitch or 0 when dense) of a bf16 matrix with unit column stride."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.is_contiguous():
         return _dense(t, shape, name), 0
     if not t.is_cuda or t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
@@ -97,12 +98,26 @@ def alloc_linear_workspace(p: Linear, backward=False, device=None) -> torch.Tens
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+STREAM_MAX_M = 8  # rows up to which the forward streams its weights (mlp_linear.h)
+_status = {}  # device -> the status word that streamed forwards share
+
+
 def _ws(ws, p, backward, device):
     if ws is None:
+        if not backward and p.M <= STREAM_MAX_M:
+            # A streamed forward uses the status word alone, waits on nothing and
+            # writes 0 there: all of them can share one, on any stream.
+            ws = _status.get(device)
+            if ws is not None:
+                return ws
         n = _ws_size(p.M, p.N, p.K, p.act, backward)
         if n == 0:  # (the call itself says why)
             n = 256
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if (not backward and p.M <= STREAM_MAX_M and n >= 1024
+                and not torch.cuda.is_current_stream_capturing()):  # (not a graph's own memory)
+            _status[device] = ws
+        return ws
     if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return ws
