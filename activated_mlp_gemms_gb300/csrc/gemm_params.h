@@ -158,6 +158,7 @@ struct Params {  // 64-byte aligned through CUtensorMap
   const int* ntiles;
   const int* offsets;
   int rows;               // rows of the sorted layout's buffers
+  int one_wave;           // EPI_LINEAR: no cluster has a second unit; the kernel clears *status
 };
 
 // Host-side launcher and co-residency query, explicitly instantiated in the

@@ -69,8 +69,15 @@ int check_ws(const Layout& L, const void* ws, size_t ws_bytes) {
   return ws_bytes < L.total ? MLP_ERR_WORKSPACE_TOO_SMALL : MLP_OK;
 }
 
+// The GEMM with the layer's epilogue.  When every unit has a cluster of its own
+// nothing is claimed from the control block's counter, and the kernel clears
+// the status word itself: no memset before it (22.7 -> 20 us for 777 x 4864 x
+// 2048).
 template <int ACT>
-int run_linear(Gemm& g, Call& c) {
+int run_linear(Gemm& g, Call& c, void* ws, void* stream) {
+  const int groups = g.cg == 2 ? groups_cached<EPI_LINEAR, false, false, 2, ACT>() : num_sms();
+  g.p.one_wave = g.p.total_units <= groups;
+  if (!g.p.one_wave) MLP_TRY(begin_call(c, ws, stream));
   return run_act<EPI_LINEAR, false, false, ACT>(g, c, MLP_KERNEL_LINEAR);
 }
 
@@ -99,7 +106,7 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   const int ldx = p->ldx ? p->ldx : K, ldr = p->ldr ? p->ldr : N, ldo = p->ldo ? p->ldo : N;
   const bool streamed = M <= LINEAR_STREAM_MAX_M;
   Call c;
-  MLP_TRY(begin_call(c, ws, stream, !streamed));
+  MLP_TRY(begin_call(c, ws, stream, L.split > 1));
   if (streamed) {
     const bool pdl = c.pdl();
     return traced(MLP_KERNEL_LINEAR, c.stream, [&] {
@@ -141,12 +148,12 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   P.ld = ldr;
   P.alpha = p->resid_scale;
   switch (act) {
-    case ACT_RELU: return run_linear<ACT_RELU>(g, c);
-    case ACT_RELU_SQ: return run_linear<ACT_RELU_SQ>(g, c);
-    case ACT_GELU_HW: return run_linear<ACT_GELU_HW>(g, c);
-    case ACT_SILU: return run_linear<ACT_SILU>(g, c);
-    case ACT_SIGMOID: return run_linear<ACT_SIGMOID>(g, c);
-    default: return run_linear<ACT_NONE>(g, c);
+    case ACT_RELU: return run_linear<ACT_RELU>(g, c, ws, stream);
+    case ACT_RELU_SQ: return run_linear<ACT_RELU_SQ>(g, c, ws, stream);
+    case ACT_GELU_HW: return run_linear<ACT_GELU_HW>(g, c, ws, stream);
+    case ACT_SILU: return run_linear<ACT_SILU>(g, c, ws, stream);
+    case ACT_SIGMOID: return run_linear<ACT_SIGMOID>(g, c, ws, stream);
+    default: return run_linear<ACT_NONE>(g, c, ws, stream);
   }
 }
 
