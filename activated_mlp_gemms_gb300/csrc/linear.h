@@ -1,8 +1,11 @@
 // linear.h -- launchers of the linear layer's own kernels (the GEMM instances
 // with its epilogue are launch_gemm<EPI_LINEAR, ...>).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
+
+#include "gemm_params.h"
 
 namespace mlpk {
 
@@ -13,6 +16,18 @@ cudaError_t launch_linear_stream(const void* x, int ldx, const void* W, const vo
                                  const void* resid, int ldr, float rs, void* out, int ldo,
                                  void* pre, int M, int N, int K, int act, cudaStream_t stream,
                                  bool pdl, int* status);
+
+// The same for up to LINEAR_SKINNY_MAX_M rows, on the tensor cores with the
+// operands' places changed (k_linear_skinny.cu).  map_w: W [N, K] in boxes
+// {64, 128}; map_x: x [M, K] in boxes {64, linear_skinny_rows(M)}.  Clears
+// *status; no_work: the bounded waits run out (testing).
+constexpr int LINEAR_SKINNY_MAX_M = 256;
+int linear_skinny_rows(int M);
+cudaError_t launch_linear_skinny(const CUtensorMap& map_w, const CUtensorMap& map_x,
+                                 const void* bias, const void* resid, int ldr, float rs, void* out,
+                                 int ldo, void* pre, int M, int N, int K, int act, int no_work,
+                                 int* status, unsigned long long limit_ns, cudaStream_t stream,
+                                 bool pdl);
 
 // The same epilogue on split-K sums acc fp32 [M, N].
 cudaError_t launch_linear_finish(const float* acc, const void* bias, const void* resid, int ldr,

@@ -40,6 +40,14 @@ int linear_act(int act) {
   }
 }
 
+// Whether the forward runs as the skinny kernel (unless a tile policy asks for
+// tiles).
+constexpr int LINEAR_SKINNY_AUTO_M = 256;
+bool skinny(const mlp_linear_t* p) {
+  const int pol = g_tile_policy.load();
+  return (pol == 0 || pol == 3) && p->M <= LINEAR_SKINNY_AUTO_M;
+}
+
 // The workspace after the control block.
 struct Layout {
   int split;                      // split-K factor of the forward's GEMM, or of dx
@@ -106,12 +114,25 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   const int ldx = p->ldx ? p->ldx : K, ldr = p->ldr ? p->ldr : N, ldo = p->ldo ? p->ldo : N;
   const bool streamed = M <= LINEAR_STREAM_MAX_M;
   Call c;
-  MLP_TRY(begin_call(c, ws, stream, L.split > 1));
+  const bool tiles = !streamed && !skinny(p);
+  MLP_TRY(begin_call(c, ws, stream, tiles && L.split > 1));
   if (streamed) {
     const bool pdl = c.pdl();
     return traced(MLP_KERNEL_LINEAR, c.stream, [&] {
       return launch_linear_stream(x, ldx, W, bias, residual, ldr, p->resid_scale, out, ldo,
                                   pre_save, M, N, K, act, c.stream, pdl, c.status);
+    });
+  }
+  if (skinny(p)) {
+    CUtensorMap map_w, map_x;
+    if (!make_map(&map_w, W, K, N, K, BK, 128) ||
+        !make_map(&map_x, x, K, M, ldx, BK, linear_skinny_rows(M)))
+      return MLP_ERR_CUDA;
+    const bool pdl = c.pdl();
+    return traced(MLP_KERNEL_LINEAR, c.stream, [&] {
+      return launch_linear_skinny(map_w, map_x, bias, residual, ldr, p->resid_scale, out, ldo,
+                                  pre_save, M, N, K, act, g_debug_flags.load() & MLP_DEBUG_NO_WORK,
+                                  c.status, wait_limit_ns(), c.stream, pdl);
     });
   }
   Gemm g(act, 1.f, c.counter(), c.status, pick_cg(M));

@@ -128,6 +128,19 @@ def test_against_formula(M, N, K, act):
     check(M, N, K, act, seed=M + N)
 
 
+@pytest.mark.parametrize("M,N,K", [(9, 8, 8), (16, 136, 4096), (31, 520, 72), (100, 4096, 2056),
+                                   (200, 264, 1160), (256, 128, 512)])
+@pytest.mark.parametrize("policy", [0, 1, 2])
+def test_few_rows_by_every_route(M, N, K, policy):
+    """The skinny kernel (policy 0: alone, and with clusters sharing K) and the tiles."""
+    m.mlp_set_tile_policy(policy)
+    try:
+        check(M, N, K, "gelu_tanh_approx", seed=M)
+        check(M, N, K, "none", residual=False, seed=M)
+    finally:
+        m.mlp_set_tile_policy(0)
+
+
 @pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("M,N,K", [(5, 264, 520), (48, 520, 2048), (300, 264, 520)])
 def test_optional_operands(M, N, K, bias, residual):

@@ -20,8 +20,9 @@ def no_work():
     m.mlp_set_wait_timeout_ms(0)
 
 
-def test_linear(no_work):
-    M, N, K = 300, 264, 520
+@pytest.mark.parametrize("M", [40, 300])  # the skinny kernel, and the tiles
+def test_linear(no_work, M):
+    N, K = 264, 520
     t = lambda *s: torch.ones(s, dtype=BF, device="cuda")  # noqa: E731
     p = m.linear(M, N, K)
     out = t(M, N)
