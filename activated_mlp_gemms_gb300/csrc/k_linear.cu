@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(32 * LS_MAX_WARPS)
   const bf* const tok[1] = {m < M ? x + static_cast<size_t>(m) * ldx : nullptr};
   float acc[1][1][1][4] = {};
   G buf[2];
+  pdl_wait();  // before the weights too: the kernel before may have written them
   if (warp < ngroups) buf[0].load_w(W, row0, N, K, warp * MD_KG, lane);
-  pdl_wait();
   if (status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   if (warp < ngroups) buf[0].load_t_rows(tok, K, warp * MD_KG, lane);
   if (warp + nwarps < ngroups) {

@@ -41,11 +41,14 @@ int linear_act(int act) {
 }
 
 // Whether the forward runs as the skinny kernel (unless a tile policy asks for
-// tiles).
-constexpr int LINEAR_SKINNY_AUTO_M = 256;
+// tiles): up to 192 rows always, up to 256 where N is at most 64 blocks of 128.
+// Measured (skinny / the better tiles): 192 x 14336 x 4096 28.8 / 30.6 us, 192 x
+// 2048 x 2048 11.6 / 16.5, 256 x 4096 x 4096 18.9 / 22.2, 256 x 14336 x 4096 33.2 /
+// 31.0.
 bool skinny(const mlp_linear_t* p) {
   const int pol = g_tile_policy.load();
-  return (pol == 0 || pol == 3) && p->M <= LINEAR_SKINNY_AUTO_M;
+  if (pol != 0 && pol != 3) return false;
+  return p->M <= 192 || (p->M <= LINEAR_SKINNY_MAX_M && p->N <= 64 * 128);
 }
 
 // The workspace after the control block.
@@ -86,6 +89,7 @@ int run_linear(Gemm& g, Call& c, void* ws, void* stream) {
   const int groups = g.cg == 2 ? groups_cached<EPI_LINEAR, false, false, 2, ACT>() : num_sms();
   g.p.one_wave = g.p.total_units <= groups;
   if (!g.p.one_wave) MLP_TRY(begin_call(c, ws, stream));
+  else c.launches = 1;  // (its kernel waits for the one before it)
   return run_act<EPI_LINEAR, false, false, ACT>(g, c, MLP_KERNEL_LINEAR);
 }
 
@@ -116,6 +120,10 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   Call c;
   const bool tiles = !streamed && !skinny(p);
   MLP_TRY(begin_call(c, ws, stream, tiles && L.split > 1));
+  // Without a memset before it, the call's first kernel may be launched while
+  // the kernel before it on the stream, whatever it is, still runs: each of
+  // these waits for that one's end before it touches memory.
+  if (!tiles) c.launches = 1;
   if (streamed) {
     const bool pdl = c.pdl();
     return traced(MLP_KERNEL_LINEAR, c.stream, [&] {

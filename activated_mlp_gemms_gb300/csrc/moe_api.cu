@@ -443,6 +443,7 @@ int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const v
   const bool stream_weights = decode_moe(p);
   Call c;
   MLP_TRY(begin_call(c, ws, stream, !stream_weights));
+  if (stream_weights) c.launches = 1;  // (its first kernel waits for the one before it)
   bool pdl = c.pdl();
   if (stream_weights) {
     MLP_TRY(traced(MLP_KERNEL_GATE_UP, c.stream, [&] {
