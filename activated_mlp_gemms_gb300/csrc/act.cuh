@@ -12,7 +12,11 @@
 // GB300 over z in [-20, 20]: at most 4e-6 from the fp64 sigmoid, 1e-5 for
 // silu and silu'; the epilogues' arithmetic is bound by instruction issue,
 // and this takes SwiGLU's fused epilogues from two special-function
-// instructions per element to one).  The GELU's tanh is CUDA's tanhf.
+// instructions per element to one).  The GELU's tanh is CUDA's tanhf, in the
+// dense MLP; the linear layer's and the experts' GELU (ACT_GELU_HW) takes the
+// hardware tanh (measured on a GB300: at most 7.6e-6 from the fp64 tanh over
+// [-100, 100], so 3.8e-6 |z| in the result; it takes 5 % off the linear
+// training step of 8192 x 4864 x 2048).
 #pragma once
 #include "gemm_params.h"
 

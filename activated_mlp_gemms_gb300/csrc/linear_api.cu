@@ -112,6 +112,8 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   MLP_TRY(opt(residual));
   MLP_TRY(need(out));
   MLP_TRY(opt(pre_save));
+  // other tiles still read x when a tile of out is stored
+  if (out == x || pre_save == x || pre_save == out) return MLP_ERR_INVALID_ARG;
   const Layout L = layout(p, false);
   MLP_TRY(check_ws(L, ws, ws_bytes));
   const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
@@ -200,6 +202,8 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
   MLP_TRY(opt(dx));
   MLP_TRY(opt(dW));
   MLP_TRY(opt(db));
+  // dW still reads dout and x while dx is stored
+  if (dx && (dx == dout || dx == x)) return MLP_ERR_INVALID_ARG;
   const Layout L = layout(p, true);
   MLP_TRY(check_ws(L, ws, ws_bytes));
   if (!dx && !dW && !db) return MLP_OK;

@@ -47,12 +47,15 @@ size_t mlp_linear_workspace_size(const mlp_linear_t* p, int backward);
 /* Forward.
  *   bias      bf16 [N] or NULL
  *   residual  bf16 [M,N] or NULL (pitch ldr); may be out itself
- *   out       bf16 [M,N] (pitch ldo)
+ *   out       bf16 [M,N] (pitch ldo); must not overlap x
  *   pre_save  bf16 [M,N] dense or NULL: z, which the backward of an
  *             activation needs (with MLP_LINEAR_NONE it is not)
- * With one to eight rows the weights are streamed on the warp-level MMA; more
- * rows run as tensor-core tiles, which split K when there are too few of
- * them to fill the GPU. */
+ * With one to eight rows the weights are streamed on the warp-level MMA; up to
+ * a few hundred run on the tensor cores with the weight rows as the MMA's M
+ * (K shared by a cluster of CTAs where N alone gives too few); more rows run
+ * as 128 x 256 or 256 x 256 output tiles.  A tile policy (mlp_set_tile_policy)
+ * of 1 or 2 keeps every size above eight rows on those tiles, which split K
+ * when there are too few of them to fill the GPU. */
 int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const void* bias,
                    const void* residual, void* out, void* pre_save, void* ws, size_t ws_bytes,
                    void* stream);
@@ -60,7 +63,7 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
 /* Backward:  dz = dout * act'(z),  dx = dz W,  dW = dz^T x,  db = sum_m dz.
  * (The residual's gradient is resid_scale * dout.)
  *   dout  bf16 [M,N] (pitch ldo)     pre  the forward's pre_save (NULL with MLP_LINEAR_NONE)
- *   dx    bf16 [M,K] dense           dW [N,K], db [N]: bf16, or with fuse_grad_accum = 1
+ *   dx    bf16 [M,K] dense, neither dout nor x;  dW [N,K], db [N]: bf16, or with fuse_grad_accum = 1
  *                                    fp32 that the gradient is added to
  * Each of dx, dW, db is NULL to skip; x and W may be NULL when what reads them
  * (dW, dx) is skipped.  dW may run on the library's second stream, as in

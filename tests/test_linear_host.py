@@ -30,11 +30,14 @@ def test_every_declared_symbol_is_exported(L):
         assert hasattr(L, n), n
 
 
-def fwd(L, p, x=FAKE, W=FAKE, bias=FAKE, resid=FAKE, out=FAKE, pre=FAKE, ws=FAKE, n=BIG):
+OUT, PRE, DX = FAKE + 0x10000, FAKE + 0x20000, FAKE + 0x30000
+
+
+def fwd(L, p, x=FAKE, W=FAKE, bias=FAKE, resid=FAKE, out=OUT, pre=PRE, ws=FAKE, n=BIG):
     return L.mlp_linear_fwd(ctypes.byref(p), x, W, bias, resid, out, pre, ws, n, None)
 
 
-def bwd(L, p, dout=FAKE, x=FAKE, W=FAKE, pre=FAKE, dx=FAKE, dW=FAKE, db=FAKE, fuse=0, ws=FAKE,
+def bwd(L, p, dout=FAKE, x=FAKE, W=FAKE, pre=FAKE, dx=DX, dW=FAKE, db=FAKE, fuse=0, ws=FAKE,
         n=BIG):
     return L.mlp_linear_bwd(ctypes.byref(p), dout, x, W, pre, dx, dW, db, fuse, ws, n, None)
 
@@ -63,6 +66,10 @@ def test_pointer_refusals(L):
     for name in ("dout", "pre", "x", "W", "dx", "dW", "db"):
         assert bwd(L, p, **{name: FAKE + 8}) == -2
     assert bwd(L, p, fuse=2) == -1
+    # outputs over operands that are still read
+    other = FAKE + 0x100000
+    assert fwd(L, p, x=other, out=other) == -1 and fwd(L, p, x=other, pre=other) == -1
+    assert bwd(L, p, dx=other, x=other) == -1 and bwd(L, p, dx=other, dout=other) == -1
     assert L.mlp_linear_fwd(None, FAKE, FAKE, None, None, FAKE, None, FAKE, BIG, None) == -1
     # nothing asked for: nothing to do
     assert bwd(L, p, x=None, W=None, dx=None, dW=None, db=None) == 0
