@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -175,6 +176,25 @@ def _stream(stream):
         # the current stream's handle without building a Stream object (2.8 us a call)
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+# Workspaces of the calls that are given none, kept where they are small: a
+# fresh tensor costs 3-5 us a call, more than the smallest calls themselves.
+# One for each device, stream and host thread: calls that share one are ordered.
+_KEEP_BYTES = 4 << 20
+_kept = {}
+
+
+def _call_workspace(n, device, stream):
+    """A workspace of n bytes for a call on `stream` (None: the current one)."""
+    if stream is not None or n > _KEEP_BYTES or torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    key = (device.index, _stream(None), threading.get_ident())
+    ws = _kept.get(key)
+    if ws is None or ws.numel() < n:
+        ws = torch.empty(max(n, 1 << 16), dtype=torch.uint8, device=device)
+        _kept[key] = ws
+    return ws
 
 
 def _check(rc, where):

@@ -1403,7 +1403,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
   // Inputs written by the previous kernel on the stream are visible after this.
   pdl_wait();
   pdl_launch_dependents();
-  if (EPI == EPI_LINEAR && p.one_wave && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
   const uint64_t lim = p.timeout_ns;
   const int ncl = gridDim.x / CG;          // clusters (CTA groups) in the grid
@@ -1469,7 +1469,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
             if (L.i1) tma_prefetch_l2_2d(L.i1, L.icol, L.m0);
           }
-          const int next = leader ? ncl + atomicAdd(p.counter, 1) : 0;
+          const int next = !leader      ? 0
+                           : p.one_wave ? total_units
+                                        : ncl + atomicAdd(p.counter, 1);
           const bool next_valid = next < total_units;
           UnitKey key{};
           Work nw{};
@@ -1549,9 +1551,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           // went two to a pair while other pairs found the queue empty, and
           // a forward of a few hundred tokens took one down unit longer.
           const bool late_claim = CLAIM_ALL && w.prob == 1;
-          // (EPI_LINEAR with a unit for every cluster claims none: its call
-          // then clears no counter)
-          int next = EPI == EPI_LINEAR && p.one_wave
+          // (With a unit for every cluster none is claimed: the call then
+          // clears no counter.)
+          int next = !CLAIM_ALL && p.one_wave
                          ? total_units
                          : late_claim ? -1 : (CLAIM_ALL ? 0 : ncl) + atomicAdd(p.counter, 1);
           auto claim = [&] {

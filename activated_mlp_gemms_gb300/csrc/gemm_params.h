@@ -158,7 +158,8 @@ struct Params {  // 64-byte aligned through CUtensorMap
   const int* ntiles;
   const int* offsets;
   int rows;               // rows of the sorted layout's buffers
-  int one_wave;           // EPI_LINEAR: no cluster has a second unit; the kernel clears *status
+  int one_wave;           // every unit has a cluster of its own: none is claimed from `counter`
+  int clear_status;       // the first kernel of a call without a memset clears *status
 };
 
 // Host-side launcher and co-residency query, explicitly instantiated in the

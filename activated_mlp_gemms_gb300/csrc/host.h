@@ -333,6 +333,8 @@ struct Call {
   int* counters;
   int next_counter = 0;
   int launches = 0;
+  bool one_wave = false;      // its GEMMs claim no units (begin_one_wave)
+  bool clear_status = false;  // its next GEMM clears the status word
   int* counter() { return counters + (next_counter++ % MAX_COUNTERS); }
   bool pdl() { return launches++ > 0; }  // the first kernel follows the memset or the caller's work
 };
@@ -432,11 +434,15 @@ int run_act(Gemm& g, Call& c, int tag) {
   if (!g.ok) return MLP_ERR_CUDA;
   if (g.p.total_units == 0) return MLP_OK;
   g.p.nmaps = g.nmaps;
+  g.p.one_wave = c.one_wave;
+  g.p.clear_status = c.clear_status;
+  c.clear_status = false;
   const bool pdl = c.pdl();
   if (g.cg == 2) {
     const int groups = groups_cached<EPI, A_MN, B_MN, 2, ACT, GRP>();
     if (groups <= 0) return MLP_ERR_CUDA;
     const int n = g.p.total_units < groups ? g.p.total_units : groups;
+    if (c.one_wave && n < g.p.total_units) return MLP_ERR_CUDA;  // (see one_wave_units)
     return traced(tag, c.stream,
                   [&] { return launch_gemm<EPI, A_MN, B_MN, 2, ACT, GRP>(g.p, 2 * n, c.stream, pdl); });
   }
@@ -445,6 +451,7 @@ int run_act(Gemm& g, Call& c, int tag) {
   } else {
     const int sms = num_sms();
     const int n = g.p.total_units < sms ? g.p.total_units : sms;
+    if (c.one_wave && n < g.p.total_units) return MLP_ERR_CUDA;
     return traced(tag, c.stream, [&] {
       return launch_gemm<EPI, A_MN, B_MN, 1, ACT, GRP>(g.p, n < 1 ? 1 : n, c.stream, pdl);
     });
@@ -560,6 +567,23 @@ inline int begin_call(Call& c, void* ws, void* stream, bool clear = true) {
   c.status = static_cast<int*>(ws);
   c.counters = static_cast<int*>(ws) + COUNTER_BASE;
   return clear ? cuda_err(cudaMemsetAsync(ws, 0, CTRL_BYTES, c.stream)) : MLP_OK;
+}
+
+// A call whose GEMMs all have a unit for every cluster: they claim none, the
+// control block needs no memset, and the call's first GEMM clears the status
+// word (clear = false: another kernel of the call does).  Every kernel waits
+// for the end of the one before it, so the first is launched while that, whatever
+// it is, still runs.
+inline void begin_one_wave(Call& c, void* ws, void* stream, bool clear = true) {
+  begin_call(c, ws, stream, false);
+  c.one_wave = true;
+  c.clear_status = clear;
+  c.launches = 1;
+}
+// Units up to which a GEMM is one wave: the clusters that are resident together
+// (every instance holds an SM's shared memory: 76 pairs, 152 single CTAs).
+inline int one_wave_units(int cg) {
+  return cg == 2 ? groups_cached<EPI_STORE_BF16, false, false, 2, 0>() : num_sms();
 }
 
 // fp32 [n] -> bf16 [n] (the split-K partial-sum region to the output), plus

@@ -203,10 +203,12 @@ constexpr int DACT_COLS = 256;  // columns of a block: 8 (16 bytes) per lane
 template <int ACT>
 __global__ void __launch_bounds__(32 * DACT_WARPS)
     k_linear_dact(const bf* __restrict__ dout, int ldd, const bf* __restrict__ pre,
-                  bf* __restrict__ dz, float* __restrict__ part, int M, int N, int chunk) {
+                  bf* __restrict__ dz, float* __restrict__ part, void* __restrict__ db, int accum,
+                  int M, int N, int chunk, int* status) {
   __shared__ float sums[DACT_WARPS][DACT_COLS];
   pdl_wait();
   pdl_launch_dependents();
+  if (status != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * DACT_COLS + 8 * lane;
   const int r0 = blockIdx.y * chunk, r1 = min(M, r0 + chunk);
@@ -240,7 +242,9 @@ __global__ void __launch_bounds__(32 * DACT_WARPS)
     float t = 0.f;
 #pragma unroll
     for (int w = 0; w < DACT_WARPS; ++w) t += sums[w][threadIdx.x];
-    part[static_cast<size_t>(blockIdx.y) * N + n] = t;
+    if (gridDim.y > 1) part[static_cast<size_t>(blockIdx.y) * N + n] = t;
+    else if (accum) static_cast<float*>(db)[n] += t;
+    else static_cast<bf*>(db)[n] = __float2bfloat16_rn(t);
   }
 }
 
@@ -288,8 +292,10 @@ cudaError_t launch_linear_finish(const float* acc, const void* bias, const void*
 }
 
 // Row chunks of the derivative pass: about four blocks an SM (152 SMs), each
-// with at least 16 rows.
+// with at least 16 rows; up to 128 rows are one chunk, which needs no second
+// kernel for db.
 static int dact_chunk(int M, int N) {
+  if (M <= 128) return M;
   const int cols = (N + DACT_COLS - 1) / DACT_COLS;
   int chunks = (4 * 152 + cols - 1) / cols;
   const int most = (M + 15) / 16;
@@ -303,12 +309,13 @@ int linear_db_chunks(int M, int N) {
 }
 
 cudaError_t launch_linear_dact(const void* dout, int ldd, const void* pre, void* dz, float* part,
-                               int M, int N, int act, cudaStream_t stream, bool pdl) {
+                               void* db, bool accum, int M, int N, int act, int* status,
+                               cudaStream_t stream, bool pdl) {
   const dim3 grid((N + DACT_COLS - 1) / DACT_COLS, linear_db_chunks(M, N));
   return with_act(act, [&](auto a) {
     return launch(k_linear_dact<decltype(a)::value>, grid, 32 * DACT_WARPS, stream, pdl,
                   static_cast<const bf*>(dout), ldd, static_cast<const bf*>(pre),
-                  static_cast<bf*>(dz), part, M, N, dact_chunk(M, N));
+                  static_cast<bf*>(dz), part, db, accum ? 1 : 0, M, N, dact_chunk(M, N), status);
   });
 }
 

@@ -36,10 +36,12 @@ cudaError_t launch_linear_finish(const float* acc, const void* bias, const void*
 
 // dz = dout * act'(pre) into dz (bf16 [M, N] dense; null: not written) and the
 // column sums of dz over each chunk of rows into part fp32 [chunks, N] (null:
-// not formed); then db[n] = sum over chunks (bf16), or db[n] += (fp32).
+// not formed); then db[n] = sum over chunks (bf16), or db[n] += (fp32).  With
+// one chunk the first writes db itself.  Clears *status (null: not).
 int linear_db_chunks(int M, int N);
 cudaError_t launch_linear_dact(const void* dout, int ldd, const void* pre, void* dz, float* part,
-                               int M, int N, int act, cudaStream_t stream, bool pdl);
+                               void* db, bool accum, int M, int N, int act, int* status,
+                               cudaStream_t stream, bool pdl);
 cudaError_t launch_linear_db(const float* part, int chunks, void* db, int N, bool accum,
                              cudaStream_t stream, bool pdl);
 

@@ -80,16 +80,8 @@ int check_ws(const Layout& L, const void* ws, size_t ws_bytes) {
   return ws_bytes < L.total ? MLP_ERR_WORKSPACE_TOO_SMALL : MLP_OK;
 }
 
-// The GEMM with the layer's epilogue.  When every unit has a cluster of its own
-// nothing is claimed from the control block's counter, and the kernel clears
-// the status word itself: no memset before it (22.7 -> 20 us for 777 x 4864 x
-// 2048).
 template <int ACT>
-int run_linear(Gemm& g, Call& c, void* ws, void* stream) {
-  const int groups = g.cg == 2 ? groups_cached<EPI_LINEAR, false, false, 2, ACT>() : num_sms();
-  g.p.one_wave = g.p.total_units <= groups;
-  if (!g.p.one_wave) MLP_TRY(begin_call(c, ws, stream));
-  else c.launches = 1;  // (its kernel waits for the one before it)
+int run_linear(Gemm& g, Call& c) {
   return run_act<EPI_LINEAR, false, false, ACT>(g, c, MLP_KERNEL_LINEAR);
 }
 
@@ -119,13 +111,15 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
   const int ldx = p->ldx ? p->ldx : K, ldr = p->ldr ? p->ldr : N, ldo = p->ldo ? p->ldo : N;
   const bool streamed = M <= LINEAR_STREAM_MAX_M;
-  Call c;
   const bool tiles = !streamed && !skinny(p);
-  MLP_TRY(begin_call(c, ws, stream, tiles && L.split > 1));
-  // Without a memset before it, the call's first kernel may be launched while
-  // the kernel before it on the stream, whatever it is, still runs: each of
-  // these waits for that one's end before it touches memory.
-  if (!tiles) c.launches = 1;
+  const int cg = pick_cg(M);
+  Call c;
+  // (one wave: 22.7 -> 18.9 us for 777 x 4864 x 2048; the stream and the skinny
+  // kernel use no counter and clear the status word themselves)
+  if (!tiles || (L.split == 1 && out_tiles(M, N, cg) <= one_wave_units(cg)))
+    begin_one_wave(c, ws, stream, tiles);
+  else
+    MLP_TRY(begin_call(c, ws, stream));
   if (streamed) {
     const bool pdl = c.pdl();
     return traced(MLP_KERNEL_LINEAR, c.stream, [&] {
@@ -145,7 +139,7 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
                                   c.status, wait_limit_ns(), c.stream, pdl);
     });
   }
-  Gemm g(act, 1.f, c.counter(), c.status, pick_cg(M));
+  Gemm g(act, 1.f, c.counter(), c.status, cg);
   const int mA = g.kmajor_a(x, M, K, ldx);
   const int mB = g.kmajor(W, N, K, g.b_rows());
   if (L.split > 1) {
@@ -179,12 +173,12 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   P.ld = ldr;
   P.alpha = p->resid_scale;
   switch (act) {
-    case ACT_RELU: return run_linear<ACT_RELU>(g, c, ws, stream);
-    case ACT_RELU_SQ: return run_linear<ACT_RELU_SQ>(g, c, ws, stream);
-    case ACT_GELU_HW: return run_linear<ACT_GELU_HW>(g, c, ws, stream);
-    case ACT_SILU: return run_linear<ACT_SILU>(g, c, ws, stream);
-    case ACT_SIGMOID: return run_linear<ACT_SIGMOID>(g, c, ws, stream);
-    default: return run_linear<ACT_NONE>(g, c, ws, stream);
+    case ACT_RELU: return run_linear<ACT_RELU>(g, c);
+    case ACT_RELU_SQ: return run_linear<ACT_RELU_SQ>(g, c);
+    case ACT_GELU_HW: return run_linear<ACT_GELU_HW>(g, c);
+    case ACT_SILU: return run_linear<ACT_SILU>(g, c);
+    case ACT_SIGMOID: return run_linear<ACT_SIGMOID>(g, c);
+    default: return run_linear<ACT_NONE>(g, c);
   }
 }
 
@@ -210,9 +204,16 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
   const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
   const int ldx = p->ldx ? p->ldx : K, ldd = p->ldo ? p->ldo : N;
   char* base = static_cast<char*>(ws);
-  Call c;
-  MLP_TRY(begin_call(c, ws, stream));
   const bool split = dx && L.split > 1;
+  const int cgx = pick_cg(M), cgw = pick_cg(N < K ? N : K);
+  // dz_out or db: the derivative pass comes first and clears the status word
+  const bool pass = (has_act && (dx || dW)) || db;
+  Call c;
+  if (!split && (!dx || out_tiles(M, K, cgx) <= one_wave_units(cgx)) &&
+      (!dW || (!fuse && out_tiles(N, K, cgw) <= one_wave_units(cgw))))
+    begin_one_wave(c, ws, stream, !pass);
+  else
+    MLP_TRY(begin_call(c, ws, stream));
   float* part = reinterpret_cast<float*>(base + L.part);
   if (split) MLP_TRY(cuda_err(cudaMemsetAsync(part, 0, (size_t)M * K * 4, c.stream)));
 
@@ -223,8 +224,8 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
   if (dz_out || db) {
     const bool pdl = c.pdl();
     MLP_TRY(traced(MLP_KERNEL_LINEAR_DACT, c.stream, [&] {
-      return launch_linear_dact(dout, ldd, pre, dz_out, db ? sums : nullptr, M, N, act, c.stream,
-                                pdl);
+      return launch_linear_dact(dout, ldd, pre, dz_out, db ? sums : nullptr, db, fuse != 0, M, N,
+                                act, c.one_wave ? c.status : nullptr, c.stream, pdl);
     }));
   }
   if (dz_out) {
@@ -232,15 +233,18 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
     ldz = N;
   }
 
-  // dW and db go to the second stream when dx runs too (mlp_bwd's reasons)
-  Side* side = dx && (dW || db) && !g_trace_flag.load() ? side_stream(c.stream) : nullptr;
+  // a single chunk of rows: the pass has written db itself
+  const bool db_left = db && linear_db_chunks(M, N) > 1;
+  // dW and db go to the second stream when dx runs too (mlp_bwd's reasons),
+  // unless all are small: then the events cost more than the overlap gives
+  Side* side = dx && (dW || db_left) && !c.one_wave && !g_trace_flag.load() ? side_stream(c.stream) : nullptr;
   std::unique_lock<std::mutex> side_lk;
   if (side) {
     side_lk = std::unique_lock<std::mutex>(side->mu);
     MLP_TRY(cuda_err(cudaEventRecord(side->fork, c.stream)));
   }
   if (dx) {
-    Gemm g(act, 1.f, c.counter(), c.status, pick_cg(M));
+    Gemm g(act, 1.f, c.counter(), c.status, cgx);
     const int mA = g.kmajor_a(dz, M, N, ldz);
     const int mB = g.mnmajor(W, N, K);  // W [N,K]: B(n=k, k=n) is contiguous along K
     const int oX = split ? g.output(part, M, K, true) : g.output(dx, M, K);
@@ -257,21 +261,21 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
       MLP_TRY((run<EPI_STORE_BF16, false, true>(g, c, MLP_KERNEL_DX)));
     }
   }
-  if (dW || db) {
+  if (dW || db_left) {
     Call cw = c;
     if (side) {
       cw.stream = side->stream;
       cw.launches = 0;  // its first kernel follows an event wait, not a kernel
       MLP_TRY(cuda_err(cudaStreamWaitEvent(side->stream, side->fork, 0)));
     }
-    if (db) {
+    if (db_left) {
       const bool pdl = cw.pdl();
       MLP_TRY(traced(MLP_KERNEL_LINEAR_DB, cw.stream, [&] {
         return launch_linear_db(sums, linear_db_chunks(M, N), db, N, fuse != 0, cw.stream, pdl);
       }));
     }
     if (dW) {
-      Gemm g(act, 1.f, cw.counter(), cw.status, pick_cg(N < K ? N : K));
+      Gemm g(act, 1.f, cw.counter(), cw.status, cgw);
       const int mA = g.mnmajor(dz, M, N, ldz);
       const int mB = g.mnmajor(x, M, K, ldx);
       const int oW = g.output(dW, N, K, fuse != 0);

@@ -132,6 +132,18 @@ struct RowGemm : Gemm {
   MoePlan L;
 };
 
+// Output tiles of a GEMM over the rows with `cols` columns in tiles of tile_n, at
+// most (the plan has their number).
+long long row_units(const mlp_moe_t* p, int cols, int tile_n) {
+  const int cg = moe_cg(p);
+  return plan_of(p).tile_cap[cg - 1] * ((cols + tile_n - 1) / tile_n);
+}
+// The forward's two GEMMs are one wave each.
+bool fwd_one_wave(const mlp_moe_t* p) {
+  const int most = one_wave_units(moe_cg(p));
+  return row_units(p, p->I, gated(p) ? 128 : MMA_N) <= most && row_units(p, p->H, MMA_N) <= most;
+}
+
 int launch_experts_act(const mlp_moe_t* p, Call& c, const int* plan, const void* xs, const void* Wg,
                        const void* Wu, void* a, void* G, void* U) {
   RowGemm g(p, c, plan);
@@ -292,7 +304,8 @@ int mlp_moe_experts_fwd(const mlp_moe_t* p, const void* plan, const void* xs, co
   if (!gated(p) && U_save) return MLP_ERR_INVALID_ARG;
   MLP_TRY(check_ws(p, MLP_MODE_FWD, ws, ws_bytes));
   Call c;
-  MLP_TRY(begin_call(c, ws, stream));
+  if (fwd_one_wave(p)) begin_one_wave(c, ws, stream);
+  else MLP_TRY(begin_call(c, ws, stream));
   void* a = static_cast<char*>(ws) + layout(p, MLP_MODE_FWD).inter;
   const int* pl = static_cast<const int*>(plan);
   MLP_TRY(launch_experts_act(p, c, pl, xs, Wg, Wu, a, G_save, U_save));
@@ -323,8 +336,16 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
   MLP_TRY(check_ws(p, MLP_MODE_BWD, ws, ws_bytes));
   const bool need_dact = dxs || dWg || dWu;
   if (!need_dact && !dWd) return MLP_OK;
+  const int cgw = p->H > BM && p->I > BM ? moe_cg(p) : pick_cg(p->H < p->I ? p->H : p->I);
+  const long long w_units = ((dWg ? 1 : 0) + (dWu ? 1 : 0)) * out_tiles(p->I, p->H, cgw) +
+                            (dWd ? 1 : 0) * out_tiles(p->H, p->I, cgw);
+  const int most = one_wave_units(moe_cg(p));
   Call c;
-  MLP_TRY(begin_call(c, ws, stream));
+  if (need_dact && row_units(p, p->I, MMA_N) <= most && row_units(p, p->H, MMA_N) <= most &&
+      w_units * p->E <= one_wave_units(cgw))
+    begin_one_wave(c, ws, stream);
+  else
+    MLP_TRY(begin_call(c, ws, stream));
   void* a = static_cast<char*>(ws) + layout(p, MLP_MODE_BWD).inter;
   const int* pl = static_cast<const int*>(plan);
   const int rows = static_cast<int>(plan_of(p).rows);
@@ -357,9 +378,10 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
     }));
   }
 
-  // the input gradient, and the weight gradients beside it (mlp_bwd's reasons)
+  // the input gradient, and the weight gradients beside it (mlp_bwd's reasons;
+  // small ones after it: the events cost more than the overlap gives)
   const bool want_w = dWg || dWu || dWd;
-  Side* side = (dxs && want_w && !g_trace_flag.load()) ? side_stream(c.stream) : nullptr;
+  Side* side = (dxs && want_w && !c.one_wave && !g_trace_flag.load()) ? side_stream(c.stream) : nullptr;
   std::unique_lock<std::mutex> side_lk;
   if (side) {
     side_lk = std::unique_lock<std::mutex>(side->mu);
@@ -392,8 +414,7 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
       MLP_TRY(cuda_err(cudaStreamWaitEvent(side->stream, side->fork, 0)));
     }
     const int fuse = fuse_grad_accum;
-    Gemm g(device_act(p->act), 1.f, cw.counter(), cw.status,
-           p->H > BM && p->I > BM ? moe_cg(p) : pick_cg(p->H < p->I ? p->H : p->I));
+    Gemm g(device_act(p->act), 1.f, cw.counter(), cw.status, cgw);
     g.p.offsets = pl + plan_of(p).offsets;
     g.p.rows = rows;
     struct W { const void* A; int m; const void* B; int n; void* out; };
@@ -440,10 +461,10 @@ int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const v
   char* base = static_cast<char*>(ws);
   int* plan = reinterpret_cast<int*>(base + w.plan);
   void *a = base + w.inter, *xs = base + w.xs, *y = base + w.y;
-  const bool stream_weights = decode_moe(p);
+  const bool stream_weights = decode_moe(p);  // (clears the status word itself)
   Call c;
-  MLP_TRY(begin_call(c, ws, stream, !stream_weights));
-  if (stream_weights) c.launches = 1;  // (its first kernel waits for the one before it)
+  if (stream_weights || fwd_one_wave(p)) begin_one_wave(c, ws, stream, !stream_weights);
+  else MLP_TRY(begin_call(c, ws, stream));
   bool pdl = c.pdl();
   if (stream_weights) {
     MLP_TRY(traced(MLP_KERNEL_GATE_UP, c.stream, [&] {

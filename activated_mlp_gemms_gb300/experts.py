@@ -13,8 +13,8 @@ from collections.abc import Mapping
 
 import torch
 
-from . import (ACTS, MODE_BWD, MODE_FWD, MODE_INFER, MlpError, _check, _ptr, _stream,
-               _wdt, lib)
+from . import (ACTS, MODE_BWD, MODE_FWD, MODE_INFER, MlpError, _call_workspace, _check, _ptr,
+               _stream, _wdt, lib)
 
 ROW_ALIGN = 16  # MLP_MOE_ROW_ALIGN
 MAX_EXPERTS = 1024  # MLP_MOE_MAX_EXPERTS
@@ -207,12 +207,10 @@ def alloc_moe_workspace(p: Moe, mode: int, device=None) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _ws(ws, p, mode, device):
-    if ws is None:
+def _ws(ws, p, mode, device, stream):
+    if ws is None:  # (of a problem that the call refuses: any)
         n = _ws_size(p.T, p.E, p.top_k, p.H, p.I, p.act, mode)
-        if n == 0:  # (the call itself says why)
-            n = 256
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        return _call_workspace(n or 256, device, stream)
     if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return ws
@@ -231,7 +229,7 @@ def mlp_moe_experts_fwd(p: Moe, plan, xs, Wg, Wu, Wd, y, G_save=None, U_save=Non
     Wd [E, H, I].  Rows of y past the plan's offsets[E] are not written.  Returns the
     workspace used."""
     rows = mlp_moe_rows(p)
-    ws = _ws(ws, p, MODE_FWD, y.device)
+    ws = _ws(ws, p, MODE_FWD, y.device, stream)
     rc = lib().mlp_moe_experts_fwd(ctypes.byref(p), _plan(p, plan), _shaped(xs, (rows, p.H), "xs"),
                                    *_weights(p, Wg, Wu, Wd), _shaped(y, (rows, p.H), "y"),
                                    _shaped(G_save, (rows, p.I), "G_save"),
@@ -247,7 +245,7 @@ def mlp_moe_experts_bwd(p: Moe, plan, dy, xs, Wg, Wu, Wd, G, U, dxs=None, dWg=No
     Outputs that are None are skipped; weight gradients are bf16 (overwritten) or fp32
     (+= in place) when fuse_grad_accum.  The padding rows of dy and xs are zero."""
     rows = mlp_moe_rows(p)
-    ws = _ws(ws, p, MODE_BWD, dy.device)
+    ws = _ws(ws, p, MODE_BWD, dy.device, stream)
     rc = lib().mlp_moe_experts_bwd(ctypes.byref(p), _plan(p, plan), _shaped(dy, (rows, p.H), "dy"),
                                    _shaped(xs, (rows, p.H), "xs"), *_weights(p, Wg, Wu, Wd),
                                    _shaped(G, (rows, p.I), "G"), _shaped(U, (rows, p.I), "U"),
@@ -263,7 +261,7 @@ def mlp_moe_experts_bwd(p: Moe, plan, dy, xs, Wg, Wu, Wd, G, U, dxs=None, dWg=No
 def mlp_moe_fwd_infer(p: Moe, x, ids, weights, Wg, Wu, Wd, residual, out, ws=None, stream=None):
     """The whole layer without gradients: out[t] = residual[t] + sum_j weights[t, j]
     MLP_{ids[t, j]}(x[t]) (residual may be None).  Returns the workspace used."""
-    ws = _ws(ws, p, MODE_INFER, out.device)
+    ws = _ws(ws, p, MODE_INFER, out.device, stream)
     th, tk = (p.T, p.H), (p.T, p.top_k)
     rc = lib().mlp_moe_fwd_infer(ctypes.byref(p), _shaped(x, th, "x"),
                                  _shaped(ids, tk, "ids", torch.int32),

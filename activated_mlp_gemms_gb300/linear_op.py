@@ -14,7 +14,7 @@ import functools
 
 import torch
 
-from . import MlpError, _check, _ptr, _stream, lib
+from . import MlpError, _call_workspace, _check, _ptr, _stream, lib
 
 LINEAR_ACTS = {"none": 0, "relu": 1, "relu_sq": 2, "gelu_tanh_approx": 3, "silu": 4, "sigmoid": 5}
 
@@ -98,26 +98,9 @@ def alloc_linear_workspace(p: Linear, backward=False, device=None) -> torch.Tens
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-STREAM_MAX_M = 8  # rows up to which the forward streams its weights (mlp_linear.h)
-_status = {}  # device -> the status word that streamed forwards share
-
-
-def _ws(ws, p, backward, device):
-    if ws is None:
-        if not backward and p.M <= STREAM_MAX_M:
-            # A streamed forward uses the status word alone, waits on nothing and
-            # writes 0 there: all of them can share one, on any stream.
-            ws = _status.get(device)
-            if ws is not None:
-                return ws
-        n = _ws_size(p.M, p.N, p.K, p.act, backward)
-        if n == 0:  # (the call itself says why)
-            n = 256
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        if (not backward and p.M <= STREAM_MAX_M and n >= 1024
-                and not torch.cuda.is_current_stream_capturing()):  # (not a graph's own memory)
-            _status[device] = ws
-        return ws
+def _ws(ws, p, backward, device, stream):
+    if ws is None:  # (of a problem that the call refuses: any)
+        return _call_workspace(_ws_size(p.M, p.N, p.K, p.act, backward) or 256, device, stream)
     if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return ws
@@ -126,12 +109,13 @@ def _ws(ws, p, backward, device):
 def mlp_linear_fwd(p: Linear, x, W, bias, residual, out, pre_save=None, ws=None, stream=None):
     """out = act(x W^T + bias) + resid_scale * residual; bias and residual may be None.
     pre_save (bf16 [M, N]) receives x W^T + bias for the backward of an activation.
-    Returns the workspace used."""
+    Returns the workspace used (given none, a small one that later calls of this thread on
+    this stream use too)."""
     xp, ldx = _pitched(x, (p.M, p.K), "x")
     rp, ldr = _pitched(residual, (p.M, p.N), "residual")
     op, ldo = _pitched(out, (p.M, p.N), "out")
     q = _problem(p, ldx, ldr, ldo)
-    ws = _ws(ws, q, False, out.device)
+    ws = _ws(ws, q, False, out.device, stream)
     rc = lib().mlp_linear_fwd(ctypes.byref(q), xp, _dense(W, (p.N, p.K), "W"),
                               _dense(bias, (p.N,), "bias"), rp, op,
                               _dense(pre_save, (p.M, p.N), "pre_save"), ws.data_ptr(), ws.numel(),
@@ -149,7 +133,7 @@ def mlp_linear_bwd(p: Linear, dout, x, W, pre=None, dx=None, dW=None, db=None,
     xp, ldx = _pitched(x, (p.M, p.K), "x")
     wd = torch.float32 if fuse_grad_accum else torch.bfloat16
     q = _problem(p, ldx, 0, ldd)
-    ws = _ws(ws, q, True, dout.device)
+    ws = _ws(ws, q, True, dout.device, stream)
     rc = lib().mlp_linear_bwd(ctypes.byref(q), dp, xp, _dense(W, (p.N, p.K), "W"),
                               _dense(pre, (p.M, p.N), "pre"), _dense(dx, (p.M, p.K), "dx"),
                               _dense(dW, (p.N, p.K), "dW", wd), _dense(db, (p.N,), "db", wd),
