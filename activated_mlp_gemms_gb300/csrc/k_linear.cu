@@ -2,7 +2,6 @@
 //   k_linear_stream  a few rows: the weights stream once (HBM-bound), dot
 //                    products on the warp-level MMA as in k_decode_mma.cu,
 //                    bias, activation and residual in the epilogue
-//   k_linear_finish  the epilogue on split-K sums
 //   k_linear_dact    dz = dout act'(z), and the bias gradient's partial sums
 //                    in the same pass over dout (HBM-bound: 3 M N bf16 values)
 //   k_linear_db      the sum of those partial sums, in a fixed order
@@ -162,39 +161,6 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(256)
-    k_linear_finish(const float* __restrict__ acc, const bf* __restrict__ bias, const bf* resid,
-                    int ldr, float rs, bf* out, int ldo, bf* __restrict__ pre, int M, int N) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int per_row = N / 8;
-  const long long total = static_cast<long long>(M) * per_row;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const long long r = i / per_row;
-    const int c = static_cast<int>(i - r * per_row) * 8;
-    const float4 a0 = *reinterpret_cast<const float4*>(acc + r * N + c);
-    const float4 a1 = *reinterpret_cast<const float4*>(acc + r * N + c + 4);
-    float z[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}, o[8];
-    if (bias) {
-      float b[8];
-      unpack8(ld_global_v4(bias + c), b);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) z[k] += b[k];
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = act_f<ACT>(z[k]);
-    if (resid) {
-      float f[8];
-      unpack8(ld_global_v4(resid + r * ldr + c), f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = fmaf(rs, f[k], o[k]);
-    }
-    if (pre) st_global_v4(pre + r * N + c, pack8(z));
-    st_global_v4(out + r * ldo + c, pack8(o));
-  }
-}
-
 constexpr int DACT_WARPS = 8;
 constexpr int DACT_COLS = 256;  // columns of a block: 8 (16 bytes) per lane
 
@@ -276,18 +242,6 @@ cudaError_t launch_linear_stream(const void* x, int ldx, const void* W, const vo
                   static_cast<const bf*>(x), ldx, static_cast<const bf*>(W),
                   static_cast<const bf*>(bias), static_cast<const bf*>(resid), ldr, rs,
                   static_cast<bf*>(out), ldo, static_cast<bf*>(pre), M, N, K, status);
-  });
-}
-
-cudaError_t launch_linear_finish(const float* acc, const void* bias, const void* resid, int ldr,
-                                 float rs, void* out, int ldo, void* pre, int M, int N, int act,
-                                 cudaStream_t stream, bool pdl) {
-  const long long blocks = (static_cast<long long>(M) * (N / 8) + 255) / 256;
-  return with_act(act, [&](auto a) {
-    return launch(k_linear_finish<decltype(a)::value>,
-                  dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), 256, stream, pdl, acc,
-                  static_cast<const bf*>(bias), static_cast<const bf*>(resid), ldr, rs,
-                  static_cast<bf*>(out), ldo, static_cast<bf*>(pre), M, N);
   });
 }
 

@@ -1,21 +1,25 @@
-// The linear layer for a few dozen to a few hundred rows: out = act(x W^T + bias)
-// + rs * resid with every weight read once.
+// The linear layer where 256 x 256 output tiles are too few: out = act(x W^T +
+// bias) + rs * resid, and dx = dz W, for a few dozen to some hundreds of rows (or
+// a narrow N).
 //
 // With M rows the layer does 2 M flops per weight, below the tensor cores'
 // balance against HBM up to M of a few hundred, so the weights' stream is the
 // bound, and tiles of 256 output columns are too few to draw it.  The operands
-// change places: 128 weight rows are the MMA's M, the rows of x its N (M rounded
-// up to 16), so a CTA streams 128 rows of W (16 KB a k-block) against all of x,
-// and the MMA wastes nothing on absent rows.  When the N / 128 blocks are fewer
-// than the SMs, a cluster of 2, 4 or 8 CTAs shares a block's K: each leaves its
-// fp32 sums in its own shared memory, [row of x][128 features], and takes a
-// share of the rows of x to finish, adding the cluster's sums in rank order
-// through distributed shared memory.  No partial sums in global memory, no
-// atomics: the same bits on every run.
+// change places: 128 weight rows are the MMA's M, the rows of x its N (up to 256
+// a tile, in equal tiles rounded up to 16), so a CTA streams 128 rows of W (16
+// KB a k-block) against all of its rows of x, and the MMA wastes nothing on
+// absent rows.  (For dx the 128 are columns of W, read MN-major in two boxes.)
+// When the blocks are fewer than the SMs, a cluster of 2, 4 or 8 CTAs shares a
+// block's K: the rows of x are dealt out to its CTAs, each writes its fp32 sums of
+// a row to the row's owner through distributed shared memory, and the owner adds
+// them in rank order.
+// (Stores that nothing waits for; owners that read the others' sums instead
+// waited for each round: 26 against 15 us for 160 x 1024 x 8192.)  No partial
+// sums in global memory, no atomics: the same bits on every run.
 //
-// Warp 0 feeds the ring by TMA, warp 1 issues tcgen05.mma, warps 2-5 move the
-// accumulator (lane = feature) to shared memory; all six finish rows, 8 features
-// (16 bytes) a thread.
+// Warp 0 feeds the ring by TMA, warp 1 issues tcgen05.mma, warps 2-9 move the
+// accumulator (lane = feature) to shared memory; all ten finish rows, 8 features
+// (16 bytes) of two rows a thread at a time.
 #include <atomic>
 
 #include "act.cuh"
@@ -28,7 +32,7 @@ namespace {
 
 using bf = __nv_bfloat16;
 
-constexpr int SK_THREADS = 192;
+constexpr int SK_THREADS = 320;
 constexpr int SK_ROWS = 128;                     // weight rows of a CTA
 constexpr int SK_A = SK_ROWS * BK * 2;           // bytes of a k-block of them
 // bytes of the ring (2 KB of alignment and control apart): one CTA an SM, or two
@@ -48,13 +52,13 @@ __host__ __device__ constexpr bool sk_sums_fit(int mp, bool two) {
 }
 static_assert(sk_sums_fit(256, false) && sk_sums_fit(16, false) && sk_sums_fit(16, true), "ring");
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  const uint4 v = ld_shared_v4(addr);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
 }
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -69,12 +73,12 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-template <int ACT>
+template <int ACT, bool A_MN>
 __global__ void __launch_bounds__(SK_THREADS, 2)
     k_linear_skinny(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                     const bf* __restrict__ bias, const bf* resid, int ldr, float rs, bf* out,
-                    int ldo, bf* __restrict__ pre, int M, int N, int K, int mp, int stages, int no_work,
-                    int* status, unsigned long long limit_ns) {
+                    int ldo, bf* __restrict__ pre, int M, int N, int K, int mp, int stages, int clear,
+                    int no_work, int* status, unsigned long long limit_ns) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   const int stage_bytes = sk_stage(mp);
@@ -88,7 +92,8 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
   const uint32_t done = smem_u32(bar + 2 * SK_MAX_STAGES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int share = gridDim.y, rank = blockIdx.y;  // the cluster that shares this block's K
-  const int row0 = blockIdx.x * SK_ROWS;
+  const int row0 = blockIdx.x * SK_ROWS;  // the features
+  const int m0 = blockIdx.z * mp, m1 = min(M, m0 + mp);
   const int kbs = (K + BK - 1) / BK;
   const int kb0 = static_cast<int>(static_cast<long long>(kbs) * rank / share);
   const int kb1 = static_cast<int>(static_cast<long long>(kbs) * (rank + 1) / share);
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
   const uint32_t tmem = *tmem_s;
   pdl_wait();
   pdl_launch_dependents();
-  if (blockIdx.x == 0 && rank == 0 && threadIdx.x == 0) *status = 0;
+  if (clear && blockIdx.x == 0 && rank == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0;
   auto give_up = [&] {
     *abort_flag = 1;
     atomicExch(status, SK_TIMEOUT);
@@ -134,8 +139,13 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
         }
         mbar_expect_tx(full(stage), stage_bytes);
         const uint32_t s = base + stage * stage_bytes;
-        tma_load_2d(s, &map_w, kb * BK, row0, full(stage), pol_w);
-        tma_load_2d(s + SK_A, &map_x, kb * BK, 0, full(stage), pol_x);
+        if constexpr (A_MN) {
+          tma_load_2d(s, &map_w, row0, kb * BK, full(stage), pol_w);
+          tma_load_2d(s + SK_A / 2, &map_w, row0 + 64, kb * BK, full(stage), pol_w);
+        } else {
+          tma_load_2d(s, &map_w, kb * BK, row0, full(stage), pol_w);
+        }
+        tma_load_2d(s + SK_A, &map_x, kb * BK, m0, full(stage), pol_x);
         ++issued;
         if (++stage == stages) {
           stage = 0;
@@ -157,7 +167,7 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(SK_ROWS, mp, false, false);
+      const uint32_t idesc = idesc_bf16(SK_ROWS, mp, A_MN, false);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -170,8 +180,10 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
         const uint32_t sA = base + stage * stage_bytes, sB = sA + SK_A;
 #pragma unroll
         for (int k = 0; k < BK / 16; ++k)
-          tc_mma_bf16(tmem, sdesc_sw128(sA + k * 32, 16, 1024), sdesc_sw128(sB + k * 32, 16, 1024),
-                      idesc, kb > kb0 || k > 0);
+          tc_mma_bf16(tmem,
+                      A_MN ? sdesc_sw128(sA + k * 2048, SK_A / 2, 1024)
+                           : sdesc_sw128(sA + k * 32, 16, 1024),
+                      sdesc_sw128(sB + k * 32, 16, 1024), idesc, kb > kb0 || k > 0);
         tc_commit(empty(stage));
         if (++stage == stages) {
           stage = 0;
@@ -187,70 +199,90 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
   const bool summed = mbar_wait(done, 0, limit_ns + limit_ns / 2, abort_flag);
   if (!summed && lane == 0) give_up();
   __syncwarp();
+  if (share > 1) cluster_sync();  // the owners' rings are free too
+  // [rank][row of the owner][feature] in every CTA: row j of the tile belongs to
+  // CTA j % share, as its row j / share
+  const int rows = mp / share;
   if (warp >= 2) {
     tc_fence_after();
     const int q = warp & 3;  // the TMEM lanes this warp may read: features 32 q + lane
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const uint32_t col = base + static_cast<uint32_t>(32 * q + lane) * 4u;
-    for (int c = 0; c < mp; c += 16) {
+    const uint32_t col = base + static_cast<uint32_t>(rank * rows) * (SK_ROWS * 4) +
+                         static_cast<uint32_t>(32 * q + lane) * 4u;
+    for (int c = 16 * ((warp - 2) >> 2); c < mp; c += 32) {  // two warps a quadrant
       uint32_t v[16];
       tmem_ld16(tb + c, v);
       tmem_wait_ld();
+      if (share == 1) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        st_shared_f32(col + static_cast<uint32_t>(c + j) * (SK_ROWS * 4), __uint_as_float(v[j]));
+        for (int j = 0; j < 16; ++j)
+          st_shared_f32(col + static_cast<uint32_t>(c + j) * (SK_ROWS * 4), __uint_as_float(v[j]));
+      } else {
+        // (16 is a multiple of share)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          st_cluster_f32(mapa_shared(col + static_cast<uint32_t>((c + j) / share) * (SK_ROWS * 4),
+                                     (c + j) % share),
+                         __uint_as_float(v[j]));
+      }
     }
     tc_fence_before();
   }
-  if (share > 1) cluster_sync();
+  if (share > 1) cluster_sync();  // every sum has arrived
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, cols);
   }
 
-  // rows of x rank, rank + share, ...: 16 threads a row, 8 features each
+  // this CTA's rows of x: 16 threads a row, 8 features each, two rows at a time
   const int seg = threadIdx.x & 15, n = row0 + 8 * seg;
   if (n < N) {
     float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (bias) unpack8(ld_global_v4(bias + n), b);
-    for (int m = rank + share * (threadIdx.x >> 4); m < M; m += share * (SK_THREADS / 16)) {
-      const uint32_t at = base + static_cast<uint32_t>(m) * (SK_ROWS * 4) + 32u * seg;
-      uint4 rv = make_uint4(0, 0, 0, 0);
-      if (resid) rv = ld_global_v4(resid + static_cast<size_t>(m) * ldr + n);
-      float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      float4 u[SK_MAX_SHARE], v[SK_MAX_SHARE];  // all in flight together
+    constexpr int STEP = SK_THREADS / 16;
+    for (int la = threadIdx.x >> 4; la < rows; la += 2 * STEP) {
+      uint4 rv[2];
+      float z[2][8];
 #pragma unroll
-      for (int c = 0; c < SK_MAX_SHARE; ++c) {
-        if (c >= share) break;
-        const uint32_t p = share > 1 ? mapa_shared(at, c) : at;
-        u[c] = ld_cluster_f4(p);
-        v[c] = ld_cluster_f4(p + 16);
+      for (int h = 0; h < 2; ++h) {
+        const int m = m0 + rank + share * (la + h * STEP);
+        rv[h] = resid && m < m1 ? ld_global_v4(resid + static_cast<size_t>(m) * ldr + n)
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[h][i] = b[i];
+      }
+      for (int c = 0; c < share; ++c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int l = la + h * STEP < rows ? la + h * STEP : la;
+          const uint32_t at = base + static_cast<uint32_t>(c * rows + l) * (SK_ROWS * 4) + 32u * seg;
+          const float4 u = ld_shared_f4(at), v = ld_shared_f4(at + 16);
+          z[h][0] += u.x, z[h][1] += u.y, z[h][2] += u.z, z[h][3] += u.w;
+          z[h][4] += v.x, z[h][5] += v.y, z[h][6] += v.z, z[h][7] += v.w;
+        }
       }
 #pragma unroll
-      for (int c = 0; c < SK_MAX_SHARE; ++c) {
-        if (c >= share) break;
-        z[0] += u[c].x, z[1] += u[c].y, z[2] += u[c].z, z[3] += u[c].w;
-        z[4] += v[c].x, z[5] += v[c].y, z[6] += v[c].z, z[7] += v[c].w;
-      }
-      float r[8], o[8];
-      unpack8(rv, r);
+      for (int h = 0; h < 2; ++h) {
+        const int l = la + h * STEP, m = m0 + rank + share * l;
+        if (l >= rows || m >= m1) break;
+        float r[8], o[8];
+        unpack8(rv[h], r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        z[i] += b[i];
-        o[i] = act_f<ACT>(z[i]);
-        if (resid) o[i] = fmaf(rs, r[i], o[i]);
+        for (int i = 0; i < 8; ++i) {
+          o[i] = act_f<ACT>(z[h][i]);
+          if (resid) o[i] = fmaf(rs, r[i], o[i]);
+        }
+        if (pre)
+          st_global_v4(pre + static_cast<size_t>(m) * N + n,
+                       make_uint4(pack_bf16x2(z[h][0], z[h][1]), pack_bf16x2(z[h][2], z[h][3]),
+                                  pack_bf16x2(z[h][4], z[h][5]), pack_bf16x2(z[h][6], z[h][7])));
+        st_global_v4(out + static_cast<size_t>(m) * ldo + n,
+                     make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])));
       }
-      if (pre)
-        st_global_v4(pre + static_cast<size_t>(m) * N + n,
-                     make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
-                                pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7])));
-      st_global_v4(out + static_cast<size_t>(m) * ldo + n,
-                   make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                              pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])));
     }
   }
-  if (share > 1) cluster_sync();  // no CTA leaves while its sums are read
 }
 
 struct Config {
@@ -300,12 +332,12 @@ int resident_clusters(Kern kern, int share) {
   return n;
 }
 
-template <int ACT>
+template <int ACT, bool A_MN>
 cudaError_t launch(const CUtensorMap& map_w, const CUtensorMap& map_x, const bf* bias,
                    const bf* resid, int ldr, float rs, bf* out, int ldo, bf* pre, int M, int N,
-                   int K, int no_work, int* status, unsigned long long limit_ns,
+                   int K, int clear, int no_work, int* status, unsigned long long limit_ns,
                    cudaStream_t stream, bool pdl) {
-  auto kern = k_linear_skinny<ACT>;
+  auto kern = k_linear_skinny<ACT, A_MN>;
   static std::atomic<unsigned> configured{0};  // devices that got the shared-memory attribute
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -317,7 +349,8 @@ cudaError_t launch(const CUtensorMap& map_w, const CUtensorMap& map_x, const bf*
     if (e != cudaSuccess) return e;
     if (dev < 31) configured.fetch_or(1u << dev);
   }
-  const int blocks = (N + SK_ROWS - 1) / SK_ROWS, kbs = (K + BK - 1) / BK;
+  const SkinnyShape sh = linear_skinny_shape(M, N, K);
+  const int blocks = sh.blocks * sh.tiles, kbs = (K + BK - 1) / BK;
   // a block's K is shared while the clusters stay resident in one wave and a
   // CTA keeps four k-blocks
   int share = 1;
@@ -325,8 +358,8 @@ cudaError_t launch(const CUtensorMap& map_w, const CUtensorMap& map_x, const bf*
          blocks <= resident_clusters(kern, 2 * share))
     share *= 2;
   Config k;
-  k.grid = dim3(blocks, share);
-  k.mp = linear_skinny_rows(M);
+  k.grid = dim3(sh.blocks, share, sh.tiles);
+  k.mp = sh.mp;
   // more blocks than SMs: two CTAs an SM, one filling its ring while the other
   // finishes
   k.stages = sk_stages(k.mp, blocks > sms && sk_sums_fit(k.mp, true));
@@ -334,31 +367,42 @@ cudaError_t launch(const CUtensorMap& map_w, const CUtensorMap& map_x, const bf*
   cudaLaunchAttribute attr[2];
   fill(cfg, attr, k, stream, pdl);
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, bias, resid, ldr, rs, out, ldo, pre, M, N, K,
-                            k.mp, k.stages, no_work, status, limit_ns);
+                            k.mp, k.stages, clear, no_work, status, limit_ns);
 }
 
 }  // namespace
 
-int linear_skinny_rows(int M) { return (M + 15) / 16 * 16; }
+SkinnyShape linear_skinny_shape(int M, int N, int K) {
+  SkinnyShape s;
+  s.tiles = (M + 255) / 256;
+  s.mp = ((M + s.tiles - 1) / s.tiles + 15) / 16 * 16;
+  s.tiles = (M + s.mp - 1) / s.mp;
+  s.blocks = (N + SK_ROWS - 1) / SK_ROWS;
+  const int units = s.blocks * s.tiles, kbs = (K + BK - 1) / BK;
+  s.share = 1;  // (of 152 SMs; the launch asks how many clusters are resident)
+  while (s.share < SK_MAX_SHARE && 2 * s.share * units <= 152 && kbs >= 8 * s.share) s.share *= 2;
+  return s;
+}
 
 cudaError_t launch_linear_skinny(const CUtensorMap& map_w, const CUtensorMap& map_x,
                                  const void* bias, const void* resid, int ldr, float rs, void* out,
-                                 int ldo, void* pre, int M, int N, int K, int act, int no_work,
-                                 int* status, unsigned long long limit_ns, cudaStream_t stream,
-                                 bool pdl) {
-  if (M < 1 || M > LINEAR_SKINNY_MAX_M) return cudaErrorInvalidValue;
+                                 int ldo, void* pre, int M, int N, int K, int act, bool w_mn,
+                                 bool clear, int no_work, int* status, unsigned long long limit_ns,
+                                 cudaStream_t stream, bool pdl) {
+  if (M < 1) return cudaErrorInvalidValue;
   const bf *b = static_cast<const bf*>(bias), *r = static_cast<const bf*>(resid);
   bf *o = static_cast<bf*>(out), *z = static_cast<bf*>(pre);
-#define MLP_SK(A)                                                                              \
-  launch<A>(map_w, map_x, b, r, ldr, rs, o, ldo, z, M, N, K, no_work, status, limit_ns, stream, \
-            pdl)
+#define MLP_SK(A, MN)                                                                         \
+  launch<A, MN>(map_w, map_x, b, r, ldr, rs, o, ldo, z, M, N, K, clear, no_work, status, limit_ns, \
+                stream, pdl)
+  if (w_mn) return act == ACT_NONE ? MLP_SK(ACT_NONE, true) : cudaErrorInvalidValue;
   switch (act) {
-    case ACT_SILU: return MLP_SK(ACT_SILU);
-    case ACT_RELU_SQ: return MLP_SK(ACT_RELU_SQ);
-    case ACT_GELU_HW: return MLP_SK(ACT_GELU_HW);
-    case ACT_RELU: return MLP_SK(ACT_RELU);
-    case ACT_SIGMOID: return MLP_SK(ACT_SIGMOID);
-    default: return MLP_SK(ACT_NONE);
+    case ACT_SILU: return MLP_SK(ACT_SILU, false);
+    case ACT_RELU_SQ: return MLP_SK(ACT_RELU_SQ, false);
+    case ACT_GELU_HW: return MLP_SK(ACT_GELU_HW, false);
+    case ACT_RELU: return MLP_SK(ACT_RELU, false);
+    case ACT_SIGMOID: return MLP_SK(ACT_SIGMOID, false);
+    default: return MLP_SK(ACT_NONE, false);
   }
 #undef MLP_SK
 }

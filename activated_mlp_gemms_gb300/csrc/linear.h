@@ -17,21 +17,20 @@ cudaError_t launch_linear_stream(const void* x, int ldx, const void* W, const vo
                                  void* pre, int M, int N, int K, int act, cudaStream_t stream,
                                  bool pdl, int* status);
 
-// The same for up to LINEAR_SKINNY_MAX_M rows, on the tensor cores with the
-// operands' places changed (k_linear_skinny.cu).  map_w: W [N, K] in boxes
-// {64, 128}; map_x: x [M, K] in boxes {64, linear_skinny_rows(M)}.  Clears
-// *status; no_work: the bounded waits run out (testing).
-constexpr int LINEAR_SKINNY_MAX_M = 256;
-int linear_skinny_rows(int M);
+// The same on the tensor cores with the operands' places changed
+// (k_linear_skinny.cu): CTAs of 128 features by up to 256 rows.  map_w: W [N, K]
+// in boxes {64, 128}; w_mn (dx = dz W, with ACT_NONE and no bias or residual):
+// W [K, N], N its contiguous features, in boxes {64, 64}; map_x: x [M, K] in boxes
+// {64, mp}.  clear: clears *status; no_work: the bounded waits run out (testing).
+struct SkinnyShape {
+  int blocks, tiles, mp;  // blocks of 128 features; tiles of mp rows
+  int share;              // CTAs that share a block's K, at most
+};
+SkinnyShape linear_skinny_shape(int M, int N, int K);
 cudaError_t launch_linear_skinny(const CUtensorMap& map_w, const CUtensorMap& map_x,
                                  const void* bias, const void* resid, int ldr, float rs, void* out,
-                                 int ldo, void* pre, int M, int N, int K, int act, int no_work,
-                                 int* status, unsigned long long limit_ns, cudaStream_t stream,
-                                 bool pdl);
-
-// The same epilogue on split-K sums acc fp32 [M, N].
-cudaError_t launch_linear_finish(const float* acc, const void* bias, const void* resid, int ldr,
-                                 float rs, void* out, int ldo, void* pre, int M, int N, int act,
+                                 int ldo, void* pre, int M, int N, int K, int act, bool w_mn,
+                                 bool clear, int no_work, int* status, unsigned long long limit_ns,
                                  cudaStream_t stream, bool pdl);
 
 // dz = dout * act'(pre) into dz (bf16 [M, N] dense; null: not written) and the

@@ -1,8 +1,7 @@
 // linear_api.cu -- the C entry points of mlp_linear.h: argument validation,
 // workspace layout and launch sequences.
-//   mlp_linear_fwd   one GEMM with the bias / activation / residual epilogue
-//                    (split K: fp32 sums, then the epilogue as its own pass;
-//                    up to eight rows: the weight stream)
+//   mlp_linear_fwd   one kernel with the bias / activation / residual epilogue: the
+//                    weight stream, the skinny kernel or the GEMM (route)
 //   mlp_linear_bwd   dz = dout act'(z) and the bias gradient's partial sums in
 //                    one pass (no activation: only those sums, dz is dout),
 //                    dx = dz W, and dW = dz^T x on the second stream beside it
@@ -40,34 +39,43 @@ int linear_act(int act) {
   }
 }
 
-// Whether the forward runs as the skinny kernel (unless a tile policy asks for
-// tiles): up to 192 rows always, up to 256 where N is at most 64 blocks of 128.
-// Measured (skinny / the better tiles): 192 x 14336 x 4096 28.8 / 30.6 us, 192 x
-// 2048 x 2048 11.6 / 16.5, 256 x 4096 x 4096 18.9 / 22.2, 256 x 14336 x 4096 33.2 /
-// 31.0.
-bool skinny(const mlp_linear_t* p) {
+// Which kernel a product [M, N] over K runs as: 128 x 256 tiles of single CTAs, 256
+// x 256 tiles of CTA pairs, or the skinny kernel's 128 features by up to 256 rows
+// with K shared by clusters.  (A tile policy of 1 or 2 asks for the first two.)
+// Up to 192 rows the skinny kernel; beyond that the least of three estimates, in
+// units of one 256 x 256 k-block of a pair (0.33 us): a pair's launch costs 4 more;
+// single-CTA MMAs draw more shared-memory bandwidth per flop, 15 % of the time; a
+// wave of the skinny kernel, whose CTAs are not persistent, 3, and the exchange
+// of the sums 6.  Rows that are no multiple of 128 bytes straddle L2 lines, and
+// those MMAs' larger share of loads costs 40 %.  Measured (skinny / singles / pairs, us): 300 x 4096 x 4096 16.5
+// / 27.0 / 27.0, 512 x 2048 x 8192 22.8 / 27.6 / 28.5, 588 x 14336 x 4096 74 / 57.7
+// / 70, 1683 x 1024 x 1024 - / 10.7 / 12.3, 4096 x 4096 x 4096 - / 104 / 91.
+enum Route { ROUTE_SINGLES = 1, ROUTE_PAIRS = 2, ROUTE_SKINNY = 3 };
+Route route(int M, int N, int K, bool whole_lines) {
   const int pol = g_tile_policy.load();
-  if (pol != 0 && pol != 3) return false;
-  return p->M <= 192 || (p->M <= LINEAR_SKINNY_MAX_M && p->N <= 64 * 128);
+  if (pol == 1 || pol == 2) return static_cast<Route>(pol);
+  if (M <= 192) return ROUTE_SKINNY;
+  const SkinnyShape s = linear_skinny_shape(M, N, K);
+  const double kbs = (K + BK - 1) / BK, loads = whole_lines ? 1.15 : 1.4;
+  auto waves = [](long long units, int slots) { return (double)((units + slots - 1) / slots); };
+  const double pairs = waves(out_tiles(M, N, 2), 76) * kbs + 4;
+  const double singles = loads * waves(out_tiles(M, N, 1), 152) * kbs;
+  const double skinny = waves((long long)s.blocks * s.tiles * s.share, 152) *
+                            (loads * kbs / s.share * s.mp / 256 + 3) + (s.share > 1 ? 6 : 0);
+  if (skinny < pairs && skinny < singles) return ROUTE_SKINNY;
+  return singles < pairs ? ROUTE_SINGLES : ROUTE_PAIRS;
 }
 
-// The workspace after the control block.
+// The workspace after the control block: the backward's dz and the bias
+// gradient's partial sums.
 struct Layout {
-  int split;                      // split-K factor of the forward's GEMM, or of dx
-  size_t part, dz, db, total;     // split-K sums, dz, the bias gradient's partial sums
+  size_t dz, db, total;
 };
 Layout layout(const mlp_linear_t* p, bool backward) {
   Layout L = {};
-  const size_t mn = (size_t)p->M * p->N, mk = (size_t)p->M * p->K;
   size_t at = CTRL_BYTES;
-  // (dx is left whole from 33 tiles on: its last wave runs beside dW)
-  L.split = backward                        ? bf16_split(p->M, p->K, p->N, false)
-            : p->M <= LINEAR_STREAM_MAX_M ? 1
-                                          : bf16_split(p->M, p->N, p->K, true);
-  L.part = at;
-  if (L.split > 1) at += round256((backward ? mk : mn) * 4);
   L.dz = at;
-  if (backward && p->act != MLP_LINEAR_NONE) at += round256(mn * 2);
+  if (backward && p->act != MLP_LINEAR_NONE) at += round256((size_t)p->M * p->N * 2);
   L.db = at;
   if (backward) at += round256((size_t)linear_db_chunks(p->M, p->N) * p->N * 4);
   L.total = at;
@@ -111,15 +119,13 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
   const int ldx = p->ldx ? p->ldx : K, ldr = p->ldr ? p->ldr : N, ldo = p->ldo ? p->ldo : N;
   const bool streamed = M <= LINEAR_STREAM_MAX_M;
-  const bool tiles = !streamed && !skinny(p);
-  const int cg = pick_cg(M);
+  const Route way = streamed ? ROUTE_SKINNY : route(M, N, K, ldx % 64 == 0 && K % 64 == 0);
+  const bool tiles = way != ROUTE_SKINNY;
   Call c;
-  // (one wave: 22.7 -> 18.9 us for 777 x 4864 x 2048; the stream and the skinny
-  // kernel use no counter and clear the status word themselves)
-  if (!tiles || (L.split == 1 && out_tiles(M, N, cg) <= one_wave_units(cg)))
-    begin_one_wave(c, ws, stream, tiles);
-  else
-    MLP_TRY(begin_call(c, ws, stream));
+  // (one wave of tiles: 22.7 -> 18.9 us for 777 x 4864 x 2048; the stream and the
+  // skinny kernel use no counter and clear the status word themselves)
+  if (!tiles || out_tiles(M, N, way) <= one_wave_units(way)) begin_one_wave(c, ws, stream, tiles);
+  else MLP_TRY(begin_call(c, ws, stream));
   if (streamed) {
     const bool pdl = c.pdl();
     return traced(MLP_KERNEL_LINEAR, c.stream, [&] {
@@ -127,38 +133,22 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
                                   pre_save, M, N, K, act, c.stream, pdl, c.status);
     });
   }
-  if (skinny(p)) {
+  if (!tiles) {
     CUtensorMap map_w, map_x;
     if (!make_map(&map_w, W, K, N, K, BK, 128) ||
-        !make_map(&map_x, x, K, M, ldx, BK, linear_skinny_rows(M)))
+        !make_map(&map_x, x, K, M, ldx, BK, linear_skinny_shape(M, N, K).mp))
       return MLP_ERR_CUDA;
     const bool pdl = c.pdl();
     return traced(MLP_KERNEL_LINEAR, c.stream, [&] {
       return launch_linear_skinny(map_w, map_x, bias, residual, ldr, p->resid_scale, out, ldo,
-                                  pre_save, M, N, K, act, g_debug_flags.load() & MLP_DEBUG_NO_WORK,
-                                  c.status, wait_limit_ns(), c.stream, pdl);
+                                  pre_save, M, N, K, act, false, true,
+                                  g_debug_flags.load() & MLP_DEBUG_NO_WORK, c.status,
+                                  wait_limit_ns(), c.stream, pdl);
     });
   }
-  Gemm g(act, 1.f, c.counter(), c.status, cg);
+  Gemm g(act, 1.f, c.counter(), c.status, way);
   const int mA = g.kmajor_a(x, M, K, ldx);
   const int mB = g.kmajor(W, N, K, g.b_rows());
-  if (L.split > 1) {
-    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part);
-    MLP_TRY(cuda_err(cudaMemsetAsync(part, 0, (size_t)M * N * 4, c.stream)));
-    const int oP = g.output(part, M, N, true);
-    Prob& P = g.add(M, N, K, 0, MMA_N, L.split);
-    P.l2a = L2_EVICT_LAST;   // x: re-read by every tile column
-    P.l2b = L2_EVICT_FIRST;  // the weights
-    P.mapA0 = mA;
-    P.mapB0 = mB;
-    P.mapO[0] = oP;
-    MLP_TRY((run<EPI_ACCUM_F32, false, false>(g, c, MLP_KERNEL_LINEAR)));
-    const bool pdl = c.pdl();
-    return traced(MLP_KERNEL_LINEAR_FINISH, c.stream, [&] {
-      return launch_linear_finish(part, bias, residual, ldr, p->resid_scale, out, ldo, pre_save, M,
-                                  N, act, c.stream, pdl);
-    });
-  }
   const int oO = g.output(out, M, N, false, ldo);
   const int oZ = g.output(pre_save, M, N);
   Prob& P = g.add(M, N, K, 0, MMA_N);
@@ -204,18 +194,17 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
   const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
   const int ldx = p->ldx ? p->ldx : K, ldd = p->ldo ? p->ldo : N;
   char* base = static_cast<char*>(ws);
-  const bool split = dx && L.split > 1;
-  const int cgx = pick_cg(M), cgw = pick_cg(N < K ? N : K);
+  const Route way = route(M, K, N, ldd % 64 == 0 && K % 64 == 0);  // dx
+  const bool skinny_dx = dx && way == ROUTE_SKINNY;
+  const int cgx = skinny_dx ? 1 : way, cgw = pick_cg(N < K ? N : K);
   // dz_out or db: the derivative pass comes first and clears the status word
   const bool pass = (has_act && (dx || dW)) || db;
   Call c;
-  if (!split && (!dx || out_tiles(M, K, cgx) <= one_wave_units(cgx)) &&
+  if ((!dx || skinny_dx || out_tiles(M, K, cgx) <= one_wave_units(cgx)) &&
       (!dW || (!fuse && out_tiles(N, K, cgw) <= one_wave_units(cgw))))
     begin_one_wave(c, ws, stream, !pass);
   else
     MLP_TRY(begin_call(c, ws, stream));
-  float* part = reinterpret_cast<float*>(base + L.part);
-  if (split) MLP_TRY(cuda_err(cudaMemsetAsync(part, 0, (size_t)M * K * 4, c.stream)));
 
   const void* dz = dout;
   int ldz = ldd;
@@ -243,23 +232,31 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
     side_lk = std::unique_lock<std::mutex>(side->mu);
     MLP_TRY(cuda_err(cudaEventRecord(side->fork, c.stream)));
   }
-  if (dx) {
+  if (skinny_dx) {
+    CUtensorMap map_w, map_z;
+    if (!make_map(&map_w, W, K, N, K, 64, BK) ||
+        !make_map(&map_z, dz, N, M, ldz, BK, linear_skinny_shape(M, K, N).mp))
+      return MLP_ERR_CUDA;
+    const bool pdl = c.pdl();
+    MLP_TRY(traced(MLP_KERNEL_DX, c.stream, [&] {
+      return launch_linear_skinny(map_w, map_z, nullptr, nullptr, 0, 0.f, dx, K, nullptr, M, K, N,
+                                  ACT_NONE, true, c.clear_status,
+                                  g_debug_flags.load() & MLP_DEBUG_NO_WORK, c.status,
+                                  wait_limit_ns(), c.stream, pdl);
+    }));
+    c.clear_status = false;
+  } else if (dx) {
     Gemm g(act, 1.f, c.counter(), c.status, cgx);
     const int mA = g.kmajor_a(dz, M, N, ldz);
     const int mB = g.mnmajor(W, N, K);  // W [N,K]: B(n=k, k=n) is contiguous along K
-    const int oX = split ? g.output(part, M, K, true) : g.output(dx, M, K);
-    Prob& P = g.add(M, K, N, 0, MMA_N, split ? L.split : 1);
+    const int oX = g.output(dx, M, K);
+    Prob& P = g.add(M, K, N, 0, MMA_N);
     P.l2a = L2_EVICT_LAST;   // dz: re-read by every tile column
     P.l2b = L2_EVICT_FIRST;  // W
     P.mapA0 = mA;
     P.mapB0 = mB;
     P.mapO[0] = oX;
-    if (split) {
-      MLP_TRY((run<EPI_ACCUM_F32, false, true>(g, c, MLP_KERNEL_DX)));
-      MLP_TRY(convert_out(c, part, dx, (long long)M * K));
-    } else {
-      MLP_TRY((run<EPI_STORE_BF16, false, true>(g, c, MLP_KERNEL_DX)));
-    }
+    MLP_TRY((run<EPI_STORE_BF16, false, true>(g, c, MLP_KERNEL_DX)));
   }
   if (dW || db_left) {
     Call cw = c;

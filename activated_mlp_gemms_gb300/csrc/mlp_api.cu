@@ -915,7 +915,6 @@ const char* mlp_kernel_name(int tag) {
     case MLP_KERNEL_MOE_COMBINE: return "moe_combine";
     case MLP_KERNEL_MOE_COMBINE_BWD: return "moe_combine_bwd";
     case MLP_KERNEL_LINEAR: return "linear";
-    case MLP_KERNEL_LINEAR_FINISH: return "linear_finish";
     case MLP_KERNEL_LINEAR_DACT: return "linear_dact";
     case MLP_KERNEL_LINEAR_DB: return "linear_db";
     default: return "unknown";

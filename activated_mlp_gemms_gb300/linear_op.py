@@ -62,6 +62,9 @@ def _pitched(t, shape, name):
     """(address, row pitch or 0 when dense) of a bf16 matrix with unit column stride."""
     if t is None:
         return None, 0
+    if (t.__class__ is torch.Tensor and t.dtype is torch.bfloat16 and t.is_cuda
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr(), 0
     if not isinstance(t, torch.Tensor) or t.is_contiguous():
         return _dense(t, shape, name), 0
     if not t.is_cuda or t.dtype != torch.bfloat16:
@@ -111,14 +114,15 @@ def mlp_linear_fwd(p: Linear, x, W, bias, residual, out, pre_save=None, ws=None,
     pre_save (bf16 [M, N]) receives x W^T + bias for the backward of an activation.
     Returns the workspace used (given none, a small one that later calls of this thread on
     this stream use too)."""
-    xp, ldx = _pitched(x, (p.M, p.K), "x")
-    rp, ldr = _pitched(residual, (p.M, p.N), "residual")
-    op, ldo = _pitched(out, (p.M, p.N), "out")
+    M, N, K = p.M, p.N, p.K
+    xp, ldx = _pitched(x, (M, K), "x")
+    rp, ldr = _pitched(residual, (M, N), "residual")
+    op, ldo = _pitched(out, (M, N), "out")
     q = _problem(p, ldx, ldr, ldo)
     ws = _ws(ws, q, False, out.device, stream)
-    rc = lib().mlp_linear_fwd(ctypes.byref(q), xp, _dense(W, (p.N, p.K), "W"),
-                              _dense(bias, (p.N,), "bias"), rp, op,
-                              _dense(pre_save, (p.M, p.N), "pre_save"), ws.data_ptr(), ws.numel(),
+    rc = lib().mlp_linear_fwd(ctypes.byref(q), xp, _dense(W, (N, K), "W"),
+                              _dense(bias, (N,), "bias"), rp, op,
+                              _dense(pre_save, (M, N), "pre_save"), ws.data_ptr(), ws.numel(),
                               _stream(stream))
     _check(rc, "mlp_linear_fwd")
     return ws

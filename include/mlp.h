@@ -472,9 +472,8 @@ typedef enum {
   MLP_KERNEL_MOE_COMBINE_BWD = 16, /* its gradients */
   /* mlp_linear.h */
   MLP_KERNEL_LINEAR = 17,          /* the linear layer with its epilogue (GEMM or weight stream) */
-  MLP_KERNEL_LINEAR_FINISH = 18,   /* its epilogue on split-K sums */
-  MLP_KERNEL_LINEAR_DACT = 19,     /* dz and the bias gradient's partial sums */
-  MLP_KERNEL_LINEAR_DB = 20        /* the bias gradient from its partial sums */
+  MLP_KERNEL_LINEAR_DACT = 18,     /* dz and the bias gradient's partial sums */
+  MLP_KERNEL_LINEAR_DB = 19        /* the bias gradient from its partial sums */
 } mlp_kernel_t;
 
 /* on != 0 starts recording, 0 stops (records already taken are kept). */

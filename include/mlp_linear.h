@@ -52,10 +52,10 @@ size_t mlp_linear_workspace_size(const mlp_linear_t* p, int backward);
  *             activation needs (with MLP_LINEAR_NONE it is not)
  * With one to eight rows the weights are streamed on the warp-level MMA; up to
  * a few hundred run on the tensor cores with the weight rows as the MMA's M
- * (K shared by a cluster of CTAs where N alone gives too few); more rows run
- * as 128 x 256 or 256 x 256 output tiles.  A tile policy (mlp_set_tile_policy)
- * of 1 or 2 keeps every size above eight rows on those tiles, which split K
- * when there are too few of them to fill the GPU. */
+ * (K shared by a cluster of CTAs where the blocks alone are too few); more rows
+ * run as 128 x 256 or 256 x 256 output tiles.  A tile policy
+ * (mlp_set_tile_policy) of 1 or 2 keeps every size above eight rows on those
+ * tiles.  Two calls with the same operands and policy give the same bits. */
 int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const void* bias,
                    const void* residual, void* out, void* pre_save, void* ws, size_t ws_bytes,
                    void* stream);
