@@ -8,7 +8,10 @@ streams.  The functions carry the names of the C ABI (include/mlp.h):
     mlp_status_string, mlp_device_status, mlp_version
 
 and mlp_func (module `autograd`) is the same forward and backward as one
-differentiable PyTorch function.
+differentiable PyTorch function.  The linear layer (module `linear_op`,
+include/mlp_linear.h) and the mixture of experts (module `experts`,
+include/mlp_moe.h) have the same forms: calls on given tensors, and linear_func
+and moe_func.
 
 Tensors are CUDA, contiguous, bf16 (fp32 for accumulated weight gradients),
 with x [M,H], Wg/Wu [I,H], Wd [H,I].  A missing library raises at the first

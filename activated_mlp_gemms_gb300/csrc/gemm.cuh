@@ -20,6 +20,15 @@
 // The double-buffered accumulator lets the epilogue of tile t overlap the
 // MMAs of tile t+1.  Every wait is bounded (globaltimer); on expiry the
 // kernel records MLP_ERR_TIMEOUT in the status word and unwinds.
+// EPI_LINEAR is the linear layer's: bias, activation and residual on the way out.
+// GRP runs the GEMMs of a mixture of experts over the rows of the sorted layout:
+// a unit is a row tile of one expert against that expert's matrix of a weight
+// stack (3-D tensor maps), rows past the expert's end are neither stored nor read
+// by the epilogue, and a weight gradient sums over its expert's rows (whole K steps
+// of 16).  Measured, 16384 rows over 16 experts of 1024, 2048 x 4864: gate/up 413 us
+// (394 as one dense GEMM), down 190 (180), dgated 258 (250), dx 370 (362), weight
+// gradients 715 (530: 956 MB of gradients go out at HBM's write rate, and a unit's
+// sum is 16 k-blocks, 1.2 us of pipeline restart on 5.3 us of MMAs).
 // EPI_FWD_FUSED runs the gated forward's two GEMMs in one launch: the
 // epilogue warps count their stored gate/up tiles per 256-row block, and the
 // producer of a down-projection unit waits for its block's count.

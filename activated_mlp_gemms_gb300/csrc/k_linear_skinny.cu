@@ -17,6 +17,9 @@
 // waited for each round: 26 against 15 us for 160 x 1024 x 8192.)  No partial
 // sums in global memory, no atomics: the same bits on every run.
 //
+// Measured: 48 x 14336 x 4096 23.3 us (5.1 TB/s), 16 x 4096 x 4096 10, 300 x 4096 x
+// 4096 16 (27 as 256 x 256 tiles), 6740 x 592 x 2016 17.7 (33).
+//
 // Warp 0 feeds the ring by TMA, warp 1 issues tcgen05.mma, warps 2-9 move the
 // accumulator (lane = feature) to shared memory; all ten finish rows, 8 features
 // (16 bytes) of two rows a thread at a time.

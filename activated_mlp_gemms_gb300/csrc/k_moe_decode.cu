@@ -19,7 +19,11 @@
 //                      items when H alone gives too few CTAs, and its first
 //                      CTA adds the others' sums in order, then the residual.
 //
-// HBM-bound: the weights are read once, everything else is small.
+// HBM-bound: the weights are read once, everything else is small.  One token
+// through 8 of 64 experts of 2048 x 1408 (138 MB): 33 us, of which about 9 are the
+// two kernels' starts and ends; from there on 5.8 TB/s.  (Sixteen warps an SM,
+// each two load groups ahead, because fewer draw less of HBM: eight took 35 us,
+// twelve with the down kernel's warps beside them 36.)
 #include <atomic>
 
 #include "act.cuh"

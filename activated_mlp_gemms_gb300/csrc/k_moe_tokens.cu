@@ -4,7 +4,9 @@
 //                      (without weights: the gradient of the dispatch)
 //   k_moe_combine_bwd  dy[pos[t, j]] = w[t, j] dout[t] (zeros in the other
 //                      rows), dw[t, j] = sum_h dout[t, h] y[pos[t, j], h]
-// All are bound by HBM: every row is read once and written once.  The work
+// All are bound by HBM: every row is read once and written once.  Measured with
+// 8192 tokens of 2048 and 8 slots each: dispatch 47 us (6.4 TB/s), combine 46 (6.7),
+// its gradients 91 (6.3); with 2 slots 6.1, 6.1 and 5.7 TB/s.  The work
 // goes by token, not by sorted row, so that a token's row (or its gradient)
 // is read once for all its slots and the sum over its slots needs no atomic
 // (the same bits on every run).  Sums are fp32 and rounded once.
