@@ -150,18 +150,10 @@ __device__ __forceinline__ Work unit_work(const Params& p, const UnitKey& k) {
   return w;
 }
 
-// Decodes a unit number: the kernels whose ring carries those.
-template <bool GRP_SUM, int TILE_M>
-__device__ __forceinline__ Work decode(const Params& p, int unit) {
-  if constexpr (GRP_SUM) return unit_work<true, TILE_M>(p, unit_key<true>(p, unit));
-  else return decode_unit(p, unit);
-}
-
-// GRP over rows: the ring carries decoded units, so that only the leader's
-// producer decodes, ahead of time (before, its peer and the MMA issuer did too,
-// between one unit's last k-block and the next one's first: 2-4 % of the down
-// projection and dx).  The weight gradients lost 3-4 % this way, at every
-// length of their sums, and keep a ring of unit numbers.
+// GRP: the ring carries decoded units, so that only the leader's producer
+// decodes, ahead of time (before, its peer and the MMA issuer did too, between
+// one unit's last k-block and the next one's first: 2-4 % of the down projection
+// and dx).
 struct alignas(16) RingUnit {
   int prob, tm, tn, kb_end;  // prob < 0: no more work
   int expert, row0, row_end, pad;
@@ -1269,7 +1261,8 @@ __device__ __forceinline__ UnitLoads unit_loads(const Params& p, const Prob& P, 
 //   B MN-major (Wd, W2_8).
 //   GRP: the weights (B, when A is K-major) are a stack, loaded at L.expert;
 //   the weight gradients' operands start at K row L.krow0.
-template <int EPI, bool A_MN, bool B_MN, int CG, bool GRP = false>
+//   PART: 0 both operands, 1 A, 2 B.
+template <int EPI, bool A_MN, bool B_MN, int CG, bool GRP = false, int PART = 0>
 __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, uint32_t sA,
                                            uint32_t sB, uint32_t full, uint64_t polA,
                                            uint64_t polB) {
@@ -1285,7 +1278,9 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
   };
   if constexpr (GRP && A_MN) kc += L.krow0;
   const CUtensorMap* mA = seg == 0 ? L.a0 : L.a1;
-  if constexpr (!A_MN) {
+  if constexpr (PART == 2) {
+    // B only
+  } else if constexpr (!A_MN) {
     ld(sA, mA, kc, L.m0);
   } else if constexpr (is_f8(EPI)) {
     ld(sA, mA, L.m0, kc);
@@ -1294,7 +1289,9 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
     ld(sA + 8192, mA, L.m0 + 64, kc);
   }
   pol = polB;
-  if constexpr (EPI == EPI_GATED_FWD) {
+  if constexpr (PART == 1) {
+    // A only
+  } else if constexpr (EPI == EPI_GATED_FWD) {
     ldw(sB, L.b0, kc, L.n0);
     if constexpr (CG == 1) ldw(sB + 16384, L.b1, kc, L.n0);
   } else {
@@ -1313,9 +1310,17 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
   }
 }
 
+// The experts' weight gradients load B with an eleventh warp.  A k-block of two
+// MN-major operands is four TMA instructions, and one thread issues them in 374 of
+// the k-block's 600 cycles (measured); what it spends between two units (about
+// 3100 cycles) it could not catch up within an expert's few k-blocks, and every
+// unit's first MMAs waited 2200-3800 cycles for their operands.
+template <bool A_MN, bool GRP>
+constexpr int gemm_threads() { return NUM_THREADS + (A_MN && GRP ? 32 : 0); }
+
 // ACT: the activation of the activation epilogues (Act; 0 for the others).
 template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP>
-__global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(gemm_threads<A_MN, GRP>(), 1) k_mlp_gemm(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   using C = Cfg<EPI, CG, GRP>;
   constexpr bool PAIR = CG == 2;
@@ -1345,7 +1350,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
   constexpr int EBAR = DRAIN + 1;
   constexpr int NBAR = EBAR + 2 * NUM_EPI_WARPS;
   // the unit ring: unit numbers, or decoded units
-  constexpr bool RING = GRP_ROWS;
+  constexpr bool RING = GRP;
   constexpr int RING_AT = RING ? (8 * NBAR + 15) / 16 * 16 : 8 * NBAR;
   constexpr int RING_BYTES = SCHED_SLOTS * static_cast<int>(RING ? sizeof(RingUnit) : sizeof(int));
   static_assert(RING_AT + RING_BYTES + 8 <= 1024, "control area");
@@ -1375,7 +1380,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
     for (int i = 0; i < SCHED_SLOTS; ++i) {
       mbar_init(bar_s(SFULL + i), 1);
       // MMA issuer + every epilogue warp of the pair + the peer's producer
-      mbar_init(bar_s(SEMPTY + i), 1 + CG * NUM_EPI_WARPS + (CG - 1));
+      // (+ the warps that load B)
+      mbar_init(bar_s(SEMPTY + i), 1 + CG * NUM_EPI_WARPS + (CG - 1) + (GRP_SUM ? CG : 0));
     }
     mbar_init(bar_s(DRAIN), 1);
     if constexpr (EPI == EPI_DGRAD_F8)
@@ -1458,7 +1464,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         Work w{};
         bool valid = unit < total_units;
         if (leader && !publish_nothing) {
-          if (valid) w = unit_work<false, C::TILE_M>(p, unit_key<false>(p, unit));
+          if (valid) w = unit_work<A_MN, C::TILE_M>(p, unit_key<A_MN>(p, unit));
           ok = publish(w, valid);
         }
         while (ok && !publish_nothing) {
@@ -1487,10 +1493,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           int step = 0;  // of the next unit: 1 its key is being loaded, 2 published
           auto advance = [&]() -> bool {
             if (++step == 1) {
-              if (next_valid) key = unit_key<false>(p, next);
+              if (next_valid) key = unit_key<A_MN>(p, next);
               return true;
             }
-            if (next_valid) nw = unit_work<false, C::TILE_M>(p, key);
+            if (next_valid) nw = unit_work<A_MN, C::TILE_M>(p, key);
             return publish(nw, next_valid);
           };
           const int mid = w.kb_end / 2;
@@ -1507,8 +1513,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             const int seg = kb < L.kb0 ? 0 : 1;
             const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
             const uint32_t sA = base_s + stage * C::STAGE;
-            load_stage<EPI, A_MN, B_MN, CG, GRP>(L, seg, kc, sA, sA + C::A_BYTES, full,
-                                                 pol_of(L.l2a), pol_of(L.l2b));
+            load_stage<EPI, A_MN, B_MN, CG, GRP, GRP_SUM ? 1 : 0>(
+                L, seg, kc, sA, sA + C::A_BYTES, full, pol_of(L.l2a), pol_of(L.l2b));
             ++issued;
             if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
             if (leader && (kb == mid || kb == mid + 1) && !advance()) {
@@ -1552,7 +1558,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             }
           }
           if (unit >= total_units) break;
-          const Work w = decode<GRP_SUM, C::TILE_M>(p, unit);
+          const Work w = decode_unit(p, unit);
           // The next unit, fetched now and needed when it is published.  A
           // down unit of the fused forward (K = I, several times a gate/up
           // unit's length) fetches it only when it publishes it, half-way
@@ -1569,7 +1575,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             if (late_claim) next = atomicAdd(p.counter, 1);
           };
           bool published = !EARLY_PUB;
-          const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
+          const UnitLoads L = unit_loads<EPI, CG>(p, p.prob[w.prob], w, rank);
           if constexpr (EpiTraits<EPI>::DACT) {
             // the epilogue reads this tile's saved inputs a tile or two later
             if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
@@ -1594,7 +1600,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             const int seg = kb < L.kb0 ? 0 : 1;
             const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
             const uint32_t sA = base_s + stage * C::STAGE;
-            load_stage<EPI, A_MN, B_MN, CG, GRP>(L, seg, kc, sA, sA + C::A_BYTES, full,
+            load_stage<EPI, A_MN, B_MN, CG>(L, seg, kc, sA, sA + C::A_BYTES, full,
                                             pol_of(L.l2a), pol_of(L.l2b));
             ++issued;
             if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
@@ -1622,8 +1628,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
           mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           if (v < 0) break;
-          const Work w = decode<GRP_SUM, C::TILE_M>(p, v);
-          const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
+          const Work w = decode_unit(p, v);
+          const UnitLoads L = unit_loads<EPI, CG>(p, p.prob[w.prob], w, rank);
           if constexpr (EpiTraits<EPI>::DACT) {
             if (L.i0) tma_prefetch_l2_2d(L.i0, L.icol, L.m0);
             if (L.i1) tma_prefetch_l2_2d(L.i1, L.icol, L.m0);
@@ -1643,7 +1649,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
             const int seg = kb < L.kb0 ? 0 : 1;
             const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
             const uint32_t sA = base_s + stage * C::STAGE;
-            load_stage<EPI, A_MN, B_MN, CG, GRP>(L, seg, kc, sA, sA + C::A_BYTES,
+            load_stage<EPI, A_MN, B_MN, CG>(L, seg, kc, sA, sA + C::A_BYTES,
                                             full_lead + 8u * stage, pol_of(L.l2a),
                                             pol_of(L.l2b));
             ++issued;
@@ -1700,7 +1706,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         mbar_arrive(bar_s(SEMPTY + slot));
         if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
         if (unit < 0) break;
-        if constexpr (!RING) w = decode<GRP_SUM, C::TILE_M>(p, unit);
+        if constexpr (!RING) w = decode_unit(p, unit);
         // the fused recompute's second K segment goes to the other accumulator
         const int kswitch = is_recomp(EPI) ? p.prob[w.prob].kb0 : -1;
         if (!mbar_wait<PAIR>(bar_s(TEMPTY + acc), aphase ^ 1u, lim, abort_flag)) { ok = false; break; }
@@ -1772,6 +1778,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
         }
       }
     }
+  } else if (GRP_SUM && warp == NUM_THREADS / 32) {
+    // ------------------------------------------- the B loads (see gemm_threads)
+    if (lane == 0) {
+      const uint64_t pol_n = policy_evict_normal(), pol_l = policy_evict_last(),
+                     pol_f = policy_evict_first();
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, sphase = 0;
+      bool ok = true;
+      const uint32_t full0 = leader ? bar_s(FULL) : lead(bar_s(FULL));
+      while (ok) {
+        if (!mbar_wait<PAIR>(bar_s(SFULL + slot), sphase, lim, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const Work w = ring_get(ring_s(slot));
+        if (leader) mbar_arrive(bar_s(SEMPTY + slot));
+        else mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
+        if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
+        if (w.prob < 0) break;
+        const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
+        const uint64_t pol = L.l2b == 1 ? pol_l : L.l2b == 2 ? pol_f : pol_n;
+        for (int kb = w.kb_begin; kb < w.kb_end; ++kb) {
+          if (!mbar_wait<PAIR>(bar_s(EMPTY + stage), phase ^ 1u, lim, abort_flag)) {
+            ok = false;
+            break;
+          }
+          // (the bytes are those that the leader's first warp expects)
+          const uint32_t sA = base_s + stage * C::STAGE;
+          load_stage<EPI, A_MN, B_MN, CG, GRP, 2>(L, 0, kb * KE, sA, sA + C::A_BYTES,
+                                                  full0 + 8u * stage, pol, pol);
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        record_timeout(p, abort_flag);
+        __nanosleep(100000);  // its copies signal the leader's barriers
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;            // TMEM lane quadrant this warp may access
@@ -1824,7 +1868,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mlp_gemm(const __grid_consta
       }
       if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
       if (unit < 0) break;
-      if constexpr (!RING) w = decode<GRP_SUM, C::TILE_M>(p, unit);
+      if constexpr (!RING) w = decode_unit(p, unit);
       const int pi = w.prob;
       EpiUnit P = epi_unit<EPI>(p, p.prob[pi],
                                       pi == 0 ? f8_deq[0] : pi == 1 ? f8_deq[1] : f8_deq[2],
@@ -1975,7 +2019,7 @@ cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.blockDim = dim3(gemm_threads<A_MN, GRP>(), 1, 1);
   cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -2010,7 +2054,7 @@ int max_groups() {
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
-  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.blockDim = dim3(gemm_threads<A_MN, GRP>(), 1, 1);
   cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
