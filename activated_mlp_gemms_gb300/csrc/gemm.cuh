@@ -26,9 +26,10 @@
 // stack (3-D tensor maps), rows past the expert's end are neither stored nor read
 // by the epilogue, and a weight gradient sums over its expert's rows (whole K steps
 // of 16).  Measured, 16384 rows over 16 experts of 1024, 2048 x 4864: gate/up 413 us
-// (394 as one dense GEMM), down 190 (180), dgated 258 (250), dx 370 (362), weight
-// gradients 715 (530: 956 MB of gradients go out at HBM's write rate, and a unit's
-// sum is 16 k-blocks, 1.2 us of pipeline restart on 5.3 us of MMAs).
+// (394 as one dense GEMM), down 190 (180), dgated 258 (250), dx 362 (362), weight
+// gradients 641 (530 for the same sums over one expert's 16384 rows: here 956 MB of
+// gradients go out at HBM's write rate, after sums of 16 k-blocks each; without
+// their epilogue 538).
 // EPI_FWD_FUSED runs the gated forward's two GEMMs in one launch: the
 // epilogue warps count their stored gate/up tiles per 256-row block, and the
 // producer of a down-projection unit waits for its block's count.
@@ -1310,17 +1311,20 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
   }
 }
 
-// The experts' weight gradients load B with an eleventh warp.  A k-block of two
-// MN-major operands is four TMA instructions, and one thread issues them in 374 of
-// the k-block's 600 cycles (measured); what it spends between two units (about
-// 3100 cycles) it could not catch up within an expert's few k-blocks, and every
-// unit's first MMAs waited 2200-3800 cycles for their operands.
-template <bool A_MN, bool GRP>
-constexpr int gemm_threads() { return NUM_THREADS + (A_MN && GRP ? 32 : 0); }
+// The experts' GEMMs with an MN-major B load it with an eleventh warp.  A weight
+// gradient's k-block is four TMA instructions (six for a single CTA), and one
+// thread issued them in 374 of the k-block's 600 cycles; what it spent between two
+// units (about 3100 cycles) it could not catch up within an expert's few
+// k-blocks, and every unit's first MMAs waited 2200-3800 cycles for their
+// operands (all measured).  With the second warp, and units decoded ahead, they take
+// 641 us in place of 714 (see above), and dx and dgated on single CTAs 405 and 272
+// in place of 444 and 293 (on pairs 362 for 373, and 266 both).
+template <bool B_MN, bool GRP>
+constexpr int gemm_threads() { return NUM_THREADS + (B_MN && GRP ? 32 : 0); }
 
 // ACT: the activation of the activation epilogues (Act; 0 for the others).
 template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP>
-__global__ void __launch_bounds__(gemm_threads<A_MN, GRP>(), 1) k_mlp_gemm(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   using C = Cfg<EPI, CG, GRP>;
   constexpr bool PAIR = CG == 2;
@@ -1329,6 +1333,7 @@ __global__ void __launch_bounds__(gemm_threads<A_MN, GRP>(), 1) k_mlp_gemm(const
                 "no grouped form of this epilogue");
   constexpr bool GRP_ROWS = GRP && !A_MN;  // output tiles are the plan's row tiles
   constexpr bool GRP_SUM = GRP && A_MN;    // every expert's own sum over its rows
+  constexpr bool B_WARP = GRP && B_MN;     // a warp of its own loads B (gemm_threads)
   // 8-bit operands: a 128-byte k-block row holds 128 elements (bf16: 64)
   constexpr bool F8 = is_f8(EPI);
   constexpr int KE = F8 ? 2 * BK : BK;
@@ -1381,7 +1386,7 @@ __global__ void __launch_bounds__(gemm_threads<A_MN, GRP>(), 1) k_mlp_gemm(const
       mbar_init(bar_s(SFULL + i), 1);
       // MMA issuer + every epilogue warp of the pair + the peer's producer
       // (+ the warps that load B)
-      mbar_init(bar_s(SEMPTY + i), 1 + CG * NUM_EPI_WARPS + (CG - 1) + (GRP_SUM ? CG : 0));
+      mbar_init(bar_s(SEMPTY + i), 1 + CG * NUM_EPI_WARPS + (CG - 1) + (B_WARP ? CG : 0));
     }
     mbar_init(bar_s(DRAIN), 1);
     if constexpr (EPI == EPI_DGRAD_F8)
@@ -1513,7 +1518,7 @@ __global__ void __launch_bounds__(gemm_threads<A_MN, GRP>(), 1) k_mlp_gemm(const
             const int seg = kb < L.kb0 ? 0 : 1;
             const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
             const uint32_t sA = base_s + stage * C::STAGE;
-            load_stage<EPI, A_MN, B_MN, CG, GRP, GRP_SUM ? 1 : 0>(
+            load_stage<EPI, A_MN, B_MN, CG, GRP, B_WARP ? 1 : 0>(
                 L, seg, kc, sA, sA + C::A_BYTES, full, pol_of(L.l2a), pol_of(L.l2b));
             ++issued;
             if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
@@ -1778,7 +1783,7 @@ __global__ void __launch_bounds__(gemm_threads<A_MN, GRP>(), 1) k_mlp_gemm(const
         }
       }
     }
-  } else if (GRP_SUM && warp == NUM_THREADS / 32) {
+  } else if (B_WARP && warp == NUM_THREADS / 32) {
     // ------------------------------------------- the B loads (see gemm_threads)
     if (lane == 0) {
       const uint64_t pol_n = policy_evict_normal(), pol_l = policy_evict_last(),
@@ -1806,8 +1811,9 @@ __global__ void __launch_bounds__(gemm_threads<A_MN, GRP>(), 1) k_mlp_gemm(const
           }
           // (the bytes are those that the leader's first warp expects)
           const uint32_t sA = base_s + stage * C::STAGE;
-          load_stage<EPI, A_MN, B_MN, CG, GRP, 2>(L, 0, kb * KE, sA, sA + C::A_BYTES,
-                                                  full0 + 8u * stage, pol, pol);
+          const int seg = kb < L.kb0 ? 0 : 1;
+          load_stage<EPI, A_MN, B_MN, CG, GRP, 2>(L, seg, (seg == 0 ? kb : kb - L.kb0) * KE, sA,
+                                                  sA + C::A_BYTES, full0 + 8u * stage, pol, pol);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
@@ -2019,7 +2025,7 @@ cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(gemm_threads<A_MN, GRP>(), 1, 1);
+  cfg.blockDim = dim3(gemm_threads<B_MN, GRP>(), 1, 1);
   cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -2054,7 +2060,7 @@ int max_groups() {
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
-  cfg.blockDim = dim3(gemm_threads<A_MN, GRP>(), 1, 1);
+  cfg.blockDim = dim3(gemm_threads<B_MN, GRP>(), 1, 1);
   cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

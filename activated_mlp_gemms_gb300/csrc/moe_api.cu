@@ -98,6 +98,16 @@ int moe_cg(const mlp_moe_t* p) {
   return (long long)p->T * p->top_k > 512LL * p->E ? 2 : 1;
 }
 
+// The weight gradients', whose sums are as long as an expert's rows: pairs above
+// 1024 rows an expert (singles / pairs, us, both gradients of
+// 2048 x 4864 over 16384 rows in all: 512 an expert 768 / 800, 1024 640 / 636
+// and up to 720 by the box, 2048 575 / 538; 1024 of 4096 x 14336 1835 / 1835).
+int wgrad_cg(const mlp_moe_t* p) {
+  const int pol = g_tile_policy.load();
+  if (pol == 1 || pol == 2) return pol;
+  return p->H > BM && p->I > BM && (long long)p->T * p->top_k > 1024LL * p->E ? 2 : 1;
+}
+
 // Whether the inference layer streams the touched experts' weights: few tokens
 // whose experts' weights are at most 1 GB, unless a tile policy asks for the
 // tiles.  The stream saves the sort, the sorted rows and their launches, about
@@ -336,7 +346,7 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
   MLP_TRY(check_ws(p, MLP_MODE_BWD, ws, ws_bytes));
   const bool need_dact = dxs || dWg || dWu;
   if (!need_dact && !dWd) return MLP_OK;
-  const int cgw = p->H > BM && p->I > BM ? moe_cg(p) : pick_cg(p->H < p->I ? p->H : p->I);
+  const int cgw = wgrad_cg(p);
   const long long w_units = ((dWg ? 1 : 0) + (dWu ? 1 : 0)) * out_tiles(p->I, p->H, cgw) +
                             (dWd ? 1 : 0) * out_tiles(p->H, p->I, cgw);
   const int most = one_wave_units(moe_cg(p));
