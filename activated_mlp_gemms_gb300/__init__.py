@@ -191,7 +191,10 @@ _kept = {}
 def _call_workspace(n, device, stream):
     """A workspace of n bytes for a call on `stream` (None: the current one)."""
     if stream is not None or n > _KEEP_BYTES or torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if stream is not None:  # its memory is reused once that stream is done with it
+            ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
+        return ws
     key = (device.index, _stream(None), threading.get_ident())
     ws = _kept.get(key)
     if ws is None or ws.numel() < n:

@@ -316,9 +316,9 @@ cudaError_t launch_moe_dispatch(const void* x, const int* plan, const MoePlan& L
                     L.rows, top_k, H, segs, tokens, zero_rows(L));
 }
 
-cudaError_t launch_moe_combine(const void* y, bool y32, const int* plan, const MoePlan& L, int T, int top_k,
-                               int H, const void* weights, bool w_bf16, const void* residual,
-                               void* out, cudaStream_t stream, bool pdl) {
+cudaError_t launch_moe_combine(const void* y, bool y32, const int* plan, const MoePlan& L, int T,
+                               int top_k, int H, const void* weights, bool w_bf16,
+                               const void* residual, void* out, cudaStream_t stream, bool pdl) {
   const int ch = pieces(T, top_k, H), segs = (H + ch * TOK_COLS - 1) / (ch * TOK_COLS);
   auto pick = [&](auto c) {
     constexpr int CH = decltype(c)::value;
@@ -331,8 +331,8 @@ cudaError_t launch_moe_combine(const void* y, bool y32, const int* plan, const M
               : ch == 2 ? pick(std::integral_constant<int, 2>{})
                         : pick(std::integral_constant<int, 4>{});
   if (y32 && weights == nullptr) return cudaErrorInvalidValue;
-  return launch_tok(kern, static_cast<long long>(T) * segs, stream, pdl, y, plan + L.pos, weights, static_cast<const bf*>(residual), static_cast<bf*>(out),
-                    top_k, H, segs);
+  return launch_tok(kern, static_cast<long long>(T) * segs, stream, pdl, y, plan + L.pos, weights,
+                    static_cast<const bf*>(residual), static_cast<bf*>(out), top_k, H, segs);
 }
 
 cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* plan,

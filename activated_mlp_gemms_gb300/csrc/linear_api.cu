@@ -47,9 +47,10 @@ int linear_act(int act) {
 // single-CTA MMAs draw more shared-memory bandwidth per flop, 15 % of the time; a
 // wave of the skinny kernel, whose CTAs are not persistent, 3, and the exchange
 // of the sums 6.  Rows that are no multiple of 128 bytes straddle L2 lines, and
-// those MMAs' larger share of loads costs 40 %.  Measured (skinny / singles / pairs, us): 300 x 4096 x 4096 16.5
-// / 27.0 / 27.0, 512 x 2048 x 8192 22.8 / 27.6 / 28.5, 588 x 14336 x 4096 74 / 57.7
-// / 70, 1683 x 1024 x 1024 - / 10.7 / 12.3, 4096 x 4096 x 4096 - / 104 / 91.
+// those MMAs' larger share of loads costs 40 %.  Measured (skinny / singles /
+// pairs, us): 300 x 4096 x 4096 16.5 / 27.0 / 27.0, 512 x 2048 x 8192 22.8 / 27.6
+// / 28.5, 588 x 14336 x 4096 74 / 57.7 / 70, 1683 x 1024 x 1024 - / 10.7 / 12.3,
+// 4096 x 4096 x 4096 - / 104 / 91.
 enum Route { ROUTE_SINGLES = 1, ROUTE_PAIRS = 2, ROUTE_SKINNY = 3 };
 Route route(int M, int N, int K, bool whole_lines) {
   const int pol = g_tile_policy.load();
@@ -226,7 +227,8 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
   const bool db_left = db && linear_db_chunks(M, N) > 1;
   // dW and db go to the second stream when dx runs too (mlp_bwd's reasons),
   // unless all are small: then the events cost more than the overlap gives
-  Side* side = dx && (dW || db_left) && !c.one_wave && !g_trace_flag.load() ? side_stream(c.stream) : nullptr;
+  Side* side = dx && (dW || db_left) && !c.one_wave && !g_trace_flag.load()
+                   ? side_stream(c.stream) : nullptr;
   std::unique_lock<std::mutex> side_lk;
   if (side) {
     side_lk = std::unique_lock<std::mutex>(side->mu);

@@ -47,15 +47,14 @@ inline MoePlan moe_plan(int T, int E, int top_k) {
   return L;
 }
 
-// The routing weights' type: fp32 or bf16.
 cudaError_t launch_moe_sort(const int* ids, int* plan, const MoePlan& L, int E, cudaStream_t stream,
                             bool pdl);
 cudaError_t launch_moe_dispatch(const void* x, const int* plan, const MoePlan& L, int T, int top_k,
                                 int H, void* xs, cudaStream_t stream, bool pdl);
-// weights == nullptr: ones (the gradient of the dispatch); y32: y is fp32, with weights
-cudaError_t launch_moe_combine(const void* y, bool y32, const int* plan, const MoePlan& L, int T, int top_k,
-                               int H, const void* weights, bool w_bf16, const void* residual,
-                               void* out, cudaStream_t stream, bool pdl);
+// w_bf16: the routing weights are bf16, else fp32; weights == nullptr: ones (the gradient of the dispatch); y32: y is fp32, with weights
+cudaError_t launch_moe_combine(const void* y, bool y32, const int* plan, const MoePlan& L, int T,
+                               int top_k, int H, const void* weights, bool w_bf16,
+                               const void* residual, void* out, cudaStream_t stream, bool pdl);
 cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* plan,
                                    const MoePlan& L, int T, int top_k, int H, const void* weights,
                                    bool w_bf16, void* dy, void* dweights, cudaStream_t stream,

@@ -24,13 +24,18 @@ int check_moe(const mlp_moe_t* p) {
 
 MoePlan plan_of(const mlp_moe_t* p) { return moe_plan(p->T, p->E, p->top_k); }
 
-// int32 ids and the routing weights: 4-byte aligned
-int need4(const void* ptr) {
+bool w_bf16(const mlp_moe_t* p) { return p->weights_type == MLP_MOE_W_BF16; }
+
+// The ids and the routing weights are read one by one: aligned as their type.
+int need_ids(const void* ptr) {
   if (!ptr) return MLP_ERR_INVALID_ARG;
   return (reinterpret_cast<uintptr_t>(ptr) & 3u) ? MLP_ERR_ALIGNMENT : MLP_OK;
 }
-
-bool w_bf16(const mlp_moe_t* p) { return p->weights_type == MLP_MOE_W_BF16; }
+int need_w(const mlp_moe_t* p, const void* ptr) {
+  if (!ptr) return MLP_ERR_INVALID_ARG;
+  const uintptr_t low = w_bf16(p) ? 1u : 3u;
+  return (reinterpret_cast<uintptr_t>(ptr) & low) ? MLP_ERR_ALIGNMENT : MLP_OK;
+}
 
 bool gated(const mlp_moe_t* p) {
   return p->act == MLP_ACT_SWIGLU || p->act == MLP_ACT_REGLU || p->act == MLP_ACT_GEGLU ||
@@ -99,9 +104,9 @@ int moe_cg(const mlp_moe_t* p) {
 }
 
 // The weight gradients', whose sums are as long as an expert's rows: pairs above
-// 1024 rows an expert (singles / pairs, us, both gradients of
-// 2048 x 4864 over 16384 rows in all: 512 an expert 768 / 800, 1024 640 / 636
-// and up to 720 by the box, 2048 575 / 538; 1024 of 4096 x 14336 1835 / 1835).
+// 1024 rows an expert (singles / pairs, us, all three of 2048 x 4864 over 16384
+// rows: 512 an expert 768 / 800, 1024 640 / 636 and up to 720 by the box, 2048 575
+// / 538; 1024 of 4096 x 14336 1835 / 1835).
 int wgrad_cg(const mlp_moe_t* p) {
   const int pol = g_tile_policy.load();
   if (pol == 1 || pol == 2) return pol;
@@ -226,7 +231,7 @@ int mlp_moe_plan_layout(const mlp_moe_t* p, mlp_moe_plan_t* layout) {
 
 int mlp_moe_sort(const mlp_moe_t* p, const int* ids, void* plan, void* stream) {
   MLP_TRY(check_moe(p));
-  MLP_TRY(need4(ids));
+  MLP_TRY(need_ids(ids));
   MLP_TRY(need(plan));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_SORT, s, [&] {
@@ -264,7 +269,7 @@ int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const v
   MLP_TRY(check_moe(p));
   MLP_TRY(need(plan));
   MLP_TRY(need(y));
-  MLP_TRY(need4(weights));
+  MLP_TRY(need_w(p, weights));
   MLP_TRY(opt(residual));
   MLP_TRY(need(out));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -281,10 +286,10 @@ int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, 
   MLP_TRY(need(dout));
   if (dy) {
     MLP_TRY(need(dy));
-    MLP_TRY(need4(weights));
+    MLP_TRY(need_w(p, weights));
   }
   if (dweights) {
-    MLP_TRY(need4(dweights));
+    MLP_TRY(need_w(p, dweights));
     MLP_TRY(need(y));
   }
   if (!dy && !dweights) return MLP_OK;
@@ -460,8 +465,8 @@ int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const v
                       void* out, void* ws, size_t ws_bytes, void* stream) {
   MLP_TRY(check_experts(p));
   MLP_TRY(need(x));
-  MLP_TRY(need4(ids));
-  MLP_TRY(need4(weights));
+  MLP_TRY(need_ids(ids));
+  MLP_TRY(need_w(p, weights));
   MLP_TRY(check_weights(p, Wg, Wu, Wd));
   MLP_TRY(opt(residual));
   MLP_TRY(need(out));

@@ -75,7 +75,7 @@ int mlp_moe_dispatch_bwd(const mlp_moe_t* p, const void* plan, const void* dxs, 
                          void* stream);
 
 /* out[t] = residual[t] + sum_j weights[t, j] y[pos[t, j]] (fp32, rounded once).
- *   y bf16 [rows,H], weights [T,top_k] (weights_type, 4-byte aligned),
+ *   y bf16 [rows,H], weights [T,top_k] (weights_type, aligned as that type),
  *   residual bf16 [T,H] or NULL, out bf16 [T,H] (may be residual itself) */
 int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const void* weights,
                     const void* residual, void* out, void* stream);

@@ -159,6 +159,30 @@ def test_no_tokens():
     assert all((g == 0).all() for g in torch.autograd.grad(y.sum(), Ws))
 
 
+def test_workspace_of_a_call_on_another_stream():
+    # the call's own workspace is freed here while its kernels still wait on
+    # their stream: memory allocated meanwhile must be other memory
+    T, E, k, H, I = 300, 8, 2, 256, 512
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(BF)  # noqa: E731
+    p = m.moe(T, E, k, H, I)
+    x, Wg, Wu, Wd = rn(T, H), rn(E, I, H) / 16, rn(E, I, H) / 16, rn(E, H, I) / 23
+    ids = torch.rand(T, E, generator=gen, device="cuda").topk(k, -1)[1].int()
+    w = torch.rand(T, k, generator=gen, device="cuda")
+    want, got = torch.empty_like(x), torch.zeros_like(x)
+    m.mlp_moe_fwd_infer(p, x, ids, w, Wg, Wu, Wd, None, want)
+    n = m.mlp_moe_workspace_size(p, m.MODE_INFER)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(20_000_000)
+    m.mlp_moe_fwd_infer(p, x, ids, w, Wg, Wu, Wd, None, got, stream=other)
+    mine = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(bool((t == 7).all()) for t in mine)
+
+
 @pytest.mark.parametrize("tokens", [1, 6, 200])
 def test_block_of_the_example(tokens):
     ex = example()

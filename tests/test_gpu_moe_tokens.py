@@ -160,6 +160,31 @@ def test_weights_gradient_against_differences():
             assert (loss(step) - loss(w)).item() == dw[t, j].item()
 
 
+def test_bf16_weights_at_an_odd_address():
+    # rows of an odd number of bf16 weights: the same bits as from an aligned copy
+    T, E, k, H, I = 7, 4, 3, 64, 128
+    gen = torch.Generator().manual_seed(3)
+    rn = lambda *s: torch.randn(s, generator=gen).to(BF).cuda()  # noqa: E731
+    p = m.moe(T, E, k, H, I, weights_dtype=BF)
+    w = rn(T + 1, k)[1:]
+    assert w.data_ptr() % 4 == 2 and w.is_contiguous()
+    ids = torch.randint(0, E, (T, k), generator=gen, dtype=torch.int32).cuda()
+    rows, plan = m.mlp_moe_rows(p), m.alloc_moe_plan(p)
+    m.mlp_moe_sort(p, ids, plan)
+    x, y, dout = rn(T, H), rn(rows, H), rn(T, H)
+    Wg, Wu, Wd = rn(E, I, H), rn(E, I, H), rn(E, H, I)
+    res = []
+    for v, dw in ((w, torch.zeros(T + 1, k, dtype=BF, device="cuda")[1:]),
+                  (w.clone(), torch.zeros(T, k, dtype=BF, device="cuda"))):
+        out, lay, dy = torch.empty_like(x), torch.empty_like(x), torch.empty_like(y)
+        m.mlp_moe_combine(p, plan, y, v, None, out)
+        m.mlp_moe_combine_bwd(p, plan, dout, y, v, dy, dw)
+        m.mlp_moe_fwd_infer(p, x, ids, v, Wg, Wu, Wd, None, lay)
+        res.append((out, dy, dw, lay))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 def test_another_stream_and_repeat():
     """On a side stream the calls order with the work there, and give the same bits again."""
     T, E, k, H = 4099, 16, 4, 512
