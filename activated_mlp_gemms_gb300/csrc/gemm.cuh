@@ -1480,7 +1480,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
             }
             w = ring_get(ring_s(slot));
             valid = w.prob >= 0;
-            mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
+            mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
             if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           }
           if (!valid) break;
@@ -1630,7 +1630,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
             break;
           }
           const int v = sched[slot];
-          mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
+          mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           if (v < 0) break;
           const Work w = decode_unit(p, v);
@@ -1799,7 +1799,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
         }
         const Work w = ring_get(ring_s(slot));
         if (leader) mbar_arrive(bar_s(SEMPTY + slot));
-        else mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
+        else mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
         if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
         if (w.prob < 0) break;
         const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
@@ -1870,7 +1870,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
       __syncwarp();
       if (lane == 0) {
         if (leader) mbar_arrive(bar_s(SEMPTY + slot));
-        else mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
+        else mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
       }
       if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
       if (unit < 0) break;
@@ -1917,7 +1917,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
         __syncwarp();
         if (lane == 0) {
           if (leader) mbar_arrive(bar_s(TEMPTY + acc));
-          else mbar_arrive_cluster(lead(bar_s(TEMPTY + acc)));
+          else mbar_arrive_cluster_reads(lead(bar_s(TEMPTY + acc)));
         }
         acc ^= 1;
         if (acc == 0) aphase ^= 1u;
@@ -1984,7 +1984,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
       __syncwarp();
       if (lane == 0) {
         if (leader) mbar_arrive(bar_s(TEMPTY + acc));
-        else mbar_arrive_cluster(lead(bar_s(TEMPTY + acc)));
+        else mbar_arrive_cluster_reads(lead(bar_s(TEMPTY + acc)));
       }
       acc ^= 1;
       if (acc == 0) aphase ^= 1u;
