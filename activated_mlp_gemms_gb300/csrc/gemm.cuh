@@ -1456,11 +1456,11 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
           const uint32_t prob = static_cast<uint32_t>(valid ? w.prob : -1);
           auto put = [&](uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t v) {
             st_shared_v4(at, x, y, z, v);
-            if constexpr (PAIR) st_shared_cluster_v4(peer(at), x, y, z, v);
+            if constexpr (PAIR) st_async_v4(peer(at), x, y, z, v, peer(bar_s(SFULL + slot)));
           };
+          if constexpr (PAIR) mbar_expect_tx_cluster(peer(bar_s(SFULL + slot)), 32);
           put(a, prob, w.tm, w.tn, w.kb_end);
           put(a + 16, w.expert, w.row0, w.row_end, 0);
-          if constexpr (PAIR) mbar_arrive_cluster(peer(bar_s(SFULL + slot)));
           mbar_arrive(bar_s(SFULL + slot));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           return true;
@@ -1547,8 +1547,9 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
             if (!mbar_wait<PAIR>(bar_s(SEMPTY + slot), sphase ^ 1u, lim, abort_flag)) return false;
             sched[slot] = v;
             if constexpr (PAIR) {
-              st_shared_cluster_u32(peer(smem_u32(sched + slot)), static_cast<uint32_t>(v));
-              mbar_arrive_cluster(peer(bar_s(SFULL + slot)));
+              const uint32_t bar = peer(bar_s(SFULL + slot));
+              mbar_expect_tx_cluster(bar, 4);
+              st_async_u32(peer(smem_u32(sched + slot)), static_cast<uint32_t>(v), bar);
             }
             mbar_arrive(bar_s(SFULL + slot));
             if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
