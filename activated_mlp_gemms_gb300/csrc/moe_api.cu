@@ -94,23 +94,17 @@ int check_ws(const mlp_moe_t* p, int mode, const void* ws, size_t ws_bytes) {
   return ws_bytes < layout(p, mode).total ? MLP_ERR_WORKSPACE_TOO_SMALL : MLP_OK;
 }
 
-// CTA pairs (256-row tiles) from an average of more than 512 rows an expert:
-// an expert's last tile is half empty on average, 128 rows of a pair's tile or
-// 64 of a single CTA's, while a pair's tile is the faster one per row.
+// CTA pairs (256-row tiles) from an average of 192 rows an expert: an expert's
+// last tile is half empty on average, 128 rows of a pair's tile or 64 of a single
+// CTA's, while a pair's tile is the faster one per row.  Measured (pairs / singles;
+// gate/up, down, dgated, dx and weight gradients of 2048 x 4864, 16 experts of as
+// many rows each): 128 rows 1.11 1.16 1.05 1.21 .98, 192 .87 .90 .98 .88 .98, 384
+// 1.04 1.02 1.03 1.10 .89, 512 .84 .84 .89 .88 .92, 1024 .83 .82 .84 .87 .87; with
+// uneven experts 192 1.01 1.08 1.02 1.13 .97, 512 .92 .98 .93 1.05 .93.
 int moe_cg(const mlp_moe_t* p) {
   const int pol = g_tile_policy.load();
   if (pol == 1 || pol == 2) return pol;
-  return (long long)p->T * p->top_k > 512LL * p->E ? 2 : 1;
-}
-
-// The weight gradients', whose sums are as long as an expert's rows: pairs above
-// 1024 rows an expert (singles / pairs, us, all three of 2048 x 4864 over 16384
-// rows: 512 an expert 768 / 800, 1024 640 / 636 and up to 720 by the box, 2048 575
-// / 538; 1024 of 4096 x 14336 1835 / 1835).
-int wgrad_cg(const mlp_moe_t* p) {
-  const int pol = g_tile_policy.load();
-  if (pol == 1 || pol == 2) return pol;
-  return p->H > BM && p->I > BM && (long long)p->T * p->top_k > 1024LL * p->E ? 2 : 1;
+  return (long long)p->T * p->top_k >= 192LL * p->E ? 2 : 1;
 }
 
 // Whether the inference layer streams the touched experts' weights: few tokens
@@ -351,7 +345,7 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
   MLP_TRY(check_ws(p, MLP_MODE_BWD, ws, ws_bytes));
   const bool need_dact = dxs || dWg || dWu;
   if (!need_dact && !dWd) return MLP_OK;
-  const int cgw = wgrad_cg(p);
+  const int cgw = p->H > BM && p->I > BM ? moe_cg(p) : pick_cg(p->H < p->I ? p->H : p->I);
   const long long w_units = ((dWg ? 1 : 0) + (dWu ? 1 : 0)) * out_tiles(p->I, p->H, cgw) +
                             (dWd ? 1 : 0) * out_tiles(p->H, p->I, cgw);
   const int most = one_wave_units(moe_cg(p));
