@@ -43,26 +43,29 @@ int linear_act(int act) {
 // x 256 tiles of CTA pairs, or the skinny kernel's 128 features by up to 256 rows
 // with K shared by clusters.  (A tile policy of 1 or 2 asks for the first two.)
 // Up to 192 rows the skinny kernel; beyond that the least of three estimates, in
-// units of one 256 x 256 k-block of a pair (0.33 us): a pair's launch costs 4 more;
-// single-CTA MMAs draw more shared-memory bandwidth per flop, 15 % of the time; a
-// wave of the skinny kernel, whose CTAs are not persistent, 3, and the exchange
-// of the sums 6.  Rows that are no multiple of 128 bytes straddle L2 lines, and
-// those MMAs' larger share of loads costs 40 %.  Measured (skinny / singles /
-// pairs, us): 300 x 4096 x 4096 16.5 / 27.0 / 27.0, 512 x 2048 x 8192 22.8 / 27.6
-// / 28.5, 588 x 14336 x 4096 74 / 57.7 / 70, 1683 x 1024 x 1024 - / 10.7 / 12.3,
-// 4096 x 4096 x 4096 - / 104 / 91.
+// units of one 256 x 256 k-block of a pair (0.33 us): a pair's launch costs 2 more,
+// 5 in the forward, whose last epilogue is longer; single-CTA MMAs draw more
+// shared-memory bandwidth per flop, 13 % of the time; a skinny tile of mp rows takes
+// (128 + mp) / 384 of a k-block's loads, a wave of them, whose CTAs are not
+// persistent, 6, and the exchange of the sums 10.  Rows that are no multiple of 128
+// bytes straddle L2 lines, and those MMAs' larger share of loads costs 40 %.
+// Measured (skinny / singles / pairs, us): 300 x 4096 x 4096 16.5 / 27 / 25, 512 x
+// 2048 x 8192 22.8 / 27.6 / 28.5, 777 x 14336 x 4096 76 / 78 / 69, 777 x 4864 x 2048
+// 16.5 / 15.7 / 17.1, 1000 x 1024 x 1024 11.2 / 10.0 / 10.4; over 250 products the
+// route was 0.8 % slower than the fastest of the tiles on average.
 enum Route { ROUTE_SINGLES = 1, ROUTE_PAIRS = 2, ROUTE_SKINNY = 3 };
-Route route(int M, int N, int K, bool whole_lines) {
+Route route(int M, int N, int K, bool whole_lines, bool forward) {
   const int pol = g_tile_policy.load();
   if (pol == 1 || pol == 2) return static_cast<Route>(pol);
   if (M <= 192) return ROUTE_SKINNY;
   const SkinnyShape s = linear_skinny_shape(M, N, K);
-  const double kbs = (K + BK - 1) / BK, loads = whole_lines ? 1.15 : 1.4;
+  const double kbs = (K + BK - 1) / BK, loads = whole_lines ? 1.13 : 1.4;
   auto waves = [](long long units, int slots) { return (double)((units + slots - 1) / slots); };
-  const double pairs = waves(out_tiles(M, N, 2), 76) * kbs + 4;
+  const double pairs = waves(out_tiles(M, N, 2), 76) * kbs + (forward ? 5 : 2);
   const double singles = loads * waves(out_tiles(M, N, 1), 152) * kbs;
   const double skinny = waves((long long)s.blocks * s.tiles * s.share, 152) *
-                            (loads * kbs / s.share * s.mp / 256 + 3) + (s.share > 1 ? 6 : 0);
+                            (loads * kbs / s.share * (128 + s.mp) / 384 + 6) +
+                        (s.share > 1 ? 10 : 0);
   if (skinny < pairs && skinny < singles) return ROUTE_SKINNY;
   return singles < pairs ? ROUTE_SINGLES : ROUTE_PAIRS;
 }
@@ -120,7 +123,7 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
   const int ldx = p->ldx ? p->ldx : K, ldr = p->ldr ? p->ldr : N, ldo = p->ldo ? p->ldo : N;
   const bool streamed = M <= LINEAR_STREAM_MAX_M;
-  const Route way = streamed ? ROUTE_SKINNY : route(M, N, K, ldx % 64 == 0 && K % 64 == 0);
+  const Route way = streamed ? ROUTE_SKINNY : route(M, N, K, ldx % 64 == 0 && K % 64 == 0, true);
   const bool tiles = way != ROUTE_SKINNY;
   Call c;
   // (one wave of tiles: 22.7 -> 18.9 us for 777 x 4864 x 2048; the stream and the
@@ -195,7 +198,7 @@ int mlp_linear_bwd(const mlp_linear_t* p, const void* dout, const void* x, const
   const int M = p->M, N = p->N, K = p->K, act = linear_act(p->act);
   const int ldx = p->ldx ? p->ldx : K, ldd = p->ldo ? p->ldo : N;
   char* base = static_cast<char*>(ws);
-  const Route way = route(M, K, N, ldd % 64 == 0 && K % 64 == 0);  // dx
+  const Route way = route(M, K, N, ldd % 64 == 0 && K % 64 == 0, false);  // dx
   const bool skinny_dx = dx && way == ROUTE_SKINNY;
   const int cgx = skinny_dx ? 1 : way, cgw = pick_cg(N < K ? N : K);
   // dz_out or db: the derivative pass comes first and clears the status word
