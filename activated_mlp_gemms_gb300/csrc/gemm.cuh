@@ -25,11 +25,10 @@
 // a unit is a row tile of one expert against that expert's matrix of a weight
 // stack (3-D tensor maps), rows past the expert's end are neither stored nor read
 // by the epilogue, and a weight gradient sums over its expert's rows (whole K steps
-// of 16).  Measured, 16384 rows over 16 experts of 1024, 2048 x 4864: gate/up 413 us
-// (394 as one dense GEMM), down 190 (180), dgated 258 (250), dx 362 (362), weight
-// gradients 641 (530 for the same sums over one expert's 16384 rows: here 956 MB of
-// gradients go out at HBM's write rate, after sums of 16 k-blocks each; without
-// their epilogue 538).
+// of 16).  Measured, 16384 rows over 16 experts of 1024, 2048 x 4864: gate/up 395 us
+// (383 as one dense GEMM), down 184 (176), dgated 238 (244), dx 356 (362), weight
+// gradients 582 (530 for the same sums over one expert's 16384 rows: here 956 MB of
+// gradients go out, after sums of 16 k-blocks each; without their epilogue 538).
 // EPI_FWD_FUSED runs the gated forward's two GEMMs in one launch: the
 // epilogue warps count their stored gate/up tiles per 256-row block, and the
 // producer of a down-projection unit waits for its block's count.
@@ -1316,9 +1315,9 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
 // thread issued them in 374 of the k-block's 600 cycles; what it spent between two
 // units (about 3100 cycles) it could not catch up within an expert's few
 // k-blocks, and every unit's first MMAs waited 2200-3800 cycles for their
-// operands (all measured).  With the second warp, and units decoded ahead, they take
-// 641 us in place of 714 (see above), and dx and dgated on single CTAs 405 and 272
-// in place of 444 and 293 (on pairs 362 for 373, and 266 both).
+// operands (all measured).  With the second warp, and units decoded ahead, they took
+// 641 us in place of 714, and dx and dgated on single CTAs 405 and 272 in place of
+// 444 and 293.
 template <bool B_MN, bool GRP>
 constexpr int gemm_threads() { return NUM_THREADS + (B_MN && GRP ? 32 : 0); }
 
