@@ -19,7 +19,8 @@ from . import (ACTS, MODE_BWD, MODE_FWD, MODE_INFER, MlpError, _call_workspace, 
 ROW_ALIGN = 16  # MLP_MOE_ROW_ALIGN
 MAX_EXPERTS = 1024  # MLP_MOE_MAX_EXPERTS
 MAX_TOP_K = 64  # MLP_MOE_MAX_TOP_K
-_W_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_W_DTYPES = (torch.float32, torch.bfloat16)
+_W_TYPES = {t: i for i, t in enumerate(_W_DTYPES)}
 
 
 class Moe(ctypes.Structure):
@@ -82,96 +83,103 @@ def _shaped(t, shape, name, dtype=torch.bfloat16):
     return p
 
 
-def _w_dtype(p: Moe):
-    return torch.bfloat16 if p.weights_type else torch.float32
+class _Sizes:
+    """What the calls need to know of a problem's sizes: the shapes of the tensors, and the
+    plan's public parts as (shape, strides, first value)."""
+
+    def __init__(self, T, E, top_k, H, weights_type):
+        p, out = Moe(T, E, top_k, H, weights_type=weights_type), _Layout()
+        _check(lib().mlp_moe_plan_layout(ctypes.byref(p), ctypes.byref(out)),
+               "mlp_moe_plan_layout")
+        rows = int(lib().mlp_moe_rows(ctypes.byref(p)))
+        self.tokens, self.slots, self.rows = (T, H), (T, top_k), (rows, H)
+        self.layout, self.plan = out, (int(out.ints),)
+        self.views = {"offsets": ((E + 1,), (1,), out.offsets), "counts": ((E,), (1,), out.counts),
+                      "pos": ((T, top_k), (top_k, 1), out.pos), "src": ((rows,), (1,), out.src)}
+        self.w_dtype = _W_DTYPES[weights_type]
 
 
-@functools.lru_cache(maxsize=1024)
-def _sizes(T, E, top_k, H, weights_type):
-    """(plan layout, rows): a function of the sizes alone."""
-    p, out = Moe(T, E, top_k, H, weights_type=weights_type), _Layout()
-    _check(lib().mlp_moe_plan_layout(ctypes.byref(p), ctypes.byref(out)), "mlp_moe_plan_layout")
-    return out, int(lib().mlp_moe_rows(ctypes.byref(p)))
+_sizes_of = functools.lru_cache(maxsize=1024)(_Sizes)
+
+
+def _sizes(p: Moe) -> _Sizes:
+    return _sizes_of(p.T, p.E, p.top_k, p.H, p.weights_type)
 
 
 def _layout(p: Moe) -> _Layout:
-    return _sizes(p.T, p.E, p.top_k, p.H, p.weights_type)[0]
+    return _sizes(p).layout
 
 
 def mlp_moe_rows(p: Moe) -> int:
     """Rows of the sorted layout's buffers (xs, y, dxs, dy, G, U)."""
-    return _sizes(p.T, p.E, p.top_k, p.H, p.weights_type)[1]
+    return _sizes(p).rows[0]
 
 
 def alloc_moe_plan(p: Moe, device=None) -> torch.Tensor:
-    return torch.empty(_layout(p).ints, dtype=torch.int32, device=device or "cuda")
+    return torch.empty(_sizes(p).plan, dtype=torch.int32, device=device or "cuda")
 
 
-def _plan(p: Moe, plan):
-    return _shaped(plan, (_layout(p).ints,), "plan", torch.int32)
+def _plan(s: _Sizes, plan):
+    return _shaped(plan, s.plan, "plan", torch.int32)
 
 
 class _PlanViews(Mapping):
     """The plan's public parts, each made a view when it is asked for."""
 
-    def __init__(self, p, plan):
-        self._p, self._plan = p, plan
+    def __init__(self, views, plan):
+        self._views, self._plan = views, plan
 
     def __getitem__(self, name):
-        p, L = self._p, _layout(self._p)
-        if name == "pos":
-            size, stride = (p.T, p.top_k), (p.top_k, 1)
-        else:
-            size, stride = {"offsets": (p.E + 1,), "counts": (p.E,),
-                            "src": (mlp_moe_rows(p),)}[name], (1,)
-        return self._plan.as_strided(size, stride,
-                                     self._plan.storage_offset() + getattr(L, name))
+        size, stride, first = self._views[name]
+        return self._plan.as_strided(size, stride, self._plan.storage_offset() + first)
 
     def __iter__(self):
-        return iter(("offsets", "counts", "pos", "src"))
+        return iter(self._views)
 
     def __len__(self):
-        return 4
+        return len(self._views)
 
 
 def moe_plan_views(p: Moe, plan) -> Mapping:
     """The plan's public parts as views: offsets [E + 1] (first row of each expert),
     counts [E], pos [T, top_k] (row of each slot, -1 when dropped), src [rows] (slot of
     each row, -1 for padding)."""
-    _plan(p, plan)
-    return _PlanViews(p, plan)
+    s = _sizes(p)
+    _plan(s, plan)
+    return _PlanViews(s.views, plan)
 
 
 def mlp_moe_sort(p: Moe, ids, plan, stream=None) -> None:
     """Fills the plan from ids (int32 [T, top_k]; an id outside [0, E) drops the slot)."""
-    rc = lib().mlp_moe_sort(ctypes.byref(p),
-                            _shaped(ids, (p.T, p.top_k), "ids", torch.int32), _plan(p, plan),
-                            _stream(stream))
+    s = _sizes(p)
+    rc = lib().mlp_moe_sort(ctypes.byref(p), _shaped(ids, s.slots, "ids", torch.int32),
+                            _plan(s, plan), _stream(stream))
     _check(rc, "mlp_moe_sort")
 
 
 def mlp_moe_dispatch(p: Moe, plan, x, xs, stream=None) -> None:
     """xs[pos[t, j]] = x[t]; the other rows of xs become zero."""
-    rc = lib().mlp_moe_dispatch(ctypes.byref(p), _plan(p, plan), _shaped(x, (p.T, p.H), "x"),
-                                _shaped(xs, (mlp_moe_rows(p), p.H), "xs"), _stream(stream))
+    s = _sizes(p)
+    rc = lib().mlp_moe_dispatch(ctypes.byref(p), _plan(s, plan), _shaped(x, s.tokens, "x"),
+                                _shaped(xs, s.rows, "xs"), _stream(stream))
     _check(rc, "mlp_moe_dispatch")
 
 
 def mlp_moe_dispatch_bwd(p: Moe, plan, dxs, dx, stream=None) -> None:
     """dx[t] = sum_j dxs[pos[t, j]]."""
-    rc = lib().mlp_moe_dispatch_bwd(ctypes.byref(p), _plan(p, plan),
-                                    _shaped(dxs, (mlp_moe_rows(p), p.H), "dxs"),
-                                    _shaped(dx, (p.T, p.H), "dx"), _stream(stream))
+    s = _sizes(p)
+    rc = lib().mlp_moe_dispatch_bwd(ctypes.byref(p), _plan(s, plan), _shaped(dxs, s.rows, "dxs"),
+                                    _shaped(dx, s.tokens, "dx"), _stream(stream))
     _check(rc, "mlp_moe_dispatch_bwd")
 
 
 def mlp_moe_combine(p: Moe, plan, y, weights, residual, out, stream=None) -> None:
     """out[t] = residual[t] + sum_j weights[t, j] y[pos[t, j]] (residual may be None)."""
-    rc = lib().mlp_moe_combine(ctypes.byref(p), _plan(p, plan),
-                               _shaped(y, (mlp_moe_rows(p), p.H), "y"),
-                               _shaped(weights, (p.T, p.top_k), "weights", _w_dtype(p)),
-                               _shaped(residual, (p.T, p.H), "residual"),
-                               _shaped(out, (p.T, p.H), "out"), _stream(stream))
+    s = _sizes(p)
+    rc = lib().mlp_moe_combine(ctypes.byref(p), _plan(s, plan), _shaped(y, s.rows, "y"),
+                               _shaped(weights, s.slots, "weights", s.w_dtype),
+                               _shaped(residual, s.tokens, "residual"),
+                               _shaped(out, s.tokens, "out"), _stream(stream))
     _check(rc, "mlp_moe_combine")
 
 
@@ -179,13 +187,12 @@ def mlp_moe_combine_bwd(p: Moe, plan, dout, y, weights, dy=None, dweights=None,
                         stream=None) -> None:
     """dy[pos[t, j]] = weights[t, j] dout[t] (the other rows zero) and
     dweights[t, j] = <dout[t], y[pos[t, j]]>; either may be None."""
-    rows = mlp_moe_rows(p)
-    rc = lib().mlp_moe_combine_bwd(ctypes.byref(p), _plan(p, plan),
-                                   _shaped(dout, (p.T, p.H), "dout"),
-                                   _shaped(y, (rows, p.H), "y"),
-                                   _shaped(weights, (p.T, p.top_k), "weights", _w_dtype(p)),
-                                   _shaped(dy, (rows, p.H), "dy"),
-                                   _shaped(dweights, (p.T, p.top_k), "dweights", _w_dtype(p)),
+    s = _sizes(p)
+    rc = lib().mlp_moe_combine_bwd(ctypes.byref(p), _plan(s, plan),
+                                   _shaped(dout, s.tokens, "dout"), _shaped(y, s.rows, "y"),
+                                   _shaped(weights, s.slots, "weights", s.w_dtype),
+                                   _shaped(dy, s.rows, "dy"),
+                                   _shaped(dweights, s.slots, "dweights", s.w_dtype),
                                    _stream(stream))
     _check(rc, "mlp_moe_combine_bwd")
 
@@ -228,12 +235,13 @@ def mlp_moe_experts_fwd(p: Moe, plan, xs, Wg, Wu, Wd, y, G_save=None, U_save=Non
     preacts (bf16 [rows, I]) for the backward.  Wg, Wu [E, I, H] (Wu None when non-gated),
     Wd [E, H, I].  Rows of y past the plan's offsets[E] are not written.  Returns the
     workspace used."""
-    rows = mlp_moe_rows(p)
+    s = _sizes(p)
+    inter = (s.rows[0], p.I)
     ws = _ws(ws, p, MODE_FWD, y.device, stream)
-    rc = lib().mlp_moe_experts_fwd(ctypes.byref(p), _plan(p, plan), _shaped(xs, (rows, p.H), "xs"),
-                                   *_weights(p, Wg, Wu, Wd), _shaped(y, (rows, p.H), "y"),
-                                   _shaped(G_save, (rows, p.I), "G_save"),
-                                   _shaped(U_save, (rows, p.I), "U_save"), ws.data_ptr(),
+    rc = lib().mlp_moe_experts_fwd(ctypes.byref(p), _plan(s, plan), _shaped(xs, s.rows, "xs"),
+                                   *_weights(p, Wg, Wu, Wd), _shaped(y, s.rows, "y"),
+                                   _shaped(G_save, inter, "G_save"),
+                                   _shaped(U_save, inter, "U_save"), ws.data_ptr(),
                                    ws.numel(), _stream(stream))
     _check(rc, "mlp_moe_experts_fwd")
     return ws
@@ -244,12 +252,13 @@ def mlp_moe_experts_bwd(p: Moe, plan, dy, xs, Wg, Wu, Wd, G, U, dxs=None, dWg=No
     """Gradients of mlp_moe_experts_fwd from its saved G, U (overwritten with dG, dU).
     Outputs that are None are skipped; weight gradients are bf16 (overwritten) or fp32
     (+= in place) when fuse_grad_accum.  The padding rows of dy and xs are zero."""
-    rows = mlp_moe_rows(p)
+    s = _sizes(p)
+    inter = (s.rows[0], p.I)
     ws = _ws(ws, p, MODE_BWD, dy.device, stream)
-    rc = lib().mlp_moe_experts_bwd(ctypes.byref(p), _plan(p, plan), _shaped(dy, (rows, p.H), "dy"),
-                                   _shaped(xs, (rows, p.H), "xs"), *_weights(p, Wg, Wu, Wd),
-                                   _shaped(G, (rows, p.I), "G"), _shaped(U, (rows, p.I), "U"),
-                                   _shaped(dxs, (rows, p.H), "dxs"),
+    rc = lib().mlp_moe_experts_bwd(ctypes.byref(p), _plan(s, plan), _shaped(dy, s.rows, "dy"),
+                                   _shaped(xs, s.rows, "xs"), *_weights(p, Wg, Wu, Wd),
+                                   _shaped(G, inter, "G"), _shaped(U, inter, "U"),
+                                   _shaped(dxs, s.rows, "dxs"),
                                    *_weights(p, dWg, dWu, dWd, _wdt(fuse_grad_accum),
                                              ("dWg", "dWu", "dWd")),
                                    int(bool(fuse_grad_accum)), ws.data_ptr(), ws.numel(),
@@ -265,7 +274,7 @@ def mlp_moe_fwd_infer(p: Moe, x, ids, weights, Wg, Wu, Wd, residual, out, ws=Non
     th, tk = (p.T, p.H), (p.T, p.top_k)
     rc = lib().mlp_moe_fwd_infer(ctypes.byref(p), _shaped(x, th, "x"),
                                  _shaped(ids, tk, "ids", torch.int32),
-                                 _shaped(weights, tk, "weights", _w_dtype(p)),
+                                 _shaped(weights, tk, "weights", _W_DTYPES[bool(p.weights_type)]),
                                  *_weights(p, Wg, Wu, Wd), _shaped(residual, th, "residual"),
                                  _shaped(out, th, "out"), ws.data_ptr(), ws.numel(),
                                  _stream(stream))
