@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS)
                      const bf* __restrict__ Wd, bf* __restrict__ h, int T, int top_k, int E, int H,
                      int I, float s, int* status) {
   constexpr int NMAT = GATED ? 2 : 1;
-  using G = MdGroup<NMAT, 8, 1>;
+  using G = MdGroup<NMAT, 8, 1, true>;
   extern __shared__ int scratch[];
   __shared__ Groups gr;
   __shared__ float4 part[2][DEC_WARPS][NMAT][32];
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS)
     k_moe_decode_down(const bf* __restrict__ h, const int* __restrict__ ids,
                       const void* __restrict__ weights, const bf* __restrict__ Wd,
                       const bf* residual, bf* out, int T, int top_k, int E, int H, int I) {
-  using G = MdGroup<1, 8, 1>;
+  using G = MdGroup<1, 8, 1, true>;
   extern __shared__ int scratch[];
   __shared__ Groups gr;
   __shared__ float4 part[DEC_WARPS][32];

@@ -1,6 +1,6 @@
 // stream.cuh -- the weight stream on the warp-level MMA that the few-token
-// kernels share: 16-byte loads of weights and tokens that are MMA fragments as
-// they come (k_decode_mma.cu explains the layout).
+// kernels share: 16- or 32-byte loads of weights and tokens that are MMA
+// fragments as they come (k_decode_mma.cu explains the layout).
 #pragma once
 #include "ptx.cuh"
 
@@ -14,6 +14,13 @@ __device__ __forceinline__ uint4 ld_weights_v4(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+
+__device__ __forceinline__ void ld_weights_v8(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(p));
 }
 
 __device__ __forceinline__ uint4 ld_tokens_v4(const void* p) {
@@ -35,10 +42,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Rows of K values at p begin at multiples of 32 bytes.
+__device__ __forceinline__ bool wide_rows(const void* p, int K) {
+  return K % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
+}
+
 // A load group: 64 k of NMAT weight matrices (RT 16-row tiles each) and of NT
-// tokens, and its MMAs.
-template <int NMAT_, int NT, int RT>
+// tokens, and its MMAs.  WIDE: a lane's two k-steps are 32 contiguous bytes of a
+// row, one load where rows are wide_rows, so that a warp's load takes whole 128-byte
+// lines (the experts' stream of 4 tokens of 4 x 44 MB 118 -> 110 us, of one token
+// 33.2 -> 32.7; the linear layer's was 20.4 without, 21.1 with).
+template <int NMAT_, int NT, int RT, bool WIDE = false>
 struct MdGroup {
+  // k from lane to lane, and from step to step
+  static constexpr int KL = WIDE ? 16 : 8, KS = WIDE ? 8 : 32;
   static constexpr int NMAT = NMAT_;
   static constexpr int NTB = NT / 8;  // 8-token blocks
   uint4 w[NMAT][RT][2][2];            // [matrix][16-row tile][row g, g + 8][k-step]
@@ -48,9 +65,27 @@ struct MdGroup {
   __device__ __forceinline__ void load_w(const __nv_bfloat16* const (&W)[2], int row0, int R,
                                          int K, int k0, int lane) {
     const int g = lane >> 2, q = lane & 3;
+    if constexpr (WIDE) {
+      if (wide_rows(W[0], K) && (NMAT == 1 || wide_rows(W[1], K))) {
+        const int k = k0 + 16 * q;
+#pragma unroll
+        for (int a = 0; a < NMAT; ++a)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = row0 + 16 * rt + g + 8 * h;
+              if (k < K && r < R)
+                ld_weights_v8(W[a] + static_cast<size_t>(r) * K + k, w[a][rt][h][0],
+                              w[a][rt][h][1]);
+              else w[a][rt][h][0] = w[a][rt][h][1] = make_uint4(0, 0, 0, 0);
+            }
+        return;
+      }
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int k = k0 + 32 * s + 8 * q;
+      const int k = k0 + KS * s + KL * q;
 #pragma unroll
       for (int a = 0; a < NMAT; ++a)
 #pragma unroll
@@ -70,7 +105,7 @@ struct MdGroup {
     const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int k = k0 + 32 * s + 8 * q;
+      const int k = k0 + KS * s + KL * q;
 #pragma unroll
       for (int b = 0; b < NTB; ++b) {
         const int m = 8 * b + g;
@@ -86,7 +121,7 @@ struct MdGroup {
     const int q = lane & 3;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int k = k0 + 32 * s + 8 * q;
+      const int k = k0 + KS * s + KL * q;
 #pragma unroll
       for (int b = 0; b < NTB; ++b)
         t[b][s] = (k < K && rows[b] != nullptr) ? ld_tokens_v4(rows[b] + k)
