@@ -150,13 +150,16 @@ __device__ __forceinline__ Work unit_work(const Params& p, const UnitKey& k) {
   return w;
 }
 
-// GRP: the ring carries decoded units, so that only the leader's producer
-// decodes, ahead of time (before, its peer and the MMA issuer did too, between
-// one unit's last k-block and the next one's first: 2-4 % of the down projection
-// and dx).
+// The ring carries decoded units, so that only the leader's producer decodes,
+// ahead of time (before, its peer and the MMA issuer did too, between one unit's
+// last k-block and the next one's first: 2-4 % of the experts' down projection and
+// dx, 1-2 % of the dense GEMMs with a K-major A, 5 % of those of one or two waves).
+// Not the dense weight gradients, which it made 1-3 % slower, nor the one-launch
+// forward, which claims some units late, nor the 8-bit and recompute kernels, which
+// have no registers for it.
 struct alignas(16) RingUnit {
   int prob, tm, tn, kb_end;  // prob < 0: no more work
-  int expert, row0, row_end, pad;
+  int expert, row0, row_end, kb_begin;
 };
 __device__ __forceinline__ Work ring_get(uint32_t slot) {
   const uint4 a = ld_shared_v4(slot), b = ld_shared_v4(slot + 16);
@@ -164,7 +167,7 @@ __device__ __forceinline__ Work ring_get(uint32_t slot) {
   w.prob = static_cast<int>(a.x);
   w.tm = static_cast<int>(a.y);
   w.tn = static_cast<int>(a.z);
-  w.kb_begin = 0;
+  w.kb_begin = static_cast<int>(b.w);
   w.kb_end = static_cast<int>(a.w);
   w.expert = static_cast<int>(b.x);
   w.row0 = static_cast<int>(b.y);
@@ -1359,7 +1362,8 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
   constexpr int EBAR = DRAIN + 1;
   constexpr int NBAR = EBAR + 2 * NUM_EPI_WARPS;
   // the unit ring: unit numbers, or decoded units
-  constexpr bool RING = GRP;
+  constexpr bool RING =
+      GRP || (!A_MN && !is_f8(EPI) && !is_recomp(EPI) && EPI != EPI_FWD_FUSED);
   constexpr int RING_AT = RING ? (8 * NBAR + 15) / 16 * 16 : 8 * NBAR;
   constexpr int RING_BYTES = SCHED_SLOTS * static_cast<int>(RING ? sizeof(RingUnit) : sizeof(int));
   static_assert(RING_AT + RING_BYTES + 8 <= 1024, "control area");
@@ -1464,7 +1468,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
           };
           if constexpr (PAIR) mbar_expect_tx_cluster(peer(bar_s(SFULL + slot)), 32);
           put(a, prob, w.tm, w.tn, w.kb_end);
-          put(a + 16, w.expert, w.row0, w.row_end, 0);
+          put(a + 16, w.expert, w.row0, w.row_end, w.kb_begin);
           mbar_arrive(bar_s(SFULL + slot));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           return true;
@@ -1473,7 +1477,10 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
         Work w{};
         bool valid = unit < total_units;
         if (leader && !publish_nothing) {
-          if (valid) w = unit_work<A_MN, C::TILE_M>(p, unit_key<A_MN>(p, unit));
+          if (valid) {
+            if constexpr (GRP) w = unit_work<A_MN, C::TILE_M>(p, unit_key<A_MN>(p, unit));
+            else w = decode_unit(p, unit);
+          }
           ok = publish(w, valid);
         }
         while (ok && !publish_nothing) {
@@ -1502,14 +1509,20 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
           int step = 0;  // of the next unit: 1 its key is being loaded, 2 published
           auto advance = [&]() -> bool {
             if (++step == 1) {
-              if (next_valid) key = unit_key<A_MN>(p, next);
+              if constexpr (GRP) {
+                if (next_valid) key = unit_key<A_MN>(p, next);
+              } else {
+                if (next_valid) nw = decode_unit(p, next);
+              }
               return true;
             }
-            if (next_valid) nw = unit_work<A_MN, C::TILE_M>(p, key);
+            if constexpr (GRP) {
+              if (next_valid) nw = unit_work<A_MN, C::TILE_M>(p, key);
+            }
             return publish(nw, next_valid);
           };
-          const int mid = w.kb_end / 2;
-          for (int kb = 0; kb < w.kb_end; ++kb) {
+          const int mid = (w.kb_begin + w.kb_end) / 2;
+          for (int kb = w.kb_begin; kb < w.kb_end; ++kb) {
             if (!mbar_wait<PAIR>(bar_s(EMPTY + stage), phase ^ 1u, lim, abort_flag)) {
               ok = false;
               break;
