@@ -1,8 +1,8 @@
 // gemm.cuh -- the persistent, warp-specialised tcgen05 GEMM with the MLP's
 // fused epilogues.
 //
-// One CTA per SM (320 threads, up to 227 KB shared memory, all 512 TMEM
-// columns):
+// One CTA per SM (320 threads, 352 where a warp of its own loads B (Roles), up to
+// 227 KB shared memory, all 512 TMEM columns):
 //   warp 0     TMA producer and tile scheduler: fetches work units from a
 //              global atomic counter (the first one is the cluster id, except
 //              in the one-launch forward), publishes
@@ -154,9 +154,6 @@ __device__ __forceinline__ Work unit_work(const Params& p, const UnitKey& k) {
 // ahead of time (before, its peer and the MMA issuer did too, between one unit's
 // last k-block and the next one's first: 2-4 % of the experts' down projection and
 // dx, 1-2 % of the dense GEMMs with a K-major A, 5 % of those of one or two waves).
-// Not the dense weight gradients, which it made 1-3 % slower, nor the one-launch
-// forward, which claims some units late, nor the 8-bit and recompute kernels, which
-// have no registers for it.
 struct alignas(16) RingUnit {
   int prob, tm, tn, kb_end;  // prob < 0: no more work
   int expert, row0, row_end, kb_begin;
@@ -1318,20 +1315,25 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
   }
 }
 
-// The experts' GEMMs with an MN-major B load it with an eleventh warp.  A weight
-// gradient's k-block is four TMA instructions (six for a single CTA), and one
-// thread issued them in 374 of the k-block's 600 cycles; what it spent between two
-// units (about 3100 cycles) it could not catch up within an expert's few
-// k-blocks, and every unit's first MMAs waited 2200-3800 cycles for their
-// operands (all measured).  With the second warp, and units decoded ahead, they took
-// 641 us in place of 714, and dx and dgated on single CTAs 405 and 272 in place of
-// 444 and 293.
-template <bool B_MN, bool GRP>
-constexpr int gemm_threads() { return NUM_THREADS + (B_MN && GRP ? 32 : 0); }
+// RING: the unit ring carries decoded units (RingUnit), published ahead.  Not in the
+// one-launch forward, which claims some units late, nor in the 8-bit and recompute
+// kernels, which have no registers for it.
+// B_WARP: an eleventh warp loads an MN-major B.  A weight gradient's k-block is four
+// TMA instructions (six for a single CTA), and one thread issued them in 374 of the
+// k-block's 600 cycles; what it spent between two units it could not catch up.  With
+// the second warp (and decoded units, which made the weight gradients alone 1-3 %
+// slower): 16384 x 2048 x 4864 weight gradients 526 -> 498 us, dgated 244 -> 231, dx
+// 359 -> 348; 8192 x 4096 x 14336 1572 -> 1490, 600 -> 575, 1026 -> 997.
+template <int EPI, bool A_MN, bool B_MN, bool GRP>
+struct Roles {
+  static constexpr bool RING = !is_f8(EPI) && !is_recomp(EPI) && EPI != EPI_FWD_FUSED;
+  static constexpr bool B_WARP = RING && B_MN;
+  static constexpr int THREADS = NUM_THREADS + (B_WARP ? 32 : 0);
+};
 
 // ACT: the activation of the activation epilogues (Act; 0 for the others).
 template <int EPI, bool A_MN, bool B_MN, int CG, int ACT, bool GRP>
-__global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp_gemm(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   using C = Cfg<EPI, CG, GRP>;
   constexpr bool PAIR = CG == 2;
@@ -1340,7 +1342,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
                 "no grouped form of this epilogue");
   constexpr bool GRP_ROWS = GRP && !A_MN;  // output tiles are the plan's row tiles
   constexpr bool GRP_SUM = GRP && A_MN;    // every expert's own sum over its rows
-  constexpr bool B_WARP = GRP && B_MN;     // a warp of its own loads B (gemm_threads)
+  constexpr bool B_WARP = Roles<EPI, A_MN, B_MN, GRP>::B_WARP;
   // 8-bit operands: a 128-byte k-block row holds 128 elements (bf16: 64)
   constexpr bool F8 = is_f8(EPI);
   constexpr int KE = F8 ? 2 * BK : BK;
@@ -1362,8 +1364,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
   constexpr int EBAR = DRAIN + 1;
   constexpr int NBAR = EBAR + 2 * NUM_EPI_WARPS;
   // the unit ring: unit numbers, or decoded units
-  constexpr bool RING =
-      GRP || (!A_MN && !is_f8(EPI) && !is_recomp(EPI) && EPI != EPI_FWD_FUSED);
+  constexpr bool RING = Roles<EPI, A_MN, B_MN, GRP>::RING;
   constexpr int RING_AT = RING ? (8 * NBAR + 15) / 16 * 16 : 8 * NBAR;
   constexpr int RING_BYTES = SCHED_SLOTS * static_cast<int>(RING ? sizeof(RingUnit) : sizeof(int));
   static_assert(RING_AT + RING_BYTES + 8 <= 1024, "control area");
@@ -1557,9 +1558,10 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
           // is published while the previous one is still being loaded (at
           // its middle k-block), so that the peer and the consumers find it
           // in the ring when they get there.  Kernels with an MN-major A
-          // (the weight gradients) publish each unit as they start loading
-          // it instead: measured, the early publication made them 1-3 %
-          // slower while it made the others 1-7 % faster.
+          // (the 8-bit weight gradients) publish each unit as they start
+          // loading it instead: measured, the early publication made the
+          // weight gradients 1-3 % slower while it made the others 1-7 %
+          // faster.
           auto publish = [&](int v) -> bool {
             if (!mbar_wait<PAIR>(bar_s(SEMPTY + slot), sphase ^ 1u, lim, abort_flag)) return false;
             sched[slot] = v;
@@ -1802,7 +1804,7 @@ __global__ void __launch_bounds__(gemm_threads<B_MN, GRP>(), 1) k_mlp_gemm(const
       }
     }
   } else if (B_WARP && warp == NUM_THREADS / 32) {
-    // ------------------------------------------- the B loads (see gemm_threads)
+    // ------------------------------------------- the B loads (see Roles)
     if (lane == 0) {
       const uint64_t pol_n = policy_evict_normal(), pol_l = policy_evict_last(),
                      pol_f = policy_evict_first();
@@ -2043,7 +2045,7 @@ cudaError_t launch_gemm(const Params& p, int grid, cudaStream_t stream, bool pdl
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(gemm_threads<B_MN, GRP>(), 1, 1);
+  cfg.blockDim = dim3(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -2078,7 +2080,7 @@ int max_groups() {
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
-  cfg.blockDim = dim3(gemm_threads<B_MN, GRP>(), 1, 1);
+  cfg.blockDim = dim3(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = Cfg<EPI, CG, GRP>::SMEM;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
