@@ -25,10 +25,10 @@
 // a unit is a row tile of one expert against that expert's matrix of a weight
 // stack (3-D tensor maps), rows past the expert's end are neither stored nor read
 // by the epilogue, and a weight gradient sums over its expert's rows (whole K steps
-// of 16).  Measured, 16384 rows over 16 experts of 1024, 2048 x 4864: gate/up 395 us
-// (383 as one dense GEMM), down 184 (176), dgated 238 (244), dx 356 (362), weight
-// gradients 582 (530 for the same sums over one expert's 16384 rows: here 956 MB of
-// gradients go out, after sums of 16 k-blocks each; without their epilogue 538).
+// of 16).  Measured, 16384 rows over 16 experts of 1024, 2048 x 4864: gate/up 398 us
+// (380 as one dense GEMM), down 192 (182), dgated 244 (235), dx 369 (362), weight
+// gradients 596 (514 for the same sums over one expert's 16384 rows: here 956 MB of
+// gradients go out, after sums of 16 k-blocks each; without the epilogue 7 % less).
 // EPI_FWD_FUSED runs the gated forward's two GEMMs in one launch: the
 // epilogue warps count their stored gate/up tiles per 256-row block, and the
 // producer of a down-projection unit waits for its block's count.
