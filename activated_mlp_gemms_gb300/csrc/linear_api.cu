@@ -42,17 +42,18 @@ int linear_act(int act) {
 // Which kernel a product [M, N] over K runs as: 128 x 256 tiles of single CTAs, 256
 // x 256 tiles of CTA pairs, or the skinny kernel's 128 features by up to 256 rows
 // with K shared by clusters.  (A tile policy of 1 or 2 asks for the first two.)
-// The least of three estimates, in units of one 256 x 256 k-block of a pair (0.33
-// us), from the start of a single-CTA launch on: a pair's launch costs 4 more than
-// that; single-CTA MMAs draw more shared-memory bandwidth per flop, 13 % of the time;
-// a skinny tile of mp rows takes (160 + mp) / 400 of a k-block, its CTAs, which are
-// not persistent, 6 a wave and mp / 50 for their end, the exchange of the sums mp /
-// 20, and its start 6 less (2 for dx, whose tiles have the shorter epilogue).  Rows that are no multiple of 128 bytes straddle L2 lines, and those MMAs'
-// larger share of loads costs 40 %.  Measured (skinny / singles / pairs, us): 128 x
-// 768 x 768 7.7 / 8.6 / 9.0, 192 x 768 x 768 9.3 / 8.5 / 8.9, 192 x 1024 x 1024 9.0 /
-// 9.5 / 10, 300 x 4096 x 4096 16.5 / 27 / 25, 512 x 2048 x 8192 22.8 / 27.6 / 28.5,
-// 777 x 14336 x 4096 76 / 78 / 69, 777 x 4864 x 2048 16.5 / 15.7 / 16.6, 1000 x 1024 x
-// 1024 11.2 / 10.0 / 10.4.
+// The least of three estimates, in units of one 256 x 256 k-block of a pair (0.33 us),
+// from the start of a single-CTA launch on: a pair's launch costs 4 more than that;
+// single-CTA MMAs draw more shared-memory bandwidth per flop, 13 % of the time; a
+// skinny tile of mp rows takes (160 + mp) / 400 of a k-block, its CTAs, which are not
+// persistent, 6 a wave and mp / 50 for their end, the exchange of the sums mp / 20,
+// and its start 6 less (2 for dx, whose tiles have the shorter epilogue).  Rows that
+// are no multiple of 128 bytes straddle L2 lines, and those MMAs' larger share of
+// loads costs 40 %.  Measured (skinny / singles / pairs, us): 128 x 768 x 768 7.7 /
+// 8.6 / 9.0, 192 x 768 x 768 9.3 / 8.5 / 8.9, 192 x 1024 x 1024 9.0 / 9.5 / 10, 300 x
+// 4096 x 4096 16.5 / 27 / 25, 512 x 2048 x 8192 22.8 / 27.6 / 28.5, 777 x 14336 x 4096
+// 76 / 78 / 69, 777 x 4864 x 2048 16.5 / 15.7 / 16.6, 1000 x 1024 x 1024 11.2 / 10.0 /
+// 10.4.
 enum Route { ROUTE_SINGLES = 1, ROUTE_PAIRS = 2, ROUTE_SKINNY = 3 };
 Route route(int M, int N, int K, bool whole_lines, bool forward) {
   const int pol = g_tile_policy.load();
