@@ -175,13 +175,13 @@ __device__ __forceinline__ Work ring_get(uint32_t slot) {
 // The units of a problem that run the gated forward epilogue.
 template <int EPI>
 __device__ __forceinline__ bool gated_unit(int prob) {
-  return EPI == EPI_GATED_FWD || (EPI == EPI_FWD_FUSED && prob == 0);
+  return EPI == EPI_GATED_FWD || EPI == EPI_GATED_LOW || (EPI == EPI_FWD_FUSED && prob == 0);
 }
 
 template <int EPI>
 struct EpiTraits {
   // output columns of a tile (EPI_FWD_FUSED: per problem, tile_n_of)
-  static constexpr int TILE_N = (EPI == EPI_GATED_FWD) ? 128 : 256;
+  static constexpr int TILE_N = (EPI == EPI_GATED_FWD || EPI == EPI_GATED_LOW) ? 128 : 256;
   // outputs staged per chunk (gated fwd: a, G, U; act fwd: a, P; dgated: dG,
   // dU, a; dact: dP, a; plain: D) and bytes of one staged 32 x 32 box
   static constexpr int NOUT = (EPI == EPI_GATED_FWD || EPI == EPI_DGATED || EPI == EPI_FWD_FUSED) ? 3
@@ -353,6 +353,59 @@ __device__ __forceinline__ void store_box(const Params& p, const EpiUnit& P, con
 __device__ __forceinline__ void staging_wait_read_but_one(const EpiWarp& e) {
   if (e.lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
   __syncwarp();
+}
+
+// The remainders of two values after their rounding to bf16, in bf16.
+__device__ __forceinline__ uint32_t pack_low(float a, float b) {
+  const float2 h = unpack_bf16x2(pack_bf16x2(a, b));
+  return pack_bf16x2(a - h.x, b - h.y);
+}
+
+template <int ACT>
+__device__ __forceinline__ void epi_gated_low(const Params& p, const EpiUnit& P, const EpiWarp& e,
+                                              uint32_t tb, int col0, int cb, int ce) {
+  const float s = p.scale;
+#pragma unroll 1
+  for (int c = cb; c < ce; c += 32) {
+    const int col = col0 + c;
+    if (col >= P.N) break;  // warp-uniform
+    uint32_t g[32], u[32];
+    __syncwarp();
+    tmem_ld32(tb + c, g);
+    tmem_ld32(tb + 128 + c, u);
+    tmem_wait_ld();
+    uint32_t pa[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      pa[j] = pack_low(s * act_f<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
+                       s * act_f<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
+    staging_acquire(e);
+    stage_bf16(e.stg, e.lane, pa);
+    flush_chunk<1, 2048, false>(p, P, e, col);
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void epi_act_low(const Params& p, const EpiUnit& P, const EpiWarp& e,
+                                            uint32_t tb, int col0, int cb, int ce) {
+  const float s = p.scale;
+#pragma unroll 1
+  for (int c = cb; c < ce; c += 32) {
+    const int col = col0 + c;
+    if (col >= P.N) break;  // warp-uniform
+    uint32_t z[32];
+    __syncwarp();
+    tmem_ld32(tb + c, z);
+    tmem_wait_ld();
+    uint32_t pa[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      pa[j] = pack_low(s * act_f<ACT>(__uint_as_float(z[2 * j])),
+                       s * act_f<ACT>(__uint_as_float(z[2 * j + 1])));
+    staging_acquire(e);
+    stage_bf16(e.stg, e.lane, pa);
+    flush_chunk<1, 2048, false>(p, P, e, col);
+  }
 }
 
 template <int ACT>
@@ -1296,7 +1349,7 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
   pol = polB;
   if constexpr (PART == 1) {
     // A only
-  } else if constexpr (EPI == EPI_GATED_FWD) {
+  } else if constexpr (EPI == EPI_GATED_FWD || EPI == EPI_GATED_LOW) {
     ldw(sB, L.b0, kc, L.n0);
     if constexpr (CG == 1) ldw(sB + 16384, L.b1, kc, L.n0);
   } else {
@@ -1973,6 +2026,10 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
           else epi_plain<EPI_STORE_BF16>(p, P, e, tb, col0, cb, ce);
         } else if constexpr (EPI == EPI_ACT_FWD) {
           epi_act_fwd<ACT>(p, P, e, tb, col0, cb, ce);
+        } else if constexpr (EPI == EPI_GATED_LOW) {
+          epi_gated_low<ACT>(p, P, e, tb, col0, cb, ce);
+        } else if constexpr (EPI == EPI_ACT_LOW) {
+          epi_act_low<ACT>(p, P, e, tb, col0, cb, ce);
         } else if constexpr (EPI == EPI_LINEAR) {
           epi_linear<ACT>(p, P, e, tb, col0, cb, ce, pg);
         } else if constexpr (EPI == EPI_DGATED) {

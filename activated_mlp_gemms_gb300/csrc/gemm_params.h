@@ -65,7 +65,10 @@ enum Epi : int {
   // alpha * residual (in0, bf16, row pitch ld; may be null) -> map 0, and
   // bf16(z) -> map 1 if requested
   EPI_LINEAR = 12,
-  EPI_STORE_F32 = 13  // D = acc (fp32; the experts' down projection of the inference layer)
+  EPI_STORE_F32 = 13,  // D = acc (fp32; the experts' down projection of the inference layer)
+  // The remainder a - bf16(a) of the activation forwards' postact, in bf16 (map 0)
+  EPI_GATED_LOW = 14,
+  EPI_ACT_LOW = 15
 };
 
 __host__ __device__ constexpr bool is_f8(int epi) {

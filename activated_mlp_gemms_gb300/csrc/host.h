@@ -429,6 +429,12 @@ int groups_cached() {
   return v;
 }
 
+// Kernels that are built for single CTAs only (few slots' rows).
+template <int EPI, bool A_MN, bool GRP>
+constexpr bool singles_only() {
+  return EPI == EPI_GATED_LOW || EPI == EPI_ACT_LOW || (EPI == EPI_ACCUM_F32 && !A_MN && GRP);
+}
+
 template <int EPI, bool A_MN, bool B_MN, int ACT, bool GRP = false>
 int run_act(Gemm& g, Call& c, int tag) {
   if (!g.ok) return MLP_ERR_CUDA;
@@ -438,7 +444,9 @@ int run_act(Gemm& g, Call& c, int tag) {
   g.p.clear_status = c.clear_status;
   c.clear_status = false;
   const bool pdl = c.pdl();
-  if (g.cg == 2) {
+  if constexpr (singles_only<EPI, A_MN, GRP>()) {
+    if (g.cg != 1) return MLP_ERR_UNSUPPORTED;
+  } else if (g.cg == 2) {
     const int groups = groups_cached<EPI, A_MN, B_MN, 2, ACT, GRP>();
     if (groups <= 0) return MLP_ERR_CUDA;
     const int n = g.p.total_units < groups ? g.p.total_units : groups;

@@ -224,7 +224,10 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
     for (int r = o + total; r < o + padded; ++r) src[r] = -1;
     plan[L.offsets + tid] = o;
     plan[L.counts + tid] = total;
-    if (tid == 0) plan[L.offsets + E] = used;
+    if (tid == 0) {
+      plan[L.offsets + E] = used;
+      if (L.fine >= 0) plan[L.fine_flag] = 0;
+    }
   }
   for (long long r = used + static_cast<long long>(cta) * SORT_THREADS + tid; r < L.rows;
        r += static_cast<long long>(ncta) * SORT_THREADS)

@@ -161,19 +161,46 @@ __global__ void __launch_bounds__(TOK_THREADS)
                               pack_bf16x2(a[i][4], a[i][5]), pack_bf16x2(a[i][6], a[i][7])));
 }
 
+// y's fp32 rows (in the plan, from the down projection) to the bf16 rows that the
+// caller gets; they stay in the plan for the routing weights' gradient.  A block a
+// row; a few MB at most (up to MOE_FINE_SLOTS slots).
+__global__ void __launch_bounds__(TOK_THREADS)
+    k_moe_fine_rows(int* plan, const MoePlan L, int E, int H, __nv_bfloat16* __restrict__ y) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int r = blockIdx.x;
+  if (r == 0 && threadIdx.x == 0) plan[L.fine_flag] = 1;
+  if (r >= plan[L.offsets + E]) return;
+  const float* f = reinterpret_cast<const float*>(plan + L.fine) + static_cast<size_t>(r) * H;
+  for (int c = 8 * threadIdx.x; c < H; c += TOK_COLS) {
+    const float4 a = *reinterpret_cast<const float4*>(f + c);
+    const float4 b = *reinterpret_cast<const float4*>(f + c + 4);
+    st_global_v4(y + static_cast<size_t>(r) * H + c,
+                 make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                            pack_bf16x2(b.z, b.w)));
+  }
+}
+
 constexpr int BWD_SLOTS = 4;   // slots of a token in one walk over its columns
 constexpr int BWD_PIECES = 2;  // 16-byte pieces of each row a thread has in flight
 
 // TPT threads per token (and the blocks that clear dy's empty rows): the token's
 // gradient row against the rows of up to BWD_SLOTS slots at a time.  A warp per
 // token needs no block-wide sum; a block per token serves few tokens.
-template <bool W_BF16, int TPT>
+// FINE: dweights is a sum of random signs, which cancels, and over a handful of
+// slots y's rounding to bf16 does not average out of it (a median of 0.0028 of
+// dweights' norm, 0.0016 of it the result's own rounding, but in 14 % of the steps of
+// up to eight slots over 0.005 and at worst 0.08).  The plan then has y in fp32
+// (fine, once *have is set): an fp32 value is taken where it rounds to the y given, so
+// that the sum is of that y whatever the plan holds.
+template <bool W_BF16, int TPT, bool FINE>
 __global__ void __launch_bounds__(TOK_THREADS)
     k_moe_combine_bwd(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ y,
                       const int* __restrict__ pos, const int* __restrict__ src,
                       const void* __restrict__ weights, __nv_bfloat16* __restrict__ dy,
-                      void* __restrict__ dweights, long long rows, int T, int top_k, int H,
-                      int per, int token_blocks) {
+                      void* __restrict__ dweights, const float* __restrict__ fine,
+                      const int* have, long long rows, int T, int top_k, int H, int per,
+                      int token_blocks) {
   __shared__ float part[TOK_THREADS / 32][BWD_SLOTS];
   pdl_wait();
   pdl_launch_dependents();
@@ -188,6 +215,7 @@ __global__ void __launch_bounds__(TOK_THREADS)
   const size_t t = static_cast<size_t>(blockIdx.x) * (TOK_THREADS / TPT) + threadIdx.x / TPT;
   if (t >= T) return;  // warp-uniform (TPT = 32) or never
   const __nv_bfloat16* d = dout + t * H;
+  const bool use_fine = FINE && *have != 0;
   for (int j0 = 0; j0 < top_k; j0 += BWD_SLOTS) {
     int r[BWD_SLOTS];
     float w[BWD_SLOTS], acc[BWD_SLOTS];
@@ -230,7 +258,16 @@ __global__ void __launch_bounds__(TOK_THREADS)
             const uint32_t q[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 u = unpack_bf16x2(q[k]);
+              float2 u = unpack_bf16x2(q[k]);
+              if constexpr (FINE) {
+                if (use_fine) {
+                  const float2 z = *reinterpret_cast<const float2*>(
+                      fine + static_cast<size_t>(r[j]) * H + c + 2 * k);
+                  const uint32_t off = pack_bf16x2(z.x, z.y) ^ q[k];
+                  if ((off & 0xffffu) == 0) u.x = z.x;
+                  if ((off >> 16) == 0) u.y = z.y;
+                }
+              }
               acc[j] = fmaf(f[2 * k], u.x, acc[j]);
               acc[j] = fmaf(f[2 * k + 1], u.y, acc[j]);
             }
@@ -341,13 +378,25 @@ cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* p
                                    bool pdl) {
   // a warp per token once that gives every SM eight of them
   const bool warps = T >= 8 * 152;
-  auto kern = w_bf16 ? (warps ? k_moe_combine_bwd<true, 32> : k_moe_combine_bwd<true, TOK_THREADS>)
-                     : (warps ? k_moe_combine_bwd<false, 32> : k_moe_combine_bwd<false, TOK_THREADS>);
+  const bool fine = dweights && L.fine >= 0;  // (then few tokens)
+  auto pick = [&](auto w) {
+    constexpr bool W = decltype(w)::value;
+    return fine    ? k_moe_combine_bwd<W, TOK_THREADS, true>
+           : warps ? k_moe_combine_bwd<W, 32, false>
+                   : k_moe_combine_bwd<W, TOK_THREADS, false>;
+  };
+  auto kern = w_bf16 ? pick(std::true_type{}) : pick(std::false_type{});
   const int tokens = warps ? (T + TOK_THREADS / 32 - 1) / (TOK_THREADS / 32) : T;
   return launch_tok(kern, tokens + (dy ? zero_blocks(L) : 0), stream, pdl,
                     static_cast<const bf*>(dout), static_cast<const bf*>(y), plan + L.pos,
-                    plan + L.src, weights, static_cast<bf*>(dy), dweights, L.rows, T, top_k, H,
-                    zero_rows(L), tokens);
+                    plan + L.src, weights, static_cast<bf*>(dy), dweights,
+                    fine ? reinterpret_cast<const float*>(plan + L.fine) : nullptr,
+                    fine ? plan + L.fine_flag : nullptr, L.rows, T, top_k, H, zero_rows(L), tokens);
+}
+
+cudaError_t launch_moe_fine_rows(int* plan, const MoePlan& L, int E, int H, void* y,
+                                 cudaStream_t stream, bool pdl) {
+  return launch_tok(k_moe_fine_rows, L.rows, stream, pdl, plan, L, E, H, static_cast<bf*>(y));
 }
 
 }  // namespace mlpk

@@ -9,6 +9,7 @@ namespace mlpk {
 
 constexpr int MOE_ALIGN = 16;          // MLP_MOE_ROW_ALIGN
 constexpr int MOE_MAX_EXPERTS = 1024;  // MLP_MOE_MAX_EXPERTS
+constexpr int MOE_FINE_SLOTS = 64;     // MLP_MOE_FINE_SLOTS
 
 // What a row tile of the experts' GEMMs (128 or 256 rows) belongs to: its
 // expert's rows [row, end), whose tiles begin at tile `first`.
@@ -22,10 +23,15 @@ struct MoePlan {
   long long offsets, counts, ntiles;  // [E + 1], [E], [2] (128- and 256-row tiles)
   long long tiles[2];                 // MoeTile lists: 128 rows, 256 rows
   long long tile_cap[2];
-  long long pos, src, ints;
+  long long pos, src;
+  // up to MOE_FINE_SLOTS slots: whether y's fp32 rows are there, and the rows
+  // [rows, H] (-1: no room for them)
+  long long fine_flag, fine;
+  long long ints;
 };
 
-inline MoePlan moe_plan(int T, int E, int top_k) {
+// H = 0: without the fp32 rows of y.
+inline MoePlan moe_plan(int T, int E, int top_k, int H) {
   MoePlan L;
   L.n = static_cast<long long>(T) * top_k;
   const long long used = L.n < E ? L.n : E;
@@ -44,6 +50,12 @@ inline MoePlan moe_plan(int T, int E, int top_k) {
   L.pos = at;
   L.src = L.pos + r4(L.n);
   L.ints = L.src + r4(L.rows);
+  L.fine_flag = L.fine = -1;
+  if (H > 0 && L.n <= MOE_FINE_SLOTS) {
+    L.fine_flag = L.ints;
+    L.fine = L.ints + 4;
+    L.ints = L.fine + L.rows * H;  // (rows are a multiple of 16)
+  }
   return L;
 }
 
@@ -59,6 +71,10 @@ cudaError_t launch_moe_combine_bwd(const void* dout, const void* y, const int* p
                                    const MoePlan& L, int T, int top_k, int H, const void* weights,
                                    bool w_bf16, void* dy, void* dweights, cudaStream_t stream,
                                    bool pdl);
+
+// y[r] = bf16(fp32 row r of the plan) for the rows in use, and the plan's flag.
+cudaError_t launch_moe_fine_rows(int* plan, const MoePlan& L, int E, int H, void* y,
+                                 cudaStream_t stream, bool pdl);
 
 // Up to eight tokens (and 128 slots): the touched experts' weights streamed,
 // straight from the tokens and ids: h[slot] bf16 [n, I] (the slots that use an

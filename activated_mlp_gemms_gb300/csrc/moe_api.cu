@@ -22,7 +22,9 @@ int check_moe(const mlp_moe_t* p) {
   return MLP_OK;
 }
 
-MoePlan plan_of(const mlp_moe_t* p) { return moe_plan(p->T, p->E, p->top_k); }
+MoePlan plan_of(const mlp_moe_t* p) { return moe_plan(p->T, p->E, p->top_k, p->H); }
+// The inference layer's own: no gradient follows.
+MoePlan plan_of_infer(const mlp_moe_t* p) { return moe_plan(p->T, p->E, p->top_k, 0); }
 
 bool w_bf16(const mlp_moe_t* p) { return p->weights_type == MLP_MOE_W_BF16; }
 
@@ -69,7 +71,7 @@ struct Layout {
   size_t plan, xs, y, total; // MLP_MODE_INFER: the plan and the sorted rows
 };
 Layout layout(const mlp_moe_t* p, int mode) {
-  const MoePlan L = plan_of(p);
+  const MoePlan L = plan_of_infer(p);
   Layout w = {};
   size_t at = CTRL_BYTES;
   w.inter = at;
@@ -123,8 +125,9 @@ bool decode_moe(const mlp_moe_t* p) {
 
 // A GEMM over the sorted rows: its output tiles are the plan's.
 struct RowGemm : Gemm {
-  RowGemm(const mlp_moe_t* p, Call& c, const int* plan)
-      : Gemm(device_act(p->act), p->gate_mult * p->down_mult, c.counter(), c.status, moe_cg(p)),
+  RowGemm(const mlp_moe_t* p, Call& c, const int* plan) : RowGemm(p, c, plan, moe_cg(p)) {}
+  RowGemm(const mlp_moe_t* p, Call& c, const int* plan, int cg_)
+      : Gemm(device_act(p->act), p->gate_mult * p->down_mult, c.counter(), c.status, cg_),
         L(plan_of(p)) {
     this->p.tiles = reinterpret_cast<const MoeTile*>(plan + L.tiles[cg - 1]);
     this->p.ntiles = plan + L.ntiles + cg - 1;
@@ -147,7 +150,8 @@ long long row_units(const mlp_moe_t* p, int cols, int tile_n) {
   const int cg = moe_cg(p);
   return plan_of(p).tile_cap[cg - 1] * ((cols + tile_n - 1) / tile_n);
 }
-// The forward's two GEMMs are one wave each.
+// The forward's two GEMMs are one wave each.  (Up to MOE_FINE_SLOTS slots the
+// remainder's two, on single CTAs, are too: an expert's rows are one tile either way.)
 bool fwd_one_wave(const mlp_moe_t* p) {
   const int most = one_wave_units(moe_cg(p));
   return row_units(p, p->I, gated(p) ? 128 : MMA_N) <= most && row_units(p, p->H, MMA_N) <= most;
@@ -183,10 +187,29 @@ int launch_experts_act(const mlp_moe_t* p, Call& c, const int* plan, const void*
   return run_nongated<EPI_ACT_FWD, false, false, true>(g, c, MLP_KERNEL_GATE_UP);
 }
 
-// y32: y is fp32
+// The postact's remainder (EPI_GATED_LOW, EPI_ACT_LOW) over the postact.
+int launch_experts_low(const mlp_moe_t* p, Call& c, const int* plan, const void* xs, const void* Wg,
+                       const void* Wu, void* a) {
+  RowGemm g(p, c, plan, 1);
+  const int mA = g.rows_a(xs, p->H);
+  const int tile_n = gated(p) ? 128 : MMA_N;
+  const int mG = g.kmajor_stack(Wg, p->E, p->I, p->H, tile_n);
+  const int mU = gated(p) ? g.kmajor_stack(Wu, p->E, p->I, p->H, tile_n) : 0;
+  Prob& P = g.add_rows(p->I, p->H, 0, tile_n);
+  P.l2a = L2_EVICT_LAST;
+  P.mapA0 = mA;
+  P.mapB0 = mG;
+  P.mapB1 = mU;
+  g.output_rows(P, 0, a, static_cast<int>(g.L.rows), p->I);
+  return gated(p) ? run_gated<EPI_GATED_LOW, false, false, true>(g, c, MLP_KERNEL_GATE_UP)
+                  : run_nongated<EPI_ACT_LOW, false, false, true>(g, c, MLP_KERNEL_GATE_UP);
+}
+
+// y is bf16, fp32, or fp32 that the product is added to (single CTAs)
+enum class Y { BF16, F32, ADD_F32 };
 int launch_experts_down(const mlp_moe_t* p, Call& c, const int* plan, const void* a, const void* Wd,
-                        void* y, bool y32) {
-  RowGemm g(p, c, plan);
+                        void* y, Y kind) {
+  RowGemm g(p, c, plan, kind == Y::ADD_F32 ? 1 : moe_cg(p));
   const int mA = g.rows_a(a, p->I);
   const int mB = g.kmajor_stack(Wd, p->E, p->H, p->I, g.b_rows());
   Prob& P = g.add_rows(p->H, p->I, 0, MMA_N);
@@ -194,9 +217,11 @@ int launch_experts_down(const mlp_moe_t* p, Call& c, const int* plan, const void
   P.l2b = L2_EVICT_FIRST;
   P.mapA0 = mA;
   P.mapB0 = mB;
-  g.output_rows(P, 0, y, static_cast<int>(g.L.rows), p->H, y32 ? Gemm::ROWS_F32 : Gemm::ROWS_WIDE);
-  return y32 ? run<EPI_STORE_F32, false, false, true>(g, c, MLP_KERNEL_DOWN)
-             : run<EPI_STORE_BF16, false, false, true>(g, c, MLP_KERNEL_DOWN);
+  g.output_rows(P, 0, y, static_cast<int>(g.L.rows), p->H,
+                kind == Y::BF16 ? Gemm::ROWS_WIDE : Gemm::ROWS_F32);
+  return kind == Y::BF16  ? run<EPI_STORE_BF16, false, false, true>(g, c, MLP_KERNEL_DOWN)
+         : kind == Y::F32 ? run<EPI_STORE_F32, false, false, true>(g, c, MLP_KERNEL_DOWN)
+                          : run<EPI_ACCUM_F32, false, false, true>(g, c, MLP_KERNEL_DOWN);
 }
 
 // The sort and the token kernels start while the kernel before them on the
@@ -300,7 +325,7 @@ size_t mlp_moe_workspace_size(const mlp_moe_t* p, int mode) {
   return layout(p, mode).total;
 }
 
-int mlp_moe_experts_fwd(const mlp_moe_t* p, const void* plan, const void* xs, const void* Wg,
+int mlp_moe_experts_fwd(const mlp_moe_t* p, void* plan, const void* xs, const void* Wg,
                         const void* Wu, const void* Wd, void* y, void* G_save, void* U_save,
                         void* ws, size_t ws_bytes, void* stream) {
   MLP_TRY(check_experts(p));
@@ -316,9 +341,21 @@ int mlp_moe_experts_fwd(const mlp_moe_t* p, const void* plan, const void* xs, co
   if (fwd_one_wave(p)) begin_one_wave(c, ws, stream);
   else MLP_TRY(begin_call(c, ws, stream));
   void* a = static_cast<char*>(ws) + layout(p, MLP_MODE_FWD).inter;
-  const int* pl = static_cast<const int*>(plan);
+  int* pl = static_cast<int*>(plan);
+  const MoePlan L = plan_of(p);
   MLP_TRY(launch_experts_act(p, c, pl, xs, Wg, Wu, a, G_save, U_save));
-  return launch_experts_down(p, c, pl, a, Wd, y, false);
+  if (L.fine < 0) return launch_experts_down(p, c, pl, a, Wd, y, Y::BF16);
+  // Few slots: y in fp32, for the routing weights' gradient (k_moe_combine_bwd), from
+  // the postact as two bf16 terms.  (y in fp32 alone leaves 5 % of the steps of up to
+  // eight slots over 0.005.)  The terms go through the postact's buffer one after the
+  // other, so Wg and Wu are read twice: the workspace has room for one.
+  void* y32 = pl + L.fine;
+  MLP_TRY(launch_experts_down(p, c, pl, a, Wd, y32, Y::F32));
+  MLP_TRY(launch_experts_low(p, c, pl, xs, Wg, Wu, a));
+  MLP_TRY(launch_experts_down(p, c, pl, a, Wd, y32, Y::ADD_F32));
+  const bool pdl = c.pdl();
+  return traced(MLP_KERNEL_CONVERT, c.stream,
+                [&] { return launch_moe_fine_rows(pl, L, p->E, p->H, y, c.stream, pdl); });
 }
 
 int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, const void* xs,
@@ -466,7 +503,7 @@ int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const v
   MLP_TRY(need(out));
   MLP_TRY(check_ws(p, MLP_MODE_INFER, ws, ws_bytes));
   const Layout w = layout(p, MLP_MODE_INFER);
-  const MoePlan L = plan_of(p);
+  const MoePlan L = plan_of_infer(p);
   char* base = static_cast<char*>(ws);
   int* plan = reinterpret_cast<int*>(base + w.plan);
   void *a = base + w.inter, *xs = base + w.xs, *y = base + w.y;
@@ -494,7 +531,7 @@ int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const v
     return launch_moe_dispatch(x, plan, L, p->T, p->top_k, p->H, xs, c.stream, pdl);
   }));
   MLP_TRY(launch_experts_act(p, c, plan, xs, Wg, Wu, a, nullptr, nullptr));
-  MLP_TRY(launch_experts_down(p, c, plan, a, Wd, y, true));
+  MLP_TRY(launch_experts_down(p, c, plan, a, Wd, y, Y::F32));
   pdl = c.pdl();
   return traced(MLP_KERNEL_MOE_COMBINE, c.stream, [&] {
     return launch_moe_combine(y, true, plan, L, p->T, p->top_k, p->H, weights, w_bf16(p), residual, out,

@@ -233,8 +233,9 @@ def mlp_moe_experts_fwd(p: Moe, plan, xs, Wg, Wu, Wd, y, G_save=None, U_save=Non
                         stream=None):
     """Each expert's MLP over its rows of xs: y[r] = MLP_e(xs[r]); optionally stores the
     preacts (bf16 [rows, I]) for the backward.  Wg, Wu [E, I, H] (Wu None when non-gated),
-    Wd [E, H, I].  Rows of y past the plan's offsets[E] are not written.  Returns the
-    workspace used."""
+    Wd [E, H, I].  Rows of y past the plan's offsets[E] are not written.  Up to
+    MLP_MOE_FINE_SLOTS slots the plan receives y in fp32 too, for dweights of
+    mlp_moe_combine_bwd.  Returns the workspace used."""
     s = _sizes(p)
     inter = (s.rows[0], p.I)
     ws = _ws(ws, p, MODE_FWD, y.device, stream)

@@ -32,6 +32,7 @@ extern "C" {
 #define MLP_MOE_ROW_ALIGN 16
 #define MLP_MOE_MAX_EXPERTS 1024
 #define MLP_MOE_MAX_TOP_K 64
+#define MLP_MOE_FINE_SLOTS 64
 
 typedef enum { MLP_MOE_W_F32 = 0, MLP_MOE_W_BF16 = 1 } mlp_moe_weight_t;
 
@@ -51,7 +52,10 @@ typedef struct {
 long long mlp_moe_rows(const mlp_moe_t* p);
 
 /* The plan: one caller-owned int32 device buffer (16-byte aligned) that
- * mlp_moe_sort fills and every other call reads. */
+ * mlp_moe_sort fills and every other call reads.  Up to MLP_MOE_FINE_SLOTS slots
+ * (T top_k) it also has room for the experts' results in fp32, rows x H values:
+ * mlp_moe_experts_fwd writes them beside y, and dweights of mlp_moe_combine_bwd
+ * reads them. */
 typedef struct {
   long long ints;     /* size of the plan, in int32 values */
   long long offsets;  /* [E + 1]: first row of each expert; [E] = rows in use */
@@ -82,7 +86,10 @@ int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const v
 
 /* Its gradients: dy[pos[t, j]] = weights[t, j] dout[t], every other row of dy
  * zero; dweights[t, j] = sum_h dout[t,h] y[pos[t, j],h] (fp32 sum; 0 for a
- * dropped slot).  dy or dweights may be NULL (then y, or weights, too). */
+ * dropped slot).  The sum cancels, and over a handful of slots y's rounding to
+ * bf16 shows in it: up to MLP_MOE_FINE_SLOTS slots, after mlp_moe_experts_fwd
+ * with this plan, it takes that call's fp32 values wherever they round to the y
+ * given.  dy or dweights may be NULL (then y, or weights, too). */
 int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, const void* y,
                         const void* weights, void* dy, void* dweights, void* stream);
 
@@ -96,8 +103,10 @@ size_t mlp_moe_workspace_size(const mlp_moe_t* p, int mode);
  *   xs  bf16 [rows,H];  Wg, Wu bf16 [E,I,H] (Wu NULL when non-gated);
  *   Wd  bf16 [E,H,I];   y bf16 [rows,H] out
  *   G_save, U_save  bf16 [rows,I] out, optional: the preacts, for the backward
- * Rows from offsets[E] on are not written. */
-int mlp_moe_experts_fwd(const mlp_moe_t* p, const void* plan, const void* xs, const void* Wg,
+ * Rows from offsets[E] on are not written.  Up to MLP_MOE_FINE_SLOTS slots the
+ * plan receives y in fp32, from a postact in two bf16 terms, and the preacts'
+ * weights are read twice; calls with such a plan do not run at the same time. */
+int mlp_moe_experts_fwd(const mlp_moe_t* p, void* plan, const void* xs, const void* Wg,
                         const void* Wu, const void* Wd, void* y, void* G_save, void* U_save,
                         void* ws, size_t ws_bytes, void* stream);
 
