@@ -1442,13 +1442,14 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s(TFULL + i), 1);
-      mbar_init(bar_s(TEMPTY + i), CG * NUM_EPI_WARPS);
+      mbar_init(bar_s(TEMPTY + i), NUM_EPI_WARPS + (PAIR && leader ? 1 : 0));
     }
     for (int i = 0; i < SCHED_SLOTS; ++i) {
       mbar_init(bar_s(SFULL + i), 1);
-      // MMA issuer + every epilogue warp of the pair + the peer's producer
-      // (+ the warps that load B)
-      mbar_init(bar_s(SEMPTY + i), 1 + CG * NUM_EPI_WARPS + (CG - 1) + (B_WARP ? CG : 0));
+      // this CTA's readers: the MMA issuer (the peer's: its producer), the epilogue
+      // warps, the warp that loads B; the leader's also: the peer's relay
+      mbar_init(bar_s(SEMPTY + i),
+                1 + NUM_EPI_WARPS + (B_WARP ? 1 : 0) + (PAIR && leader ? 1 : 0));
     }
     mbar_init(bar_s(DRAIN), 1);
     if constexpr (EPI == EPI_DGRAD_F8)
@@ -1545,7 +1546,7 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
             }
             w = ring_get(ring_s(slot));
             valid = w.prob >= 0;
-            mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
+            mbar_arrive(bar_s(SEMPTY + slot));
             if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           }
           if (!valid) break;
@@ -1703,7 +1704,7 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
             break;
           }
           const int v = sched[slot];
-          mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
+          mbar_arrive(bar_s(SEMPTY + slot));
           if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
           if (v < 0) break;
           const Work w = decode_unit(p, v);
@@ -1855,6 +1856,35 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
           mbar_wait<PAIR>(bar_s(DRAIN), 0, 10000000ull, &never);
         }
       }
+    } else if (PAIR && lane == 0) {
+      // ------------------------------------------------- the peer's relay
+      // Tells the leader that the peer has read a ring slot, and an accumulator.
+      // Its readers arrive at their own CTA's barriers; one thread waits for each
+      // phase of those and arrives at the leader's with a release at cluster scope,
+      // which orders all of the readers' reads before the leader's overwrite.  (That
+      // release takes about 2500 cycles in a thread whose writes are under way: twice
+      // a unit in each epilogue warp and once in the producer without the relay.)
+      int slot = 0, acc = 0;
+      uint32_t sphase = 0, aphase = 0;
+      bool ok = true;
+      while (ok) {
+        if (!mbar_wait<PAIR>(bar_s(SFULL + slot), sphase, lim, abort_flag)) { ok = false; break; }
+        const int unit = RING ? ring_get(ring_s(slot)).prob : sched[slot];
+        if (!mbar_wait(bar_s(SEMPTY + slot), sphase, lim, abort_flag)) { ok = false; break; }
+        mbar_arrive_cluster(lead(bar_s(SEMPTY + slot)));
+        if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
+        if (unit < 0) break;
+        // (the fused recomputes read two accumulators a unit)
+        for (int i = 0; i < (is_recomp(EPI) ? 2 : 1); ++i) {
+          if (!mbar_wait(bar_s(TEMPTY + acc), aphase, lim, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          tc_fence_before();
+          mbar_arrive_cluster(lead(bar_s(TEMPTY + acc)));
+          acc ^= 1;
+          if (acc == 0) aphase ^= 1u;
+        }
+      }
+      if (!ok) record_timeout(p, abort_flag);
     }
   } else if (B_WARP && warp == NUM_THREADS / 32) {
     // ------------------------------------------- the B loads (see Roles)
@@ -1871,8 +1901,7 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
           break;
         }
         const Work w = ring_get(ring_s(slot));
-        if (leader) mbar_arrive(bar_s(SEMPTY + slot));
-        else mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
+        mbar_arrive(bar_s(SEMPTY + slot));
         if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
         if (w.prob < 0) break;
         const UnitLoads L = unit_loads<EPI, CG, GRP, A_MN>(p, p.prob[w.prob], w, rank);
@@ -1942,8 +1971,7 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
       }
       __syncwarp();
       if (lane == 0) {
-        if (leader) mbar_arrive(bar_s(SEMPTY + slot));
-        else mbar_arrive_cluster_reads(lead(bar_s(SEMPTY + slot)));
+        mbar_arrive(bar_s(SEMPTY + slot));
       }
       if (++slot == SCHED_SLOTS) { slot = 0; sphase ^= 1u; }
       if (unit < 0) break;
@@ -1989,8 +2017,7 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (leader) mbar_arrive(bar_s(TEMPTY + acc));
-          else mbar_arrive_cluster_reads(lead(bar_s(TEMPTY + acc)));
+          mbar_arrive(bar_s(TEMPTY + acc));
         }
         acc ^= 1;
         if (acc == 0) aphase ^= 1u;
@@ -2060,8 +2087,7 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (leader) mbar_arrive(bar_s(TEMPTY + acc));
-        else mbar_arrive_cluster_reads(lead(bar_s(TEMPTY + acc)));
+        mbar_arrive(bar_s(TEMPTY + acc));
       }
       acc ^= 1;
       if (acc == 0) aphase ^= 1u;

@@ -119,19 +119,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// The same where the arrival publishes no writes: it only says that this CTA's reads
-// (of a ring slot; of an accumulator, after tcgen05.wait::ld) are done.  The release
-// orders them before the arrival within this SM, where both are; at cluster scope it
-// also waits for the thread's writes to be performed there, about 2500 cycles.
-__device__ __forceinline__ void mbar_arrive_cluster_reads(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
 // An arrival that also tells the barrier to expect `bytes`, and the asynchronous
-// stores that bring them: the barrier's phase ends when they have landed, so the
-// sender waits for nothing.
+// stores that bring them: the barrier's phase ends when they have landed (their
+// completion is a release at cluster scope), so the arrival itself orders nothing and
+// the sender waits for nothing.
 __device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
                    cluster_addr),
                "r"(bytes)
                : "memory");
