@@ -181,6 +181,16 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty_on(n, dtype, device, stream):
+    """n fresh values for a call on `stream` (None: the current one): of that stream's
+    own memory, which work queued on another stream neither still uses nor gets before
+    that stream is done with it."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
 # Workspaces of the calls that are given none, kept where they are small: a
 # fresh tensor costs 3-5 us a call, more than the smallest calls themselves.
 # One for each device, stream and host thread: calls that share one are ordered.
@@ -191,10 +201,7 @@ _kept = {}
 def _call_workspace(n, device, stream):
     """A workspace of n bytes for a call on `stream` (None: the current one)."""
     if stream is not None or n > _KEEP_BYTES or torch._C._cuda_isCurrentStreamCapturing():
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        if stream is not None:  # its memory is reused once that stream is done with it
-            ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
-        return ws
+        return _empty_on(n, torch.uint8, device, stream)
     key = (device.index, _stream(None), threading.get_ident())
     ws = _kept.get(key)
     if ws is None or ws.numel() < n:
@@ -227,9 +234,12 @@ def alloc_workspace(prob: Problem, mode: int, device=None) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _ws(ws, prob, mode, device):
+def _ws(ws, prob, mode, device, stream):
     if ws is None:
-        ws = alloc_workspace(prob, mode, device)
+        n = mlp_workspace_size(prob, mode)
+        if n == 0:
+            raise MlpError(-1, "mlp_workspace_size")
+        ws = _empty_on(n, torch.uint8, device, stream)
     if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return ws
@@ -238,7 +248,7 @@ def _ws(ws, prob, mode, device):
 def mlp_fwd(prob: Problem, x, Wg, Wu, Wd, out, G_save=None, U_save=None, ws=None, stream=None):
     """Training forward: out = down_mult * Wd (gate_mult * act(x Wg^T) * (x Wu^T)); optionally
     stores the preacts G = x Wg^T, U = x Wu^T (bf16 [M,I]).  Returns the workspace used."""
-    ws = _ws(ws, prob, MODE_FWD, x.device)
+    ws = _ws(ws, prob, MODE_FWD, x.device, stream)
     rc = lib().mlp_fwd(ctypes.byref(prob), _ptr(x, name="x"), _ptr(Wg, name="Wg"),
                        _ptr(Wu, name="Wu"), _ptr(Wd, name="Wd"), _ptr(out, name="out"),
                        _ptr(G_save, name="G_save"), _ptr(U_save, name="U_save"),
@@ -249,7 +259,7 @@ def mlp_fwd(prob: Problem, x, Wg, Wu, Wd, out, G_save=None, U_save=None, ws=None
 
 def mlp_fwd_infer(prob: Problem, x, Wg, Wu, Wd, out, ws=None, stream=None):
     """No-grad forward; stores no intermediates outside the workspace."""
-    ws = _ws(ws, prob, MODE_INFER, x.device)
+    ws = _ws(ws, prob, MODE_INFER, x.device, stream)
     rc = lib().mlp_fwd_infer(ctypes.byref(prob), _ptr(x, name="x"), _ptr(Wg, name="Wg"),
                              _ptr(Wu, name="Wu"), _ptr(Wd, name="Wd"), _ptr(out, name="out"),
                              ws.data_ptr(), ws.numel(), _stream(stream))
@@ -266,7 +276,7 @@ def mlp_bwd(prob: Problem, dout, x, Wg, Wu, Wd, G, U, dx=None, dWg=None, dWu=Non
     """Backward from saved preacts G, U (overwritten with dG, dU).  Outputs that are None
     are skipped; weight gradients are bf16 (overwritten) or fp32 (+= in place) when
     fuse_grad_accum."""
-    ws = _ws(ws, prob, MODE_BWD, x.device)
+    ws = _ws(ws, prob, MODE_BWD, x.device, stream)
     wd = _wdt(fuse_grad_accum)
     rc = lib().mlp_bwd(ctypes.byref(prob), _ptr(dout, name="dout"), _ptr(x, name="x"),
                        _ptr(Wg, name="Wg"), _ptr(Wu, name="Wu"), _ptr(Wd, name="Wd"),
@@ -280,7 +290,7 @@ def mlp_bwd(prob: Problem, dout, x, Wg, Wu, Wd, G, U, dx=None, dWg=None, dWu=Non
 def mlp_bwd_recompute(prob: Problem, dout, x, Wg, Wu, Wd, dx=None, dWg=None, dWu=None, dWd=None,
                       fuse_grad_accum=False, ws=None, stream=None):
     """Backward that recomputes the preacts from x (save-only-x training)."""
-    ws = _ws(ws, prob, MODE_BWD_RECOMPUTE, x.device)
+    ws = _ws(ws, prob, MODE_BWD_RECOMPUTE, x.device, stream)
     wd = _wdt(fuse_grad_accum)
     rc = lib().mlp_bwd_recompute(ctypes.byref(prob), _ptr(dout, name="dout"), _ptr(x, name="x"),
                                  _ptr(Wg, name="Wg"), _ptr(Wu, name="Wu"), _ptr(Wd, name="Wd"),
@@ -295,9 +305,9 @@ def mlp_block_fwd(prob: Problem, blk: Block, x, Wg, Wu, Wd, y, G_save=None, U_sa
                   rstd=None, ws=None, stream=None):
     """The MLP block: y = resid_lambda x + post_lambda MLP(RMSNorm(x)).  Returns
     (rstd, ws): the fp32 per-token 1/r the backward takes, and the workspace."""
-    ws = _ws(ws, prob, MODE_FWD, x.device)
+    ws = _ws(ws, prob, MODE_FWD, x.device, stream)
     if rstd is None:
-        rstd = torch.empty(prob.M, dtype=torch.float32, device=x.device)
+        rstd = _empty_on(prob.M, torch.float32, x.device, stream)
     rc = lib().mlp_block_fwd(ctypes.byref(prob), ctypes.byref(blk), _ptr(x, name="x"),
                              _ptr(Wg, name="Wg"), _ptr(Wu, name="Wu"), _ptr(Wd, name="Wd"),
                              _ptr(y, name="y"), _ptr(G_save, name="G_save"),
@@ -310,7 +320,7 @@ def mlp_block_fwd(prob: Problem, blk: Block, x, Wg, Wu, Wd, y, G_save=None, U_sa
 def mlp_block_bwd(prob: Problem, blk: Block, dy, x, Wg, Wu, Wd, G, U, rstd, dx=None, dWg=None,
                   dWu=None, dWd=None, fuse_grad_accum=False, ws=None, stream=None):
     """Backward of mlp_block_fwd from its saved G, U (overwritten) and rstd."""
-    ws = _ws(ws, prob, MODE_BWD, x.device)
+    ws = _ws(ws, prob, MODE_BWD, x.device, stream)
     wd = _wdt(fuse_grad_accum)
     rc = lib().mlp_block_bwd(ctypes.byref(prob), ctypes.byref(blk), _ptr(dy, name="dy"),
                              _ptr(x, name="x"), _ptr(Wg, name="Wg"), _ptr(Wu, name="Wu"),
@@ -344,7 +354,7 @@ def mlp_fp8_fwd(prob: Problem, x8, W1_8, W2_8, scales, out, a8_save=None, amax_a
                 stream=None, pre_save=None):
     """e4m3 forward of the ReLU^2 MLP; scales = fp32 device tensor {sx, s1, s2, s_post, ...};
     pre_save (bf16 [M, I]) receives the preact for mlp_fp8_bwd."""
-    ws = _ws(ws, prob, MODE_FP8_FWD, out.device)
+    ws = _ws(ws, prob, MODE_FP8_FWD, out.device, stream)
     rc = lib().mlp_fp8_fwd(ctypes.byref(prob), _u8(x8, "x8"), _u8(W1_8, "W1_8"), _u8(W2_8, "W2_8"),
                            _ptr(scales, torch.float32, "scales"), _ptr(out, name="out"),
                            _u8(a8_save, "a8_save"), _ptr(pre_save, name="pre_save"),
@@ -358,7 +368,7 @@ def mlp_fp8_bwd(prob: Problem, dout, x8, W1_8, W2_8, pre, a8, scales, dx=None, d
                 amax_dpre=None, ws=None, stream=None):
     """8-bit backward of the ReLU^2 MLP (e5m2 gradients); scales = fp32 [6] device tensor
     {sx, s1, s2, s_post, sg, s_dpre}; dx [M,H], dW1 [I,H], dW2 [H,I] bf16 outputs."""
-    ws = _ws(ws, prob, MODE_FP8_BWD, dout.device)
+    ws = _ws(ws, prob, MODE_FP8_BWD, dout.device, stream)
     if scales is not None and scales.numel() < 6:
         raise ValueError("scales must hold {sx, s1, s2, s_post, sg, s_dpre}")
     rc = lib().mlp_fp8_bwd(ctypes.byref(prob), _ptr(dout, name="dout"), _u8(x8, "x8"),
