@@ -15,6 +15,8 @@
 // Bound by the latency of its phases (a few cluster barriers and two passes
 // over ids), not by its bytes (12 a slot): 5 us for 8198 slots over 8 experts, 13
 // us for 65536 over 64.
+#include <atomic>
+
 #include "gemm_params.h"
 #include "moe.h"
 #include "ptx.cuh"
@@ -252,9 +254,18 @@ cudaError_t launch_moe_sort(const int* ids, int* plan, const MoePlan& L, int E, 
   int bits = 1;  // of the keys 0 .. E (E: dropped)
   while ((E >> bits) != 0) ++bits;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_moe_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // once a device, to the most that any call takes: the attribute is the kernel's, and
+    // another thread's call between this and the launch must not lower it
+    static std::atomic<unsigned> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 31 || !(configured.load() & (1u << dev))) {
+      e = cudaFuncSetAttribute(k_moe_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(sort_smem(MOE_MAX_EXPERTS)));
+      if (e != cudaSuccess) return e;
+      if (dev < 31) configured.fetch_or(1u << dev);
+    }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
