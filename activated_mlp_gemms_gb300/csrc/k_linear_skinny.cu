@@ -95,8 +95,10 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
   const uint32_t done = smem_u32(bar + 2 * SK_MAX_STAGES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int share = gridDim.y, rank = blockIdx.y;  // the cluster that shares this block's K
-  const int row0 = blockIdx.x * SK_ROWS;  // the features
-  const int m0 = blockIdx.z * mp, m1 = min(M, m0 + mp);
+  // x: the blocks of features, a row tile after the other (y and z end at 65535)
+  const int blocks = (N + SK_ROWS - 1) / SK_ROWS, tile = blockIdx.x / blocks;
+  const int row0 = (blockIdx.x - tile * blocks) * SK_ROWS;  // the features
+  const int m0 = tile * mp, m1 = min(M, m0 + mp);
   const int kbs = (K + BK - 1) / BK;
   const int kb0 = static_cast<int>(static_cast<long long>(kbs) * rank / share);
   const int kb1 = static_cast<int>(static_cast<long long>(kbs) * (rank + 1) / share);
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
   const uint32_t tmem = *tmem_s;
   pdl_wait();
   pdl_launch_dependents();
-  if (clear && blockIdx.x == 0 && rank == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0;
+  if (clear && blockIdx.x == 0 && rank == 0 && threadIdx.x == 0) *status = 0;
   auto give_up = [&] {
     *abort_flag = 1;
     atomicExch(status, SK_TIMEOUT);
@@ -361,7 +363,7 @@ cudaError_t launch(const CUtensorMap& map_w, const CUtensorMap& map_x, const bf*
          blocks <= resident_clusters(kern, 2 * share))
     share *= 2;
   Config k;
-  k.grid = dim3(sh.blocks, share, sh.tiles);
+  k.grid = dim3(blocks, share);
   k.mp = sh.mp;
   // more blocks than SMs: two CTAs an SM, one filling its ring while the other
   // finishes

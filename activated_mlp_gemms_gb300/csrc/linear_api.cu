@@ -25,6 +25,9 @@ int check_linear(const mlp_linear_t* p) {
   if (p->N % 8 || p->K % 8 || p->ldx % 8 || p->ldr % 8 || p->ldo % 8) return MLP_ERR_ALIGNMENT;
   if ((long long)p->M * p->N >= (1LL << 40) || (long long)p->M * p->K >= (1LL << 40))
     return MLP_ERR_UNSUPPORTED;
+  // rows and columns rounded up to whole tiles are 32-bit
+  constexpr int MOST = 0x7fffffff - 1023;
+  if (p->M > MOST || p->N > MOST || p->K > MOST) return MLP_ERR_UNSUPPORTED;
   return MLP_OK;
 }
 

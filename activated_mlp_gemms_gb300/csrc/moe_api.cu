@@ -16,7 +16,8 @@ int check_moe(const mlp_moe_t* p) {
     return MLP_ERR_INVALID_ARG;
   if (p->H % 8) return MLP_ERR_ALIGNMENT;
   if (p->E > MLP_MOE_MAX_EXPERTS || p->top_k > MLP_MOE_MAX_TOP_K) return MLP_ERR_UNSUPPORTED;
-  // rows and slots are 32-bit; the token kernels' grids too
+  // rows and slots are 32-bit, the token kernels' grids and rounded-up widths too
+  if (p->H > 0x7fffffff - 8191) return MLP_ERR_UNSUPPORTED;
   if ((long long)p->T * p->top_k > (1LL << 30) || (long long)p->T * p->H >= (1LL << 40))
     return MLP_ERR_UNSUPPORTED;
   return MLP_OK;
@@ -50,6 +51,7 @@ int check_experts(const mlp_moe_t* p) {
   if (p->I <= 0 || p->act < MLP_ACT_SWIGLU || p->act > MLP_ACT_GLU) return MLP_ERR_INVALID_ARG;
   if (!std::isfinite(p->gate_mult) || !std::isfinite(p->down_mult)) return MLP_ERR_INVALID_ARG;
   if (p->I % 8) return MLP_ERR_ALIGNMENT;
+  if (p->I > 0x7fffffff - 8191) return MLP_ERR_UNSUPPORTED;
   const MoePlan L = plan_of(p);
   // 32-bit work units (three weight gradients of 128 x 256 tiles at most)
   const long long tiles = out_tiles(p->I, p->H, 1) + out_tiles(p->H, p->I, 1);
