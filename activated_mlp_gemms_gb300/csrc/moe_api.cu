@@ -265,6 +265,7 @@ int mlp_moe_dispatch(const mlp_moe_t* p, const void* plan, const void* x, void* 
   MLP_TRY(need(plan));
   MLP_TRY(need(x));
   MLP_TRY(need(xs));
+  if (xs == x) return MLP_ERR_INVALID_ARG;  // other blocks still read x
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_DISPATCH, s, [&] {
     return launch_moe_dispatch(x, static_cast<const int*>(plan), plan_of(p), p->T, p->top_k, p->H,
@@ -278,6 +279,7 @@ int mlp_moe_dispatch_bwd(const mlp_moe_t* p, const void* plan, const void* dxs, 
   MLP_TRY(need(plan));
   MLP_TRY(need(dxs));
   MLP_TRY(need(dx));
+  if (dx == dxs) return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_COMBINE, s, [&] {
     return launch_moe_combine(dxs, false, static_cast<const int*>(plan), plan_of(p), p->T, p->top_k, p->H,
@@ -293,6 +295,7 @@ int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const v
   MLP_TRY(need_w(p, weights));
   MLP_TRY(opt(residual));
   MLP_TRY(need(out));
+  if (out == y) return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_COMBINE, s, [&] {
     return launch_moe_combine(y, false, static_cast<const int*>(plan), plan_of(p), p->T, p->top_k, p->H,
@@ -314,6 +317,7 @@ int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, 
     MLP_TRY(need(y));
   }
   if (!dy && !dweights) return MLP_OK;
+  if (dy && (dy == dout || (dweights && dy == y))) return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_MOE_COMBINE_BWD, s, [&] {
     return launch_moe_combine_bwd(dout, y, static_cast<const int*>(plan), plan_of(p), p->T,
@@ -384,6 +388,8 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
   MLP_TRY(check_ws(p, MLP_MODE_BWD, ws, ws_bytes));
   const bool need_dact = dxs || dWg || dWu;
   if (!need_dact && !dWd) return MLP_OK;
+  // the weight gradients still read dy and xs while dxs is stored
+  if (dxs && ((dWd && dxs == dy) || ((dWg || dWu) && dxs == xs))) return MLP_ERR_INVALID_ARG;
   const int cgw = p->H > BM && p->I > BM ? moe_cg(p) : pick_cg(p->H < p->I ? p->H : p->I);
   const long long w_units = ((dWg ? 1 : 0) + (dWu ? 1 : 0)) * out_tiles(p->I, p->H, cgw) +
                             (dWd ? 1 : 0) * out_tiles(p->H, p->I, cgw);

@@ -70,17 +70,17 @@ int mlp_moe_plan_layout(const mlp_moe_t* p, mlp_moe_plan_t* layout);
 int mlp_moe_sort(const mlp_moe_t* p, const int* ids, void* plan, void* stream);
 
 /* xs[pos[t, j]] = x[t]; every other row of xs is zero.
- *   x bf16 [T,H] in, xs bf16 [rows,H] out */
+ *   x bf16 [T,H] in, xs bf16 [rows,H] out, not x */
 int mlp_moe_dispatch(const mlp_moe_t* p, const void* plan, const void* x, void* xs, void* stream);
 
 /* Its gradient: dx[t] = sum_j dxs[pos[t, j]] (fp32 sum, rounded once).
- *   dxs bf16 [rows,H] in, dx bf16 [T,H] out */
+ *   dxs bf16 [rows,H] in, dx bf16 [T,H] out, not dxs */
 int mlp_moe_dispatch_bwd(const mlp_moe_t* p, const void* plan, const void* dxs, void* dx,
                          void* stream);
 
 /* out[t] = residual[t] + sum_j weights[t, j] y[pos[t, j]] (fp32, rounded once).
  *   y bf16 [rows,H], weights [T,top_k] (weights_type, aligned as that type),
- *   residual bf16 [T,H] or NULL, out bf16 [T,H] (may be residual itself) */
+ *   residual bf16 [T,H] or NULL, out bf16 [T,H] (may be residual itself, not y) */
 int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const void* weights,
                     const void* residual, void* out, void* stream);
 
@@ -89,7 +89,8 @@ int mlp_moe_combine(const mlp_moe_t* p, const void* plan, const void* y, const v
  * dropped slot).  The sum cancels, and over a handful of slots y's rounding to
  * bf16 shows in it: up to MLP_MOE_FINE_SLOTS slots, after mlp_moe_experts_fwd
  * with this plan, it takes that call's fp32 values wherever they round to the y
- * given.  dy or dweights may be NULL (then y, or weights, too). */
+ * given.  dy NULL: weights may be NULL; dweights NULL: y may be NULL.  dy is
+ * neither dout nor y. */
 int mlp_moe_combine_bwd(const mlp_moe_t* p, const void* plan, const void* dout, const void* y,
                         const void* weights, void* dy, void* dweights, void* stream);
 
@@ -112,7 +113,8 @@ int mlp_moe_experts_fwd(const mlp_moe_t* p, void* plan, const void* xs, const vo
 
 /* Its gradients, from the saved preacts (which become dG, dU, as in mlp_bwd):
  *   dy   bf16 [rows,H] in, with zero padding rows (mlp_moe_combine_bwd's)
- *   dxs  bf16 [rows,H] out; dWg, dWu [E,I,H], dWd [E,H,I]: bf16, or with
+ *   dxs  bf16 [rows,H] out, neither dy nor xs where weight gradients are asked
+ *        for; dWg, dWu [E,I,H], dWd [E,H,I]: bf16, or with
  *        fuse_grad_accum = 1 fp32 that the gradients are added to; each NULL
  *        to skip.  An expert without rows gets a zero gradient.
  * xs has zero padding rows (mlp_moe_dispatch's).  dxs is not written from
