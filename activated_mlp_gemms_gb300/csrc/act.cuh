@@ -13,10 +13,13 @@
 // silu and silu'; the epilogues' arithmetic is bound by instruction issue,
 // and this takes SwiGLU's fused epilogues from two special-function
 // instructions per element to one).  The GELU's tanh is CUDA's tanhf, in the
-// dense MLP; the linear layer's and the experts' GELU (ACT_GELU_HW) takes the
-// hardware tanh (measured on a GB300: at most 7.6e-6 from the fp64 tanh over
-// [-100, 100], so 3.8e-6 |z| in the result; it takes 5 % off the linear
-// training step of 8192 x 4864 x 2048).
+// dense MLP.
+// The _EXP forms keep the relative error small where the result is (for z below
+// -3 an absolute error of 4e-6 in the sigmoid is percents of it, and 1 + tanh
+// cancels): sigmoid(z) = 1 / (1 + e^-z) with the hardware's exponential and
+// reciprocal, and gelu_tanh(z) = z sigmoid(2u), u = c (z + 0.044715 z^3), since
+// (1 + tanh(u)) / 2 = sigmoid(2u).  The linear layer, whose result the activation
+// is, takes all three; the experts take the GELU's.
 #pragma once
 #include "gemm_params.h"
 
@@ -32,6 +35,15 @@ __device__ __forceinline__ float sigmoid_f(float z) {
   return fmaf(0.5f, tanh_hw(0.5f * z), 0.5f);
 }
 
+// sigmoid(x) = 1 / (1 + 2^-t), t = x log2(e)
+__device__ __forceinline__ float sigmoid_exp2(float t) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+constexpr float LOG2_E = 1.4426950408889634f;
+
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
   if constexpr (ACT == ACT_NONE) {
@@ -45,10 +57,13 @@ __device__ __forceinline__ float act_f(float z) {
     return fmaxf(z, 0.0f);
   } else if constexpr (ACT == ACT_SIGMOID) {
     return sigmoid_f(z);
-  } else if constexpr (ACT == ACT_GELU_HW) {
-    const float c = 0.7978845608028654f;  // sqrt(2/pi)
-    const float h = 0.5f * z;
-    return fmaf(h, tanh_hw(c * fmaf(0.044715f * z, z * z, z)), h);
+  } else if constexpr (ACT == ACT_SILU_EXP) {
+    return z * sigmoid_exp2(LOG2_E * z);
+  } else if constexpr (ACT == ACT_SIGMOID_EXP) {
+    return sigmoid_exp2(LOG2_E * z);
+  } else if constexpr (ACT == ACT_GELU_EXP) {
+    const float c2 = 2.0f * 0.7978845608028654f;  // 2 sqrt(2/pi)
+    return z * sigmoid_exp2(LOG2_E * c2 * fmaf(0.044715f * z, z * z, z));
   } else {
     const float c = 0.7978845608028654f;  // sqrt(2/pi)
     float t = tanhf(c * fmaf(0.044715f * z, z * z, z));
@@ -77,13 +92,22 @@ __device__ __forceinline__ void act_and_grad(float z, float& a, float& da) {
     const float s = sigmoid_f(z);
     a = s;
     da = s * (1.0f - s);
-  } else if constexpr (ACT == ACT_GELU_HW) {
-    const float c = 0.7978845608028654f;
+  } else if constexpr (ACT == ACT_SILU_EXP) {
+    const float s = sigmoid_exp2(LOG2_E * z);
+    a = z * s;
+    da = s * fmaf(z, 1.0f - s, 1.0f);
+  } else if constexpr (ACT == ACT_SIGMOID_EXP) {
+    const float s = sigmoid_exp2(LOG2_E * z);
+    a = s;
+    da = s * (1.0f - s);
+  } else if constexpr (ACT == ACT_GELU_EXP) {
+    // with s = sigmoid(2u): s + z s (1 - s) 2u',  u' = c (1 + 3 * 0.044715 z^2)
+    const float c2 = 2.0f * 0.7978845608028654f;
     const float k = 0.044715f;
-    const float z2 = z * z, h = 0.5f * z;
-    const float t = tanh_hw(c * fmaf(k * z, z2, z));
-    a = fmaf(h, t, h);
-    da = fmaf(0.5f, t, 0.5f) + h * fmaf(-t, t, 1.0f) * fmaf(3.0f * k * c, z2, c);
+    const float z2 = z * z;
+    const float s = sigmoid_exp2(LOG2_E * c2 * fmaf(k * z, z2, z));
+    a = z * s;
+    da = fmaf(a * (1.0f - s), fmaf(3.0f * k * c2, z2, c2), s);
   } else {
     const float c = 0.7978845608028654f;
     const float k = 0.044715f;

@@ -84,8 +84,8 @@ __host__ __device__ constexpr bool is_recomp(int epi) {
 constexpr int F8_E4M3 = 0, F8_E5M2 = 1;
 
 // The function applied to the gate (gated MLPs) or to the preact (non-gated).
-// (ACT_NONE: the linear layer without one.  ACT_GELU_HW: the tanh GELU on the
-// hardware tanh, for the linear layer's and the experts' kernels.)
+// (ACT_NONE: the linear layer without one.  _EXP: the forms of act.cuh on the
+// exponential, for the linear layer's and, the GELU's, the experts' kernels.)
 enum Act : int {
   ACT_SILU = 0,
   ACT_RELU_SQ = 1,
@@ -93,7 +93,9 @@ enum Act : int {
   ACT_RELU = 3,
   ACT_SIGMOID = 4,
   ACT_NONE = 5,
-  ACT_GELU_HW = 6
+  ACT_GELU_EXP = 6,
+  ACT_SILU_EXP = 7,
+  ACT_SIGMOID_EXP = 8
 };
 
 // One GEMM D[M,N] = sum_k A[m,k] B[n,k] of a (possibly grouped) launch.

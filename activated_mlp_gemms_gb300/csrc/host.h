@@ -477,7 +477,7 @@ template <int EPI, bool A_MN, bool B_MN, bool GRP = false>
 int run_gated(Gemm& g, Call& c, int tag) {
   switch (g.p.act) {
     case ACT_RELU: return run_act<EPI, A_MN, B_MN, ACT_RELU, GRP>(g, c, tag);
-    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, GRP ? ACT_GELU_HW : ACT_GELU_TANH, GRP>(g, c, tag);
+    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, GRP ? ACT_GELU_EXP : ACT_GELU_TANH, GRP>(g, c, tag);
     case ACT_SIGMOID: return run_act<EPI, A_MN, B_MN, ACT_SIGMOID, GRP>(g, c, tag);
     default: return run_act<EPI, A_MN, B_MN, ACT_SILU, GRP>(g, c, tag);
   }
@@ -486,7 +486,7 @@ template <int EPI, bool A_MN, bool B_MN, bool GRP = false>
 int run_nongated(Gemm& g, Call& c, int tag) {
   switch (g.p.act) {
     case ACT_RELU: return run_act<EPI, A_MN, B_MN, ACT_RELU, GRP>(g, c, tag);
-    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, GRP ? ACT_GELU_HW : ACT_GELU_TANH, GRP>(g, c, tag);
+    case ACT_GELU_TANH: return run_act<EPI, A_MN, B_MN, GRP ? ACT_GELU_EXP : ACT_GELU_TANH, GRP>(g, c, tag);
     default: return run_act<EPI, A_MN, B_MN, ACT_RELU_SQ, GRP>(g, c, tag);
   }
 }

@@ -40,11 +40,11 @@ cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t s
 template <class F>
 cudaError_t with_act(int act, F&& f) {
   switch (act) {
-    case ACT_SILU: return f(std::integral_constant<int, ACT_SILU>{});
+    case ACT_SILU_EXP: return f(std::integral_constant<int, ACT_SILU_EXP>{});
     case ACT_RELU_SQ: return f(std::integral_constant<int, ACT_RELU_SQ>{});
-    case ACT_GELU_HW: return f(std::integral_constant<int, ACT_GELU_HW>{});
+    case ACT_GELU_EXP: return f(std::integral_constant<int, ACT_GELU_EXP>{});
     case ACT_RELU: return f(std::integral_constant<int, ACT_RELU>{});
-    case ACT_SIGMOID: return f(std::integral_constant<int, ACT_SIGMOID>{});
+    case ACT_SIGMOID_EXP: return f(std::integral_constant<int, ACT_SIGMOID_EXP>{});
     default: return f(std::integral_constant<int, ACT_NONE>{});
   }
 }

@@ -15,16 +15,16 @@ template cudaError_t launch_gemm<EPI_LINEAR, false, false, 1, ACT_RELU_SQ>(const
 template int max_groups<EPI_LINEAR, false, false, 1, ACT_RELU_SQ>();
 template cudaError_t launch_gemm<EPI_LINEAR, false, false, 2, ACT_RELU_SQ>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_LINEAR, false, false, 2, ACT_RELU_SQ>();
-template cudaError_t launch_gemm<EPI_LINEAR, false, false, 1, ACT_GELU_HW>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_LINEAR, false, false, 1, ACT_GELU_HW>();
-template cudaError_t launch_gemm<EPI_LINEAR, false, false, 2, ACT_GELU_HW>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_LINEAR, false, false, 2, ACT_GELU_HW>();
-template cudaError_t launch_gemm<EPI_LINEAR, false, false, 1, ACT_SILU>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_LINEAR, false, false, 1, ACT_SILU>();
-template cudaError_t launch_gemm<EPI_LINEAR, false, false, 2, ACT_SILU>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_LINEAR, false, false, 2, ACT_SILU>();
-template cudaError_t launch_gemm<EPI_LINEAR, false, false, 1, ACT_SIGMOID>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_LINEAR, false, false, 1, ACT_SIGMOID>();
-template cudaError_t launch_gemm<EPI_LINEAR, false, false, 2, ACT_SIGMOID>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_LINEAR, false, false, 2, ACT_SIGMOID>();
+template cudaError_t launch_gemm<EPI_LINEAR, false, false, 1, ACT_GELU_EXP>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_LINEAR, false, false, 1, ACT_GELU_EXP>();
+template cudaError_t launch_gemm<EPI_LINEAR, false, false, 2, ACT_GELU_EXP>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_LINEAR, false, false, 2, ACT_GELU_EXP>();
+template cudaError_t launch_gemm<EPI_LINEAR, false, false, 1, ACT_SILU_EXP>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_LINEAR, false, false, 1, ACT_SILU_EXP>();
+template cudaError_t launch_gemm<EPI_LINEAR, false, false, 2, ACT_SILU_EXP>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_LINEAR, false, false, 2, ACT_SILU_EXP>();
+template cudaError_t launch_gemm<EPI_LINEAR, false, false, 1, ACT_SIGMOID_EXP>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_LINEAR, false, false, 1, ACT_SIGMOID_EXP>();
+template cudaError_t launch_gemm<EPI_LINEAR, false, false, 2, ACT_SIGMOID_EXP>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_LINEAR, false, false, 2, ACT_SIGMOID_EXP>();
 }  // namespace mlpk

@@ -402,11 +402,11 @@ cudaError_t launch_linear_skinny(const CUtensorMap& map_w, const CUtensorMap& ma
                 stream, pdl)
   if (w_mn) return act == ACT_NONE ? MLP_SK(ACT_NONE, true) : cudaErrorInvalidValue;
   switch (act) {
-    case ACT_SILU: return MLP_SK(ACT_SILU, false);
+    case ACT_SILU_EXP: return MLP_SK(ACT_SILU_EXP, false);
     case ACT_RELU_SQ: return MLP_SK(ACT_RELU_SQ, false);
-    case ACT_GELU_HW: return MLP_SK(ACT_GELU_HW, false);
+    case ACT_GELU_EXP: return MLP_SK(ACT_GELU_EXP, false);
     case ACT_RELU: return MLP_SK(ACT_RELU, false);
-    case ACT_SIGMOID: return MLP_SK(ACT_SIGMOID, false);
+    case ACT_SIGMOID_EXP: return MLP_SK(ACT_SIGMOID_EXP, false);
     default: return MLP_SK(ACT_NONE, false);
   }
 #undef MLP_SK

@@ -427,14 +427,14 @@ cudaError_t launch_moe_decode_act(const void* x, const int* ids, const void* Wg,
   if (gated) {
     switch (act) {
       case ACT_RELU: return MLP_DEC(ACT_RELU, true);
-      case ACT_GELU_TANH: return MLP_DEC(ACT_GELU_HW, true);
+      case ACT_GELU_TANH: return MLP_DEC(ACT_GELU_EXP, true);
       case ACT_SIGMOID: return MLP_DEC(ACT_SIGMOID, true);
       default: return MLP_DEC(ACT_SILU, true);
     }
   }
   switch (act) {
     case ACT_RELU: return MLP_DEC(ACT_RELU, false);
-    case ACT_GELU_TANH: return MLP_DEC(ACT_GELU_HW, false);
+    case ACT_GELU_TANH: return MLP_DEC(ACT_GELU_EXP, false);
     default: return MLP_DEC(ACT_RELU_SQ, false);
   }
 #undef MLP_DEC

@@ -11,10 +11,10 @@ template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 1, ACT_RELU, true>
 template int max_groups<EPI_GATED_FWD, false, false, 1, ACT_RELU, true>();
 template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 2, ACT_RELU, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_GATED_FWD, false, false, 2, ACT_RELU, true>();
-template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 1, ACT_GELU_HW, true>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_GATED_FWD, false, false, 1, ACT_GELU_HW, true>();
-template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 2, ACT_GELU_HW, true>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_GATED_FWD, false, false, 2, ACT_GELU_HW, true>();
+template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 1, ACT_GELU_EXP, true>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_GATED_FWD, false, false, 1, ACT_GELU_EXP, true>();
+template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 2, ACT_GELU_EXP, true>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_GATED_FWD, false, false, 2, ACT_GELU_EXP, true>();
 template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 1, ACT_SIGMOID, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_GATED_FWD, false, false, 1, ACT_SIGMOID, true>();
 template cudaError_t launch_gemm<EPI_GATED_FWD, false, false, 2, ACT_SIGMOID, true>(const Params&, int, cudaStream_t, bool);
@@ -23,10 +23,10 @@ template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 1, ACT_RELU_SQ, true
 template int max_groups<EPI_ACT_FWD, false, false, 1, ACT_RELU_SQ, true>();
 template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 2, ACT_RELU_SQ, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_ACT_FWD, false, false, 2, ACT_RELU_SQ, true>();
-template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 1, ACT_GELU_HW, true>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_ACT_FWD, false, false, 1, ACT_GELU_HW, true>();
-template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 2, ACT_GELU_HW, true>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_ACT_FWD, false, false, 2, ACT_GELU_HW, true>();
+template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 1, ACT_GELU_EXP, true>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_ACT_FWD, false, false, 1, ACT_GELU_EXP, true>();
+template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 2, ACT_GELU_EXP, true>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_ACT_FWD, false, false, 2, ACT_GELU_EXP, true>();
 template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 1, ACT_RELU, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_ACT_FWD, false, false, 1, ACT_RELU, true>();
 template cudaError_t launch_gemm<EPI_ACT_FWD, false, false, 2, ACT_RELU, true>(const Params&, int, cudaStream_t, bool);

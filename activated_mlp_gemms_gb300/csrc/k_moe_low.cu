@@ -7,14 +7,14 @@ template cudaError_t launch_gemm<EPI_GATED_LOW, false, false, 1, ACT_SILU, true>
 template int max_groups<EPI_GATED_LOW, false, false, 1, ACT_SILU, true>();
 template cudaError_t launch_gemm<EPI_GATED_LOW, false, false, 1, ACT_RELU, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_GATED_LOW, false, false, 1, ACT_RELU, true>();
-template cudaError_t launch_gemm<EPI_GATED_LOW, false, false, 1, ACT_GELU_HW, true>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_GATED_LOW, false, false, 1, ACT_GELU_HW, true>();
+template cudaError_t launch_gemm<EPI_GATED_LOW, false, false, 1, ACT_GELU_EXP, true>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_GATED_LOW, false, false, 1, ACT_GELU_EXP, true>();
 template cudaError_t launch_gemm<EPI_GATED_LOW, false, false, 1, ACT_SIGMOID, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_GATED_LOW, false, false, 1, ACT_SIGMOID, true>();
 template cudaError_t launch_gemm<EPI_ACT_LOW, false, false, 1, ACT_RELU_SQ, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_ACT_LOW, false, false, 1, ACT_RELU_SQ, true>();
-template cudaError_t launch_gemm<EPI_ACT_LOW, false, false, 1, ACT_GELU_HW, true>(const Params&, int, cudaStream_t, bool);
-template int max_groups<EPI_ACT_LOW, false, false, 1, ACT_GELU_HW, true>();
+template cudaError_t launch_gemm<EPI_ACT_LOW, false, false, 1, ACT_GELU_EXP, true>(const Params&, int, cudaStream_t, bool);
+template int max_groups<EPI_ACT_LOW, false, false, 1, ACT_GELU_EXP, true>();
 template cudaError_t launch_gemm<EPI_ACT_LOW, false, false, 1, ACT_RELU, true>(const Params&, int, cudaStream_t, bool);
 template int max_groups<EPI_ACT_LOW, false, false, 1, ACT_RELU, true>();
 template cudaError_t launch_gemm<EPI_ACCUM_F32, false, false, 1, 0, true>(const Params&, int, cudaStream_t, bool);

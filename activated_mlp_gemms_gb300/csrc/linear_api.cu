@@ -35,9 +35,9 @@ int linear_act(int act) {
   switch (act) {
     case MLP_LINEAR_RELU: return ACT_RELU;
     case MLP_LINEAR_RELU_SQ: return ACT_RELU_SQ;
-    case MLP_LINEAR_GELU_TANH: return ACT_GELU_HW;
-    case MLP_LINEAR_SILU: return ACT_SILU;
-    case MLP_LINEAR_SIGMOID: return ACT_SIGMOID;
+    case MLP_LINEAR_GELU_TANH: return ACT_GELU_EXP;
+    case MLP_LINEAR_SILU: return ACT_SILU_EXP;
+    case MLP_LINEAR_SIGMOID: return ACT_SIGMOID_EXP;
     default: return ACT_NONE;
   }
 }
@@ -172,9 +172,9 @@ int mlp_linear_fwd(const mlp_linear_t* p, const void* x, const void* W, const vo
   switch (act) {
     case ACT_RELU: return run_linear<ACT_RELU>(g, c);
     case ACT_RELU_SQ: return run_linear<ACT_RELU_SQ>(g, c);
-    case ACT_GELU_HW: return run_linear<ACT_GELU_HW>(g, c);
-    case ACT_SILU: return run_linear<ACT_SILU>(g, c);
-    case ACT_SIGMOID: return run_linear<ACT_SIGMOID>(g, c);
+    case ACT_GELU_EXP: return run_linear<ACT_GELU_EXP>(g, c);
+    case ACT_SILU_EXP: return run_linear<ACT_SILU_EXP>(g, c);
+    case ACT_SIGMOID_EXP: return run_linear<ACT_SIGMOID_EXP>(g, c);
     default: return run_linear<ACT_NONE>(g, c);
   }
 }
