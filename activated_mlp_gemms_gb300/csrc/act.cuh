@@ -44,6 +44,13 @@ __device__ __forceinline__ float sigmoid_exp2(float t) {
 }
 constexpr float LOG2_E = 1.4426950408889634f;
 
+// max(z, 0), NaN where z is
+__device__ __forceinline__ float relu_f(float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+  return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
   if constexpr (ACT == ACT_NONE) {
@@ -51,10 +58,10 @@ __device__ __forceinline__ float act_f(float z) {
   } else if constexpr (ACT == ACT_SILU) {
     return z * sigmoid_f(z);
   } else if constexpr (ACT == ACT_RELU_SQ) {
-    float r = fmaxf(z, 0.0f);
+    float r = relu_f(z);
     return r * r;
   } else if constexpr (ACT == ACT_RELU) {
-    return fmaxf(z, 0.0f);
+    return relu_f(z);
   } else if constexpr (ACT == ACT_SIGMOID) {
     return sigmoid_f(z);
   } else if constexpr (ACT == ACT_SILU_EXP) {
@@ -82,11 +89,11 @@ __device__ __forceinline__ void act_and_grad(float z, float& a, float& da) {
     a = z * s;
     da = s * fmaf(z, 1.0f - s, 1.0f);
   } else if constexpr (ACT == ACT_RELU_SQ) {
-    float r = fmaxf(z, 0.0f);
+    float r = relu_f(z);
     a = r * r;
     da = 2.0f * r;
   } else if constexpr (ACT == ACT_RELU) {
-    a = fmaxf(z, 0.0f);
+    a = relu_f(z);
     da = z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == ACT_SIGMOID) {
     const float s = sigmoid_f(z);
