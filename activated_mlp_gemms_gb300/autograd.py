@@ -28,6 +28,8 @@ moe_func the mixture-of-experts MLP (at the end of this file).
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import (GATED_ACTS, block, mlp_block_bwd, mlp_block_fwd, mlp_bwd, mlp_bwd_recompute,
@@ -220,18 +222,37 @@ def _grad_like(t, fuse, name):
     return g
 
 
+def _check_shape(t, shape, name):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _check_rows(t, lead, last, name):
+    """A row of `last` values for each of x's rows: x's own leading dimensions, or flat."""
+    if t.dim() != 2 or t.shape != (math.prod(lead), last):
+        _check_shape(t, (*lead, last), name)
+
+
 class _LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, bias, residual, act, resid_scale, fuse_grad_accum):
         for t, name in ((x, "x"), (W, "W")) + (((bias, "bias"),) if bias is not None else ()) + (
                 ((residual, "residual"),) if residual is not None else ()):
             _check_operand(t, name)
+        if W.dim() != 2:
+            raise ValueError(f"W must be [N, K], got {tuple(W.shape)}")
         N, K = W.shape
         shape = x.shape
+        if x.dim() == 0 or shape[-1] != K:
+            raise ValueError(f"x must have {K} values in its last dimension, got {tuple(shape)}")
+        if bias is not None:
+            _check_shape(bias, (N,), "bias")
+        if residual is not None:
+            _check_rows(residual, shape[:-1], N, "residual")
         x2 = x.reshape(-1, K).contiguous()
         M = x2.shape[0]
         ctx.x_shape, ctx.fuse, ctx.scale = shape, fuse_grad_accum, resid_scale
-        ctx.has_residual = residual is not None
+        ctx.r_shape = residual.shape if residual is not None else None
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
         ctx.prob = linear(M, N, K, act, resid_scale)
         pre = None
@@ -263,8 +284,8 @@ class _LinearFunction(torch.autograd.Function):
         elif dx is not None or dW is not None or db is not None:
             mlp_linear_bwd(ctx.prob, d2, x2, W, pre, dx, dW, db, fuse_grad_accum=ctx.fuse)
         dr = None
-        if ctx.has_residual and need[3]:
-            dr = dout if ctx.scale == 1.0 else dout * ctx.scale
+        if ctx.r_shape is not None and need[3]:
+            dr = (dout if ctx.scale == 1.0 else dout * ctx.scale).reshape(ctx.r_shape)
         return (dx.view(ctx.x_shape) if dx is not None else None, None if ctx.fuse else dW,
                 None if ctx.fuse else db, dr, None, None, None)
 
@@ -338,13 +359,25 @@ def moe_func(x, ids, weights, Wg, Wu, Wd, activation="swiglu", residual=None, ga
     gradients)."""
     gated = _check_weights(activation, Wg, Wu, Wd)
     _check_operand(x, "x")
+    if Wg.dim() != 3:
+        raise ValueError(f"Wg must be [E, I, H], got {tuple(Wg.shape)}")
     E, inner, H = Wg.shape
+    if x.dim() == 0 or x.shape[-1] != H:
+        raise ValueError(f"x must have {H} values in its last dimension, got {tuple(x.shape)}")
+    if ids.dim() == 0:
+        raise ValueError("ids must be [..., top_k]")
     shape, k = x.shape, ids.shape[-1]
+    _check_rows(ids, shape[:-1], k, "ids")
+    _check_rows(weights, shape[:-1], k, "weights")
+    if gated:
+        _check_shape(Wu, (E, inner, H), "Wu")
+    _check_shape(Wd, (E, H, inner), "Wd")
     x2 = x.reshape(-1, H).contiguous()
     T = x2.shape[0]
     r2 = None
     if residual is not None:
         _check_operand(residual, "residual")
+        _check_rows(residual, shape[:-1], H, "residual")
         r2 = residual.reshape(T, H).contiguous()
     if T == 0:
         parts = [t for t in (x2, weights, Wg, Wu if gated else None, Wd, r2) if t is not None]

@@ -1,0 +1,59 @@
+"""What linear_func and moe_func refuse, and how they behave under autograd's modes."""
+import pytest
+import torch
+
+import activated_mlp_gemms_gb300 as m
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def randn(seed, *shapes):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return [(torch.randn(s, generator=gen, device="cuda") / 8).to(BF) for s in shapes]
+
+
+def moe_args(lead, k, E=4, H=64, inner=72):
+    x, Wg, Wu, Wd = randn(1, (*lead, H), (E, inner, H), (E, inner, H), (E, H, inner))
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.rand((*lead, E), generator=gen, device="cuda").topk(k, -1)[1].int()
+    w = torch.rand((*lead, k), generator=gen, device="cuda")
+    return x, ids, w, Wg, Wu, Wd
+
+
+def test_shapes_that_only_have_the_right_number_of_values():
+    x, ids, w, *Ws = moe_args((6,), 2)
+    with pytest.raises(ValueError, match="weights"):
+        m.moe_func(x, ids, w.t().contiguous(), *Ws)
+    with pytest.raises(ValueError, match="ids|weights"):
+        m.moe_func(x, ids.t().contiguous(), w, *Ws)
+    with pytest.raises(ValueError, match="residual"):
+        m.moe_func(x, ids, w, *Ws, residual=x.t().contiguous())
+    with pytest.raises(ValueError, match="x must"):
+        m.moe_func(x.view(3, 128), ids, w, *Ws)
+    with pytest.raises(ValueError, match="Wd"):
+        m.moe_func(x, ids, w, Ws[0], Ws[1], Ws[0])
+    x, W, b, r = randn(3, (6, 64), (8, 64), (8,), (6, 8))
+    for bad in (dict(residual=r.t().contiguous()), dict(residual=r.view(8, 6)),
+                dict(residual=r.view(2, 3, 8)), dict(bias=r), dict(bias=randn(4, (16,))[0])):
+        with pytest.raises(ValueError, match=next(iter(bad))):
+            m.linear_func(x, W, **bad)
+    with pytest.raises(ValueError, match="x must"):
+        m.linear_func(x.view(3, 128), W)
+
+
+def test_flat_rows():
+    # routing and residual of [tokens, .] beside x of more dimensions
+    x, ids, w, *Ws = moe_args((2, 3), 2)
+    r = randn(5, x.shape)[0]
+    whole = m.moe_func(x, ids, w, *Ws, residual=r)
+    assert torch.equal(m.moe_func(x, ids.view(6, 2), w.view(6, 2), *Ws, residual=r.view(6, 64)), whole)
+    x, W, r = randn(6, (2, 3, 64), (8, 64), (2, 3, 8))
+    flat = r.view(6, 8).clone().requires_grad_(True)
+    r.requires_grad_(True)
+    a, b = m.linear_func(x, W, residual=r, resid_scale=0.5), m.linear_func(x, W, residual=flat,
+                                                                         resid_scale=0.5)
+    assert torch.equal(a, b)
+    ga, = torch.autograd.grad(a.float().sum(), r)
+    gb, = torch.autograd.grad(b.float().sum(), flat)
+    assert torch.equal(ga.view(6, 8), gb)
