@@ -23,6 +23,8 @@ mlp_block_func is modded-nanogpt gpt.py's "process mlp" step, y =
 resid_lambda x + post_lambda MLP(norm(x)), as one mlp_block_fwd and one
 mlp_block_bwd call (saved preacts and the per-token 1/rms).
 
+None of them can be differentiated twice: a second derivative raises.
+
 linear_func is the linear layer with bias, activation and residual, and
 moe_func the mixture-of-experts MLP (at the end of this file).
 """
@@ -31,6 +33,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (GATED_ACTS, block, mlp_block_bwd, mlp_block_fwd, mlp_bwd, mlp_bwd_recompute,
                mlp_fwd, problem)
@@ -112,6 +115,7 @@ class _MlpFunction(torch.autograd.Function):
         return out.view(shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         x2, Wg, Wu, Wd, G, U = ctx.saved_tensors
         if ctx.spent and not ctx.recompute:
@@ -177,6 +181,7 @@ class _MlpBlockFunction(torch.autograd.Function):
         return y.view(shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x2, Wg, Wu, Wd, G, U, rstd = ctx.saved_tensors
         if ctx.spent:
@@ -265,6 +270,7 @@ class _LinearFunction(torch.autograd.Function):
         return out.view(*shape[:-1], N)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         x2, W, bias, pre = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -319,6 +325,7 @@ class _MoeFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         plan, xs, weights, Wg, Wu, Wd, G, U, y = ctx.saved_tensors
         need, p = ctx.needs_input_grad, ctx.prob

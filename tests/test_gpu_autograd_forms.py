@@ -57,3 +57,18 @@ def test_flat_rows():
     ga, = torch.autograd.grad(a.float().sum(), r)
     gb, = torch.autograd.grad(b.float().sum(), flat)
     assert torch.equal(ga.view(6, 8), gb)
+
+
+def test_second_derivatives_raise():
+    # (a gradient without a graph would drop out of a sum with other terms)
+    x, ids, w, *Ws = moe_args((6,), 2)
+    W = randn(7, (8, 64))[0]
+    forms = {"linear": lambda z: m.linear_func(z, W, activation="silu"),
+             "moe": lambda z: m.moe_func(z, ids, w, *Ws),
+             "mlp": lambda z: m.mlp_func(z, *(t[0] for t in Ws)),
+             "block": lambda z: m.mlp_block_func(z, *(t[0] for t in Ws))}
+    for name, f in forms.items():
+        z = x.clone().requires_grad_(True)
+        (g,) = torch.autograd.grad(f(z).float().square().sum(), z, create_graph=True)
+        with pytest.raises(RuntimeError, match="twice"):
+            (g.float().square().sum() + z.float().sum()).backward()
