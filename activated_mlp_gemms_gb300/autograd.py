@@ -240,7 +240,7 @@ def _check_rows(t, lead, last, name):
 
 class _LinearFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, W, bias, residual, act, resid_scale, fuse_grad_accum):
+    def forward(ctx, x, W, bias, residual, act, resid_scale, fuse_grad_accum, keep_pre):
         for t, name in ((x, "x"), (W, "W")) + (((bias, "bias"),) if bias is not None else ()) + (
                 ((residual, "residual"),) if residual is not None else ()):
             _check_operand(t, name)
@@ -263,7 +263,7 @@ class _LinearFunction(torch.autograd.Function):
         pre = None
         if M:
             r2 = residual.reshape(M, N).contiguous() if residual is not None else None
-            if act != "none" and any(ctx.needs_input_grad[:3]):
+            if act != "none" and keep_pre:
                 pre = torch.empty_like(out)
             mlp_linear_fwd(ctx.prob, x2, W, bias, r2, out, pre)
         ctx.save_for_backward(x2, W, bias, pre)
@@ -293,7 +293,7 @@ class _LinearFunction(torch.autograd.Function):
         if ctx.r_shape is not None and need[3]:
             dr = (dout if ctx.scale == 1.0 else dout * ctx.scale).reshape(ctx.r_shape)
         return (dx.view(ctx.x_shape) if dx is not None else None, None if ctx.fuse else dW,
-                None if ctx.fuse else db, dr, None, None, None)
+                None if ctx.fuse else db, dr, None, None, None, None)
 
 
 def linear_func(x, W, bias=None, residual=None, activation="none", resid_scale=1.0,
@@ -301,8 +301,11 @@ def linear_func(x, W, bias=None, residual=None, activation="none", resid_scale=1
     """out = act(x W^T + bias) + resid_scale * residual over the last dimension of x,
     differentiable with respect to x, W, bias and residual (one mlp_linear_fwd and one
     mlp_linear_bwd call)."""
+    # (ctx.needs_input_grad stays true for parameters where gradients are off)
+    keep_pre = torch.is_grad_enabled() and any(
+        isinstance(t, torch.Tensor) and t.requires_grad for t in (x, W, bias))
     return _LinearFunction.apply(x, W, bias, residual, activation, float(resid_scale),
-                                 bool(fuse_grad_accum))
+                                 bool(fuse_grad_accum), keep_pre)
 
 
 class _MoeFunction(torch.autograd.Function):

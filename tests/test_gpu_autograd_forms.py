@@ -72,3 +72,25 @@ def test_second_derivatives_raise():
         (g,) = torch.autograd.grad(f(z).float().square().sum(), z, create_graph=True)
         with pytest.raises(RuntimeError, match="twice"):
             (g.float().square().sum() + z.float().sum()).backward()
+
+
+def test_preact_only_where_a_gradient_follows(monkeypatch):
+    from activated_mlp_gemms_gb300 import autograd
+    saved, real = [], autograd.mlp_linear_fwd
+
+    def fwd(p, x, W, b, r, out, pre=None):
+        saved.append(pre is not None)
+        return real(p, x, W, b, r, out, pre)
+
+    monkeypatch.setattr(autograd, "mlp_linear_fwd", fwd)
+    x, W, b, r = randn(8, (6, 64), (8, 64), (8,), (6, 8))
+    for t in (W, b, r):
+        t.requires_grad_(True)
+    with torch.no_grad():
+        m.linear_func(x, W, b, r, "silu")
+    with torch.inference_mode():
+        m.linear_func(x, W, b, r, "silu")
+    m.linear_func(x, W.detach(), None, r, "silu")  # the residual's gradient needs none
+    assert saved == [False] * 3
+    m.linear_func(x, W.detach(), b, None, "silu")
+    assert saved[3]
