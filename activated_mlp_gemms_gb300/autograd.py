@@ -313,6 +313,10 @@ class _MoeFunction(torch.autograd.Function):
     def forward(ctx, x, weights, Wg, Wu, Wd, residual, ids, prob, fuse_grad_accum):
         T, H = x.shape
         new = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=x.device)  # noqa: E731
+        ctx.prob, ctx.fuse, ctx.spent = prob, fuse_grad_accum, False
+        if prob is None:  # no tokens
+            ctx.save_for_backward(x, weights, Wg, Wu, Wd)
+            return new(0, H)
         rows = mlp_moe_rows(prob)
         plan = alloc_moe_plan(prob, x.device)
         xs, y, G = new(rows, H), new(rows, H), new(rows, prob.I)
@@ -322,7 +326,6 @@ class _MoeFunction(torch.autograd.Function):
         mlp_moe_dispatch(prob, plan, x, xs)
         mlp_moe_experts_fwd(prob, plan, xs, Wg, Wu, Wd, y, G, U)
         mlp_moe_combine(prob, plan, y, weights, residual, out)
-        ctx.prob, ctx.fuse, ctx.spent = prob, fuse_grad_accum, False
         keep_y = y if ctx.needs_input_grad[1] else None  # only the weights' gradient reads it
         ctx.save_for_backward(plan, xs, weights, Wg, Wu, Wd, G, U, keep_y)
         return out
@@ -330,8 +333,13 @@ class _MoeFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
+        need = ctx.needs_input_grad
+        if ctx.prob is None:
+            grads = [torch.zeros_like(t) if t is not None and n and not (ctx.fuse and i >= 2) else None
+                     for i, (t, n) in enumerate(zip(ctx.saved_tensors, need))]
+            return (*grads, dout if need[5] else None, None, None, None)
         plan, xs, weights, Wg, Wu, Wd, G, U, y = ctx.saved_tensors
-        need, p = ctx.needs_input_grad, ctx.prob
+        p = ctx.prob
         experts = need[0] or any(need[2:5])
         if ctx.spent and experts:
             raise RuntimeError("moe_func: the saved preacts were overwritten by the first backward")
@@ -389,15 +397,14 @@ def moe_func(x, ids, weights, Wg, Wu, Wd, activation="swiglu", residual=None, ga
         _check_operand(residual, "residual")
         _check_rows(residual, shape[:-1], H, "residual")
         r2 = residual.reshape(T, H).contiguous()
-    if T == 0:
-        parts = [t for t in (x2, weights, Wg, Wu if gated else None, Wd, r2) if t is not None]
-        return x2.new_zeros((0, H)).view(shape) + 0 * sum(t.sum() for t in parts)
     i2, w2 = ids.reshape(T, k).contiguous(), weights.reshape(T, k).contiguous()
-    prob = moe(T, E, k, H, inner, activation, gate_mult, down_mult, weights_dtype=w2.dtype)
+    prob = moe(T, E, k, H, inner, activation, gate_mult, down_mult,
+               weights_dtype=w2.dtype) if T else None
     args = [t for t in (x2, w2, Wg, Wu, Wd, r2) if t is not None]
     if torch.is_grad_enabled() and any(t.requires_grad for t in args):
         out = _MoeFunction.apply(x2, w2, Wg, Wu, Wd, r2, i2, prob, bool(fuse_grad_accum))
     else:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-        mlp_moe_fwd_infer(prob, x2, i2, w2, Wg, Wu, Wd, r2, out)
+        if T:
+            mlp_moe_fwd_infer(prob, x2, i2, w2, Wg, Wu, Wd, r2, out)
     return out.view(shape)

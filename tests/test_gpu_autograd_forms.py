@@ -94,3 +94,19 @@ def test_preact_only_where_a_gradient_follows(monkeypatch):
     assert saved == [False] * 3
     m.linear_func(x, W.detach(), b, None, "silu")
     assert saved[3]
+
+
+def test_no_tokens_into_main_grad():
+    # nothing to add, no gradient returned, and the weights are not read
+    x, ids, w, *Ws = moe_args((6,), 2)
+    Ws = [t.requires_grad_(True) for t in Ws]
+    for t in Ws:
+        t.main_grad = torch.ones_like(t, dtype=torch.float32)
+    empty = x[:0].clone().requires_grad_(True)
+    y = m.moe_func(empty, ids[:0], w[:0].requires_grad_(True), *Ws, residual=empty,
+                   fuse_grad_accum=True)
+    y.sum().backward()
+    assert empty.grad.shape == (0, 64)
+    assert all(t.grad is None and (t.main_grad == 1).all() for t in Ws)
+    with torch.no_grad():
+        assert m.moe_func(empty, ids[:0], w[:0], *Ws).shape == (0, 64)
