@@ -194,19 +194,24 @@ def _empty_on(n, dtype, device, stream):
 # Workspaces of the calls that are given none, kept where they are small: a
 # fresh tensor costs 3-5 us a call, more than the smallest calls themselves.
 # One for each device, stream and host thread: calls that share one are ordered.
+# They go with their thread, back to their stream's memory.  (A kept workspace's status
+# word is the last call's; who wants a call's own passes a workspace.)
 _KEEP_BYTES = 4 << 20
-_kept = {}
+_kept = threading.local()
 
 
 def _call_workspace(n, device, stream):
     """A workspace of n bytes for a call on `stream` (None: the current one)."""
     if stream is not None or n > _KEEP_BYTES or torch._C._cuda_isCurrentStreamCapturing():
         return _empty_on(n, torch.uint8, device, stream)
-    key = (device.index, _stream(None), threading.get_ident())
-    ws = _kept.get(key)
+    try:
+        mine = _kept.by_stream
+    except AttributeError:
+        mine = _kept.by_stream = {}
+    key = (device.index, _stream(None))
+    ws = mine.get(key)
     if ws is None or ws.numel() < n:
-        ws = torch.empty(max(n, 1 << 16), dtype=torch.uint8, device=device)
-        _kept[key] = ws
+        ws = mine[key] = torch.empty(max(n, 1 << 16), dtype=torch.uint8, device=device)
     return ws
 
 

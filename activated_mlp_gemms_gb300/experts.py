@@ -1,6 +1,9 @@
 """The mixture-of-experts MLP (include/mlp_moe.h): tokens sorted by expert and
 back with their routing weights, and the gradients.
 
+Calls return the workspace that they used: given none, a small one that later calls
+of the same thread on the same stream use too, and then hold their status.
+
 Argument marshalling only, as in the package's other calls: outputs are
 tensors that the caller passes.  Every shape is checked, because the kernels
 take their row numbers from the plan.

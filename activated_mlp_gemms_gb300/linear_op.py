@@ -113,7 +113,7 @@ def mlp_linear_fwd(p: Linear, x, W, bias, residual, out, pre_save=None, ws=None,
     """out = act(x W^T + bias) + resid_scale * residual; bias and residual may be None.
     pre_save (bf16 [M, N]) receives x W^T + bias for the backward of an activation.
     Returns the workspace used (given none, a small one that later calls of this thread on
-    this stream use too)."""
+    this stream use too, and then hold their status)."""
     M, N, K = p.M, p.N, p.K
     xp, ldx = _pitched(x, (M, K), "x")
     rp, ldr = _pitched(residual, (M, N), "residual")
