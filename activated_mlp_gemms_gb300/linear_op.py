@@ -74,6 +74,8 @@ def _pitched(t, shape, name):
     if t.stride(1) != 1 or t.stride(0) < shape[1]:
         raise ValueError(f"{name} must have unit stride along its last dimension and rows "
                          "that do not overlap")
+    if t.stride(0) > 0x7fffffff:  # the C ABI's int; ctypes would wrap it
+        raise ValueError(f"{name}'s row stride of {t.stride(0)} passes 32 bits")
     return t.data_ptr(), t.stride(0)
 
 

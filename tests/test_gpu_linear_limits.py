@@ -57,3 +57,13 @@ def test_sizes_whose_tiles_pass_32_bits_are_refused():
         p = m.moe(1, 1, 1, **kw)
         assert m.mlp_moe_workspace_size(p, m.MODE_FWD) == 0
         assert (m.lib().mlp_moe_rows(ctypes.byref(p)) == 0) == (kw["H"] > 8)
+
+
+@pytest.mark.gpu
+def test_row_strides_past_32_bits_are_refused():
+    x = torch.zeros((1 << 32) + 64, dtype=BF, device="cuda").as_strided((2, 64), (1 << 32, 1))
+    W, out = torch.zeros((8, 64), dtype=BF, device="cuda"), torch.zeros((2, 8), dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="stride"):
+        m.mlp_linear_fwd(m.linear(2, 8, 64), x, W, None, None, out)
+    with pytest.raises(ValueError, match="stride"):
+        m.mlp_linear_bwd(m.linear(2, 8, 64), out, x, W, dW=torch.empty_like(W))
