@@ -98,17 +98,28 @@ int check_ws(const mlp_moe_t* p, int mode, const void* ws, size_t ws_bytes) {
   return ws_bytes < layout(p, mode).total ? MLP_ERR_WORKSPACE_TOO_SMALL : MLP_OK;
 }
 
-// CTA pairs (256-row tiles) from an average of 192 rows an expert: an expert's
-// last tile is half empty on average, 128 rows of a pair's tile or 64 of a single
-// CTA's, while a pair's tile is the faster one per row.  Measured (pairs / singles;
-// gate/up, down, dgated, dx and weight gradients of 2048 x 4864, 16 experts of as
-// many rows each): 128 rows 1.11 1.16 1.05 1.21 .98, 192 .87 .90 .98 .88 .98, 384
-// 1.04 1.02 1.03 1.10 .89, 512 .84 .84 .89 .88 .92, 1024 .83 .82 .84 .87 .87; with
-// uneven experts 192 1.01 1.08 1.02 1.13 .97, 512 .92 .98 .93 1.05 .93.
-int moe_cg(const mlp_moe_t* p) {
+// CTA pairs (256-row tiles) from an average of 160 rows an expert, for the weight
+// gradients from 256: an expert's last tile is half empty on average, 128 rows of a
+// pair's tile or 64 of a single CTA's, while a pair's tile is the faster one per row.
+// What decides is how the rows of each expert fill whole tiles, which only the device
+// knows; the average decides well enough.  Measured (time on pairs / on singles;
+// gate/up, down, dgated, dx | weight gradients; 16 experts of 2048 x 4864):
+//   rows   96   1.03 1.10 1.01 1.11 | 1.11    uneven counts 1.05  .79  .99  .78 | 1.05
+//         128   1.04 1.10 1.00 1.11 | 1.13                  1.02  .83 1.08  .82 | 1.09
+//         160    .85  .87  .98  .86 | 1.06                   .97  .85 1.02  .85 | 1.07
+//         192    .86  .88  .96  .87 | 1.09                   .91 1.09  .90 1.13 | 1.04
+//         256    .88  .90  .97  .87 |  .98                   .88  .82  .90  .83 | 1.01
+//         320   1.01 1.00 1.03 1.05 |  .99                   .92  .84  .96  .86 |  .98
+//         384   1.02 1.00 1.03 1.05 |  .90                   .92  .99  .95 1.05 |  .96
+//         512    .85  .82  .91  .88 |  .92                   .94  .97  .99 1.04 |  .94
+//        1024    .85  .83  .86  .87 |  .90                   .88  .83  .91  .88 |  .92
+// (the entries above 1.0 at 320 and 384 rows are pairs' tiles half empty in every
+// expert, those of the uneven counts one more tile in the last wave).
+constexpr int MOE_PAIR_ROWS = 160, MOE_PAIR_ROWS_W = 256;
+int moe_cg(const mlp_moe_t* p, int rows = MOE_PAIR_ROWS) {
   const int pol = g_tile_policy.load();
   if (pol == 1 || pol == 2) return pol;
-  return (long long)p->T * p->top_k >= 192LL * p->E ? 2 : 1;
+  return (long long)p->T * p->top_k >= (long long)rows * p->E ? 2 : 1;
 }
 
 // Whether the inference layer streams the touched experts' weights: few tokens
@@ -390,7 +401,8 @@ int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, co
   if (!need_dact && !dWd) return MLP_OK;
   // the weight gradients still read dy and xs while dxs is stored
   if (dxs && ((dWd && dxs == dy) || ((dWg || dWu) && dxs == xs))) return MLP_ERR_INVALID_ARG;
-  const int cgw = p->H > BM && p->I > BM ? moe_cg(p) : pick_cg(p->H < p->I ? p->H : p->I);
+  const int cgw = p->H > BM && p->I > BM ? moe_cg(p, MOE_PAIR_ROWS_W)
+                                         : pick_cg(p->H < p->I ? p->H : p->I);
   const long long w_units = ((dWg ? 1 : 0) + (dWu ? 1 : 0)) * out_tiles(p->I, p->H, cgw) +
                             (dWd ? 1 : 0) * out_tiles(p->H, p->I, cgw);
   const int most = one_wave_units(moe_cg(p));
