@@ -175,16 +175,17 @@ __device__ __forceinline__ Work ring_get(uint32_t slot) {
 // The units of a problem that run the gated forward epilogue.
 template <int EPI>
 __device__ __forceinline__ bool gated_unit(int prob) {
-  return EPI == EPI_GATED_FWD || EPI == EPI_GATED_LOW || (EPI == EPI_FWD_FUSED && prob == 0);
+  return EPI == EPI_GATED_FWD || EPI == EPI_GATED_FINE || (EPI == EPI_FWD_FUSED && prob == 0);
 }
 
 template <int EPI>
 struct EpiTraits {
   // output columns of a tile (EPI_FWD_FUSED: per problem, tile_n_of)
-  static constexpr int TILE_N = (EPI == EPI_GATED_FWD || EPI == EPI_GATED_LOW) ? 128 : 256;
+  static constexpr int TILE_N = (EPI == EPI_GATED_FWD || EPI == EPI_GATED_FINE) ? 128 : 256;
   // outputs staged per chunk (gated fwd: a, G, U; act fwd: a, P; dgated: dG,
   // dU, a; dact: dP, a; plain: D) and bytes of one staged 32 x 32 box
-  static constexpr int NOUT = (EPI == EPI_GATED_FWD || EPI == EPI_DGATED || EPI == EPI_FWD_FUSED) ? 3
+  static constexpr int NOUT = (EPI == EPI_GATED_FWD || EPI == EPI_DGATED || EPI == EPI_FWD_FUSED ||
+                               EPI == EPI_GATED_FINE || EPI == EPI_ACT_FINE) ? 3
                               : (EPI == EPI_ACT_FWD || EPI == EPI_DACT ||
                                  EPI == EPI_DACT_RECOMP || EPI == EPI_ACT_FWD_F8 ||
                                  EPI == EPI_LINEAR) ? 2
@@ -361,9 +362,22 @@ __device__ __forceinline__ uint32_t pack_low(float a, float b) {
   return pack_bf16x2(a - h.x, b - h.y);
 }
 
-template <int ACT>
-__device__ __forceinline__ void epi_gated_low(const Params& p, const EpiUnit& P, const EpiWarp& e,
-                                              uint32_t tb, int col0, int cb, int ce) {
+// Store staged box `buf` through map m (nullptr: not) as a bulk group of its own.
+__device__ __forceinline__ void store_map(const CUtensorMap* m, const EpiWarp& e, uint32_t buf,
+                                          int col) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (e.lane == 0) {
+    if (m) tma_store_2d(m, buf, col, e.row0);
+    bulk_commit();
+  }
+}
+
+// The activation forwards for few rows, their postact in two bf16 terms (the weights'
+// stream bounds them; the epilogue takes no care of its time).
+template <int ACT, bool GATED>
+__device__ __forceinline__ void epi_fine(const Params& p, const EpiUnit& P, const EpiWarp& e,
+                                         uint32_t tb, int col0, int cb, int ce) {
   const float s = p.scale;
 #pragma unroll 1
   for (int c = cb; c < ce; c += 32) {
@@ -372,39 +386,38 @@ __device__ __forceinline__ void epi_gated_low(const Params& p, const EpiUnit& P,
     uint32_t g[32], u[32];
     __syncwarp();
     tmem_ld32(tb + c, g);
-    tmem_ld32(tb + 128 + c, u);
+    if constexpr (GATED) tmem_ld32(tb + 128 + c, u);
     tmem_wait_ld();
-    uint32_t pa[16];
+    uint32_t hi[16], lo[16], pg[16], pu[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      pa[j] = pack_low(s * act_f<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
-                       s * act_f<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
+    for (int j = 0; j < 16; ++j) {
+      const float g0 = __uint_as_float(g[2 * j]), g1 = __uint_as_float(g[2 * j + 1]);
+      float a0 = s * act_f<ACT>(g0), a1 = s * act_f<ACT>(g1);
+      if constexpr (GATED) {
+        const float u0 = __uint_as_float(u[2 * j]), u1 = __uint_as_float(u[2 * j + 1]);
+        a0 *= u0;
+        a1 *= u1;
+        pu[j] = pack_bf16x2(u0, u1);
+      }
+      hi[j] = pack_bf16x2(a0, a1);
+      lo[j] = pack_low(a0, a1);
+      pg[j] = pack_bf16x2(g0, g1);
+    }
     staging_acquire(e);
-    stage_bf16(e.stg, e.lane, pa);
-    flush_chunk<1, 2048, false>(p, P, e, col);
-  }
-}
-
-template <int ACT>
-__device__ __forceinline__ void epi_act_low(const Params& p, const EpiUnit& P, const EpiWarp& e,
-                                            uint32_t tb, int col0, int cb, int ce) {
-  const float s = p.scale;
-#pragma unroll 1
-  for (int c = cb; c < ce; c += 32) {
-    const int col = col0 + c;
-    if (col >= P.N) break;  // warp-uniform
-    uint32_t z[32];
-    __syncwarp();
-    tmem_ld32(tb + c, z);
-    tmem_wait_ld();
-    uint32_t pa[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      pa[j] = pack_low(s * act_f<ACT>(__uint_as_float(z[2 * j])),
-                       s * act_f<ACT>(__uint_as_float(z[2 * j + 1])));
-    staging_acquire(e);
-    stage_bf16(e.stg, e.lane, pa);
-    flush_chunk<1, 2048, false>(p, P, e, col);
+    stage_bf16(e.stg, e.lane, hi);
+    store_map(P.out[0], e, e.stg, col);
+    stage_bf16(e.stg + 2048, e.lane, lo);
+    store_map(P.ein, e, e.stg + 2048, col);
+    if (P.out[1]) {
+      staging_wait_read_but_one(e);
+      stage_bf16(e.stg, e.lane, pg);
+      store_map(P.out[1], e, e.stg, col);
+    }
+    if (GATED && P.out[2]) {
+      staging_acquire(e);
+      stage_bf16(e.stg + 2048, e.lane, pu);
+      store_map(P.out[2], e, e.stg + 2048, col);
+    }
   }
 }
 
@@ -1349,7 +1362,7 @@ __device__ __forceinline__ void load_stage(const UnitLoads& L, int seg, int kc, 
   pol = polB;
   if constexpr (PART == 1) {
     // A only
-  } else if constexpr (EPI == EPI_GATED_FWD || EPI == EPI_GATED_LOW) {
+  } else if constexpr (EPI == EPI_GATED_FWD || EPI == EPI_GATED_FINE) {
     ldw(sB, L.b0, kc, L.n0);
     if constexpr (CG == 1) ldw(sB + 16384, L.b1, kc, L.n0);
   } else {
@@ -1587,8 +1600,11 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
               full = bar_s(FULL + stage);
               mbar_expect_tx(full, tx_bytes);
             }
-            const int seg = kb < L.kb0 ? 0 : 1;
-            const int kc = (seg == 0 ? kb : kb - L.kb0) * KE;
+            // (two segments against one B, alternating: B's second load is in L2)
+            constexpr bool ALT = EPI == EPI_STORE_F32 || (EPI == EPI_ACCUM_F32 && GRP_ROWS);
+            const bool alt = ALT && L.b1 == L.b0 && p.prob[0].kb1 > 0;
+            const int seg = alt ? kb & 1 : kb < L.kb0 ? 0 : 1;
+            const int kc = (alt ? kb >> 1 : seg == 0 ? kb : kb - L.kb0) * KE;
             const uint32_t sA = base_s + stage * C::STAGE;
             load_stage<EPI, A_MN, B_MN, CG, GRP, B_WARP ? 1 : 0>(
                 L, seg, kc, sA, sA + C::A_BYTES, full, pol_of(L.l2a), pol_of(L.l2b));
@@ -1990,6 +2006,8 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
 #pragma unroll
           for (int o = 0; o < 3; ++o)
             if (P.out[o]) P.out[o] = &p.maps[p.prob[pi].mapO16[o]];
+          if constexpr (EPI == EPI_GATED_FINE || EPI == EPI_ACT_FINE)
+            P.ein = &p.maps[p.prob[pi].mapI1];
         }
       }
       e.expert = w.expert;
@@ -2053,10 +2071,8 @@ __global__ void __launch_bounds__(Roles<EPI, A_MN, B_MN, GRP>::THREADS, 1) k_mlp
           else epi_plain<EPI_STORE_BF16>(p, P, e, tb, col0, cb, ce);
         } else if constexpr (EPI == EPI_ACT_FWD) {
           epi_act_fwd<ACT>(p, P, e, tb, col0, cb, ce);
-        } else if constexpr (EPI == EPI_GATED_LOW) {
-          epi_gated_low<ACT>(p, P, e, tb, col0, cb, ce);
-        } else if constexpr (EPI == EPI_ACT_LOW) {
-          epi_act_low<ACT>(p, P, e, tb, col0, cb, ce);
+        } else if constexpr (EPI == EPI_GATED_FINE || EPI == EPI_ACT_FINE) {
+          epi_fine<ACT, EPI == EPI_GATED_FINE>(p, P, e, tb, col0, cb, ce);
         } else if constexpr (EPI == EPI_LINEAR) {
           epi_linear<ACT>(p, P, e, tb, col0, cb, ce, pg);
         } else if constexpr (EPI == EPI_DGATED) {

@@ -66,9 +66,10 @@ enum Epi : int {
   // bf16(z) -> map 1 if requested
   EPI_LINEAR = 12,
   EPI_STORE_F32 = 13,  // D = acc (fp32; the experts' down projection of the inference layer)
-  // The remainder a - bf16(a) of the activation forwards' postact, in bf16 (map 0)
-  EPI_GATED_LOW = 14,
-  EPI_ACT_LOW = 15
+  // The activation forwards with their postact in two bf16 terms: bf16(a) -> map 0,
+  // bf16(a - bf16(a)) -> mapE (mapI1 with boxes of 16 rows); preacts as theirs
+  EPI_GATED_FINE = 14,
+  EPI_ACT_FINE = 15
 };
 
 __host__ __device__ constexpr bool is_f8(int epi) {
@@ -111,7 +112,7 @@ struct Prob {
   int ld;                 // row pitch (elements) of the epilogue's outputs and inputs
   int mapI0, mapI1;       // derivative epilogues: maps of in0 / in1 with boxes {256, 128}
                           // whose tiles the producer prefetches into L2 (-1: none)
-  int mapE;               // EPI_DGRAD_F8: map of in0 with the epilogue warps' 32 x 32 bf16
+  int mapE;               // EPI_*_FINE: map of the second term; EPI_DGRAD_F8: map of in0 with the epilogue warps' 32 x 32 bf16
                           // boxes (64-byte swizzle), loaded by TMA (-1: plain loads)
   int mapO[3];            // tensor maps of the epilogue's outputs (-1: output not written)
   int mapO16[3];          // GRP over token rows: the same outputs with boxes of 16 rows, for the

@@ -260,10 +260,12 @@ struct Gemm {
   }
   // Stacks [depth, rows, cols] (dense): a K-major weight operand, an MN-major
   // one ([K, MN] each), and a stack of outputs
-  int kmajor_stack(const void* ptr, int depth, int rows, int K, int box_rows) {
+  // (or a part of each matrix: row pitch `pitch`, matrices pitch2 apart)
+  int kmajor_stack(const void* ptr, int depth, int rows, int K, int box_rows, int pitch = 0,
+                   uint64_t pitch2 = 0) {
     if (nmaps >= MAX_MAPS) { ok = false; return 0; }
-    if (!make_map(&p.maps[nmaps], ptr, K, rows, K, BK, box_rows, 0, CU_TENSOR_MAP_SWIZZLE_128B,
-                  depth, (uint64_t)rows * K))
+    if (!make_map(&p.maps[nmaps], ptr, K, rows, pitch ? pitch : K, BK, box_rows, 0,
+                  CU_TENSOR_MAP_SWIZZLE_128B, depth, pitch2 ? pitch2 : (uint64_t)rows * K))
       ok = false;
     return nmaps++;
   }
@@ -287,16 +289,19 @@ struct Gemm {
   // rows of an expert.  bf16 boxes have 32 columns (64-byte swizzle), or 64
   // (ROWS_WIDE, the plain store's; 128-byte swizzle), fp32 boxes 32.
   enum RowsKind { ROWS_BF16, ROWS_WIDE, ROWS_F32 };
-  void output_rows(Prob& P, int i, void* ptr, int rows, int cols, RowsKind kind = ROWS_BF16) {
+  void output_rows(Prob& P, int i, void* ptr, int rows, int cols, RowsKind kind = ROWS_BF16,
+                   int pitch = 0) {
     P.mapO[i] = P.mapO16[i] = -1;
-    if (!ptr) return;
+    if (ptr) row_boxes(ptr, rows, cols, kind, pitch, P.mapO[i], P.mapO16[i]);
+  }
+  void row_boxes(void* ptr, int rows, int cols, RowsKind kind, int pitch, int& map32, int& map16) {
     for (int box : {32, 16}) {
       if (nmaps >= MAX_MAPS) { ok = false; return; }
-      if (!make_map(&p.maps[nmaps], ptr, cols, rows, cols, kind == ROWS_WIDE ? 64 : 32, box,
-                    kind == ROWS_F32,
+      if (!make_map(&p.maps[nmaps], ptr, cols, rows, pitch ? pitch : cols,
+                    kind == ROWS_WIDE ? 64 : 32, box, kind == ROWS_F32,
                     kind == ROWS_BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
         ok = false;
-      (box == 32 ? P.mapO : P.mapO16)[i] = nmaps++;
+      (box == 32 ? map32 : map16) = nmaps++;
     }
   }
   // ke: K elements per k-block (bf16 64, e4m3 128: a 128-byte row either way)
@@ -432,7 +437,7 @@ int groups_cached() {
 // Kernels that are built for single CTAs only (few slots' rows).
 template <int EPI, bool A_MN, bool GRP>
 constexpr bool singles_only() {
-  return EPI == EPI_GATED_LOW || EPI == EPI_ACT_LOW || (EPI == EPI_ACCUM_F32 && !A_MN && GRP);
+  return EPI == EPI_GATED_FINE || EPI == EPI_ACT_FINE || (EPI == EPI_ACCUM_F32 && !A_MN && GRP);
 }
 
 template <int EPI, bool A_MN, bool B_MN, int ACT, bool GRP = false>

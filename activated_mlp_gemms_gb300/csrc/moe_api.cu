@@ -163,8 +163,8 @@ long long row_units(const mlp_moe_t* p, int cols, int tile_n) {
   const int cg = moe_cg(p);
   return plan_of(p).tile_cap[cg - 1] * ((cols + tile_n - 1) / tile_n);
 }
-// The forward's two GEMMs are one wave each.  (Up to MOE_FINE_SLOTS slots the
-// remainder's two, on single CTAs, are too: an expert's rows are one tile either way.)
+// The forward's GEMMs are one wave each.  (Up to MOE_FINE_SLOTS slots, too, where they
+// are single CTAs whatever the tile policy: an expert's rows are one tile either way.)
 bool fwd_one_wave(const mlp_moe_t* p) {
   const int most = one_wave_units(moe_cg(p));
   return row_units(p, p->I, gated(p) ? 128 : MMA_N) <= most && row_units(p, p->H, MMA_N) <= most;
@@ -200,29 +200,10 @@ int launch_experts_act(const mlp_moe_t* p, Call& c, const int* plan, const void*
   return run_nongated<EPI_ACT_FWD, false, false, true>(g, c, MLP_KERNEL_GATE_UP);
 }
 
-// The postact's remainder (EPI_GATED_LOW, EPI_ACT_LOW) over the postact.
-int launch_experts_low(const mlp_moe_t* p, Call& c, const int* plan, const void* xs, const void* Wg,
-                       const void* Wu, void* a) {
-  RowGemm g(p, c, plan, 1);
-  const int mA = g.rows_a(xs, p->H);
-  const int tile_n = gated(p) ? 128 : MMA_N;
-  const int mG = g.kmajor_stack(Wg, p->E, p->I, p->H, tile_n);
-  const int mU = gated(p) ? g.kmajor_stack(Wu, p->E, p->I, p->H, tile_n) : 0;
-  Prob& P = g.add_rows(p->I, p->H, 0, tile_n);
-  P.l2a = L2_EVICT_LAST;
-  P.mapA0 = mA;
-  P.mapB0 = mG;
-  P.mapB1 = mU;
-  g.output_rows(P, 0, a, static_cast<int>(g.L.rows), p->I);
-  return gated(p) ? run_gated<EPI_GATED_LOW, false, false, true>(g, c, MLP_KERNEL_GATE_UP)
-                  : run_nongated<EPI_ACT_LOW, false, false, true>(g, c, MLP_KERNEL_GATE_UP);
-}
-
-// y is bf16, fp32, or fp32 that the product is added to (single CTAs)
-enum class Y { BF16, F32, ADD_F32 };
+// y32: y is fp32
 int launch_experts_down(const mlp_moe_t* p, Call& c, const int* plan, const void* a, const void* Wd,
-                        void* y, Y kind) {
-  RowGemm g(p, c, plan, kind == Y::ADD_F32 ? 1 : moe_cg(p));
+                        void* y, bool y32) {
+  RowGemm g(p, c, plan);
   const int mA = g.rows_a(a, p->I);
   const int mB = g.kmajor_stack(Wd, p->E, p->H, p->I, g.b_rows());
   Prob& P = g.add_rows(p->H, p->I, 0, MMA_N);
@@ -230,11 +211,71 @@ int launch_experts_down(const mlp_moe_t* p, Call& c, const int* plan, const void
   P.l2b = L2_EVICT_FIRST;
   P.mapA0 = mA;
   P.mapB0 = mB;
-  g.output_rows(P, 0, y, static_cast<int>(g.L.rows), p->H,
-                kind == Y::BF16 ? Gemm::ROWS_WIDE : Gemm::ROWS_F32);
-  return kind == Y::BF16  ? run<EPI_STORE_BF16, false, false, true>(g, c, MLP_KERNEL_DOWN)
-         : kind == Y::F32 ? run<EPI_STORE_F32, false, false, true>(g, c, MLP_KERNEL_DOWN)
-                          : run<EPI_ACCUM_F32, false, false, true>(g, c, MLP_KERNEL_DOWN);
+  g.output_rows(P, 0, y, static_cast<int>(g.L.rows), p->H, y32 ? Gemm::ROWS_F32 : Gemm::ROWS_WIDE);
+  return y32 ? run<EPI_STORE_F32, false, false, true>(g, c, MLP_KERNEL_DOWN)
+             : run<EPI_STORE_BF16, false, false, true>(g, c, MLP_KERNEL_DOWN);
+}
+
+// Few slots (MOE_FINE_SLOTS): y in fp32 into the plan, for the routing weights'
+// gradient (k_moe_combine_bwd), from the postact as two bf16 terms: the k-blocks of
+// both alternate against the same Wd, which the second finds in L2.  (y in fp32 from a postact of one
+// term leaves 5 % of the steps of up to eight slots over 0.005.)  The first term has
+// the workspace, the second waits in y, at most H columns of the postact at a time;
+// y itself is written last, from the fp32 rows.  Single CTAs.
+int launch_experts_fine(const mlp_moe_t* p, Call& c, int* plan, const void* xs, const void* Wg,
+                        const void* Wu, const void* Wd, void* a, void* y, void* G, void* U) {
+  const MoePlan L = plan_of(p);
+  const int rows = static_cast<int>(L.rows), H = p->H, I = p->I;
+  const bool gt = gated(p);
+  const int tile_n = gt ? 128 : MMA_N;
+  auto at = [](const void* ptr, long long n) {  // n bf16 values on
+    return ptr ? const_cast<char*>(static_cast<const char*>(ptr)) + 2 * n : nullptr;
+  };
+  void* y32 = plan + L.fine;
+  const int parts = (I + H - 1) / H;
+  int most = ((I + parts - 1) / parts + 127) / 128 * 128;  // equal parts, whole tiles
+  if (most > H) most = H;
+  for (int c0 = 0; c0 < I; c0 += most) {
+    const int w = I - c0 < most ? I - c0 : most;
+    if (!c.one_wave && c.next_counter + 2 > MAX_COUNTERS) {  // (I above 56 H) counters to use again
+      MLP_TRY(cuda_err(cudaMemsetAsync(c.counters, 0, MAX_COUNTERS * sizeof(int), c.stream)));
+      c.next_counter = c.launches = 0;
+    }
+    {
+      RowGemm g(p, c, plan, 1);
+      const int mA = g.rows_a(xs, H);
+      const int mG = g.kmajor_stack(at(Wg, (long long)c0 * H), p->E, w, H, tile_n, H, (uint64_t)I * H);
+      const int mU = gt ? g.kmajor_stack(at(Wu, (long long)c0 * H), p->E, w, H, tile_n, H,
+                                         (uint64_t)I * H) : 0;
+      Prob& P = g.add_rows(w, H, 0, tile_n);
+      P.l2a = L2_EVICT_LAST;
+      P.l2b = L2_EVICT_FIRST;
+      P.mapA0 = mA;
+      P.mapB0 = mG;
+      P.mapB1 = mU;
+      g.output_rows(P, 0, at(a, c0), rows, w, Gemm::ROWS_BF16, I);
+      g.output_rows(P, 1, at(G, c0), rows, w, Gemm::ROWS_BF16, I);
+      g.output_rows(P, 2, at(U, c0), rows, w, Gemm::ROWS_BF16, I);
+      g.row_boxes(y, rows, w, Gemm::ROWS_BF16, H, P.mapE, P.mapI1);
+      MLP_TRY(gt ? run_gated<EPI_GATED_FINE, false, false, true>(g, c, MLP_KERNEL_GATE_UP)
+                 : run_nongated<EPI_ACT_FINE, false, false, true>(g, c, MLP_KERNEL_GATE_UP));
+    }
+    RowGemm g(p, c, plan, 1);
+    const int mA0 = g.kmajor(at(a, c0), rows, w, BM, I);
+    const int mA1 = g.kmajor(y, rows, w, BM, H);
+    const int mB = g.kmajor_stack(at(Wd, c0), p->E, H, w, MMA_N, I, (uint64_t)H * I);
+    Prob& P = g.add_rows(H, w, w, MMA_N);
+    P.l2a = L2_EVICT_LAST;
+    P.mapA0 = mA0;
+    P.mapA1 = mA1;
+    P.mapB0 = P.mapB1 = mB;
+    g.output_rows(P, 0, y32, rows, H, Gemm::ROWS_F32);
+    MLP_TRY(c0 == 0 ? (run<EPI_STORE_F32, false, false, true>(g, c, MLP_KERNEL_DOWN))
+                    : (run<EPI_ACCUM_F32, false, false, true>(g, c, MLP_KERNEL_DOWN)));
+  }
+  const bool pdl = c.pdl();
+  return traced(MLP_KERNEL_CONVERT, c.stream,
+                [&] { return launch_moe_fine_rows(plan, L, p->E, H, y, c.stream, pdl); });
 }
 
 // The sort and the token kernels start while the kernel before them on the
@@ -354,25 +395,16 @@ int mlp_moe_experts_fwd(const mlp_moe_t* p, void* plan, const void* xs, const vo
   MLP_TRY(opt(U_save));
   if (!gated(p) && U_save) return MLP_ERR_INVALID_ARG;
   MLP_TRY(check_ws(p, MLP_MODE_FWD, ws, ws_bytes));
+  if (y == xs) return MLP_ERR_INVALID_ARG;  // (few slots: y is written while xs is read)
   Call c;
   if (fwd_one_wave(p)) begin_one_wave(c, ws, stream);
   else MLP_TRY(begin_call(c, ws, stream));
   void* a = static_cast<char*>(ws) + layout(p, MLP_MODE_FWD).inter;
   int* pl = static_cast<int*>(plan);
-  const MoePlan L = plan_of(p);
+  if (plan_of(p).fine >= 0)
+    return launch_experts_fine(p, c, pl, xs, Wg, Wu, Wd, a, y, G_save, U_save);
   MLP_TRY(launch_experts_act(p, c, pl, xs, Wg, Wu, a, G_save, U_save));
-  if (L.fine < 0) return launch_experts_down(p, c, pl, a, Wd, y, Y::BF16);
-  // Few slots: y in fp32, for the routing weights' gradient (k_moe_combine_bwd), from
-  // the postact as two bf16 terms.  (y in fp32 alone leaves 5 % of the steps of up to
-  // eight slots over 0.005.)  The terms go through the postact's buffer one after the
-  // other, so Wg and Wu are read twice: the workspace has room for one.
-  void* y32 = pl + L.fine;
-  MLP_TRY(launch_experts_down(p, c, pl, a, Wd, y32, Y::F32));
-  MLP_TRY(launch_experts_low(p, c, pl, xs, Wg, Wu, a));
-  MLP_TRY(launch_experts_down(p, c, pl, a, Wd, y32, Y::ADD_F32));
-  const bool pdl = c.pdl();
-  return traced(MLP_KERNEL_CONVERT, c.stream,
-                [&] { return launch_moe_fine_rows(pl, L, p->E, p->H, y, c.stream, pdl); });
+  return launch_experts_down(p, c, pl, a, Wd, y, false);
 }
 
 int mlp_moe_experts_bwd(const mlp_moe_t* p, const void* plan, const void* dy, const void* xs,
@@ -551,7 +583,7 @@ int mlp_moe_fwd_infer(const mlp_moe_t* p, const void* x, const int* ids, const v
     return launch_moe_dispatch(x, plan, L, p->T, p->top_k, p->H, xs, c.stream, pdl);
   }));
   MLP_TRY(launch_experts_act(p, c, plan, xs, Wg, Wu, a, nullptr, nullptr));
-  MLP_TRY(launch_experts_down(p, c, plan, a, Wd, y, Y::F32));
+  MLP_TRY(launch_experts_down(p, c, plan, a, Wd, y, true));
   pdl = c.pdl();
   return traced(MLP_KERNEL_MOE_COMBINE, c.stream, [&] {
     return launch_moe_combine(y, true, plan, L, p->T, p->top_k, p->H, weights, w_bf16(p), residual, out,

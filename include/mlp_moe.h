@@ -104,9 +104,9 @@ size_t mlp_moe_workspace_size(const mlp_moe_t* p, int mode);
  *   xs  bf16 [rows,H];  Wg, Wu bf16 [E,I,H] (Wu NULL when non-gated);
  *   Wd  bf16 [E,H,I];   y bf16 [rows,H] out
  *   G_save, U_save  bf16 [rows,I] out, optional: the preacts, for the backward
- * Rows from offsets[E] on are not written.  Up to MLP_MOE_FINE_SLOTS slots the
- * plan receives y in fp32, from a postact in two bf16 terms, and the preacts'
- * weights are read twice; calls with such a plan do not run at the same time. */
+ * Rows from offsets[E] on are not written; y is not xs.  Up to MLP_MOE_FINE_SLOTS
+ * slots the plan receives y in fp32, from a postact in two bf16 terms (calls with
+ * such a plan do not run at the same time). */
 int mlp_moe_experts_fwd(const mlp_moe_t* p, void* plan, const void* xs, const void* Wg,
                         const void* Wu, const void* Wd, void* y, void* G_save, void* U_save,
                         void* ws, size_t ws_bytes, void* stream);

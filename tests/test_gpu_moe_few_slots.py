@@ -93,7 +93,8 @@ def step(T, k, E, H, inner, act, wdt, seed, drop=0.0):
 @pytest.mark.parametrize("act", ["swiglu", "relu_sq", "geglu"])
 @pytest.mark.parametrize("T,k,E,H,inner", [
     (1, 1, 8, 384, 264), (1, 3, 4, 1384, 1384), (4, 3, 4, 264, 512), (7, 1, 1, 520, 136),
-    (19, 2, 60, 256, 392), (5, 8, 16, 768, 72), (64, 1, 3, 136, 264), (2, 2, 2, 72, 8)])
+    (19, 2, 60, 256, 392), (5, 8, 16, 768, 72), (64, 1, 3, 136, 264), (2, 2, 2, 72, 8),
+    (3, 2, 4, 72, 520), (2, 8, 16, 8, 520)])
 def test_dweights_of_few_slots(T, k, E, H, inner, act):
     for seed in range(12):
         wdt = torch.float32 if seed % 2 else BF

@@ -37,3 +37,10 @@ def test_experts_backward(L, over):
     for grads in wanted:
         assert L.mlp_moe_experts_bwd(ctypes.byref(p), plan, dy, xs, Wg, Wu, Wd, G, U, dxs, *grads,
                                      0, ws, 1 << 40, None) == -1
+
+
+def test_experts_forward(L):
+    p = m.moe(16, 8, 2, 64, 128)
+    plan, xs, Wg, Wu, Wd, ws = A[:6]
+    assert L.mlp_moe_experts_fwd(ctypes.byref(p), plan, xs, Wg, Wu, Wd, xs, None, None, ws, 1 << 40,
+                                 None) == -1
