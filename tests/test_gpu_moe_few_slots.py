@@ -138,3 +138,26 @@ def test_plan_without_a_forward():
     m.mlp_moe_combine_bwd(p, plan, dout, rows, w, None, got)
     picked = rows[pos].double() * dout[:, None].double()
     assert ((got.double() - picked.sum(-1)).abs() <= sums(264) * picked.norm(dim=-1)).all()
+
+
+def test_bounded_waits():
+    # no work is published: every wait runs out, the status says so, the next call is right
+    T, E, H, inner = 12, 2, 264, 136
+    ones = lambda *s: torch.ones(s, dtype=BF, device="cuda")  # noqa: E731
+    p = m.moe(T, E, 1, H, inner, "relu")
+    ids = (torch.arange(T, device="cuda") % E).int().view(T, 1)
+    plan, rows = m.alloc_moe_plan(p), m.mlp_moe_rows(p)
+    m.mlp_moe_sort(p, ids, plan)
+    xs, y, W1, Wd = ones(rows, H), ones(rows, H) * 7, ones(E, inner, H), ones(E, H, inner)
+    m.mlp_set_wait_timeout_ms(20)
+    m.mlp_debug_set_flags(m.DEBUG_NO_WORK)
+    try:
+        ws = m.mlp_moe_experts_fwd(p, plan, xs, W1, None, Wd, y)
+        assert m.mlp_device_status(ws) == -6
+    finally:
+        m.mlp_debug_set_flags(0)
+        m.mlp_set_wait_timeout_ms(0)
+    ws = m.mlp_moe_experts_fwd(p, plan, xs, W1, None, Wd, y)
+    assert m.mlp_device_status(ws) == 0
+    used = int(m.moe_plan_views(p, plan)["offsets"][-1])
+    assert (y[:used] == float(torch.tensor(float(H * inner)).to(BF))).all()
