@@ -146,6 +146,8 @@ def lib():
     L.mlp_kernel_name.restype = ctypes.c_char_p
     experts.declare(L)
     linear_op.declare(L)
+    router_op.declare(L)
+    norm_op.declare(L)
     _LIB = L
     return L
 
@@ -477,7 +479,7 @@ def mlp_debug_set_flags(flags: int) -> None:
 
 
 
-from . import experts, linear_op  # noqa: E402  (mixture of experts; linear layer)
+from . import experts, linear_op, norm_op, router_op  # noqa: E402
 from .experts import (Moe, alloc_moe_plan, alloc_moe_workspace, mlp_moe_combine,  # noqa: E402
                       mlp_moe_combine_bwd, mlp_moe_dispatch, mlp_moe_dispatch_bwd,
                       mlp_moe_experts_bwd, mlp_moe_experts_fwd, mlp_moe_fwd_infer, mlp_moe_rows,
@@ -494,6 +496,18 @@ from .linear_op import (LINEAR_ACTS, Linear, alloc_linear_workspace, linear,  # 
 __all__ += ["LINEAR_ACTS", "Linear", "linear", "alloc_linear_workspace", "mlp_linear_fwd",
             "mlp_linear_bwd", "mlp_linear_workspace_size"]
 
-from .autograd import linear_func, mlp_block_func, mlp_func, moe_func  # noqa: E402  (differentiable)
+from .norm_op import (LayerNorm, alloc_layernorm_workspace, layernorm,  # noqa: E402
+                      mlp_layernorm_bwd, mlp_layernorm_fwd, mlp_layernorm_workspace_size)
+from .router_op import (Router, alloc_router_workspace, mlp_moe_router_bwd,  # noqa: E402
+                        mlp_moe_router_fwd, mlp_moe_router_workspace_size, router)
 
-__all__ += ["mlp_func", "mlp_block_func", "linear_func", "moe_func"]
+__all__ += ["LayerNorm", "layernorm", "alloc_layernorm_workspace", "mlp_layernorm_fwd",
+            "mlp_layernorm_bwd", "mlp_layernorm_workspace_size", "Router", "router",
+            "alloc_router_workspace", "mlp_moe_router_fwd", "mlp_moe_router_bwd",
+            "mlp_moe_router_workspace_size"]
+
+from .autograd import (layer_norm_func, linear_func, mlp_block_func, mlp_func,  # noqa: E402
+                       moe_func, router_func)  # (differentiable)
+
+__all__ += ["mlp_func", "mlp_block_func", "linear_func", "moe_func", "router_func",
+            "layer_norm_func"]

@@ -25,8 +25,9 @@ mlp_block_bwd call (saved preacts and the per-token 1/rms).
 
 None of them can be differentiated twice: a second derivative raises.
 
-linear_func is the linear layer with bias, activation and residual, and
-moe_func the mixture-of-experts MLP (at the end of this file).
+linear_func is the linear layer with bias, activation and residual, moe_func the
+mixture-of-experts MLP, router_func its router, and layer_norm_func the layer norm
+(at the end of this file).
 """
 from __future__ import annotations
 
@@ -41,6 +42,8 @@ from .experts import (alloc_moe_plan, mlp_moe_combine, mlp_moe_combine_bwd, mlp_
                       mlp_moe_dispatch_bwd, mlp_moe_experts_bwd, mlp_moe_experts_fwd,
                       mlp_moe_fwd_infer, mlp_moe_rows, mlp_moe_sort, moe)
 from .linear_op import linear, mlp_linear_bwd, mlp_linear_fwd
+from .norm_op import layernorm, mlp_layernorm_bwd, mlp_layernorm_fwd
+from .router_op import mlp_moe_router_bwd, mlp_moe_router_fwd, router
 
 
 def _check_operand(t, name):
@@ -408,3 +411,151 @@ def moe_func(x, ids, weights, Wg, Wu, Wd, activation="swiglu", residual=None, ga
         if T:
             mlp_moe_fwd_infer(prob, x2, i2, w2, Wg, Wu, Wd, r2, out)
     return out.view(shape)
+
+
+class _RouterFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, mask, prob, balance):
+        T, k, dev = prob.T, prob.top_k, logits.device
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), device=dev,
+                              dtype=torch.bfloat16 if prob.weights_type else torch.float32)
+        counts = sums = loss = None
+        if balance:
+            counts = torch.empty(prob.E, dtype=torch.int32, device=dev)
+            sums = torch.empty(prob.E + 1, dtype=torch.float32, device=dev)
+        mlp_moe_router_fwd(prob, logits, mask, ids, weights, counts, sums)
+        if balance:
+            loss = sums.as_strided((), ())
+            ctx.mark_non_differentiable(ids, counts)
+        else:
+            ctx.mark_non_differentiable(ids)
+        ctx.prob = prob
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(logits, mask, ids, sums)
+        return ids, weights, counts, loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _ids, dweights, _counts, dloss):
+        logits, mask, ids, sums = ctx.saved_tensors
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        if dweights is None and dloss is None:
+            return dlogits.zero_(), None, None, None
+        if dweights is not None:
+            dweights = dweights.to(
+                torch.bfloat16 if ctx.prob.weights_type else torch.float32).contiguous()
+        if dloss is not None:
+            dloss = dloss.to(torch.float32)
+        mlp_moe_router_bwd(ctx.prob, logits, mask, ids, sums, dweights, dloss, dlogits)
+        return dlogits, None, None, None
+
+
+def router_func(logits, top_k, mask=None, renormalize=True, weights_dtype=torch.float32,
+                balance=True):
+    """(ids, weights, counts, loss) of the router's logits [..., E] (fp32 or bf16): the top_k
+    experts of each token (int32 [..., top_k]) and their softmax weights (with renormalize
+    divided by their sum), what moe_func takes; the experts' slots (int32 [E]) and the balance
+    loss E sum_e f_e P_e (fp32, no dimensions), both None with balance=False.  mask [...]
+    (bool): false for tokens that are not routed (ids -1).  Differentiable with respect to
+    logits through weights and loss."""
+    for t, name in ((logits, "logits"),) + (((mask, "mask"),) if mask is not None else ()):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    if logits.dim() == 0:
+        raise ValueError("logits must be [..., E]")
+    lead, E = logits.shape[:-1], logits.shape[-1]
+    l2 = logits if logits.dim() == 2 else logits.reshape(-1, E)
+    if l2.shape[0] and (l2.stride(1) != 1 and E > 1 or l2.stride(0) < E):
+        l2 = l2.contiguous()
+    T, m2 = l2.shape[0], None
+    if mask is not None:
+        _check_shape(mask, lead, "mask")
+        m2 = mask.reshape(T).contiguous()
+    prob = router(T, E, top_k, renormalize, logits.dtype, weights_dtype)
+    if T == 0:
+        ids = torch.empty((0, top_k), dtype=torch.int32, device=logits.device)
+        weights = l2.new_empty((0, top_k), dtype=weights_dtype) + l2.sum().to(weights_dtype)
+        counts = loss = None
+        if balance:
+            counts, loss = ids.new_zeros(E), l2.sum(dtype=torch.float32)
+    else:
+        ids, weights, counts, loss = _RouterFunction.apply(l2, m2, prob, bool(balance))
+    return ids.view(*lead, top_k), weights.view(*lead, top_k), counts, loss
+
+
+class _LayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, prob, fuse_grad_accum):
+        y = torch.empty((prob.M, prob.H), dtype=x.dtype, device=x.device)
+        h = torch.empty_like(y) if residual is not None else None
+        mean = torch.empty(prob.M, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        ctx.prob, ctx.fuse = prob, fuse_grad_accum
+        ctx.set_materialize_grads(False)
+        if prob.M:
+            mlp_layernorm_fwd(prob, x, residual, weight, bias, y, h, mean, rstd)
+        ctx.save_for_backward(x if h is None else h, weight, bias, mean, rstd)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        h, weight, bias, mean, rstd = ctx.saved_tensors
+        p, need = ctx.prob, ctx.needs_input_grad
+        none = (None, None)
+        if dy is None:  # h alone was used
+            return (dh, dh if need[1] else None, None, None, *none)
+        dy = dy.to(h.dtype).contiguous()
+        dh = None if dh is None else dh.to(h.dtype).contiguous()
+        dx = torch.empty_like(dy) if need[0] or need[1] else None
+        dw = _grad_like(weight, ctx.fuse, "weight") if weight is not None and need[2] else None
+        db = _grad_like(bias, ctx.fuse, "bias") if bias is not None and need[3] else None
+        if p.M == 0:
+            if not ctx.fuse:
+                for g in (dw, db):
+                    if g is not None:
+                        g.zero_()
+        else:
+            # (a row's gradient needs h dense)
+            mlp_layernorm_bwd(p, dy, h.contiguous(), weight, mean, rstd, dh, dx, dw, db,
+                              fuse_grad_accum=ctx.fuse)
+        return (dx if need[0] else None, dx if need[1] else None, None if ctx.fuse else dw,
+                None if ctx.fuse else db, *none)
+
+
+def layer_norm_func(x, weight=None, bias=None, residual=None, eps=1e-5, fuse_grad_accum=False):
+    """The layer norm over the last dimension of x (fp32 or bf16), of at most NORM_MAX_H values:
+    y = (h - mean) * rstd * weight + bias with h = x + residual.  Without a residual it returns
+    y, with one (y, h).  Differentiable with respect to x, residual, weight and bias (weight and
+    bias in one type, fp32 or bf16)."""
+    for t, name in ((x, "x"), (weight, "weight"), (bias, "bias"), (residual, "residual")):
+        if t is None and name != "x":
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dim() == 0:
+        raise ValueError("x must be [..., H]")
+    shape, H = x.shape, x.shape[-1]
+
+    def rows(t):
+        t = t if t.dim() == 2 else t.reshape(-1, H)
+        ok = t.stride(1) == 1 and t.stride(0) >= H and t.stride(0) % 8 == 0
+        return t if ok and t.data_ptr() % 16 == 0 else t.contiguous()
+
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _check_shape(t, (H,), name)
+    if residual is not None:
+        _check_rows(residual, shape[:-1], H, "residual")
+        if residual.dtype != x.dtype:
+            raise ValueError(f"residual must be {x.dtype}, got {residual.dtype}")
+    x2, r2 = rows(x), None if residual is None else rows(residual)
+    wt = next((t.dtype for t in (weight, bias) if t is not None), x.dtype)
+    prob = layernorm(x2.shape[0], H, eps, x.dtype, wt)
+    y, h = _LayerNormFunction.apply(x2, r2, weight, bias, prob, bool(fuse_grad_accum))
+    return y.view(shape) if h is None else (y.view(shape), h.view(shape))

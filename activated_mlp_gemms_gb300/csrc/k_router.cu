@@ -1,0 +1,537 @@
+// The router of a mixture of experts (mlp_router.h): softmax over a token's logits,
+// its top_k experts, their weights, the experts' counts and the balance loss; and the
+// logits' gradient.
+//
+// G lanes take a token, each V of its logits (E <= G V) in registers; a warp holds 32 / G
+// tokens.  The choice is top_k rounds of a largest value over the lanes: the values as
+// integers of the same order, of equals the lowest expert.  What a row needs of the others
+// (counts, the probabilities' sums) stays in registers and shared memory until the block's
+// tokens are done, goes out as one partial sum a block, and a second kernel adds the blocks
+// in their order.
+#include <cuda_bf16.h>
+
+#include "gemm_params.h"
+#include "ptx.cuh"
+#include "step.h"
+
+namespace mlpk {
+
+namespace {
+
+constexpr int ROUTER_THREADS = 256;
+constexpr int FINISH_CTAS = 8;  // one cluster
+constexpr uint32_t KEY_NEG_INF = 0x007fffffu;
+
+// A float as an unsigned integer of the same order: -0 is 0, a NaN above all.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t b = __float_as_uint(f + 0.f);
+  if (f != f) return 0xffffffffu;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (G == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+
+// A lane's V values of a row come in chunks of one load: chunk i at i G C + lane C.
+template <typename L, int G, int V>
+struct Row {
+  static constexpr int MOST = 16 / static_cast<int>(sizeof(L));
+  static constexpr int C = V < MOST ? V : MOST;
+  static __device__ __forceinline__ int at(int lane, int v) {
+    return (v / C) * (G * C) + lane * C + v % C;
+  }
+  // vec: the row's chunks are aligned
+  static __device__ __forceinline__ void load(const L* row, int lane, int E, bool vec,
+                                              float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += C) {
+      const int e = at(lane, i);
+      if (vec && e + C <= E) {
+        alignas(16) L raw[C];
+        if constexpr (sizeof(raw) == 16)
+          *reinterpret_cast<uint4*>(raw) = __ldg(reinterpret_cast<const uint4*>(row + e));
+        else
+          *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + e));
+#pragma unroll
+        for (int j = 0; j < C; ++j) x[i + j] = static_cast<float>(raw[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+          x[i + j] = e + j < E ? static_cast<float>(row[e + j]) : -INFINITY;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(L* row, int lane, int E, bool vec,
+                                               const float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += C) {
+      const int e = at(lane, i);
+      alignas(16) L raw[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) raw[j] = static_cast<L>(x[i + j]);
+      if (vec && e + C <= E) {
+        if constexpr (sizeof(raw) == 16)
+          *reinterpret_cast<uint4*>(row + e) = *reinterpret_cast<const uint4*>(raw);
+        else
+          *reinterpret_cast<uint2*>(row + e) = *reinterpret_cast<const uint2*>(raw);
+      } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+          if (e + j < E) row[e + j] = raw[j];
+      }
+    }
+  }
+};
+
+// d loss / d p of an expert with c slots, of N routed tokens.
+__device__ __forceinline__ float balance_coef(int E, int top_k, int c, int N) {
+  return N > 0 ? static_cast<float>(static_cast<double>(E) * c /
+                                    (static_cast<double>(top_k) * N * N))
+               : 0.f;
+}
+
+// The sum of the block's threads (in a fixed order), in thread 0.
+__device__ __forceinline__ float block_sum(float v) {
+  __shared__ float warps_s[ROUTER_THREADS / 32];
+  v = group_sum<32>(v);
+  if (threadIdx.x % 32 == 0) warps_s[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < ROUTER_THREADS / 32; ++i) v += warps_s[i];
+  return v;
+}
+
+struct FwdOut {
+  int* ids;
+  void* weights;
+  int* counts;
+  float* balance;
+  RouterParts parts;
+  int* status;
+};
+
+template <typename L, int G, int V, bool SUMS>
+__global__ void __launch_bounds__(ROUTER_THREADS)
+    k_router_fwd(const RouterArgs a, const FwdOut o, const bool vec) {
+  constexpr int NG = ROUTER_THREADS / G;
+  using R = Row<L, G, V>;
+  extern __shared__ float router_smem[];
+  const int tid = threadIdx.x, lane = tid % G, g = tid / G, E = a.E, k = a.top_k;
+  int* sel_id = reinterpret_cast<int*>(router_smem) + g * k;
+  float* sel_x = router_smem + (NG + g) * k;
+  int* cnt = reinterpret_cast<int*>(router_smem + 2 * NG * k);  // [E], SUMS
+  float* psum = router_smem + 2 * NG * k + E;                   // [NG, E], SUMS
+  __shared__ int routed_s[NG];
+  if constexpr (SUMS) {
+    for (int e = tid; e < E; e += ROUTER_THREADS) cnt[e] = 0;
+    __syncthreads();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (SUMS && o.status && blockIdx.x == 0 && tid == 0) *o.status = 0;
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  int n_routed = 0;
+  // (every group of a warp stays in the loop to its end: they share the shuffles)
+  for (long long base = static_cast<long long>(blockIdx.x) * NG; base < a.T;
+       base += static_cast<long long>(gridDim.x) * NG) {
+    const long long t = base + g;
+    const bool in = t < a.T;
+    const bool take = in && (!a.mask || a.mask[t]);
+    float x[V];
+    uint32_t key[V];
+    if (take) {
+      R::load(static_cast<const L*>(a.logits) + t * a.ldl, lane, E, vec, x);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = -INFINITY;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);
+    uint32_t top = 0;
+    for (int j = 0; j < k; ++j) {
+      uint32_t bk = 0;
+      int be = 0;
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v) {
+        const bool better = key[v] >= bk;
+        bk = better ? key[v] : bk;
+        be = better ? R::at(lane, v) : be;
+      }
+      if constexpr (G == 32) {
+        const uint32_t most = __reduce_max_sync(0xffffffffu, bk);
+        be = __reduce_min_sync(0xffffffffu, bk == most ? be : 0x7fffffff);
+        bk = most;
+      } else {
+#pragma unroll
+        for (int s = G / 2; s > 0; s >>= 1) {
+          const uint32_t ok = __shfl_xor_sync(0xffffffffu, bk, s);
+          const int oe = __shfl_xor_sync(0xffffffffu, be, s);
+          const bool better = ok > bk || (ok == bk && oe < be);
+          bk = better ? ok : bk;
+          be = better ? oe : be;
+        }
+      }
+      if (j == 0) top = bk;
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = R::at(lane, v) == be ? 0u : key[v];
+      if (lane == 0) {
+        sel_id[j] = bk > KEY_NEG_INF ? be : -1;
+        sel_x[j] = key_value(bk);
+      }
+    }
+    __syncwarp();
+    const bool routed = top > KEY_NEG_INF;
+    const float m = key_value(top);
+    float total = 0.f;  // of the softmax, or of the chosen
+    if (SUMS || !a.renorm) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[v] = routed ? expf(x[v] - m) : 0.f;
+        total += x[v];
+      }
+      total = group_sum<G>(total);
+      if constexpr (SUMS) {
+        const float inv = routed ? 1.f / total : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += x[v] * inv;
+        n_routed += routed;
+      }
+    }
+    if (a.renorm) {
+      total = 0.f;
+      for (int j = lane; j < k; j += G)
+        if (sel_id[j] >= 0) total += expf(sel_x[j] - m);
+      total = group_sum<G>(total);
+    }
+    if (in) {
+      for (int j = lane; j < k; j += G) {
+        const int id = sel_id[j];
+        const float w = id >= 0 ? expf(sel_x[j] - m) / total : 0.f;
+        o.ids[t * k + j] = id;
+        if (a.w_bf16) static_cast<__nv_bfloat16*>(o.weights)[t * k + j] = __float2bfloat16_rn(w);
+        else static_cast<float*>(o.weights)[t * k + j] = w;
+        if (SUMS && id >= 0) atomicAdd(&cnt[id], 1);
+      }
+    }
+    __syncwarp();
+  }
+  if constexpr (SUMS) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = R::at(lane, v);
+      if (e < E) psum[g * E + e] = acc[v];
+    }
+    if (lane == 0) routed_s[g] = n_routed;
+    __syncthreads();
+    int n = 0;
+    for (int i = 0; i < NG; ++i) n += routed_s[i];
+    float loss = 0.f;
+    for (int e = tid; e < E; e += ROUTER_THREADS) {
+      float s = 0.f;
+      for (int i = 0; i < NG; ++i) s += psum[i * E + e];
+      if (gridDim.x > 1) {
+        const size_t at = static_cast<size_t>(blockIdx.x) * E + e;
+        o.parts.c[at] = cnt[e];
+        o.parts.p[at] = s;
+      } else {  // all tokens were here
+        const float coef = balance_coef(E, k, cnt[e], n);
+        if (o.counts) o.counts[e] = cnt[e];
+        if (o.balance) o.balance[1 + e] = coef;
+        loss += coef * s;
+      }
+    }
+    if (gridDim.x > 1) {
+      if (tid == 0) o.parts.n[blockIdx.x] = n;
+    } else if (o.balance) {
+      loss = block_sum(loss);
+      if (tid == 0) o.balance[0] = loss;
+    }
+  }
+}
+
+// The blocks' sums in their order: one cluster, each CTA its share of the experts.
+__global__ void __launch_bounds__(ROUTER_THREADS)
+    k_router_finish(const int blocks, const int E, const int top_k, const RouterParts parts,
+                    int* __restrict__ counts, float* __restrict__ balance) {
+  __shared__ float p_s[ROUTER_THREADS];
+  __shared__ int c_s[ROUTER_THREADS];
+  __shared__ int n_s[ROUTER_THREADS / 32];
+  __shared__ float loss_s[FINISH_CTAS];  // CTA 0's
+  const int tid = threadIdx.x;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int share = (E + FINISH_CTAS - 1) / FINISH_CTAS;  // at most 128
+  int wide = 1;
+  while (wide < share) wide *= 2;
+  const int lane = tid % wide, row = tid / wide, rows = ROUTER_THREADS / wide;
+  const int e = rank * share + lane;
+  const bool mine = lane < share && e < E;
+  cluster_sync();  // CTA 0 is there
+  pdl_wait();
+  pdl_launch_dependents();
+  int n = 0;
+  for (int b = tid; b < blocks; b += ROUTER_THREADS) n += parts.n[b];
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (tid % 32 == 0) n_s[tid / 32] = n;
+  int c = 0;
+  float s = 0.f;
+  if (mine) {
+#pragma unroll 4
+    for (int b = row; b < blocks; b += rows) {
+      c += parts.c[static_cast<size_t>(b) * E + e];
+      s += parts.p[static_cast<size_t>(b) * E + e];
+    }
+  }
+  c_s[tid] = c;
+  p_s[tid] = s;
+  __syncthreads();
+  for (int i = ROUTER_THREADS / 2; i >= wide; i /= 2) {
+    if (tid < i) {
+      c_s[tid] += c_s[tid + i];
+      p_s[tid] += p_s[tid + i];
+    }
+    __syncthreads();
+  }
+  float loss = 0.f;
+  if (row == 0 && mine) {
+    n = 0;
+    for (int i = 0; i < ROUTER_THREADS / 32; ++i) n += n_s[i];
+    const float coef = balance_coef(E, top_k, c_s[lane], n);
+    if (counts) counts[e] = c_s[lane];
+    if (balance) balance[1 + e] = coef;
+    loss = coef * p_s[lane];
+  }
+  loss = block_sum(loss);
+  if (tid == 0) {
+    const uint32_t to = mapa_shared(smem_u32(&loss_s[rank]), 0);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(loss) : "memory");
+  }
+  cluster_sync();
+  if (rank == 0 && tid == 0 && balance) {
+    loss = 0.f;
+    for (int i = 0; i < FINISH_CTAS; ++i) loss += loss_s[i];
+    balance[0] = loss;
+  }
+}
+
+template <typename L, int G, int V>
+__global__ void __launch_bounds__(ROUTER_THREADS)
+    k_router_bwd(const RouterArgs a, const int* __restrict__ ids,
+                 const float* __restrict__ balance, const void* __restrict__ dweights,
+                 const float* __restrict__ dloss, void* dlogits, const bool vec, const bool vec_d) {
+  constexpr int NG = ROUTER_THREADS / G;
+  using R = Row<L, G, V>;
+  extern __shared__ float router_smem[];
+  const int tid = threadIdx.x, lane = tid % G, g = tid / G, E = a.E, k = a.top_k;
+  // what the weights' gradient adds at the chosen experts; zero between tokens
+  float* extra = router_smem + g * (G * V);
+#pragma unroll
+  for (int v = 0; v < V; ++v) extra[v * G + lane] = 0.f;
+  __syncwarp();
+  pdl_wait();
+  pdl_launch_dependents();
+  float coef[V];
+  {
+    const float d = dloss ? *dloss : 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = R::at(lane, v);
+      coef[v] = dloss && e < E ? balance[1 + e] * d : 0.f;
+    }
+  }
+  auto dw_at = [&](long long i) {
+    return a.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(dweights)[i])
+                    : static_cast<const float*>(dweights)[i];
+  };
+  for (long long base = static_cast<long long>(blockIdx.x) * NG; base < a.T;
+       base += static_cast<long long>(gridDim.x) * NG) {
+    const long long t = base + g;
+    const bool in = t < a.T;
+    const bool take = in && (!a.mask || a.mask[t]);
+    const L* row = static_cast<const L*>(a.logits) + t * a.ldl;
+    float x[V];
+    if (take) {
+      R::load(row, lane, E, vec, x);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = -INFINITY;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) top = max(top, order_key(x[v]));
+    top = group_max<G>(top);
+    const bool routed = top > KEY_NEG_INF;
+    const float m = key_value(top);
+    const bool slots = dweights != nullptr;
+    if (slots) {
+      float total = 1.f, dot = 0.f;
+      if (a.renorm) {
+        float s = 0.f, d = 0.f;
+        for (int j = lane; j < k; j += G) {
+          const int id = routed ? ids[t * k + j] : -1;
+          if (id < 0 || id >= E) continue;
+          const float e = expf(static_cast<float>(row[id]) - m);
+          s += e;
+          d += e * dw_at(t * k + j);
+        }
+        total = group_sum<G>(s);
+        dot = group_sum<G>(d) / total;
+      }
+      for (int j = lane; j < k; j += G) {
+        const int id = routed ? ids[t * k + j] : -1;
+        if (id < 0 || id >= E) continue;
+        float v = dw_at(t * k + j);
+        if (a.renorm) v = expf(static_cast<float>(row[id]) - m) / total * (v - dot);
+        atomicAdd(&extra[id], v);  // (a caller's ids may name an expert twice)
+      }
+      __syncwarp();
+    }
+    float total = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = routed ? expf(x[v] - m) : 0.f;
+      total += x[v];
+    }
+    total = group_sum<G>(total);
+    const float inv = routed ? 1.f / total : 0.f;
+    float dot = 0.f;
+    float more[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      more[v] = slots ? extra[R::at(lane, v)] : 0.f;
+      x[v] *= inv;
+      dot += x[v] * (a.renorm ? coef[v] : coef[v] + more[v]);
+    }
+    dot = group_sum<G>(dot);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      x[v] = a.renorm ? x[v] * (coef[v] - dot) + more[v] : x[v] * (coef[v] + more[v] - dot);
+    // (the row was read by all of its lanes: dlogits may lie over logits)
+    __syncwarp();
+    if (in) R::store(static_cast<L*>(dlogits) + t * a.ldd, lane, E, vec_d, x);
+    if (slots) {
+      for (int j = lane; j < k; j += G) {
+        const int id = routed ? ids[t * k + j] : -1;
+        if (id >= 0 && id < E) extra[id] = 0.f;
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// Lanes and values a lane by the number of experts: few lanes for few experts, so that a
+// warp takes several tokens.
+template <class F>
+cudaError_t by_experts(int E, F&& f) {
+  if (E <= 32) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+  if (E <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+  if (E <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+  if (E <= 512) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
+  return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
+}
+int lanes_of(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : 32; }
+
+bool rows_aligned(const void* ptr, int ld, bool bf16) {
+  return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 &&
+         static_cast<long long>(ld) * (bf16 ? 2 : 4) % 16 == 0;
+}
+
+cudaLaunchConfig_t config(int blocks, size_t smem, cudaStream_t stream,
+                          cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(ROUTER_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+int tokens_blocks(int T, int E) {  // one round of a block's groups each
+  const int ng = ROUTER_THREADS / lanes_of(E);
+  return (T - 1) / ng + 1;
+}
+
+}  // namespace
+
+// (a function of the sizes alone: the workspace is, too)
+int router_blocks(int T, int E) {
+  const int all = tokens_blocks(T, E);
+  if (all <= 8) return 1;
+  return all < 2 * 152 ? all : 2 * 152;
+}
+
+cudaError_t launch_router_fwd(const RouterArgs& a, int* ids, void* weights, int* counts,
+                              float* balance, const RouterParts& parts, int* status,
+                              cudaStream_t stream) {
+  const bool sums = parts.n != nullptr;
+  const int all = tokens_blocks(a.T, a.E);
+  const int blocks = sums ? router_blocks(a.T, a.E) : all < 8 * 152 ? all : 8 * 152;
+  const FwdOut o{ids, weights, counts, balance, parts, status};
+  const bool vec = rows_aligned(a.logits, a.ldl, a.l_bf16);
+  return by_experts(a.E, [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value, NG = ROUTER_THREADS / G;
+    const size_t smem = (2ull * NG * a.top_k + (sums ? (NG + 1ull) * a.E : 0)) * 4;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(blocks, smem, stream, attr);
+    auto go = [&](auto kern) { return cudaLaunchKernelEx(&cfg, kern, a, o, vec); };
+    if (a.l_bf16) return sums ? go(k_router_fwd<__nv_bfloat16, G, V, true>)
+                              : go(k_router_fwd<__nv_bfloat16, G, V, false>);
+    return sums ? go(k_router_fwd<float, G, V, true>) : go(k_router_fwd<float, G, V, false>);
+  });
+}
+
+cudaError_t launch_router_finish(int T, int E, int top_k, const RouterParts& parts, int* counts,
+                                 float* balance, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config(FINISH_CTAS, 0, stream, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = FINISH_CTAS;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_router_finish, router_blocks(T, E), E, top_k, parts, counts,
+                            balance);
+}
+
+cudaError_t launch_router_bwd(const RouterArgs& a, const int* ids, const float* balance,
+                              const void* dweights, const float* dloss, void* dlogits,
+                              cudaStream_t stream) {
+  const int all = tokens_blocks(a.T, a.E);
+  const int blocks = all < 8 * 152 ? all : 8 * 152;
+  const bool vec = rows_aligned(a.logits, a.ldl, a.l_bf16);
+  const bool vec_d = rows_aligned(dlogits, a.ldd, a.l_bf16);
+  return by_experts(a.E, [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(blocks, ROUTER_THREADS * V * 4ull, stream, attr);
+    auto go = [&](auto kern) {
+      return cudaLaunchKernelEx(&cfg, kern, a, ids, balance, dweights, dloss, dlogits, vec, vec_d);
+    };
+    return a.l_bf16 ? go(k_router_bwd<__nv_bfloat16, G, V>) : go(k_router_bwd<float, G, V>);
+  });
+}
+
+}  // namespace mlpk

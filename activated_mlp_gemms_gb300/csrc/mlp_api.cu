@@ -917,6 +917,15 @@ const char* mlp_kernel_name(int tag) {
     case MLP_KERNEL_LINEAR: return "linear";
     case MLP_KERNEL_LINEAR_DACT: return "linear_dact";
     case MLP_KERNEL_LINEAR_DB: return "linear_db";
+    case MLP_KERNEL_ROUTER: return "router";
+    case MLP_KERNEL_ROUTER_BWD: return "router_bwd";
+    case MLP_KERNEL_LAYERNORM: return "layernorm";
+    case MLP_KERNEL_LAYERNORM_BWD: return "layernorm_bwd";
+    case MLP_KERNEL_LAYERNORM_SUMS: return "layernorm_sums";
+    case MLP_KERNEL_ORTHO_SCALE: return "ortho_scale";
+    case MLP_KERNEL_ORTHO_GRAM: return "ortho_gram";
+    case MLP_KERNEL_ORTHO_POLY: return "ortho_poly";
+    case MLP_KERNEL_ORTHO_STEP: return "ortho_step";
     default: return "unknown";
   }
 }

@@ -473,7 +473,19 @@ typedef enum {
   /* mlp_linear.h */
   MLP_KERNEL_LINEAR = 17,          /* the linear layer with its epilogue (GEMM or weight stream) */
   MLP_KERNEL_LINEAR_DACT = 18,     /* dz and the bias gradient's partial sums */
-  MLP_KERNEL_LINEAR_DB = 19        /* the bias gradient from its partial sums */
+  MLP_KERNEL_LINEAR_DB = 19,       /* the bias gradient from its partial sums */
+  /* mlp_router.h */
+  MLP_KERNEL_ROUTER = 20,          /* the experts' choice, weights, counts and balance loss */
+  MLP_KERNEL_ROUTER_BWD = 21,      /* the logits' gradient */
+  /* mlp_norm.h */
+  MLP_KERNEL_LAYERNORM = 22,       /* the layer norm with the residual sum */
+  MLP_KERNEL_LAYERNORM_BWD = 23,   /* its gradient and the weight gradients' partial sums */
+  MLP_KERNEL_LAYERNORM_SUMS = 24,  /* the weight gradients from their partial sums */
+  /* mlp_ortho.h */
+  MLP_KERNEL_ORTHO_SCALE = 25,     /* an update's norm, and X from it */
+  MLP_KERNEL_ORTHO_GRAM = 26,      /* A = X X^T */
+  MLP_KERNEL_ORTHO_POLY = 27,      /* b A + c A A */
+  MLP_KERNEL_ORTHO_STEP = 28       /* a X + (b A + c A A) X */
 } mlp_kernel_t;
 
 /* on != 0 starts recording, 0 stops (records already taken are kept). */
