@@ -148,6 +148,7 @@ def lib():
     linear_op.declare(L)
     router_op.declare(L)
     norm_op.declare(L)
+    ortho_op.declare(L)
     _LIB = L
     return L
 
@@ -479,7 +480,7 @@ def mlp_debug_set_flags(flags: int) -> None:
 
 
 
-from . import experts, linear_op, norm_op, router_op  # noqa: E402
+from . import experts, linear_op, norm_op, ortho_op, router_op  # noqa: E402
 from .experts import (Moe, alloc_moe_plan, alloc_moe_workspace, mlp_moe_combine,  # noqa: E402
                       mlp_moe_combine_bwd, mlp_moe_dispatch, mlp_moe_dispatch_bwd,
                       mlp_moe_experts_bwd, mlp_moe_experts_fwd, mlp_moe_fwd_infer, mlp_moe_rows,
@@ -498,13 +499,16 @@ __all__ += ["LINEAR_ACTS", "Linear", "linear", "alloc_linear_workspace", "mlp_li
 
 from .norm_op import (LayerNorm, alloc_layernorm_workspace, layernorm,  # noqa: E402
                       mlp_layernorm_bwd, mlp_layernorm_fwd, mlp_layernorm_workspace_size)
+from .ortho_op import (MUON_COEFFS, Ortho, alloc_ortho_workspace,  # noqa: E402
+                       mlp_ortho_workspace_size, mlp_orthogonalize, ortho)
 from .router_op import (Router, alloc_router_workspace, mlp_moe_router_bwd,  # noqa: E402
                         mlp_moe_router_fwd, mlp_moe_router_workspace_size, router)
 
 __all__ += ["LayerNorm", "layernorm", "alloc_layernorm_workspace", "mlp_layernorm_fwd",
             "mlp_layernorm_bwd", "mlp_layernorm_workspace_size", "Router", "router",
             "alloc_router_workspace", "mlp_moe_router_fwd", "mlp_moe_router_bwd",
-            "mlp_moe_router_workspace_size"]
+            "mlp_moe_router_workspace_size", "MUON_COEFFS", "Ortho", "ortho", "alloc_ortho_workspace",
+            "mlp_ortho_workspace_size", "mlp_orthogonalize"]
 
 from .autograd import (layer_norm_func, linear_func, mlp_block_func, mlp_func,  # noqa: E402
                        moe_func, router_func)  # (differentiable)

@@ -1,0 +1,48 @@
+// ortho.h -- launchers of the orthogonalised update's kernels (mlp_ortho.h).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mlpk {
+
+// X, A and b A + c A A are fp16 at these powers of two: with singular values below 4, X's
+// entries stay below 2^16, and with them below 1.3 A's and the polynomial's, which are its
+// largest, below 20 2^11.  What a matrix's typical entry is (1 / sqrt(m n) of X at the
+// start, 1 / (m sqrt(n)) of A off its diagonal) stays above fp16's smallest normal value
+// for m, n up to 16384.
+constexpr float ORTHO_X = 16384.f, ORTHO_A = 2048.f;
+
+constexpr int ORTHO_PARTS = 64;  // partial sums of a matrix's norm
+
+// One product D = alpha in + beta P Q of a stack, P [M, K] K-major, Q [N, K] K-major or
+// [K, N]; the three products hi lo + lo hi + hi hi with `terms` 2.  in and D in one or two
+// fp16 terms.
+struct OrthoGemm {
+  CUtensorMap p, q;  // depth batch x terms
+  int M, N, kblocks, terms, batch;
+  int sym;           // D is symmetric: the tiles below the diagonal, and their mirror images
+  int tiles_m, tiles_n, units;
+  float alpha, beta;
+  const void *in_hi, *in_lo;  // null: none
+  void *hi, *lo;              // fp16 terms out (null: none)
+  void* out;                  // or the result: bf16 or fp32, as it is or transposed
+  int out_bf16, transposed;
+  int* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
+};
+// cg 2: CTA pairs, 256 x 256 tiles; 1: single CTAs, 128 x 128 tiles.
+cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, bool q_mn, cudaStream_t stream);
+// Clusters of an instance that are resident together (0 on error).
+int ortho_clusters(int cg, bool q_mn);
+
+// part [batch, ORTHO_PARTS] = sums of squares of G's matrices; clears *status.
+cudaError_t launch_ortho_norm(const void* G, bool bf16, long long size, int batch, float* part,
+                              int* status, cudaStream_t stream);
+// X = ORTHO_X G / (|G| + eps) in two fp16 terms [2, batch, m, n], transposed where rows > cols.
+cudaError_t launch_ortho_scale(const void* G, bool bf16, int rows, int cols, int batch,
+                               const float* part, float eps, void* X, cudaStream_t stream);
+
+}  // namespace mlpk

@@ -1,0 +1,58 @@
+/*
+ * mlp_ortho.h -- C ABI of the orthogonalised update of libmlp.so: a gradient or
+ * momentum G of a weight matrix, or of a stack of them (the experts'), brought
+ * near the orthogonal matrix of its own singular vectors by Newton-Schulz
+ * products, as the Muon optimiser does with a linear layer's update (the
+ * optimiser of modded-nanogpt's training script):
+ *
+ *   X = G / (|G| + eps)                      |G| the Frobenius norm of one matrix
+ *   X <- a X + (b A + c A A) X,  A = X X^T   `steps` times
+ *   out = scale * X
+ *
+ * (G with more rows than columns: the same with X^T X on the other side.)  An
+ * addition of this library; the conventions of mlp.h (ownership, streams,
+ * alignment, return values, workspace, device-side errors, determinism) hold
+ * here.
+ */
+#ifndef MLP_GB300_ORTHO_H
+#define MLP_GB300_ORTHO_H
+
+#include "mlp.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { MLP_ORTHO_F32 = 0, MLP_ORTHO_BF16 = 1 } mlp_ortho_type_t;
+
+/* A stack of `batch` matrices [rows, cols] (dense), rows and cols multiples of
+ * 8.  coeff: a, b, c; they keep every singular value below 4 (those of the Muon
+ * optimiser, 3.4445, -4.7750, 2.0315, below 1.3).  steps 1 to 32; eps >= 0.
+ *
+ * Arithmetic: X and A are held as fp16 at a fixed power of two (X has no entry
+ * above 4), X with the remainder of its rounding beside it, the products summed
+ * in fp32.  A bf16 out takes the products of the leading terms (relative error of
+ * the result 1.7e-3 at most in the tests, the rounding of out itself 1.7e-3); an
+ * fp32 out takes those with the remainders too (1e-5).  |G| is summed in fp32:
+ * entries above 1e19 overflow it. */
+typedef struct {
+  int rows, cols, batch;
+  int steps;
+  float coeff[3];
+  float eps, scale;
+  int type;      /* mlp_ortho_type_t of G */
+  int out_type;  /* mlp_ortho_type_t of out */
+} mlp_ortho_t;
+
+/* Bytes of workspace; 0 on invalid arguments. */
+size_t mlp_ortho_workspace_size(const mlp_ortho_t* p);
+
+/*   G [batch, rows, cols] in;  out [batch, rows, cols] out (may be G itself where the
+ *   types are the same) */
+int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, size_t ws_bytes,
+                      void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MLP_GB300_ORTHO_H */

@@ -22,7 +22,8 @@ def L():
 
 
 @pytest.mark.parametrize("header,prefix,n", [("mlp_router.h", "mlp_moe_router_", 3),
-                                             ("mlp_norm.h", "mlp_layernorm_", 3)])
+                                             ("mlp_norm.h", "mlp_layernorm_", 3),
+                                             ("mlp_ortho.h", "mlp_ortho", 2)])
 def test_every_declared_symbol_is_exported(L, header, prefix, n):
     src = open(os.path.join(ROOT, "include", header)).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
@@ -147,3 +148,42 @@ def test_python_refusals():
         m.layer_norm_func(t)
     with pytest.raises(TypeError):
         m.layer_norm_func(None)
+
+
+# ----------------------------------------------------------- orthogonalisation
+
+def ortho(L, p, G=FAKE, out=FAKE + 0x10000, ws=FAKE, n=BIG):
+    return L.mlp_orthogonalize(ctypes.byref(p), G, out, ws, n, None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(rows=0), -1), (dict(cols=-8), -1), (dict(batch=0), -1), (dict(steps=0), -1),
+    (dict(steps=33), -1), (dict(coeff=(float("nan"), 0, 0)), -1), (dict(eps=-1.0), -1),
+    (dict(eps=float("inf")), -1), (dict(scale=float("nan")), -1), (dict(type=2), -1),
+    (dict(out_type=-1), -1), (dict(rows=12), -2), (dict(cols=100), -2),
+    (dict(rows=40000, cols=40000), -3), (dict(rows=8, cols=1 << 22), -3),
+    (dict(batch=65536), -3), (dict(rows=32768, cols=32768, batch=65), -3)])
+def test_ortho_problem_refusals(L, change, code):
+    p = m.ortho(64, 128)
+    for k, v in change.items():
+        setattr(p, k, type(p.coeff)(*v) if k == "coeff" else v)
+    assert m.mlp_ortho_workspace_size(p) == 0
+    assert ortho(L, p) == code
+    with pytest.raises(m.MlpError):
+        m.alloc_ortho_workspace(p)
+
+
+def test_ortho_pointer_refusals(L):
+    p = m.ortho(64, 128)
+    assert ortho(L, p, G=None) == -1 and ortho(L, p, out=None) == -1
+    assert ortho(L, p, G=FAKE + 8) == -2 and ortho(L, p, out=FAKE + 8) == -2
+    assert ortho(L, p, ws=None) == -1 and ortho(L, p, ws=FAKE + 64) == -2
+    assert ortho(L, p, n=m.mlp_ortho_workspace_size(p) - 1) == -4
+    q = m.ortho(64, 128, out_dtype=torch.float32)
+    assert ortho(L, q, G=FAKE, out=FAKE) == -1  # the result over an update of another type
+    assert L.mlp_orthogonalize(None, FAKE, FAKE, FAKE, BIG, None) == -1
+    # X twice in two fp16 terms, A and the polynomial in one or two
+    assert m.mlp_ortho_workspace_size(p) == 1024 + 256 + 2 * 64 * 128 * 4 + 2 * 64 * 64 * 2
+    assert m.mlp_ortho_workspace_size(q) == m.mlp_ortho_workspace_size(p) + 2 * 64 * 64 * 2
+    with pytest.raises(ValueError):
+        m.ortho(64, 64, dtype=torch.float16)
