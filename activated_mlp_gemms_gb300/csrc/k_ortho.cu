@@ -13,10 +13,14 @@
 //
 // The GEMM: one CTA of 320 threads an SM; CTA pairs with 256 x 256 tiles (tcgen05
 // cta_group::2), or single CTAs with 128 x 128 tiles where those are too few.
-//   warp 0     TMA loads of both operands' 64-wide k-blocks into a ring of six 32 KB stages
+//   warp 0     TMA loads of both operands' 64-wide k-blocks into a ring of five 32 KB stages
 //   warp 1     issues tcgen05.mma into one of two accumulators; in a pair's other CTA it
 //              tells the leader that the accumulator has been read
-//   warps 2-9  read the accumulator (a row a thread), add `in`, round and store
+//   warps 2-9  read the accumulator (a row a thread) 32 columns at a time, add `in`, round and
+//              store; `in` and what is stored pass through 32 x 32 boxes in shared memory, two
+//              sets a warp, that TMA fills ahead of the accumulator and empties behind it
+//              (sixteen warps with a set each were no faster: 16 x 1408 x 2048 step 122 us, 118
+//              so; a unit's k-blocks draw 12 TB/s of L2, and that is what `in` and D wait for)
 // The units are dealt in turn (unit u to cluster u mod clusters): all cost the same.  Of a
 // symmetric product only the tiles on and below the diagonal are formed, and stored twice.
 #include <cuda_bf16.h>
@@ -32,11 +36,15 @@ namespace mlpk {
 
 namespace {
 
-constexpr int OSTAGES = 6;
+constexpr int OSTAGES = 5;
 constexpr int OPERAND = 128 * 64 * 2;  // bytes of an operand's k-block in one CTA
 constexpr int OSTAGE = 2 * OPERAND;
-constexpr int OTHREADS = 320;
-constexpr int OSMEM = OSTAGES * OSTAGE + 1024 + 256;  // ring, alignment, control block
+constexpr int EPI_WARPS = 8;  // two a TMEM lane quadrant
+constexpr int OTHREADS = 64 + 32 * EPI_WARPS;
+constexpr int BOX = 2048;                              // 32 x 32 fp16 or bf16
+constexpr int SET = 2 * BOX;                           // two terms, or a box and its mirror image
+constexpr int OSTAGING = EPI_WARPS * 2 * SET;
+constexpr int OSMEM = OSTAGES * OSTAGE + OSTAGING + 1024 + 512;  // ... alignment, control block
 constexpr int O_TIMEOUT = -6;                         // MLP_ERR_TIMEOUT
 
 // kind::f16 with fp16 operands (format 0), fp32 accumulators, M = N = TILE.
@@ -48,12 +56,13 @@ constexpr uint32_t IDESC_FP16 = (1u << 4) | ((Q_MN ? 1u : 0u) << 16) |
 struct Tile {
   int b, tm, tn;
 };
+template <int KIND>
 __device__ __forceinline__ Tile tile_of(const OrthoGemm& g, int unit) {
   Tile t;
   const int per = g.units / g.batch;
   t.b = unit / per;
   const int u = unit - t.b * per;
-  if (g.sym) {  // row tm of the triangle begins at tm (tm + 1) / 2
+  if (KIND == ORTHO_SYM) {  // row tm of the triangle begins at tm (tm + 1) / 2
     t.tm = static_cast<int>((sqrtf(8.f * static_cast<float>(u) + 1.f) - 1.f) * 0.5f);
     while (t.tm * (t.tm + 1) / 2 > u) --t.tm;
     while ((t.tm + 1) * (t.tm + 2) / 2 <= u) ++t.tm;
@@ -73,105 +82,72 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// A thread's 32 columns [col, col + 32) of row `row` of matrix b of the stack.
-__device__ __forceinline__ void store_chunk(const OrthoGemm& g, int b, int row, int col,
-                                            bool mirror, const uint32_t (&acc)[32]) {
-  const bool row_ok = row < g.M;
-  const size_t mn = static_cast<size_t>(g.M) * g.N;
-  const size_t at = b * mn + static_cast<size_t>(row) * g.N + col;
-  float v[32];
+// Row r of a 32 x 32 box of 2-byte values: 64 bytes, the 16-byte parts swizzled (64-byte
+// swizzle), so that a row a thread passes without bank conflicts.
+__device__ __forceinline__ uint32_t part16(uint32_t box, int r, int j) {
+  return box + static_cast<uint32_t>(r * 64 + ((j ^ (r >> 1 & 3)) << 4));
+}
+// The same of a box of 4-byte values: 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint32_t part32(uint32_t box, int r, int j) {
+  return box + static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// The thread's row of 32 packed values, as it is or as column `lane` of the box.
+__device__ __forceinline__ void put16(uint32_t box, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = g.beta * __uint_as_float(acc[i]);
-  if (g.in_hi && row_ok) {
+  for (int j = 0; j < 4; ++j)
+    st_shared_v4(part16(box, lane, j), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+__device__ __forceinline__ void put16_across(uint32_t box, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    st_shared_u16(part16(box, i, lane >> 3) + static_cast<uint32_t>((lane & 7) * 2),
+                  i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+}
+// Adds a row of fp16 values, times alpha.
+__device__ __forceinline__ void add16(uint32_t box, int lane, float alpha, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 q = ld_shared_v4(part16(box, lane, j));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (col + 8 * i >= g.N) break;
-      const uint4 h = ld_global_v4(static_cast<const __half*>(g.in_hi) + at + 8 * i);
-      const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-      uint32_t lw[4] = {};
-      if (g.in_lo) {
-        const uint4 l = ld_global_v4(static_cast<const __half*>(g.in_lo) + at + 8 * i);
-        lw[0] = l.x, lw[1] = l.y, lw[2] = l.z, lw[3] = l.w;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = unpack_half2(hw[j]), y = unpack_half2(lw[j]);
-        v[8 * i + 2 * j] += g.alpha * (x.x + y.x);
-        v[8 * i + 2 * j + 1] += g.alpha * (x.y + y.y);
-      }
-    }
-  }
-  if (g.out) {
-    if (g.transposed) {  // the warp's 32 rows are contiguous
-      if (row_ok) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (col + i >= g.N) break;
-          const size_t o = b * mn + static_cast<size_t>(col + i) * g.M + row;
-          if (g.out_bf16) static_cast<__nv_bfloat16*>(g.out)[o] = __float2bfloat16_rn(v[i]);
-          else static_cast<float*>(g.out)[o] = v[i];
-        }
-      }
-    } else if (row_ok) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (col + 8 * i >= g.N) break;
-        const float* f = v + 8 * i;
-        if (g.out_bf16) {
-          st_global_v4(static_cast<__nv_bfloat16*>(g.out) + at + 8 * i,
-                       make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
-        } else {
-          float* o = static_cast<float*>(g.out) + at + 8 * i;
-          *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<float4*>(o + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        }
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int term = 0; term < 2; ++term) {
-    __half* to = static_cast<__half*>(term ? g.lo : g.hi);
-    if (!to) break;
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-      const float2 x = unpack_half2(w[i]);  // the second term: what the first leaves
-      v[2 * i] -= x.x;
-      v[2 * i + 1] -= x.y;
-    }
-    if (!row_ok) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (col + 8 * i < g.N)
-        st_global_v4(to + at + 8 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
-    if (mirror) {  // (symmetric: M is N)
-      uint16_t* m = reinterpret_cast<uint16_t*>(to) + b * mn + row;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (col + i >= g.N) break;
-        m[static_cast<size_t>(col + i) * g.N] =
-            static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
-      }
+      const float2 x = unpack_half2(w[i]);
+      v[8 * j + 2 * i] += alpha * x.x;
+      v[8 * j + 2 * i + 1] += alpha * x.y;
     }
   }
 }
+// v as fp16, and what that leaves of it in v.
+__device__ __forceinline__ void take_term(float (&v)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+    const float2 x = unpack_half2(w[i]);
+    v[2 * i] -= x.x;
+    v[2 * i + 1] -= x.y;
+  }
+}
 
-template <int CG, bool Q_MN>
+template <int CG, int KIND>
 __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constant__ OrthoGemm g) {
   extern __shared__ uint8_t ortho_smem[];
   constexpr bool PAIR = CG == 2;
+  constexpr bool Q_MN = KIND != ORTHO_SYM;
   constexpr int TILE = 128 * CG;  // rows and columns of a tile
   constexpr uint32_t IDESC = IDESC_FP16<TILE, Q_MN>;
   constexpr uint32_t COLS = 2 * TILE;  // two accumulators
   const uint32_t base = (smem_u32(ortho_smem) + 1023u) & ~1023u;
-  uint8_t* ctrl = ortho_smem + (base - smem_u32(ortho_smem)) + OSTAGES * OSTAGE;
+  uint8_t* ctrl = ortho_smem + (base - smem_u32(ortho_smem)) + OSTAGES * OSTAGE + OSTAGING;
   uint64_t* bar = reinterpret_cast<uint64_t*>(ctrl);
   constexpr int FULL = 0, EMPTY = OSTAGES, TFULL = 2 * OSTAGES, TEMPTY = TFULL + 2,
-                DRAIN = TEMPTY + 2, NBAR = DRAIN + 1;
-  static_assert(8 * NBAR + 8 <= 256, "control block");
+                DRAIN = TEMPTY + 2, IN = DRAIN + 1, NBAR = IN + 2 * EPI_WARPS;
+  static_assert(8 * NBAR + 8 <= 512, "control block");
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(ctrl + 8 * NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
   auto bar_s = [&](int i) { return smem_u32(bar + i); };
@@ -187,14 +163,17 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s(TFULL + i), 1);
-      // the eight epilogue warps; the leader's also: the other CTA's
-      mbar_init(bar_s(TEMPTY + i), 8 + (PAIR && leader ? 1 : 0));
+      // the epilogue warps; the leader's also: the other CTA's
+      mbar_init(bar_s(TEMPTY + i), EPI_WARPS + (PAIR && leader ? 1 : 0));
     }
     mbar_init(bar_s(DRAIN), 1);
+    for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(bar_s(IN + i), 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&g.p);
     prefetch_tmap(&g.q);
+    prefetch_tmap(&g.in);
+    prefetch_tmap(&g.d);
   }
   if (warp == 1) {
     tmem_alloc<CG>(smem_u32(tmem_s), COLS);
@@ -230,7 +209,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       uint32_t phase = 0;
       bool ok = true;
       for (int unit = first; ok && unit < g.units; unit += step) {
-        const Tile t = tile_of(g, unit);
+        const Tile t = tile_of<KIND>(g, unit);
         const int m0 = t.tm * TILE + static_cast<int>(rank) * 128;
         const int n0 = t.tn * TILE + static_cast<int>(rank) * 128;
         int seg = 0, kb = 0;
@@ -336,29 +315,148 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes, half of the columns
+    constexpr int WIDTH = TILE / (EPI_WARPS / 4);  // a warp's columns of the tile
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const uint32_t stg = base + OSTAGES * OSTAGE + static_cast<uint32_t>(warp - 2) * 2 * SET;
+    const uint32_t in_bar = bar_s(IN + 2 * (warp - 2));
+    const uint64_t pol = policy_evict_normal();
+    fence_proxy_async_global();
+    const bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && g.terms == 2);
+    const bool two_in = KIND != ORTHO_SYM || g.terms == 2;
+    const bool has_in = g.alpha != 0.f;
+    uint32_t in_phase = 0;  // a bit a set
+    uint32_t loading = 0;   // sets with a load in flight
     int acc = 0;
     uint32_t aphase = 0;
     for (int unit = first; unit < g.units; unit += step) {
-      const Tile t = tile_of(g, unit);
+      const Tile t = tile_of<KIND>(g, unit);
+      const int row0 = t.tm * TILE + static_cast<int>(rank) * 128 + q * 32;
+      const int col0 = t.tn * TILE + part * WIDTH;
+      const bool mirror = KIND == ORTHO_SYM && t.tm != t.tn;
+      // chunks of 32 columns inside the output
+      int chunks = row0 < g.M ? (g.N - col0 + 31) / 32 : 0;
+      chunks = chunks < 0 ? 0 : chunks < WIDTH / 32 ? chunks : WIDTH / 32;
+      // `in` of chunk c into set c & 1, once what that held has been stored
+      auto load = [&](int c) {
+        const int s = c & 1;
+        if (lane == 0) {
+          const uint32_t bar_in = in_bar + 8 * s, box = stg + s * SET;
+          mbar_expect_tx(bar_in, two_in ? 2 * BOX : BOX);
+          tma_load_3d(box, &g.in, col0 + 32 * c, row0, t.b, bar_in, pol);
+          if (two_in) tma_load_3d(box + BOX, &g.in, col0 + 32 * c, row0, g.batch + t.b, bar_in, pol);
+        }
+        loading |= 1u << s;
+      };
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+      if (has_in) {
+        if (chunks > 0) load(0);
+        if (chunks > 1) load(1);
+      }
       if (!mbar_wait<PAIR>(bar_s(TFULL + acc), aphase, lim, abort_flag)) {
         failed();
         break;
       }
       tc_fence_after();
-      const int row0 = t.tm * TILE + static_cast<int>(rank) * 128 + q * 32;
-      const uint32_t tb = tmem + acc * TILE + (static_cast<uint32_t>(q * 32) << 16);
-      if (row0 < g.M) {
+      const uint32_t tb = tmem + acc * TILE + (static_cast<uint32_t>(q * 32) << 16) +
+                          static_cast<uint32_t>(part * WIDTH);
+      bool ok = true;
 #pragma unroll 1
-        for (int c = half * (TILE / 2); c < (half + 1) * (TILE / 2); c += 32) {
-          const int col = t.tn * TILE + c;
-          if (col >= g.N) break;
+      for (int c = 0; c < chunks; ++c) {
+        const int s = c & 1, col = col0 + 32 * c;
+        const uint32_t box = stg + s * SET;
+        float v[32];
+        {
           uint32_t a[32];
           __syncwarp();
-          tmem_ld32(tb + c, a);
+          tmem_ld32(tb + 32 * c, a);
           tmem_wait_ld();
-          store_chunk(g, t.b, row0 + lane, col, g.sym && t.tm != t.tn, a);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = g.beta * __uint_as_float(a[i]);
         }
+        if (has_in) {
+          if (!mbar_wait(in_bar + 8 * s, in_phase >> s & 1u, lim, abort_flag)) {
+            ok = false;
+            break;
+          }
+          in_phase ^= 1u << s;
+          loading &= ~(1u << s);
+          if (two_in) add16(box + BOX, lane, g.alpha, v);
+          add16(box, lane, g.alpha, v);
+        } else if (lane == 0) {  // the set's last store has read it
+          if (KIND == ORTHO_SYM && two_terms) bulk_wait_read_all();
+          else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        }
+        __syncwarp();  // (the rows are read before another thread's column goes over them)
+        if constexpr (KIND == ORTHO_LAST) {
+          if (g.out_bf16) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            if (g.transposed) put16_across(box, lane, w);
+            else put16(box, lane, w);
+          } else if (g.transposed) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              st_shared_u32(part32(box, i, lane >> 2) + static_cast<uint32_t>((lane & 3) * 4),
+                            __float_as_uint(v[i]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(part32(box, lane, j), __float_as_uint(v[4 * j]),
+                           __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                           __float_as_uint(v[4 * j + 3]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (g.transposed) tma_store_3d(&g.d, box, row0, col, t.b);
+            else tma_store_3d(&g.d, box, col, row0, t.b);
+            bulk_commit();
+          }
+        } else if constexpr (KIND == ORTHO_STEP) {
+          uint32_t w[16];
+          take_term(v, w);
+          put16(box, lane, w);
+          take_term(v, w);
+          put16(box + BOX, lane, w);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&g.d, box, col, row0, t.b);
+            tma_store_3d(&g.d, box + BOX, col, row0, g.batch + t.b);
+            bulk_commit();
+          }
+        } else {
+          // a term and its mirror image at a time
+#pragma unroll 1
+          for (int z = t.b; z < (two_terms ? 2 : 1) * g.batch; z += g.batch) {
+            uint32_t w[16];
+            take_term(v, w);
+            if (z != t.b) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
+            put16(box, lane, w);
+            if (mirror) put16_across(box + BOX, lane, w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&g.d, box, col, row0, z);
+              if (mirror) tma_store_3d(&g.d, box + BOX, row0, col, z);
+              bulk_commit();
+            }
+          }
+        }
+        if (has_in && c + 2 < chunks) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          load(c + 2);
+        }
+      }
+      if (!ok) {
+        failed();
+        break;
       }
       tc_fence_before();
       __syncwarp();
@@ -366,6 +464,14 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       acc ^= 1;
       if (acc == 0) aphase ^= 1u;
     }
+    // what is in flight ends before shared memory is released
+    for (int s = 0; s < 2; ++s)
+      if (loading >> s & 1u) {
+        volatile int never = 0;
+        mbar_wait(in_bar + 8 * s, in_phase >> s & 1u, 10000000ull, &never);
+      }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -375,19 +481,6 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     tc_fence_after();
     tmem_dealloc<CG>(tmem, COLS);
   }
-}
-
-template <int CG, bool Q_MN>
-cudaError_t prepare() {
-  auto kern = k_ortho_gemm<CG, Q_MN>;
-  static std::atomic<unsigned long long> done{0};  // devices that have the attribute
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (done.load() >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, OSMEM);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
-  return e;
 }
 
 cudaLaunchConfig_t ortho_config(int cg, int grid, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -407,9 +500,300 @@ cudaLaunchConfig_t ortho_config(int cg, int grid, cudaStream_t stream, cudaLaunc
   return cfg;
 }
 
-template <int CG, bool Q_MN>
+// Few units with a long K: a cluster of CTAs shares a 128 x 128 tile's k-blocks.  Each leaves
+// its fp32 sums in its shared memory; then each adds up its share of the rows over the
+// cluster's memories, in the CTAs' order, and finishes them.
+constexpr int SPLIT_STAGES = 6;
+constexpr int SPLIT_SMEM = SPLIT_STAGES * OSTAGE + 1024 + 256;
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Part j (16 bytes) of row r of the 128 x 128 fp32 sums: the parts of a row swapped by the row,
+// so that a row a thread and a row a warp both pass without bank conflicts.
+__device__ __forceinline__ uint32_t sum_part(uint32_t at, int r, int j) {
+  return at + static_cast<uint32_t>(r * 512 + ((j ^ (r & 31)) << 4));
+}
+// Stores the terms of eight consecutive values (of D, or of its mirror image).
+__device__ __forceinline__ void store_terms(const OrthoGemm& g, size_t at, size_t term, bool two,
+                                            const float (&f)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_half2(f[2 * i], f[2 * i + 1]);
+    const float2 x = unpack_half2(h[i]);
+    l[i] = pack_half2(f[2 * i] - x.x, f[2 * i + 1] - x.y);
+  }
+  __half* d = static_cast<__half*>(g.d_ptr) + at;
+  st_global_v4(d, make_uint4(h[0], h[1], h[2], h[3]));
+  if (two) st_global_v4(d + term, make_uint4(l[0], l[1], l[2], l[3]));
+}
+__device__ __forceinline__ void store_out(const OrthoGemm& g, size_t at, const float (&f)[8]) {
+  if (g.out_bf16) {
+    st_global_v4(static_cast<__nv_bfloat16*>(g.d_ptr) + at,
+                 make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+  } else {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.d_ptr) + at);
+    o[0] = make_float4(f[0], f[1], f[2], f[3]);
+    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_constant__ OrthoGemm g) {
+  extern __shared__ uint8_t ortho_smem[];
+  constexpr bool Q_MN = KIND != ORTHO_SYM;
+  constexpr uint32_t IDESC = IDESC_FP16<128, Q_MN>;
+  const uint32_t base = (smem_u32(ortho_smem) + 1023u) & ~1023u;
+  uint8_t* base_g = ortho_smem + (base - smem_u32(ortho_smem));
+  uint8_t* ctrl = base_g + SPLIT_STAGES * OSTAGE;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(ctrl);
+  constexpr int FULL = 0, EMPTY = SPLIT_STAGES, DONE = 2 * SPLIT_STAGES, NBAR = DONE + 1;
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(ctrl + 8 * NBAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
+  auto bar_s = [&](int i) { return smem_u32(bar + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SPLIT_STAGES; ++i) {
+      mbar_init(bar_s(FULL + i), 1);
+      mbar_init(bar_s(EMPTY + i), 1);
+    }
+    mbar_init(bar_s(DONE), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&g.p);
+    prefetch_tmap(&g.q);
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(smem_u32(tmem_s), 128);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_s;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const uint64_t lim = g.timeout_ns;
+  const Tile t = tile_of<KIND>(g, static_cast<int>(blockIdx.x) / S);
+  const int m0 = t.tm * 128, n0 = t.tn * 128;
+  const int segs = g.terms == 2 ? 3 : 1, kb_all = g.kblocks * segs;
+  const int per = (kb_all + S - 1) / S;  // (the last CTAs may have none)
+  const int kb0 = rank * per < kb_all ? rank * per : kb_all;
+  const int kb1 = kb0 + per < kb_all ? kb0 + per : kb_all;
+  auto failed = [&] {
+    *abort_flag = 1;
+    atomicExch(g.status, O_TIMEOUT);
+  };
+
+  if (warp == 0) {
+    if (lane == 0 && !(g.debug_flags & 1)) {
+      fence_proxy_async_global();
+      const uint64_t pol = policy_evict_normal();
+      int seg = kb0 / g.kblocks, kb = kb0 - seg * g.kblocks;
+      for (int i = kb0; i < kb1; ++i) {
+        const int n = i - kb0, stage = n % SPLIT_STAGES;
+        if (!mbar_wait(bar_s(EMPTY + stage), (n / SPLIT_STAGES + 1) & 1, lim, abort_flag)) {
+          failed();
+          for (int j = n - SPLIT_STAGES; j < n; ++j) {  // copies in flight land first
+            volatile int never = 0;
+            if (j >= 0)
+              mbar_wait(bar_s(FULL + j % SPLIT_STAGES), j / SPLIT_STAGES & 1, 10000000ull, &never);
+          }
+          break;
+        }
+        const uint32_t full = bar_s(FULL + stage), s = base + stage * OSTAGE;
+        mbar_expect_tx(full, OSTAGE);
+        const int k0 = kb * 64;
+        const int zp = t.b + (segs == 3 && seg == 1 ? g.batch : 0);
+        const int zq = t.b + (segs == 3 && seg == 0 ? g.batch : 0);
+        tma_load_3d(s, &g.p, k0, m0, zp, full, pol);
+        if constexpr (Q_MN) {
+          tma_load_3d(s + OPERAND, &g.q, n0, k0, zq, full, pol);
+          tma_load_3d(s + OPERAND + OPERAND / 2, &g.q, n0 + 64, k0, zq, full, pol);
+        } else {
+          tma_load_3d(s + OPERAND, &g.q, k0, n0, zq, full, pol);
+        }
+        if (++kb == g.kblocks) { kb = 0; ++seg; }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = kb0; ok && i < kb1; ++i) {
+        const int n = i - kb0, stage = n % SPLIT_STAGES;
+        ok = mbar_wait(bar_s(FULL + stage), n / SPLIT_STAGES & 1, lim, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sp = base + stage * OSTAGE, sq = sp + OPERAND;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t pd = sdesc_sw128(sp + k * 32, 16, 1024);
+          const uint64_t qd =
+              Q_MN ? sdesc_sw128(sq + k * 2048, 8192, 1024) : sdesc_sw128(sq + k * 32, 16, 1024);
+          tc_mma_bf16(tmem, pd, qd, IDESC, n > 0 || k > 0);
+        }
+        tc_commit(bar_s(EMPTY + stage));
+      }
+      tc_commit(bar_s(DONE));
+      if (!ok) {
+        failed();
+        volatile int never = 0;  // what was issued ends before TMEM is freed
+        mbar_wait(bar_s(DONE), 0, 10000000ull, &never);
+      }
+    }
+  }
+  __syncwarp();
+  // the sums to shared memory, over the ring (every load has been read when the MMAs are done)
+  bool ok = mbar_wait(bar_s(DONE), 0, lim + 20000000ull, abort_flag) && !*abort_flag;
+  if (!ok && lane == 0) failed();
+  tc_fence_after();
+  if (warp >= 2 && ok && kb1 > kb0) {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      uint32_t a[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 64 + c, a);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        st_shared_v4(sum_part(base, q * 32 + lane, (half * 64 + c) / 4 + j), a[4 * j],
+                     a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  // my rows
+  const int R = 128 / S, busy = (kb_all + per - 1) / per;  // CTAs that had k-blocks
+  const int first_row = m0 + rank * R;
+  const size_t mn = static_cast<size_t>(g.M) * g.N, term = mn * g.batch;
+  const bool mirror = KIND == ORTHO_SYM && t.tm != t.tn;
+  const bool across = mirror || (KIND == ORTHO_LAST && g.transposed);
+  const bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && g.terms == 2);
+  const bool two_in = KIND != ORTHO_SYM || g.terms == 2;
+  const int pitch = R + 4;  // of the rows turned to columns, in floats
+  float* turned = reinterpret_cast<float*>(base_g + 65536);
+  if (warp >= 2) {
+    // half a warp a row: 16 lanes of eight columns
+    const int c8 = (lane & 15) * 8, col = n0 + c8;
+    for (int i = (warp - 2) * 2 + (lane >> 4); i < R; i += 16) {
+      const int row = first_row + i, r = rank * R + i;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      float4 x[8], y[8];  // (all on their way at once)
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < busy) {
+          const uint32_t from = mapa_shared(base, static_cast<uint32_t>(s));
+          x[s] = ld_cluster_f4(sum_part(from, r, c8 / 4));
+          y[s] = ld_cluster_f4(sum_part(from, r, c8 / 4 + 1));
+        }
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < busy) {
+          f[0] += x[s].x, f[1] += x[s].y, f[2] += x[s].z, f[3] += x[s].w;
+          f[4] += y[s].x, f[5] += y[s].y, f[6] += y[s].z, f[7] += y[s].w;
+        }
+      const bool in_d = row < g.M && col < g.N;
+      const size_t at = t.b * mn + static_cast<size_t>(row) * g.N + col;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= g.beta;
+      if (in_d && g.alpha != 0.f) {
+        const __half* x = static_cast<const __half*>(g.in_ptr) + at;
+        for (int z = two_in ? 1 : 0; z >= 0; --z) {
+          const uint4 h = ld_global_v4(x + z * term);
+          const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = unpack_half2(w[j]);
+            f[2 * j] += g.alpha * y.x;
+            f[2 * j + 1] += g.alpha * y.y;
+          }
+        }
+      }
+      if (across) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) turned[(c8 + j) * pitch + i] = f[j];
+      }
+      if (in_d && ok) {
+        if constexpr (KIND == ORTHO_LAST) {
+          if (!g.transposed) store_out(g, at, f);
+        } else {
+          store_terms(g, at, term, two_terms, f);
+        }
+      }
+    }
+  }
+  if (across) {  // (the same in all of the CTA's threads)
+    __syncthreads();
+    for (int i = threadIdx.x; i < 128 * (R / 8); i += OTHREADS) {
+      const int c = i / (R / 8), r8 = i % (R / 8) * 8;
+      if (!ok || n0 + c >= g.N || first_row + r8 >= g.M) continue;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = turned[c * pitch + r8 + j];
+      const size_t at = t.b * mn + static_cast<size_t>(n0 + c) * g.M + first_row + r8;
+      if constexpr (KIND == ORTHO_LAST) store_out(g, at, f);
+      else store_terms(g, at, term, two_terms, f);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // my sums have been read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, 128);
+  }
+}
+
+template <int KIND>
+cudaError_t launch_split(const OrthoGemm& g, int share, cudaStream_t stream) {
+  auto kern = k_ortho_split<KIND>;
+  static std::atomic<unsigned long long> done{0};  // devices that have the attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(done.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SPLIT_SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done.fetch_or(1ull << dev);
+  }
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = ortho_config(share, g.units * share, stream, attr);
+  cfg.dynamicSmemBytes = SPLIT_SMEM;
+  return cudaLaunchKernelEx(&cfg, kern, g);
+}
+
+template <int CG, int KIND>
+cudaError_t prepare() {
+  auto kern = k_ortho_gemm<CG, KIND>;
+  static std::atomic<unsigned long long> done{0};  // devices that have the attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load() >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, OSMEM);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+  return e;
+}
+
+template <int CG, int KIND>
 int clusters() {
-  if (prepare<CG, Q_MN>() != cudaSuccess) return 0;
   int dev = 0, sms = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   static std::atomic<int> cache[64];
@@ -418,18 +802,20 @@ int clusters() {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = ortho_config(CG, sms / CG * CG, nullptr, attr);
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_ortho_gemm<CG, Q_MN>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k_ortho_gemm<CG, KIND>, &cfg) != cudaSuccess) return 0;
   if (dev < 64) cache[dev].store(n);
   return n;
 }
 
-template <int CG, bool Q_MN>
+template <int CG, int KIND>
 cudaError_t launch_of(const OrthoGemm& g, cudaStream_t stream) {
-  const int n = clusters<CG, Q_MN>();
+  const cudaError_t e = prepare<CG, KIND>();
+  if (e != cudaSuccess) return e;
+  const int n = clusters<CG, KIND>();
   if (n <= 0) return cudaErrorUnknown;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = ortho_config(CG, CG * (g.units < n ? g.units : n), stream, attr);
-  return cudaLaunchKernelEx(&cfg, k_ortho_gemm<CG, Q_MN>, g);
+  return cudaLaunchKernelEx(&cfg, k_ortho_gemm<CG, KIND>, g);
 }
 
 // ------------------------------------------------------------- norm and scale
@@ -565,19 +951,20 @@ cudaLaunchConfig_t plain_config(dim3 grid, int threads, cudaStream_t stream,
 
 }  // namespace
 
-int ortho_clusters(int cg, bool q_mn) {
-  if (cg == 2) return q_mn ? clusters<2, true>() : clusters<2, false>();
-  return q_mn ? clusters<1, true>() : clusters<1, false>();
+cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, OrthoKind kind, cudaStream_t stream) {
+  switch (kind) {
+    case ORTHO_SYM: return cg == 2 ? launch_of<2, ORTHO_SYM>(g, stream) : launch_of<1, ORTHO_SYM>(g, stream);
+    case ORTHO_STEP: return cg == 2 ? launch_of<2, ORTHO_STEP>(g, stream) : launch_of<1, ORTHO_STEP>(g, stream);
+    default: return cg == 2 ? launch_of<2, ORTHO_LAST>(g, stream) : launch_of<1, ORTHO_LAST>(g, stream);
+  }
 }
 
-cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, bool q_mn, cudaStream_t stream) {
-  cudaError_t e;
-  if (cg == 2) {
-    if ((e = q_mn ? prepare<2, true>() : prepare<2, false>()) != cudaSuccess) return e;
-    return q_mn ? launch_of<2, true>(g, stream) : launch_of<2, false>(g, stream);
+cudaError_t launch_ortho_split(const OrthoGemm& g, int share, OrthoKind kind, cudaStream_t stream) {
+  switch (kind) {
+    case ORTHO_SYM: return launch_split<ORTHO_SYM>(g, share, stream);
+    case ORTHO_STEP: return launch_split<ORTHO_STEP>(g, share, stream);
+    default: return launch_split<ORTHO_LAST>(g, share, stream);
   }
-  if ((e = q_mn ? prepare<1, true>() : prepare<1, false>()) != cudaSuccess) return e;
-  return q_mn ? launch_of<1, true>(g, stream) : launch_of<1, false>(g, stream);
 }
 
 cudaError_t launch_ortho_norm(const void* G, bool bf16, long long size, int batch, float* part,

@@ -3,11 +3,16 @@
 // logits' gradient.
 //
 // G lanes take a token, each V of its logits (E <= G V) in registers; a warp holds 32 / G
-// tokens.  The choice is top_k rounds of a largest value over the lanes: the values as
-// integers of the same order, of equals the lowest expert.  What a row needs of the others
-// (counts, the probabilities' sums) stays in registers and shared memory until the block's
-// tokens are done, goes out as one partial sum a block, and a second kernel adds the blocks
-// in their order.
+// tokens.  Values compare as integers of the same order, of equals the lowest expert first.
+// Instructions bound these kernels, most of them the choice:
+//   G < 32   top_k rounds of a largest value over the lanes
+//   G = 32   the top_k-th largest of the lanes' own largest values bounds the choice from
+//            below; what reaches it (top_k values and a few more) goes to shared memory, and
+//            each of those counts how many are before it.  (More than 32 of them, from equal
+//            values: the rounds.)
+// What a row needs of the others (counts, the probabilities' sums) stays in registers and
+// shared memory until the block's tokens are done, goes out as one partial sum a block, and a
+// second kernel adds the blocks in their order.
 #include <cuda_bf16.h>
 
 #include "gemm_params.h"
@@ -22,11 +27,11 @@ constexpr int ROUTER_THREADS = 256;
 constexpr int FINISH_CTAS = 8;  // one cluster
 constexpr uint32_t KEY_NEG_INF = 0x007fffffu;
 
-// A float as an unsigned integer of the same order: -0 is 0, a NaN above all.
+// A float as an unsigned integer of the same order: -0 is 0, a NaN above all.  (Adding zero
+// makes -0 zero, and any NaN the canonical one, 0x7fffffff.)
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t b = __float_as_uint(f + 0.f);
-  if (f != f) return 0xffffffffu;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
@@ -38,13 +43,20 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The largest of the group's, a NaN if there is one.  (As every collective here: all groups of
+// a warp call it together, routed or not.)
 template <int G>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+__device__ __forceinline__ float group_max(float v) {
   if constexpr (G == 32) {
-    return __reduce_max_sync(0xffffffffu, v);
+    return key_value(__reduce_max_sync(0xffffffffu, order_key(v)));
   } else {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = G / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
   }
 }
@@ -108,13 +120,14 @@ __device__ __forceinline__ float balance_coef(int E, int top_k, int c, int N) {
 }
 
 // The sum of the block's threads (in a fixed order), in thread 0.
+template <int THREADS>
 __device__ __forceinline__ float block_sum(float v) {
-  __shared__ float warps_s[ROUTER_THREADS / 32];
+  __shared__ float warps_s[THREADS / 32];
   v = group_sum<32>(v);
   if (threadIdx.x % 32 == 0) warps_s[threadIdx.x / 32] = v;
   __syncthreads();
   v = 0.f;
-  for (int i = 0; i < ROUTER_THREADS / 32; ++i) v += warps_s[i];
+  for (int i = 0; i < THREADS / 32; ++i) v += warps_s[i];
   return v;
 }
 
@@ -127,20 +140,113 @@ struct FwdOut {
   int* status;
 };
 
-template <typename L, int G, int V, bool SUMS>
-__global__ void __launch_bounds__(ROUTER_THREADS)
+// The top_k largest of the group's keys, largest first, by rounds: into sel_id and sel_x.
+// Returns the largest.
+template <class R, int G, int V>
+__device__ __forceinline__ uint32_t choose_by_rounds(uint32_t (&key)[V], int lane, int k,
+                                                     int* sel_id, float* sel_x) {
+  uint32_t top = 0;
+  for (int j = 0; j < k; ++j) {
+    uint32_t bk = 0;
+    int be = 0;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) {
+      const bool better = key[v] >= bk;
+      bk = better ? key[v] : bk;
+      be = better ? R::at(lane, v) : be;
+    }
+    if constexpr (G == 32) {
+      const uint32_t most = __reduce_max_sync(0xffffffffu, bk);
+      be = __reduce_min_sync(0xffffffffu, bk == most ? be : 0x7fffffff);
+      bk = most;
+    } else {
+#pragma unroll
+      for (int s = G / 2; s > 0; s >>= 1) {
+        const uint32_t ok = __shfl_xor_sync(0xffffffffu, bk, s);
+        const int oe = __shfl_xor_sync(0xffffffffu, be, s);
+        const bool better = ok > bk || (ok == bk && oe < be);
+        bk = better ? ok : bk;
+        be = better ? oe : be;
+      }
+    }
+    if (j == 0) top = bk;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = R::at(lane, v) == be ? 0u : key[v];
+    if (lane == 0) {
+      sel_id[j] = bk > KEY_NEG_INF ? be : -1;
+      sel_x[j] = key_value(bk);
+    }
+  }
+  return top;
+}
+
+// The same for a whole warp and top_k <= 32 by a bound from below; `some` holds 32 pairs.
+// (All lanes come here together.)
+template <class R, int V>
+__device__ __forceinline__ uint32_t choose_by_bound(uint32_t (&key)[V], int lane, int k,
+                                                    int* sel_id, float* sel_x, uint2* some) {
+  uint32_t most = key[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) most = max(most, key[v]);
+  uint32_t left = most, bound = 0, top = 0;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {  // (equal ones leave together: the bound only gets lower)
+    bound = __reduce_max_sync(0xffffffffu, left);
+    if (j == 0) top = bound;
+    left = left == bound ? 0u : left;
+  }
+  bound = max(bound, KEY_NEG_INF + 1);  // -inf is never chosen
+  uint32_t mine_in = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) mine_in |= key[v] >= bound ? 1u << v : 0u;
+  int n = __popc(mine_in);  // then: those up to this lane's
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int below = __shfl_up_sync(0xffffffffu, n, o);
+    n += lane >= o ? below : 0;
+  }
+  int at = n - __popc(mine_in);
+  n = __shfl_sync(0xffffffffu, n, 31);
+  if (n > 32) return choose_by_rounds<R, 32, V>(key, lane, k, sel_id, sel_x);
+  if (mine_in) {  // (few lanes, one or two values each)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (mine_in >> v & 1u) some[at++] = make_uint2(key[v], R::at(lane, v));
+  }
+  __syncwarp();
+  const uint2 mine = some[lane < n ? lane : 0];
+  int before = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const uint2 o = some[i];
+    before += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+  }
+  if (lane < n && before < k) {
+    sel_id[before] = static_cast<int>(mine.y);
+    sel_x[before] = key_value(mine.x);
+  }
+  if (lane >= n && lane < k) {
+    sel_id[lane] = -1;
+    sel_x[lane] = 0.f;
+  }
+  return top;
+}
+
+template <typename L, int G, int V, bool SUMS, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     k_router_fwd(const RouterArgs a, const FwdOut o, const bool vec) {
-  constexpr int NG = ROUTER_THREADS / G;
+  constexpr int NG = THREADS / G;
   using R = Row<L, G, V>;
-  extern __shared__ float router_smem[];
+  extern __shared__ __align__(16) float router_smem[];
   const int tid = threadIdx.x, lane = tid % G, g = tid / G, E = a.E, k = a.top_k;
   int* sel_id = reinterpret_cast<int*>(router_smem) + g * k;
   float* sel_x = router_smem + (NG + g) * k;
   int* cnt = reinterpret_cast<int*>(router_smem + 2 * NG * k);  // [E], SUMS
   float* psum = router_smem + 2 * NG * k + E;                   // [NG, E], SUMS
   __shared__ int routed_s[NG];
+  __shared__ uint2 some_s[G == 32 ? NG : 1][32];
   if constexpr (SUMS) {
-    for (int e = tid; e < E; e += ROUTER_THREADS) cnt[e] = 0;
+    for (int e = tid; e < E; e += THREADS) cnt[e] = 0;
     __syncthreads();
   }
   pdl_wait();
@@ -166,70 +272,54 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);
-    uint32_t top = 0;
-    for (int j = 0; j < k; ++j) {
-      uint32_t bk = 0;
-      int be = 0;
-#pragma unroll
-      for (int v = V - 1; v >= 0; --v) {
-        const bool better = key[v] >= bk;
-        bk = better ? key[v] : bk;
-        be = better ? R::at(lane, v) : be;
-      }
-      if constexpr (G == 32) {
-        const uint32_t most = __reduce_max_sync(0xffffffffu, bk);
-        be = __reduce_min_sync(0xffffffffu, bk == most ? be : 0x7fffffff);
-        bk = most;
-      } else {
-#pragma unroll
-        for (int s = G / 2; s > 0; s >>= 1) {
-          const uint32_t ok = __shfl_xor_sync(0xffffffffu, bk, s);
-          const int oe = __shfl_xor_sync(0xffffffffu, be, s);
-          const bool better = ok > bk || (ok == bk && oe < be);
-          bk = better ? ok : bk;
-          be = better ? oe : be;
-        }
-      }
-      if (j == 0) top = bk;
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = R::at(lane, v) == be ? 0u : key[v];
-      if (lane == 0) {
-        sel_id[j] = bk > KEY_NEG_INF ? be : -1;
-        sel_x[j] = key_value(bk);
-      }
-    }
+    uint32_t top;
+    if (G == 32 && k <= 32)
+      top = choose_by_bound<R, V>(key, lane, k, sel_id, sel_x, some_s[G == 32 ? g : 0]);
+    else
+      top = choose_by_rounds<R, G, V>(key, lane, k, sel_id, sel_x);
     __syncwarp();
     const bool routed = top > KEY_NEG_INF;
-    const float m = key_value(top);
-    float total = 0.f;  // of the softmax, or of the chosen
+    // (what is not routed gets no weights, and no NaN from -inf - -inf)
+    const float m = routed ? key_value(top) : 0.f;
+    float inv = 0.f;  // of the softmax's sum, or of the chosen ones'
     if (SUMS || !a.renorm) {
+      float total = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        x[v] = routed ? expf(x[v] - m) : 0.f;
+        x[v] = __expf(x[v] - m);
         total += x[v];
       }
       total = group_sum<G>(total);
+      inv = routed ? 1.f / total : 0.f;
       if constexpr (SUMS) {
-        const float inv = routed ? 1.f / total : 0.f;
+        if (routed) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += x[v] * inv;
-        n_routed += routed;
+          for (int v = 0; v < V; ++v) acc[v] += x[v] * inv;
+          ++n_routed;
+        }
       }
     }
-    if (a.renorm) {
-      total = 0.f;
-      for (int j = lane; j < k; j += G)
-        if (sel_id[j] >= 0) total += expf(sel_x[j] - m);
-      total = group_sum<G>(total);
-    }
-    if (in) {
-      for (int j = lane; j < k; j += G) {
-        const int id = sel_id[j];
-        const float w = id >= 0 ? expf(sel_x[j] - m) / total : 0.f;
-        o.ids[t * k + j] = id;
-        if (a.w_bf16) static_cast<__nv_bfloat16*>(o.weights)[t * k + j] = __float2bfloat16_rn(w);
-        else static_cast<float*>(o.weights)[t * k + j] = w;
-        if (SUMS && id >= 0) atomicAdd(&cnt[id], 1);
+    auto put = [&](int j, int id, float w) {
+      o.ids[t * k + j] = id;
+      if (a.w_bf16) static_cast<__nv_bfloat16*>(o.weights)[t * k + j] = __float2bfloat16_rn(w);
+      else static_cast<float*>(o.weights)[t * k + j] = w;
+      if (SUMS && id >= 0) atomicAdd(&cnt[id], 1);
+    };
+    if (k <= G) {  // a slot a lane
+      const int id = lane < k ? sel_id[lane] : -1;
+      float w = id >= 0 ? __expf(sel_x[lane] - m) : 0.f;
+      w *= a.renorm ? 1.f / group_sum<G>(w) : inv;
+      if (in && lane < k) put(lane, id, id >= 0 ? w : 0.f);
+    } else {
+      if (a.renorm) {
+        float total = 0.f;
+        for (int j = lane; j < k; j += G)
+          if (sel_id[j] >= 0) total += __expf(sel_x[j] - m);
+        inv = 1.f / group_sum<G>(total);
+      }
+      if (in) {
+        for (int j = lane; j < k; j += G)
+          put(j, sel_id[j], sel_id[j] >= 0 ? __expf(sel_x[j] - m) * inv : 0.f);
       }
     }
     __syncwarp();
@@ -245,7 +335,7 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
     int n = 0;
     for (int i = 0; i < NG; ++i) n += routed_s[i];
     float loss = 0.f;
-    for (int e = tid; e < E; e += ROUTER_THREADS) {
+    for (int e = tid; e < E; e += THREADS) {
       float s = 0.f;
       for (int i = 0; i < NG; ++i) s += psum[i * E + e];
       if (gridDim.x > 1) {
@@ -262,7 +352,7 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
     if (gridDim.x > 1) {
       if (tid == 0) o.parts.n[blockIdx.x] = n;
     } else if (o.balance) {
-      loss = block_sum(loss);
+      loss = block_sum<THREADS>(loss);
       if (tid == 0) o.balance[0] = loss;
     }
   }
@@ -319,11 +409,12 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
     if (balance) balance[1 + e] = coef;
     loss = coef * p_s[lane];
   }
-  loss = block_sum(loss);
+  loss = block_sum<ROUTER_THREADS>(loss);
   if (tid == 0) {
     const uint32_t to = mapa_shared(smem_u32(&loss_s[rank]), 0);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(loss) : "memory");
   }
+  __syncwarp();
   cluster_sync();
   if (rank == 0 && tid == 0 && balance) {
     loss = 0.f;
@@ -339,13 +430,16 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
                  const float* __restrict__ dloss, void* dlogits, const bool vec, const bool vec_d) {
   constexpr int NG = ROUTER_THREADS / G;
   using R = Row<L, G, V>;
-  extern __shared__ float router_smem[];
+  extern __shared__ __align__(16) float router_smem[];
   const int tid = threadIdx.x, lane = tid % G, g = tid / G, E = a.E, k = a.top_k;
-  // what the weights' gradient adds at the chosen experts; zero between tokens
-  float* extra = router_smem + g * (G * V);
+  // the token's exponentials by expert, then its gradients
+  float* buf = router_smem + g * (G * V);
+  auto put_row = [&](const float (&f)[V]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) extra[v * G + lane] = 0.f;
-  __syncwarp();
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(buf + R::at(lane, i)) =
+          make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  };
   pdl_wait();
   pdl_launch_dependents();
   float coef[V];
@@ -357,83 +451,125 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
       coef[v] = dloss && e < E ? balance[1 + e] * d : 0.f;
     }
   }
+  const bool slots = dweights != nullptr;
+  const bool one = k <= G;  // a slot a lane
   auto dw_at = [&](long long i) {
     return a.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(dweights)[i])
                     : static_cast<const float*>(dweights)[i];
   };
-  for (long long base = static_cast<long long>(blockIdx.x) * NG; base < a.T;
-       base += static_cast<long long>(gridDim.x) * NG) {
-    const long long t = base + g;
-    const bool in = t < a.T;
-    const bool take = in && (!a.mask || a.mask[t]);
-    const L* row = static_cast<const L*>(a.logits) + t * a.ldl;
-    float x[V];
+  // a token's operands are loaded while the one before it is worked on
+  float next_x[V], next_dw = 0.f;
+  int next_id = -1;
+  auto fetch = [&](long long t) {
+    const bool take = t < a.T && (!a.mask || a.mask[t]);
+    next_id = -1;
     if (take) {
-      R::load(row, lane, E, vec, x);
+      R::load(static_cast<const L*>(a.logits) + t * a.ldl, lane, E, vec, next_x);
+      if (slots && one && lane < k) {
+        next_id = ids[t * k + lane];
+        next_dw = dw_at(t * k + lane);
+      }
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = -INFINITY;
+      for (int v = 0; v < V; ++v) next_x[v] = -INFINITY;
     }
-    uint32_t top = 0;
+  };
+  const long long step = static_cast<long long>(gridDim.x) * NG;
+  fetch(static_cast<long long>(blockIdx.x) * NG + g);
+  for (long long base = static_cast<long long>(blockIdx.x) * NG; base < a.T; base += step) {
+    const long long t = base + g;
+    float x[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) top = max(top, order_key(x[v]));
-    top = group_max<G>(top);
-    const bool routed = top > KEY_NEG_INF;
-    const float m = key_value(top);
-    const bool slots = dweights != nullptr;
-    if (slots) {
-      float total = 1.f, dot = 0.f;
-      if (a.renorm) {
-        float s = 0.f, d = 0.f;
-        for (int j = lane; j < k; j += G) {
-          const int id = routed ? ids[t * k + j] : -1;
-          if (id < 0 || id >= E) continue;
-          const float e = expf(static_cast<float>(row[id]) - m);
-          s += e;
-          d += e * dw_at(t * k + j);
-        }
-        total = group_sum<G>(s);
-        dot = group_sum<G>(d) / total;
-      }
-      for (int j = lane; j < k; j += G) {
-        const int id = routed ? ids[t * k + j] : -1;
-        if (id < 0 || id >= E) continue;
-        float v = dw_at(t * k + j);
-        if (a.renorm) v = expf(static_cast<float>(row[id]) - m) / total * (v - dot);
-        atomicAdd(&extra[id], v);  // (a caller's ids may name an expert twice)
-      }
-      __syncwarp();
-    }
+    for (int v = 0; v < V; ++v) x[v] = next_x[v];
+    int id = next_id;
+    const float dw = next_dw;
+    fetch(t + step);
+    float m = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = max_nan(m, x[v]);
+    m = group_max<G>(m);
+    const bool routed = m != -INFINITY;
+    if (!routed) m = 0.f;
+    if (!routed || id >= E) id = -1;
     float total = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      x[v] = routed ? expf(x[v] - m) : 0.f;
+      x[v] = __expf(x[v] - m);
       total += x[v];
     }
+    put_row(x);
+    __syncwarp();
     total = group_sum<G>(total);
     const float inv = routed ? 1.f / total : 0.f;
-    float dot = 0.f;
-    float more[V];
+    // what the weights' gradient adds at the chosen experts: w (dw - <w, dw>), or p dw of
+    // p (dw - <p, dw>)
+    float add = 0.f, dot = 0.f, w_inv = 1.f, w_dot = 0.f;
+    if (slots && one) {
+      const float e = id >= 0 ? buf[id] : 0.f;
+      if (a.renorm) {
+        const float s = group_sum<G>(e);
+        const float d = group_sum<G>(id >= 0 ? e * dw : 0.f);
+        if (id >= 0) add = e / s * (dw - d / s);
+      } else if (id >= 0) {
+        add = dot = e * inv * dw;
+      }
+    } else if (slots) {
+      float s = 0.f, d = 0.f;
+      for (int j = lane; j < k; j += G) {
+        const int i = routed && t < a.T ? ids[t * k + j] : -1;
+        if (i < 0 || i >= E) continue;
+        s += buf[i];
+        d += buf[i] * dw_at(t * k + j);
+      }
+      if (a.renorm) {
+        w_inv = 1.f / group_sum<G>(s);
+        w_dot = group_sum<G>(d) * w_inv;
+      } else {
+        w_inv = inv;
+        dot = d * inv;
+      }
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      more[v] = slots ? extra[R::at(lane, v)] : 0.f;
       x[v] *= inv;
-      dot += x[v] * (a.renorm ? coef[v] : coef[v] + more[v]);
+      dot += x[v] * coef[v];
     }
     dot = group_sum<G>(dot);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      x[v] = a.renorm ? x[v] * (coef[v] - dot) + more[v] : x[v] * (coef[v] + more[v] - dot);
-    // (the row was read by all of its lanes: dlogits may lie over logits)
-    __syncwarp();
-    if (in) R::store(static_cast<L*>(dlogits) + t * a.ldd, lane, E, vec_d, x);
+    for (int v = 0; v < V; ++v) x[v] *= coef[v] - dot;
     if (slots) {
-      for (int j = lane; j < k; j += G) {
-        const int id = routed ? ids[t * k + j] : -1;
-        if (id >= 0 && id < E) extra[id] = 0.f;
+      if (one) {
+        __syncwarp();  // (the exponentials have been read)
+        put_row(x);
+        __syncwarp();
+        if (id >= 0) atomicAdd(&buf[id], add);  // (a caller's ids may name an expert twice)
+      } else {  // a slot's exponential goes as its gradient comes: one at a time
+        float keep[ROUTER_MAX_TOP_K / 8];
+#pragma unroll
+        for (int i = 0; i < ROUTER_MAX_TOP_K / 8; ++i) {
+          const int j = lane + i * G;
+          const int e = routed && t < a.T && j < k ? ids[t * k + j] : -1;
+          keep[i] = e >= 0 && e < E ? buf[e] * w_inv * (dw_at(t * k + j) - w_dot) : 0.f;
+        }
+        __syncwarp();
+        put_row(x);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < ROUTER_MAX_TOP_K / 8; ++i) {
+          const int j = lane + i * G;
+          const int e = routed && t < a.T && j < k ? ids[t * k + j] : -1;
+          if (e >= 0 && e < E) atomicAdd(&buf[e], keep[i]);
+        }
       }
       __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(buf + R::at(lane, i));
+        x[i] = q.x, x[i + 1] = q.y, x[i + 2] = q.z, x[i + 3] = q.w;
+      }
     }
+    if (t < a.T) R::store(static_cast<L*>(dlogits) + t * a.ldd, lane, E, vec_d, x);
+    __syncwarp();  // (before the next token's values go over these)
   }
 }
 
@@ -469,37 +605,56 @@ cudaLaunchConfig_t config(int blocks, size_t smem, cudaStream_t stream,
   return cfg;
 }
 
-int tokens_blocks(int T, int E) {  // one round of a block's groups each
-  const int ng = ROUTER_THREADS / lanes_of(E);
-  return (T - 1) / ng + 1;
+int rounds(int T, int groups) { return (T - 1) / groups + 1; }
+
+// Threads of the forward's blocks where the sums are wanted: as many as the registers allow (64
+// a thread up to 256 experts), since every block is a partial sum, and 256 where those would be
+// too few blocks for the GPU.
+int sum_threads(int T, int E) {
+  return E <= 256 && rounds(T, 1024 / lanes_of(E)) > 152 ? 1024 : ROUTER_THREADS;
 }
 
 }  // namespace
 
 // (a function of the sizes alone: the workspace is, too)
 int router_blocks(int T, int E) {
-  const int all = tokens_blocks(T, E);
-  if (all <= 8) return 1;
-  return all < 2 * 152 ? all : 2 * 152;
+  const int threads = sum_threads(T, E);
+  const int all = rounds(T, threads / lanes_of(E));
+  if (all <= 8) return 1;  // one block, no second kernel
+  const int most = threads == 1024 ? 152 : 2 * 152;
+  return all < most ? all : most;
 }
 
 cudaError_t launch_router_fwd(const RouterArgs& a, int* ids, void* weights, int* counts,
                               float* balance, const RouterParts& parts, int* status,
                               cudaStream_t stream) {
   const bool sums = parts.n != nullptr;
-  const int all = tokens_blocks(a.T, a.E);
+  const int threads = sums ? sum_threads(a.T, a.E) : ROUTER_THREADS;
+  const int all = rounds(a.T, ROUTER_THREADS / lanes_of(a.E));
   const int blocks = sums ? router_blocks(a.T, a.E) : all < 8 * 152 ? all : 8 * 152;
   const FwdOut o{ids, weights, counts, balance, parts, status};
   const bool vec = rows_aligned(a.logits, a.ldl, a.l_bf16);
   return by_experts(a.E, [&](auto g, auto v) {
-    constexpr int G = decltype(g)::value, V = decltype(v)::value, NG = ROUTER_THREADS / G;
-    const size_t smem = (2ull * NG * a.top_k + (sums ? (NG + 1ull) * a.E : 0)) * 4;
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    const int ng = threads / G;
+    const size_t smem = (2ull * ng * a.top_k + (sums ? (ng + 1ull) * a.E : 0)) * 4;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(blocks, smem, stream, attr);
-    auto go = [&](auto kern) { return cudaLaunchKernelEx(&cfg, kern, a, o, vec); };
-    if (a.l_bf16) return sums ? go(k_router_fwd<__nv_bfloat16, G, V, true>)
-                              : go(k_router_fwd<__nv_bfloat16, G, V, false>);
-    return sums ? go(k_router_fwd<float, G, V, true>) : go(k_router_fwd<float, G, V, false>);
+    cfg.blockDim.x = static_cast<unsigned>(threads);
+    auto go = [&](auto kern) {
+      // (at most 97 KB: 128 groups of 64 experts, and 64 slots a group)
+      const cudaError_t e = kern.allow_smem(128 * 1024);
+      if (e != cudaSuccess) return e;
+      return cudaLaunchKernelEx(&cfg, kern.kernel, a, o, vec);
+    };
+    if (!sums) return a.l_bf16 ? go(KernelOf<k_router_fwd<__nv_bfloat16, G, V, false, ROUTER_THREADS>>{})
+                               : go(KernelOf<k_router_fwd<float, G, V, false, ROUTER_THREADS>>{});
+    if constexpr (V <= 8) {
+      if (threads == 1024) return a.l_bf16 ? go(KernelOf<k_router_fwd<__nv_bfloat16, G, V, true, 1024>>{})
+                                           : go(KernelOf<k_router_fwd<float, G, V, true, 1024>>{});
+    }
+    return a.l_bf16 ? go(KernelOf<k_router_fwd<__nv_bfloat16, G, V, true, ROUTER_THREADS>>{})
+                    : go(KernelOf<k_router_fwd<float, G, V, true, ROUTER_THREADS>>{});
   });
 }
 
@@ -519,7 +674,7 @@ cudaError_t launch_router_finish(int T, int E, int top_k, const RouterParts& par
 cudaError_t launch_router_bwd(const RouterArgs& a, const int* ids, const float* balance,
                               const void* dweights, const float* dloss, void* dlogits,
                               cudaStream_t stream) {
-  const int all = tokens_blocks(a.T, a.E);
+  const int all = rounds(a.T, ROUTER_THREADS / lanes_of(a.E));
   const int blocks = all < 8 * 152 ? all : 8 * 152;
   const bool vec = rows_aligned(a.logits, a.ldl, a.l_bf16);
   const bool vec_d = rows_aligned(dlogits, a.ldd, a.l_bf16);

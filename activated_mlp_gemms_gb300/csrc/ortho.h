@@ -14,29 +14,34 @@ namespace mlpk {
 // for m, n up to 16384.
 constexpr float ORTHO_X = 16384.f, ORTHO_A = 2048.f;
 
-constexpr int ORTHO_PARTS = 64;  // partial sums of a matrix's norm
+constexpr int ORTHO_PARTS = 256;  // partial sums of a matrix's norm
 
 // One product D = alpha in + beta P Q of a stack, P [M, K] K-major, Q [N, K] K-major or
-// [K, N]; the three products hi lo + lo hi + hi hi with `terms` 2.  in and D in one or two
-// fp16 terms.
+// [K, N]; the three products hi lo + lo hi + hi hi with `terms` 2.
+enum OrthoKind : int {
+  ORTHO_SYM = 0,   // D symmetric (P is Q), in as many terms as the operands: the tiles on and
+                   // below the diagonal, and their mirror images
+  ORTHO_STEP = 1,  // Q is [K, N]; in and D in two terms
+  ORTHO_LAST = 2   // the same, D the result: bf16 or fp32, as it is or transposed
+};
 struct OrthoGemm {
-  CUtensorMap p, q;  // depth batch x terms
+  CUtensorMap p, q;   // depth terms x batch
+  CUtensorMap in, d;  // in 32 x 32 boxes
+  const void* in_ptr;  // the same, for the kernel of few units
+  void* d_ptr;
   int M, N, kblocks, terms, batch;
-  int sym;           // D is symmetric: the tiles below the diagonal, and their mirror images
   int tiles_m, tiles_n, units;
-  float alpha, beta;
-  const void *in_hi, *in_lo;  // null: none
-  void *hi, *lo;              // fp16 terms out (null: none)
-  void* out;                  // or the result: bf16 or fp32, as it is or transposed
+  float alpha, beta;  // alpha 0: no `in`
   int out_bf16, transposed;
   int* status;
   unsigned long long timeout_ns;
   int debug_flags;
 };
 // cg 2: CTA pairs, 256 x 256 tiles; 1: single CTAs, 128 x 128 tiles.
-cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, bool q_mn, cudaStream_t stream);
-// Clusters of an instance that are resident together (0 on error).
-int ortho_clusters(int cg, bool q_mn);
+cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, OrthoKind kind, cudaStream_t stream);
+// 128 x 128 tiles whose k-blocks are shared by clusters of `share` CTAs (2, 4 or 8, at most
+// half of the k-blocks).
+cudaError_t launch_ortho_split(const OrthoGemm& g, int share, OrthoKind kind, cudaStream_t stream);
 
 // part [batch, ORTHO_PARTS] = sums of squares of G's matrices; clears *status.
 cudaError_t launch_ortho_norm(const void* G, bool bf16, long long size, int batch, float* part,

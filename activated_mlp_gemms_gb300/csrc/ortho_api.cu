@@ -54,17 +54,39 @@ Layout layout(const mlp_ortho_t* p) {
   return w;
 }
 
-// Products run on CTA pairs (256 x 256 tiles) where their tiles fill the pairs at least as
-// well as the singles' 128 x 128.
-int pick(const OrthoGemm& g) {
+// Products run on CTA pairs (256 x 256 tiles) unless the singles' 128 x 128 fill the GPU that
+// much better: a wave of 76 pairs takes 1.3 times one of 152 singles, for twice the work
+// (their tiles load half as much for a flop).  Measured (pairs / singles, us): 4096 x 14336 step
+// 299 / 460, 16 x 1408 x 2048 step 118 / 155, gram 64 / 74; 2048 x 4864 step 37 / 49, gram 33 /
+// 29; 1024 x 1024 16 / 12.
+int pick(const OrthoGemm& g, bool sym) {
   const int pol = g_tile_policy.load();
   if (pol == 1 || pol == 2) return pol;
   auto waves = [&](int tile, int slots) {
     const long long tm = (g.M + tile - 1) / tile, tn = (g.N + tile - 1) / tile;
-    const long long units = (g.sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
+    const long long units = (sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
     return (units + slots - 1) / slots;
   };
-  return 2 * waves(256, 76) <= waves(128, 152) + 1 ? 2 : 1;
+  return 1.3 * waves(256, 76) <= waves(128, 152) ? 2 : 1;
+}
+
+// CTAs that share the k-blocks of a 128 x 128 tile where the tiles are few (1: none do).  The
+// least estimate in us: 0.27 a k-block of one CTA (its loads' latency over the stages in
+// flight), and 3.2 + 0.3 a CTA for the cluster's launch, its two barriers and the exchange of
+// the sums.  Measured (1 / 2 / 4 / 8 CTAs, us of an X X^T with 5 of event time): 64 x 1024 10 / 12 /
+// 12 / 12, 64 x 2048 16 / 14 / 12 / 13, 64 x 4096 24 / 18 / 14 / 14, 256 x 14336 65 / 43 / 27 / 20,
+// 1024 x 2048 16 / 18 / 16 / 35 (more CTAs than SMs).
+int pick_share(int units, int kblocks) {
+  int best = 1;
+  double least = 0.27 * kblocks;
+  for (int share = 2; share <= 8 && units * share <= 144; share *= 2) {
+    const double us = 0.27 * ((kblocks + share - 1) / share) + 3.2 + 0.3 * share;
+    if (us < least) {
+      least = us;
+      best = share;
+    }
+  }
+  return best;
 }
 
 struct Products {
@@ -74,15 +96,19 @@ struct Products {
   int* status;
   bool ok = true;
 
-  // A stack [terms x batch, rows, cols] in boxes {64, box}.
-  CUtensorMap map(const void* ptr, int rows, int cols, int terms, int box) {
+  // A stack [depth, rows, cols] of fp16 (or bf16, fp32) matrices in boxes {c, r}.
+  CUtensorMap map(const void* ptr, int depth, int rows, int cols, int c, int r,
+                  CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, int f32 = 0) {
     CUtensorMap m;
-    if (!make_map(&m, ptr, cols, rows, cols, 64, box, 0, CU_TENSOR_MAP_SWIZZLE_128B,
-                  (uint64_t)terms * p->batch, (uint64_t)rows * cols))
+    if (!make_map(&m, ptr, cols, rows, cols, c, r, f32, swz, depth, (uint64_t)rows * cols))
       ok = false;
     return m;
   }
-  OrthoGemm gemm(int M, int N, int K, bool sym) {
+  // ... in the boxes of the epilogue
+  CUtensorMap boxes(const void* ptr, int depth, int rows, int cols) {
+    return map(ptr, depth, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
+  OrthoGemm gemm(int M, int N, int K) {
     OrthoGemm g;
     std::memset(&g, 0, sizeof(g));
     g.M = M;
@@ -90,19 +116,24 @@ struct Products {
     g.kblocks = (K + 63) / 64;
     g.terms = w.terms;
     g.batch = p->batch;
-    g.sym = sym;
     g.status = status;
     g.timeout_ns = wait_limit_ns();
     g.debug_flags = g_debug_flags.load();
     return g;
   }
-  int run(OrthoGemm& g, bool q_mn, int tag) {
+  int run(OrthoGemm& g, OrthoKind kind, int tag) {
     if (!ok) return MLP_ERR_CUDA;
-    const int cg = pick(g), tile = 128 * cg;
+    const bool sym = kind == ORTHO_SYM;
+    const int cg = pick(g, sym), tile = 128 * cg;
     g.tiles_m = (g.M + tile - 1) / tile;
     g.tiles_n = (g.N + tile - 1) / tile;
-    g.units = (g.sym ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n) * g.batch;
-    return traced(tag, stream, [&] { return launch_ortho_gemm(g, cg, q_mn, stream); });
+    g.units = (sym ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n) * g.batch;
+    const int share =
+        cg == 1 && g_tile_policy.load() != 1 ? pick_share(g.units, g.kblocks * (g.terms == 2 ? 3 : 1)) : 1;
+    return traced(tag, stream, [&] {
+      return share > 1 ? launch_ortho_split(g, share, kind, stream)
+                       : launch_ortho_gemm(g, cg, kind, stream);
+    });
   }
 };
 
@@ -128,7 +159,6 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
   char* at = static_cast<char*>(ws);
   float* part = reinterpret_cast<float*>(at + w.part);
   const bool bf16 = p->type == MLP_ORTHO_BF16;
-  const size_t mn = (size_t)p->batch * w.m * w.n, mm = (size_t)p->batch * w.m * w.m;
   MLP_TRY(traced(MLP_KERNEL_ORTHO_SCALE, s, [&] {
     return launch_ortho_norm(G, bf16, (long long)w.m * w.n, p->batch, part,
                              static_cast<int*>(ws), s);
@@ -137,50 +167,51 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
     return launch_ortho_scale(G, bf16, p->rows, p->cols, p->batch, part, p->eps, at + w.x[0], s);
   }));
   Products run{p, w, s, static_cast<int*>(ws)};
-  auto second = [&](void* first, size_t n) {  // of two terms
-    return w.terms == 2 ? static_cast<char*>(first) + 2 * n : nullptr;
-  };
+  const int m = w.m, n = w.n, xs = 2 * p->batch, as = w.terms * p->batch;  // depths
   char *A = at + w.a, *P = at + w.poly;
   for (int i = 0; i < p->steps; ++i) {
     char *X = at + w.x[i & 1], *next = at + w.x[(i & 1) ^ 1];
     {
-      OrthoGemm g = run.gemm(w.m, w.m, w.n, true);
-      g.p = g.q = run.map(X, w.m, w.n, 2, 128);
+      OrthoGemm g = run.gemm(m, m, n);
+      g.p = g.q = run.map(X, xs, m, n, 64, 128);
+      g.in = g.d = run.boxes(A, as, m, m);
+      g.d_ptr = A;
       g.beta = ORTHO_A / (ORTHO_X * ORTHO_X);
-      g.hi = A;
-      g.lo = second(A, mm);
-      MLP_TRY(run.run(g, false, MLP_KERNEL_ORTHO_GRAM));
+      MLP_TRY(run.run(g, ORTHO_SYM, MLP_KERNEL_ORTHO_GRAM));
     }
     {
-      OrthoGemm g = run.gemm(w.m, w.m, w.m, true);
-      g.p = g.q = run.map(A, w.m, w.m, w.terms, 128);
+      OrthoGemm g = run.gemm(m, m, m);
+      g.p = g.q = run.map(A, as, m, m, 64, 128);
+      g.in = run.boxes(A, as, m, m);
+      g.d = run.boxes(P, as, m, m);
+      g.in_ptr = A;
+      g.d_ptr = P;
       g.alpha = p->coeff[1];
       g.beta = p->coeff[2] / ORTHO_A;
-      g.in_hi = A;
-      g.in_lo = second(A, mm);
-      g.hi = P;
-      g.lo = second(P, mm);
-      MLP_TRY(run.run(g, false, MLP_KERNEL_ORTHO_POLY));
+      MLP_TRY(run.run(g, ORTHO_SYM, MLP_KERNEL_ORTHO_POLY));
     }
-    OrthoGemm g = run.gemm(w.m, w.n, w.m, false);
-    g.p = run.map(P, w.m, w.m, w.terms, 128);
-    g.q = run.map(X, w.m, w.n, 2, 64);
+    OrthoGemm g = run.gemm(m, n, m);
+    g.p = run.map(P, as, m, m, 64, 128);
+    g.q = run.map(X, xs, m, n, 64, 64);
+    g.in = run.boxes(X, xs, m, n);
+    g.in_ptr = X;
+    g.d_ptr = i + 1 < p->steps ? next : out;
     g.alpha = p->coeff[0];
     g.beta = 1.f / ORTHO_A;
-    g.in_hi = X;
-    g.in_lo = X + 2 * mn;
     if (i + 1 < p->steps) {
-      g.hi = next;
-      g.lo = next + 2 * mn;
-    } else {
-      const float scale = p->scale / ORTHO_X;
-      g.alpha *= scale;
-      g.beta *= scale;
-      g.out = out;
-      g.out_bf16 = p->out_type == MLP_ORTHO_BF16;
-      g.transposed = p->rows > p->cols;
+      g.d = run.boxes(next, xs, m, n);
+      MLP_TRY(run.run(g, ORTHO_STEP, MLP_KERNEL_ORTHO_STEP));
+      continue;
     }
-    MLP_TRY(run.run(g, true, MLP_KERNEL_ORTHO_STEP));
+    const float scale = p->scale / ORTHO_X;
+    g.alpha *= scale;
+    g.beta *= scale;
+    g.out_bf16 = p->out_type == MLP_ORTHO_BF16;
+    g.transposed = p->rows > p->cols;
+    g.d = g.out_bf16 ? run.boxes(out, p->batch, p->rows, p->cols)
+                     : run.map(out, p->batch, p->rows, p->cols, 32, 32,
+                               CU_TENSOR_MAP_SWIZZLE_128B, 1);
+    MLP_TRY(run.run(g, ORTHO_LAST, MLP_KERNEL_ORTHO_STEP));
   }
   return MLP_OK;
 }

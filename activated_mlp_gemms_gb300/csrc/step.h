@@ -5,7 +5,25 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mlpk {
+
+// A kernel as a type, so that what is set up once for it has a place.
+template <auto KERNEL>
+struct KernelOf {
+  static constexpr auto kernel = KERNEL;
+  // Allows `most` bytes of dynamic shared memory, once a device.
+  static cudaError_t allow_smem(int most) {
+    static std::atomic<unsigned long long> done{0};  // devices
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+    return e;
+  }
+};
 
 // ------------------------------------------------------------------ router
 constexpr int ROUTER_MAX_EXPERTS = 1024;
@@ -48,7 +66,7 @@ cudaError_t launch_layernorm_fwd(const NormArgs& a, const void* x, const void* r
                                  float* mean, float* rstd, cudaStream_t stream);
 // Blocks of the backward where dweight or dbias is wanted: each leaves its rows' sums in
 // part fp32 [blocks, 2, H] (dweight's, dbias's), which the second kernel adds up.
-int layernorm_blocks(int M, int H);
+int layernorm_blocks(int M, int H, bool bf16);
 cudaError_t launch_layernorm_bwd(const NormArgs& a, const void* dy, const void* h,
                                  const void* weight, const float* mean, const float* rstd,
                                  const void* dh, void* dx, float* part, int* status,

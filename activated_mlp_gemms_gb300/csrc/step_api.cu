@@ -86,7 +86,7 @@ NormArgs norm_args(const mlp_layernorm_t* p) {
                   p->ldr ? p->ldr : p->H};
 }
 size_t norm_total(const mlp_layernorm_t* p) {
-  return CTRL_BYTES + round256((size_t)layernorm_blocks(p->M, p->H) * 2 * p->H * 4);
+  return CTRL_BYTES + round256((size_t)layernorm_blocks(p->M, p->H, p->type == MLP_NORM_BF16) * 2 * p->H * 4);
 }
 
 }  // namespace
@@ -198,7 +198,7 @@ int mlp_layernorm_bwd(const mlp_layernorm_t* p, const void* dy, const void* h, c
   }));
   if (!sums) return MLP_OK;
   return traced(MLP_KERNEL_LAYERNORM_SUMS, s, [&] {
-    return launch_layernorm_sums(p->H, layernorm_blocks(p->M, p->H), part, dweight, dbias,
+    return launch_layernorm_sums(p->H, layernorm_blocks(p->M, p->H, p->type == MLP_NORM_BF16), part, dweight, dbias,
                                  p->weight_type == MLP_NORM_BF16, fuse_grad_accum == 1, s);
   });
 }

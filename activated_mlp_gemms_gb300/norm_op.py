@@ -53,9 +53,9 @@ def mlp_layernorm_workspace_size(p: LayerNorm) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def _ws_size(M, H):
-    """The workspace size: a function of the sizes alone."""
-    return mlp_layernorm_workspace_size(LayerNorm(M, H, 0.0, 0, 0, 0, 0))
+def _ws_size(M, H, kind):
+    """The workspace size: a function of the sizes and the rows' type."""
+    return mlp_layernorm_workspace_size(LayerNorm(M, H, 0.0, kind, 0, 0, 0))
 
 
 def alloc_layernorm_workspace(p: LayerNorm, device=None) -> torch.Tensor:
@@ -103,7 +103,7 @@ def mlp_layernorm_bwd(p: LayerNorm, dy, h, weight, mean, rstd, dh=None, dx=None,
     if dweight is None and dbias is None:
         ws, at = None, (None, 0)
     else:
-        ws = _ws(ws, lambda: _ws_size(p.M, p.H), dy.device, stream)
+        ws = _ws(ws, lambda: _ws_size(p.M, p.H, p.type), dy.device, stream)
         at = (ws.data_ptr(), ws.numel())
     rc = lib().mlp_layernorm_bwd(ctypes.byref(p), *args, int(bool(fuse_grad_accum)), *at,
                                  _stream(stream))

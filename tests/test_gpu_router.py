@@ -128,7 +128,8 @@ def make(T, E, dtype, seed=0, scale=1.5):
 @pytest.mark.parametrize("dtype,wt", [(F32, F32), (BF, F32), (F32, BF), (BF, BF)])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (3, 5, 5), (31, 8, 2), (33, 60, 4),
                                    (257, 100, 7), (700, 128, 1), (65, 200, 8), (2049, 256, 8),
-                                   (300, 500, 3), (40, 1024, 64), (5000, 64, 64), (20011, 16, 2)])
+                                   (300, 500, 3), (40, 1024, 64), (5000, 64, 64), (20011, 16, 2),
+                                   (40003, 64, 64), (20001, 128, 33), (9001, 250, 64)])
 def test_sizes(T, E, k, dtype, wt, renorm):
     check(make(T, E, dtype, T + E), k, renorm, wt=wt)
 
@@ -308,7 +309,7 @@ def test_autograd_forms():
     assert counts is None and loss is None and not w.requires_grad
     e = torch.zeros(0, 16, device="cuda", requires_grad=True)
     ids, w, counts, loss = m.router_func(e, 3)
-    assert ids.shape == (0, 3) and float(loss) == 0 and not counts.any()
+    assert ids.shape == (0, 3) and float(loss.detach()) == 0 and not counts.any()
     assert torch.autograd.grad(loss + w.sum(), [e])[0].shape == (0, 16)
     with pytest.raises(ValueError):
         m.router_func(x.half(), 2)
@@ -351,3 +352,12 @@ def test_replayed_graph_and_streams():
     side.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_a_nan_of_either_sign():
+    for bits in (0x7fc00000, 0xffc00000 - (1 << 32), 0x7f800001):
+        x = make(5, 256, F32, 71)
+        x[2, 77] = torch.tensor(bits, dtype=torch.int32, device="cuda").view(F32)
+        ids, w, *_ = run(x, 4)
+        assert ids[2, 0] == 77 and w[2].isnan().all()
+        assert w[[0, 1, 3, 4]].isfinite().all()

@@ -183,7 +183,7 @@ def test_ortho_pointer_refusals(L):
     assert ortho(L, q, G=FAKE, out=FAKE) == -1  # the result over an update of another type
     assert L.mlp_orthogonalize(None, FAKE, FAKE, FAKE, BIG, None) == -1
     # X twice in two fp16 terms, A and the polynomial in one or two
-    assert m.mlp_ortho_workspace_size(p) == 1024 + 256 + 2 * 64 * 128 * 4 + 2 * 64 * 64 * 2
+    assert m.mlp_ortho_workspace_size(p) == 1024 + 1024 + 2 * 64 * 128 * 4 + 2 * 64 * 64 * 2
     assert m.mlp_ortho_workspace_size(q) == m.mlp_ortho_workspace_size(p) + 2 * 64 * 64 * 2
     with pytest.raises(ValueError):
         m.ortho(64, 64, dtype=torch.float16)
