@@ -18,60 +18,42 @@ namespace mlpk {
 
 namespace {
 
-// Eight values of a row, 16 bytes (bf16) or 32 (fp32), and as four pairs of fp32 for the
-// two-wide instructions.
+// A piece of a row: 16 bytes, and as pairs of fp32 for the two-wide instructions.
 template <typename T>
-struct Vec8;
-template <>
-struct Vec8<__nv_bfloat16> {
+struct Piece {
+  static constexpr int C = 16 / sizeof(T);  // its columns
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = ld_global_v4(p); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { st_global_v4(p, a); }
-  __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
+  __device__ __forceinline__ void store(T* p) const { st_global_v4(p, a); }
+  __device__ __forceinline__ void get(uint64_t (&f)[C / 2]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    if constexpr (C == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack_bf16x2(w[i]);
-      f[i] = f2_pack(v.x, v.y);
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack_bf16x2(w[i]);
+        f[i] = f2_pack(v.x, v.y);
+      }
+    } else {
+      f[0] = f2_pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      f[1] = f2_pack(__uint_as_float(w[2]), __uint_as_float(w[3]));
     }
   }
-  __device__ __forceinline__ void set(const uint64_t (&f)[4]) {
+  __device__ __forceinline__ void set(const uint64_t (&f)[C / 2]) {
     uint32_t w[4];
+    if constexpr (C == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = f2_unpack(f[i]);
-      w[i] = pack_bf16x2(v.x, v.y);
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = f2_unpack(f[i]);
+        w[i] = pack_bf16x2(v.x, v.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 v = f2_unpack(f[i]);
+        w[2 * i] = __float_as_uint(v.x);
+        w[2 * i + 1] = __float_as_uint(v.y);
+      }
     }
     a = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec8<float> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = ld_global_v4(p);
-    b = ld_global_v4(p + 4);
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    st_global_v4(p, a);
-    st_global_v4(p + 4, b);
-  }
-  __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
-    f[0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y));
-    f[1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
-    f[2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y));
-    f[3] = f2_pack(__uint_as_float(b.z), __uint_as_float(b.w));
-  }
-  __device__ __forceinline__ void set(const uint64_t (&f)[4]) {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = f2_unpack(f[i]);
-      w[2 * i] = __float_as_uint(v.x);
-      w[2 * i + 1] = __float_as_uint(v.y);
-    }
-    a = make_uint4(w[0], w[1], w[2], w[3]);
-    b = make_uint4(w[4], w[5], w[6], w[7]);
   }
 };
 __device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
@@ -92,43 +74,56 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
 }
 
-// A thread's vectors of the next rows in shared memory: some rows of ARRAYS arrays of NV
-// vectors, in planes of 16 bytes a thread.
-template <typename T, int NV, int ARRAYS>
+// A thread's pieces of the next rows in shared memory: some rows of ARRAYS arrays of NP pieces,
+// in planes of 16 bytes a thread.
+template <typename T, int NP, int ARRAYS>
 struct Ahead {
-  static constexpr int PLANES = sizeof(T) == 2 ? 1 : 2;  // 16-byte parts of a vector
   uint32_t mine;   // this thread's first plane
   uint32_t plane;  // bytes of a plane
   __device__ __forceinline__ uint32_t at(int stage, int array, int i) const {
-    return mine + plane * static_cast<uint32_t>(((stage * ARRAYS + array) * NV + i) * PLANES);
+    return mine + plane * static_cast<uint32_t>((stage * ARRAYS + array) * NP + i);
   }
   __device__ __forceinline__ void copy(int stage, int array, int i, const T* src) const {
-    const uint32_t to = at(stage, array, i);
-    cp_async16(to, src);
-    if constexpr (PLANES == 2) cp_async16(to + plane, src + 4);
+    cp_async16(at(stage, array, i), src);
   }
-  __device__ __forceinline__ void get(int stage, int array, int i, uint64_t (&f)[4]) const {
-    Vec8<T> q;
+  __device__ __forceinline__ void get(int stage, int array, int i,
+                                      uint64_t (&f)[Piece<T>::C / 2]) const {
+    Piece<T> q;
     q.a = ld_shared_v4(at(stage, array, i));
-    if constexpr (PLANES == 2) q.b = ld_shared_v4(at(stage, array, i) + plane);
     q.get(f);
   }
 };
 
-// Eight of the weight's or bias's values (null: `none`).
+// 2 N of the weight's or bias's values (null: `none`).
+template <int N>
 __device__ __forceinline__ void load_param(const void* p, bool bf16, int at, float none,
-                                           uint64_t (&f)[4]) {
+                                           uint64_t (&f)[N]) {
   if (!p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = f2_both(none);
+    for (int i = 0; i < N; ++i) f[i] = f2_both(none);
   } else if (bf16) {
-    Vec8<__nv_bfloat16> v;
-    v.load(static_cast<const __nv_bfloat16*>(p) + at);
-    v.get(f);
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(p) + at;
+    uint32_t w[N];
+    if constexpr (N == 4) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(from));
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(from));
+      w[0] = q.x, w[1] = q.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 v = unpack_bf16x2(w[i]);
+      f[i] = f2_pack(v.x, v.y);
+    }
   } else {
-    Vec8<float> v;
-    v.load(static_cast<const float*>(p) + at);
-    v.get(f);
+    const float4* w = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float4 v = __ldg(w + i);
+      f[2 * i] = f2_pack(v.x, v.y);
+      f[2 * i + 1] = f2_pack(v.z, v.w);
+    }
   }
 }
 
@@ -138,62 +133,78 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-constexpr int MAX_THREADS = 512;
-
-// Sums over the row's threads (a warp's, or the block's), in every one of them.  `turn`
-// alternates between calls, so that one barrier a call is enough.
-template <bool WARP>
+// Sums of N values over the row's threads (a warp's, or the block's), in every one of them.
+// `turn` alternates between calls, so that one barrier a call is enough.
+template <bool WARP, int N>
 struct RowSum {
-  float2 (*s)[MAX_THREADS / 32];
+  float (*s)[N][32];  // [2]: a warp's sums each
+  int warps;          // the block's; groups of 8, 16 or 32 lanes add them up
   int turn = 0;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if constexpr (WARP) {
-      return make_float2(a, b);
-    } else {
-      if (threadIdx.x % 32 == 0) s[turn][threadIdx.x / 32] = make_float2(a, b);
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if constexpr (!WARP) {
+      const int lane = threadIdx.x % 32, group = warps > 16 ? 32 : warps > 8 ? 16 : 8;
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[turn][i][threadIdx.x / 32] = v[i];
+      }
       __syncthreads();
-      float2 t = make_float2(0.f, 0.f);
-      const int warps = blockDim.x / 32;
-#pragma unroll 8
-      for (int i = 0; i < warps; ++i) {
-        const float2 v = s[turn][i];
-        t.x += v.x;
-        t.y += v.y;
+      const int from = lane & (group - 1);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = from < warps ? s[turn][i][from] : 0.f;
+      if (group == 32) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+      }
+      if (group >= 16) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
       }
       turn ^= 1;
-      return t;
     }
   }
 };
 
-// How a row is laid out.  Up to 1024 values it is a warp's, and a block of 256 threads has eight
-// rows at a time; wider ones are a block's, of just the warps that they need.
-struct Shape {
-  int nv, threads, depth;
-  bool warp;
+// How a row is laid out.  Up to four pieces a lane it is a warp's, and a block of 256 threads has
+// eight rows at a time; a wider one is a block's, of just the warps that it needs: NP pieces a
+// thread, so that a thread holds 8, 16 or (the widest) 32 columns.
+template <typename T, bool WARP, int NP>
+struct Layout {
+  static constexpr int COLUMNS = NP * Piece<T>::C;  // a thread
+  // (85 registers a thread of 768 are enough for 8 columns)
+  static constexpr int THREADS = WARP || NP == 1 ? 256 : NP == 2 && COLUMNS == 8 ? 768 : 512;
+  // rows under way: three, fewer where three arrays of the widest would not fit (216 KB)
+  static constexpr int DEPTH = THREADS * NP <= 1536 ? 3 : THREADS * NP <= 2048 ? 2 : 1;
+  static constexpr bool KEEP = COLUMNS <= 16;  // weights stay in registers
 };
-// Rows under way: three, fewer where three arrays of the widest would not fit (192 KB).
-template <typename T, bool WARP, int NV>
-constexpr int DEPTH = (WARP ? 256 : NV == 1 ? 256 : 512) * NV * sizeof(T) * 8 <= 16384   ? 3
-                      : (WARP ? 256 : NV == 1 ? 256 : 512) * NV * sizeof(T) * 8 <= 32768 ? 2
-                                                                                         : 1;
+constexpr int NORM_SMEM = 216 * 1024;
 
-template <typename T, bool WARP, int NV, bool RESIDUAL>
-__global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS, WARP || NV == 1 ? 3 : 1)
+template <typename T, bool WARP, int NP, bool RESIDUAL>
+__global__ void __launch_bounds__(Layout<T, WARP, NP>::THREADS,
+                                  Layout<T, WARP, NP>::THREADS == 256 ? 3 : 1)
     k_layernorm_fwd(const NormArgs a, const T* x, const T* residual, const void* __restrict__ weight,
                     const void* __restrict__ bias, T* y, T* h, float* __restrict__ mean,
                     float* __restrict__ rstd) {
-  constexpr int D = DEPTH<T, WARP, NV>;
+  using Lay = Layout<T, WARP, NP>;
+  constexpr int D = Lay::DEPTH, C = Piece<T>::C, N2 = C / 2;  // columns, pairs of a piece
+  constexpr bool KEEP = Lay::KEEP;
   extern __shared__ uint4 norm_smem[];
-  __shared__ float2 sums_s[2][MAX_THREADS / 32];
-  RowSum<WARP> sum{sums_s};
+  __shared__ float sums_s[2][1][32];
+  RowSum<WARP, 1> sum{sums_s, static_cast<int>(blockDim.x) / 32};
   const int G = WARP ? 32 : static_cast<int>(blockDim.x);  // threads of a row
   constexpr int AT_ONCE = WARP ? 8 : 1;                    // rows of a block at a time
-  const Ahead<T, NV, RESIDUAL ? 2 : 1> ahead{smem_u32(norm_smem) + threadIdx.x * 16,
+  const Ahead<T, NP, RESIDUAL ? 2 : 1> ahead{smem_u32(norm_smem) + threadIdx.x * 16,
                                              blockDim.x * 16};
-  const int first = threadIdx.x % G * 8;  // this thread's first column; the next G * 8 on
+  const int first = threadIdx.x % G * C;  // this thread's first column; its next piece G C on
+  bool has[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) has[i] = first + i * G * C < a.H;
   const int step = gridDim.x * AT_ONCE;
   const int row0 = blockIdx.x * AT_ONCE + threadIdx.x / G;
   pdl_wait();
@@ -206,10 +217,10 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS, WARP || N
   auto fetch = [&](int stage) {
     if (to_fetch > 0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (first + i * G * 8 < a.H) {
-          ahead.copy(stage, 0, i, next_x + i * G * 8);
-          if constexpr (RESIDUAL) ahead.copy(stage, 1, i, next_r + i * G * 8);
+      for (int i = 0; i < NP; ++i)
+        if (has[i]) {
+          ahead.copy(stage, 0, i, next_x + i * G * C);
+          if constexpr (RESIDUAL) ahead.copy(stage, 1, i, next_r + i * G * C);
         }
       --to_fetch;
       next_x += x_step;
@@ -220,14 +231,13 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS, WARP || N
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(d);
   // the thread's weights and biases, kept from row to row where the registers are there
-  constexpr bool KEEP = NV <= 2;
-  uint64_t kept_w[KEEP ? NV : 1][4], kept_b[KEEP ? NV : 1][4];
+  uint64_t kept_w[KEEP ? NP : 1][N2], kept_b[KEEP ? NP : 1][N2];
   if constexpr (KEEP) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (first + i * G * 8 < a.H) {
-        load_param(weight, a.w_bf16, first + i * G * 8, 1.f, kept_w[i]);
-        load_param(bias, a.w_bf16, first + i * G * 8, 0.f, kept_b[i]);
+    for (int i = 0; i < NP; ++i)
+      if (has[i]) {
+        load_param(weight, a.w_bf16, first + i * G * C, 1.f, kept_w[i]);
+        load_param(bias, a.w_bf16, first + i * G * C, 0.f, kept_b[i]);
       }
   }
   const float inv = 1.f / static_cast<float>(a.H);
@@ -235,98 +245,107 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS, WARP || N
   int stage = 0, row = row0;
   for (; left > 0; --left, row += step, at += static_cast<size_t>(step) * a.H) {
     cp_async_wait<D>();
-    uint64_t v[NV][4];
+    uint64_t v[NP][N2];
     uint64_t s = 0;  // two zeros
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (first + i * G * 8 < a.H) {
+    for (int i = 0; i < NP; ++i)
+      if (has[i]) {
         ahead.get(stage, 0, i, v[i]);
         if constexpr (RESIDUAL) {
-          uint64_t r[4];
+          uint64_t r[N2];
           ahead.get(stage, 1, i, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = f2_add(v[i][j], r[j]);
+          for (int j = 0; j < N2; ++j) v[i][j] = f2_add(v[i][j], r[j]);
         }
         if (h) {
-          Vec8<T> q;
+          Piece<T> q;
           q.set(v[i]);
-          q.store(h + at + i * G * 8);
+          q.store(h + at + i * G * C);
         }
         if constexpr (RESIDUAL) {  // what is normed is the sum as it is stored
-          Vec8<T> q;
+          Piece<T> q;
           q.set(v[i]);
           q.get(v[i]);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s = f2_add(s, v[i][j]);
+        for (int j = 0; j < N2; ++j) s = f2_add(s, v[i][j]);
       }
     fetch(stage);
     stage = stage + 1 == D ? 0 : stage + 1;
-    const float mu = sum(f2_sum(s), 0.f).x * inv;
+    float total[1] = {f2_sum(s)};
+    sum(total);
+    const float mu = total[0] * inv;
     const uint64_t minus = f2_both(-mu);
     s = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (first + i * G * 8 < a.H) {
+    for (int i = 0; i < NP; ++i)
+      if (has[i]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < N2; ++j) {
           v[i][j] = f2_add(v[i][j], minus);
           s = f2_fma(v[i][j], v[i][j], s);
         }
       }
-    const float rs = 1.f / sqrtf(sum(f2_sum(s), 0.f).x * inv + a.eps);
+    total[0] = f2_sum(s);
+    sum(total);
+    const float rs = 1.f / sqrtf(total[0] * inv + a.eps);
     if (first == 0) {
       if (mean) mean[row] = mu;
       if (rstd) rstd[row] = rs;
     }
     const uint64_t rs2 = f2_both(rs);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (first + i * G * 8 < a.H) {
+    for (int i = 0; i < NP; ++i)
+      if (has[i]) {
         if constexpr (KEEP) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < N2; ++j)
             v[i][j] = f2_fma(f2_mul(v[i][j], rs2), kept_w[i][j], kept_b[i][j]);
         } else {
-          uint64_t w[4], b[4];
-          load_param(weight, a.w_bf16, first + i * G * 8, 1.f, w);
-          load_param(bias, a.w_bf16, first + i * G * 8, 0.f, b);
+          uint64_t w[N2], b[N2];
+          load_param(weight, a.w_bf16, first + i * G * C, 1.f, w);
+          load_param(bias, a.w_bf16, first + i * G * C, 0.f, b);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = f2_fma(f2_mul(v[i][j], rs2), w[j], b[j]);
+          for (int j = 0; j < N2; ++j) v[i][j] = f2_fma(f2_mul(v[i][j], rs2), w[j], b[j]);
         }
-        Vec8<T> q;
+        Piece<T> q;
         q.set(v[i]);
-        q.store(y + at + i * G * 8);
+        q.store(y + at + i * G * C);
       }
   }
 }
 
-template <typename T, bool WARP, int NV, bool SUMS, bool DH>
-__global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS)
+template <typename T, bool WARP, int NP, bool SUMS, bool DH>
+__global__ void __launch_bounds__(Layout<T, WARP, NP>::THREADS)
     k_layernorm_bwd(const NormArgs a, const T* dy, const T* __restrict__ h,
                     const void* __restrict__ weight, const float* __restrict__ mean,
                     const float* __restrict__ rstd, const T* dh, T* dx, float* __restrict__ part,
                     int* status) {
-  constexpr int D = DEPTH<T, WARP, NV>;
+  using Lay = Layout<T, WARP, NP>;
+  constexpr int D = Lay::DEPTH, C = Piece<T>::C, N2 = C / 2;  // columns, pairs of a piece
+  constexpr bool KEEP = Lay::KEEP;
   extern __shared__ uint4 norm_smem[];
-  __shared__ float2 sums_s[2][MAX_THREADS / 32];
-  RowSum<WARP> sum{sums_s};
+  __shared__ float sums_s[2][2][32];
+  RowSum<WARP, 2> sum{sums_s, static_cast<int>(blockDim.x) / 32};
   const int G = WARP ? 32 : static_cast<int>(blockDim.x);  // threads of a row
   constexpr int AT_ONCE = WARP ? 8 : 1;                    // rows of a block at a time
-  const Ahead<T, NV, DH ? 3 : 2> ahead{smem_u32(norm_smem) + threadIdx.x * 16, blockDim.x * 16};
+  const Ahead<T, NP, DH ? 3 : 2> ahead{smem_u32(norm_smem) + threadIdx.x * 16, blockDim.x * 16};
   const int lane = threadIdx.x % G;
-  const int first = lane * 8;  // this thread's first column; the next G * 8 on
+  const int first = lane * C;  // this thread's first column; its next piece G C on
+  bool has[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) has[i] = first + i * G * C < a.H;
   const int step = gridDim.x * AT_ONCE;
   const int row0 = blockIdx.x * AT_ONCE + threadIdx.x / G;
   pdl_wait();
   pdl_launch_dependents();
   if (SUMS && status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
-  uint64_t dw[SUMS ? NV : 1][4], db[SUMS ? NV : 1][4];
+  uint64_t dw[SUMS ? NP : 1][N2], db[SUMS ? NP : 1][N2];
   if constexpr (SUMS) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NP; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0;
+      for (int j = 0; j < N2; ++j) dw[i][j] = db[i][j] = 0;
   }
   size_t at = static_cast<size_t>(row0) * a.H + first;
   const size_t at_step = static_cast<size_t>(step) * a.H;
@@ -336,11 +355,11 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS)
   auto fetch = [&](int stage) {
     if (to_fetch > 0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (first + i * G * 8 < a.H) {
-          ahead.copy(stage, 0, i, dy + next + i * G * 8);
-          ahead.copy(stage, 1, i, h + next + i * G * 8);
-          if constexpr (DH) ahead.copy(stage, 2, i, dh + next + i * G * 8);
+      for (int i = 0; i < NP; ++i)
+        if (has[i]) {
+          ahead.copy(stage, 0, i, dy + next + i * G * C);
+          ahead.copy(stage, 1, i, h + next + i * G * C);
+          if constexpr (DH) ahead.copy(stage, 2, i, dh + next + i * G * C);
         }
       --to_fetch;
       next += at_step;
@@ -350,19 +369,18 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS)
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(d);
   // the thread's weights, kept from row to row where the registers are there
-  constexpr bool KEEP = NV <= 2;
-  uint64_t kept[KEEP ? NV : 1][4];
+  uint64_t kept[KEEP ? NP : 1][N2];
   if constexpr (KEEP) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (first + i * G * 8 < a.H) load_param(weight, a.w_bf16, first + i * G * 8, 1.f, kept[i]);
+    for (int i = 0; i < NP; ++i)
+      if (has[i]) load_param(weight, a.w_bf16, first + i * G * C, 1.f, kept[i]);
   }
-  auto weights = [&](int i, uint64_t (&w)[4]) {
+  auto weights = [&](int i, uint64_t (&w)[N2]) {
     if constexpr (KEEP) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = kept[i][j];
+      for (int j = 0; j < N2; ++j) w[j] = kept[i][j];
     } else {
-      load_param(weight, a.w_bf16, first + i * G * 8, 1.f, w);
+      load_param(weight, a.w_bf16, first + i * G * C, 1.f, w);
     }
   };
   const float inv = 1.f / static_cast<float>(a.H);
@@ -376,14 +394,14 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS)
     const uint64_t minus = f2_both(-mu), rs2 = f2_both(rs);
     uint64_t s1 = 0, s2 = 0;  // two zeros each
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (first + i * G * 8 < a.H) {
-        uint64_t d[4], x[4], w[4];
+    for (int i = 0; i < NP; ++i)
+      if (has[i]) {
+        uint64_t d[N2], x[N2], w[N2];
         ahead.get(stage, 0, i, d);
         ahead.get(stage, 1, i, x);
         weights(i, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < N2; ++j) {
           const uint64_t xh = f2_mul(f2_add(x[j], minus), rs2), g = f2_mul(d[j], w[j]);
           s1 = f2_add(s1, g);
           s2 = f2_fma(g, xh, s2);
@@ -394,29 +412,30 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS)
         }
       }
     if (dx) {
-      const float2 t = sum(f2_sum(s1), f2_sum(s2));
-      const uint64_t m1 = f2_both(-t.x * inv), m2 = f2_both(-t.y * inv);
+      float t[2] = {f2_sum(s1), f2_sum(s2)};
+      sum(t);
+      const uint64_t m1 = f2_both(-t[0] * inv), m2 = f2_both(-t[1] * inv);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (first + i * G * 8 < a.H) {
-          uint64_t d[4], x[4], w[4];
+      for (int i = 0; i < NP; ++i)
+        if (has[i]) {
+          uint64_t d[N2], x[N2], w[N2];
           ahead.get(stage, 0, i, d);
           ahead.get(stage, 1, i, x);
           weights(i, w);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < N2; ++j) {
             const uint64_t xh = f2_mul(f2_add(x[j], minus), rs2);
             d[j] = f2_mul(f2_fma(xh, m2, f2_fma(d[j], w[j], m1)), rs2);
           }
           if constexpr (DH) {
-            uint64_t e[4];
+            uint64_t e[N2];
             ahead.get(stage, 2, i, e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = f2_add(d[j], e[j]);
+            for (int j = 0; j < N2; ++j) d[j] = f2_add(d[j], e[j]);
           }
-          Vec8<T> q;
+          Piece<T> q;
           q.set(d);
-          q.store(dx + at + i * G * 8);
+          q.store(dx + at + i * G * C);
         }
     }
     fetch(stage);
@@ -428,36 +447,40 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : MAX_THREADS)
     float* out = part + static_cast<size_t>(blockIdx.x) * 2 * a.H;
     if constexpr (!WARP) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (first + i * G * 8 < a.H) {
-          Vec8<float> q;
-          q.set(dw[i]);
-          q.store(out + first + i * G * 8);
-          q.set(db[i]);
-          q.store(out + a.H + first + i * G * 8);
+      for (int i = 0; i < NP; ++i)
+        if (has[i]) {
+#pragma unroll
+          for (int j = 0; j < N2; ++j) {
+            float2* to = reinterpret_cast<float2*>(out + first + i * G * C) + j;
+            to[0] = f2_unpack(dw[i][j]);
+            to[a.H / 2] = f2_unpack(db[i][j]);
+          }
         }
     } else {  // the block's warps in their order
-      __shared__ float cols_s[2][32 * NV * 8];
+      __shared__ float2 cols_s[2][NP * N2][32];
       for (int w = 0; w < AT_ONCE; ++w) {
         if (threadIdx.x / 32 == w) {
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
+          for (int i = 0; i < NP; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 p = f2_unpack(dw[i][j]), q = f2_unpack(db[i][j]);
-              const int c = (i * 8 + 2 * j) * 32 + lane;
-              cols_s[0][c] = w ? cols_s[0][c] + p.x : p.x;
-              cols_s[0][c + 32] = w ? cols_s[0][c + 32] + p.y : p.y;
-              cols_s[1][c] = w ? cols_s[1][c] + q.x : q.x;
-              cols_s[1][c + 32] = w ? cols_s[1][c + 32] + q.y : q.y;
+            for (int j = 0; j < N2; ++j) {
+              float2 p = f2_unpack(dw[i][j]), q = f2_unpack(db[i][j]);
+              float2 &to_p = cols_s[0][i * N2 + j][lane], &to_q = cols_s[1][i * N2 + j][lane];
+              if (w) {
+                p.x += to_p.x, p.y += to_p.y;
+                q.x += to_q.x, q.y += to_q.y;
+              }
+              to_p = p;
+              to_q = q;
             }
         }
         __syncthreads();
       }
       for (int c = threadIdx.x; c < a.H; c += static_cast<int>(blockDim.x)) {
-        const int from = (c / 256 * 8 + c % 8) * 32 + c / 8 % 32;
-        out[c] = cols_s[0][from];
-        out[a.H + c] = cols_s[1][from];
+        const int i = c / (32 * C), l = c / C % 32, j = c % C;  // piece, lane, column of it
+        const float2 p = cols_s[0][i * N2 + j / 2][l], q = cols_s[1][i * N2 + j / 2][l];
+        out[c] = j % 2 ? p.y : p.x;
+        out[a.H + c] = j % 2 ? q.y : q.x;
       }
     }
   }
@@ -494,38 +517,41 @@ __global__ void __launch_bounds__(32 * SUM_ROWS)
   else static_cast<float*>(out)[mine] = t;
 }
 
-template <class F>
+template <typename T, class F>
 auto by_width(int H, F&& f) {
-  const int vecs = H / 8;
-#define MLP_NORM_SHAPE(WARP, NV) \
-  return f(std::integral_constant<bool, WARP>{}, std::integral_constant<int, NV>{})
-  if (vecs <= 32) MLP_NORM_SHAPE(true, 1);
-  if (vecs <= 64) MLP_NORM_SHAPE(true, 2);
-  if (vecs <= 128) MLP_NORM_SHAPE(true, 4);
-  if (vecs <= 256) MLP_NORM_SHAPE(false, 1);
-  if (vecs <= 1024) MLP_NORM_SHAPE(false, 2);
-  MLP_NORM_SHAPE(false, 4);
-#undef MLP_NORM_SHAPE
+  const int pieces = H / Piece<T>::C;
+#define MLP_NORM_LAYOUT(WARP, NP) return f(Layout<T, WARP, NP>{}, std::integral_constant<bool, WARP>{}, std::integral_constant<int, NP>{})
+  if (pieces <= 32) MLP_NORM_LAYOUT(true, 1);
+  if (pieces <= 64) MLP_NORM_LAYOUT(true, 2);
+  if (pieces <= 128) MLP_NORM_LAYOUT(true, 4);
+  if (pieces <= 256) MLP_NORM_LAYOUT(false, 1);
+  if (pieces <= 2 * Layout<T, false, 2>::THREADS) MLP_NORM_LAYOUT(false, 2);
+  if constexpr (sizeof(T) == 4) {
+    if (pieces > 2048) MLP_NORM_LAYOUT(false, 8);
+  }
+  MLP_NORM_LAYOUT(false, 4);
+#undef MLP_NORM_LAYOUT
 }
-Shape shape(int H, bool bf16) {
-  return by_width(H, [&](auto w, auto v) {
-    constexpr bool WARP = decltype(w)::value;
-    constexpr int NV = decltype(v)::value;
-    const int threads = WARP ? 256 : ((H / 8 + NV - 1) / NV + 31) / 32 * 32;
-    return Shape{NV, threads,
-                 bf16 ? DEPTH<__nv_bfloat16, WARP, NV> : DEPTH<float, WARP, NV>, WARP};
+struct Shape {
+  int rows, threads, columns;  // of a block; of a thread
+  size_t ahead;                // bytes of one array's rows under way in a block
+};
+template <typename T>
+Shape shape_of(int H) {
+  return by_width<T>(H, [&](auto lay, auto warp, auto np) {
+    constexpr int NP = decltype(np)::value;
+    const int threads =
+        decltype(warp)::value ? 256 : ((H / Piece<T>::C + NP - 1) / NP + 31) / 32 * 32;
+    return Shape{decltype(warp)::value ? 8 : 1, threads, decltype(lay)::COLUMNS,
+                 (size_t)decltype(lay)::DEPTH * threads * NP * 16};
   });
 }
-// Bytes of the rows under way in a block.
-size_t ahead_bytes(const Shape& p, int arrays, bool bf16) {
-  return (size_t)arrays * p.depth * p.threads * p.nv * (bf16 ? 16 : 32);
-}
-int block_rows(const Shape& p) { return p.warp ? 8 : 1; }
-// Blocks of an SM, by the shared memory that they take (a KB of each is the driver's, 8 KB the
-// columns' sums) and `most` threads, which the registers allow.
-int sm_blocks(const Shape& p, int arrays, bool bf16, int most) {
-  const int fit = static_cast<int>(228 * 1024 / (ahead_bytes(p, arrays, bf16) +
-                                                 (p.warp ? 9 * 1024 : 1280)));
+Shape shape(int H, bool bf16) { return bf16 ? shape_of<__nv_bfloat16>(H) : shape_of<float>(H); }
+// Blocks of an SM, by the shared memory that they take (a KB of each is the driver's; 8 KB the
+// columns' sums of a warp a row) and `most` threads, which the registers allow.
+int sm_blocks(const Shape& p, int arrays, int most) {
+  const int fit =
+      static_cast<int>(228 * 1024 / (arrays * p.ahead + (p.rows > 1 ? 10 * 1024 : 1536)));
   const int n = fit < most / p.threads ? fit : most / p.threads;
   return n < 1 ? 1 : n;
 }
@@ -543,22 +569,21 @@ cudaLaunchConfig_t config(dim3 blocks, int threads, cudaStream_t stream,
   return cfg;
 }
 
-constexpr int NORM_SMEM = 192 * 1024;  // the most that a row's depth takes
-
 template <typename T>
 cudaError_t fwd_of(const NormArgs& a, const void* x, const void* residual, const void* weight,
                    const void* bias, void* y, void* h, float* mean, float* rstd,
                    cudaStream_t stream) {
-  const Shape p = shape(a.H, a.bf16);
+  const Shape p = shape_of<T>(a.H);
   const int arrays = residual ? 2 : 1;
-  const int all = (a.M - 1) / block_rows(p) + 1;
-  const int most = 152 * sm_blocks(p, arrays, a.bf16, p.nv == 1 ? 768 : 640);
+  const int all = (a.M - 1) / p.rows + 1;
+  // (registers: up to 80 a thread for 8 columns, 102 for 16)
+  const int most = 152 * sm_blocks(p, arrays, p.columns <= 8 ? 768 : 640);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(dim3(all < most ? all : most), p.threads, stream, attr);
-  cfg.dynamicSmemBytes = ahead_bytes(p, arrays, a.bf16);
-  return by_width(a.H, [&](auto w, auto nv) {
-    constexpr bool WARP = decltype(w)::value;
-    constexpr int NV = decltype(nv)::value;
+  cfg.dynamicSmemBytes = arrays * p.ahead;
+  return by_width<T>(a.H, [&](auto, auto warp, auto np) {
+    constexpr bool WARP = decltype(warp)::value;
+    constexpr int NP = decltype(np)::value;
     auto go = [&](auto kern) {
       const cudaError_t e = kern.allow_smem(NORM_SMEM);
       if (e != cudaSuccess) return e;
@@ -566,8 +591,8 @@ cudaError_t fwd_of(const NormArgs& a, const void* x, const void* residual, const
                                 static_cast<const T*>(residual), weight, bias, static_cast<T*>(y),
                                 static_cast<T*>(h), mean, rstd);
     };
-    return residual ? go(KernelOf<k_layernorm_fwd<T, WARP, NV, true>>{})
-                    : go(KernelOf<k_layernorm_fwd<T, WARP, NV, false>>{});
+    return residual ? go(KernelOf<k_layernorm_fwd<T, WARP, NP, true>>{})
+                    : go(KernelOf<k_layernorm_fwd<T, WARP, NP, false>>{});
   });
 }
 
@@ -575,14 +600,14 @@ template <typename T>
 cudaError_t bwd_of(const NormArgs& a, const void* dy, const void* h, const void* weight,
                    const float* mean, const float* rstd, const void* dh, void* dx, float* part,
                    int* status, cudaStream_t stream) {
-  const Shape p = shape(a.H, a.bf16);
+  const Shape p = shape_of<T>(a.H);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg =
       config(dim3(layernorm_blocks(a.M, a.H, a.bf16)), p.threads, stream, attr);
-  cfg.dynamicSmemBytes = ahead_bytes(p, dh ? 3 : 2, a.bf16);
-  return by_width(a.H, [&](auto w, auto nv) {
-    constexpr bool WARP = decltype(w)::value;
-    constexpr int NV = decltype(nv)::value;
+  cfg.dynamicSmemBytes = (dh ? 3 : 2) * p.ahead;
+  return by_width<T>(a.H, [&](auto, auto warp, auto np) {
+    constexpr bool WARP = decltype(warp)::value;
+    constexpr int NP = decltype(np)::value;
     auto go = [&](auto kern) {
       const cudaError_t e = kern.allow_smem(NORM_SMEM);
       if (e != cudaSuccess) return e;
@@ -590,10 +615,10 @@ cudaError_t bwd_of(const NormArgs& a, const void* dy, const void* h, const void*
                                 static_cast<const T*>(h), weight, mean, rstd,
                                 static_cast<const T*>(dh), static_cast<T*>(dx), part, status);
     };
-    if (part) return dh ? go(KernelOf<k_layernorm_bwd<T, WARP, NV, true, true>>{})
-                        : go(KernelOf<k_layernorm_bwd<T, WARP, NV, true, false>>{});
-    return dh ? go(KernelOf<k_layernorm_bwd<T, WARP, NV, false, true>>{})
-              : go(KernelOf<k_layernorm_bwd<T, WARP, NV, false, false>>{});
+    if (part) return dh ? go(KernelOf<k_layernorm_bwd<T, WARP, NP, true, true>>{})
+                        : go(KernelOf<k_layernorm_bwd<T, WARP, NP, true, false>>{});
+    return dh ? go(KernelOf<k_layernorm_bwd<T, WARP, NP, false, true>>{})
+              : go(KernelOf<k_layernorm_bwd<T, WARP, NP, false, false>>{});
   });
 }
 
@@ -602,8 +627,8 @@ cudaError_t bwd_of(const NormArgs& a, const void* dy, const void* h, const void*
 // (a function of the sizes and the type alone: the workspace is, too)
 int layernorm_blocks(int M, int H, bool bf16) {
   const Shape p = shape(H, bf16);
-  const int all = (M - 1) / block_rows(p) + 1;
-  const int most = 152 * sm_blocks(p, 3, bf16, p.warp || p.nv == 4 ? 512 : p.nv == 1 ? 768 : 640);
+  const int all = (M - 1) / p.rows + 1;
+  const int most = 152 * sm_blocks(p, 3, p.columns <= 8 ? 768 : p.columns <= 16 ? 640 : 512);
   return all < most ? all : most;
 }
 

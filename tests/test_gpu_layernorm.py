@@ -102,7 +102,8 @@ def check(a, eps=1e-5):
 @pytest.mark.parametrize("t,wt", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
 @pytest.mark.parametrize("M,H", [(1, 8), (1, 4096), (7, 64), (9, 256), (130, 264), (33, 512),
                                  (65, 1024), (5, 1032), (700, 2048), (31, 2056), (400, 4096),
-                                 (37, 4872), (20, 8192), (11, 8200), (6, 14336), (3, 16384)])
+                                 (37, 4872), (20, 8192), (11, 8200), (6, 14336), (3, 16384),
+                                 (9, 520), (300, 3064), (5, 6152)])
 @pytest.mark.parametrize("residual", [True, False])
 def test_sizes(M, H, t, wt, residual):
     check(make(M, H, t, wt, residual, bias=M % 2 == 1))
