@@ -21,6 +21,10 @@
 //              sets a warp, that TMA fills ahead of the accumulator and empties behind it
 //              (sixteen warps with a set each were no faster: 16 x 1408 x 2048 step 122 us, 118
 //              so; a unit's k-blocks draw 12 TB/s of L2, and that is what `in` and D wait for)
+// The tensor cores truncate their accumulator at every instruction, by about half of its last bit:
+// over a long K an fp32 result would lose two digits by it (4864: 3e-5, now 4e-6).  With both
+// terms the leading products therefore come in chunks of CHUNK k-blocks, whose sums the epilogue's
+// warps add up in fp32, rounded to nearest, in tensor memory of their own.
 // The units are dealt in turn (unit u to cluster u mod clusters): all cost the same.  Of a
 // symmetric product only the tiles on and below the diagonal are formed, and stored twice.
 #include <cuda_bf16.h>
@@ -52,6 +56,24 @@ template <int TILE, bool Q_MN>
 constexpr uint32_t IDESC_FP16 = (1u << 4) | ((Q_MN ? 1u : 0u) << 16) |
                                 (static_cast<uint32_t>(TILE >> 3) << 17) |
                                 (static_cast<uint32_t>(TILE >> 4) << 24);
+
+// (X X^T: half as long, its error is stretched by two more products.  4864 x 2048 with chunks of
+// 8 everywhere: off by 1.0e-5, 579 us a call of three steps; of 4 in X X^T: 5.9e-6, 585; of 4
+// everywhere: 5.5e-6, 621.)
+template <int KIND>
+constexpr int CHUNK = KIND == ORTHO_SYM ? 4 : 8;
+// Chunks of a unit's k-blocks, and where chunk c ends: the small products (hi lo, lo hi) belong
+// to the first.
+template <int KIND>
+__device__ __forceinline__ int chunks_of(const OrthoGemm& g) {
+  return g.terms == 2 ? (g.kblocks + CHUNK<KIND> - 1) / CHUNK<KIND> : 1;
+}
+template <int KIND>
+__device__ __forceinline__ int chunk_end(const OrthoGemm& g, int c) {
+  if (g.terms != 2) return g.kblocks;
+  const int end = 2 * g.kblocks + (c + 1) * CHUNK<KIND>;
+  return end < 3 * g.kblocks ? end : 3 * g.kblocks;
+}
 
 struct Tile {
   int b, tm, tn;
@@ -141,7 +163,8 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
   constexpr bool Q_MN = KIND != ORTHO_SYM;
   constexpr int TILE = 128 * CG;  // rows and columns of a tile
   constexpr uint32_t IDESC = IDESC_FP16<TILE, Q_MN>;
-  constexpr uint32_t COLS = 2 * TILE;  // two accumulators
+  // two accumulators and, behind them (for a pair: in the second's place), the chunks' sums
+  constexpr uint32_t COLS = 512, SUMS = 256;
   const uint32_t base = (smem_u32(ortho_smem) + 1023u) & ~1023u;
   uint8_t* ctrl = ortho_smem + (base - smem_u32(ortho_smem)) + OSTAGES * OSTAGE + OSTAGING;
   uint64_t* bar = reinterpret_cast<uint64_t*>(ctrl);
@@ -191,6 +214,18 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
   const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
   const int segs = g.terms == 2 ? 3 : 1;
   const int kb_all = g.kblocks * segs;
+  const int chunks = chunks_of<KIND>(g);
+  const bool one_acc = PAIR && chunks > 1;  // the second accumulator holds the sums
+  int acc = 0;  // of the next chunk (or unit), in its readers and its writer alike
+  uint32_t aphase = 0;
+  auto next_acc = [&] {
+    if (one_acc) {
+      aphase ^= 1u;
+    } else {
+      acc ^= 1;
+      if (acc == 0) aphase ^= 1u;
+    }
+  };
   auto failed = [&] {
     *abort_flag = 1;
     atomicExch(g.status, O_TIMEOUT);
@@ -252,41 +287,40 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, aphase = 0;
+      int stage = 0;
+      uint32_t phase = 0;
       bool ok = true, any = false;
       for (int unit = first; ok && unit < g.units; unit += step) {
-        if (!mbar_wait<PAIR>(bar_s(TEMPTY + acc), aphase ^ 1u, lim, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + acc * TILE;
-        for (int i = 0; i < kb_all; ++i) {
-          if (!mbar_wait<PAIR>(bar_s(FULL + stage), phase, lim, abort_flag)) {
-            ok = false;
-            break;
-          }
+        int i = 0;
+        for (int c = 0; ok && c < chunks; ++c) {
+          ok = mbar_wait<PAIR>(bar_s(TEMPTY + acc), aphase ^ 1u, lim, abort_flag);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sp = base + stage * OSTAGE, sq = sp + OPERAND;
+          const uint32_t d = tmem + acc * TILE;
+          const int begin = i;
+          for (const int end = chunk_end<KIND>(g, c); i < end; ++i) {
+            ok = mbar_wait<PAIR>(bar_s(FULL + stage), phase, lim, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sp = base + stage * OSTAGE, sq = sp + OPERAND;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t pd = sdesc_sw128(sp + k * 32, 16, 1024);
-            const uint64_t qd = Q_MN ? sdesc_sw128(sq + k * 2048, 8192, 1024)
-                                     : sdesc_sw128(sq + k * 32, 16, 1024);
-            if constexpr (PAIR) tc_mma_bf16_pair(d, pd, qd, IDESC, i > 0 || k > 0);
-            else tc_mma_bf16(d, pd, qd, IDESC, i > 0 || k > 0);
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t pd = sdesc_sw128(sp + k * 32, 16, 1024);
+              const uint64_t qd = Q_MN ? sdesc_sw128(sq + k * 2048, 8192, 1024)
+                                       : sdesc_sw128(sq + k * 32, 16, 1024);
+              if constexpr (PAIR) tc_mma_bf16_pair(d, pd, qd, IDESC, i > begin || k > 0);
+              else tc_mma_bf16(d, pd, qd, IDESC, i > begin || k > 0);
+            }
+            any = true;
+            if constexpr (PAIR) tc_commit_pair(bar_s(EMPTY + stage), 3);
+            else tc_commit(bar_s(EMPTY + stage));
+            if (++stage == OSTAGES) { stage = 0; phase ^= 1u; }
           }
-          any = true;
-          if constexpr (PAIR) tc_commit_pair(bar_s(EMPTY + stage), 3);
-          else tc_commit(bar_s(EMPTY + stage));
-          if (++stage == OSTAGES) { stage = 0; phase ^= 1u; }
+          if (!ok) break;
+          if constexpr (PAIR) tc_commit_pair(bar_s(TFULL + acc), 3);
+          else tc_commit(bar_s(TFULL + acc));
+          next_acc();
         }
-        if (!ok) break;
-        if constexpr (PAIR) tc_commit_pair(bar_s(TFULL + acc), 3);
-        else tc_commit(bar_s(TFULL + acc));
-        acc ^= 1;
-        if (acc == 0) aphase ^= 1u;
       }
       if (!ok) {
         failed();
@@ -300,19 +334,17 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     } else if (PAIR && lane == 0) {
       // tells the leader that this CTA's warps have read an accumulator: one release at
       // cluster scope, from a thread that has no stores of its own to wait for
-      int acc = 0;
-      uint32_t aphase = 0;
-      for (int unit = first; unit < g.units; unit += step) {
-        if (!mbar_wait(bar_s(TEMPTY + acc), aphase, lim, abort_flag)) {
-          failed();
-          break;
+      bool ok = true;
+      for (int unit = first; ok && unit < g.units; unit += step)
+        for (int c = 0; ok && c < chunks; ++c) {
+          ok = mbar_wait(bar_s(TEMPTY + acc), aphase, lim, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          tc_fence_before();
+          mbar_arrive_cluster(lead(bar_s(TEMPTY + acc)));
+          next_acc();
         }
-        tc_fence_after();
-        tc_fence_before();
-        mbar_arrive_cluster(lead(bar_s(TEMPTY + acc)));
-        acc ^= 1;
-        if (acc == 0) aphase ^= 1u;
-      }
+      if (!ok) failed();
     }
   } else {
     constexpr int WIDTH = TILE / (EPI_WARPS / 4);  // a warp's columns of the tile
@@ -326,17 +358,17 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     const bool has_in = g.alpha != 0.f;
     uint32_t in_phase = 0;  // a bit a set
     uint32_t loading = 0;   // sets with a load in flight
-    int acc = 0;
-    uint32_t aphase = 0;
+    const uint32_t my_lanes = (static_cast<uint32_t>(q * 32) << 16) +
+                              static_cast<uint32_t>(part * WIDTH);
     for (int unit = first; unit < g.units; unit += step) {
       const Tile t = tile_of<KIND>(g, unit);
       const int row0 = t.tm * TILE + static_cast<int>(rank) * 128 + q * 32;
       const int col0 = t.tn * TILE + part * WIDTH;
       const bool mirror = KIND == ORTHO_SYM && t.tm != t.tn;
-      // chunks of 32 columns inside the output
-      int chunks = row0 < g.M ? (g.N - col0 + 31) / 32 : 0;
-      chunks = chunks < 0 ? 0 : chunks < WIDTH / 32 ? chunks : WIDTH / 32;
-      // `in` of chunk c into set c & 1, once what that held has been stored
+      // strips of 32 columns inside the output
+      int strips = row0 < g.M ? (g.N - col0 + 31) / 32 : 0;
+      strips = strips < 0 ? 0 : strips < WIDTH / 32 ? strips : WIDTH / 32;
+      // `in` of strip c into set c & 1, once what that held has been stored
       auto load = [&](int c) {
         const int s = c & 1;
         if (lane == 0) {
@@ -350,19 +382,49 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       if (lane == 0) bulk_wait_read_all();
       __syncwarp();
       if (has_in) {
-        if (chunks > 0) load(0);
-        if (chunks > 1) load(1);
+        if (strips > 0) load(0);
+        if (strips > 1) load(1);
       }
-      if (!mbar_wait<PAIR>(bar_s(TFULL + acc), aphase, lim, abort_flag)) {
+      bool ok = true;
+      uint32_t tb = tmem + my_lanes + acc * TILE;
+      if (chunks == 1) {
+        ok = mbar_wait<PAIR>(bar_s(TFULL + acc), aphase, lim, abort_flag);
+        tc_fence_after();
+      } else {  // the chunks' sums, each accumulator given back as soon as it is added
+        tb = tmem + my_lanes + SUMS;
+        for (int c = 0; c < chunks; ++c) {
+          ok = mbar_wait<PAIR>(bar_s(TFULL + acc), aphase, lim, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int col = 0; col < WIDTH; col += 32) {
+            uint32_t a[32], sum[32];
+            __syncwarp();
+            tmem_ld32(tmem + my_lanes + acc * TILE + col, a);
+            if (c > 0) {
+              tmem_ld32(tb + col, sum);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                a[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(a[i]));
+            } else {
+              tmem_wait_ld();
+            }
+            tmem_st32(tb + col, a);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_s(TEMPTY + acc));
+          next_acc();
+        }
+      }
+      if (!ok) {
         failed();
         break;
       }
-      tc_fence_after();
-      const uint32_t tb = tmem + acc * TILE + (static_cast<uint32_t>(q * 32) << 16) +
-                          static_cast<uint32_t>(part * WIDTH);
-      bool ok = true;
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
+      for (int c = 0; c < strips; ++c) {
         const int s = c & 1, col = col0 + 32 * c;
         const uint32_t box = stg + s * SET;
         float v[32];
@@ -448,7 +510,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
             }
           }
         }
-        if (has_in && c + 2 < chunks) {
+        if (has_in && c + 2 < strips) {
           if (lane == 0) bulk_wait_read_all();
           __syncwarp();
           load(c + 2);
@@ -458,11 +520,12 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
         failed();
         break;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_s(TEMPTY + acc));
-      acc ^= 1;
-      if (acc == 0) aphase ^= 1u;
+      if (chunks == 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_s(TEMPTY + acc));
+        next_acc();
+      }
     }
     // what is in flight ends before shared memory is released
     for (int s = 0; s < 2; ++s)
@@ -502,7 +565,10 @@ cudaLaunchConfig_t ortho_config(int cg, int grid, cudaStream_t stream, cudaLaunc
 
 // Few units with a long K: a cluster of CTAs shares a 128 x 128 tile's k-blocks.  Each leaves
 // its fp32 sums in its shared memory; then each adds up its share of the rows over the
-// cluster's memories, in the CTAs' order, and finishes them.
+// cluster's memories, in the CTAs' order, and finishes them.  With both terms the leading
+// products come in parts of PART k-blocks (see CHUNK), each in the next of four accumulators,
+// which the epilogue's warps add up in registers.
+constexpr int PART = 4;
 constexpr int SPLIT_STAGES = 6;
 constexpr int SPLIT_SMEM = SPLIT_STAGES * OSTAGE + 1024 + 256;
 
@@ -559,7 +625,9 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
   uint8_t* base_g = ortho_smem + (base - smem_u32(ortho_smem));
   uint8_t* ctrl = base_g + SPLIT_STAGES * OSTAGE;
   uint64_t* bar = reinterpret_cast<uint64_t*>(ctrl);
-  constexpr int FULL = 0, EMPTY = SPLIT_STAGES, DONE = 2 * SPLIT_STAGES, NBAR = DONE + 1;
+  constexpr int FULL = 0, EMPTY = SPLIT_STAGES, DONE = 2 * SPLIT_STAGES, FREE = DONE + 4,
+                DRAIN = FREE + 4, NBAR = DRAIN + 1;
+  static_assert(8 * NBAR + 8 <= 256, "control block");
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(ctrl + 8 * NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
   auto bar_s = [&](int i) { return smem_u32(bar + i); };
@@ -571,14 +639,18 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
       mbar_init(bar_s(FULL + i), 1);
       mbar_init(bar_s(EMPTY + i), 1);
     }
-    mbar_init(bar_s(DONE), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar_s(DONE + i), 1);
+      mbar_init(bar_s(FREE + i), EPI_WARPS);
+    }
+    mbar_init(bar_s(DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&g.p);
     prefetch_tmap(&g.q);
   }
   if (warp == 1) {
-    tmem_alloc<1>(smem_u32(tmem_s), 128);
+    tmem_alloc<1>(smem_u32(tmem_s), 512);
     tmem_relinquish<1>();
   }
   tc_fence_before();
@@ -591,10 +663,18 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
   const uint64_t lim = g.timeout_ns;
   const Tile t = tile_of<KIND>(g, static_cast<int>(blockIdx.x) / S);
   const int m0 = t.tm * 128, n0 = t.tn * 128;
-  const int segs = g.terms == 2 ? 3 : 1, kb_all = g.kblocks * segs;
-  const int per = (kb_all + S - 1) / S;  // (the last CTAs may have none)
-  const int kb0 = rank * per < kb_all ? rank * per : kb_all;
-  const int kb1 = kb0 + per < kb_all ? kb0 + per : kb_all;
+  const int segs = g.terms == 2 ? 3 : 1;
+  // a CTA's slice of K, for all of the products (the last CTAs may have none)
+  const int per = (g.kblocks + S - 1) / S;
+  const int slice0 = rank * per < g.kblocks ? rank * per : g.kblocks;
+  const int slice1 = slice0 + per < g.kblocks ? slice0 + per : g.kblocks;
+  const int len = slice1 - slice0, mine = len * segs;
+  // parts, and where one ends: the small products belong to the first
+  const int parts = len == 0 ? 0 : segs == 1 ? 1 : (len + PART - 1) / PART;
+  auto part_end = [&](int i) {
+    const int end = segs == 1 ? mine : mine - len + (i + 1) * PART;
+    return end < mine ? end : mine;
+  };
   auto failed = [&] {
     *abort_flag = 1;
     atomicExch(g.status, O_TIMEOUT);
@@ -604,9 +684,9 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
     if (lane == 0 && !(g.debug_flags & 1)) {
       fence_proxy_async_global();
       const uint64_t pol = policy_evict_normal();
-      int seg = kb0 / g.kblocks, kb = kb0 - seg * g.kblocks;
-      for (int i = kb0; i < kb1; ++i) {
-        const int n = i - kb0, stage = n % SPLIT_STAGES;
+      int seg = 0, kb = slice0;
+      for (int n = 0; n < mine; ++n) {
+        const int stage = n % SPLIT_STAGES;
         if (!mbar_wait(bar_s(EMPTY + stage), (n / SPLIT_STAGES + 1) & 1, lim, abort_flag)) {
           failed();
           for (int j = n - SPLIT_STAGES; j < n; ++j) {  // copies in flight land first
@@ -628,58 +708,80 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
         } else {
           tma_load_3d(s + OPERAND, &g.q, k0, n0, zq, full, pol);
         }
-        if (++kb == g.kblocks) { kb = 0; ++seg; }
+        if (++kb == slice1) { kb = slice0; ++seg; }
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
       bool ok = true;
-      for (int i = kb0; ok && i < kb1; ++i) {
-        const int n = i - kb0, stage = n % SPLIT_STAGES;
-        ok = mbar_wait(bar_s(FULL + stage), n / SPLIT_STAGES & 1, lim, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sp = base + stage * OSTAGE, sq = sp + OPERAND;
+      int n = 0;
+      for (int i = 0; ok && i < parts; ++i) {
+        const int acc = i % 4, begin = n;
+        if (i >= 4) ok = mbar_wait(bar_s(FREE + acc), (i / 4 + 1) & 1, lim, abort_flag);
+        for (const int end = part_end(i); ok && n < end; ++n) {
+          const int stage = n % SPLIT_STAGES;
+          ok = mbar_wait(bar_s(FULL + stage), n / SPLIT_STAGES & 1, lim, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sp = base + stage * OSTAGE, sq = sp + OPERAND;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t pd = sdesc_sw128(sp + k * 32, 16, 1024);
-          const uint64_t qd =
-              Q_MN ? sdesc_sw128(sq + k * 2048, 8192, 1024) : sdesc_sw128(sq + k * 32, 16, 1024);
-          tc_mma_bf16(tmem, pd, qd, IDESC, n > 0 || k > 0);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t pd = sdesc_sw128(sp + k * 32, 16, 1024);
+            const uint64_t qd =
+                Q_MN ? sdesc_sw128(sq + k * 2048, 8192, 1024) : sdesc_sw128(sq + k * 32, 16, 1024);
+            tc_mma_bf16(tmem + acc * 128, pd, qd, IDESC, n > begin || k > 0);
+          }
+          tc_commit(bar_s(EMPTY + stage));
         }
-        tc_commit(bar_s(EMPTY + stage));
+        if (ok) tc_commit(bar_s(DONE + acc));
       }
-      tc_commit(bar_s(DONE));
       if (!ok) {
         failed();
+        tc_commit(bar_s(DRAIN));
         volatile int never = 0;  // what was issued ends before TMEM is freed
-        mbar_wait(bar_s(DONE), 0, 10000000ull, &never);
+        mbar_wait(bar_s(DRAIN), 0, 10000000ull, &never);
       }
     }
   }
   __syncwarp();
   // the sums to shared memory, over the ring (every load has been read when the MMAs are done)
-  bool ok = mbar_wait(bar_s(DONE), 0, lim + 20000000ull, abort_flag) && !*abort_flag;
-  if (!ok && lane == 0) failed();
-  tc_fence_after();
-  if (warp >= 2 && ok && kb1 > kb0) {
+  bool ok = true;
+  if (warp >= 2 && parts > 0) {
     const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 64;
+    float sum[64];
+    for (int i = 0; ok && i < parts; ++i) {
+      ok = mbar_wait(bar_s(DONE + i % 4), i / 4 & 1, lim, abort_flag);
+      if (!ok) break;
+      __syncwarp();
+      tc_fence_after();
 #pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-      uint32_t a[32];
-      tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 64 + c, a);
-      tmem_wait_ld();
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t a[32];
+        tmem_ld32(from + (i % 4) * 128 + c, a);
+        tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        st_shared_v4(sum_part(base, q * 32 + lane, (half * 64 + c) / 4 + j), a[4 * j],
-                     a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+        for (int j = 0; j < 32; ++j)
+          sum[c + j] = i ? sum[c + j] + __uint_as_float(a[j]) : __uint_as_float(a[j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_s(FREE + i % 4));
+    }
+    if (!ok) failed();
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        st_shared_v4(sum_part(base, q * 32 + lane, half * 16 + j), __float_as_uint(sum[4 * j]),
+                     __float_as_uint(sum[4 * j + 1]), __float_as_uint(sum[4 * j + 2]),
+                     __float_as_uint(sum[4 * j + 3]));
     }
   }
   tc_fence_before();
   __syncwarp();
   cluster_sync();
   // my rows
-  const int R = 128 / S, busy = (kb_all + per - 1) / per;  // CTAs that had k-blocks
+  const int R = 128 / S, busy = (g.kblocks + per - 1) / per;  // CTAs that had k-blocks
   const int first_row = m0 + rank * R;
   const size_t mn = static_cast<size_t>(g.M) * g.N, term = mn * g.batch;
   const bool mirror = KIND == ORTHO_SYM && t.tm != t.tn;
@@ -757,7 +859,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
   cluster_sync();  // my sums have been read
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<1>(tmem, 128);
+    tmem_dealloc<1>(tmem, 512);
   }
 }
 

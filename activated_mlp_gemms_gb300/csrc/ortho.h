@@ -7,12 +7,13 @@
 
 namespace mlpk {
 
-// X, A and b A + c A A are fp16 at these powers of two: with singular values below 4, X's
-// entries stay below 2^16, and with them below 1.3 A's and the polynomial's, which are its
-// largest, below 20 2^11.  What a matrix's typical entry is (1 / sqrt(m n) of X at the
-// start, 1 / (m sqrt(n)) of A off its diagonal) stays above fp16's smallest normal value
-// for m, n up to 16384.
-constexpr float ORTHO_X = 16384.f, ORTHO_A = 2048.f;
+// X, A and P = b A + c A A are fp16 at these powers of two.  With singular values s below 2 X's
+// entries stay below 2^15, A's too, and P's below 2^16 where |b s^2 + c s^4| < 8 (Muon's
+// coefficients: s < 1.3, P < 2.8).  At the other end, what a matrix's typical entry is (1 / sqrt(m
+// n) of X at the start, 1 / (m sqrt(n)) of A off its diagonal) and the second terms, 2^-11 of it,
+// should stay above fp16's smallest steps, 2^-24: with A at 2^11 an fp32 result of 4864 x 2048
+// was off by 1.0e-5.
+constexpr float ORTHO_X = 16384.f, ORTHO_A = 8192.f;
 
 constexpr int ORTHO_PARTS = 256;  // partial sums of a matrix's norm
 

@@ -76,11 +76,11 @@ int pick(const OrthoGemm& g, bool sym) {
 // the sums.  Measured (1 / 2 / 4 / 8 CTAs, us of an X X^T with 5 of event time): 64 x 1024 10 / 12 /
 // 12 / 12, 64 x 2048 16 / 14 / 12 / 13, 64 x 4096 24 / 18 / 14 / 14, 256 x 14336 65 / 43 / 27 / 20,
 // 1024 x 2048 16 / 18 / 16 / 35 (more CTAs than SMs).
-int pick_share(int units, int kblocks) {
+int pick_share(int units, int kblocks, int products) {
   int best = 1;
-  double least = 0.27 * kblocks;
+  double least = 0.27 * products * kblocks;
   for (int share = 2; share <= 8 && units * share <= 144; share *= 2) {
-    const double us = 0.27 * ((kblocks + share - 1) / share) + 3.2 + 0.3 * share;
+    const double us = 0.27 * products * ((kblocks + share - 1) / share) + 3.2 + 0.3 * share;
     if (us < least) {
       least = us;
       best = share;
@@ -129,7 +129,8 @@ struct Products {
     g.tiles_n = (g.N + tile - 1) / tile;
     g.units = (sym ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n) * g.batch;
     const int share =
-        cg == 1 && g_tile_policy.load() != 1 ? pick_share(g.units, g.kblocks * (g.terms == 2 ? 3 : 1)) : 1;
+        cg == 1 && g_tile_policy.load() != 1 ? pick_share(g.units, g.kblocks, g.terms == 2 ? 3 : 1)
+                                           : 1;
     return traced(tag, stream, [&] {
       return share > 1 ? launch_ortho_split(g, share, kind, stream)
                        : launch_ortho_gemm(g, cg, kind, stream);

@@ -26,15 +26,18 @@ extern "C" {
 typedef enum { MLP_ORTHO_F32 = 0, MLP_ORTHO_BF16 = 1 } mlp_ortho_type_t;
 
 /* A stack of `batch` matrices [rows, cols] (dense), rows and cols multiples of
- * 8.  coeff: a, b, c; they keep every singular value below 4 (those of the Muon
- * optimiser, 3.4445, -4.7750, 2.0315, below 1.3).  steps 1 to 32; eps >= 0.
+ * 8, the lesser of them at most 32768.  coeff: a, b, c; they keep every singular
+ * value s below 2 and |b s^2 + c s^4| below 8 (those of the Muon optimiser, 3.4445,
+ * -4.7750, 2.0315, below 1.3 and 2.8; what leaves that range comes out infinite or
+ * NaN).  steps 1 to 32; eps >= 0.
  *
- * Arithmetic: X and A are held as fp16 at a fixed power of two (X has no entry
- * above 4), X with the remainder of its rounding beside it, the products summed
- * in fp32.  A bf16 out takes the products of the leading terms (relative error of
- * the result 1.7e-3 at most in the tests, the rounding of out itself 1.7e-3); an
- * fp32 out takes those with the remainders too (1e-5).  |G| is summed in fp32:
- * entries above 1e19 overflow it. */
+ * Arithmetic: X and A are held as fp16 at fixed powers of two, X with the remainder
+ * of its rounding beside it, the products summed in fp32.  A bf16 out takes the
+ * products of the leading terms (the result is off by 2e-3 of its Frobenius norm, as
+ * much as the rounding of out itself; by up to 4e-3 below 16 rows); an fp32 out takes
+ * those with the remainders too (1e-6 to 1e-5, as an fp32 product; 1e-4 where all but
+ * a few singular values are zero).  |G| is summed in fp32: entries above 1e19 overflow
+ * it. */
 typedef struct {
   int rows, cols, batch;
   int steps;
