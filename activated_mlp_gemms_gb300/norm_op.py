@@ -14,7 +14,7 @@ import functools
 import torch
 
 from . import MlpError, _check, _stream, lib
-from .router_op import _device, _rows, _tensor, _ws
+from .router_op import _F32, _device, _rows, _tensor, _ws
 
 _DTYPES = (torch.float32, torch.bfloat16)
 _TYPES = {t: i for i, t in enumerate(_DTYPES)}
@@ -71,7 +71,7 @@ def mlp_layernorm_fwd(p: LayerNorm, x, residual, weight, bias, y, h=None, mean=N
     mean and rstd (fp32 [M]) the rows' statistics: what the backward takes."""
     dev, mh = _device(), (p.M, p.H)
     dt, wt = _DTYPES[p.type == 1], (_DTYPES[p.weight_type == 1],)
-    f32 = (torch.float32,)
+    f32 = _F32
     xp, ldx = _rows(x, mh, dt, "x", dev)
     rp, ldr = _rows(residual, mh, dt, "residual", dev)
     q = p
@@ -93,7 +93,7 @@ def mlp_layernorm_bwd(p: LayerNorm, dy, h, weight, mean, rstd, dh=None, dx=None,
     workspace used (None without dweight and dbias)."""
     dev, mh = _device(), (p.M, p.H)
     dt, wt = (_DTYPES[p.type == 1],), (_DTYPES[p.weight_type == 1],)
-    f32 = (torch.float32,)
+    f32 = _F32
     gt = f32 if fuse_grad_accum else wt
     args = (_tensor(dy, mh, dt, "dy", dev), _tensor(h, mh, dt, "h", dev),
             _tensor(weight, (p.H,), wt, "weight", dev), _tensor(mean, (p.M,), f32, "mean", dev),
@@ -103,7 +103,7 @@ def mlp_layernorm_bwd(p: LayerNorm, dy, h, weight, mean, rstd, dh=None, dx=None,
     if dweight is None and dbias is None:
         ws, at = None, (None, 0)
     else:
-        ws = _ws(ws, lambda: _ws_size(p.M, p.H, p.type), dy.device, stream)
+        ws = _ws(ws, _ws_size(p.M, p.H, p.type), dy.device, stream)
         at = (ws.data_ptr(), ws.numel())
     rc = lib().mlp_layernorm_bwd(ctypes.byref(p), *args, int(bool(fuse_grad_accum)), *at,
                                  _stream(stream))

@@ -74,7 +74,7 @@ def mlp_orthogonalize(p: Ortho, G, out, ws=None, stream=None):
         shape = (p.rows, p.cols)
     args = (_tensor(G, shape, (_DTYPES[p.type == 1],), "G", dev),
             _tensor(out, shape, (_DTYPES[p.out_type == 1],), "out", dev))
-    ws = _ws(ws, lambda: _ws_size(p.rows, p.cols, p.batch, p.out_type), G.device, stream)
+    ws = _ws(ws, _ws_size(p.rows, p.cols, p.batch, p.out_type), G.device, stream)
     rc = lib().mlp_orthogonalize(ctypes.byref(p), *args, ws.data_ptr(), ws.numel(),
                                  _stream(stream))
     _check(rc, "mlp_orthogonalize")

@@ -9,6 +9,7 @@ output); the other tensors are contiguous.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -16,6 +17,8 @@ from . import MlpError, _call_workspace, _check, _stream, lib
 
 _DTYPES = (torch.float32, torch.bfloat16)
 _TYPES = {t: i for i, t in enumerate(_DTYPES)}
+_T = torch.Tensor
+_I32, _F32, _BOOL = (torch.int32,), (torch.float32,), (torch.bool, torch.uint8)
 
 
 class Router(ctypes.Structure):
@@ -51,6 +54,9 @@ def _tensor(t, shape, dtypes, name, device):
     right: dense."""
     if t is None:
         return None
+    if (t.__class__ is _T and t.dtype in dtypes and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -66,6 +72,9 @@ def _tensor(t, shape, dtypes, name, device):
 
 def _rows(t, shape, dtype, name, device):
     """(address, row pitch or 0 when dense) of a matrix with unit column stride."""
+    if (t.__class__ is _T and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr(), 0
     if not isinstance(t, torch.Tensor) or t.is_contiguous() or t.shape != shape:
         return _tensor(t, shape, (dtype,), name, device), 0
     if t.dtype != dtype:
@@ -101,9 +110,15 @@ def alloc_router_workspace(p: Router, device=None) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+@functools.lru_cache(maxsize=1024)
+def _ws_size(T, E, top_k):
+    """The workspace size: a function of the sizes alone."""
+    return mlp_moe_router_workspace_size(Router(T, E, top_k, 0, 0, 0, 0, 0))
+
+
 def _ws(ws, size, device, stream):
     if ws is None:  # (of a problem that the call refuses: any)
-        return _call_workspace(size() or 256, device, stream)
+        return _call_workspace(size or 256, device, stream)
     if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return ws
@@ -121,15 +136,15 @@ def mlp_moe_router_fwd(p: Router, logits, mask, ids, weights, counts=None, balan
     slots = (p.T, p.top_k)
     lp, ldl = _rows(logits, (p.T, p.E), ld, "logits", dev)
     q = _pitched(p, ldl, 0)
-    args = (lp, _tensor(mask, (p.T,), (torch.bool, torch.uint8), "mask", dev),
-            _tensor(ids, slots, (torch.int32,), "ids", dev),
+    args = (lp, _tensor(mask, (p.T,), _BOOL, "mask", dev),
+            _tensor(ids, slots, _I32, "ids", dev),
             _tensor(weights, slots, (wd,), "weights", dev),
-            _tensor(counts, (p.E,), (torch.int32,), "counts", dev),
-            _tensor(balance, (p.E + 1,), (torch.float32,), "balance", dev))
+            _tensor(counts, (p.E,), _I32, "counts", dev),
+            _tensor(balance, (p.E + 1,), _F32, "balance", dev))
     if counts is None and balance is None:
         ws, at = None, (None, 0)
     else:
-        ws = _ws(ws, lambda: mlp_moe_router_workspace_size(q), ids.device, stream)
+        ws = _ws(ws, _ws_size(p.T, p.E, p.top_k), ids.device, stream)
         at = (ws.data_ptr(), ws.numel())
     _check(lib().mlp_moe_router_fwd(ctypes.byref(q), *args, *at, _stream(stream)),
            "mlp_moe_router_fwd")
@@ -149,9 +164,9 @@ def mlp_moe_router_bwd(p: Router, logits, mask, ids, balance, dweights, dloss, d
     if dloss is not None and dloss.numel() == 1:
         dloss = dloss.reshape(1)
     rc = lib().mlp_moe_router_bwd(
-        ctypes.byref(q), lp, _tensor(mask, (p.T,), (torch.bool, torch.uint8), "mask", dev),
-        _tensor(ids, slots, (torch.int32,), "ids", dev),
-        _tensor(balance, (p.E + 1,), (torch.float32,), "balance", dev),
+        ctypes.byref(q), lp, _tensor(mask, (p.T,), _BOOL, "mask", dev),
+        _tensor(ids, slots, _I32, "ids", dev),
+        _tensor(balance, (p.E + 1,), _F32, "balance", dev),
         _tensor(dweights, slots, (wd,), "dweights", dev),
-        _tensor(dloss, (1,), (torch.float32,), "dloss", dev), dp, _stream(stream))
+        _tensor(dloss, (1,), _F32, "dloss", dev), dp, _stream(stream))
     _check(rc, "mlp_moe_router_bwd")
