@@ -25,6 +25,7 @@ namespace {
 
 constexpr int ROUTER_THREADS = 256;
 constexpr int FINISH_CTAS = 8;  // one cluster
+constexpr int FINISH_THREADS = 256;
 constexpr uint32_t KEY_NEG_INF = 0x007fffffu;
 
 // A float as an unsigned integer of the same order: -0 is 0, a NaN above all.  (Adding zero
@@ -112,11 +113,11 @@ struct Row {
   }
 };
 
-// d loss / d p of an expert with c slots, of N routed tokens.
-__device__ __forceinline__ float balance_coef(int E, int top_k, int c, int N) {
-  return N > 0 ? static_cast<float>(static_cast<double>(E) * c /
-                                    (static_cast<double>(top_k) * N * N))
-               : 0.f;
+// d loss / d p of an expert with c slots, of N routed tokens: six roundings of fp32 (a double's
+// division took 2 us of these kernels' last 5).
+__device__ __forceinline__ float balance_coef(float E_k, int c, int N) {
+  const float n = static_cast<float>(N);
+  return N > 0 ? E_k * (static_cast<float>(c) / n) / n : 0.f;
 }
 
 // The sum of the block's threads (in a fixed order), in thread 0.
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(THREADS)
     __syncthreads();
     int n = 0;
     for (int i = 0; i < NG; ++i) n += routed_s[i];
+    const float E_k = static_cast<float>(E) / static_cast<float>(k);
     float loss = 0.f;
     for (int e = tid; e < E; e += THREADS) {
       float s = 0.f;
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(THREADS)
         o.parts.c[at] = cnt[e];
         o.parts.p[at] = s;
       } else {  // all tokens were here
-        const float coef = balance_coef(E, k, cnt[e], n);
+        const float coef = balance_coef(E_k, cnt[e], n);
         if (o.counts) o.counts[e] = cnt[e];
         if (o.balance) o.balance[1 + e] = coef;
         loss += coef * s;
@@ -359,41 +361,41 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // The blocks' sums in their order: one cluster, each CTA its share of the experts.
-__global__ void __launch_bounds__(ROUTER_THREADS)
+__global__ void __launch_bounds__(FINISH_THREADS)
     k_router_finish(const int blocks, const int E, const int top_k, const RouterParts parts,
                     int* __restrict__ counts, float* __restrict__ balance) {
-  __shared__ float p_s[ROUTER_THREADS];
-  __shared__ int c_s[ROUTER_THREADS];
-  __shared__ int n_s[ROUTER_THREADS / 32];
+  __shared__ float p_s[FINISH_THREADS];
+  __shared__ int c_s[FINISH_THREADS];
+  __shared__ int n_s[FINISH_THREADS / 32];
   __shared__ float loss_s[FINISH_CTAS];  // CTA 0's
   const int tid = threadIdx.x;
   const int rank = static_cast<int>(cluster_ctarank());
   const int share = (E + FINISH_CTAS - 1) / FINISH_CTAS;  // at most 128
   int wide = 1;
   while (wide < share) wide *= 2;
-  const int lane = tid % wide, row = tid / wide, rows = ROUTER_THREADS / wide;
+  const int lane = tid % wide, row = tid / wide, rows = FINISH_THREADS / wide;
   const int e = rank * share + lane;
   const bool mine = lane < share && e < E;
   cluster_sync();  // CTA 0 is there
   pdl_wait();
   pdl_launch_dependents();
   int n = 0;
-  for (int b = tid; b < blocks; b += ROUTER_THREADS) n += parts.n[b];
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (tid % 32 == 0) n_s[tid / 32] = n;
+  for (int b = tid; b < blocks; b += FINISH_THREADS) n += parts.n[b];
   int c = 0;
   float s = 0.f;
   if (mine) {
-#pragma unroll 4
+#pragma unroll 10
     for (int b = row; b < blocks; b += rows) {
       c += parts.c[static_cast<size_t>(b) * E + e];
       s += parts.p[static_cast<size_t>(b) * E + e];
     }
   }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (tid % 32 == 0) n_s[tid / 32] = n;
   c_s[tid] = c;
   p_s[tid] = s;
   __syncthreads();
-  for (int i = ROUTER_THREADS / 2; i >= wide; i /= 2) {
+  for (int i = FINISH_THREADS / 2; i >= wide; i /= 2) {
     if (tid < i) {
       c_s[tid] += c_s[tid + i];
       p_s[tid] += p_s[tid + i];
@@ -403,13 +405,15 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
   float loss = 0.f;
   if (row == 0 && mine) {
     n = 0;
-    for (int i = 0; i < ROUTER_THREADS / 32; ++i) n += n_s[i];
-    const float coef = balance_coef(E, top_k, c_s[lane], n);
+#pragma unroll
+    for (int i = 0; i < FINISH_THREADS / 32; ++i) n += n_s[i];
+    const float coef =
+        balance_coef(static_cast<float>(E) / static_cast<float>(top_k), c_s[lane], n);
     if (counts) counts[e] = c_s[lane];
     if (balance) balance[1 + e] = coef;
     loss = coef * p_s[lane];
   }
-  loss = block_sum<ROUTER_THREADS>(loss);
+  loss = block_sum<FINISH_THREADS>(loss);
   if (tid == 0) {
     const uint32_t to = mapa_shared(smem_u32(&loss_s[rank]), 0);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(loss) : "memory");
@@ -662,6 +666,7 @@ cudaError_t launch_router_finish(int T, int E, int top_k, const RouterParts& par
                                  float* balance, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config(FINISH_CTAS, 0, stream, attr);
+  cfg.blockDim.x = FINISH_THREADS;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = FINISH_CTAS;
   attr[1].val.clusterDim.y = 1;

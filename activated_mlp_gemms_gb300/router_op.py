@@ -161,7 +161,7 @@ def mlp_moe_router_bwd(p: Router, logits, mask, ids, balance, dweights, dloss, d
     lp, ldl = _rows(logits, (p.T, p.E), ld, "logits", dev)
     dp, ldd = _rows(dlogits, (p.T, p.E), ld, "dlogits", dev)
     q = _pitched(p, ldl, ldd)
-    if dloss is not None and dloss.numel() == 1:
+    if dloss is not None and dloss.dim() == 0:
         dloss = dloss.reshape(1)
     rc = lib().mlp_moe_router_bwd(
         ctypes.byref(q), lp, _tensor(mask, (p.T,), _BOOL, "mask", dev),
