@@ -1,0 +1,436 @@
+// The orthogonalised update (mlp_ortho.h) of matrices whose lesser side m is at most 128, in one
+// launch: a cluster of up to eight CTAs a matrix, each with WIDTH columns of X in its shared
+// memory, in two fp16 terms, from G to the result.  A step:
+//   each CTA's share of A = X X^T over its own columns, in fp32 to its shared memory;
+//   each adds up 128 / CTAs of A's rows over the cluster and hands them, as fp16, to all;
+//   each forms P = b A + c A A for itself, and a X + P X of its columns.
+// X is the K-major operand of the first product and the MN-major one of the last: the same
+// 128-byte rows serve both.  (Arithmetic and scales as in k_ortho.cu; no sum here is long enough
+// to need its chunks.)  What bounds it is latency: three rounds of MMA, two cluster barriers and
+// three passes over tensor memory a step.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "gemm_params.h"
+#include "ortho.h"
+#include "ptx.cuh"
+
+namespace mlpk {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int BLOCK = 128 * 128;       // bytes of 128 rows x 64 fp16 columns
+constexpr int SUMS = 128 * 128 * 4;    // of the fp32 share of A; P lies over it
+constexpr int O_TIMEOUT = -6;          // MLP_ERR_TIMEOUT
+
+template <int WIDTH>
+struct Smem {
+  static constexpr int X = 0, TERM = WIDTH / 64 * BLOCK;  // X's first term, then its second
+  static constexpr int A = X + 2 * TERM;                  // in one term (256 columns) or two
+  static constexpr int A_TERM = 2 * BLOCK;
+  static constexpr int P = A + (WIDTH == 128 ? 2 : 1) * A_TERM;
+  static constexpr int CTRL = P + SUMS;
+  static constexpr int BYTES = CTRL + 256 + 1024;  // control block, alignment
+};
+
+template <int N, bool B_MN>
+constexpr uint32_t IDESC = (1u << 4) | ((B_MN ? 1u : 0u) << 16) |
+                           (static_cast<uint32_t>(N >> 3) << 17) | (128u >> 4 << 24);
+
+// Eight columns (c, a multiple of 8) of row r of an operand of 64-column blocks: 128-byte rows,
+// 128-byte swizzle.
+__device__ __forceinline__ uint32_t piece(uint32_t at, int r, int c) {
+  return at + static_cast<uint32_t>((c >> 6) * BLOCK + r * 128 + (((c >> 3 & 7) ^ (r & 7)) << 4));
+}
+// Part j (16 bytes) of row r of the fp32 sums, swapped by the row.
+__device__ __forceinline__ uint32_t sum_part(uint32_t at, int r, int j) {
+  return at + static_cast<uint32_t>(r * 512 + ((j ^ (r & 31)) << 4));
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// Eight values as fp16, and what that leaves of them.
+__device__ __forceinline__ uint4 take_term(float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = pack_half2(f[2 * i], f[2 * i + 1]);
+    const float2 x = unpack_half2(w[i]);
+    f[2 * i] -= x.x;
+    f[2 * i + 1] -= x.y;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void add_term(uint4 q, float k, float (&f)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack_half2(w[i]);
+    f[2 * i] += k * x.x;
+    f[2 * i + 1] += k * x.y;
+  }
+}
+__device__ __forceinline__ void put(uint32_t at, uint4 v) { st_shared_v4(at, v.x, v.y, v.z, v.w); }
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Plain stores before MMA reads, wherever in the cluster's shared memory.
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* p, size_t at, float (&f)[8]) {
+  if constexpr (BF16) {
+    const uint4 v = ld_global_v4(static_cast<const __nv_bfloat16*>(p) + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack_bf16x2(w[i]);
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    }
+  } else {
+    const float* q = static_cast<const float*>(p) + at;
+    const uint4 a = ld_global_v4(q), b = ld_global_v4(q + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  }
+}
+
+template <int WIDTH, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) {
+  using S = Smem<WIDTH>;
+  extern __shared__ uint8_t small_smem[];
+  const uint32_t base = (smem_u32(small_smem) + 1023u) & ~1023u;
+  uint8_t* ctrl = small_smem + (base - smem_u32(small_smem)) + S::CTRL;
+  const uint32_t bar = smem_u32(ctrl);
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(ctrl + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 12);
+  float* norm_s = reinterpret_cast<float*>(ctrl + 16);   // a CTA's sum of squares each
+  float* warps_s = reinterpret_cast<float*>(ctrl + 64);  // a warp's
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+  const int b = static_cast<int>(blockIdx.x) / ctas;
+  const int col0 = rank * WIDTH;  // of this CTA's columns
+  const size_t first = static_cast<size_t>(b) * g.m * g.n;
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc<1>(smem_u32(tmem_s), 512);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  cluster_sync();  // (every CTA is there, too)
+  tc_fence_after();
+  const uint32_t tmem = *tmem_s;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && tid == 0) *g.status = 0;
+
+  // G's columns, eight values at a time: f(row, column of this CTA's, values) with zeros outside.
+  // Along X's rows, or along its columns where G holds X transposed.
+  constexpr int EIGHTS = 128 * WIDTH / 8;
+  auto eight = [&](int i, int& r, int& c, float (&f)[8]) {
+    r = g.transposed ? i % 16 * 8 : i / (WIDTH / 8);
+    c = g.transposed ? i / 16 : i % (WIDTH / 8) * 8;
+    if (r < g.m && col0 + c < g.n) {
+      load8<BF16>(g.G, first + (g.transposed ? static_cast<size_t>(col0 + c) * g.m + r
+                                             : static_cast<size_t>(r) * g.n + col0 + c), f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+    }
+  };
+  float squares = 0.f;
+#pragma unroll 4
+  for (int i = tid; i < EIGHTS; i += THREADS) {
+    int r, c;
+    float f[8], t = 0.f;
+    eight(i, r, c, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t += f[j] * f[j];
+    squares += t;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xffffffffu, squares, o);
+  if (lane == 0) warps_s[warp] = squares;
+  __syncthreads();
+  if (tid < ctas) {
+    float t = 0.f;
+    for (int i = 0; i < THREADS / 32; ++i) t += warps_s[i];
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                     mapa_shared(smem_u32(norm_s + rank), static_cast<uint32_t>(tid))),
+                 "f"(t)
+                 : "memory");
+  }
+  __syncwarp();
+  cluster_sync();
+  float total = 0.f;
+  for (int i = 0; i < ctas; ++i) total += norm_s[i];
+  const float factor = ORTHO_X / (sqrtf(total) + g.eps);
+#pragma unroll 4
+  for (int i = tid; i < EIGHTS; i += THREADS) {
+    int r, c;
+    float f[8];
+    eight(i, r, c, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= factor;
+    const uint4 hi = take_term(f), lo = take_term(f);
+    if (!g.transposed) {
+      put(piece(base + S::X, r, c), hi);
+      put(piece(base + S::X + S::TERM, r, c), lo);
+    } else {  // eight rows of a column
+      const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t at = piece(base + S::X, r + j, c & ~7) + (c & 7) * 2;
+        const int sh = j & 1 ? 16 : 0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at),
+                     "h"(static_cast<uint16_t>(h[j / 2] >> sh)) : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + S::TERM),
+                     "h"(static_cast<uint16_t>(l[j / 2] >> sh)) : "memory");
+      }
+    }
+  }
+
+  // A round of MMA: everyone's stores, then thread 0's instructions, then their end.
+  uint32_t phase = 0;
+  bool ok = true;
+  auto round = [&](auto&& issue) {
+    fence_proxy_async_all();
+    __syncthreads();
+    if (tid == 0 && !(g.debug_flags & 1)) {  // (testing: without MMAs the wait runs out)
+      tc_fence_after();
+      issue();
+      tc_commit(bar);
+    }
+    __syncwarp();
+    if (!mbar_wait(bar, phase, g.timeout_ns, abort_flag)) {
+      ok = false;
+      *abort_flag = 1;
+      atomicExch(g.status, O_TIMEOUT);
+    }
+    phase ^= 1u;
+    __syncwarp();
+    tc_fence_after();
+  };
+  // D = P Q over 16-element steps of K, step k's operands at p(k), q(k) in their first terms:
+  // with two terms hi lo, lo hi, hi hi.
+  auto products = [&](uint32_t d, uint32_t idesc, int ksteps, auto&& p, int p_term, auto&& q,
+                      int q_term) {
+    uint32_t more = 0;
+    for (int seg = g.terms == 2 ? 0 : 2; seg < 3; ++seg)
+      for (int k = 0; k < ksteps; ++k) {
+        tc_mma_bf16(d, p(k, seg == 1 ? p_term : 0), q(k, seg == 0 ? q_term : 0), idesc, more);
+        more = 1;
+      }
+  };
+  auto kmajor = [](uint32_t at) {  // step k of an operand of 64-column blocks
+    return [at](int k, int term) {
+      return sdesc_sw128(at + term + (k >> 2) * BLOCK + (k & 3) * 32, 16, 1024);
+    };
+  };
+  const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+  const uint32_t D1 = tmem, D2 = tmem + 128, D3 = tmem + 256;
+  const int share = 128 / ctas;
+
+  for (int step = 0; step < g.steps; ++step) {
+    // this CTA's share of A
+    round([&] {
+      products(D1, IDESC<128, false>, WIDTH / 16, kmajor(base + S::X), S::TERM,
+               kmajor(base + S::X), S::TERM);
+    });
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      uint32_t a[32];
+      tmem_ld32(D1 + lanes + half * 64 + c, a);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        st_shared_v4(sum_part(base + S::P, row, (half * 64 + c) / 4 + j), a[4 * j], a[4 * j + 1],
+                     a[4 * j + 2], a[4 * j + 3]);
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    // my rows of A over the cluster, to all of it: half a warp a row, a lane eight columns
+    for (int i = warp * 2 + (lane >> 4); i < share; i += 16) {
+      const int r = rank * share + i, c = (lane & 15) * 8;
+      float4 x[ORTHO_SMALL_CTAS], y[ORTHO_SMALL_CTAS];
+#pragma unroll
+      for (int s = 0; s < ORTHO_SMALL_CTAS; ++s)
+        if (s < ctas) {
+          const uint32_t from = mapa_shared(base + S::P, static_cast<uint32_t>(s));
+          x[s] = ld_cluster_f4(sum_part(from, r, c / 4));
+          y[s] = ld_cluster_f4(sum_part(from, r, c / 4 + 1));
+        }
+      float f[8] = {};
+#pragma unroll
+      for (int s = 0; s < ORTHO_SMALL_CTAS; ++s)
+        if (s < ctas) {
+          f[0] += x[s].x, f[1] += x[s].y, f[2] += x[s].z, f[3] += x[s].w;
+          f[4] += y[s].x, f[5] += y[s].y, f[6] += y[s].z, f[7] += y[s].w;
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= ORTHO_A / (ORTHO_X * ORTHO_X);
+      const uint4 hi = take_term(f), lo = take_term(f);
+      for (int s = 0; s < ctas; ++s) {
+        const uint32_t to = mapa_shared(piece(base + S::A, r, c), static_cast<uint32_t>(s));
+        st_cluster_v4(to, hi);
+        if (g.terms == 2) st_cluster_v4(to + S::A_TERM, lo);
+      }
+    }
+    fence_proxy_async_all();
+    __syncwarp();
+    cluster_sync();
+    // P = b A + c A A
+    round([&] {
+      products(D2, IDESC<128, false>, 8, kmajor(base + S::A), S::A_TERM, kmajor(base + S::A),
+               S::A_TERM);
+    });
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      uint32_t a[32];
+      tmem_ld32(D2 + lanes + half * 64 + c, a);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        const int col = half * 64 + c + j;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = g.c / ORTHO_A * __uint_as_float(a[j + i]);
+        if (g.terms == 2) add_term(ld_shared_v4(piece(base + S::A + S::A_TERM, row, col)), g.b, f);
+        add_term(ld_shared_v4(piece(base + S::A, row, col)), g.b, f);
+        put(piece(base + S::P, row, col), take_term(f));
+        if (g.terms == 2) put(piece(base + S::P + S::A_TERM, row, col), take_term(f));
+      }
+    }
+    tc_fence_before();
+    // a X + P X of my columns
+    const bool last = step + 1 == g.steps;
+    round([&] {
+      products(D3, IDESC<WIDTH, true>, 8, kmajor(base + S::P), S::A_TERM,
+               [&](int k, int term) {
+                 return sdesc_sw128(base + S::X + term + k * 2048, BLOCK, 1024);
+               },
+               S::TERM);
+    });
+    const float alpha = last ? g.a * (g.scale / ORTHO_X) : g.a;
+    const float beta = last ? g.scale / ORTHO_X / ORTHO_A : 1.f / ORTHO_A;
+#pragma unroll 1
+    for (int c = half * (WIDTH / 2); c < (half + 1) * (WIDTH / 2); c += 32) {
+      uint32_t a[32];
+      __syncwarp();
+      tmem_ld32(D3 + lanes + c, a);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        const uint32_t hi = piece(base + S::X, row, c + j), lo = hi + S::TERM;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = beta * __uint_as_float(a[j + i]);
+        add_term(ld_shared_v4(lo), alpha, f);
+        add_term(ld_shared_v4(hi), alpha, f);
+        if (!last) {
+          put(hi, take_term(f));
+          put(lo, take_term(f));
+        } else if (ok && row < g.m && col0 + c + j < g.n) {
+          if (g.transposed) {  // the warp's rows are contiguous
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const size_t at = first + static_cast<size_t>(col0 + c + j + i) * g.m + row;
+              if (g.out_bf16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(f[i]);
+              else static_cast<float*>(g.out)[at] = f[i];
+            }
+          } else {
+            const size_t at = first + static_cast<size_t>(row) * g.n + col0 + c + j;
+            if (g.out_bf16) {
+              st_global_v4(static_cast<__nv_bfloat16*>(g.out) + at,
+                           make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                      pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+            } else {
+              float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.out) + at);
+              o[0] = make_float4(f[0], f[1], f[2], f[3]);
+              o[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, 512);
+  }
+}
+
+template <int WIDTH, bool BF16>
+cudaError_t launch_of(const OrthoSmall& g, cudaStream_t stream) {
+  auto kern = k_ortho_small<WIDTH, BF16>;
+  static std::atomic<unsigned long long> done{0};  // devices that have the attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(done.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<WIDTH>::BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done.fetch_or(1ull << dev);
+  }
+  int ctas = 1;
+  while (ctas * WIDTH < g.n) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(g.batch * ctas), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Smem<WIDTH>::BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, g);
+}
+
+}  // namespace
+
+cudaError_t launch_ortho_small(const OrthoSmall& g, int width, cudaStream_t stream) {
+  if (width == 128) return g.bf16 ? launch_of<128, true>(g, stream) : launch_of<128, false>(g, stream);
+  return g.bf16 ? launch_of<256, true>(g, stream) : launch_of<256, false>(g, stream);
+}
+
+}  // namespace mlpk

@@ -44,6 +44,21 @@ cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, OrthoKind kind, cudaSt
 // half of the k-blocks).
 cudaError_t launch_ortho_split(const OrthoGemm& g, int share, OrthoKind kind, cudaStream_t stream);
 
+// The whole call for matrices whose lesser side is at most 128: a cluster of CTAs keeps a matrix's
+// X in shared memory, `width` (128 or 256) columns each, from G to the result.
+constexpr int ORTHO_SMALL_M = 128, ORTHO_SMALL_CTAS = 8;
+struct OrthoSmall {
+  const void* G;
+  void* out;
+  int m, n, batch, steps, terms, transposed;  // transposed: G and out are [n, m]
+  int bf16, out_bf16;
+  float a, b, c, eps, scale;
+  int* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
+};
+cudaError_t launch_ortho_small(const OrthoSmall& g, int width, cudaStream_t stream);
+
 // part [batch, ORTHO_PARTS] = sums of squares of G's matrices; clears *status.
 cudaError_t launch_ortho_norm(const void* G, bool bf16, long long size, int batch, float* part,
                               int* status, cudaStream_t stream);

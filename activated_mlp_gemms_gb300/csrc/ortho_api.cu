@@ -89,6 +89,14 @@ int pick_share(int units, int kblocks, int products) {
   return best;
 }
 
+// Columns a CTA where the whole call runs on one cluster a matrix (0: it does not): what fits
+// its shared memory, X in two terms and A and P in `terms`.
+int small_width(const Layout& w) {
+  if (g_tile_policy.load() != 0 || w.m > ORTHO_SMALL_M) return 0;
+  if (w.n <= 128 * ORTHO_SMALL_CTAS) return 128;
+  return w.terms == 1 && w.n <= 256 * ORTHO_SMALL_CTAS ? 256 : 0;
+}
+
 struct Products {
   const mlp_ortho_t* p;
   Layout w;
@@ -160,6 +168,27 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
   char* at = static_cast<char*>(ws);
   float* part = reinterpret_cast<float*>(at + w.part);
   const bool bf16 = p->type == MLP_ORTHO_BF16;
+  if (const int width = small_width(w)) {
+    const OrthoSmall g{G,
+                       out,
+                       w.m,
+                       w.n,
+                       p->batch,
+                       p->steps,
+                       w.terms,
+                       p->rows > p->cols,
+                       bf16,
+                       p->out_type == MLP_ORTHO_BF16,
+                       p->coeff[0],
+                       p->coeff[1],
+                       p->coeff[2],
+                       p->eps,
+                       p->scale,
+                       static_cast<int*>(ws),
+                       wait_limit_ns(),
+                       g_debug_flags.load()};
+    return traced(MLP_KERNEL_ORTHO_STEP, s, [&] { return launch_ortho_small(g, width, s); });
+  }
   MLP_TRY(traced(MLP_KERNEL_ORTHO_SCALE, s, [&] {
     return launch_ortho_norm(G, bf16, (long long)w.m * w.n, p->batch, part,
                              static_cast<int*>(ws), s);

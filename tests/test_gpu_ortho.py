@@ -71,7 +71,8 @@ def make(*shape, dtype=F32, seed=0):
 SIZES = [(8, 8), (8, 1000), (1000, 8), (64, 64), (72, 136), (128, 128), (136, 128), (264, 248),
          (256, 2048), (2048, 256), (520, 520), (352, 256), (1032, 1024), (776, 2056), (1408, 2048),
          (2048, 1408), (1536, 1536), (2304, 2320),
-         (64, 4104), (264, 8200), (8200, 136)]
+         (64, 4104), (264, 8200), (8200, 136), (128, 2048), (2048, 120), (120, 1032), (24, 264),
+         (1024, 128), (16, 520), (8, 2048)]
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32])
@@ -83,7 +84,8 @@ def test_sizes(rows, cols, dtype, out_dtype):
 
 @pytest.mark.parametrize("out_dtype", [BF, F32])
 @pytest.mark.parametrize("batch,rows,cols", [(3, 8, 8), (5, 136, 264), (8, 352, 256),
-                                             (16, 256, 352), (2, 1408, 1024), (4, 1032, 520)])
+                                             (16, 256, 352), (2, 1408, 1024), (4, 1032, 520),
+                                             (30, 64, 1024), (41, 2048, 40)])
 def test_stacks(batch, rows, cols, out_dtype):
     G = make(batch, rows, cols)
     G *= torch.logspace(-3, 3, batch, device="cuda")[:, None, None]  # each by its own norm
@@ -110,7 +112,8 @@ def test_tile_policies(rows, cols, tile_policy, out_dtype):
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32])
-@pytest.mark.parametrize("rows,cols", [(512, 512), (512, 1408), (1408, 512)])
+@pytest.mark.parametrize("rows,cols", [(512, 512), (512, 1408), (1408, 512), (128, 512),
+                                       (1024, 96)])
 def test_spectra(rows, cols, out_dtype):
     """Singular values down to 1e-4 of the largest, and a few strong directions over noise (what
     momenta look like): in bf16 terms alone these are off by 5-30 %."""
@@ -239,11 +242,12 @@ def test_refusals():
 
 def test_bounded_waits():
     """Without loads every wait runs out: the status says so and the next call works."""
-    G = make(520, 520)
-    want = run(G)
-    p = m.ortho(520, 520, dtype=F32)
-    out = torch.empty(520, 520, dtype=BF, device="cuda")
-    for policy in (0, 1, 2):  # (0: K shared by clusters)
+    for size, policy in ((520, 0), (520, 1), (520, 2), (104, 0)):
+        # (0: K shared by clusters; the whole call on one)
+        G = make(size, size)
+        want = run(G)
+        p = m.ortho(size, size, dtype=F32)
+        out = torch.empty(size, size, dtype=BF, device="cuda")
         m.mlp_set_tile_policy(policy)
         m.mlp_set_wait_timeout_ms(20)
         m.mlp_debug_set_flags(m.DEBUG_NO_WORK)
