@@ -581,9 +581,24 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));  // (no clobber: all of a row's are on their way together)
   return v;
+}
+// The sum of eight columns of a row over the shared memories of the first N CTAs, in their order;
+// x, y: the parts' addresses in each.
+template <int N>
+__device__ __forceinline__ void cluster_sums(uint32_t x, uint32_t y, float (&f)[8]) {
+  float4 u[N], v[N];
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    u[s] = ld_cluster_f4(mapa_shared(x, s));
+    v[s] = ld_cluster_f4(mapa_shared(y, s));
+  }
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    f[0] += u[s].x, f[1] += u[s].y, f[2] += u[s].z, f[3] += u[s].w;
+    f[4] += v[s].x, f[5] += v[s].y, f[6] += v[s].z, f[7] += v[s].w;
+  }
 }
 // Part j (16 bytes) of row r of the 128 x 128 fp32 sums: the parts of a row swapped by the row,
 // so that a row a thread and a row a warp both pass without bank conflicts.
@@ -798,20 +813,17 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = 0.f;
-      float4 x[8], y[8];  // (all on their way at once)
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s < busy) {
-          const uint32_t from = mapa_shared(base, static_cast<uint32_t>(s));
-          x[s] = ld_cluster_f4(sum_part(from, r, c8 / 4));
-          y[s] = ld_cluster_f4(sum_part(from, r, c8 / 4 + 1));
-        }
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s < busy) {
-          f[0] += x[s].x, f[1] += x[s].y, f[2] += x[s].z, f[3] += x[s].w;
-          f[4] += y[s].x, f[5] += y[s].y, f[6] += y[s].z, f[7] += y[s].w;
-        }
+      const uint32_t x = sum_part(base, r, c8 / 4), y = sum_part(base, r, c8 / 4 + 1);
+      switch (busy) {
+        case 8: cluster_sums<8>(x, y, f); break;
+        case 7: cluster_sums<7>(x, y, f); break;
+        case 6: cluster_sums<6>(x, y, f); break;
+        case 5: cluster_sums<5>(x, y, f); break;
+        case 4: cluster_sums<4>(x, y, f); break;
+        case 3: cluster_sums<3>(x, y, f); break;
+        case 2: cluster_sums<2>(x, y, f); break;
+        default: cluster_sums<1>(x, y, f);
+      }
       const bool in_d = row < g.M && col < g.N;
       const size_t at = t.b * mn + static_cast<size_t>(row) * g.N + col;
 #pragma unroll

@@ -7,7 +7,9 @@
 // X is the K-major operand of the first product and the MN-major one of the last: the same
 // 128-byte rows serve both.  (Arithmetic and scales as in k_ortho.cu; no sum here is long enough
 // to need its chunks.)  What bounds it is latency: three rounds of MMA, two cluster barriers and
-// three passes over tensor memory a step.
+// three passes over tensor memory a step, and the exchange of A's rows, whose shared-memory
+// traffic between CTAs runs at some 10 bytes a cycle (so only the m x m that there are move).
+// Measured: 64 x 2048 43 us, of them 7 a step; 128 x 2048 76; 128 x 128, one CTA, 35.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,7 +23,7 @@ namespace mlpk {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 512;  // four warps a TMEM lane quadrant
 constexpr int BLOCK = 128 * 128;       // bytes of 128 rows x 64 fp16 columns
 constexpr int SUMS = 128 * 128 * 4;    // of the fp32 share of A; P lies over it
 constexpr int O_TIMEOUT = -6;          // MLP_ERR_TIMEOUT
@@ -87,8 +89,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));  // (no clobber: all of a row's are on their way together)
   return v;
 }
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
@@ -96,6 +97,23 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
                "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
+// The sum of eight columns of a row over the shared memories of the cluster's N CTAs, in their
+// order; x, y: the parts' addresses in each.
+template <int N>
+__device__ __forceinline__ void cluster_sums(uint32_t x, uint32_t y, float (&f)[8]) {
+  float4 u[N], v[N];
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    u[s] = ld_cluster_f4(mapa_shared(x, s));
+    v[s] = ld_cluster_f4(mapa_shared(y, s));
+  }
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    f[0] += u[s].x, f[1] += u[s].y, f[2] += u[s].z, f[3] += u[s].w;
+    f[4] += v[s].x, f[5] += v[s].y, f[6] += v[s].z, f[7] += v[s].w;
+  }
+}
+
 // Plain stores before MMA reads, wherever in the cluster's shared memory.
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
@@ -131,7 +149,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(ctrl + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 12);
   float* norm_s = reinterpret_cast<float*>(ctrl + 16);   // a CTA's sum of squares each
-  float* warps_s = reinterpret_cast<float*>(ctrl + 64);  // a warp's
+  float* warps_s = reinterpret_cast<float*>(ctrl + 64);  // a warp's (16)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
   const int b = static_cast<int>(blockIdx.x) / ctas;
@@ -221,6 +239,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     }
   }
 
+  for (int i = tid * 16; i < S::P - S::A; i += THREADS * 16) put(base + S::A + i, uint4{});
+  // (the first remote stores to A come after the first barrier of a step)
+
   // A round of MMA: everyone's stores, then thread 0's instructions, then their end.
   uint32_t phase = 0;
   bool ok = true;
@@ -258,10 +279,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
       return sdesc_sw128(at + term + (k >> 2) * BLOCK + (k & 3) * 32, 16, 1024);
     };
   };
-  const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+  const int q = warp & 3, part = warp >> 2, row = q * 32 + lane;  // lanes, quarter of columns
   const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
   const uint32_t D1 = tmem, D2 = tmem + 128, D3 = tmem + 256;
-  const int share = 128 / ctas;
+  const int share = (g.m + ctas - 1) / ctas;  // A's rows of a CTA
 
   for (int step = 0; step < g.steps; ++step) {
     // this CTA's share of A
@@ -269,37 +290,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
       products(D1, IDESC<128, false>, WIDTH / 16, kmajor(base + S::X), S::TERM,
                kmajor(base + S::X), S::TERM);
     });
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
+    if (q * 32 < g.m && part * 32 < g.m) {
       uint32_t a[32];
-      tmem_ld32(D1 + lanes + half * 64 + c, a);
+      tmem_ld32(D1 + lanes + part * 32, a);
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        st_shared_v4(sum_part(base + S::P, row, (half * 64 + c) / 4 + j), a[4 * j], a[4 * j + 1],
+        st_shared_v4(sum_part(base + S::P, row, part * 8 + j), a[4 * j], a[4 * j + 1],
                      a[4 * j + 2], a[4 * j + 3]);
     }
     tc_fence_before();
     __syncwarp();
     cluster_sync();
-    // my rows of A over the cluster, to all of it: half a warp a row, a lane eight columns
-    for (int i = warp * 2 + (lane >> 4); i < share; i += 16) {
+    // my rows of A over the cluster, to all of it: half a warp a row, a lane eight columns (what
+    // lies outside m x m is zero and stays so: the exchange's bytes are most of a step's time)
+    for (int i = warp * 2 + (lane >> 4); i < share; i += THREADS / 16) {
       const int r = rank * share + i, c = (lane & 15) * 8;
-      float4 x[ORTHO_SMALL_CTAS], y[ORTHO_SMALL_CTAS];
-#pragma unroll
-      for (int s = 0; s < ORTHO_SMALL_CTAS; ++s)
-        if (s < ctas) {
-          const uint32_t from = mapa_shared(base + S::P, static_cast<uint32_t>(s));
-          x[s] = ld_cluster_f4(sum_part(from, r, c / 4));
-          y[s] = ld_cluster_f4(sum_part(from, r, c / 4 + 1));
-        }
+      if (r >= g.m || c >= g.m) continue;
+      const uint32_t x = sum_part(base + S::P, r, c / 4), y = sum_part(base + S::P, r, c / 4 + 1);
       float f[8] = {};
-#pragma unroll
-      for (int s = 0; s < ORTHO_SMALL_CTAS; ++s)
-        if (s < ctas) {
-          f[0] += x[s].x, f[1] += x[s].y, f[2] += x[s].z, f[3] += x[s].w;
-          f[4] += y[s].x, f[5] += y[s].y, f[6] += y[s].z, f[7] += y[s].w;
-        }
+      if (ctas == 8) cluster_sums<8>(x, y, f);
+      else if (ctas == 4) cluster_sums<4>(x, y, f);
+      else if (ctas == 2) cluster_sums<2>(x, y, f);
+      else cluster_sums<1>(x, y, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= ORTHO_A / (ORTHO_X * ORTHO_X);
       const uint4 hi = take_term(f), lo = take_term(f);
@@ -317,14 +330,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
       products(D2, IDESC<128, false>, 8, kmajor(base + S::A), S::A_TERM, kmajor(base + S::A),
                S::A_TERM);
     });
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
+    {
       uint32_t a[32];
-      tmem_ld32(D2 + lanes + half * 64 + c, a);
+      tmem_ld32(D2 + lanes + part * 32, a);
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
-        const int col = half * 64 + c + j;
+        const int col = part * 32 + j;
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = g.c / ORTHO_A * __uint_as_float(a[j + i]);
@@ -347,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     const float alpha = last ? g.a * (g.scale / ORTHO_X) : g.a;
     const float beta = last ? g.scale / ORTHO_X / ORTHO_A : 1.f / ORTHO_A;
 #pragma unroll 1
-    for (int c = half * (WIDTH / 2); c < (half + 1) * (WIDTH / 2); c += 32) {
+    for (int c = part * (WIDTH / 4); c < (part + 1) * (WIDTH / 4); c += 32) {
       uint32_t a[32];
       __syncwarp();
       tmem_ld32(D3 + lanes + c, a);

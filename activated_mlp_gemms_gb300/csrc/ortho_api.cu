@@ -90,11 +90,18 @@ int pick_share(int units, int kblocks, int products) {
 }
 
 // Columns a CTA where the whole call runs on one cluster a matrix (0: it does not): what fits
-// its shared memory, X in two terms and A and P in `terms`.
-int small_width(const Layout& w) {
+// its shared memory, X in two terms and A and P in `terms`, and at most one wave of such clusters
+// (15 of eight CTAs are resident together), two up to 64 rows.  Measured, five steps in us (one
+// launch / a launch a product): 64 x 1024 39 / 89, 64 x 2048 50 / 89, 128 x 2048 82 / 121, 128 x 128
+// 40 / 79; stacks of 30 x 64 x 1024 74 / 116, 16 x 128 x 2048 153 / 146.
+int small_width(const mlp_ortho_t* p, const Layout& w) {
   if (g_tile_policy.load() != 0 || w.m > ORTHO_SMALL_M) return 0;
-  if (w.n <= 128 * ORTHO_SMALL_CTAS) return 128;
-  return w.terms == 1 && w.n <= 256 * ORTHO_SMALL_CTAS ? 256 : 0;
+  const int width = w.n <= 128 * ORTHO_SMALL_CTAS ? 128 : w.terms == 1 ? 256 : 0;
+  int ctas = 1;
+  while (ctas * width < w.n && ctas <= ORTHO_SMALL_CTAS) ctas *= 2;
+  if (width == 0 || ctas > ORTHO_SMALL_CTAS) return 0;
+  const long long waves = ((long long)p->batch * ctas + 119) / 120;
+  return waves <= (w.m <= 64 ? 2 : 1) ? width : 0;
 }
 
 struct Products {
@@ -168,7 +175,7 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
   char* at = static_cast<char*>(ws);
   float* part = reinterpret_cast<float*>(at + w.part);
   const bool bf16 = p->type == MLP_ORTHO_BF16;
-  if (const int width = small_width(w)) {
+  if (const int width = small_width(p, w)) {
     const OrthoSmall g{G,
                        out,
                        w.m,

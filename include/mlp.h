@@ -485,7 +485,7 @@ typedef enum {
   MLP_KERNEL_ORTHO_SCALE = 25,     /* an update's norm, and X from it */
   MLP_KERNEL_ORTHO_GRAM = 26,      /* A = X X^T */
   MLP_KERNEL_ORTHO_POLY = 27,      /* b A + c A A */
-  MLP_KERNEL_ORTHO_STEP = 28       /* a X + (b A + c A A) X */
+  MLP_KERNEL_ORTHO_STEP = 28       /* a X + (b A + c A A) X; or the whole call of small matrices */
 } mlp_kernel_t;
 
 /* on != 0 starts recording, 0 stops (records already taken are kept). */
