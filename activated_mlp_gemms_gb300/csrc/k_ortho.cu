@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
   // my rows
   const int R = 128 / S, busy = (g.kblocks + per - 1) / per;  // CTAs that had k-blocks
   const int first_row = m0 + rank * R;
-  const size_t mn = static_cast<size_t>(g.M) * g.N, term = mn * g.batch;
+  const size_t in_mat = static_cast<size_t>(g.M) * g.ld_in, d_mat = static_cast<size_t>(g.M) * g.ld_d;
+  const size_t term = d_mat * g.batch;  // (of D in terms)
   const bool mirror = KIND == ORTHO_SYM && t.tm != t.tn;
   const bool across = mirror || (KIND == ORTHO_LAST && g.transposed);
   const bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && g.terms == 2);
@@ -825,13 +826,14 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
         default: cluster_sums<1>(x, y, f);
       }
       const bool in_d = row < g.M && col < g.N;
-      const size_t at = t.b * mn + static_cast<size_t>(row) * g.N + col;
+      const size_t at = t.b * d_mat + static_cast<size_t>(row) * g.ld_d + col;
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= g.beta;
       if (in_d && g.alpha != 0.f) {
-        const __half* x = static_cast<const __half*>(g.in_ptr) + at;
+        const __half* x = static_cast<const __half*>(g.in_ptr) + t.b * in_mat +
+                          static_cast<size_t>(row) * g.ld_in + col;
         for (int z = two_in ? 1 : 0; z >= 0; --z) {
-          const uint4 h = ld_global_v4(x + z * term);
+          const uint4 h = ld_global_v4(x + z * (in_mat * g.batch));
           const uint32_t w[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -862,7 +864,8 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = turned[c * pitch + r8 + j];
-      const size_t at = t.b * mn + static_cast<size_t>(n0 + c) * g.M + first_row + r8;
+      const size_t at =
+          static_cast<size_t>(t.b) * g.N * g.ld_d + static_cast<size_t>(n0 + c) * g.ld_d + first_row + r8;
       if constexpr (KIND == ORTHO_LAST) store_out(g, at, f);
       else store_terms(g, at, term, two_terms, f);
     }
@@ -986,7 +989,7 @@ __global__ void __launch_bounds__(NORM_THREADS)
 // 64 x 64 values a block: straight, or through shared memory with rows and columns changed.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    k_ortho_scale(const T* __restrict__ G, int rows, int cols, int batch,
+    k_ortho_scale(const T* __restrict__ G, int rows, int cols, int batch, int pitch,
                   const float* __restrict__ part, float eps, __half* __restrict__ X) {
   __shared__ float tile[64][65];
   __shared__ float factor_s;
@@ -1002,8 +1005,8 @@ __global__ void __launch_bounds__(256)
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (threadIdx.x == 0) factor_s = ORTHO_X / (sqrtf(s) + eps);
   }
-  const size_t size = static_cast<size_t>(rows) * cols;
-  const T* M = G + b * size;
+  const T* M = G + b * (static_cast<size_t>(rows) * cols);
+  const size_t size = static_cast<size_t>(rows < cols ? rows : cols) * pitch;
   __half* hi = X + b * size;
   __half* lo = hi + static_cast<size_t>(batch) * size;
   const int r0 = static_cast<int>(blockIdx.y) * 64, c0 = static_cast<int>(blockIdx.x) * 64;
@@ -1029,7 +1032,7 @@ __global__ void __launch_bounds__(256)
       float f[8];
       load8(M + static_cast<size_t>(r0 + r) * cols + c0 + c, f);
       if (!transposed) {
-        put(static_cast<size_t>(r0 + r) * cols + c0 + c, f);
+        put(static_cast<size_t>(r0 + r) * pitch + c0 + c, f);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) tile[r][c + j] = f[j];
@@ -1045,7 +1048,7 @@ __global__ void __launch_bounds__(256)
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = tile[r + j][c];
-      put(static_cast<size_t>(c0 + c) * rows + r0 + r, f);
+      put(static_cast<size_t>(c0 + c) * pitch + r0 + r, f);
     }
   }
 }
@@ -1092,17 +1095,17 @@ cudaError_t launch_ortho_norm(const void* G, bool bf16, long long size, int batc
                             status);
 }
 
-cudaError_t launch_ortho_scale(const void* G, bool bf16, int rows, int cols, int batch,
+cudaError_t launch_ortho_scale(const void* G, bool bf16, int rows, int cols, int batch, int pitch,
                                const float* part, float eps, void* X, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg =
       plain_config(dim3((cols + 63) / 64, (rows + 63) / 64, batch), 256, stream, attr);
   if (bf16)
     return cudaLaunchKernelEx(&cfg, k_ortho_scale<__nv_bfloat16>,
-                              static_cast<const __nv_bfloat16*>(G), rows, cols, batch, part, eps,
-                              static_cast<__half*>(X));
+                              static_cast<const __nv_bfloat16*>(G), rows, cols, batch, pitch, part,
+                              eps, static_cast<__half*>(X));
   return cudaLaunchKernelEx(&cfg, k_ortho_scale<float>, static_cast<const float*>(G), rows, cols,
-                            batch, part, eps, static_cast<__half*>(X));
+                            batch, pitch, part, eps, static_cast<__half*>(X));
 }
 
 }  // namespace mlpk

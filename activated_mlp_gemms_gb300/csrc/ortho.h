@@ -30,6 +30,7 @@ struct OrthoGemm {
   CUtensorMap in, d;  // in 32 x 32 boxes
   const void* in_ptr;  // the same, for the kernel of few units
   void* d_ptr;
+  int ld_in, ld_d;     // their row pitches
   int M, N, kblocks, terms, batch;
   int tiles_m, tiles_n, units;
   float alpha, beta;  // alpha 0: no `in`
@@ -62,8 +63,9 @@ cudaError_t launch_ortho_small(const OrthoSmall& g, int width, cudaStream_t stre
 // part [batch, ORTHO_PARTS] = sums of squares of G's matrices; clears *status.
 cudaError_t launch_ortho_norm(const void* G, bool bf16, long long size, int batch, float* part,
                               int* status, cudaStream_t stream);
-// X = ORTHO_X G / (|G| + eps) in two fp16 terms [2, batch, m, n], transposed where rows > cols.
-cudaError_t launch_ortho_scale(const void* G, bool bf16, int rows, int cols, int batch,
+// X = ORTHO_X G / (|G| + eps) in two fp16 terms [2, batch, m, n] with a row pitch, transposed
+// where rows > cols.
+cudaError_t launch_ortho_scale(const void* G, bool bf16, int rows, int cols, int batch, int pitch,
                                const float* part, float eps, void* X, cudaStream_t stream);
 
 }  // namespace mlpk

@@ -31,9 +31,11 @@ int check_ortho(const mlp_ortho_t* p) {
 }
 
 // After the control block (of which only the status word is used): the norms' partial sums, X
-// in two terms twice, and A and P = b A + c A A in one term or two.
+// in two terms twice, and A and P = b A + c A A in one term or two.  Their rows begin at multiples
+// of 128 bytes: boxes of rows that straddle L2's lines took 1.5-1.8 times as long (3000 x 3000).
 struct Layout {
   int m, n, terms;
+  int mp, np;  // row pitches of A and P, and of X
   size_t part, x[2], a, poly, total;
 };
 Layout layout(const mlp_ortho_t* p) {
@@ -41,8 +43,10 @@ Layout layout(const mlp_ortho_t* p) {
   w.m = p->rows < p->cols ? p->rows : p->cols;
   w.n = p->rows < p->cols ? p->cols : p->rows;
   w.terms = p->out_type == MLP_ORTHO_F32 ? 2 : 1;
-  const size_t x = round256((size_t)p->batch * w.m * w.n * 4);
-  const size_t a = round256((size_t)p->batch * w.m * w.m * 2 * w.terms);
+  w.mp = (w.m + 63) / 64 * 64;
+  w.np = (w.n + 63) / 64 * 64;
+  const size_t x = round256((size_t)p->batch * w.m * w.np * 4);
+  const size_t a = round256((size_t)p->batch * w.m * w.mp * 2 * w.terms);
   size_t at = CTRL_BYTES;
   w.part = at;
   at += round256((size_t)p->batch * ORTHO_PARTS * 4);
@@ -112,16 +116,16 @@ struct Products {
   bool ok = true;
 
   // A stack [depth, rows, cols] of fp16 (or bf16, fp32) matrices in boxes {c, r}.
-  CUtensorMap map(const void* ptr, int depth, int rows, int cols, int c, int r,
+  CUtensorMap map(const void* ptr, int depth, int rows, int cols, int pitch, int c, int r,
                   CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, int f32 = 0) {
     CUtensorMap m;
-    if (!make_map(&m, ptr, cols, rows, cols, c, r, f32, swz, depth, (uint64_t)rows * cols))
+    if (!make_map(&m, ptr, cols, rows, pitch, c, r, f32, swz, depth, (uint64_t)rows * pitch))
       ok = false;
     return m;
   }
   // ... in the boxes of the epilogue
-  CUtensorMap boxes(const void* ptr, int depth, int rows, int cols) {
-    return map(ptr, depth, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  CUtensorMap boxes(const void* ptr, int depth, int rows, int cols, int pitch) {
+    return map(ptr, depth, rows, cols, pitch, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   }
   OrthoGemm gemm(int M, int N, int K) {
     OrthoGemm g;
@@ -201,7 +205,8 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
                              static_cast<int*>(ws), s);
   }));
   MLP_TRY(traced(MLP_KERNEL_ORTHO_SCALE, s, [&] {
-    return launch_ortho_scale(G, bf16, p->rows, p->cols, p->batch, part, p->eps, at + w.x[0], s);
+    return launch_ortho_scale(G, bf16, p->rows, p->cols, p->batch, w.np, part, p->eps,
+                              at + w.x[0], s);
   }));
   Products run{p, w, s, static_cast<int*>(ws)};
   const int m = w.m, n = w.n, xs = 2 * p->batch, as = w.terms * p->batch;  // depths
@@ -210,33 +215,37 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
     char *X = at + w.x[i & 1], *next = at + w.x[(i & 1) ^ 1];
     {
       OrthoGemm g = run.gemm(m, m, n);
-      g.p = g.q = run.map(X, xs, m, n, 64, 128);
-      g.in = g.d = run.boxes(A, as, m, m);
+      g.p = g.q = run.map(X, xs, m, n, w.np, 64, 128);
+      g.in = g.d = run.boxes(A, as, m, m, w.mp);
       g.d_ptr = A;
+      g.ld_d = w.mp;
       g.beta = ORTHO_A / (ORTHO_X * ORTHO_X);
       MLP_TRY(run.run(g, ORTHO_SYM, MLP_KERNEL_ORTHO_GRAM));
     }
     {
       OrthoGemm g = run.gemm(m, m, m);
-      g.p = g.q = run.map(A, as, m, m, 64, 128);
-      g.in = run.boxes(A, as, m, m);
-      g.d = run.boxes(P, as, m, m);
+      g.p = g.q = run.map(A, as, m, m, w.mp, 64, 128);
+      g.in = run.boxes(A, as, m, m, w.mp);
+      g.d = run.boxes(P, as, m, m, w.mp);
       g.in_ptr = A;
       g.d_ptr = P;
+      g.ld_in = g.ld_d = w.mp;
       g.alpha = p->coeff[1];
       g.beta = p->coeff[2] / ORTHO_A;
       MLP_TRY(run.run(g, ORTHO_SYM, MLP_KERNEL_ORTHO_POLY));
     }
     OrthoGemm g = run.gemm(m, n, m);
-    g.p = run.map(P, as, m, m, 64, 128);
-    g.q = run.map(X, xs, m, n, 64, 64);
-    g.in = run.boxes(X, xs, m, n);
+    g.p = run.map(P, as, m, m, w.mp, 64, 128);
+    g.q = run.map(X, xs, m, n, w.np, 64, 64);
+    g.in = run.boxes(X, xs, m, n, w.np);
     g.in_ptr = X;
     g.d_ptr = i + 1 < p->steps ? next : out;
+    g.ld_in = w.np;
+    g.ld_d = i + 1 < p->steps ? w.np : p->cols;
     g.alpha = p->coeff[0];
     g.beta = 1.f / ORTHO_A;
     if (i + 1 < p->steps) {
-      g.d = run.boxes(next, xs, m, n);
+      g.d = run.boxes(next, xs, m, n, w.np);
       MLP_TRY(run.run(g, ORTHO_STEP, MLP_KERNEL_ORTHO_STEP));
       continue;
     }
@@ -245,8 +254,8 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
     g.beta *= scale;
     g.out_bf16 = p->out_type == MLP_ORTHO_BF16;
     g.transposed = p->rows > p->cols;
-    g.d = g.out_bf16 ? run.boxes(out, p->batch, p->rows, p->cols)
-                     : run.map(out, p->batch, p->rows, p->cols, 32, 32,
+    g.d = g.out_bf16 ? run.boxes(out, p->batch, p->rows, p->cols, p->cols)
+                     : run.map(out, p->batch, p->rows, p->cols, p->cols, 32, 32,
                                CU_TENSOR_MAP_SWIZZLE_128B, 1);
     MLP_TRY(run.run(g, ORTHO_LAST, MLP_KERNEL_ORTHO_STEP));
   }
