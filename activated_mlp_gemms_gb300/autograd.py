@@ -426,7 +426,9 @@ class _RouterFunction(torch.autograd.Function):
             sums = torch.empty(prob.E + 1, dtype=torch.float32, device=dev)
         mlp_moe_router_fwd(prob, logits, mask, ids, weights, counts, sums)
         if balance:
-            loss = sums.as_strided((), ())
+            # (not a view, and a version of its own: a caller may add to the loss in place; the
+            # backward reads what lies behind it)
+            loss = sums.as_strided((), ()).data
             ctx.mark_non_differentiable(ids, counts)
         else:
             ctx.mark_non_differentiable(ids)

@@ -37,7 +37,8 @@ typedef enum { MLP_ORTHO_F32 = 0, MLP_ORTHO_BF16 = 1 } mlp_ortho_type_t;
  * much as the rounding of out itself; by up to 4e-3 below 16 rows); an fp32 out takes
  * those with the remainders too (1e-6 to 1e-5, as an fp32 product; 1e-4 where all but
  * a few singular values are zero).  |G| is summed in fp32: entries above 1e19 overflow
- * it. */
+ * it, and of a G whose entries are all below 1e-19 it is lost (the result is then G / eps's:
+ * zero, but not with an eps of 0). */
 typedef struct {
   int rows, cols, batch;
   int steps;
