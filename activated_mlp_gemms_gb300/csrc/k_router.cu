@@ -15,6 +15,8 @@
 // second kernel adds the blocks in their order.
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "gemm_params.h"
 #include "ptx.cuh"
 #include "step.h"
@@ -49,12 +51,45 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// The warp's largest, a NaN if there is one.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// (zero below 2^-126)
+__device__ __forceinline__ float exp2_of(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float exp_of(float v) { return exp2_of(v * 1.44269504f); }
+// x = e^(x - m), and their sum.
+template <int V>
+__device__ __forceinline__ float exps(float (&x)[V], float m) {
+  const uint64_t minus = f2_pack(-m, -m), log2e = f2_pack(1.44269504f, 1.44269504f);
+  uint64_t sum = 0;  // two zeros
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    const float2 t = f2_unpack(f2_mul(f2_add(f2_pack(x[v], x[v + 1]), minus), log2e));
+    x[v] = exp2_of(t.x);
+    x[v + 1] = exp2_of(t.y);
+    sum = f2_add(sum, f2_pack(x[v], x[v + 1]));
+  }
+  const float2 s = f2_unpack(sum);
+  return s.x + s.y;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 // The largest of the group's, a NaN if there is one.  (As every collective here: all groups of
 // a warp call it together, routed or not.)
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
   if constexpr (G == 32) {
-    return key_value(__reduce_max_sync(0xffffffffu, order_key(v)));
+    return warp_max(v);
   } else {
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -141,12 +176,17 @@ struct FwdOut {
   int* status;
 };
 
-// The top_k largest of the group's keys, largest first, by rounds: into sel_id and sel_x.
-// Returns the largest.
+// The top_k largest of the group's values, largest first, by rounds: into sel_id and sel_x.
+// Returns the largest, and -inf in all of x.
 template <class R, int G, int V>
-__device__ __forceinline__ uint32_t choose_by_rounds(uint32_t (&key)[V], int lane, int k,
-                                                     int* sel_id, float* sel_x) {
-  uint32_t top = 0;
+__device__ __forceinline__ float choose_by_rounds(float (&x)[V], int lane, int k,
+                                                  int* sel_id, float* sel_x) {
+  uint32_t key[V], top = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    key[v] = order_key(x[v]);
+    x[v] = -INFINITY;
+  }
   for (int j = 0; j < k; ++j) {
     uint32_t bk = 0;
     int be = 0;
@@ -178,57 +218,94 @@ __device__ __forceinline__ uint32_t choose_by_rounds(uint32_t (&key)[V], int lan
       sel_x[j] = key_value(bk);
     }
   }
-  return top;
+  return key_value(top);
 }
 
-// The same for a whole warp and top_k <= 32 by a bound from below; `some` holds 32 pairs.
-// (All lanes come here together.)
-template <class R, int V>
-__device__ __forceinline__ uint32_t choose_by_bound(uint32_t (&key)[V], int lane, int k,
-                                                    int* sel_id, float* sel_x, uint2* some) {
-  uint32_t most = key[0];
+// The same by a bound from below: the top_k-th largest of four partial largest values a lane.
+// What reaches it (top_k values and a few more) goes to `some`, SOME pairs of value and expert,
+// and each of those counts how many are before it.  (More than SOME of them, from equal values,
+// or a NaN: the rounds, which all groups of a warp take together.)
+template <int G>
+constexpr int SOME = 4 * G < ROUTER_MAX_TOP_K ? 4 * G : ROUTER_MAX_TOP_K;
+template <typename L, class R, int G, int V>
+__device__ __forceinline__ float choose_by_bound(const float (&x)[V], const L* row, int lane,
+                                                 int k, int* sel_id, float* sel_x, float2* some) {
+  constexpr uint32_t ALL = 0xffffffffu;
+  float m[4];
 #pragma unroll
-  for (int v = 1; v < V; ++v) most = max(most, key[v]);
-  uint32_t left = most, bound = 0, top = 0;
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {  // (equal ones leave together: the bound only gets lower)
-    bound = __reduce_max_sync(0xffffffffu, left);
-    if (j == 0) top = bound;
-    left = left == bound ? 0u : left;
+  for (int s = 0; s < 4; ++s) {
+    m[s] = x[s * (V / 4)];
+#pragma unroll
+    for (int v = 1; v < V / 4; ++v) m[s] = max_nan(m[s], x[s * (V / 4) + v]);
   }
-  bound = max(bound, KEY_NEG_INF + 1);  // -inf is never chosen
-  uint32_t mine_in = 0;
+  const float top = group_max<G>(max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])));
+  auto order = [&](int i, int j) {
+    const float a = m[i];
+    m[i] = fmaxf(a, m[j]);
+    m[j] = fminf(a, m[j]);
+  };
+  order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+  float bound = top;
+#pragma unroll 4
+  for (int j = 1; j < k; ++j) {  // (equal ones leave together: the bound only gets lower)
+    const bool gone = m[0] == bound;
+    m[0] = gone ? m[1] : m[0];
+    m[1] = gone ? m[2] : m[1];
+    m[2] = gone ? m[3] : m[2];
+    m[3] = gone ? -INFINITY : m[3];
+    bound = m[0];
 #pragma unroll
-  for (int v = 0; v < V; ++v) mine_in |= key[v] >= bound ? 1u << v : 0u;
+    for (int o = G / 2; o > 0; o >>= 1) bound = fmaxf(bound, __shfl_xor_sync(ALL, bound, o));
+  }
+  bound = fmaxf(bound, -FLT_MAX);  // -inf is never chosen
+  // by the difference's sign (inf - inf has none, and no zero has one with +0 added)
+  uint32_t below_it = 0;  // x[0] the top bit
+  const uint64_t minus = f2_pack(0.f - bound, 0.f - bound);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    const float2 d = f2_unpack(f2_add(f2_pack(x[v], x[v + 1]), minus));
+    below_it = __funnelshift_l(__float_as_uint(d.x), below_it, 1);
+    below_it = __funnelshift_l(__float_as_uint(d.y), below_it, 1);
+  }
+  uint32_t mine_in = ~below_it & (0xffffffffu >> (32 - V));
   int n = __popc(mine_in);  // then: those up to this lane's
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int below = __shfl_up_sync(0xffffffffu, n, o);
+  for (int o = 1; o < G; o <<= 1) {
+    const int below = __shfl_up_sync(ALL, n, o, G);
     n += lane >= o ? below : 0;
   }
   int at = n - __popc(mine_in);
-  n = __shfl_sync(0xffffffffu, n, 31);
-  if (n > 32) return choose_by_rounds<R, 32, V>(key, lane, k, sel_id, sel_x);
-  if (mine_in) {  // (few lanes, one or two values each)
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (mine_in >> v & 1u) some[at++] = make_uint2(key[v], R::at(lane, v));
-  }
+  n = __shfl_sync(ALL, n, G - 1, G);
+  if (__any_sync(ALL, n > SOME<G> || top != top)) return NAN;
+  for (; mine_in; mine_in &= mine_in - 1)  // (a lane has one or two)
+    some[at++].y = __int_as_float(R::at(lane, V - __ffs(mine_in)));
   __syncwarp();
-  const uint2 mine = some[lane < n ? lane : 0];
-  int before = 0;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const uint2 o = some[i];
-    before += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+  for (int i = lane; i < n; i += G) some[i].x = static_cast<float>(row[__float_as_int(some[i].y)]);
+  __syncwarp();
+  for (int i = lane; i < n; i += 2 * G) {  // two a lane
+    const int i2 = i + G < n ? i + G : i;
+    const float2 p = some[i], q = some[i2];
+    const int pe = __float_as_int(p.y), qe = __float_as_int(q.y);
+    int before_p = 0, before_q = 0;
+#pragma unroll 2
+    for (int j = 0; j < n; ++j) {
+      const float2 o = some[j];
+      const int e = __float_as_int(o.y);
+      before_p += o.x > p.x || (o.x == p.x && e < pe);
+      before_q += o.x > q.x || (o.x == q.x && e < qe);
+    }
+    if (before_p < k) {
+      sel_id[before_p] = pe;
+      sel_x[before_p] = p.x;
+    }
+    if (before_q < k) {
+      sel_id[before_q] = qe;
+      sel_x[before_q] = q.x;
+    }
   }
-  if (lane < n && before < k) {
-    sel_id[before] = static_cast<int>(mine.y);
-    sel_x[before] = key_value(mine.x);
-  }
-  if (lane >= n && lane < k) {
-    sel_id[lane] = -1;
-    sel_x[lane] = 0.f;
+  for (int j = n + lane; j < k; j += G) {
+    sel_id[j] = -1;
+    sel_x[j] = 0.f;
   }
   return top;
 }
@@ -240,12 +317,13 @@ __global__ void __launch_bounds__(THREADS)
   using R = Row<L, G, V>;
   extern __shared__ __align__(16) float router_smem[];
   const int tid = threadIdx.x, lane = tid % G, g = tid / G, E = a.E, k = a.top_k;
-  int* sel_id = reinterpret_cast<int*>(router_smem) + g * k;
-  float* sel_x = router_smem + (NG + g) * k;
-  int* cnt = reinterpret_cast<int*>(router_smem + 2 * NG * k);  // [E], SUMS
-  float* psum = router_smem + 2 * NG * k + E;                   // [NG, E], SUMS
+  float2* some = reinterpret_cast<float2*>(router_smem) + g * SOME<G>;
+  float* sels = router_smem + 2 * NG * SOME<G>;
+  int* sel_id = reinterpret_cast<int*>(sels) + g * k;
+  float* sel_x = sels + (NG + g) * k;
+  int* cnt = reinterpret_cast<int*>(sels + 2 * NG * k);  // [E], SUMS
+  float* psum = sels + 2 * NG * k + E;                   // [NG, E], SUMS
   __shared__ int routed_s[NG];
-  __shared__ uint2 some_s[G == 32 ? NG : 1][32];
   if constexpr (SUMS) {
     for (int e = tid; e < E; e += THREADS) cnt[e] = 0;
     __syncthreads();
@@ -253,49 +331,44 @@ __global__ void __launch_bounds__(THREADS)
   pdl_wait();
   pdl_launch_dependents();
   if (SUMS && o.status && blockIdx.x == 0 && tid == 0) *o.status = 0;
-  float acc[V];
+  uint64_t acc[V / 2];  // two sums each
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int v = 0; v < V / 2; ++v) acc[v] = 0;
   int n_routed = 0;
   // (every group of a warp stays in the loop to its end: they share the shuffles)
-  for (long long base = static_cast<long long>(blockIdx.x) * NG; base < a.T;
-       base += static_cast<long long>(gridDim.x) * NG) {
+  const long long step = static_cast<long long>(gridDim.x) * NG;
+  for (long long base = static_cast<long long>(blockIdx.x) * NG; base < a.T; base += step) {
     const long long t = base + g;
     const bool in = t < a.T;
     const bool take = in && (!a.mask || a.mask[t]);
     float x[V];
-    uint32_t key[V];
+    const L* row = static_cast<const L*>(a.logits) + t * a.ldl;
     if (take) {
-      R::load(static_cast<const L*>(a.logits) + t * a.ldl, lane, E, vec, x);
+      R::load(row, lane, E, vec, x);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[v] = -INFINITY;
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);
-    uint32_t top;
-    if (G == 32 && k <= 32)
-      top = choose_by_bound<R, V>(key, lane, k, sel_id, sel_x, some_s[G == 32 ? g : 0]);
-    else
-      top = choose_by_rounds<R, G, V>(key, lane, k, sel_id, sel_x);
+    float top = NAN;
+    if (k <= SOME<G>) top = choose_by_bound<L, R, G, V>(x, row, lane, k, sel_id, sel_x, some);
+    if (__any_sync(0xffffffffu, top != top)) {
+      top = choose_by_rounds<R, G, V>(x, lane, k, sel_id, sel_x);
+      if (take) R::load(row, lane, E, vec, x);  // (no registers for it and its keys)
+    }
     __syncwarp();
-    const bool routed = top > KEY_NEG_INF;
+    const bool routed = top != -INFINITY;
     // (what is not routed gets no weights, and no NaN from -inf - -inf)
-    const float m = routed ? key_value(top) : 0.f;
+    const float m = routed ? top : 0.f;
     float inv = 0.f;  // of the softmax's sum, or of the chosen ones'
     if (SUMS || !a.renorm) {
-      float total = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        x[v] = __expf(x[v] - m);
-        total += x[v];
-      }
+      float total = exps(x, m);
       total = group_sum<G>(total);
-      inv = routed ? 1.f / total : 0.f;
+      inv = routed ? reciprocal(total) : 0.f;
       if constexpr (SUMS) {
         if (routed) {
+          const uint64_t by = f2_pack(inv, inv);
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] += x[v] * inv;
+          for (int v = 0; v < V; v += 2) acc[v / 2] = f2_fma(f2_pack(x[v], x[v + 1]), by, acc[v / 2]);
           ++n_routed;
         }
       }
@@ -308,19 +381,19 @@ __global__ void __launch_bounds__(THREADS)
     };
     if (k <= G) {  // a slot a lane
       const int id = lane < k ? sel_id[lane] : -1;
-      float w = id >= 0 ? __expf(sel_x[lane] - m) : 0.f;
-      w *= a.renorm ? 1.f / group_sum<G>(w) : inv;
+      float w = id >= 0 ? exp_of(sel_x[lane] - m) : 0.f;
+      w *= a.renorm ? reciprocal(group_sum<G>(w)) : inv;
       if (in && lane < k) put(lane, id, id >= 0 ? w : 0.f);
     } else {
       if (a.renorm) {
         float total = 0.f;
         for (int j = lane; j < k; j += G)
-          if (sel_id[j] >= 0) total += __expf(sel_x[j] - m);
-        inv = 1.f / group_sum<G>(total);
+          if (sel_id[j] >= 0) total += exp_of(sel_x[j] - m);
+        inv = reciprocal(group_sum<G>(total));
       }
       if (in) {
         for (int j = lane; j < k; j += G)
-          put(j, sel_id[j], sel_id[j] >= 0 ? __expf(sel_x[j] - m) * inv : 0.f);
+          put(j, sel_id[j], sel_id[j] >= 0 ? exp_of(sel_x[j] - m) * inv : 0.f);
       }
     }
     __syncwarp();
@@ -329,7 +402,8 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = R::at(lane, v);
-      if (e < E) psum[g * E + e] = acc[v];
+      const float2 two = f2_unpack(acc[v / 2]);
+      if (e < E) psum[g * E + e] = v % 2 ? two.y : two.x;
     }
     if (lane == 0) routed_s[g] = n_routed;
     __syncthreads();
@@ -495,16 +569,11 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
     const bool routed = m != -INFINITY;
     if (!routed) m = 0.f;
     if (!routed || id >= E) id = -1;
-    float total = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      x[v] = __expf(x[v] - m);
-      total += x[v];
-    }
+    float total = exps(x, m);
     put_row(x);
     __syncwarp();
     total = group_sum<G>(total);
-    const float inv = routed ? 1.f / total : 0.f;
+    const float inv = routed ? reciprocal(total) : 0.f;
     // what the weights' gradient adds at the chosen experts: w (dw - <w, dw>), or p dw of
     // p (dw - <p, dw>)
     float add = 0.f, dot = 0.f, w_inv = 1.f, w_dot = 0.f;
@@ -513,7 +582,8 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
       if (a.renorm) {
         const float s = group_sum<G>(e);
         const float d = group_sum<G>(id >= 0 ? e * dw : 0.f);
-        if (id >= 0) add = e / s * (dw - d / s);
+        const float r = reciprocal(s);
+        if (id >= 0) add = e * r * (dw - d * r);
       } else if (id >= 0) {
         add = dot = e * inv * dw;
       }
@@ -526,7 +596,7 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
         d += buf[i] * dw_at(t * k + j);
       }
       if (a.renorm) {
-        w_inv = 1.f / group_sum<G>(s);
+        w_inv = reciprocal(group_sum<G>(s));
         w_dot = group_sum<G>(d) * w_inv;
       } else {
         w_inv = inv;
@@ -577,10 +647,9 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
   }
 }
 
-// Lanes and values a lane by the number of experts: few lanes for few experts, so that a
-// warp takes several tokens.
+// Lanes and values a lane of the backward by the number of experts.
 template <class F>
-cudaError_t by_experts(int E, F&& f) {
+cudaError_t by_experts_bwd(int E, F&& f) {
   if (E <= 32) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
   if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
   if (E <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
@@ -588,7 +657,19 @@ cudaError_t by_experts(int E, F&& f) {
   if (E <= 512) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
   return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
 }
-int lanes_of(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : 32; }
+int lanes_bwd(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : 32; }
+// ... and of the forward: as few lanes as the registers allow, so that a warp chooses for up to
+// four tokens at once.
+template <class F>
+cudaError_t by_experts(int E, F&& f) {
+  if (E <= 32) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+  if (E <= 128) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{});
+  if (E <= 256) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{});
+  if (E <= 512) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 32>{});
+  return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
+}
+int lanes_of(int E) { return E <= 256 ? 8 : E <= 512 ? 16 : 32; }
 
 bool rows_aligned(const void* ptr, int ld, bool bf16) {
   return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 &&
@@ -615,7 +696,8 @@ int rounds(int T, int groups) { return (T - 1) / groups + 1; }
 // a thread up to 256 experts), since every block is a partial sum, and 256 where those would be
 // too few blocks for the GPU.
 int sum_threads(int T, int E) {
-  return E <= 256 && rounds(T, 1024 / lanes_of(E)) > 152 ? 1024 : ROUTER_THREADS;
+  const int many = E <= 64 ? 1024 : 512;
+  return rounds(T, many / lanes_of(E)) > 152 ? many : ROUTER_THREADS;
 }
 
 }  // namespace
@@ -625,7 +707,7 @@ int router_blocks(int T, int E) {
   const int threads = sum_threads(T, E);
   const int all = rounds(T, threads / lanes_of(E));
   if (all <= 8) return 1;  // one block, no second kernel
-  const int most = threads == 1024 ? 152 : 2 * 152;
+  const int most = threads > ROUTER_THREADS ? 152 : 2 * 152;
   return all < most ? all : most;
 }
 
@@ -641,22 +723,22 @@ cudaError_t launch_router_fwd(const RouterArgs& a, int* ids, void* weights, int*
   return by_experts(a.E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
     const int ng = threads / G;
-    const size_t smem = (2ull * ng * a.top_k + (sums ? (ng + 1ull) * a.E : 0)) * 4;
+    const size_t smem =
+        (2ull * ng * (SOME<G> + a.top_k) + (sums ? (ng + 1ull) * a.E : 0)) * 4;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(blocks, smem, stream, attr);
     cfg.blockDim.x = static_cast<unsigned>(threads);
     auto go = [&](auto kern) {
-      // (at most 97 KB: 128 groups of 64 experts, and 64 slots a group)
-      const cudaError_t e = kern.allow_smem(128 * 1024);
+      // (at most 129 KB: 128 groups of 64 experts, and 64 slots a group)
+      const cudaError_t e = kern.allow_smem(160 * 1024);
       if (e != cudaSuccess) return e;
       return cudaLaunchKernelEx(&cfg, kern.kernel, a, o, vec);
     };
     if (!sums) return a.l_bf16 ? go(KernelOf<k_router_fwd<__nv_bfloat16, G, V, false, ROUTER_THREADS>>{})
                                : go(KernelOf<k_router_fwd<float, G, V, false, ROUTER_THREADS>>{});
-    if constexpr (V <= 8) {
-      if (threads == 1024) return a.l_bf16 ? go(KernelOf<k_router_fwd<__nv_bfloat16, G, V, true, 1024>>{})
-                                           : go(KernelOf<k_router_fwd<float, G, V, true, 1024>>{});
-    }
+    constexpr int MANY = V <= 8 ? 1024 : 512;
+    if (threads == MANY) return a.l_bf16 ? go(KernelOf<k_router_fwd<__nv_bfloat16, G, V, true, MANY>>{})
+                                         : go(KernelOf<k_router_fwd<float, G, V, true, MANY>>{});
     return a.l_bf16 ? go(KernelOf<k_router_fwd<__nv_bfloat16, G, V, true, ROUTER_THREADS>>{})
                     : go(KernelOf<k_router_fwd<float, G, V, true, ROUTER_THREADS>>{});
   });
@@ -679,11 +761,11 @@ cudaError_t launch_router_finish(int T, int E, int top_k, const RouterParts& par
 cudaError_t launch_router_bwd(const RouterArgs& a, const int* ids, const float* balance,
                               const void* dweights, const float* dloss, void* dlogits,
                               cudaStream_t stream) {
-  const int all = rounds(a.T, ROUTER_THREADS / lanes_of(a.E));
+  const int all = rounds(a.T, ROUTER_THREADS / lanes_bwd(a.E));
   const int blocks = all < 8 * 152 ? all : 8 * 152;
   const bool vec = rows_aligned(a.logits, a.ldl, a.l_bf16);
   const bool vec_d = rows_aligned(dlogits, a.ldd, a.l_bf16);
-  return by_experts(a.E, [&](auto g, auto v) {
+  return by_experts_bwd(a.E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(blocks, ROUTER_THREADS * V * 4ull, stream, attr);
