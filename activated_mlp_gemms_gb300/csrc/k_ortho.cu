@@ -24,13 +24,14 @@
 // The tensor cores truncate their accumulator at every instruction, by about half of its last bit:
 // over a long K an fp32 result would lose two digits by it (4864: 3e-5, now 4e-6).  With both
 // terms the leading products therefore come in chunks of CHUNK k-blocks, whose sums the epilogue's
-// warps add up in fp32, rounded to nearest, in tensor memory of their own.
+// warps add up in fp32, rounded to nearest, in registers.
 // The units are dealt in turn (unit u to cluster u mod clusters): all cost the same.  Of a
 // symmetric product only the tiles on and below the diagonal are formed, and stored twice.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "gemm_params.h"
 #include "ortho.h"
@@ -66,11 +67,10 @@ constexpr int CHUNK = KIND == ORTHO_SYM ? 4 : 8;
 // to the first.
 template <int KIND>
 __device__ __forceinline__ int chunks_of(const OrthoGemm& g) {
-  return g.terms == 2 ? (g.kblocks + CHUNK<KIND> - 1) / CHUNK<KIND> : 1;
+  return (g.kblocks + CHUNK<KIND> - 1) / CHUNK<KIND>;
 }
 template <int KIND>
 __device__ __forceinline__ int chunk_end(const OrthoGemm& g, int c) {
-  if (g.terms != 2) return g.kblocks;
   const int end = 2 * g.kblocks + (c + 1) * CHUNK<KIND>;
   return end < 3 * g.kblocks ? end : 3 * g.kblocks;
 }
@@ -156,15 +156,14 @@ __device__ __forceinline__ void take_term(float (&v)[32], uint32_t (&w)[16]) {
   }
 }
 
-template <int CG, int KIND>
+template <int CG, int KIND, bool TWO>
 __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constant__ OrthoGemm g) {
   extern __shared__ uint8_t ortho_smem[];
   constexpr bool PAIR = CG == 2;
   constexpr bool Q_MN = KIND != ORTHO_SYM;
   constexpr int TILE = 128 * CG;  // rows and columns of a tile
   constexpr uint32_t IDESC = IDESC_FP16<TILE, Q_MN>;
-  // two accumulators and, behind them (for a pair: in the second's place), the chunks' sums
-  constexpr uint32_t COLS = 512, SUMS = 256;
+  constexpr uint32_t COLS = 2 * TILE;  // two accumulators
   const uint32_t base = (smem_u32(ortho_smem) + 1023u) & ~1023u;
   uint8_t* ctrl = ortho_smem + (base - smem_u32(ortho_smem)) + OSTAGES * OSTAGE + OSTAGING;
   uint64_t* bar = reinterpret_cast<uint64_t*>(ctrl);
@@ -212,19 +211,14 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
 
   const uint64_t lim = g.timeout_ns;
   const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
-  const int segs = g.terms == 2 ? 3 : 1;
+  constexpr int segs = TWO ? 3 : 1;
   const int kb_all = g.kblocks * segs;
-  const int chunks = chunks_of<KIND>(g);
-  const bool one_acc = PAIR && chunks > 1;  // the second accumulator holds the sums
+  const int chunks = TWO ? chunks_of<KIND>(g) : 1;
   int acc = 0;  // of the next chunk (or unit), in its readers and its writer alike
   uint32_t aphase = 0;
   auto next_acc = [&] {
-    if (one_acc) {
-      aphase ^= 1u;
-    } else {
-      acc ^= 1;
-      if (acc == 0) aphase ^= 1u;
-    }
+    acc ^= 1;
+    if (acc == 0) aphase ^= 1u;
   };
   auto failed = [&] {
     *abort_flag = 1;
@@ -298,7 +292,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
           tc_fence_after();
           const uint32_t d = tmem + acc * TILE;
           const int begin = i;
-          for (const int end = chunk_end<KIND>(g, c); i < end; ++i) {
+          for (const int end = TWO ? chunk_end<KIND>(g, c) : kb_all; i < end; ++i) {
             ok = mbar_wait<PAIR>(bar_s(FULL + stage), phase, lim, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -353,8 +347,8 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     const uint32_t in_bar = bar_s(IN + 2 * (warp - 2));
     const uint64_t pol = policy_evict_normal();
     fence_proxy_async_global();
-    const bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && g.terms == 2);
-    const bool two_in = KIND != ORTHO_SYM || g.terms == 2;
+    constexpr bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && TWO);
+    constexpr bool two_in = KIND != ORTHO_SYM || TWO;
     const bool has_in = g.alpha != 0.f;
     uint32_t in_phase = 0;  // a bit a set
     uint32_t loading = 0;   // sets with a load in flight
@@ -387,36 +381,43 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       }
       bool ok = true;
       uint32_t tb = tmem + my_lanes + acc * TILE;
-      if (chunks == 1) {
+      if (!TWO || chunks == 1) {
         ok = mbar_wait<PAIR>(bar_s(TFULL + acc), aphase, lim, abort_flag);
         tc_fence_after();
-      } else {  // the chunks' sums, each accumulator given back as soon as it is added
-        tb = tmem + my_lanes + SUMS;
+      } else {  // the chunks' sums, in registers; then over the last accumulator
+        float sum[WIDTH];
+#pragma unroll
+        for (int i = 0; i < WIDTH; ++i) sum[i] = 0.f;
         for (int c = 0; c < chunks; ++c) {
           ok = mbar_wait<PAIR>(bar_s(TFULL + acc), aphase, lim, abort_flag);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll 1
-          for (int col = 0; col < WIDTH; col += 32) {
-            uint32_t a[32], sum[32];
-            __syncwarp();
-            tmem_ld32(tmem + my_lanes + acc * TILE + col, a);
-            if (c > 0) {
-              tmem_ld32(tb + col, sum);
-              tmem_wait_ld();
+          __syncwarp();
+          tb = tmem + my_lanes + acc * TILE;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                a[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(a[i]));
-            } else {
-              tmem_wait_ld();
-            }
+          for (int col = 0; col < WIDTH; col += 32) {
+            uint32_t a[32];
+            tmem_ld32(tb + col, a);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[col + i] += __uint_as_float(a[i]);
+          }
+          if (c + 1 < chunks) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_s(TEMPTY + acc));
+            next_acc();
+          }
+        }
+        if (ok) {
+#pragma unroll
+          for (int col = 0; col < WIDTH; col += 32) {
+            uint32_t a[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(sum[col + i]);
             tmem_st32(tb + col, a);
           }
           tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_s(TEMPTY + acc));
-          next_acc();
         }
       }
       if (!ok) {
@@ -520,12 +521,10 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
         failed();
         break;
       }
-      if (chunks == 1) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_s(TEMPTY + acc));
-        next_acc();
-      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_s(TEMPTY + acc));
+      next_acc();
     }
     // what is in flight ends before shared memory is released
     for (int s = 0; s < 2; ++s)
@@ -896,9 +895,9 @@ cudaError_t launch_split(const OrthoGemm& g, int share, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, g);
 }
 
-template <int CG, int KIND>
+template <int CG, int KIND, bool TWO>
 cudaError_t prepare() {
-  auto kern = k_ortho_gemm<CG, KIND>;
+  auto kern = k_ortho_gemm<CG, KIND, TWO>;
   static std::atomic<unsigned long long> done{0};  // devices that have the attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -909,7 +908,7 @@ cudaError_t prepare() {
   return e;
 }
 
-template <int CG, int KIND>
+template <int CG, int KIND, bool TWO>
 int clusters() {
   int dev = 0, sms = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -919,20 +918,20 @@ int clusters() {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = ortho_config(CG, sms / CG * CG, nullptr, attr);
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_ortho_gemm<CG, KIND>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k_ortho_gemm<CG, KIND, TWO>, &cfg) != cudaSuccess) return 0;
   if (dev < 64) cache[dev].store(n);
   return n;
 }
 
-template <int CG, int KIND>
+template <int CG, int KIND, bool TWO>
 cudaError_t launch_of(const OrthoGemm& g, cudaStream_t stream) {
-  const cudaError_t e = prepare<CG, KIND>();
+  const cudaError_t e = prepare<CG, KIND, TWO>();
   if (e != cudaSuccess) return e;
-  const int n = clusters<CG, KIND>();
+  const int n = clusters<CG, KIND, TWO>();
   if (n <= 0) return cudaErrorUnknown;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = ortho_config(CG, CG * (g.units < n ? g.units : n), stream, attr);
-  return cudaLaunchKernelEx(&cfg, k_ortho_gemm<CG, KIND>, g);
+  return cudaLaunchKernelEx(&cfg, k_ortho_gemm<CG, KIND, TWO>, g);
 }
 
 // ------------------------------------------------------------- norm and scale
@@ -1069,10 +1068,16 @@ cudaLaunchConfig_t plain_config(dim3 grid, int threads, cudaStream_t stream,
 }  // namespace
 
 cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, OrthoKind kind, cudaStream_t stream) {
+  auto of = [&](auto k) {
+    constexpr int KIND = decltype(k)::value;
+    if (g.terms == 2)
+      return cg == 2 ? launch_of<2, KIND, true>(g, stream) : launch_of<1, KIND, true>(g, stream);
+    return cg == 2 ? launch_of<2, KIND, false>(g, stream) : launch_of<1, KIND, false>(g, stream);
+  };
   switch (kind) {
-    case ORTHO_SYM: return cg == 2 ? launch_of<2, ORTHO_SYM>(g, stream) : launch_of<1, ORTHO_SYM>(g, stream);
-    case ORTHO_STEP: return cg == 2 ? launch_of<2, ORTHO_STEP>(g, stream) : launch_of<1, ORTHO_STEP>(g, stream);
-    default: return cg == 2 ? launch_of<2, ORTHO_LAST>(g, stream) : launch_of<1, ORTHO_LAST>(g, stream);
+    case ORTHO_SYM: return of(std::integral_constant<int, ORTHO_SYM>{});
+    case ORTHO_STEP: return of(std::integral_constant<int, ORTHO_STEP>{});
+    default: return of(std::integral_constant<int, ORTHO_LAST>{});
   }
 }
 
