@@ -25,6 +25,9 @@
 // over a long K an fp32 result would lose two digits by it (4864: 3e-5, now 4e-6).  With both
 // terms the leading products therefore come in chunks of CHUNK k-blocks, whose sums the epilogue's
 // warps add up in fp32, rounded to nearest, in registers.
+// With SPLIT a unit of a symmetric product has a cluster of two pairs, each with half of its
+// k-blocks: a pair keeps half of the tile's columns, leaves its sums of the others in its shared
+// memory over the ring, and adds to its own the other pair's, read from there strip by strip.
 // The units are dealt in turn (unit u to cluster u mod clusters): all cost the same.  Of a
 // symmetric product only the tiles on and below the diagonal are formed, and stored twice.
 #include <cuda_bf16.h>
@@ -66,13 +69,13 @@ constexpr int CHUNK = KIND == ORTHO_SYM ? 4 : 8;
 // Chunks of a unit's k-blocks, and where chunk c ends: the small products (hi lo, lo hi) belong
 // to the first.
 template <int KIND>
-__device__ __forceinline__ int chunks_of(const OrthoGemm& g) {
-  return (g.kblocks + CHUNK<KIND> - 1) / CHUNK<KIND>;
+__device__ __forceinline__ int chunks_of(int kblocks) {
+  return (kblocks + CHUNK<KIND> - 1) / CHUNK<KIND>;
 }
 template <int KIND>
-__device__ __forceinline__ int chunk_end(const OrthoGemm& g, int c) {
-  const int end = 2 * g.kblocks + (c + 1) * CHUNK<KIND>;
-  return end < 3 * g.kblocks ? end : 3 * g.kblocks;
+__device__ __forceinline__ int chunk_end(int kblocks, int c) {
+  const int end = 2 * kblocks + (c + 1) * CHUNK<KIND>;
+  return end < 3 * kblocks ? end : 3 * kblocks;
 }
 
 struct Tile {
@@ -156,10 +159,24 @@ __device__ __forceinline__ void take_term(float (&v)[32], uint32_t (&w)[16]) {
   }
 }
 
-template <int CG, int KIND, bool TWO>
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));  // (no clobber: all of a row's are on their way together)
+  return v;
+}
+// Part j (16 bytes) of row r of the 128 x 128 fp32 sums: the parts of a row swapped by the row,
+// so that a row a thread and a row a warp both pass without bank conflicts.
+__device__ __forceinline__ uint32_t sum_part(uint32_t at, int r, int j) {
+  return at + static_cast<uint32_t>(r * 512 + ((j ^ (r & 31)) << 4));
+}
+
+template <int CG, int KIND, bool TWO, bool SPLIT>
 __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constant__ OrthoGemm g) {
   extern __shared__ uint8_t ortho_smem[];
   constexpr bool PAIR = CG == 2;
+  static_assert(PAIR || !SPLIT, "pairs share K");
   constexpr bool Q_MN = KIND != ORTHO_SYM;
   constexpr int TILE = 128 * CG;  // rows and columns of a tile
   constexpr uint32_t IDESC = IDESC_FP16<TILE, Q_MN>;
@@ -174,9 +191,10 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
   auto bar_s = [&](int i) { return smem_u32(bar + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const uint32_t in_cluster = PAIR ? cluster_ctarank() : 0u;
+  const uint32_t rank = in_cluster & 1u, pair = in_cluster >> 1;  // of the pair; which pair
   const bool leader = rank == 0;
-  auto lead = [&](uint32_t local) { return PAIR ? mapa_shared(local, 0) : local; };
+  auto lead = [&](uint32_t local) { return PAIR ? mapa_shared(local, 2 * pair) : local; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < OSTAGES; ++i) {
@@ -210,10 +228,15 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
   pdl_launch_dependents();
 
   const uint64_t lim = g.timeout_ns;
-  const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+  constexpr int CTAS = SPLIT ? 2 * CG : CG;  // of a unit
+  const int first = static_cast<int>(blockIdx.x) / CTAS, step = static_cast<int>(gridDim.x) / CTAS;
   constexpr int segs = TWO ? 3 : 1;
-  const int kb_all = g.kblocks * segs;
-  const int chunks = TWO ? chunks_of<KIND>(g) : 1;
+  // this pair's k-blocks
+  const int half = (g.kblocks + 1) / 2;
+  const int kb0 = SPLIT && pair ? half : 0;
+  const int kb_len = !SPLIT ? g.kblocks : pair ? g.kblocks - half : half;
+  const int kb_all = kb_len * segs;
+  const int chunks = TWO ? chunks_of<KIND>(kb_len) : 1;
   int acc = 0;  // of the next chunk (or unit), in its readers and its writer alike
   uint32_t aphase = 0;
   auto next_acc = [&] {
@@ -249,7 +272,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
           }
           const uint32_t full = full0 + 8u * stage, s = base + stage * OSTAGE;
           if (leader) mbar_expect_tx(bar_s(FULL + stage), CG * OSTAGE);
-          const int k0 = kb * 64;
+          const int k0 = (kb0 + kb) * 64;
           // the terms' depths: hi lo, lo hi, hi hi.  (The accumulator truncates at every
           // instruction, by more the larger its sum: the small products come first.)
           const int zp = t.b + (segs == 3 && seg == 1 ? g.batch : 0);
@@ -262,7 +285,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
             load(s + OPERAND, &g.q, k0, n0, zq, full);
           }
           ++issued;
-          if (++kb == g.kblocks) { kb = 0; ++seg; }
+          if (++kb == kb_len) { kb = 0; ++seg; }
           if (++stage == OSTAGES) { stage = 0; phase ^= 1u; }
         }
       }
@@ -280,6 +303,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       }
     }
   } else if (warp == 1) {
+    const uint16_t both = static_cast<uint16_t>(3u << (2 * pair));  // CTAs of the pair
     if (lane == 0 && leader) {
       int stage = 0;
       uint32_t phase = 0;
@@ -292,7 +316,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
           tc_fence_after();
           const uint32_t d = tmem + acc * TILE;
           const int begin = i;
-          for (const int end = TWO ? chunk_end<KIND>(g, c) : kb_all; i < end; ++i) {
+          for (const int end = TWO ? chunk_end<KIND>(kb_len, c) : kb_all; i < end; ++i) {
             ok = mbar_wait<PAIR>(bar_s(FULL + stage), phase, lim, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -306,12 +330,12 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
               else tc_mma_bf16(d, pd, qd, IDESC, i > begin || k > 0);
             }
             any = true;
-            if constexpr (PAIR) tc_commit_pair(bar_s(EMPTY + stage), 3);
+            if constexpr (PAIR) tc_commit_pair(bar_s(EMPTY + stage), both);
             else tc_commit(bar_s(EMPTY + stage));
             if (++stage == OSTAGES) { stage = 0; phase ^= 1u; }
           }
           if (!ok) break;
-          if constexpr (PAIR) tc_commit_pair(bar_s(TFULL + acc), 3);
+          if constexpr (PAIR) tc_commit_pair(bar_s(TFULL + acc), both);
           else tc_commit(bar_s(TFULL + acc));
           next_acc();
         }
@@ -319,7 +343,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       if (!ok) {
         failed();
         if (any) {  // the MMAs already issued end before TMEM is freed
-          if constexpr (PAIR) tc_commit_pair(bar_s(DRAIN), 1);
+          if constexpr (PAIR) tc_commit_pair(bar_s(DRAIN), both & 0x5);
           else tc_commit(bar_s(DRAIN));
           volatile int never = 0;
           mbar_wait<PAIR>(bar_s(DRAIN), 0, 10000000ull, &never);
@@ -330,7 +354,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       // cluster scope, from a thread that has no stores of its own to wait for
       bool ok = true;
       for (int unit = first; ok && unit < g.units; unit += step)
-        for (int c = 0; ok && c < chunks; ++c) {
+        for (int c = 0; ok && c < (SPLIT ? chunks - 1 : chunks); ++c) {  // (no unit follows)
           ok = mbar_wait(bar_s(TEMPTY + acc), aphase, lim, abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -362,6 +386,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
       // strips of 32 columns inside the output
       int strips = row0 < g.M ? (g.N - col0 + 31) / 32 : 0;
       strips = strips < 0 ? 0 : strips < WIDTH / 32 ? strips : WIDTH / 32;
+      if (SPLIT && part != static_cast<int>(pair)) strips = 0;  // the other pair's columns
       // `in` of strip c into set c & 1, once what that held has been stored
       auto load = [&](int c) {
         const int s = c & 1;
@@ -420,6 +445,23 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
           tmem_wait_st();
         }
       }
+      if constexpr (SPLIT) {  // (the ring is free: the pair's last MMA is done)
+        if (ok && part != static_cast<int>(pair)) {
+#pragma unroll 1
+          for (int col = 0; col < WIDTH; col += 32) {
+            uint32_t a[32];
+            __syncwarp();
+            tmem_ld32(tb + col, a);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(sum_part(base, q * 32 + lane, col / 4 + j), a[4 * j], a[4 * j + 1],
+                           a[4 * j + 2], a[4 * j + 3]);
+          }
+        }
+        __syncwarp();
+        cluster_sync();
+      }
       if (!ok) {
         failed();
         break;
@@ -435,8 +477,21 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
           tmem_ld32(tb + 32 * c, a);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = g.beta * __uint_as_float(a[i]);
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
         }
+        if constexpr (SPLIT) {  // the other pair's sums of these columns
+          float4 o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = ld_cluster_f4(mapa_shared(sum_part(base, q * 32 + lane, 8 * c + j), in_cluster ^ 2u));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[4 * j] += o[j].x, v[4 * j + 1] += o[j].y;
+            v[4 * j + 2] += o[j].z, v[4 * j + 3] += o[j].w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= g.beta;
         if (has_in) {
           if (!mbar_wait(in_bar + 8 * s, in_phase >> s & 1u, lim, abort_flag)) {
             ok = false;
@@ -536,6 +591,12 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     __syncwarp();
   }
 
+  if constexpr (SPLIT) {
+    if (warp < 2) {  // (the epilogue's barrier)
+      __syncwarp();
+      cluster_sync();
+    }
+  }
   tc_fence_before();
   if constexpr (PAIR) cluster_sync();  // no remote arrival or copy may target an exited CTA
   else __syncthreads();
@@ -576,13 +637,6 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));  // (no clobber: all of a row's are on their way together)
-  return v;
-}
 // The sum of eight columns of a row over the shared memories of the first N CTAs, in their order;
 // x, y: the parts' addresses in each.
 template <int N>
@@ -598,11 +652,6 @@ __device__ __forceinline__ void cluster_sums(uint32_t x, uint32_t y, float (&f)[
     f[0] += u[s].x, f[1] += u[s].y, f[2] += u[s].z, f[3] += u[s].w;
     f[4] += v[s].x, f[5] += v[s].y, f[6] += v[s].z, f[7] += v[s].w;
   }
-}
-// Part j (16 bytes) of row r of the 128 x 128 fp32 sums: the parts of a row swapped by the row,
-// so that a row a thread and a row a warp both pass without bank conflicts.
-__device__ __forceinline__ uint32_t sum_part(uint32_t at, int r, int j) {
-  return at + static_cast<uint32_t>(r * 512 + ((j ^ (r & 31)) << 4));
 }
 // Stores the terms of eight consecutive values (of D, or of its mirror image).
 __device__ __forceinline__ void store_terms(const OrthoGemm& g, size_t at, size_t term, bool two,
@@ -895,9 +944,9 @@ cudaError_t launch_split(const OrthoGemm& g, int share, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, g);
 }
 
-template <int CG, int KIND, bool TWO>
+template <int CG, int KIND, bool TWO, bool SPLIT = false>
 cudaError_t prepare() {
-  auto kern = k_ortho_gemm<CG, KIND, TWO>;
+  auto kern = k_ortho_gemm<CG, KIND, TWO, SPLIT>;
   static std::atomic<unsigned long long> done{0};  // devices that have the attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -908,30 +957,34 @@ cudaError_t prepare() {
   return e;
 }
 
-template <int CG, int KIND, bool TWO>
+template <int CG, int KIND, bool TWO, bool SPLIT = false>
 int clusters() {
+  constexpr int CTAS = SPLIT ? 2 * CG : CG;
   int dev = 0, sms = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   static std::atomic<int> cache[64];
   if (dev < 64 && cache[dev].load() > 0) return cache[dev].load();
+  if (prepare<CG, KIND, TWO, SPLIT>() != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = ortho_config(CG, sms / CG * CG, nullptr, attr);
+  cudaLaunchConfig_t cfg = ortho_config(CTAS, sms / CTAS * CTAS, nullptr, attr);
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_ortho_gemm<CG, KIND, TWO>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k_ortho_gemm<CG, KIND, TWO, SPLIT>, &cfg) != cudaSuccess) return 0;
   if (dev < 64) cache[dev].store(n);
   return n;
 }
 
-template <int CG, int KIND, bool TWO>
+template <int CG, int KIND, bool TWO, bool SPLIT = false>
 cudaError_t launch_of(const OrthoGemm& g, cudaStream_t stream) {
-  const cudaError_t e = prepare<CG, KIND, TWO>();
+  const cudaError_t e = prepare<CG, KIND, TWO, SPLIT>();
   if (e != cudaSuccess) return e;
-  const int n = clusters<CG, KIND, TWO>();
+  const int n = clusters<CG, KIND, TWO, SPLIT>();
   if (n <= 0) return cudaErrorUnknown;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = ortho_config(CG, CG * (g.units < n ? g.units : n), stream, attr);
-  return cudaLaunchKernelEx(&cfg, k_ortho_gemm<CG, KIND, TWO>, g);
+  constexpr int CTAS = SPLIT ? 2 * CG : CG;
+  const int grid = SPLIT || g.units < n ? g.units : n;  // (split: a unit a cluster)
+  cudaLaunchConfig_t cfg = ortho_config(CTAS, CTAS * grid, stream, attr);
+  return cudaLaunchKernelEx(&cfg, k_ortho_gemm<CG, KIND, TWO, SPLIT>, g);
 }
 
 // ------------------------------------------------------------- norm and scale
@@ -1080,6 +1133,12 @@ cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, OrthoKind kind, cudaSt
     default: return of(std::integral_constant<int, ORTHO_LAST>{});
   }
 }
+
+cudaError_t launch_ortho_pairs(const OrthoGemm& g, cudaStream_t stream) {
+  return g.terms == 2 ? launch_of<2, ORTHO_SYM, true, true>(g, stream)
+                      : launch_of<2, ORTHO_SYM, false, true>(g, stream);
+}
+int ortho_pairs_clusters() { return clusters<2, ORTHO_SYM, true, true>(); }
 
 cudaError_t launch_ortho_split(const OrthoGemm& g, int share, OrthoKind kind, cudaStream_t stream) {
   switch (kind) {

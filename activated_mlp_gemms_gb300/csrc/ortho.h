@@ -41,6 +41,10 @@ struct OrthoGemm {
 };
 // cg 2: CTA pairs, 256 x 256 tiles; 1: single CTAs, 128 x 128 tiles.
 cudaError_t launch_ortho_gemm(const OrthoGemm& g, int cg, OrthoKind kind, cudaStream_t stream);
+// 256 x 256 tiles of a symmetric product, the k-blocks (at least two) shared by two CTA pairs; how
+// many of their clusters are resident together (0: not known).
+cudaError_t launch_ortho_pairs(const OrthoGemm& g, cudaStream_t stream);
+int ortho_pairs_clusters();
 // 128 x 128 tiles whose k-blocks are shared by clusters of `share` CTAs (2, 4 or 8, at most
 // half of the k-blocks).
 cudaError_t launch_ortho_split(const OrthoGemm& g, int share, OrthoKind kind, cudaStream_t stream);

@@ -80,17 +80,30 @@ int pick(const OrthoGemm& g, bool sym) {
 // the sums.  Measured (1 / 2 / 4 / 8 CTAs, us of an X X^T with 5 of event time): 64 x 1024 10 / 12 /
 // 12 / 12, 64 x 2048 16 / 14 / 12 / 13, 64 x 4096 24 / 18 / 14 / 14, 256 x 14336 65 / 43 / 27 / 20,
 // 1024 x 2048 16 / 18 / 16 / 35 (more CTAs than SMs).
+double share_us(int share, int kblocks, int products) {
+  return 0.27 * products * ((kblocks + share - 1) / share) + (share > 1 ? 3.2 + 0.3 * share : 0.);
+}
 int pick_share(int units, int kblocks, int products) {
   int best = 1;
-  double least = 0.27 * products * kblocks;
-  for (int share = 2; share <= 8 && units * share <= 144; share *= 2) {
-    const double us = 0.27 * products * ((kblocks + share - 1) / share) + 3.2 + 0.3 * share;
-    if (us < least) {
-      least = us;
-      best = share;
-    }
-  }
+  for (int share = 2; share <= 8 && units * share <= 144; share *= 2)
+    if (share_us(share, kblocks, products) < share_us(best, kblocks, products)) best = share;
   return best;
+}
+
+// Whether two CTA pairs share the k-blocks of a symmetric product's 256 x 256 tiles: these are
+// too few for the GPU's pairs, and singles with their 128 x 128 ones load twice as much for a
+// flop.  At most one wave of such clusters (36 on this GPU); 0.14 us a k-block and 12 for the
+// cluster's launch and the exchange of half a tile's sums, with three products 0.2 and 5 (the
+// singles' own epilogues are longer, too).  Measured (pairs / singles or clusters of them, us of
+// an X X^T with 5 of event time): 2048 x 14336 51 / 69, 1536 x 8192 35 / 43, 2048 x 4864 31 / 29,
+// 1024 x 4096 25 / 17; for an fp32 result 145 / 201, 80 / 117, 57 / 75, 49 / 26; 2048 x 2048 37 / 37.
+bool share_pairs(const OrthoGemm& g) {
+  if (g_tile_policy.load() != 0 || g.kblocks < 2) return false;
+  const long long t = (g.M + 255) / 256, s = (g.M + 127) / 128;
+  if (t * (t + 1) / 2 * g.batch > ortho_pairs_clusters()) return false;
+  const int products = g.terms == 2 ? 3 : 1, units = static_cast<int>(s * (s + 1) / 2) * g.batch;
+  const double us = products == 3 ? 0.6 * g.kblocks + 5 : 0.14 * g.kblocks + 12;
+  return us < share_us(pick_share(units, g.kblocks, products), g.kblocks, products);
 }
 
 // Columns a CTA where the whole call runs on one cluster a matrix (0: it does not): what fits
@@ -143,6 +156,11 @@ struct Products {
   int run(OrthoGemm& g, OrthoKind kind, int tag) {
     if (!ok) return MLP_ERR_CUDA;
     const bool sym = kind == ORTHO_SYM;
+    if (sym && share_pairs(g)) {
+      g.tiles_m = g.tiles_n = (g.M + 255) / 256;
+      g.units = g.tiles_m * (g.tiles_m + 1) / 2 * g.batch;
+      return traced(tag, stream, [&] { return launch_ortho_pairs(g, stream); });
+    }
     const int cg = pick(g, sym), tile = 128 * cg;
     g.tiles_m = (g.M + tile - 1) / tile;
     g.tiles_n = (g.N + tile - 1) / tile;

@@ -259,3 +259,29 @@ def test_bounded_waits():
             m.mlp_set_wait_timeout_ms(0)
             m.mlp_set_tile_policy(0)
         assert torch.equal(run(G), want)
+
+
+@pytest.mark.parametrize("batch,rows,cols,out_dtype", [
+    (1, 1536, 8200, BF), (1, 8200, 1288, BF), (1, 2048, 4872, F32), (1, 1544, 2568, F32),
+    (3, 1000, 4104, F32), (2, 1032, 14336, BF)])
+def test_long_rows_shared_by_pairs(batch, rows, cols, out_dtype):
+    """X X^T of few large tiles over a long K (two CTA pairs a tile), odd halves of it too."""
+    G = make(batch, rows, cols, dtype=BF if out_dtype == BF else F32)
+    got = check(G, out_dtype)
+    assert torch.equal(got, run(G, out_dtype))
+
+
+def test_bounded_waits_of_pairs():
+    G = make(1536, 8192, dtype=BF)
+    want = run(G)
+    out = torch.empty_like(want)
+    m.mlp_set_wait_timeout_ms(20)
+    m.mlp_debug_set_flags(m.DEBUG_NO_WORK)
+    try:
+        p = m.ortho(1536, 8192)
+        ws = m.mlp_orthogonalize(p, G, out, ws=m.alloc_ortho_workspace(p))
+        assert m.mlp_device_status(ws) == -6
+    finally:
+        m.mlp_debug_set_flags(0)
+        m.mlp_set_wait_timeout_ms(0)
+    assert torch.equal(run(G), want)
