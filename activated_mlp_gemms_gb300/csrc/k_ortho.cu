@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
   auto bar_s = [&](int i) { return smem_u32(bar + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t in_cluster = PAIR ? cluster_ctarank() : 0u;
-  const uint32_t rank = in_cluster & 1u, pair = in_cluster >> 1;  // of the pair; which pair
+  // the CTA of its pair, and which pair
+  const uint32_t rank = SPLIT ? in_cluster & 1u : in_cluster, pair = SPLIT ? in_cluster >> 1 : 0u;
   const bool leader = rank == 0;
   auto lead = [&](uint32_t local) { return PAIR ? mapa_shared(local, 2 * pair) : local; };
 
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
   constexpr int segs = TWO ? 3 : 1;
   // this pair's k-blocks
   const int half = (g.kblocks + 1) / 2;
-  const int kb0 = SPLIT && pair ? half : 0;
+  const int kb0 = pair ? half : 0;
   const int kb_len = !SPLIT ? g.kblocks : pair ? g.kblocks - half : half;
   const int kb_all = kb_len * segs;
   const int chunks = TWO ? chunks_of<KIND>(kb_len) : 1;
