@@ -85,8 +85,8 @@ template <int KIND>
 __device__ __forceinline__ Tile tile_of(const OrthoGemm& g, int unit) {
   Tile t;
   const int per = g.units / g.batch;
-  t.b = unit / per;
-  const int u = unit - t.b * per;
+  const int b = unit / per, u = unit - b * per;
+  t.b = g.backwards ? g.batch - 1 - b : b;
   if (KIND == ORTHO_SYM) {  // row tm of the triangle begins at tm (tm + 1) / 2
     t.tm = static_cast<int>((sqrtf(8.f * static_cast<float>(u) + 1.f) - 1.f) * 0.5f);
     while (t.tm * (t.tm + 1) / 2 > u) --t.tm;
@@ -1048,7 +1048,8 @@ __global__ void __launch_bounds__(256)
   __shared__ float factor_s;
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.z;
+  // (from the end, which the norm's reads have left in L2)
+  const int b = static_cast<int>(gridDim.z - 1 - blockIdx.z);
   if (threadIdx.x < 32) {
     const float* p = part + b * ORTHO_PARTS;
     float s = 0.f;
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(256)
   const size_t size = static_cast<size_t>(rows < cols ? rows : cols) * pitch;
   __half* hi = X + b * size;
   __half* lo = hi + static_cast<size_t>(batch) * size;
-  const int r0 = static_cast<int>(blockIdx.y) * 64, c0 = static_cast<int>(blockIdx.x) * 64;
+  const int r0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * 64, c0 = static_cast<int>(blockIdx.x) * 64;
   const bool transposed = rows > cols;
   __syncthreads();
   const float factor = factor_s;

@@ -35,6 +35,7 @@ struct OrthoGemm {
   int tiles_m, tiles_n, units;
   float alpha, beta;  // alpha 0: no `in`
   int out_bf16, transposed;
+  int backwards;  // the stack from its last matrix to its first
   int* status;
   unsigned long long timeout_ns;
   int debug_flags;

@@ -127,6 +127,9 @@ struct Products {
   cudaStream_t stream;
   int* status;
   bool ok = true;
+  // Each product walks over the stack against the one before it, whose last results are still in
+  // L2.
+  bool backwards = false;
 
   // A stack [depth, rows, cols] of fp16 (or bf16, fp32) matrices in boxes {c, r}.
   CUtensorMap map(const void* ptr, int depth, int rows, int cols, int pitch, int c, int r,
@@ -156,6 +159,8 @@ struct Products {
   int run(OrthoGemm& g, OrthoKind kind, int tag) {
     if (!ok) return MLP_ERR_CUDA;
     const bool sym = kind == ORTHO_SYM;
+    g.backwards = backwards;
+    backwards = !backwards;
     if (sym && share_pairs(g)) {
       g.tiles_m = g.tiles_n = (g.M + 255) / 256;
       g.units = g.tiles_m * (g.tiles_m + 1) / 2 * g.batch;
