@@ -22,7 +22,7 @@
 //              (sixteen warps with a set each were no faster: 16 x 1408 x 2048 step 122 us, 118
 //              so; a unit's k-blocks draw 12 TB/s of L2, and that is what `in` and D wait for)
 // The tensor cores truncate their accumulator at every instruction, by about half of its last bit:
-// over a long K an fp32 result would lose two digits by it (4864: 3e-5, now 4e-6).  With both
+// over a long K an fp32 result would lose a digit by it (4864: 3e-5, now 5e-6).  With both
 // terms the leading products therefore come in chunks of CHUNK k-blocks, whose sums the epilogue's
 // warps add up in fp32, rounded to nearest, in registers.
 // With SPLIT a unit of a symmetric product has a cluster of two pairs, each with half of its
@@ -61,9 +61,8 @@ constexpr uint32_t IDESC_FP16 = (1u << 4) | ((Q_MN ? 1u : 0u) << 16) |
                                 (static_cast<uint32_t>(TILE >> 3) << 17) |
                                 (static_cast<uint32_t>(TILE >> 4) << 24);
 
-// (X X^T: half as long, its error is stretched by two more products.  4864 x 2048 with chunks of
-// 8 everywhere: off by 1.0e-5, 579 us a call of three steps; of 4 in X X^T: 5.9e-6, 585; of 4
-// everywhere: 5.5e-6, 621.)
+// (X X^T: half as long, its error is stretched by two more products.  4864 x 2048, five steps: off
+// by 4.7e-6, 938 us; with chunks of 2 and 4: 2.6e-6, 982.)
 template <int KIND>
 constexpr int CHUNK = KIND == ORTHO_SYM ? 4 : 8;
 // Chunks of a unit's k-blocks, and where chunk c ends: the small products (hi lo, lo hi) belong
