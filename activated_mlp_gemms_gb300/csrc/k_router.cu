@@ -574,14 +574,15 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
     total = group_sum<G>(total);
     const float inv = routed ? reciprocal(total) : 0.f;
     // what the weights' gradient adds at the chosen experts: w (dw - <w, dw>), or p dw of
-    // p (dw - <p, dw>)
+    // p (dw - <p, dw>).  (A caller's own ids may all be of experts whose exponentials vanish:
+    // their sum is kept from zero, and nothing is added.)
     float add = 0.f, dot = 0.f, w_inv = 1.f, w_dot = 0.f;
     if (slots && one) {
       const float e = id >= 0 ? buf[id] : 0.f;
       if (a.renorm) {
         const float s = group_sum<G>(e);
         const float d = group_sum<G>(id >= 0 ? e * dw : 0.f);
-        const float r = reciprocal(s);
+        const float r = reciprocal(fmaxf(s, FLT_MIN));
         if (id >= 0) add = e * r * (dw - d * r);
       } else if (id >= 0) {
         add = dot = e * inv * dw;
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
         d += buf[i] * dw_at(t * k + j);
       }
       if (a.renorm) {
-        w_inv = reciprocal(group_sum<G>(s));
+        w_inv = reciprocal(fmaxf(group_sum<G>(s), FLT_MIN));
         w_dot = group_sum<G>(d) * w_inv;
       } else {
         w_inv = inv;

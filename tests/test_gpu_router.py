@@ -362,3 +362,15 @@ def test_a_nan_of_either_sign():
         ids, w, *_ = run(x, 4)
         assert ids[2, 0] == 77 and w[2].isnan().all()
         assert w[[0, 1, 3, 4]].isfinite().all()
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (256, 2), (64, 20)])
+def test_ids_of_experts_that_vanish(E, k):
+    """A caller's own choice of experts 200 below the largest: no gradient, and no NaN."""
+    x = make(9, E, F32, 81)
+    x[:, -1] = 250
+    ids = torch.arange(k, dtype=torch.int32, device="cuda").expand(9, k).contiguous()
+    dl = torch.full((9, E), 7.0, device="cuda")
+    m.mlp_moe_router_bwd(m.router(9, E, k), x, None, ids, None,
+                         torch.ones(9, k, device="cuda"), None, dl)
+    assert not dl.any()

@@ -3,7 +3,10 @@ threads of their own, captured with their gradients, and with results changed in
 
 A row's results (a matrix's) do not depend on the rows beside it, so that the last ones of a
 large call are those of a small call on them alone."""
+import subprocess
+import sys
 import threading
+from pathlib import Path
 
 import pytest
 import torch
@@ -188,3 +191,34 @@ def test_results_changed_in_place():
     loss += 2 * w.square().sum()
     got, = torch.autograd.grad(loss, [x])
     assert torch.equal(got, want)
+
+
+FIRST_CALLS = """
+import torch, activated_mlp_gemms_gb300 as m
+torch.manual_seed(0)
+l, x = torch.randn(3000, 60, device="cuda"), torch.randn(700, 2048, device="cuda").bfloat16()
+Gs = [torch.randn(*s, device="cuda") for s in ((64, 512), (520, 264), (1536, 4096), (2, 1032, 1024))]
+def calls():
+    r = list(m.router_func(l, 4)) + [m.layer_norm_func(x)]
+    for G in Gs:
+        for t in (torch.bfloat16, torch.float32):
+            o = torch.empty_like(G, dtype=t)
+            p = m.ortho(*G.shape[-2:], G.shape[0] if G.dim() == 3 else 1, dtype=G.dtype, out_dtype=t)
+            m.mlp_orthogonalize(p, G, o)
+            r.append(o)
+    return r
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, calls()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """What is set up once (attributes, occupancies) may be set up while a graph is captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True,
+                       timeout=300, cwd=Path(__file__).resolve().parent.parent)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
