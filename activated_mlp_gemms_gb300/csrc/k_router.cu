@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(FINISH_THREADS)
 }
 
 template <typename L, int G, int V>
-__global__ void __launch_bounds__(ROUTER_THREADS)
+__global__ void __launch_bounds__(ROUTER_THREADS, V <= 8 ? 0 : V <= 16 ? 4 : 3)
     k_router_bwd(const RouterArgs a, const int* __restrict__ ids,
                  const float* __restrict__ balance, const void* __restrict__ dweights,
                  const float* __restrict__ dloss, void* dlogits, const bool vec, const bool vec_d) {
@@ -519,22 +519,37 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
   };
   pdl_wait();
   pdl_launch_dependents();
-  float coef[V];
+  // The loss's gradient by each expert's probability: in registers up to 256 experts, and the
+  // next token's operands, too.  Above, more blocks an SM are worth more: 32768 x 1024 bf16 115 us
+  // so, now 57, 65536 x 512 68 and 49; but 131072 x 256 fp32 57 without them, 48 with.
+  constexpr bool ROOM = V <= 8;
+  float kept[ROOM ? V : 1];
+  float* coef_s = router_smem + NG * (G * V);
   {
     const float d = dloss ? *dloss : 0.f;
+    if constexpr (ROOM) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = R::at(lane, v);
-      coef[v] = dloss && e < E ? balance[1 + e] * d : 0.f;
+      for (int v = 0; v < V; ++v) {
+        const int e = R::at(lane, v);
+        kept[v] = dloss && e < E ? balance[1 + e] * d : 0.f;
+      }
+    } else {
+      for (int e = tid; e < G * V; e += ROUTER_THREADS)
+        coef_s[e] = dloss && e < E ? balance[1 + e] * d : 0.f;
+      __syncthreads();
     }
   }
+  auto coefs = [&](int v) {  // four of them from v
+    if constexpr (ROOM) return make_float4(kept[v], kept[v + 1], kept[v + 2], kept[v + 3]);
+    else return *reinterpret_cast<const float4*>(coef_s + R::at(lane, v));
+  };
   const bool slots = dweights != nullptr;
   const bool one = k <= G;  // a slot a lane
   auto dw_at = [&](long long i) {
     return a.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(dweights)[i])
                     : static_cast<const float*>(dweights)[i];
   };
-  // a token's operands are loaded while the one before it is worked on
+  // (with ROOM a token's are loaded while the one before it is worked on)
   float next_x[V], next_dw = 0.f;
   int next_id = -1;
   auto fetch = [&](long long t) {
@@ -552,15 +567,16 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
     }
   };
   const long long step = static_cast<long long>(gridDim.x) * NG;
-  fetch(static_cast<long long>(blockIdx.x) * NG + g);
+  if (ROOM) fetch(static_cast<long long>(blockIdx.x) * NG + g);
   for (long long base = static_cast<long long>(blockIdx.x) * NG; base < a.T; base += step) {
     const long long t = base + g;
+    if (!ROOM) fetch(t);
     float x[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) x[v] = next_x[v];
     int id = next_id;
     const float dw = next_dw;
-    fetch(t + step);
+    if (ROOM) fetch(t + step);
     float m = x[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = max_nan(m, x[v]);
@@ -604,13 +620,23 @@ __global__ void __launch_bounds__(ROUTER_THREADS)
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      x[v] *= inv;
-      dot += x[v] * coef[v];
+    for (int v = 0; v < V; v += 4) {
+      const float4 c = coefs(v);
+      const float cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[v + j] *= inv;
+        dot += x[v + j] * cs[j];
+      }
     }
     dot = group_sum<G>(dot);
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] *= coef[v] - dot;
+    for (int v = 0; v < V; v += 4) {
+      const float4 c = coefs(v);
+      const float cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[v + j] *= cs[j] - dot;
+    }
     if (slots) {
       if (one) {
         __syncwarp();  // (the exponentials have been read)
@@ -769,7 +795,7 @@ cudaError_t launch_router_bwd(const RouterArgs& a, const int* ids, const float* 
   return by_experts_bwd(a.E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config(blocks, ROUTER_THREADS * V * 4ull, stream, attr);
+    cudaLaunchConfig_t cfg = config(blocks, (ROUTER_THREADS * V + (V > 8 ? G * V : 0)) * 4ull, stream, attr);
     auto go = [&](auto kern) {
       return cudaLaunchKernelEx(&cfg, kern, a, ids, balance, dweights, dloss, dlogits, vec, vec_d);
     };
