@@ -14,6 +14,8 @@
 // fp32 46 (5.8) and 66 (6.1).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "gemm_params.h"
 #include "ptx.cuh"
 #include "step.h"
@@ -521,14 +523,20 @@ __global__ void __launch_bounds__(32 * SUM_ROWS)
   else static_cast<float*>(out)[mine] = t;
 }
 
-template <typename T, class F>
+// A row of 129 to 256 pieces has 128 threads of two, so that an SM has five or six rows under way;
+// ONE a thread is faster for bf16 with a residual in the forward alone (16384 x 2048 bf16, one /
+// two pieces: 45 / 52 us; without a residual 32 / 26, the backward 59 / 50, with dh 63 / 62; 32768
+// x 1024 fp32 54 / 49, with a residual 93 / 88, the backward 89 / 68).
+template <typename T, bool ONE, class F>
 auto by_width(int H, F&& f) {
   const int pieces = H / Piece<T>::C;
 #define MLP_NORM_LAYOUT(WARP, NP) return f(Layout<T, WARP, NP>{}, std::integral_constant<bool, WARP>{}, std::integral_constant<int, NP>{})
   if (pieces <= 32) MLP_NORM_LAYOUT(true, 1);
   if (pieces <= 64) MLP_NORM_LAYOUT(true, 2);
   if (pieces <= 128) MLP_NORM_LAYOUT(true, 4);
-  if (pieces <= 256) MLP_NORM_LAYOUT(false, 1);
+  if constexpr (ONE) {
+    if (pieces <= 256) MLP_NORM_LAYOUT(false, 1);
+  }
   if (pieces <= 2 * Layout<T, false, 2>::THREADS) MLP_NORM_LAYOUT(false, 2);
   if constexpr (sizeof(T) == 4) {
     if (pieces > 2048) MLP_NORM_LAYOUT(false, 8);
@@ -540,9 +548,9 @@ struct Shape {
   int rows, threads, columns;  // of a block; of a thread
   size_t ahead;                // bytes of one array's rows under way in a block
 };
-template <typename T>
+template <typename T, bool ONE = false>
 Shape shape_of(int H) {
-  return by_width<T>(H, [&](auto lay, auto warp, auto np) {
+  return by_width<T, ONE>(H, [&](auto lay, auto warp, auto np) {
     constexpr int NP = decltype(np)::value;
     const int threads =
         decltype(warp)::value ? 256 : ((H / Piece<T>::C + NP - 1) / NP + 31) / 32 * 32;
@@ -573,30 +581,28 @@ cudaLaunchConfig_t config(dim3 blocks, int threads, cudaStream_t stream,
   return cfg;
 }
 
-template <typename T>
+template <typename T, bool RESIDUAL>
 cudaError_t fwd_of(const NormArgs& a, const void* x, const void* residual, const void* weight,
                    const void* bias, void* y, void* h, float* mean, float* rstd,
                    cudaStream_t stream) {
-  const Shape p = shape_of<T>(a.H);
-  const int arrays = residual ? 2 : 1;
+  constexpr bool ONE = RESIDUAL && sizeof(T) == 2;
+  const Shape p = shape_of<T, ONE>(a.H);
+  const int arrays = RESIDUAL ? 2 : 1;
   const int all = (a.M - 1) / p.rows + 1;
   // (registers: up to 80 a thread for 8 columns, 102 for 16)
   const int most = 152 * sm_blocks(p, arrays, p.columns <= 8 ? 768 : 640);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(dim3(all < most ? all : most), p.threads, stream, attr);
   cfg.dynamicSmemBytes = arrays * p.ahead;
-  return by_width<T>(a.H, [&](auto, auto warp, auto np) {
+  return by_width<T, ONE>(a.H, [&](auto, auto warp, auto np) {
     constexpr bool WARP = decltype(warp)::value;
     constexpr int NP = decltype(np)::value;
-    auto go = [&](auto kern) {
-      const cudaError_t e = kern.allow_smem(NORM_SMEM);
-      if (e != cudaSuccess) return e;
-      return cudaLaunchKernelEx(&cfg, kern.kernel, a, static_cast<const T*>(x),
-                                static_cast<const T*>(residual), weight, bias, static_cast<T*>(y),
-                                static_cast<T*>(h), mean, rstd);
-    };
-    return residual ? go(KernelOf<k_layernorm_fwd<T, WARP, NP, true>>{})
-                    : go(KernelOf<k_layernorm_fwd<T, WARP, NP, false>>{});
+    using Kernel = KernelOf<k_layernorm_fwd<T, WARP, NP, RESIDUAL>>;
+    const cudaError_t e = Kernel::allow_smem(NORM_SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, Kernel::kernel, a, static_cast<const T*>(x),
+                              static_cast<const T*>(residual), weight, bias, static_cast<T*>(y),
+                              static_cast<T*>(h), mean, rstd);
   });
 }
 
@@ -609,7 +615,7 @@ cudaError_t bwd_of(const NormArgs& a, const void* dy, const void* h, const void*
   cudaLaunchConfig_t cfg =
       config(dim3(layernorm_blocks(a.M, a.H, a.bf16)), p.threads, stream, attr);
   cfg.dynamicSmemBytes = (dh ? 3 : 2) * p.ahead;
-  return by_width<T>(a.H, [&](auto, auto warp, auto np) {
+  return by_width<T, false>(a.H, [&](auto, auto warp, auto np) {
     constexpr bool WARP = decltype(warp)::value;
     constexpr int NP = decltype(np)::value;
     auto go = [&](auto kern) {
@@ -639,8 +645,12 @@ int layernorm_blocks(int M, int H, bool bf16) {
 cudaError_t launch_layernorm_fwd(const NormArgs& a, const void* x, const void* residual,
                                  const void* weight, const void* bias, void* y, void* h,
                                  float* mean, float* rstd, cudaStream_t stream) {
-  return a.bf16 ? fwd_of<__nv_bfloat16>(a, x, residual, weight, bias, y, h, mean, rstd, stream)
-                : fwd_of<float>(a, x, residual, weight, bias, y, h, mean, rstd, stream);
+  auto go = [&](auto type, auto has) {
+    return fwd_of<decltype(type), decltype(has)::value>(a, x, residual, weight, bias, y, h, mean,
+                                                        rstd, stream);
+  };
+  if (residual) return a.bf16 ? go(__nv_bfloat16{}, std::true_type{}) : go(0.f, std::true_type{});
+  return a.bf16 ? go(__nv_bfloat16{}, std::false_type{}) : go(0.f, std::false_type{});
 }
 
 cudaError_t launch_layernorm_bwd(const NormArgs& a, const void* dy, const void* h,
