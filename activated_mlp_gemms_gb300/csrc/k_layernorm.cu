@@ -177,7 +177,7 @@ struct RowSum {
   }
 };
 
-// How a row is laid out.  Up to four pieces a lane it is a warp's, and a block of 256 threads has
+// How a row is laid out.  Up to 16 columns a lane it is a warp's, and a block of 256 threads has
 // eight rows at a time; a wider one is a block's, of just the warps that it needs: NP pieces a
 // thread, so that a thread holds 8, 16 or (the widest) 32 columns.
 template <typename T, bool WARP, int NP>
@@ -526,14 +526,18 @@ __global__ void __launch_bounds__(32 * SUM_ROWS)
 // A row of 129 to 256 pieces has 128 threads of two, so that an SM has five or six rows under way;
 // ONE a thread is faster for bf16 with a residual in the forward alone (16384 x 2048 bf16, one /
 // two pieces: 45 / 52 us; without a residual 32 / 26, the backward 59 / 50, with dh 63 / 62; 32768
-// x 1024 fp32 54 / 49, with a residual 93 / 88, the backward 89 / 68).
+// x 1024 fp32 54 / 49, with a residual 93 / 88, the backward 89 / 68).  Of bf16 also a row of 65 to
+// 128 pieces, where a warp's four a lane, 32 columns, would leave no registers for the weights
+// (32768 x 1024: a warp a row 44, two warps 26; with a residual 54 / 49, the backward 70 / 51).
 template <typename T, bool ONE, class F>
 auto by_width(int H, F&& f) {
   const int pieces = H / Piece<T>::C;
 #define MLP_NORM_LAYOUT(WARP, NP) return f(Layout<T, WARP, NP>{}, std::integral_constant<bool, WARP>{}, std::integral_constant<int, NP>{})
   if (pieces <= 32) MLP_NORM_LAYOUT(true, 1);
   if (pieces <= 64) MLP_NORM_LAYOUT(true, 2);
-  if (pieces <= 128) MLP_NORM_LAYOUT(true, 4);
+  if constexpr (sizeof(T) == 4) {
+    if (pieces <= 128) MLP_NORM_LAYOUT(true, 4);
+  }
   if constexpr (ONE) {
     if (pieces <= 256) MLP_NORM_LAYOUT(false, 1);
   }
