@@ -6,10 +6,12 @@
 //   each forms P = b A + c A A for itself, and a X + P X of its columns.
 // X is the K-major operand of the first product and the MN-major one of the last: the same
 // 128-byte rows serve both.  (Arithmetic and scales as in k_ortho.cu; no sum here is long enough
-// to need its chunks.)  What bounds it is latency: three rounds of MMA, two cluster barriers and
+// to need its chunks.  But P X takes both terms of both for a bf16 result, too: its operands make
+// most of that result's error, 2.6e-3 of 64 x 512 with the leading terms, now 1.8e-3, of which
+// rounding it is 1.7e-3, for 29 -> 32 us.)  What bounds it is latency: three rounds of MMA, two cluster barriers and
 // three passes over tensor memory a step, and the exchange of A's rows, whose shared-memory
 // traffic between CTAs runs at some 10 bytes a cycle (so only the m x m that there are move).
-// Measured: 64 x 2048 43 us, of them 7 a step; 128 x 2048 76; 128 x 128, one CTA, 35.
+// Measured: 64 x 512 32 us, 64 x 1024 34, 128 x 1024 60; 64 x 2048 41, of them 7 a step.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -265,10 +267,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
   };
   // D = P Q over 16-element steps of K, step k's operands at p(k), q(k) in their first terms:
   // with two terms hi lo, lo hi, hi hi.
-  auto products = [&](uint32_t d, uint32_t idesc, int ksteps, auto&& p, int p_term, auto&& q,
-                      int q_term) {
+  auto products = [&](bool two, uint32_t d, uint32_t idesc, int ksteps, auto&& p, int p_term,
+                      auto&& q, int q_term) {
     uint32_t more = 0;
-    for (int seg = g.terms == 2 ? 0 : 2; seg < 3; ++seg)
+    for (int seg = two ? 0 : 2; seg < 3; ++seg)
       for (int k = 0; k < ksteps; ++k) {
         tc_mma_bf16(d, p(k, seg == 1 ? p_term : 0), q(k, seg == 0 ? q_term : 0), idesc, more);
         more = 1;
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
   for (int step = 0; step < g.steps; ++step) {
     // this CTA's share of A
     round([&] {
-      products(D1, IDESC<128, false>, WIDTH / 16, kmajor(base + S::X), S::TERM,
+      products(g.terms == 2, D1, IDESC<128, false>, WIDTH / 16, kmajor(base + S::X), S::TERM,
                kmajor(base + S::X), S::TERM);
     });
     if (q * 32 < g.m && part * 32 < g.m) {
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     cluster_sync();
     // P = b A + c A A
     round([&] {
-      products(D2, IDESC<128, false>, 8, kmajor(base + S::A), S::A_TERM, kmajor(base + S::A),
+      products(g.terms == 2, D2, IDESC<128, false>, 8, kmajor(base + S::A), S::A_TERM, kmajor(base + S::A),
                S::A_TERM);
     });
     {
@@ -343,14 +345,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
         if (g.terms == 2) add_term(ld_shared_v4(piece(base + S::A + S::A_TERM, row, col)), g.b, f);
         add_term(ld_shared_v4(piece(base + S::A, row, col)), g.b, f);
         put(piece(base + S::P, row, col), take_term(f));
-        if (g.terms == 2) put(piece(base + S::P + S::A_TERM, row, col), take_term(f));
+        put(piece(base + S::P + S::A_TERM, row, col), take_term(f));
       }
     }
     tc_fence_before();
     // a X + P X of my columns
     const bool last = step + 1 == g.steps;
     round([&] {
-      products(D3, IDESC<WIDTH, true>, 8, kmajor(base + S::P), S::A_TERM,
+      products(true, D3, IDESC<WIDTH, true>, 8, kmajor(base + S::P), S::A_TERM,
                [&](int k, int term) {
                  return sdesc_sw128(base + S::X + term + k * 2048, BLOCK, 1024);
                },
