@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(ctrl + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 12);
   float* norm_s = reinterpret_cast<float*>(ctrl + 16);   // a CTA's sum of squares each
+  const uint32_t drain = smem_u32(ctrl + 48);
   float* warps_s = reinterpret_cast<float*>(ctrl + 64);  // a warp's (16)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
 
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -245,19 +247,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
   for (int i = tid * 16; i < S::P - S::A; i += THREADS * 16) put(base + S::A + i, uint4{});
   // (the first remote stores to A come after the first barrier of a step)
 
-  // A round of MMA: everyone's stores, then thread 0's instructions, then their end.
+  // A round of MMA: everyone's stores, then thread 0's instructions, then their end.  Once a
+  // thread's wait has run out the CTA issues none any more, and that thread waits for none: the
+  // end of a round, should it still come, is not taken for another's.  What is left of the steps
+  // are the cluster's barriers (other CTAs' are open), over values that are not stored.
   uint32_t phase = 0;
   bool ok = true;
   auto round = [&](auto&& issue) {
     fence_proxy_async_all();
     __syncthreads();
-    if (tid == 0 && !(g.debug_flags & 1)) {  // (testing: without MMAs the wait runs out)
+    // (debug_flags: testing; without MMAs the wait runs out)
+    if (tid == 0 && !*abort_flag && !(g.debug_flags & 1)) {
       tc_fence_after();
       issue();
       tc_commit(bar);
     }
     __syncwarp();
-    if (!mbar_wait(bar, phase, g.timeout_ns, abort_flag)) {
+    if (ok && !mbar_wait(bar, phase, g.timeout_ns, abort_flag)) {
       ok = false;
       *abort_flag = 1;
       atomicExch(g.status, O_TIMEOUT);
@@ -402,6 +408,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
       }
     }
     tc_fence_before();
+  }
+  __syncthreads();
+  if (tid == 0 && *abort_flag) {  // what was issued ends before TMEM and shared memory are freed
+    tc_commit(drain);
+    volatile int never = 0;
+    mbar_wait(drain, 0, 10000000ull, &never);
   }
   __syncthreads();
   if (warp == 0) {
