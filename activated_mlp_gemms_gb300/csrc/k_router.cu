@@ -637,6 +637,10 @@ __global__ void __launch_bounds__(ROUTER_THREADS, V <= 8 ? 0 : V <= 16 ? 4 : 3)
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[v + j] *= cs[j] - dot;
     }
+    if (!routed) {  // (whatever the loss's gradient is: zeros times an infinity are none)
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = 0.f;
+    }
     if (slots) {
       if (one) {
         __syncwarp();  // (the exponentials have been read)
