@@ -488,6 +488,15 @@ def router_func(logits, top_k, mask=None, renormalize=True, weights_dtype=torch.
     return ids.view(*lead, top_k), weights.view(*lead, top_k), counts, loss
 
 
+def _aligned(t):
+    """t dense and at a multiple of 16 bytes, as the kernels read it (None stays None).  A dense
+    slice of a larger buffer may begin elsewhere, and contiguous() leaves it there."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, bias, prob, fuse_grad_accum):
@@ -498,7 +507,8 @@ class _LayerNormFunction(torch.autograd.Function):
         ctx.prob, ctx.fuse = prob, fuse_grad_accum
         ctx.set_materialize_grads(False)
         if prob.M:
-            mlp_layernorm_fwd(prob, x, residual, weight, bias, y, h, mean, rstd)
+            mlp_layernorm_fwd(prob, x, residual, _aligned(weight), _aligned(bias), y, h, mean,
+                              rstd)
         ctx.save_for_backward(x if h is None else h, weight, bias, mean, rstd)
         return y, h
 
@@ -510,8 +520,8 @@ class _LayerNormFunction(torch.autograd.Function):
         none = (None, None)
         if dy is None:  # h alone was used
             return (dh, dh if need[1] else None, None, None, *none)
-        dy = dy.to(h.dtype).contiguous()
-        dh = None if dh is None else dh.to(h.dtype).contiguous()
+        dy = _aligned(dy.to(h.dtype))  # (autograd's, a view of anything)
+        dh = None if dh is None else _aligned(dh.to(h.dtype))
         dx = torch.empty_like(dy) if need[0] or need[1] else None
         dw = _grad_like(weight, ctx.fuse, "weight") if weight is not None and need[2] else None
         db = _grad_like(bias, ctx.fuse, "bias") if bias is not None and need[3] else None
@@ -522,17 +532,17 @@ class _LayerNormFunction(torch.autograd.Function):
                         g.zero_()
         else:
             # (a row's gradient needs h dense)
-            mlp_layernorm_bwd(p, dy, h.contiguous(), weight, mean, rstd, dh, dx, dw, db,
+            mlp_layernorm_bwd(p, dy, _aligned(h), _aligned(weight), mean, rstd, dh, dx, dw, db,
                               fuse_grad_accum=ctx.fuse)
         return (dx if need[0] else None, dx if need[1] else None, None if ctx.fuse else dw,
                 None if ctx.fuse else db, *none)
 
 
 def layer_norm_func(x, weight=None, bias=None, residual=None, eps=1e-5, fuse_grad_accum=False):
-    """The layer norm over the last dimension of x (fp32 or bf16), of at most NORM_MAX_H values:
-    y = (h - mean) * rstd * weight + bias with h = x + residual.  Without a residual it returns
-    y, with one (y, h).  Differentiable with respect to x, residual, weight and bias (weight and
-    bias in one type, fp32 or bf16)."""
+    """The layer norm over the last dimension of x (fp32 or bf16), of H values, a multiple of 8
+    and at most NORM_MAX_H: y = (h - mean) * rstd * weight + bias with h = x + residual.
+    Without a residual it returns y, with one (y, h).  Differentiable with respect to x,
+    residual, weight and bias (weight and bias in one type, fp32 or bf16)."""
     for t, name in ((x, "x"), (weight, "weight"), (bias, "bias"), (residual, "residual")):
         if t is None and name != "x":
             continue
@@ -547,7 +557,7 @@ def layer_norm_func(x, weight=None, bias=None, residual=None, eps=1e-5, fuse_gra
     def rows(t):
         t = t if t.dim() == 2 else t.reshape(-1, H)
         ok = t.stride(1) == 1 and t.stride(0) >= H and t.stride(0) % 8 == 0
-        return t if ok and t.data_ptr() % 16 == 0 else t.contiguous()
+        return t if ok and t.data_ptr() % 16 == 0 else _aligned(t)
 
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
