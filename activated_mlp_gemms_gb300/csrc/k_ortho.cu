@@ -7,9 +7,9 @@
 // with them the rounding of X: in bf16 terms alone five steps leave 1-30 % of error.  Here X is
 // the sum of two fp16 terms (22 bits), so that a X carries no rounding; the products take the
 // leading terms (11 bits, the same speed as bf16), whose errors the contraction of the other
-// singular values damps: 0.2-1.7e-3 of the result over spectra from flat to 1e-4, at or below
-// the rounding of a bf16 result.  An fp32 result takes hi lo + lo hi + hi hi, as an fp32
-// product would have it (1e-5 and below).
+// singular values damps: 0.2-2.4e-3 of the result beside the 1.7e-3 of rounding it to bf16, the
+// most where the smallest singular values are a tenth of the largest (up to 128 rows P X takes both
+// terms: 1.1e-3 at most).  An fp32 result takes hi lo + lo hi + hi hi (1e-5 and below).
 //
 // The GEMM: one CTA of 320 threads an SM; CTA pairs with 256 x 256 tiles (tcgen05
 // cta_group::2), or single CTAs with 128 x 128 tiles where those are too few.
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
     const uint32_t in_bar = bar_s(IN + 2 * (warp - 2));
     const uint64_t pol = policy_evict_normal();
     fence_proxy_async_global();
-    constexpr bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && TWO);
+    const bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && g.d_terms == 2);
     constexpr bool two_in = KIND != ORTHO_SYM || TWO;
     const bool has_in = g.alpha != 0.f;
     uint32_t in_phase = 0;  // a bit a set
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
   const size_t term = d_mat * g.batch;  // (of D in terms)
   const bool mirror = KIND == ORTHO_SYM && t.tm != t.tn;
   const bool across = mirror || (KIND == ORTHO_LAST && g.transposed);
-  const bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && g.terms == 2);
+  const bool two_terms = KIND == ORTHO_STEP || (KIND == ORTHO_SYM && g.d_terms == 2);
   const bool two_in = KIND != ORTHO_SYM || g.terms == 2;
   const int pitch = R + 4;  // of the rows turned to columns, in floats
   float* turned = reinterpret_cast<float*>(base_g + 65536);

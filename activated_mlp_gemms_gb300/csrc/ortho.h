@@ -20,8 +20,8 @@ constexpr int ORTHO_PARTS = 256;  // partial sums of a matrix's norm
 // One product D = alpha in + beta P Q of a stack, P [M, K] K-major, Q [N, K] K-major or
 // [K, N]; the three products hi lo + lo hi + hi hi with `terms` 2.
 enum OrthoKind : int {
-  ORTHO_SYM = 0,   // D symmetric (P is Q), in as many terms as the operands: the tiles on and
-                   // below the diagonal, and their mirror images
+  ORTHO_SYM = 0,   // D symmetric (P is Q), in d_terms terms: the tiles on and below the diagonal,
+                   // and their mirror images
   ORTHO_STEP = 1,  // Q is [K, N]; in and D in two terms
   ORTHO_LAST = 2   // the same, D the result: bf16 or fp32, as it is or transposed
 };
@@ -32,6 +32,7 @@ struct OrthoGemm {
   void* d_ptr;
   int ld_in, ld_d;     // their row pitches
   int M, N, kblocks, terms, batch;
+  int d_terms;  // of D where it is symmetric
   int tiles_m, tiles_n, units;
   float alpha, beta;  // alpha 0: no `in`
   int out_bf16, transposed;

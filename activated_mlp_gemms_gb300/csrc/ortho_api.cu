@@ -31,18 +31,26 @@ int check_ortho(const mlp_ortho_t* p) {
 }
 
 // After the control block (of which only the status word is used): the norms' partial sums, X
-// in two terms twice, and A and P = b A + c A A in one term or two.  Their rows begin at multiples
+// in two terms twice, and P = b A + c A A and A in one term or two.  Their rows begin at multiples
 // of 128 bytes: boxes of rows that straddle L2's lines took 1.5-1.8 times as long (3000 x 3000).
+//
+// Up to 128 rows P X takes both terms of both for a bf16 result, too, as in the one launch: the
+// result is as exact whichever way a matrix goes, alone or in a stack, and K is two k-blocks at
+// most (16 x 128 x 2048 2.8e-3 -> 2.0e-3 off, 125 -> 138 us; 1 x 128 x 2056 2.7e-3 -> 1.9e-3, 97 ->
+// 111; 1 x 64 x 4096 2.5e-3 -> 1.7e-3, 101 -> 107).  P's second term then goes over A, which lies
+// behind P.  A is one tile there: all of it has been multiplied before any of P is stored, and
+// the boxes of it that are added to P are read by the warp that stores there, before it does.
 struct Layout {
-  int m, n, terms;
-  int mp, np;  // row pitches of A and P, and of X
-  size_t part, x[2], a, poly, total;
+  int m, n, terms, p_terms;  // terms: of A, and of the products' operands but P X's
+  int mp, np;                // row pitches of A and P, and of X
+  size_t part, x[2], poly, a, total;
 };
 Layout layout(const mlp_ortho_t* p) {
   Layout w;
   w.m = p->rows < p->cols ? p->rows : p->cols;
   w.n = p->rows < p->cols ? p->cols : p->rows;
   w.terms = p->out_type == MLP_ORTHO_F32 ? 2 : 1;
+  w.p_terms = w.terms == 2 || w.m <= ORTHO_SMALL_M ? 2 : 1;
   w.mp = (w.m + 63) / 64 * 64;
   w.np = (w.n + 63) / 64 * 64;
   const size_t x = round256((size_t)p->batch * w.m * w.np * 4);
@@ -52,9 +60,9 @@ Layout layout(const mlp_ortho_t* p) {
   at += round256((size_t)p->batch * ORTHO_PARTS * 4);
   w.x[0] = at;
   w.x[1] = at + x;
-  w.a = at + 2 * x;
-  w.poly = w.a + a;
-  w.total = w.poly + a;
+  w.poly = at + 2 * x;
+  w.a = w.poly + a;  // (m is a multiple of 8, mp of 64: nothing between them)
+  w.total = w.a + a;
   return w;
 }
 
@@ -149,7 +157,7 @@ struct Products {
     g.M = M;
     g.N = N;
     g.kblocks = (K + 63) / 64;
-    g.terms = w.terms;
+    g.terms = g.d_terms = w.terms;
     g.batch = p->batch;
     g.status = status;
     g.timeout_ns = wait_limit_ns();
@@ -232,7 +240,8 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
                               at + w.x[0], s);
   }));
   Products run{p, w, s, static_cast<int*>(ws)};
-  const int m = w.m, n = w.n, xs = 2 * p->batch, as = w.terms * p->batch;  // depths
+  const int m = w.m, n = w.n;  // and the depths of X, A and P:
+  const int xs = 2 * p->batch, as = w.terms * p->batch, ps = w.p_terms * p->batch;
   char *A = at + w.a, *P = at + w.poly;
   for (int i = 0; i < p->steps; ++i) {
     char *X = at + w.x[i & 1], *next = at + w.x[(i & 1) ^ 1];
@@ -249,7 +258,8 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
       OrthoGemm g = run.gemm(m, m, m);
       g.p = g.q = run.map(A, as, m, m, w.mp, 64, 128);
       g.in = run.boxes(A, as, m, m, w.mp);
-      g.d = run.boxes(P, as, m, m, w.mp);
+      g.d = run.boxes(P, ps, m, m, w.mp);
+      g.d_terms = w.p_terms;
       g.in_ptr = A;
       g.d_ptr = P;
       g.ld_in = g.ld_d = w.mp;
@@ -258,7 +268,8 @@ int mlp_orthogonalize(const mlp_ortho_t* p, const void* G, void* out, void* ws, 
       MLP_TRY(run.run(g, ORTHO_SYM, MLP_KERNEL_ORTHO_POLY));
     }
     OrthoGemm g = run.gemm(m, n, m);
-    g.p = run.map(P, as, m, m, w.mp, 64, 128);
+    g.terms = w.p_terms;
+    g.p = run.map(P, ps, m, m, w.mp, 64, 128);
     g.q = run.map(X, xs, m, n, w.np, 64, 64);
     g.in = run.boxes(X, xs, m, n, w.np);
     g.in_ptr = X;

@@ -33,8 +33,10 @@ typedef enum { MLP_ORTHO_F32 = 0, MLP_ORTHO_BF16 = 1 } mlp_ortho_type_t;
  *
  * Arithmetic: X and A are held as fp16 at fixed powers of two, X with the remainder
  * of its rounding beside it, the products summed in fp32.  A bf16 out takes the
- * products of the leading terms (the result is off by 2e-3 of its Frobenius norm, as
- * much as the rounding of out itself; by up to 4e-3 below 16 rows); an fp32 out takes
+ * products of the leading terms, and up to 128 rows (the lesser side) both terms in the
+ * last product of a step.  Its rounding alone is 1.7e-3 of its Frobenius norm; the result
+ * is off by 1.7e-3 to 2.0e-3 up to 128 rows (by up to 3.3e-3 below 16), by 2.0e-3 to
+ * 2.9e-3 above, whichever way it is computed, alone or in a stack.  An fp32 out takes
  * those with the remainders too (1e-6 to 1e-5, as an fp32 product; 1e-4 where all but
  * a few singular values are zero).  |G| is summed in fp32: entries above 1e19 overflow
  * it, and of a G whose entries are all below 1e-19 it is lost (the result is then G / eps's:
