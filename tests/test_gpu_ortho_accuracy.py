@@ -3,7 +3,7 @@ test_ortho_arithmetic.py)."""
 import pytest
 import torch
 from ortho_arithmetic import momentum, off, plain
-from test_ortho_arithmetic import BF16_128
+from test_ortho_arithmetic import BF16_128, rank_one_bound
 
 import activated_mlp_gemms_gb300 as m
 
@@ -76,3 +76,14 @@ def test_without_the_linear_term():
             A = X @ X.t()
             X = a0 * X + c0 * (A @ A) @ X
         assert off(a, X) < BF16_128 and off(c, X) < 1e-4
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 512), (96, 1024), (1024, 96), (128, 4096), (136, 4152),
+                                       (256, 2048), (512, 512), (512, 1408), (1408, 512),
+                                       (1408, 2048), (2048, 4872)])
+def test_fp32_of_rank_one(rows, cols):
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.float64)  # noqa: E731
+    G = (rn(1, rows, 1) @ rn(1, 1, cols)).float()
+    e = worst(run(G, F32), G)
+    assert e < rank_one_bound(min(rows, cols)), e
