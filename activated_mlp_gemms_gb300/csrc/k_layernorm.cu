@@ -1,6 +1,6 @@
 // The layer norm with the residual sum in front of it (mlp_norm.h), forward and backward.
 //
-// A row belongs to G threads, each with NV vectors of 8 of its values, so that it is read once:
+// A row belongs to G threads, each with NP pieces of 16 bytes of it, so that it is read once:
 // the mean first, then the squares of what is left of it (no cancellation), then the outputs.
 // HBM's bandwidth bounds both passes, and what reaches it is bytes in flight: a block walks over
 // rows and copies the next ones' values to shared memory (cp.async) while it works on one.  A
@@ -563,11 +563,16 @@ Shape shape_of(int H) {
   });
 }
 Shape shape(int H, bool bf16) { return bf16 ? shape_of<__nv_bfloat16>(H) : shape_of<float>(H); }
-// Blocks of an SM, by the shared memory that they take (a KB of each is the driver's; 8 KB the
-// columns' sums of a warp a row) and `most` threads, which the registers allow.
+// Blocks of an SM, by the shared memory that they take (a KB of each is the driver's; 4 KB the
+// columns' sums of a warp a row) and by `most` threads: 768 with 8 columns a thread, whose kernels
+// use up to 80 registers, 640 with 16, the backward 512 with 32.  With 16 columns of bf16 the
+// forward with a residual (101 registers) and the backward with dh and sums (112) fit 512 threads
+// alone, and some of the blocks planned come as a second wave: planned / resident an SM 10 / 8
+// of 64 threads (the backward of 520 to 1024 columns), 5 / 4 of 128 (2048), both passes 2 / 1 of
+// 320 (5120), but 2 / 2 of 256 (4096).  A plan by each kernel's own registers has not been tried.
 int sm_blocks(const Shape& p, int arrays, int most) {
   const int fit =
-      static_cast<int>(228 * 1024 / (arrays * p.ahead + (p.rows > 1 ? 10 * 1024 : 1536)));
+      static_cast<int>(228 * 1024 / (arrays * p.ahead + (p.rows > 1 ? 6 * 1024 : 1536)));
   const int n = fit < most / p.threads ? fit : most / p.threads;
   return n < 1 ? 1 : n;
 }
@@ -593,7 +598,6 @@ cudaError_t fwd_of(const NormArgs& a, const void* x, const void* residual, const
   const Shape p = shape_of<T, ONE>(a.H);
   const int arrays = RESIDUAL ? 2 : 1;
   const int all = (a.M - 1) / p.rows + 1;
-  // (registers: up to 80 a thread for 8 columns, 102 for 16)
   const int most = 152 * sm_blocks(p, arrays, p.columns <= 8 ? 768 : 640);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(dim3(all < most ? all : most), p.threads, stream, attr);
