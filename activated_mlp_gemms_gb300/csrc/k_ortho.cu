@@ -23,8 +23,8 @@
 //              so; a unit's k-blocks draw 12 TB/s of L2, and that is what `in` and D wait for)
 // The tensor cores truncate their accumulator at every instruction, by about half of its last bit:
 // over a long K an fp32 result would lose a digit by it (4864: 3e-5, now 5e-6).  With both
-// terms the leading products therefore come in chunks of CHUNK k-blocks, whose sums the epilogue's
-// warps add up in fp32, rounded to nearest, in registers.
+// terms the leading products therefore come in chunks of g.chunk k-blocks, whose sums the
+// epilogue's warps add up in fp32, rounded to nearest, in registers.
 // With SPLIT a unit of a symmetric product has a cluster of two pairs, each with half of its
 // k-blocks: a pair keeps half of the tile's columns, leaves its sums of the others in its shared
 // memory over the ring, and adds to its own the other pair's, read from there strip by strip.
@@ -61,19 +61,13 @@ constexpr uint32_t IDESC_FP16 = (1u << 4) | ((Q_MN ? 1u : 0u) << 16) |
                                 (static_cast<uint32_t>(TILE >> 3) << 17) |
                                 (static_cast<uint32_t>(TILE >> 4) << 24);
 
-// (X X^T: half as long, its error is stretched by two more products.  4864 x 2048, five steps: off
-// by 4.7e-6, 938 us; with chunks of 2 and 4: 2.6e-6, 982.)
-template <int KIND>
-constexpr int CHUNK = KIND == ORTHO_SYM ? 4 : 8;
 // Chunks of a unit's k-blocks, and where chunk c ends: the small products (hi lo, lo hi) belong
 // to the first.
-template <int KIND>
-__device__ __forceinline__ int chunks_of(int kblocks) {
-  return (kblocks + CHUNK<KIND> - 1) / CHUNK<KIND>;
+__device__ __forceinline__ int chunks_of(const OrthoGemm& g, int kblocks) {
+  return (kblocks + g.chunk - 1) / g.chunk;
 }
-template <int KIND>
-__device__ __forceinline__ int chunk_end(int kblocks, int c) {
-  const int end = 2 * kblocks + (c + 1) * CHUNK<KIND>;
+__device__ __forceinline__ int chunk_end(const OrthoGemm& g, int kblocks, int c) {
+  const int end = 2 * kblocks + (c + 1) * g.chunk;
   return end < 3 * kblocks ? end : 3 * kblocks;
 }
 
@@ -236,7 +230,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
   const int kb0 = pair ? half : 0;
   const int kb_len = !SPLIT ? g.kblocks : pair ? g.kblocks - half : half;
   const int kb_all = kb_len * segs;
-  const int chunks = TWO ? chunks_of<KIND>(kb_len) : 1;
+  const int chunks = TWO ? chunks_of(g, kb_len) : 1;
   int acc = 0;  // of the next chunk (or unit), in its readers and its writer alike
   uint32_t aphase = 0;
   auto next_acc = [&] {
@@ -316,7 +310,7 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_gemm(const __grid_constan
           tc_fence_after();
           const uint32_t d = tmem + acc * TILE;
           const int begin = i;
-          for (const int end = TWO ? chunk_end<KIND>(kb_len, c) : kb_all; i < end; ++i) {
+          for (const int end = TWO ? chunk_end(g, kb_len, c) : kb_all; i < end; ++i) {
             ok = mbar_wait<PAIR>(bar_s(FULL + stage), phase, lim, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -626,9 +620,8 @@ cudaLaunchConfig_t ortho_config(int cg, int grid, cudaStream_t stream, cudaLaunc
 // Few units with a long K: a cluster of CTAs shares a 128 x 128 tile's k-blocks.  Each leaves
 // its fp32 sums in its shared memory; then each adds up its share of the rows over the
 // cluster's memories, in the CTAs' order, and finishes them.  With both terms the leading
-// products come in parts of PART k-blocks (see CHUNK), each in the next of four accumulators,
-// which the epilogue's warps add up in registers.
-constexpr int PART = 4;
+// products come in parts, as the chunks above, each in the next of four accumulators, which the
+// epilogue's warps add up in registers.
 constexpr int SPLIT_STAGES = 6;
 constexpr int SPLIT_SMEM = SPLIT_STAGES * OSTAGE + 1024 + 256;
 
@@ -732,12 +725,8 @@ __global__ void __launch_bounds__(OTHREADS, 1) k_ortho_split(const __grid_consta
   const int slice0 = rank * per < g.kblocks ? rank * per : g.kblocks;
   const int slice1 = slice0 + per < g.kblocks ? slice0 + per : g.kblocks;
   const int len = slice1 - slice0, mine = len * segs;
-  // parts, and where one ends: the small products belong to the first
-  const int parts = len == 0 ? 0 : segs == 1 ? 1 : (len + PART - 1) / PART;
-  auto part_end = [&](int i) {
-    const int end = segs == 1 ? mine : mine - len + (i + 1) * PART;
-    return end < mine ? end : mine;
-  };
+  const int parts = len == 0 ? 0 : segs == 1 ? 1 : chunks_of(g, len);
+  auto part_end = [&](int i) { return segs == 1 ? mine : chunk_end(g, len, i); };
   auto failed = [&] {
     *abort_flag = 1;
     atomicExch(g.status, O_TIMEOUT);

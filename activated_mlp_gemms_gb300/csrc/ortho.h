@@ -33,6 +33,7 @@ struct OrthoGemm {
   int ld_in, ld_d;     // their row pitches
   int M, N, kblocks, terms, batch;
   int d_terms;  // of D where it is symmetric
+  int chunk;    // with two terms: k-blocks that an accumulator sums up
   int tiles_m, tiles_n, units;
   float alpha, beta;  // alpha 0: no `in`
   int out_bf16, transposed;

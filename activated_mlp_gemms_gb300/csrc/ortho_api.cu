@@ -129,6 +129,16 @@ int small_width(const mlp_ortho_t* p, const Layout& w) {
   return waves <= (w.m <= 64 ? 2 : 1) ? width : 0;
 }
 
+// k-blocks of a leading product that one accumulator sums up where both terms are taken (the
+// tensor cores truncate it at every instruction).  X X^T and A A half as long: their errors are
+// stretched by two more products and one.  Up to 512 rows, whose own error is small, one and
+// two, so that an fp32 result is as exact as with products of fp32; above, where it grows by the
+// sums' length, four and eight are, for 5-20 % less time.  Measured (off by and us, short / long;
+// products of fp32): 256 x 14336 2.2e-6, 331 / 7.6e-6, 291; 2.0e-6 -- 256 x 512 1.7e-6, 147 / 5.7e-6,
+// 140; 2.2e-6 -- 4 x 512 x 1408 2.0e-6, 274 / 5.8e-6, 247; 3.2e-6 -- 640 x 4096 2.1e-6, 270 / 4.9e-6, 251;
+// 3.7e-6 -- 4864 x 2048 1.6e-6, 1030 / 4.7e-6, 844; 5.0e-6.
+int chunk_of(int m, bool sym) { return (m <= 512 ? 2 : 8) / (sym ? 2 : 1); }
+
 struct Products {
   const mlp_ortho_t* p;
   Layout w;
@@ -167,6 +177,7 @@ struct Products {
   int run(OrthoGemm& g, OrthoKind kind, int tag) {
     if (!ok) return MLP_ERR_CUDA;
     const bool sym = kind == ORTHO_SYM;
+    g.chunk = chunk_of(g.M, sym);
     g.backwards = backwards;
     backwards = !backwards;
     if (sym && share_pairs(g)) {
@@ -181,6 +192,7 @@ struct Products {
     const int share =
         cg == 1 && g_tile_policy.load() != 1 ? pick_share(g.units, g.kblocks, g.terms == 2 ? 3 : 1)
                                            : 1;
+    if (share > 1 && g.chunk > 4) g.chunk = 4;  // (a CTA's slice is short)
     return traced(tag, stream, [&] {
       return share > 1 ? launch_ortho_split(g, share, kind, stream)
                        : launch_ortho_gemm(g, cg, kind, stream);

@@ -87,3 +87,20 @@ def test_fp32_of_rank_one(rows, cols):
     G = (rn(1, rows, 1) @ rn(1, 1, cols)).float()
     e = worst(run(G, F32), G)
     assert e < rank_one_bound(min(rows, cols)), e
+
+
+# An fp32 result of 129 to 512 rows.  Emulated on the CPU with sums truncated to 24 bits twice an
+# instruction (every 8 products), chunks of one and two k-blocks (64 of K) leave 1.0e-6 to 1.4e-6 at
+# 136 x 512 to 512 x 512; twice that.  (Chunks of four and eight: measured up to 7.6e-6.)
+FP32_512 = 2.8e-6
+
+
+@pytest.mark.parametrize("make", [momentum, noise])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 136, 1024), (1, 136, 4152), (1, 256, 512),
+                                             (1, 256, 14336), (1, 2048, 256), (1, 304, 1000),
+                                             (1, 320, 6000), (4, 512, 1408), (1, 512, 8192),
+                                             (20, 264, 264)])
+def test_fp32_of_129_to_512_rows(make, batch, rows, cols):
+    G = stack(make, batch, rows, cols)
+    e = worst(run(G, F32), G)
+    assert e < FP32_512, e
