@@ -5,18 +5,21 @@
 //   each adds up 128 / CTAs of A's rows over the cluster and hands them, as fp16, to all;
 //   each forms P = b A + c A A for itself, and a X + P X of its columns.
 // X is the K-major operand of the first product and the MN-major one of the last: the same
-// 128-byte rows serve both.  (Arithmetic and scales as in k_ortho.cu; no sum here is long enough
-// to need its chunks.  But P X takes both terms of both for a bf16 result, too: its operands make
-// most of that result's error, 2.6e-3 of 64 x 512 with the leading terms, now 1.8e-3, of which
-// rounding it is 1.7e-3, for 29 -> 32 us.)  What bounds it is latency: three rounds of MMA, two cluster barriers and
-// three passes over tensor memory a step, and the exchange of A's rows, whose shared-memory
-// traffic between CTAs runs at some 10 bytes a cycle (so only the m x m that there are move).
-// Measured: 64 x 512 32 us, 64 x 1024 34, 128 x 1024 60; 64 x 2048
-// (256 columns a CTA) 45, of them 8 a step, 39 without the second terms in P X.
+// 128-byte rows serve both.  (Arithmetic and scales as in k_ortho.cu.  P X takes both terms of
+// both for a bf16 result, too: its operands make most of that result's error, 2.6e-3 of 64 x 512
+// with the leading terms, now 1.8e-3, of which rounding it is 1.7e-3, for 29 -> 32 us.  An fp32
+// result's leading products are summed two instructions at a time: 64 x 1024 1.9e-6 -> 0.9e-6 off,
+// 43 -> 45 us, 128 x 1024 3.5e-6 -> 1.5e-6, 73 -> 76; products of fp32 0.9e-6 and 1.7e-6.)
+// What bounds it is latency: three rounds of MMA, two cluster barriers and three passes over tensor
+// memory a step, and the exchange of A's rows, whose shared-memory traffic between CTAs runs at
+// some 10 bytes a cycle (so only the m x m that there are move).
+// Measured: 64 x 512 32 us, 64 x 1024 33, 128 x 1024 58; 64 x 2048 (256 columns a CTA) 45, of them
+// 8 a step, 39 without the second terms in P X; 128 x 2048 76.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "gemm_params.h"
 #include "ortho.h"
@@ -142,7 +145,8 @@ __device__ __forceinline__ void load8(const void* p, size_t at, float (&f)[8]) {
   }
 }
 
-template <int WIDTH, bool BF16>
+// PARTS: an fp32 result (128 columns a CTA).
+template <int WIDTH, bool BF16, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) {
   using S = Smem<WIDTH>;
   extern __shared__ uint8_t small_smem[];
@@ -273,13 +277,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     tc_fence_after();
   };
   // D = P Q over 16-element steps of K, step k's operands at p(k), q(k) in their first terms:
-  // with two terms hi lo, lo hi, hi hi.
-  auto products = [&](bool two, uint32_t d, uint32_t idesc, int ksteps, auto&& p, int p_term,
-                      auto&& q, int q_term) {
+  // with two terms hi lo, lo hi, hi hi.  For an fp32 result the leading product comes in four parts
+  // of two steps, an accumulator each: the tensor cores truncate what they add to.
+  static_assert(!PARTS || WIDTH == 128, "four accumulators");
+  auto products = [&](bool two, uint32_t idesc, int ksteps, auto&& p, int p_term, auto&& q,
+                      int q_term) {
     uint32_t more = 0;
     for (int seg = two ? 0 : 2; seg < 3; ++seg)
       for (int k = 0; k < ksteps; ++k) {
-        tc_mma_bf16(d, p(k, seg == 1 ? p_term : 0), q(k, seg == 0 ? q_term : 0), idesc, more);
+        const int acc = PARTS && seg == 2 ? k >> 1 : 0;
+        if (acc > 0) more = k & 1;
+        tc_mma_bf16(tmem + acc * 128, p(k, seg == 1 ? p_term : 0), q(k, seg == 0 ? q_term : 0),
+                    idesc, more);
         more = 1;
       }
   };
@@ -290,23 +299,37 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
   };
   const int q = warp & 3, part = warp >> 2, row = q * 32 + lane;  // lanes, quarter of columns
   const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
-  const uint32_t D1 = tmem, D2 = tmem + 128, D3 = tmem + 256;
+  // 32 columns of D from c, a row a thread.
+  auto read = [&](int c, float (&f)[32]) {
+    uint32_t a[32];
+    tmem_ld32(tmem + lanes + c, a);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(a[i]);
+#pragma unroll 1
+    for (int acc = 1; PARTS && acc < 4; ++acc) {
+      tmem_ld32(tmem + acc * 128 + lanes + c, a);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) f[i] += __uint_as_float(a[i]);
+    }
+  };
   const int share = (g.m + ctas - 1) / ctas;  // A's rows of a CTA
 
   for (int step = 0; step < g.steps; ++step) {
     // this CTA's share of A
     round([&] {
-      products(g.terms == 2, D1, IDESC<128, false>, WIDTH / 16, kmajor(base + S::X), S::TERM,
+      products(PARTS, IDESC<128, false>, WIDTH / 16, kmajor(base + S::X), S::TERM,
                kmajor(base + S::X), S::TERM);
     });
     if (q * 32 < g.m && part * 32 < g.m) {
-      uint32_t a[32];
-      tmem_ld32(D1 + lanes + part * 32, a);
-      tmem_wait_ld();
+      float a[32];
+      read(part * 32, a);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        st_shared_v4(sum_part(base + S::P, row, part * 8 + j), a[4 * j], a[4 * j + 1],
-                     a[4 * j + 2], a[4 * j + 3]);
+        st_shared_v4(sum_part(base + S::P, row, part * 8 + j), __float_as_uint(a[4 * j]),
+                     __float_as_uint(a[4 * j + 1]), __float_as_uint(a[4 * j + 2]),
+                     __float_as_uint(a[4 * j + 3]));
     }
     tc_fence_before();
     __syncwarp();
@@ -328,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
       for (int s = 0; s < ctas; ++s) {
         const uint32_t to = mapa_shared(piece(base + S::A, r, c), static_cast<uint32_t>(s));
         st_cluster_v4(to, hi);
-        if (g.terms == 2) st_cluster_v4(to + S::A_TERM, lo);
+        if (PARTS) st_cluster_v4(to + S::A_TERM, lo);
       }
     }
     fence_proxy_async_all();
@@ -336,20 +359,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     cluster_sync();
     // P = b A + c A A
     round([&] {
-      products(g.terms == 2, D2, IDESC<128, false>, 8, kmajor(base + S::A), S::A_TERM, kmajor(base + S::A),
-               S::A_TERM);
+      products(PARTS, IDESC<128, false>, 8, kmajor(base + S::A), S::A_TERM,
+               kmajor(base + S::A), S::A_TERM);
     });
     {
-      uint32_t a[32];
-      tmem_ld32(D2 + lanes + part * 32, a);
-      tmem_wait_ld();
+      float a[32];
+      read(part * 32, a);
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         const int col = part * 32 + j;
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = g.c / ORTHO_A * __uint_as_float(a[j + i]);
-        if (g.terms == 2) add_term(ld_shared_v4(piece(base + S::A + S::A_TERM, row, col)), g.b, f);
+        for (int i = 0; i < 8; ++i) f[i] = g.c / ORTHO_A * a[j + i];
+        if (PARTS) add_term(ld_shared_v4(piece(base + S::A + S::A_TERM, row, col)), g.b, f);
         add_term(ld_shared_v4(piece(base + S::A, row, col)), g.b, f);
         put(piece(base + S::P, row, col), take_term(f));
         put(piece(base + S::P + S::A_TERM, row, col), take_term(f));
@@ -359,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     // a X + P X of my columns
     const bool last = step + 1 == g.steps;
     round([&] {
-      products(true, D3, IDESC<WIDTH, true>, 8, kmajor(base + S::P), S::A_TERM,
+      products(true, IDESC<WIDTH, true>, 8, kmajor(base + S::P), S::A_TERM,
                [&](int k, int term) {
                  return sdesc_sw128(base + S::X + term + k * 2048, BLOCK, 1024);
                },
@@ -369,16 +391,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     const float beta = last ? g.scale / ORTHO_X / ORTHO_A : 1.f / ORTHO_A;
 #pragma unroll 1
     for (int c = part * (WIDTH / 4); c < (part + 1) * (WIDTH / 4); c += 32) {
-      uint32_t a[32];
+      float a[32];
       __syncwarp();
-      tmem_ld32(D3 + lanes + c, a);
-      tmem_wait_ld();
+      read(c, a);
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         const uint32_t hi = piece(base + S::X, row, c + j), lo = hi + S::TERM;
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = beta * __uint_as_float(a[j + i]);
+        for (int i = 0; i < 8; ++i) f[i] = beta * a[j + i];
         add_term(ld_shared_v4(lo), alpha, f);
         add_term(ld_shared_v4(hi), alpha, f);
         if (!last) {
@@ -422,9 +443,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
   }
 }
 
-template <int WIDTH, bool BF16>
+template <int WIDTH, bool BF16, bool PARTS>
 cudaError_t launch_of(const OrthoSmall& g, cudaStream_t stream) {
-  auto kern = k_ortho_small<WIDTH, BF16>;
+  auto kern = k_ortho_small<WIDTH, BF16, PARTS>;
   static std::atomic<unsigned long long> done{0};  // devices that have the attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -456,8 +477,13 @@ cudaError_t launch_of(const OrthoSmall& g, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_ortho_small(const OrthoSmall& g, int width, cudaStream_t stream) {
-  if (width == 128) return g.bf16 ? launch_of<128, true>(g, stream) : launch_of<128, false>(g, stream);
-  return g.bf16 ? launch_of<256, true>(g, stream) : launch_of<256, false>(g, stream);
+  auto of = [&](auto bf16) {
+    constexpr bool BF16 = decltype(bf16)::value;
+    if (width == 256) return launch_of<256, BF16, false>(g, stream);
+    return g.terms == 2 ? launch_of<128, BF16, true>(g, stream)
+                        : launch_of<128, BF16, false>(g, stream);
+  };
+  return g.bf16 ? of(std::true_type{}) : of(std::false_type{});
 }
 
 }  // namespace mlpk

@@ -38,8 +38,8 @@ typedef enum { MLP_ORTHO_F32 = 0, MLP_ORTHO_BF16 = 1 } mlp_ortho_type_t;
  * is off by 1.7e-3 to 2.2e-3 up to 128 rows (up to 3.5e-3 below 64), by 2.0e-3 to 3.4e-3
  * above (4.4e-3 where all singular values are equal), whichever way it is computed, alone
  * or in a stack.  An fp32 out takes those with the remainders too: 22 bits of X, A and P.  It
- * is off by 1e-6 to 5e-6 for momenta, as products of fp32 are (up to 128 rows by up to 3.6e-6,
- * two to three times those); by 5e-5 where a few directions stand over 1e-2 of noise, and by
+ * is off by 0.5e-6 to 5e-6 for momenta, as products of fp32 are (at most 1.8 times those: 64 x
+ * 4096 1.7e-6 and 1.0e-6); by 5e-5 where a few directions stand over 1e-2 of noise, and by
  * 1.6e-4 where all but a few singular values are zero (fp32 products: 3e-5 to 6e-5, 4e-4).
  * |G| is summed in fp32: entries above 1e19 overflow
  * it, and of a G whose entries are all below 1e-19 it is lost (the result is then G / eps's:

@@ -104,3 +104,17 @@ def test_fp32_of_129_to_512_rows(make, batch, rows, cols):
     G = stack(make, batch, rows, cols)
     e = worst(run(G, F32), G)
     assert e < FP32_512, e
+
+
+# One launch, momenta: sums of two instructions leave 0.7e-6 to 0.8e-6 by the same emulation; two and
+# a half times that, for the sums over the CTAs and what an instruction truncates inside.  (Sums of
+# eight instructions: measured 1.9e-6 at 64 x 1024, 2.7e-6 to 3.6e-6 from 96 x 1024.)
+FP32_ONE_LAUNCH = 2.0e-6
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 64, 64), (1, 64, 1024), (1, 96, 1024),
+                                             (1, 1024, 128), (1, 128, 512), (10, 128, 768)])
+def test_fp32_in_one_launch(batch, rows, cols):
+    G = stack(momentum, batch, rows, cols)
+    e = worst(run(G, F32), G)
+    assert e < FP32_ONE_LAUNCH, e
