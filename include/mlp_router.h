@@ -19,6 +19,13 @@
  * logits' gradient is 0.  An expert at -inf is never chosen: a routed token
  * with fewer than top_k experts left has ids -1 and weights 0 behind them.  A
  * NaN counts as the largest value and makes its token's weights NaN.
+ *
+ * Arithmetic in fp32, with the hardware's base-2 exponential (within 2^-22 of its
+ * value) and reciprocal (2^-23).  A weight is within (2.3 d + 49) 2^-24 of its value,
+ * beside its type's rounding, where d is its logit's distance from the token's
+ * largest (measured 3e-8 to 9e-8 of it in the mean square); one below 2^-126 may be
+ * zero.  Sums over tokens are sums of fp32; the derivatives behind the loss have six
+ * roundings.
  */
 #ifndef MLP_GB300_ROUTER_H
 #define MLP_GB300_ROUTER_H
