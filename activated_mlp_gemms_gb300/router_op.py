@@ -119,8 +119,9 @@ def _ws_size(T, E, top_k):
 def _ws(ws, size, device, stream):
     if ws is None:  # (of a problem that the call refuses: any)
         return _call_workspace(size or 256, device, stream)
-    if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
+    if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()
+            and ws.get_device() == device.index):
+        raise ValueError("workspace must be a contiguous CUDA uint8 tensor on the current device")
     return ws
 
 
