@@ -109,6 +109,15 @@ int mlp_moe_router_fwd(const mlp_router_t* p, const void* logits, const unsigned
   const bool sums = counts || balance;
   const RouterLayout w = router_layout(p);
   if (sums) MLP_TRY(check_ws(w.total, ws, ws_bytes));
+  // one token's results over another's logits, or over each other
+  auto same = [](const void* a, const void* b) { return a && a == b; };
+  if (same(ids, logits) || same(weights, logits) || same(ids, weights) || same(ids, mask) ||
+      same(weights, mask))
+    return MLP_ERR_INVALID_ARG;
+  for (const void* o : {static_cast<const void*>(counts), static_cast<const void*>(balance)})
+    if (same(o, logits) || same(o, ids) || same(o, weights) || same(o, mask))
+      return MLP_ERR_INVALID_ARG;
+  if (same(counts, balance)) return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* at = static_cast<char*>(ws);
   RouterParts parts = {};
@@ -137,6 +146,11 @@ int mlp_moe_router_bwd(const mlp_router_t* p, const void* logits, const unsigned
   if (dloss) MLP_TRY(need_as(balance, 4));
   const RouterArgs a = args_of(p, logits, mask);
   if (dlogits == logits && a.ldl != a.ldd) return MLP_ERR_INVALID_ARG;
+  // one token's gradient over what another's is computed from
+  for (const void* in : {static_cast<const void*>(mask), static_cast<const void*>(ids),
+                         static_cast<const void*>(balance), dweights,
+                         static_cast<const void*>(dloss)})
+    if (dlogits == in) return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_ROUTER_BWD, s, [&] {
     return launch_router_bwd(a, ids, balance, dweights, dloss, dlogits, s);

@@ -59,8 +59,8 @@ size_t mlp_moe_router_workspace_size(const mlp_router_t* p);
  *   balance  fp32 [E + 1] out or NULL: the loss, then d loss / d p[t,e] for each
  *            expert (the same for every routed token), which the backward takes
  *   ws       256-byte aligned; NULL where counts and balance both are
- * The sums over tokens do not depend on any order of arrival: two calls with the
- * same operands give the same bits. */
+ * No output may overlap an operand or another output.  The sums over tokens do not
+ * depend on any order of arrival: two calls with the same operands give the same bits. */
 int mlp_moe_router_fwd(const mlp_router_t* p, const void* logits, const unsigned char* mask,
                        int* ids, void* weights, int* counts, float* balance, void* ws,
                        size_t ws_bytes, void* stream);
@@ -69,7 +69,8 @@ int mlp_moe_router_fwd(const mlp_router_t* p, const void* logits, const unsigned
  *   ids      the forward's
  *   balance  the forward's, or NULL with dloss
  *   dweights [T,top_k] (weights_type) or NULL;  dloss fp32 [1] (on the device) or NULL
- *   dlogits  [T,E] (logits_type, pitch ldd) out; may be logits itself (then ldd = ldl)
+ *   dlogits  [T,E] (logits_type, pitch ldd) out; may be logits itself (then ldd = ldl),
+ *            and overlaps no other operand
  * (An id outside [0, E) takes no part.) */
 int mlp_moe_router_bwd(const mlp_router_t* p, const void* logits, const unsigned char* mask,
                        const int* ids, const float* balance, const void* dweights,
