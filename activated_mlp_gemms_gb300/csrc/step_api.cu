@@ -1,5 +1,8 @@
 // step_api.cu -- the C entry points of mlp_router.h and mlp_norm.h: argument
 // validation, workspace layout and launch sequences.
+#include <algorithm>
+#include <initializer_list>
+
 #include "host.h"
 #include "mlp_norm.h"
 #include "mlp_router.h"
@@ -14,6 +17,11 @@ int need_as(const void* ptr, uintptr_t size) {
   return reinterpret_cast<uintptr_t>(ptr) % size ? MLP_ERR_ALIGNMENT : MLP_OK;
 }
 int opt_as(const void* ptr, uintptr_t size) { return ptr ? need_as(ptr, size) : MLP_OK; }
+
+// Whether an output (or NULL) is one of the others.
+bool any(const void* o, std::initializer_list<const void*> of) {
+  return o && std::find(of.begin(), of.end(), o) != of.end();
+}
 
 int check_ws(size_t total, const void* ws, size_t ws_bytes) {
   if (!ws) return MLP_ERR_INVALID_ARG;
@@ -110,14 +118,10 @@ int mlp_moe_router_fwd(const mlp_router_t* p, const void* logits, const unsigned
   const RouterLayout w = router_layout(p);
   if (sums) MLP_TRY(check_ws(w.total, ws, ws_bytes));
   // one token's results over another's logits, or over each other
-  auto same = [](const void* a, const void* b) { return a && a == b; };
-  if (same(ids, logits) || same(weights, logits) || same(ids, weights) || same(ids, mask) ||
-      same(weights, mask))
+  if (any(ids, {logits, mask, weights, counts, balance}) ||
+      any(weights, {logits, mask, counts, balance}) || any(counts, {logits, mask, balance}) ||
+      any(balance, {logits, mask}))
     return MLP_ERR_INVALID_ARG;
-  for (const void* o : {static_cast<const void*>(counts), static_cast<const void*>(balance)})
-    if (same(o, logits) || same(o, ids) || same(o, weights) || same(o, mask))
-      return MLP_ERR_INVALID_ARG;
-  if (same(counts, balance)) return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* at = static_cast<char*>(ws);
   RouterParts parts = {};
@@ -147,10 +151,7 @@ int mlp_moe_router_bwd(const mlp_router_t* p, const void* logits, const unsigned
   const RouterArgs a = args_of(p, logits, mask);
   if (dlogits == logits && a.ldl != a.ldd) return MLP_ERR_INVALID_ARG;
   // one token's gradient over what another's is computed from
-  for (const void* in : {static_cast<const void*>(mask), static_cast<const void*>(ids),
-                         static_cast<const void*>(balance), dweights,
-                         static_cast<const void*>(dloss)})
-    if (dlogits == in) return MLP_ERR_INVALID_ARG;
+  if (any(dlogits, {mask, ids, balance, dweights, dloss})) return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_ROUTER_BWD, s, [&] {
     return launch_router_bwd(a, ids, balance, dweights, dloss, dlogits, s);
@@ -179,6 +180,11 @@ int mlp_layernorm_fwd(const mlp_layernorm_t* p, const void* x, const void* resid
     return (o == x && a.ldx != p->H) || (o == residual && a.ldr != p->H);
   };
   if (y == h || over(y) || (h && over(h))) return MLP_ERR_INVALID_ARG;
+  // one row's results over what another row reads
+  if (any(y, {weight, bias}) || any(h, {weight, bias}) ||
+      any(mean, {x, residual, weight, bias, y, h, rstd}) ||
+      any(rstd, {x, residual, weight, bias, y, h}))
+    return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(MLP_KERNEL_LAYERNORM, s, [&] {
     return launch_layernorm_fwd(a, x, residual, weight, bias, y, h, mean, rstd, s);
@@ -204,6 +210,9 @@ int mlp_layernorm_bwd(const mlp_layernorm_t* p, const void* dy, const void* h, c
   if (sums) MLP_TRY(check_ws(norm_total(p), ws, ws_bytes));
   if (!dx && !sums) return MLP_OK;
   if (dx == h) return MLP_ERR_INVALID_ARG;
+  // (a weight's gradient may go over the weight: it is written when all rows are done)
+  if (any(dx, {weight, mean, rstd, dweight, dbias}) || any(dweight, {dbias}))
+    return MLP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* part = sums ? reinterpret_cast<float*>(static_cast<char*>(ws) + CTRL_BYTES) : nullptr;
   MLP_TRY(traced(MLP_KERNEL_LAYERNORM_BWD, s, [&] {

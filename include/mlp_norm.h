@@ -44,7 +44,8 @@ size_t mlp_layernorm_workspace_size(const mlp_layernorm_t* p);
  *   y            [M,H] out, dense; may be x or residual itself (dense)
  *   h            [M,H] out, dense, or NULL; with a residual, what the backward takes (it may
  *                be x or residual itself (dense), not y)
- *   mean, rstd   fp32 [M] out or NULL: for the backward */
+ *   mean, rstd   fp32 [M] out or NULL: for the backward
+ * (No other output overlaps an operand or another output.) */
 int mlp_layernorm_fwd(const mlp_layernorm_t* p, const void* x, const void* residual,
                       const void* weight, const void* bias, void* y, void* h, float* mean,
                       float* rstd, void* stream);
@@ -57,7 +58,8 @@ int mlp_layernorm_fwd(const mlp_layernorm_t* p, const void* x, const void* resid
  *            dy or dh itself, not h
  *   dweight, dbias  [H] out or NULL: in weight_type, or with fuse_grad_accum = 1 fp32 that
  *            the gradient is added to
- *   ws       NULL where dweight and dbias both are */
+ *   ws       NULL where dweight and dbias both are
+ * (No other output overlaps an operand or another output.) */
 int mlp_layernorm_bwd(const mlp_layernorm_t* p, const void* dy, const void* h, const void* weight,
                       const float* mean, const float* rstd, const void* dh, void* dx,
                       void* dweight, void* dbias, int fuse_grad_accum, void* ws, size_t ws_bytes,
