@@ -8,10 +8,12 @@
 // threads hold their columns' sums for the weight's and the bias's gradients in registers from
 // row to row; a block leaves one partial sum a column, and a second kernel adds the blocks up in
 // their order.
-// Measured (us; TB/s of what the pass reads and writes): 8192 x 4096 bf16 with the residual sum
-// 40.6 (6.6), its backward with dh and the weight's and bias's gradients 48 (5.6) and their sums 3;
-// 4097 x 4872 fp32 34 (4.7: two reductions a row, in one block an SM) and 44 (5.4); 16384 x 2048
-// fp32 46 (5.8) and 66 (6.1).
+// Measured (us; TB/s of what the pass reads and writes), a launch by itself, when half of what it
+// wrote is still in L2: 8192 x 4096 bf16 with the residual sum 40.6 (6.6), its backward with dh and
+// the weight's and bias's gradients 49 (5.5) and their sums 3 (9 alone); 4097 x 4872 fp32 34 (4.7:
+// two reductions a row, in one block an SM) and 44 (5.4).  Back to back: 8192 x 4096 48 (5.6) and 53
+// with the sums; 4097 x 4872 33 and 48; 16384 x 2048 fp32 46 (5.8) and 66 (6.1); 20000 x 768 bf16
+// 16 (3.9) and 38, 16384 x 2560 bf16 32 (5.3) and 79.
 #include <cuda_bf16.h>
 
 #include <type_traits>

@@ -115,10 +115,11 @@ bool share_pairs(const OrthoGemm& g) {
 }
 
 // Columns a CTA where the whole call runs on one cluster a matrix (0: it does not): what fits
-// its shared memory, X in two terms and A and P in `terms`, and at most one wave of such clusters
-// (15 of eight CTAs are resident together), two up to 64 rows.  Measured, five steps in us (one
-// launch / a launch a product): 64 x 1024 39 / 89, 64 x 2048 50 / 89, 128 x 2048 82 / 121, 128 x 128
-// 40 / 79; stacks of 30 x 64 x 1024 74 / 116, 16 x 128 x 2048 153 / 146.
+// its shared memory, X in two terms and A in `terms`, P in two, and at most one wave of such
+// clusters (15 of eight CTAs are resident together), two up to 64 rows.  Measured, five steps in us
+// (one launch / a launch a product): 64 x 1024 33 / 90, 64 x 2048 45 / 98, 128 x 2048 76 / 109, 128 x
+// 128 34 / 85; fp32 results 64 x 1024 45 / 107, 128 x 1024 76 / 125; two waves, 30 x 64 x 1024 70 / 114,
+// 16 x 128 x 2048 155 / 138, 30 x 128 x 1024 133 / 130.
 int small_width(const mlp_ortho_t* p, const Layout& w) {
   if (g_tile_policy.load() != 0 || w.m > ORTHO_SMALL_M) return 0;
   const int width = w.n <= 128 * ORTHO_SMALL_CTAS ? 128 : w.terms == 1 ? 256 : 0;
