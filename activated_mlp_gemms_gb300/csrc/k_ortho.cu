@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "gemm_params.h"
+#include "ortho.cuh"
 #include "ortho.h"
 #include "ptx.cuh"
 
@@ -53,7 +54,6 @@ constexpr int BOX = 2048;                              // 32 x 32 fp16 or bf16
 constexpr int SET = 2 * BOX;                           // two terms, or a box and its mirror image
 constexpr int OSTAGING = EPI_WARPS * 2 * SET;
 constexpr int OSMEM = OSTAGES * OSTAGE + OSTAGING + 1024 + 512;  // ... alignment, control block
-constexpr int O_TIMEOUT = -6;                         // MLP_ERR_TIMEOUT
 
 // kind::f16 with fp16 operands (format 0), fp32 accumulators, M = N = TILE.
 template <int TILE, bool Q_MN>
@@ -90,14 +90,6 @@ __device__ __forceinline__ Tile tile_of(const OrthoGemm& g, int unit) {
     t.tm = u - t.tn * g.tiles_m;
   }
   return t;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
 // Row r of a 32 x 32 box of 2-byte values: 64 bytes, the 16-byte parts swizzled (64-byte
@@ -150,19 +142,6 @@ __device__ __forceinline__ void take_term(float (&v)[32], uint32_t (&w)[16]) {
     v[2 * i] -= x.x;
     v[2 * i + 1] -= x.y;
   }
-}
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));  // (no clobber: all of a row's are on their way together)
-  return v;
-}
-// Part j (16 bytes) of row r of the 128 x 128 fp32 sums: the parts of a row swapped by the row,
-// so that a row a thread and a row a warp both pass without bank conflicts.
-__device__ __forceinline__ uint32_t sum_part(uint32_t at, int r, int j) {
-  return at + static_cast<uint32_t>(r * 512 + ((j ^ (r & 31)) << 4));
 }
 
 template <int CG, int KIND, bool TWO, bool SPLIT>
@@ -625,27 +604,6 @@ cudaLaunchConfig_t ortho_config(int cg, int grid, cudaStream_t stream, cudaLaunc
 constexpr int SPLIT_STAGES = 6;
 constexpr int SPLIT_SMEM = SPLIT_STAGES * OSTAGE + 1024 + 256;
 
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// The sum of eight columns of a row over the shared memories of the first N CTAs, in their order;
-// x, y: the parts' addresses in each.
-template <int N>
-__device__ __forceinline__ void cluster_sums(uint32_t x, uint32_t y, float (&f)[8]) {
-  float4 u[N], v[N];
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
-    u[s] = ld_cluster_f4(mapa_shared(x, s));
-    v[s] = ld_cluster_f4(mapa_shared(y, s));
-  }
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
-    f[0] += u[s].x, f[1] += u[s].y, f[2] += u[s].z, f[3] += u[s].w;
-    f[4] += v[s].x, f[5] += v[s].y, f[6] += v[s].z, f[7] += v[s].w;
-  }
-}
 // Stores the terms of eight consecutive values (of D, or of its mirror image).
 __device__ __forceinline__ void store_terms(const OrthoGemm& g, size_t at, size_t term, bool two,
                                             const float (&f)[8]) {
@@ -978,25 +936,6 @@ cudaError_t launch_of(const OrthoGemm& g, cudaStream_t stream) {
 
 // ------------------------------------------------------------- norm and scale
 constexpr int NORM_THREADS = 512;
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = ld_global_v4(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack_bf16x2(w[i]);
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
-  } else {
-    const uint4 a = ld_global_v4(p), b = ld_global_v4(p + 4);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-  }
-}
 
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)

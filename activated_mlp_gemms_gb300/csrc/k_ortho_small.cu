@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "gemm_params.h"
+#include "ortho.cuh"
 #include "ortho.h"
 #include "ptx.cuh"
 
@@ -32,7 +33,6 @@ namespace {
 constexpr int THREADS = 512;  // four warps a TMEM lane quadrant
 constexpr int BLOCK = 128 * 128;       // bytes of 128 rows x 64 fp16 columns
 constexpr int SUMS = 128 * 128 * 4;    // of the fp32 share of A; P lies over it
-constexpr int O_TIMEOUT = -6;          // MLP_ERR_TIMEOUT
 
 template <int WIDTH>
 struct Smem {
@@ -52,17 +52,6 @@ constexpr uint32_t IDESC = (1u << 4) | ((B_MN ? 1u : 0u) << 16) |
 // 128-byte swizzle.
 __device__ __forceinline__ uint32_t piece(uint32_t at, int r, int c) {
   return at + static_cast<uint32_t>((c >> 6) * BLOCK + r * 128 + (((c >> 3 & 7) ^ (r & 7)) << 4));
-}
-// Part j (16 bytes) of row r of the fp32 sums, swapped by the row.
-__device__ __forceinline__ uint32_t sum_part(uint32_t at, int r, int j) {
-  return at + static_cast<uint32_t>(r * 512 + ((j ^ (r & 31)) << 4));
-}
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 // Eight values as fp16, and what that leaves of them.
 __device__ __forceinline__ uint4 take_term(float (&f)[8]) {
@@ -86,69 +75,21 @@ __device__ __forceinline__ void add_term(uint4 q, float k, float (&f)[8]) {
   }
 }
 __device__ __forceinline__ void put(uint32_t at, uint4 v) { st_shared_v4(at, v.x, v.y, v.z, v.w); }
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));  // (no clobber: all of a row's are on their way together)
-  return v;
-}
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x),
                "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
-// The sum of eight columns of a row over the shared memories of the cluster's N CTAs, in their
-// order; x, y: the parts' addresses in each.
-template <int N>
-__device__ __forceinline__ void cluster_sums(uint32_t x, uint32_t y, float (&f)[8]) {
-  float4 u[N], v[N];
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
-    u[s] = ld_cluster_f4(mapa_shared(x, s));
-    v[s] = ld_cluster_f4(mapa_shared(y, s));
-  }
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
-    f[0] += u[s].x, f[1] += u[s].y, f[2] += u[s].z, f[3] += u[s].w;
-    f[4] += v[s].x, f[5] += v[s].y, f[6] += v[s].z, f[7] += v[s].w;
-  }
-}
-
 // Plain stores before MMA reads, wherever in the cluster's shared memory.
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
-}
-
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, size_t at, float (&f)[8]) {
-  if constexpr (BF16) {
-    const uint4 v = ld_global_v4(static_cast<const __nv_bfloat16*>(p) + at);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack_bf16x2(w[i]);
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
-  } else {
-    const float* q = static_cast<const float*>(p) + at;
-    const uint4 a = ld_global_v4(q), b = ld_global_v4(q + 4);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-  }
 }
 
 // PARTS: an fp32 result (128 columns a CTA).
 template <int WIDTH, bool BF16, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) {
   using S = Smem<WIDTH>;
+  using T = std::conditional_t<BF16, __nv_bfloat16, float>;  // of G
   extern __shared__ uint8_t small_smem[];
   const uint32_t base = (smem_u32(small_smem) + 1023u) & ~1023u;
   uint8_t* ctrl = small_smem + (base - smem_u32(small_smem)) + S::CTRL;
@@ -189,8 +130,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ortho_small(const OrthoSmall g) 
     r = g.transposed ? i % 16 * 8 : i / (WIDTH / 8);
     c = g.transposed ? i / 16 : i % (WIDTH / 8) * 8;
     if (r < g.m && col0 + c < g.n) {
-      load8<BF16>(g.G, first + (g.transposed ? static_cast<size_t>(col0 + c) * g.m + r
-                                             : static_cast<size_t>(r) * g.n + col0 + c), f);
+      load8(static_cast<const T*>(g.G) + first +
+                (g.transposed ? static_cast<size_t>(col0 + c) * g.m + r
+                              : static_cast<size_t>(r) * g.n + col0 + c),
+            f);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = 0.f;
