@@ -202,7 +202,11 @@ __global__ void __launch_bounds__(SK_THREADS, 2)
   __syncwarp();
   // every MMA has completed, and with them every copy: the ring is free
   const bool summed = mbar_wait(done, 0, limit_ns + limit_ns / 2, abort_flag);
-  if (!summed && lane == 0) give_up();
+  if (!summed) {  // (what was issued ends before shared memory and TMEM are used again)
+    if (lane == 0) give_up();
+    volatile int never = 0;
+    mbar_wait(done, 0, 10000000ull, &never);
+  }
   __syncwarp();
   if (share > 1) cluster_sync();  // the owners' rings are free too
   // [rank][row of the owner][feature] in every CTA: row j of the tile belongs to

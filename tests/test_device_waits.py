@@ -53,3 +53,12 @@ def test_the_small_kernel_issues_nothing_after_a_failed_wait():
     assert "!*abort_flag" in body[guard:issue]
     assert re.search(r"__syncthreads\(\);\s*if \([^)]*$", body[:body.index("!*abort_flag")])
     assert re.search(r"if \(ok && !mbar_wait\(bar, phase,", body)
+
+
+def test_the_skinny_linear_kernel_waits_for_what_it_issued():
+    # its MMA warp commits what it has issued, also when it gives up; a failure elsewhere cuts the
+    # other warps' wait for that short, so that they wait once more, whatever has failed
+    body = next(b for _, b in kernels("k_linear_skinny.cu") if "tmem_dealloc" in b)
+    first = body.index("const bool summed = mbar_wait(done, 0,")
+    again = re.search(r"if \(!summed\) \{[^}]*mbar_wait\(done, 0, \d+ull, &never\);", body[first:])
+    assert again and first + again.end() < body.index("tmem_ld16")
